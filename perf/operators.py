@@ -232,7 +232,8 @@ def _batch(case, gen):
     index = _ints(first, torch.int64)[:, None] + torch.arange(width, device="cuda")
     table = perm[index.clamp(max=blocks - 1)].contiguous()
     return dict(table=table, seq=_ints(seq), qsl=_ints([i * new for i in range(len(seq) + 1)]), blocks=blocks,
-                block=block, longest=max(seq), tokens=len(seq) * new)
+                block=block, longest=max(seq), tokens=len(seq) * new,
+                error=torch.zeros(1, dtype=torch.int32, device="cuda"))
 
 
 def _prepare_select(case, gen):
@@ -276,13 +277,6 @@ def _prepare_attn(case, gen):
 def run(state):
     return {"tables": _run_tables, "rope": _run_rope, "bounds": _run_bounds, "select": _run_select,
             "attn": _run_attn}[state["op"]](state)
-
-
-def _workspace(s, bytes_of):
-    """The scratch memory that a program asks the size of once and keeps."""
-    if "workspace" not in s:
-        s["workspace"] = torch.empty(bytes_of(), dtype=torch.uint8, device="cuda")
-    return s["workspace"]
 
 
 def _run_tables(s):
@@ -388,10 +382,8 @@ def _positions(s):
 def _run_select(s):
     if own:
         from paged_kv_attention_07_gb300 import pka
-        hkv, pages = s["selected"].shape[1:]
-        work = _workspace(s, lambda: pka.pka_select_pages_workspace_size(s["tokens"], hkv, s["longest"], s["block"]))
         pka.pka_select_pages(s["q"], s["codes"], s["scales"], s["table"], s["qsl"], s["seq"], s["block"], FIRST, LAST,
-                             s["longest"], s["selected"], work)
+                             s["longest"], s["selected"], error_word=s["error"])
         return s["selected"]
     tokens, heads, dim = s["q"].shape
     hkv = s["codes"].shape[1]
@@ -421,11 +413,9 @@ def _run_select(s):
 def _run_attn(s):
     if own:
         from paged_kv_attention_07_gb300 import pka
-        hkv, dim = s["k_cache"].shape[1], s["k_cache"].shape[3]
-        work = _workspace(s, lambda: pka.pka_sparse_attn_workspace_size(s["tokens"], Q_HEADS, hkv, dim,
-                                                                        s["selected"].shape[2], s["block"]))
         pka.pka_sparse_attn_forward(s["q"], s["k_cache"], s["v_cache"], s["table"], s["qsl"], s["seq"], s["selected"],
-                                    s["scale"], s["longest"], s["out"], s["lse"], work, kv_scales=s["scales"])
+                                    s["scale"], s["longest"], s["out"], s["lse"], kv_scales=s["scales"],
+                                    error_word=s["error"])
         return dict(out=s["out"], lse=s["lse"])
     tokens, heads, dim = s["q"].shape
     hkv = s["k_cache"].shape[1]
