@@ -77,7 +77,8 @@ typedef enum {
 #define PKA_DEVERR_SLOT 0x40            /* a cache slot >= num_blocks * block_size */
 #define PKA_DEVERR_CAPACITY 0x80        /* the plan outgrew the workspace (inconsistent hints) */
 #define PKA_DEVERR_TIMEOUT 0x100        /* a pipeline wait gave up (bounded spin); results invalid */
-#define PKA_DEVERR_INDEX 0x200          /* pka_gather_rows: a row index outside [0, src_rows) */
+#define PKA_DEVERR_INDEX 0x200          /* pka_gather_rows: a row index outside [0, src_rows); a position past the
+                                           rotation table; a page list that does not ascend up to the token's page */
 
 /*
  * pka_cache_write -- write the new tokens' K and V rows into the paged cache.
@@ -390,7 +391,12 @@ typedef enum {
     PKA_KERNEL_MERGE = 6,
     PKA_KERNEL_GATHER = 7,          /* pka_gather_rows */
     PKA_KERNEL_CTX_DEQUANT = 8,     /* 8-bit cache: the extends' context gather */
-    PKA_KERNEL_COUNT = 9
+    PKA_KERNEL_STEP_TABLES = 9,     /* pka_step_tables */
+    PKA_KERNEL_QK_ROPE = 10,        /* pka_qk_rope_cache_write(_fp8) */
+    PKA_KERNEL_PAGE_BOUNDS = 11,    /* pka_page_bounds */
+    PKA_KERNEL_PAGE_SELECT = 12,    /* pka_select_pages */
+    PKA_KERNEL_SPARSE_ATTN = 13,    /* pka_sparse_attn_forward(_fp8) */
+    PKA_KERNEL_COUNT = 14
 } pka_kernel;
 
 /* enable != 0 turns timing on for `kernel` (and resets it); 0 turns it off. */
@@ -438,6 +444,214 @@ PKA_API pka_status pka_batch_order(int num_reqs, const int32_t *query_lens, cons
  */
 PKA_API pka_status pka_gather_rows(void *dst, const void *src, const int32_t *index, int64_t num_rows,
                                    int64_t src_rows, int64_t row_bytes, int32_t *error_word, void *stream);
+
+/*
+ * The block-sparse step
+ * ---------------------
+ * A serving step over contexts too long to read in full, as calls of their own
+ * next to (and freely mixed with) the ones above:
+ *   pka_step_tables           the step's block tables, slot map and positions
+ *   pka_qk_rope_cache_write   norms of q and k, position rotation, cache write
+ *   pka_page_bounds           bounds of the keys of each page the step filled
+ *   pka_select_pages          the pages each new token reads
+ *   pka_sparse_attn_forward   attention over those pages
+ * None of them needs a workspace. Each takes an `error_word` (device int32, or
+ * NULL): PKA_DEVERR_* bits are OR-ed into it and never cleared. Each is one
+ * kernel launch, may be captured into a CUDA graph, and may run at the same
+ * time as any other call on buffers of its own. Unless a call says otherwise,
+ * outputs must not overlap inputs or each other.
+ */
+
+/*
+ * pka_step_tables -- the tables of one step, made on the GPU from the
+ * requests' lengths. Request r has c = ctx_lens[r] cached and n =
+ * query_lens[r] new tokens; with bs = block_size
+ *     seq_lens[r]            = c + n
+ *     query_start_loc[r + 1] = sum of query_lens[0 .. r],  query_start_loc[0] = 0
+ *     need_r                 = ceil((c + n) / bs) - ceil(c / bs)  new pages
+ *     block_table[r][ceil(c / bs) + j] = free_pages[head + sum of need_i, i < r, + j],  0 <= j < need_r
+ *     *free_head_out         = head + sum of all need_r,  head = *free_head
+ * and for new token t of request r at position p = c + (t - query_start_loc[r])
+ *     positions[t]    = p
+ *     slot_mapping[t] = block_table[r][p / bs] * bs + p % bs   (-1 where that page's id is negative)
+ * Rows [query_start_loc[B], num_tokens) of a padded step get position -1 and
+ * slot -1: the cache writes skip them.
+ *
+ *   ctx_lens, query_lens  device int32 [num_reqs], both >= 0
+ *   num_tokens            rows of positions and slot_mapping, >= the sum of query_lens
+ *   block_table           device int32 [num_reqs, max_blocks_per_req]; the entries of cached pages
+ *                         are read, those of new pages written, all others left as they are
+ *   free_pages            device int32 [num_free_pages], of which [head, num_free_pages) are free
+ *   free_head, free_head_out  device int32; may be the same address
+ *   query_start_loc       device int32 [num_reqs + 1]
+ *   seq_lens              device int32 [num_reqs]; must not be ctx_lens or query_lens
+ *   positions             device int32 [num_tokens], or NULL
+ *   slot_mapping          device int64 [num_tokens]
+ * All or nothing: a negative length (PKA_DEVERR_QUERY_LEN, PKA_DEVERR_SEQ_LEN),
+ * a request longer than max_blocks_per_req pages (PKA_DEVERR_BLOCK_TABLE), more
+ * new tokens than num_tokens (PKA_DEVERR_QUERY_START_LOC) or too few free pages
+ * (PKA_DEVERR_CAPACITY) set the bit and take nothing: the table is left as it
+ * is, *free_head_out = head, query_start_loc and seq_lens are 0 and all
+ * positions and slots -1.
+ * num_reqs <= 4096 and max_blocks_per_req * block_size <= INT32_MAX, else
+ * PKA_ERR_UNSUPPORTED.
+ */
+PKA_API pka_status pka_step_tables(const int32_t *ctx_lens, const int32_t *query_lens, int num_reqs,
+                                   int64_t num_tokens, int32_t *block_table, int max_blocks_per_req, int block_size,
+                                   const int32_t *free_pages, int num_free_pages, const int32_t *free_head,
+                                   int32_t *free_head_out, int32_t *query_start_loc, int32_t *seq_lens,
+                                   int32_t *positions, int64_t *slot_mapping, int32_t *error_word, void *stream);
+
+/*
+ * pka_qk_rope_cache_write / _fp8 -- norms of each query and key head, the
+ * position rotation and the cache write of the new tokens, in one pass.
+ * For every head x of q and k (weight w, without weights y = x):
+ *     y_i = x_i / sqrt(mean_j(x_j^2) + eps) * w_i
+ * then, for the first rotary_dim elements and c, s the cosines and sines of
+ * the token's position, the pairs
+ *     (a, b) = (y[i], y[i + rotary_dim / 2])  interleaved == 0
+ *              (y[2 i], y[2 i + 1])           interleaved == 1,   0 <= i < rotary_dim / 2
+ * become (a c_i - b s_i, b c_i + a s_i). Arithmetic is float32 with one
+ * rounding at the end. q goes to q_out; k and v go to the token's cache slot
+ * as in pka_cache_write (v unchanged), or as E4M3 codes of k / k_scale and
+ * v / v_scale as in pka_cache_write_fp8 (k is not rounded to bf16 in between),
+ * and to k_out / v_out in bf16 where those are given.
+ *
+ *   q, k, v        device bf16; row t at t * q_stride (k_stride, v_stride) elements, its
+ *                  num_q_heads (num_kv_heads) heads packed: slices of one
+ *                  [num_tokens, (Hq + 2 Hkv) * d] projection, or tensors of their own.
+ *                  Strides >= the row and multiples of 8, bases 16-byte aligned.
+ *   q_weight, k_weight  device bf16 [head_dim], both or neither; eps >= 0
+ *   cos_sin        device float32 [max_position, rotary_dim]: rotary_dim / 2 cosines, then as many
+ *                  sines; may be NULL when rotary_dim == 0
+ *   positions      device int32 [num_tokens]. A row with a negative position is skipped: nothing of
+ *                  it is written. One >= max_position too, with PKA_DEVERR_INDEX (when rotary_dim > 0).
+ *   slot_mapping   device int64 [num_tokens]: a negative slot leaves the cache alone (q_out, k_out
+ *                  and v_out are written); one past the cache too, with PKA_DEVERR_SLOT
+ *   q_out          device bf16 [num_tokens, Hq, d]; may be q itself when q_stride == Hq * d
+ *   k_out, v_out   device bf16 [num_tokens, Hkv, d], or NULL; may be k (v) itself likewise
+ *   k_cache, v_cache  device [num_blocks, Hkv, block_size, d] bf16 (_fp8: uint8 codes)
+ * Two tokens with the same slot: one of them is kept, element by element.
+ * head_dim a multiple of 8 up to 256, rotary_dim a multiple of 16 up to
+ * head_dim, else PKA_ERR_UNSUPPORTED.
+ */
+PKA_API pka_status pka_qk_rope_cache_write(const void *q, const void *k, const void *v, int64_t q_stride,
+                                           int64_t k_stride, int64_t v_stride, const void *q_weight,
+                                           const void *k_weight, float eps, const float *cos_sin, int rotary_dim,
+                                           int max_position, int interleaved, const int32_t *positions,
+                                           const int64_t *slot_mapping, int64_t num_tokens, int num_q_heads,
+                                           int num_kv_heads, int head_dim, void *q_out, void *k_out, void *v_out,
+                                           void *k_cache, void *v_cache, int64_t num_blocks, int block_size,
+                                           int32_t *error_word, void *stream);
+PKA_API pka_status pka_qk_rope_cache_write_fp8(const void *q, const void *k, const void *v, int64_t q_stride,
+                                               int64_t k_stride, int64_t v_stride, const void *q_weight,
+                                               const void *k_weight, float eps, const float *cos_sin, int rotary_dim,
+                                               int max_position, int interleaved, const int32_t *positions,
+                                               const int64_t *slot_mapping, int64_t num_tokens, int num_q_heads,
+                                               int num_kv_heads, int head_dim, void *q_out, void *k_out, void *v_out,
+                                               void *k_cache, void *v_cache, int64_t num_blocks, int block_size,
+                                               float k_scale, float v_scale, int32_t *error_word, void *stream);
+
+/*
+ * pka_page_bounds -- element-wise bounds of the keys of every page whose last
+ * slot is in slot_mapping (call it after the cache write of a step; a page's
+ * earlier slots must hold its earlier tokens, as they do when a request's
+ * tokens arrive in order). With lo, hi the smallest and largest value of each
+ * element over the page's block_size keys, a the largest magnitude and 2^e the
+ * least power of two with a <= 127 * 2^e and e >= -60:
+ *     bounds[b][h][0][i] = floor(lo_i / 2^e),  bounds[b][h][1][i] = ceil(hi_i / 2^e)
+ *     bound_scales[b][h] = 2^e
+ * so bounds * bound_scales encloses the page's keys (exactly, for keys of
+ * magnitude 2^-60 and more). A page with a NaN or an infinity gets bounds 0
+ * and the scale +infinity. Pages that are not filled are left as they are.
+ *
+ *   k_cache       device [num_blocks, Hkv, block_size, d], cache_dtype 1 = bf16, 2 = E4M3 codes
+ *                 (bounds then in units of one code, whatever the cache's k_scale)
+ *   slot_mapping  device int64 [num_tokens]; negative slots are skipped, slots past the cache
+ *                 set PKA_DEVERR_SLOT
+ *   bounds        device int8 [num_blocks, Hkv, 2, d], 16-byte aligned
+ *   bound_scales  device float32 [num_blocks, Hkv]
+ * head_dim 64 or 128, else PKA_ERR_UNSUPPORTED.
+ */
+PKA_API pka_status pka_page_bounds(const void *k_cache, int cache_dtype, const int64_t *slot_mapping,
+                                   int64_t num_tokens, int num_kv_heads, int head_dim, int64_t num_blocks,
+                                   int block_size, int8_t *bounds, float *bound_scales, int32_t *error_word,
+                                   void *stream);
+
+/*
+ * pka_select_pages -- the pages each new token reads. Token t of request r at
+ * position p (= seq_lens[r] - query_start_loc[r + 1] + t) may read pages
+ * 0 .. P, P = p / block_size its own. When there are at most num_pages of them
+ * all are selected; otherwise the first num_first, the last num_last (its own
+ * among them) and the best of the rest, num_pages together. A page's score for
+ * a kv head is the largest over the head's group of query heads h of
+ *     2^x_h * bound_scales * sum_i max(c_i * lo_i, c_i * hi_i)
+ * where c = round(q_h / 2^x_h), half to even, 2^x_h the least power of two with
+ * max |q_h| <= 127 * 2^x_h and x_h >= -60, and lo, hi the page's bounds: an
+ * upper bound of <c * 2^x_h, key> over the page's keys. The sum is an integer
+ * and the factors are powers of two, so a score is exact and of equal scores
+ * the lower page is taken. A head with a NaN or an infinity scores 0
+ * everywhere; a page with the scale +infinity comes first. The score of a page
+ * before the last num_last ones is read from its bounds, so those pages have
+ * to have been through pka_page_bounds.
+ *
+ *   q              device bf16 [num_tokens, Hq, d]
+ *   bounds, bound_scales  as pka_page_bounds writes them
+ *   block_table    device int32 [num_reqs, max_blocks_per_req]
+ *   query_start_loc, seq_lens  device int32 [num_reqs + 1], [num_reqs]; requests without new
+ *                  tokens are allowed, and rows behind the last request's: those of `selected`
+ *                  are left as they are
+ *   num_first >= 0, num_last >= 1, num_first + num_last <= num_pages
+ *   max_seq_len    host upper bound of seq_lens
+ *   selected       device int32 [num_tokens, Hkv, num_pages]: ascending page indices of the request
+ *                  (columns of its block table row), then -1
+ * A seq_len that does not fit its request sets PKA_DEVERR_SEQ_LEN, a block id
+ * outside the cache PKA_DEVERR_BLOCK_ID.
+ * head_dim 64 or 128, Hq / Hkv <= 16, max_seq_len / block_size <= 32768, num_tokens <= 2^27, else
+ * PKA_ERR_UNSUPPORTED.
+ */
+PKA_API pka_status pka_select_pages(const void *q, const int8_t *bounds, const float *bound_scales,
+                                    const int32_t *block_table, int max_blocks_per_req,
+                                    const int32_t *query_start_loc, const int32_t *seq_lens, int num_reqs,
+                                    int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int64_t num_blocks, int block_size, int num_first, int num_last, int max_seq_len,
+                                    int num_pages, int32_t *selected, int32_t *error_word, void *stream);
+
+/*
+ * pka_sparse_attn_forward / _fp8 -- attention of each new token over the pages
+ * listed for it. Token t at position p of request r, query head h of kv head g:
+ * the definition of pka_paged_attn_forward with the keys restricted to those
+ * at positions j <= p in the pages selected[t][g][0 .. count - 1] of the
+ * request. A list ends at its first negative entry and ascends strictly up to
+ * at most the token's own page; an entry that does not ends the list too and
+ * sets PKA_DEVERR_INDEX. An empty list gives out = 0 and lse = -infinity. With
+ * every page listed the result is the dense one. Reads only the cache (the new
+ * tokens' keys and values must have been written).
+ *
+ *   q, out         device bf16 [num_tokens, Hq, d];  lse device float32 [num_tokens, Hq], or NULL
+ *   k_cache, v_cache  device [num_blocks, Hkv, block_size, d] bf16; _fp8: E4M3 codes with
+ *                  k_scale and v_scale (finite, > 0), q as in pka_paged_attn_forward_fp8
+ *   block_table, query_start_loc, seq_lens, max_seq_len  as in pka_select_pages (rows behind
+ *                  the last request are left as they are)
+ *   selected       device int32 [num_tokens, Hkv, num_pages]
+ *   scale          finite and > 0
+ * head_dim 64 or 128 (_fp8: 128), Hq / Hkv <= 16, block_size a power of two in [8, 128], else
+ * PKA_ERR_UNSUPPORTED.
+ */
+PKA_API pka_status pka_sparse_attn_forward(const void *q, const void *k_cache, const void *v_cache,
+                                           const int32_t *block_table, int max_blocks_per_req,
+                                           const int32_t *query_start_loc, const int32_t *seq_lens, int num_reqs,
+                                           int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                           int64_t num_blocks, int block_size, float scale, const int32_t *selected,
+                                           int num_pages, int max_seq_len, void *out, float *lse,
+                                           int32_t *error_word, void *stream);
+PKA_API pka_status pka_sparse_attn_forward_fp8(const void *q, const void *k_cache, const void *v_cache,
+                                               const int32_t *block_table, int max_blocks_per_req,
+                                               const int32_t *query_start_loc, const int32_t *seq_lens, int num_reqs,
+                                               int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                               int64_t num_blocks, int block_size, float scale, float k_scale,
+                                               float v_scale, const int32_t *selected, int num_pages, int max_seq_len,
+                                               void *out, float *lse, int32_t *error_word, void *stream);
 
 /*
  * pka_selftest_wait -- the library's bounded pipeline wait (the one every

@@ -43,6 +43,13 @@ bool decode_mla_tc_supported(int Hq);
 cudaError_t launch_decode_mla_tc(const CUtensorMap& kvmap, const CUtensorMap& qmap, const CUtensorMap& gmap,
                                  const DecodeMlaParams& p, int num_sms, cudaStream_t stream);
 
+cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream);
+cudaError_t launch_qk_rope(const QkRopeParams& p, bool fp8, int num_sms, cudaStream_t stream);
+cudaError_t launch_page_bounds(const PageBoundsParams& p, bool fp8, cudaStream_t stream);
+cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_sparse_attn(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnParams& p, int head_dim,
+                               bool fp8, int num_sms, cudaStream_t stream);
+
 // MLA decode units per (request, split): on the tensor-core kernel two value
 // halves per group of 128 heads, otherwise one unit per 64-head group.
 static int mla_units_per_pair(int Hq) {
@@ -110,6 +117,22 @@ bool encode_rows_u8(CUtensorMap* map, const void* base, uint64_t rows, uint32_t 
     cuuint32_t box[2] = {128, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D bf16 view of dense rows [rows, D] as [D / 64 segments, rows, 64 columns],
+// read in boxes of 64 columns x box_rows rows x `segments` (128-byte swizzle):
+// one box gives whole rows, segment after segment.
+bool encode_segments(CUtensorMap* map, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows,
+                     uint32_t segments) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {64, rows, D / 64};
+    cuuint64_t strides[2] = {D * 2, 128};
+    cuuint32_t box[3] = {64, box_rows, segments};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1028,6 +1051,318 @@ pka_status pka_get_error(const void* workspace, int32_t* code_out, void* stream)
     if (cudaStreamSynchronize(st) != cudaSuccess) return PKA_ERR_CUDA;
     if (code_out) *code_out = code;
     return code ? PKA_ERR_DEVICE_METADATA : PKA_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the block-sparse step
+
+namespace {
+
+bool positive_finite(float x) { return std::isfinite(x) && x > 0.f; }
+
+pka_status qk_rope_impl(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
+                        int rotary_dim, int max_position, int interleaved, const int32_t* positions,
+                        const int64_t* slot_mapping, int64_t num_tokens, int num_q_heads, int num_kv_heads,
+                        int head_dim, void* q_out, void* k_out, void* v_out, void* k_cache, void* v_cache,
+                        int64_t num_blocks, int block_size, int32_t* error_word, void* stream, const CacheFormat& cf) {
+    if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || rotary_dim < 0 ||
+        num_blocks <= 0 || block_size <= 0)
+        return PKA_ERR_INVALID_ARG;
+    if (cf.fp8 && (!positive_finite(cf.k_scale) || !positive_finite(cf.v_scale))) return PKA_ERR_INVALID_ARG;
+    if ((q_weight == nullptr) != (k_weight == nullptr)) return PKA_ERR_INVALID_ARG;
+    if (q_weight && (!std::isfinite(eps) || eps < 0.f)) return PKA_ERR_INVALID_ARG;
+    if (rotary_dim > head_dim || (rotary_dim > 0 && (!cos_sin || max_position <= 0))) return PKA_ERR_INVALID_ARG;
+    if (interleaved != 0 && interleaved != 1) return PKA_ERR_INVALID_ARG;
+    if (head_dim % 8 != 0 || head_dim > 256 || rotary_dim % 16 != 0) return PKA_ERR_UNSUPPORTED;
+    if (num_blocks > INT64_MAX / block_size) return PKA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKA_OK;
+    if (!q || !k || !v || !positions || !slot_mapping || !q_out || !k_cache || !v_cache) return PKA_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)num_q_heads * head_dim || k_stride < (int64_t)num_kv_heads * head_dim ||
+        v_stride < (int64_t)num_kv_heads * head_dim)
+        return PKA_ERR_INVALID_ARG;
+    // 16-byte pieces: strides of 8 elements, aligned bases
+    if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0) return PKA_ERR_UNSUPPORTED;
+    for (const void* x : {q, k, v, q_weight, k_weight, static_cast<const void*>(cos_sin),
+                          static_cast<const void*>(q_out), static_cast<const void*>(k_out),
+                          static_cast<const void*>(v_out), static_cast<const void*>(k_cache),
+                          static_cast<const void*>(v_cache)})
+        if (!aligned(x, 16)) return PKA_ERR_INVALID_ARG;
+    if (!aligned(positions, 4) || !aligned(slot_mapping, 8) || !aligned(error_word, 4)) return PKA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PKA_ERR_CUDA;
+    QkRopeParams p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+    p.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
+    p.cos_sin = cos_sin;
+    p.positions = positions;
+    p.slots = slot_mapping;
+    p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.k_out = static_cast<__nv_bfloat16*>(k_out);
+    p.v_out = static_cast<__nv_bfloat16*>(v_out);
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.err = error_word;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.num_tokens = num_tokens;
+    p.num_slots = num_blocks * block_size;
+    p.Hq = num_q_heads;
+    p.Hkv = num_kv_heads;
+    p.head_dim = head_dim;
+    p.rotary = rotary_dim;
+    p.max_position = max_position;
+    p.interleaved = interleaved;
+    p.block_size = block_size;
+    p.eps = eps;
+    p.k_scale = cf.k_scale;
+    p.v_scale = cf.v_scale;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed(PKA_KERNEL_QK_ROPE, st, [&] { return launch_qk_rope(p, cf.fp8, sms, st); }));
+}
+
+// What page selection and attention over selected pages ask of their batch.
+pka_status check_sparse_batch(int num_reqs, int num_tokens, int Hq, int Hkv, int head_dim, int64_t num_blocks,
+                              int block_size, int max_blocks, int max_seq_len, int num_pages) {
+    if (num_reqs <= 0 || num_tokens < 0 || Hq <= 0 || Hkv <= 0 || head_dim <= 0 || num_blocks <= 0 ||
+        block_size <= 0 || max_blocks <= 0 || max_seq_len <= 0 || num_pages <= 0)
+        return PKA_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0) return PKA_ERR_INVALID_ARG;
+    if ((int64_t)max_blocks * block_size < max_seq_len) return PKA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PKA_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 16 || Hkv > 65535 || num_tokens > (1 << 27)) return PKA_ERR_UNSUPPORTED;
+    return PKA_OK;
+}
+
+pka_status sparse_attn_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            int max_blocks_per_req, const int32_t* query_start_loc, const int32_t* seq_lens,
+                            int num_reqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                            int64_t num_blocks, int block_size, float scale, const int32_t* selected, int num_pages,
+                            int max_seq_len, void* out, float* lse, int32_t* error_word, void* stream,
+                            const CacheFormat& cf) {
+    const pka_status sc = check_sparse_batch(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks,
+                                             block_size, max_blocks_per_req, max_seq_len, num_pages);
+    if (sc != PKA_OK) return sc;
+    if (!positive_finite(scale)) return PKA_ERR_INVALID_ARG;
+    if (cf.fp8) {
+        if (head_dim != 128) return PKA_ERR_UNSUPPORTED;
+        if (!positive_finite(cf.k_scale) || !positive_finite(cf.v_scale)) return PKA_ERR_INVALID_ARG;
+    }
+    if (!pow2(block_size) || block_size < 8 || block_size > 128) return PKA_ERR_UNSUPPORTED;
+    if (num_blocks > INT32_MAX || num_blocks * block_size > INT32_MAX / num_kv_heads) return PKA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKA_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !query_start_loc || !seq_lens || !selected || !out)
+        return PKA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(block_table, 4) || !aligned(query_start_loc, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4) ||
+        !aligned(error_word, 4))
+        return PKA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PKA_ERR_CUDA;
+    const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * block_size;
+    const uint32_t br = (uint32_t)std::min(block_size, 16);
+    CUtensorMap km, vm;
+    const uint32_t segments = br == 16 ? (uint32_t)head_dim / 64 : 1;
+    const bool ok = cf.fp8 ? encode_rows_u8(&km, k_cache, rows, br) && encode_rows_u8(&vm, v_cache, rows, br)
+                           : encode_segments(&km, k_cache, rows, (uint64_t)head_dim, br, segments) &&
+                                 encode_segments(&vm, v_cache, rows, (uint64_t)head_dim, br, segments);
+    if (!ok) return PKA_ERR_CUDA;
+    SparseAttnParams p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.block_table = block_table;
+    p.qsl = query_start_loc;
+    p.seq_lens = seq_lens;
+    p.sel = selected;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.err = error_word;
+    p.num_blocks = num_blocks;
+    p.num_tokens = num_tokens;
+    p.num_reqs = num_reqs;
+    p.max_blocks = max_blocks_per_req;
+    p.Hq = num_q_heads;
+    p.Hkv = num_kv_heads;
+    p.G = num_q_heads / num_kv_heads;
+    p.bs = block_size;
+    p.num_pages = num_pages;
+    p.max_seq_len = max_seq_len;
+    p.scale_log2 = scale * 1.4426950408889634f * (cf.fp8 ? cf.k_scale : 1.f);
+    p.v_scale = cf.fp8 ? cf.v_scale : 1.f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(
+        timed(PKA_KERNEL_SPARSE_ATTN, st, [&] { return launch_sparse_attn(km, vm, p, head_dim, cf.fp8, sms, st); }));
+}
+
+}  // namespace
+
+extern "C" {
+
+pka_status pka_step_tables(const int32_t* ctx_lens, const int32_t* query_lens, int num_reqs, int64_t num_tokens,
+                           int32_t* block_table, int max_blocks_per_req, int block_size, const int32_t* free_pages,
+                           int num_free_pages, const int32_t* free_head, int32_t* free_head_out,
+                           int32_t* query_start_loc, int32_t* seq_lens, int32_t* positions, int64_t* slot_mapping,
+                           int32_t* error_word, void* stream) {
+    if (num_reqs <= 0 || num_tokens < 0 || max_blocks_per_req <= 0 || block_size <= 0 || num_free_pages < 0)
+        return PKA_ERR_INVALID_ARG;
+    if (!ctx_lens || !query_lens || !block_table || !free_head || !free_head_out || !query_start_loc || !seq_lens ||
+        (num_tokens > 0 && !slot_mapping) || (num_free_pages > 0 && !free_pages))
+        return PKA_ERR_INVALID_ARG;
+    if (seq_lens == ctx_lens || seq_lens == query_lens || query_start_loc == ctx_lens || query_start_loc == query_lens)
+        return PKA_ERR_INVALID_ARG;  // the lengths are read again while these are written
+    if (num_reqs > kMaxRequests) return PKA_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_req * block_size > INT32_MAX || num_tokens > INT32_MAX) return PKA_ERR_UNSUPPORTED;
+    if (!aligned(ctx_lens, 4) || !aligned(query_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+        !aligned(free_head, 4) || !aligned(free_head_out, 4) || !aligned(query_start_loc, 4) ||
+        !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(slot_mapping, 8) || !aligned(error_word, 4))
+        return PKA_ERR_INVALID_ARG;
+    StepTablesParams p;
+    p.ctx_lens = ctx_lens;
+    p.query_lens = query_lens;
+    p.free_pages = free_pages;
+    p.free_head = free_head;
+    p.free_head_out = free_head_out;
+    p.block_table = block_table;
+    p.qsl = query_start_loc;
+    p.seq_lens = seq_lens;
+    p.positions = positions;
+    p.slots = slot_mapping;
+    p.err = error_word;
+    p.num_tokens = num_tokens;
+    p.num_reqs = num_reqs;
+    p.max_blocks = max_blocks_per_req;
+    p.block_size = block_size;
+    p.num_free = num_free_pages;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed(PKA_KERNEL_STEP_TABLES, st, [&] { return launch_step_tables(p, st); }));
+}
+
+pka_status pka_qk_rope_cache_write(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                   int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+                                   const float* cos_sin, int rotary_dim, int max_position, int interleaved,
+                                   const int32_t* positions, const int64_t* slot_mapping, int64_t num_tokens,
+                                   int num_q_heads, int num_kv_heads, int head_dim, void* q_out, void* k_out,
+                                   void* v_out, void* k_cache, void* v_cache, int64_t num_blocks, int block_size,
+                                   int32_t* error_word, void* stream) {
+    return qk_rope_impl(q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, cos_sin, rotary_dim,
+                        max_position, interleaved, positions, slot_mapping, num_tokens, num_q_heads, num_kv_heads,
+                        head_dim, q_out, k_out, v_out, k_cache, v_cache, num_blocks, block_size, error_word, stream,
+                        CacheFormat{false, 1.f, 1.f});
+}
+
+pka_status pka_qk_rope_cache_write_fp8(const void* q, const void* k, const void* v, int64_t q_stride,
+                                       int64_t k_stride, int64_t v_stride, const void* q_weight, const void* k_weight,
+                                       float eps, const float* cos_sin, int rotary_dim, int max_position,
+                                       int interleaved, const int32_t* positions, const int64_t* slot_mapping,
+                                       int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                       void* q_out, void* k_out, void* v_out, void* k_cache, void* v_cache,
+                                       int64_t num_blocks, int block_size, float k_scale, float v_scale,
+                                       int32_t* error_word, void* stream) {
+    return qk_rope_impl(q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, cos_sin, rotary_dim,
+                        max_position, interleaved, positions, slot_mapping, num_tokens, num_q_heads, num_kv_heads,
+                        head_dim, q_out, k_out, v_out, k_cache, v_cache, num_blocks, block_size, error_word, stream,
+                        CacheFormat{true, k_scale, v_scale});
+}
+
+pka_status pka_page_bounds(const void* k_cache, int cache_dtype, const int64_t* slot_mapping, int64_t num_tokens,
+                           int num_kv_heads, int head_dim, int64_t num_blocks, int block_size, int8_t* bounds,
+                           float* bound_scales, int32_t* error_word, void* stream) {
+    if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || block_size <= 0 ||
+        (cache_dtype != 1 && cache_dtype != 2))
+        return PKA_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || num_kv_heads > 65535) return PKA_ERR_UNSUPPORTED;
+    if (num_blocks > INT64_MAX / block_size) return PKA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKA_OK;
+    if (!k_cache || !slot_mapping || !bounds || !bound_scales) return PKA_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(slot_mapping, 8) || !aligned(bounds, 16) || !aligned(bound_scales, 4) ||
+        !aligned(error_word, 4))
+        return PKA_ERR_INVALID_ARG;
+    PageBoundsParams p;
+    p.k_cache = k_cache;
+    p.slots = slot_mapping;
+    p.bounds = bounds;
+    p.scales = bound_scales;
+    p.err = error_word;
+    p.num_tokens = num_tokens;
+    p.num_slots = num_blocks * block_size;
+    p.Hkv = num_kv_heads;
+    p.block_size = block_size;
+    p.head_dim = head_dim;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(
+        timed(PKA_KERNEL_PAGE_BOUNDS, st, [&] { return launch_page_bounds(p, cache_dtype == 2, st); }));
+}
+
+pka_status pka_select_pages(const void* q, const int8_t* bounds, const float* bound_scales,
+                            const int32_t* block_table, int max_blocks_per_req, const int32_t* query_start_loc,
+                            const int32_t* seq_lens, int num_reqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                            int head_dim, int64_t num_blocks, int block_size, int num_first, int num_last,
+                            int max_seq_len, int num_pages, int32_t* selected, int32_t* error_word, void* stream) {
+    const pka_status sc = check_sparse_batch(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks,
+                                             block_size, max_blocks_per_req, max_seq_len, num_pages);
+    if (sc != PKA_OK) return sc;
+    if (num_first < 0 || num_last < 1 || num_first > num_pages - num_last) return PKA_ERR_INVALID_ARG;
+    if (((int64_t)max_seq_len + block_size - 1) / block_size > kPageSelectMaxPages) return PKA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKA_OK;
+    if (!q || !bounds || !bound_scales || !block_table || !query_start_loc || !seq_lens || !selected)
+        return PKA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(bound_scales, 4) || !aligned(block_table, 4) ||
+        !aligned(query_start_loc, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4) || !aligned(error_word, 4))
+        return PKA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PKA_ERR_CUDA;
+    PageSelectParams p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.bounds = bounds;
+    p.scales = bound_scales;
+    p.block_table = block_table;
+    p.qsl = query_start_loc;
+    p.seq_lens = seq_lens;
+    p.sel = selected;
+    p.err = error_word;
+    p.num_blocks = num_blocks;
+    p.num_tokens = num_tokens;
+    p.num_reqs = num_reqs;
+    p.max_blocks = max_blocks_per_req;
+    p.Hq = num_q_heads;
+    p.Hkv = num_kv_heads;
+    p.G = num_q_heads / num_kv_heads;
+    p.block_size = block_size;
+    p.num_first = num_first;
+    p.num_last = num_last;
+    p.num_pages = num_pages;
+    p.max_seq_len = max_seq_len;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(
+        timed(PKA_KERNEL_PAGE_SELECT, st, [&] { return launch_page_select(p, head_dim, sms, st); }));
+}
+
+pka_status pka_sparse_attn_forward(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, int max_blocks_per_req, const int32_t* query_start_loc,
+                                   const int32_t* seq_lens, int num_reqs, int num_tokens, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int64_t num_blocks, int block_size, float scale,
+                                   const int32_t* selected, int num_pages, int max_seq_len, void* out, float* lse,
+                                   int32_t* error_word, void* stream) {
+    return sparse_attn_impl(q, k_cache, v_cache, block_table, max_blocks_per_req, query_start_loc, seq_lens, num_reqs,
+                            num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, selected,
+                            num_pages, max_seq_len, out, lse, error_word, stream, CacheFormat{false, 1.f, 1.f});
+}
+
+pka_status pka_sparse_attn_forward_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_table, int max_blocks_per_req,
+                                       const int32_t* query_start_loc, const int32_t* seq_lens, int num_reqs,
+                                       int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                       int64_t num_blocks, int block_size, float scale, float k_scale, float v_scale,
+                                       const int32_t* selected, int num_pages, int max_seq_len, void* out, float* lse,
+                                       int32_t* error_word, void* stream) {
+    return sparse_attn_impl(q, k_cache, v_cache, block_table, max_blocks_per_req, query_start_loc, seq_lens, num_reqs,
+                            num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, selected,
+                            num_pages, max_seq_len, out, lse, error_word, stream,
+                            CacheFormat{true, k_scale, v_scale});
 }
 
 }  // extern "C"

@@ -40,15 +40,6 @@ struct CacheWriteParams {
     int32_t* err;
 };
 
-// Four floats -> four E4M3 codes (x / s, RN-even, saturating), lowest first.
-PKA_DEVICE uint32_t quantize4(float a, float b, float c, float d, float s) {
-    uint32_t lo, hi;
-    const float qa = __fdiv_rn(a, s), qb = __fdiv_rn(b, s), qc = __fdiv_rn(c, s), qd = __fdiv_rn(d, s);
-    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(lo) : "f"(qa), "f"(qb));
-    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(hi) : "f"(qc), "f"(qd));
-    return lo | (hi << 16);
-}
-
 PKA_DEVICE uint2 quantize8(uint4 x, float s) {
     uint2 r;
     r.x = quantize4(bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y), s);

@@ -7,6 +7,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -283,7 +284,6 @@ PKA_DEVICE void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two floats -> bf16x2 (round to nearest even); `lo` lands in the low half.
 // Two E4M3 codes (low byte -> low half) to an f16 pair; exact (every E4M3
 // value is an f16 value).
 PKA_DEVICE uint32_t e4m3x2_to_f16x2(uint32_t x16) {
@@ -292,6 +292,18 @@ PKA_DEVICE uint32_t e4m3x2_to_f16x2(uint32_t x16) {
     return d;
 }
 
+PKA_DEVICE __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+
+// Four floats -> four E4M3 codes (x / s, RN-even, saturating), lowest first.
+PKA_DEVICE uint32_t quantize4(float a, float b, float c, float d, float s) {
+    uint32_t lo, hi;
+    const float qa = __fdiv_rn(a, s), qb = __fdiv_rn(b, s), qc = __fdiv_rn(c, s), qd = __fdiv_rn(d, s);
+    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(lo) : "f"(qa), "f"(qb));
+    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(hi) : "f"(qc), "f"(qd));
+    return lo | (hi << 16);
+}
+
+// Two floats -> bf16x2 (round to nearest even); `lo` lands in the low half.
 PKA_DEVICE uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -307,6 +319,35 @@ PKA_DEVICE void st_global_v8(void* p, uint32_t a0, uint32_t a1, uint32_t a2, uin
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a0), "r"(a1), "r"(a2),
                  "r"(a3), "r"(a4), "r"(a5), "r"(a6), "r"(a7)
                  : "memory");
+}
+
+// bf16 pair -> f16 pair (finite results saturate at the f16 maximum).
+PKA_DEVICE uint32_t bf16x2_to_f16x2(uint32_t w) {
+    uint32_t d;
+    const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+PKA_DEVICE uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// D(16x8 f32) += A(16x16 f16, row) * B(16x8 f16, col)
+PKA_DEVICE void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+PKA_DEVICE uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
 }
 
 // max(a, b, c) in one instruction (three-input max, sm_100 and later).
@@ -371,7 +412,115 @@ PKA_DEVICE void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependen
 // with a 1024-byte aligned base): chunks are XOR-ed with row % 8.
 PKA_DEVICE uint32_t sw128(uint32_t row, uint32_t c) { return row * 128u + ((c ^ (row & 7u)) << 4); }
 
+// ---------------------------------------------------------------- clusters
+PKA_DEVICE uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+PKA_DEVICE uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+// All threads of all the cluster's CTAs; orders shared and global memory
+// accesses before it with those after it.
+PKA_DEVICE void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+PKA_DEVICE void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+PKA_DEVICE void cluster_barrier() {
+    cluster_arrive();
+    cluster_wait();
+}
+// Stores v where `p` lies in the shared memory of the cluster's CTA `rank`
+// (which must have started: a cluster barrier before the first such store).
+PKA_DEVICE void store_cluster(uint32_t* p, uint32_t rank, uint32_t v) {
+    asm volatile(
+        "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(
+            smem_u32(p)),
+        "r"(rank), "r"(v)
+        : "memory");
+}
+
+PKA_DEVICE float load_cluster(const float* p, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(smem_u32(p)), "r"(rank)
+                 : "memory");
+    return v;
+}
+PKA_DEVICE float4 load_cluster4(const float* p, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// ---------------------------------------------------------------- the block-sparse step
+// Largest exponent magnitude below which key bounds and query codes stop
+// following the values: 2^-60 is far below any bf16 activation that counts,
+// and products of two such units stay normal numbers.
+constexpr int kBoundMinExp = -60;
+
+// 2^e, -126 <= e <= 127.
+PKA_DEVICE float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The least e >= kBoundMinExp with a <= 127 * 2^e (a >= 0, finite, a bf16 or
+// E4M3 value: e <= 122).
+PKA_DEVICE int bound_exponent(float a) {
+    int x;
+    frexpf(a, &x);  // a = f * 2^x, 0.5 <= f < 1
+    const int e = a > 0.f ? x - 7 : kBoundMinExp;  // a <= 128 * 2^e
+    if (e < kBoundMinExp) return kBoundMinExp;
+    return a * exp2i(-e) > 127.f ? e + 1 : e;
+}
+
+// The request that owns token t (the last r with qsl[r] <= t), or -1 behind
+// the last one (t >= qsl[n]). With whole warps: every lane gets the answer.
+PKA_DEVICE int request_of(const int32_t* qsl, int n, int t) {
+    const int a = __ldg(qsl + min(t, n)), b = __ldg(qsl + min(t + 1, n));
+    if (t >= __ldg(qsl + n)) return -1;
+    if (t < n && a == t && b == t + 1) return t;  // one token per request up to here
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;  // the answer lies in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int i = lo + lane * step;
+        const uint32_t at_most = __ballot_sync(0xffffffffu, i < hi && __ldg(qsl + i) <= t);
+        const int k = at_most ? 31 - __clz(at_most) : 0;
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
 #ifdef __CUDACC__
+// Launch `kern` in clusters of `cluster` CTAs along x, as a programmatic
+// dependent (see grid_dep_wait) of the previous work on `stream`.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                                  cudaStream_t stream, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 // Launch `kern` as a programmatic dependent of the previous work on `stream`
 // (see grid_dep_wait: the kernel must call it before reading its inputs).
 template <typename... KArgs, typename... Args>

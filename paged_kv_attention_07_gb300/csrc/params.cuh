@@ -122,6 +122,81 @@ struct ExtendReduceParams {
     int num_decodes, num_extends, Hq, dv, chunk;
 };
 
+// ---- the block-sparse step
+
+struct StepTablesParams {
+    const int32_t* ctx_lens;
+    const int32_t* query_lens;
+    const int32_t* free_pages;
+    const int32_t* free_head;
+    int32_t* free_head_out;
+    int32_t* block_table;
+    int32_t* qsl;
+    int32_t* seq_lens;
+    int32_t* positions;  // or null
+    int64_t* slots;
+    int32_t* err;
+    int64_t num_tokens;
+    int num_reqs, max_blocks, block_size, num_free;
+};
+
+struct QkRopeParams {
+    const __nv_bfloat16* q;  // rows of num_heads * head_dim, `*_stride` elements apart
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    const __nv_bfloat16* q_weight;  // [head_dim], both or neither
+    const __nv_bfloat16* k_weight;
+    const float* cos_sin;  // [max_position, rotary]: cosines, then sines
+    const int32_t* positions;
+    const int64_t* slots;
+    __nv_bfloat16* q_out;
+    __nv_bfloat16* k_out;  // or null
+    __nv_bfloat16* v_out;  // or null
+    void* k_cache;
+    void* v_cache;
+    int32_t* err;
+    int64_t q_stride, k_stride, v_stride, num_tokens, num_slots;
+    int Hq, Hkv, head_dim, rotary, max_position, interleaved, block_size;
+    float eps, k_scale, v_scale;
+};
+
+struct PageBoundsParams {
+    const void* k_cache;  // [num_blocks, Hkv, bs, d] bf16 or E4M3 codes
+    const int64_t* slots;
+    int8_t* bounds;  // [num_blocks, Hkv, 2, d]
+    float* scales;   // [num_blocks, Hkv]
+    int32_t* err;
+    int64_t num_tokens, num_slots;
+    int Hkv, block_size, head_dim;
+};
+
+struct PageSelectParams {
+    const __nv_bfloat16* q;  // [T, Hq, d]
+    const int8_t* bounds;
+    const float* scales;
+    const int32_t* block_table;
+    const int32_t* qsl;
+    const int32_t* seq_lens;
+    int32_t* sel;  // [T, Hkv, num_pages]
+    int32_t* err;
+    int64_t num_blocks;
+    int num_tokens, num_reqs, max_blocks, Hq, Hkv, G, block_size, num_first, num_last, num_pages, max_seq_len;
+};
+
+struct SparseAttnParams {
+    const __nv_bfloat16* q;  // [T, Hq, d]
+    const int32_t* block_table;
+    const int32_t* qsl;
+    const int32_t* seq_lens;
+    const int32_t* sel;  // [T, Hkv, num_pages]
+    __nv_bfloat16* out;
+    float* lse;  // or null
+    int32_t* err;
+    int64_t num_blocks;
+    int num_tokens, num_reqs, max_blocks, Hq, Hkv, G, bs, num_pages, max_seq_len;
+    float scale_log2, v_scale;  // 8-bit cache: scale * k_scale, and the output's factor
+};
+
 struct FaMaps {
     CUtensorMap q;     // [T, Hq, D]  box {64, 1, 128}
     CUtensorMap knew;  // [T, Hkv, D] box {64, 1, 128}

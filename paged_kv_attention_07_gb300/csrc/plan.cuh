@@ -20,6 +20,7 @@ namespace pka {
 
 constexpr int kMaxRequests = 4096;     // planner keeps per-request metadata in smem
 constexpr int kDecodeMinSplit = 256;   // fewest keys per GQA decode split
+constexpr int kPageSelectMaxPages = 32768;  // the page selection keeps a request's scores in smem
 constexpr int kFaBlockM = 128;         // query rows per prefill/extend query tile (TMEM lanes)
 constexpr int kFaItemTiles = 2;        // query tiles per prefill/extend item
 constexpr int kFaItemRows = kFaBlockM * kFaItemTiles;

@@ -1,0 +1,181 @@
+// step_tables.cu -- the metadata of one serving step, made on the GPU from the
+// requests' lengths: new pages taken from a free list into the block table,
+// query_start_loc, seq_lens, and each new token's position and cache slot.
+//
+//   seq_r   = ctx_r + new_r
+//   need_r  = ceil(seq_r / bs) - ceil(ctx_r / bs)      pages the request takes
+//   page j of request r's need is free_pages[head + sum_{i<r} need_i + j]
+//   token t of request r: p = ctx_r + (t - qsl_r), slot = table[r][p / bs] * bs + p % bs
+//
+// Two prefix sums over at most kMaxRequests requests, then one independent
+// search and write per token. The bytes are few (12 per token), so the cost is
+// latency: one launch of one cluster. Every CTA of the cluster repeats the
+// prefix sums in its own shared memory (a few kilobytes from L2) and writes its
+// share of the tokens and pages; the page of a token on a new page comes from
+// the free list itself, not from the table entry another CTA writes. The
+// cluster barrier separates the reads of the list's head from its update, so
+// the head can be advanced in place.
+#include "common.cuh"
+#include "params.cuh"
+#include "plan.cuh"
+
+namespace pka {
+
+namespace {
+
+constexpr int kStThreads = 1024;
+// Tokens from which the writes are spread over a cluster of kStCluster CTAs.
+constexpr int kStCluster = 8;
+constexpr int64_t kStClusterTokens = 4096;
+
+// Last r in [0, n) with first[r] <= x (first[0] == 0 <= x).
+PKA_DEVICE int last_at_most(const int32_t* first, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParams p) {
+    __shared__ int32_t s_qsl[kMaxRequests];    // first token of each request
+    __shared__ int32_t s_first[kMaxRequests];  // pages taken by the requests before it
+    __shared__ long long s_tok[33], s_pag[33];
+    grid_dep_launch();
+    grid_dep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ncta = gridDim.x, cta = blockIdx.x;
+    const int B = p.num_reqs, bs = p.block_size;
+    const int head = *p.free_head;
+    const long long longest = (long long)p.max_blocks * bs;
+
+    // ---- lengths: validate, sum, scan (each thread a contiguous run of requests)
+    const int per = (B + kStThreads - 1) / kStThreads;  // <= kMaxRequests / kStThreads
+    const int r0 = min(B, tid * per), r1 = min(B, r0 + per);
+    int err = 0;
+    long long tok = 0, pag = 0;
+    constexpr int kPer = kMaxRequests / kStThreads;
+    int nw[kPer], nd[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        nw[i] = nd[i] = 0;
+        const int r = r0 + i;
+        if (r >= r1) continue;
+        const int c = p.ctx_lens[r], q = p.query_lens[r];
+        const long long s = (long long)c + q;
+        if (q < 0) err |= PKA_DEVERR_QUERY_LEN;
+        if (c < 0) err |= PKA_DEVERR_SEQ_LEN;
+        if (s > longest) err |= PKA_DEVERR_BLOCK_TABLE;
+        if (q < 0 || c < 0 || s > longest) continue;
+        nw[i] = q;
+        nd[i] = (int)((s + bs - 1) / bs) - (int)(((long long)c + bs - 1) / bs);
+        tok += q;
+        pag += nd[i];
+    }
+    long long ti = tok, pi = pag;  // inclusive scans within the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, ti, o), b = __shfl_up_sync(0xffffffffu, pi, o);
+        if (lane >= o) {
+            ti += a;
+            pi += b;
+        }
+    }
+    if (lane == 31) {
+        s_tok[warp] = ti;
+        s_pag[warp] = pi;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const long long a = s_tok[lane], b = s_pag[lane];
+        long long ai = a, bi = b;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, ai, o), y = __shfl_up_sync(0xffffffffu, bi, o);
+            if (lane >= o) {
+                ai += x;
+                bi += y;
+            }
+        }
+        s_tok[lane] = ai - a;
+        s_pag[lane] = bi - b;
+        if (lane == 31) {
+            s_tok[32] = ai;
+            s_pag[32] = bi;
+        }
+    }
+    __syncthreads();
+    const long long total = s_tok[32], taken = s_pag[32];
+    if (total > p.num_tokens) err |= PKA_DEVERR_QUERY_START_LOC;
+    if (head < 0 || taken > (long long)p.num_free - head) err |= PKA_DEVERR_CAPACITY;
+    const int any = __syncthreads_or(err);
+    if (any) {
+        // nothing is taken: empty requests and no slots, so that the calls
+        // that read these tables write and read nothing
+        if (err) set_error(p.err, err);
+        for (int r = cta * kStThreads + tid; r < B; r += ncta * kStThreads) {
+            p.qsl[r + 1] = 0;
+            p.seq_lens[r] = 0;
+        }
+        if (cta == 0 && tid == 0) p.qsl[0] = 0;
+        for (int64_t t = (int64_t)cta * kStThreads + tid; t < p.num_tokens; t += (int64_t)ncta * kStThreads) {
+            if (p.positions) p.positions[t] = -1;
+            p.slots[t] = -1;
+        }
+    } else {
+        // the sums fit 32 bits: total <= num_tokens, taken <= num_free
+        int t0 = (int)(s_tok[warp] + ti - tok), g0 = (int)(s_pag[warp] + pi - pag);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int r = r0 + i;
+            if (r >= r1) continue;
+            s_qsl[r] = t0;
+            s_first[r] = g0;
+            t0 += nw[i];
+            g0 += nd[i];
+            if (r % ncta == cta) {
+                p.qsl[r + 1] = t0;
+                p.seq_lens[r] = p.ctx_lens[r] + nw[i];
+            }
+        }
+        if (cta == 0 && tid == 0) p.qsl[0] = 0;
+        __syncthreads();
+        const int32_t* list = p.free_pages + head;
+        // ---- the new pages' table entries
+        for (int j = cta * kStThreads + tid; j < (int)taken; j += ncta * kStThreads) {
+            const int r = last_at_most(s_first, B, j);
+            const int held = (int)(((long long)p.ctx_lens[r] + bs - 1) / bs);
+            p.block_table[(int64_t)r * p.max_blocks + held + (j - s_first[r])] = list[j];
+        }
+        // ---- the tokens
+        for (int64_t t = (int64_t)cta * kStThreads + tid; t < p.num_tokens; t += (int64_t)ncta * kStThreads) {
+            int pos = -1;
+            int64_t slot = -1;
+            if (t < total) {
+                const int r = last_at_most(s_qsl, B, (int)t);
+                const int c = p.ctx_lens[r];
+                pos = c + ((int)t - s_qsl[r]);
+                const int held = (int)(((long long)c + bs - 1) / bs), page = pos / bs;
+                const int id = page < held ? p.block_table[(int64_t)r * p.max_blocks + page]
+                                           : list[s_first[r] + page - held];
+                if (id >= 0) slot = (int64_t)id * bs + (pos - page * bs);
+            }
+            if (p.positions) p.positions[t] = pos;
+            p.slots[t] = slot;
+        }
+    }
+    // every CTA has read the list's head before it is advanced (in place, perhaps)
+    cluster_barrier();
+    if (cta == 0 && tid == 0) *p.free_head_out = any ? head : head + (int)taken;
+}
+
+}  // namespace
+
+cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream) {
+    const int n = p.num_tokens >= kStClusterTokens ? kStCluster : 1;
+    return launch_cluster(step_tables_kernel, dim3(n), dim3(kStThreads), 0, n, stream, p);
+}
+
+}  // namespace pka
