@@ -306,16 +306,31 @@ def pka_gather_rows(dst, src, index, error_word=None, stream=None):
                                   int(row_bytes), _ptr(error_word), _stream(stream)), "pka_gather_rows")
 
 
-def _require(where, device, **tensors):
-    """Every (tensor, dtype, shape) packed, of that type and shape, on that
-    device; None as a length leaves that length open."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
-            raise ValueError(f"{where}: {name} must be a packed {dtype} tensor on the current CUDA device")
-        if len(t.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _packed(where, device, *specs):
+    """Every (name, tensor or None, dtype, shape) packed, of that type and shape, on that device."""
+    for name, t, dtype, shape in specs:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                              or t.get_device() != device):
+            raise ValueError(f"{where}: {name} must be a packed {dtype} tensor of shape {shape} on the current CUDA "
+                             f"device, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _torch():
+    """torch, the current CUDA device, and a function from a call's `stream` to its address there (the
+    torch.cuda forms build a Stream object on each call, which costs as much as a small launch)."""
+    import torch
+    device = torch.cuda.current_device()
+
+    def address(stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(device)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    return torch, device, address
 
 
 def pka_step_tables(ctx_lens, query_lens, block_table, block_size, free_pages, free_head, free_head_out,
@@ -323,20 +338,20 @@ def pka_step_tables(ctx_lens, query_lens, block_table, block_size, free_pages, f
     """ctx_lens, query_lens, seq_lens [B] int32; block_table [B, max_blocks] int32 (new pages are added);
     free_pages [n] int32, free_head / free_head_out [1] int32 (may be the same tensor); query_start_loc [B + 1]
     int32; positions [T] int32 or None, slot_mapping [T] int64 (T >= the new tokens; the rest gets -1)."""
-    import torch
+    torch, device, address = _torch()
     i32 = torch.int32
     B, width = block_table.shape
-    T = slot_mapping.shape[0]
-    _require("pka_step_tables", torch.cuda.current_device(), ctx_lens=(ctx_lens, i32, (B,)),
-             query_lens=(query_lens, i32, (B,)), block_table=(block_table, i32, (B, width)),
-             free_pages=(free_pages, i32, (None,)), free_head=(free_head, i32, (1,)),
-             free_head_out=(free_head_out, i32, (1,)), query_start_loc=(query_start_loc, i32, (B + 1,)),
-             seq_lens=(seq_lens, i32, (B,)), positions=(positions, i32, (T,)),
-             slot_mapping=(slot_mapping, torch.int64, (T,)), error_word=(error_word, i32, (1,)))
+    T, pages = slot_mapping.numel(), free_pages.numel()
+    _packed("pka_step_tables", device, ("ctx_lens", ctx_lens, i32, (B,)), ("query_lens", query_lens, i32, (B,)),
+            ("block_table", block_table, i32, (B, width)), ("free_pages", free_pages, i32, (pages,)),
+            ("free_head", free_head, i32, (1,)), ("free_head_out", free_head_out, i32, (1,)),
+            ("query_start_loc", query_start_loc, i32, (B + 1,)), ("seq_lens", seq_lens, i32, (B,)),
+            ("positions", positions, i32, (T,)), ("slot_mapping", slot_mapping, torch.int64, (T,)),
+            ("error_word", error_word, i32, (1,)))
     st = load().pka_step_tables(ctx_lens.data_ptr(), query_lens.data_ptr(), B, T, block_table.data_ptr(), width,
-                                block_size, free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(),
+                                block_size, free_pages.data_ptr(), pages, free_head.data_ptr(),
                                 free_head_out.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(),
-                                _ptr(positions), slot_mapping.data_ptr(), _ptr(error_word), _stream(stream))
+                                _addr(positions), slot_mapping.data_ptr(), _addr(error_word), address(stream))
     _check(st, "pka_step_tables")
 
 
@@ -346,53 +361,51 @@ def pka_qk_rope_cache_write(q, k, v, q_weight, k_weight, eps, cos_sin, interleav
     k_weight [d] bf16 or None; cos_sin [max_position, rotary_dim] float32 (cosines, then sines) or None;
     positions [T] int32, slot_mapping [T] int64; q_out [T, Hq, d], k_out, v_out [T, Hkv, d] or None; caches
     [nb, Hkv, bs, d] bf16, or uint8 E4M3 codes with kv_scales=(k_scale, v_scale)."""
-    import torch
+    torch, device, address = _torch()
     bf16, where = torch.bfloat16, "pka_qk_rope_cache_write"
     T, Hq, d = q.shape
     Hkv = k.shape[1]
     nb, _, bs, _ = k_cache.shape
-    rotary, longest = (0, 0) if cos_sin is None else (cos_sin.shape[1], cos_sin.shape[0])
-    device = torch.cuda.current_device()
+    longest, rotary = (0, 0) if cos_sin is None else cos_sin.shape
+    q_row, k_row, v_row = Hq * d, Hkv * d, Hkv * d
+    if T > 1:  # (the row stride of a single row is free)
+        q_row, k_row, v_row = q.stride(0), k.stride(0), v.stride(0)
     for name, x, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
         if x.dtype is not bf16 or x.get_device() != device or x.shape != (T, heads, d):
             raise ValueError(f"{where}: {name} must be bf16 [{T}, {heads}, {d}] on the current CUDA device")
         if (heads > 1 and x.stride(1) != d) or (d > 1 and x.stride(2) != 1):
             raise ValueError(f"{where}: the heads of a row of {name} must be packed")
-    cache = bf16 if kv_scales is None else torch.uint8
-    _require(where, device, q_weight=(q_weight, bf16, (d,)), k_weight=(k_weight, bf16, (d,)),
-             cos_sin=(cos_sin, torch.float32, (longest, rotary)), positions=(positions, torch.int32, (T,)),
-             slot_mapping=(slot_mapping, torch.int64, (T,)), q_out=(q_out, bf16, (T, Hq, d)),
-             k_out=(k_out, bf16, (T, Hkv, d)), v_out=(v_out, bf16, (T, Hkv, d)),
-             k_cache=(k_cache, cache, (nb, Hkv, bs, d)), v_cache=(v_cache, cache, (nb, Hkv, bs, d)),
-             error_word=(error_word, torch.int32, (1,)))
-    # the row stride of a single row is free: give the packed one
-    step = lambda x, heads: x.stride(0) if T > 1 else heads * d
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), step(q, Hq), step(k, Hkv), step(v, Hkv), _ptr(q_weight),
-            _ptr(k_weight), float(eps), _ptr(cos_sin), rotary, longest, 1 if interleaved else 0, positions.data_ptr(),
-            slot_mapping.data_ptr(), T, Hq, Hkv, d, q_out.data_ptr(), _ptr(k_out), _ptr(v_out), k_cache.data_ptr(),
-            v_cache.data_ptr(), nb, bs)
+    caches = (nb, Hkv, bs, d)
+    kind = bf16 if kv_scales is None else torch.uint8
+    _packed(where, device, ("q_weight", q_weight, bf16, (d,)), ("k_weight", k_weight, bf16, (d,)),
+            ("cos_sin", cos_sin, torch.float32, (longest, rotary)), ("positions", positions, torch.int32, (T,)),
+            ("slot_mapping", slot_mapping, torch.int64, (T,)), ("q_out", q_out, bf16, (T, Hq, d)),
+            ("k_out", k_out, bf16, (T, Hkv, d)), ("v_out", v_out, bf16, (T, Hkv, d)),
+            ("k_cache", k_cache, kind, caches), ("v_cache", v_cache, kind, caches),
+            ("error_word", error_word, torch.int32, (1,)))
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, _addr(q_weight), _addr(k_weight), float(eps),
+            _addr(cos_sin), rotary, longest, 1 if interleaved else 0, positions.data_ptr(), slot_mapping.data_ptr(),
+            T, Hq, Hkv, d, q_out.data_ptr(), _addr(k_out), _addr(v_out), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs)
     if kv_scales is None:
-        st = load().pka_qk_rope_cache_write(*args, _ptr(error_word), _stream(stream))
+        st = load().pka_qk_rope_cache_write(*args, _addr(error_word), address(stream))
     else:
-        st = load().pka_qk_rope_cache_write_fp8(*args, float(kv_scales[0]), float(kv_scales[1]), _ptr(error_word),
-                                                _stream(stream))
+        st = load().pka_qk_rope_cache_write_fp8(*args, float(kv_scales[0]), float(kv_scales[1]),
+                                                _addr(error_word), address(stream))
     _check(st, where)
 
 
 def pka_page_bounds(k_cache, slot_mapping, bounds, bound_scales, error_word=None, stream=None):
     """k_cache [nb, Hkv, bs, d] bf16, or uint8 E4M3 codes; slot_mapping [T] int64; bounds [nb, Hkv, 2, d] int8,
     bound_scales [nb, Hkv] float32 (the entries of pages that are not filled stay)."""
-    import torch
+    torch, device, address = _torch()
     nb, Hkv, bs, d = k_cache.shape
-    T = slot_mapping.shape[0]
-    cache = {torch.bfloat16: 1, torch.uint8: 2}.get(k_cache.dtype)
-    if cache is None:
-        raise ValueError("pka_page_bounds: k_cache must be bf16 or uint8 codes")
-    _require("pka_page_bounds", torch.cuda.current_device(), k_cache=(k_cache, k_cache.dtype, (nb, Hkv, bs, d)),
-             slot_mapping=(slot_mapping, torch.int64, (T,)), bounds=(bounds, torch.int8, (nb, Hkv, 2, d)),
-             bound_scales=(bound_scales, torch.float32, (nb, Hkv)), error_word=(error_word, torch.int32, (1,)))
-    st = load().pka_page_bounds(k_cache.data_ptr(), cache, slot_mapping.data_ptr(), T, Hkv, d, nb, bs,
-                                bounds.data_ptr(), bound_scales.data_ptr(), _ptr(error_word), _stream(stream))
+    T = slot_mapping.numel()
+    kind = torch.uint8 if k_cache.dtype is torch.uint8 else torch.bfloat16
+    _packed("pka_page_bounds", device, ("k_cache", k_cache, kind, (nb, Hkv, bs, d)),
+            ("slot_mapping", slot_mapping, torch.int64, (T,)), ("bounds", bounds, torch.int8, (nb, Hkv, 2, d)),
+            ("bound_scales", bound_scales, torch.float32, (nb, Hkv)), ("error_word", error_word, torch.int32, (1,)))
+    st = load().pka_page_bounds(k_cache.data_ptr(), 2 if kind is torch.uint8 else 1, slot_mapping.data_ptr(), T,
+                                Hkv, d, nb, bs, bounds.data_ptr(), bound_scales.data_ptr(), _addr(error_word), address(stream))
     _check(st, "pka_page_bounds")
 
 
@@ -400,21 +413,21 @@ def pka_select_pages(q, bounds, bound_scales, block_table, query_start_loc, seq_
                      num_last, max_seq_len, selected, error_word=None, stream=None):
     """q [T, Hq, d] bf16; bounds [nb, Hkv, 2, d] int8, bound_scales [nb, Hkv] float32; block_table [B, max_blocks]
     int32, query_start_loc [B + 1], seq_lens [B] int32; selected [T, Hkv, num_pages] int32: page indices, then -1."""
-    import torch
+    torch, device, address = _torch()
     i32 = torch.int32
     T, Hq, d = q.shape
     nb, Hkv = bound_scales.shape
     B, width = block_table.shape
     pages = selected.shape[2]
-    _require("pka_select_pages", torch.cuda.current_device(), q=(q, torch.bfloat16, (T, Hq, d)),
-             bounds=(bounds, torch.int8, (nb, Hkv, 2, d)), bound_scales=(bound_scales, torch.float32, (nb, Hkv)),
-             block_table=(block_table, i32, (B, width)), query_start_loc=(query_start_loc, i32, (B + 1,)),
-             seq_lens=(seq_lens, i32, (B,)), selected=(selected, i32, (T, Hkv, pages)),
-             error_word=(error_word, i32, (1,)))
+    _packed("pka_select_pages", device, ("q", q, torch.bfloat16, (T, Hq, d)),
+            ("bounds", bounds, torch.int8, (nb, Hkv, 2, d)), ("bound_scales", bound_scales, torch.float32, (nb, Hkv)),
+            ("block_table", block_table, i32, (B, width)), ("query_start_loc", query_start_loc, i32, (B + 1,)),
+            ("seq_lens", seq_lens, i32, (B,)), ("selected", selected, i32, (T, Hkv, pages)),
+            ("error_word", error_word, i32, (1,)))
     st = load().pka_select_pages(q.data_ptr(), bounds.data_ptr(), bound_scales.data_ptr(), block_table.data_ptr(),
                                  width, query_start_loc.data_ptr(), seq_lens.data_ptr(), B, T, Hq, Hkv, d, nb,
                                  block_size, num_first, num_last, max_seq_len, pages, selected.data_ptr(),
-                                 _ptr(error_word), _stream(stream))
+                                 _addr(error_word), address(stream))
     _check(st, "pka_select_pages")
 
 
@@ -422,23 +435,21 @@ def pka_sparse_attn_forward(q, k_cache, v_cache, block_table, query_start_loc, s
                             out, lse, kv_scales=None, error_word=None, stream=None):
     """q, out [T, Hq, d] bf16, lse [T, Hq] float32 or None; caches [nb, Hkv, bs, d] bf16, or uint8 E4M3 codes with
     kv_scales=(k_scale, v_scale); selected [T, Hkv, num_pages] int32 as pka_select_pages writes it."""
-    import torch
-    i32 = torch.int32
-    T, Hq, d = q.shape
+    torch, device, address = _torch()
+    i32, bf16, where = torch.int32, torch.bfloat16, "pka_sparse_attn_forward"
+    T, Hq, d = rows = q.shape
     nb, Hkv, bs, _ = k_cache.shape
     B, width = block_table.shape
     pages = selected.shape[2]
-    cache = torch.bfloat16 if kv_scales is None else torch.uint8
-    where = "pka_sparse_attn_forward"
-    _require(where, torch.cuda.current_device(), q=(q, torch.bfloat16, (T, Hq, d)),
-             k_cache=(k_cache, cache, (nb, Hkv, bs, d)), v_cache=(v_cache, cache, (nb, Hkv, bs, d)),
-             block_table=(block_table, i32, (B, width)), query_start_loc=(query_start_loc, i32, (B + 1,)),
-             seq_lens=(seq_lens, i32, (B,)), selected=(selected, i32, (T, Hkv, pages)),
-             out=(out, torch.bfloat16, (T, Hq, d)), lse=(lse, torch.float32, (T, Hq)),
-             error_word=(error_word, i32, (1,)))
+    kind, caches = bf16 if kv_scales is None else torch.uint8, (nb, Hkv, bs, d)
+    _packed(where, device, ("q", q, bf16, rows), ("k_cache", k_cache, kind, caches),
+            ("v_cache", v_cache, kind, caches), ("block_table", block_table, i32, (B, width)),
+            ("query_start_loc", query_start_loc, i32, (B + 1,)), ("seq_lens", seq_lens, i32, (B,)),
+            ("selected", selected, i32, (T, Hkv, pages)), ("out", out, bf16, rows),
+            ("lse", lse, torch.float32, (T, Hq)), ("error_word", error_word, i32, (1,)))
     args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), width,
             query_start_loc.data_ptr(), seq_lens.data_ptr(), B, T, Hq, Hkv, d, nb, bs, float(scale))
-    tail = (selected.data_ptr(), pages, max_seq_len, out.data_ptr(), _ptr(lse), _ptr(error_word), _stream(stream))
+    tail = (selected.data_ptr(), pages, max_seq_len, out.data_ptr(), _addr(lse), _addr(error_word), address(stream))
     if kv_scales is None:
         st = load().pka_sparse_attn_forward(*args, *tail)
     else:
