@@ -45,7 +45,7 @@ cudaError_t launch_decode_mla_tc(const CUtensorMap& kvmap, const CUtensorMap& qm
 
 cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream);
 cudaError_t launch_qk_rope(const QkRopeParams& p, bool fp8, int num_sms, cudaStream_t stream);
-cudaError_t launch_page_bounds(const PageBoundsParams& p, bool fp8, cudaStream_t stream);
+cudaError_t launch_page_bounds(PageBoundsParams p, bool fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_sparse_attn(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnParams& p, int head_dim,
                                bool fp8, int num_sms, cudaStream_t stream);
@@ -1281,6 +1281,8 @@ pka_status pka_page_bounds(const void* k_cache, int cache_dtype, const int64_t* 
     if (!aligned(k_cache, 16) || !aligned(slot_mapping, 8) || !aligned(bounds, 16) || !aligned(bound_scales, 4) ||
         !aligned(error_word, 4))
         return PKA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PKA_ERR_CUDA;
     PageBoundsParams p;
     p.k_cache = k_cache;
     p.slots = slot_mapping;
@@ -1294,7 +1296,7 @@ pka_status pka_page_bounds(const void* k_cache, int cache_dtype, const int64_t* 
     p.head_dim = head_dim;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(
-        timed(PKA_KERNEL_PAGE_BOUNDS, st, [&] { return launch_page_bounds(p, cache_dtype == 2, st); }));
+        timed(PKA_KERNEL_PAGE_BOUNDS, st, [&] { return launch_page_bounds(p, cache_dtype == 2, sms, st); }));
 }
 
 pka_status pka_select_pages(const void* q, const int8_t* bounds, const float* bound_scales,

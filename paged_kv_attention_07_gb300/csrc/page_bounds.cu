@@ -10,8 +10,13 @@
 // NaN or an infinity gets codes 0 and the scale +inf (it bounds nothing).
 //
 // The pages are found from the slot mapping alone: a page is filled by the
-// token that goes to its last slot. HBM-bound: block_size x d elements read
-// per filled (page, kv head), 2 d + 4 bytes written.
+// token that goes to its last slot. A CTA looks at the slots of `chunk` tokens
+// with one load per warp and takes the filled pages of its kv head one after
+// another: 128 threads read a page in 16-byte pieces, all of a thread's pieces
+// in flight together, and keep minima and maxima as packed 16-bit pairs (bf16
+// as it is, codes widened to f16, exact). Bound by latency (a slot, a page, the
+// join) up to some thousand tokens, by HBM beyond: block_size x d elements
+// read per filled (page, kv head), 2 d + 4 bytes written.
 #include "common.cuh"
 #include "params.cuh"
 
@@ -20,108 +25,150 @@ namespace pka {
 namespace {
 
 constexpr int kPbThreads = 128;
-constexpr int kPbTokens = 8;  // tokens whose slots one CTA looks at
+constexpr int kPbWarps = kPbThreads / 32;
+constexpr int kPbBatch = 8;  // 16-byte pieces per thread in flight
+
+// Packed pairs: bf16, or f16 of codes. NaN wins over any value.
+template <bool kFp8>
+PKA_DEVICE uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (kFp8) asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool kFp8>
+PKA_DEVICE uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (kFp8) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool kFp8>
+PKA_DEVICE float2 pair(uint32_t x) {
+    return kFp8 ? __half22float2(h2(x)) : make_float2(bf16_lo(x), bf16_hi(x));
+}
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kPbThreads) page_bounds_kernel(PageBoundsParams p) {
-    constexpr int kVec = kFp8 ? 16 : 8;          // elements of a 16-byte piece
-    __shared__ float s_lo[kPbThreads * kVec], s_hi[kPbThreads * kVec];
-    __shared__ uint32_t s_bad;
+    constexpr int kVec = kFp8 ? 16 : 8;  // elements of a 16-byte piece
+    constexpr int kWords = kVec / 2;     // and their packed pairs
+    constexpr uint32_t kInf = kFp8 ? 0x7c007c00u : 0x7f807f80u, kMinusInf = kInf | 0x80008000u;
+    __shared__ uint32_t s_lo[kPbWarps][64], s_hi[kPbWarps][64];  // head_dim / 2 pairs per warp
+    __shared__ float s_amax[2];
     grid_dep_launch();
     grid_dep_wait();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = blockIdx.y;
-    const int pieces = p.head_dim / kVec;        // 16-byte pieces of a key: a power of two, at most 16
-    const int rows = kPbThreads / pieces;        // keys read side by side
+    const int pieces = p.head_dim / kVec;  // of a key: a power of two, 4 to 16
+    const int rows = kPbThreads / pieces;  // keys read side by side
     const int c = tid % pieces, r0 = tid / pieces;
-    for (int64_t t0 = (int64_t)blockIdx.x * kPbTokens; t0 < p.num_tokens; t0 += (int64_t)gridDim.x * kPbTokens) {
-        for (int64_t t = t0; t < t0 + kPbTokens && t < p.num_tokens; ++t) {
-            const int64_t slot = __ldg(p.slots + t);
-            if (slot < 0) continue;
+    for (int64_t t0 = (int64_t)blockIdx.x * p.chunk; t0 < p.num_tokens; t0 += (int64_t)gridDim.x * p.chunk) {
+        // the pages that this chunk fills: one token per lane, the same in every warp
+        int64_t blk = -1;
+        if (lane < p.chunk && t0 + lane < p.num_tokens) {
+            const int64_t slot = __ldg(p.slots + t0 + lane);
             if (slot >= p.num_slots) {
-                if (tid == 0 && g == 0) set_error(p.err, PKA_DEVERR_SLOT);
-                continue;
+                if (warp == 0 && g == 0) set_error(p.err, PKA_DEVERR_SLOT);
+            } else if (slot >= 0) {
+                const int64_t b = slot / p.block_size;
+                if (slot - b * p.block_size == p.block_size - 1) blk = b;
             }
-            const int64_t blk = slot / p.block_size;
-            if (slot - blk * p.block_size != p.block_size - 1) continue;  // the same for the whole CTA
-            const int64_t page = blk * p.Hkv + g;
-            float lo[kVec], hi[kVec];
-            bool bad = false;
+        }
+        for (uint32_t todo = __ballot_sync(0xffffffffu, blk >= 0); todo; todo &= todo - 1) {
+            const int64_t page = __shfl_sync(0xffffffffu, blk, __ffs(todo) - 1) * p.Hkv + g;
+            const uint8_t* src = static_cast<const uint8_t*>(p.k_cache) +
+                                 (page * p.block_size * p.head_dim + c * kVec) * (kFp8 ? 1 : 2);
+            const int64_t row = (int64_t)p.head_dim * (kFp8 ? 1 : 2);
+            uint32_t lo[kWords], hi[kWords];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                lo[i] = INFINITY;
-                hi[i] = -INFINITY;
+            for (int i = 0; i < kWords; ++i) {
+                lo[i] = kInf;
+                hi[i] = kMinusInf;
             }
-            for (int r = r0; r < p.block_size; r += rows) {
-                const uint4 v = *reinterpret_cast<const uint4*>(
-                    static_cast<const uint8_t*>(p.k_cache) +
-                    ((page * p.block_size + r) * p.head_dim + c * kVec) * (kFp8 ? 1 : 2));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                float x[kVec];
+            for (int r = r0; r < p.block_size; r += kPbBatch * rows) {
+                uint4 v[kPbBatch];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (kFp8) {
-                        const float2 a = __half22float2(h2(e4m3x2_to_f16x2(w[i] & 0xffffu)));
-                        const float2 b = __half22float2(h2(e4m3x2_to_f16x2(w[i] >> 16)));
-                        x[4 * i % kVec] = a.x, x[(4 * i + 1) % kVec] = a.y;
-                        x[(4 * i + 2) % kVec] = b.x, x[(4 * i + 3) % kVec] = b.y;
-                    } else {
-                        x[2 * i] = bf16_lo(w[i]);
-                        x[2 * i + 1] = bf16_hi(w[i]);
+                for (int j = 0; j < kPbBatch; ++j)
+                    if (r + j * rows < p.block_size) v[j] = *reinterpret_cast<const uint4*>(src + (r + j * rows) * row);
+#pragma unroll
+                for (int j = 0; j < kPbBatch; ++j) {
+                    if (r + j * rows >= p.block_size) continue;
+                    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (kFp8) {
+                            const uint32_t a = e4m3x2_to_f16x2(w[i] & 0xffffu), b = e4m3x2_to_f16x2(w[i] >> 16);
+                            lo[2 * i % kWords] = min2<kFp8>(lo[2 * i % kWords], a);
+                            hi[2 * i % kWords] = max2<kFp8>(hi[2 * i % kWords], a);
+                            lo[(2 * i + 1) % kWords] = min2<kFp8>(lo[(2 * i + 1) % kWords], b);
+                            hi[(2 * i + 1) % kWords] = max2<kFp8>(hi[(2 * i + 1) % kWords], b);
+                        } else {
+                            lo[i] = min2<kFp8>(lo[i], w[i]);
+                            hi[i] = max2<kFp8>(hi[i], w[i]);
+                        }
                     }
                 }
+            }
+            // ---- join: the warp's rows by shuffles, the warps in shared memory
+            for (int o = pieces; o < 32; o <<= 1) {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    bad |= !(fabsf(x[i]) <= 3.4e38f);
-                    lo[i] = fminf(lo[i], x[i]);
-                    hi[i] = fmaxf(hi[i], x[i]);
+                for (int i = 0; i < kWords; ++i) {
+                    lo[i] = min2<kFp8>(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+                    hi[i] = max2<kFp8>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
                 }
             }
             __syncthreads();  // the last page's results have been read
-            if (tid == 0) s_bad = 0;
+            if (lane < pieces) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                s_lo[r0 * p.head_dim + c * kVec + i] = lo[i];
-                s_hi[r0 * p.head_dim + c * kVec + i] = hi[i];
-            }
-            __syncthreads();
-            if (bad) s_bad = 1;
-            // element tid (head_dim <= kPbThreads): join the rows, then the largest magnitude
-            float l = 0.f, h = 0.f;
-            if (tid < p.head_dim) {
-                l = s_lo[tid], h = s_hi[tid];
-                const int n = min(rows, p.block_size);
-                for (int r = 1; r < n; ++r) {
-                    l = fminf(l, s_lo[r * p.head_dim + tid]);
-                    h = fmaxf(h, s_hi[r * p.head_dim + tid]);
+                for (int i = 0; i < kWords; ++i) {
+                    s_lo[warp][lane * kWords + i] = lo[i];
+                    s_hi[warp][lane * kWords + i] = hi[i];
                 }
             }
-            __shared__ float s_amax[kPbThreads / 32];
-            float a = fmaxf(-l, h);
+            __syncthreads();
+            // ---- two elements per thread of the first two warps (head_dim <= 128)
+            const int pairs = p.head_dim / 2;
+            float2 l = make_float2(0.f, 0.f), h = l;
+            if (tid < pairs) {
+                uint32_t x = s_lo[0][tid], y = s_hi[0][tid];
+#pragma unroll
+                for (int w = 1; w < kPbWarps; ++w) {
+                    x = min2<kFp8>(x, s_lo[w][tid]);
+                    y = max2<kFp8>(y, s_hi[w][tid]);
+                }
+                l = pair<kFp8>(x);
+                h = pair<kFp8>(y);
+            }
+            // the largest magnitude, an infinity where there is a NaN
+            float a = fmaxf(fmaxf(-l.x, h.x), fmaxf(-l.y, h.y));
+            if (isnan(l.x) || isnan(l.y)) a = INFINITY;
 #pragma unroll
             for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            if ((tid & 31) == 0) s_amax[tid >> 5] = a;
+            if (lane == 0 && warp < 2) s_amax[warp] = a;
             __syncthreads();
-            a = 0.f;
-#pragma unroll
-            for (int i = 0; i < kPbThreads / 32; ++i) a = fmaxf(a, s_amax[i]);
-            const bool nan = s_bad != 0;
-            const int e = nan ? 0 : bound_exponent(a);
-            const float unit = exp2i(-e);
-            if (tid < p.head_dim) {
-                int8_t* code = p.bounds + page * 2 * p.head_dim;
-                code[tid] = nan ? 0 : (int8_t)(int)floorf(l * unit);
-                code[p.head_dim + tid] = nan ? 0 : (int8_t)(int)ceilf(h * unit);
+            a = fmaxf(s_amax[0], s_amax[1]);
+            const bool none = a == INFINITY;
+            const int e = none ? 0 : bound_exponent(a);
+            const float unit = none ? 0.f : exp2i(-e);
+            if (tid < pairs) {
+                auto two = [](float x, float y) { return (uint16_t)((uint8_t)(int8_t)(int)x | (uint8_t)(int8_t)(int)y << 8); };
+                uint16_t* code = reinterpret_cast<uint16_t*>(p.bounds + page * 2 * p.head_dim);
+                code[tid] = none ? 0 : two(floorf(l.x * unit), floorf(l.y * unit));
+                code[pairs + tid] = none ? 0 : two(ceilf(h.x * unit), ceilf(h.y * unit));
             }
-            if (tid == 0) p.scales[page] = nan ? INFINITY : exp2i(e);
+            if (tid == 0) p.scales[page] = none ? INFINITY : exp2i(e);
         }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_page_bounds(const PageBoundsParams& p, bool fp8, cudaStream_t stream) {
-    const int64_t chunks = (p.num_tokens + kPbTokens - 1) / kPbTokens;
+cudaError_t launch_page_bounds(PageBoundsParams p, bool fp8, int num_sms, cudaStream_t stream) {
+    // a chunk of tokens may fill up to as many pages (decodes): small chunks
+    // while the GPU has room for them, a warp's lanes at most
+    p.chunk = 32;
+    while (p.chunk > 4 && (p.num_tokens + p.chunk - 1) / p.chunk * p.Hkv < num_sms) p.chunk /= 2;
+    const int64_t chunks = (p.num_tokens + p.chunk - 1) / p.chunk;
     const dim3 grid((unsigned)std::min<int64_t>(chunks, 1 << 20), (unsigned)p.Hkv);
     return fp8 ? launch_dependent(page_bounds_kernel<true>, grid, dim3(kPbThreads), 0, stream, p)
                : launch_dependent(page_bounds_kernel<false>, grid, dim3(kPbThreads), 0, stream, p);

@@ -168,6 +168,7 @@ struct PageBoundsParams {
     int32_t* err;
     int64_t num_tokens, num_slots;
     int Hkv, block_size, head_dim;
+    int chunk;  // tokens per CTA, set by the launch
 };
 
 struct PageSelectParams {
