@@ -24,9 +24,12 @@ namespace pka {
 namespace {
 
 constexpr int kStThreads = 1024;
+constexpr int kStBatch = 4;  // tokens of a thread in flight
 // Tokens from which the writes are spread over a cluster of kStCluster CTAs.
 constexpr int kStCluster = 8;
 constexpr int64_t kStClusterTokens = 4096;
+
+PKA_DEVICE int pages_of(int tokens, int bs) { return (int)(((uint32_t)tokens + (uint32_t)bs - 1) / (uint32_t)bs); }
 
 // Last r in [0, n) with first[r] <= x (first[0] == 0 <= x).
 PKA_DEVICE int last_at_most(const int32_t* first, int n, int x) {
@@ -40,8 +43,10 @@ PKA_DEVICE int last_at_most(const int32_t* first, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParams p) {
-    __shared__ int32_t s_qsl[kMaxRequests];    // first token of each request
-    __shared__ int32_t s_first[kMaxRequests];  // pages taken by the requests before it
+    extern __shared__ int32_t s_req[];
+    int32_t* s_qsl = s_req;                   // first token of each request
+    int32_t* s_first = s_qsl + p.num_reqs;    // pages taken by the requests before it
+    int32_t* s_ctx = s_first + p.num_reqs;    // its cached tokens
     __shared__ long long s_tok[33], s_pag[33];
     grid_dep_launch();
     grid_dep_wait();
@@ -57,10 +62,10 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
     int err = 0;
     long long tok = 0, pag = 0;
     constexpr int kPer = kMaxRequests / kStThreads;
-    int nw[kPer], nd[kPer];
+    int nw[kPer], nd[kPer], cl[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        nw[i] = nd[i] = 0;
+        nw[i] = nd[i] = cl[i] = 0;
         const int r = r0 + i;
         if (r >= r1) continue;
         const int c = p.ctx_lens[r], q = p.query_lens[r];
@@ -70,7 +75,8 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
         if (s > longest) err |= PKA_DEVERR_BLOCK_TABLE;
         if (q < 0 || c < 0 || s > longest) continue;
         nw[i] = q;
-        nd[i] = (int)((s + bs - 1) / bs) - (int)(((long long)c + bs - 1) / bs);
+        cl[i] = c;
+        nd[i] = pages_of((int)s, bs) - pages_of(c, bs);  // (s <= longest, which fits)
         tok += q;
         pag += nd[i];
     }
@@ -133,11 +139,12 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
             if (r >= r1) continue;
             s_qsl[r] = t0;
             s_first[r] = g0;
+            s_ctx[r] = cl[i];
             t0 += nw[i];
             g0 += nd[i];
             if (r % ncta == cta) {
                 p.qsl[r + 1] = t0;
-                p.seq_lens[r] = p.ctx_lens[r] + nw[i];
+                p.seq_lens[r] = cl[i] + nw[i];
             }
         }
         if (cta == 0 && tid == 0) p.qsl[0] = 0;
@@ -146,24 +153,33 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
         // ---- the new pages' table entries
         for (int j = cta * kStThreads + tid; j < (int)taken; j += ncta * kStThreads) {
             const int r = last_at_most(s_first, B, j);
-            const int held = (int)(((long long)p.ctx_lens[r] + bs - 1) / bs);
+            const int held = pages_of(s_ctx[r], bs);
             p.block_table[(int64_t)r * p.max_blocks + held + (j - s_first[r])] = list[j];
         }
-        // ---- the tokens
-        for (int64_t t = (int64_t)cta * kStThreads + tid; t < p.num_tokens; t += (int64_t)ncta * kStThreads) {
-            int pos = -1;
-            int64_t slot = -1;
-            if (t < total) {
+        // ---- the tokens, kStBatch of a thread's at a time: their table loads overlap
+        const int64_t step = (int64_t)ncta * kStThreads;
+        for (int64_t tb = (int64_t)cta * kStThreads + tid; tb < p.num_tokens; tb += step * kStBatch) {
+            int pos[kStBatch], off[kStBatch], id[kStBatch];
+#pragma unroll
+            for (int i = 0; i < kStBatch; ++i) {
+                const int64_t t = tb + step * i;
+                pos[i] = id[i] = -1;
+                off[i] = 0;
+                if (t >= total) continue;
                 const int r = last_at_most(s_qsl, B, (int)t);
-                const int c = p.ctx_lens[r];
-                pos = c + ((int)t - s_qsl[r]);
-                const int held = (int)(((long long)c + bs - 1) / bs), page = pos / bs;
-                const int id = page < held ? p.block_table[(int64_t)r * p.max_blocks + page]
-                                           : list[s_first[r] + page - held];
-                if (id >= 0) slot = (int64_t)id * bs + (pos - page * bs);
+                const int c = s_ctx[r];
+                pos[i] = c + ((int)t - s_qsl[r]);
+                const int held = pages_of(c, bs), page = (int)((uint32_t)pos[i] / (uint32_t)bs);
+                off[i] = pos[i] - page * bs;
+                id[i] = page < held ? p.block_table[(int64_t)r * p.max_blocks + page] : list[s_first[r] + page - held];
             }
-            if (p.positions) p.positions[t] = pos;
-            p.slots[t] = slot;
+#pragma unroll
+            for (int i = 0; i < kStBatch; ++i) {
+                const int64_t t = tb + step * i;
+                if (t >= p.num_tokens) continue;
+                if (p.positions) p.positions[t] = pos[i];
+                p.slots[t] = id[i] >= 0 ? (int64_t)id[i] * bs + off[i] : -1;
+            }
         }
     }
     // every CTA has read the list's head before it is advanced (in place, perhaps)
@@ -174,8 +190,14 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
 }  // namespace
 
 cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream) {
+    const size_t smem = sizeof(int32_t) * 3 * (size_t)p.num_reqs;
+    if (smem > 47 * 1024) {  // past what every kernel may use
+        const cudaError_t e =
+            cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     const int n = p.num_tokens >= kStClusterTokens ? kStCluster : 1;
-    return launch_cluster(step_tables_kernel, dim3(n), dim3(kStThreads), 0, n, stream, p);
+    return launch_cluster(step_tables_kernel, dim3(n), dim3(kStThreads), smem, n, stream, p);
 }
 
 }  // namespace pka
