@@ -441,6 +441,20 @@ PKA_DEVICE void store_cluster(uint32_t* p, uint32_t rank, uint32_t v) {
         : "memory");
 }
 
+PKA_DEVICE void min_cluster(uint32_t* p, uint32_t rank, uint32_t v) {
+    asm volatile(
+        "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tred.shared::cluster.min.u32 [a], %2;\n\t}" ::"r"(
+            smem_u32(p)),
+        "r"(rank), "r"(v)
+        : "memory");
+}
+PKA_DEVICE void max_cluster(uint32_t* p, uint32_t rank, uint32_t v) {
+    asm volatile(
+        "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tred.shared::cluster.max.u32 [a], %2;\n\t}" ::"r"(
+            smem_u32(p)),
+        "r"(rank), "r"(v)
+        : "memory");
+}
 PKA_DEVICE float load_cluster(const float* p, uint32_t rank) {
     float v;
     asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
@@ -479,12 +493,24 @@ PKA_DEVICE int bound_exponent(float a) {
     return a * exp2i(-e) > 127.f ? e + 1 : e;
 }
 
-// The request that owns token t (the last r with qsl[r] <= t), or -1 behind
-// the last one (t >= qsl[n]). With whole warps: every lane gets the answer.
-PKA_DEVICE int request_of(const int32_t* qsl, int n, int t) {
-    const int a = __ldg(qsl + min(t, n)), b = __ldg(qsl + min(t + 1, n));
-    if (t >= __ldg(qsl + n)) return -1;
-    if (t < n && a == t && b == t + 1) return t;  // one token per request up to here
+// Where token t stands: its request (the last r with qsl[r] <= t), that
+// request's tokens [q0, q1) and length; r = -1 behind the last request (t >=
+// qsl[n]). With whole warps: every lane gets the answer. A batch of one token
+// per request (r = t) costs one round of loads.
+struct TokenPlace {
+    int r, q0, q1, len;
+};
+PKA_DEVICE TokenPlace place_of(const int32_t* qsl, const int32_t* seq_lens, int n, int t) {
+    TokenPlace at;
+    at.r = min(t, n - 1);
+    at.q0 = __ldg(qsl + at.r);
+    at.q1 = __ldg(qsl + at.r + 1);
+    at.len = __ldg(seq_lens + at.r);
+    if (t >= __ldg(qsl + n)) {
+        at.r = -1;
+        return at;
+    }
+    if (at.q0 == t && at.q1 == t + 1) return at;
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = n;  // the answer lies in [lo, hi)
     while (hi - lo > 1) {
@@ -495,7 +521,11 @@ PKA_DEVICE int request_of(const int32_t* qsl, int n, int t) {
         lo += k * step;
         hi = min(hi, lo + step);
     }
-    return lo;
+    at.r = lo;
+    at.q0 = __ldg(qsl + lo);
+    at.q1 = __ldg(qsl + lo + 1);
+    at.len = __ldg(seq_lens + lo);
+    return at;
 }
 
 #ifdef __CUDACC__

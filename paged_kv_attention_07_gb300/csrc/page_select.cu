@@ -13,15 +13,31 @@
 // sum_i max(c_i lo_i, c_i hi_i) = <min(c, 0), lo> + <max(c, 0), hi>: one product
 // of length 2 d with the page's record as it lies in memory (lo then hi).
 // One warp scores 16 pages: it loads their 16 records (2 d bytes each) straight
-// into the A fragments of m16n8k32 -- which of a fragment's columns holds which
-// element does not matter as long as B agrees, so each lane's 16-byte load
-// feeds two MMAs -- and the queries' codes wait as B fragments in registers.
+// into the fragments of the product. The block ids of the CTA's pages are
+// fetched together beforehand, into the places where the scores will go: the
+// chain id -> record costs the time. Other warps hide a tile's loads: a second
+// tile in registers costs more in resident CTAs than it gains (96 requests of
+// 4096 to 65536 tokens, 8 kv heads: 27.6 us, 30.0 us with two tiles; records by
+// asynchronous copies 28.4 us, by one bulk copy each 39 us, bound by the rate
+// at which an SM takes copies; int8 products 39 us).
+//
+// The product runs on the f16 tensor cores: an int8 MMA takes 65 cycles here
+// and two f16 ones of half its length 16. A code c becomes the f16 number
+// 1152 + c with one byte permutation (the byte of c + 128 under the exponent of
+// 1024), the queries' codes are f16, and 1152 * sum c_q is taken off at the end.
+// All of it is exact: of a pair min(c, 0), max(c, 0) one is zero, so each of the
+// two accumulators sums at most d / 2 <= 64 products of at most 1279 * 127, below
+// 2^24. Which of a fragment's columns holds which element does not matter as long
+// as A and B agree: a lane's 16-byte read of a record is the A operand of four
+// MMAs.
 //
 // One cluster per (token, kv head): its CTAs score a slice of the pages each
 // and leave the scores in the first CTA's shared memory, which then picks the
-// pages: a radix selection of the num_pages-th largest score, digit by digit,
-// and one prefix sum that writes the chosen pages in ascending order (ties: the
-// lowest page). The scores never go to memory. HBM-bound for a full batch:
+// pages. The scores never go to memory. The pick is a radix selection of the
+// want-th largest score over the range the scores take: one histogram of 256
+// bins usually leaves a handful of pages in the border bin, and those are
+// ranked one against all. The chosen pages become a bit map, whose prefix sum
+// gives ascending output (ties: the lowest page). HBM-bound for a full batch:
 // 2 d + 4 bytes per (page, kv head).
 #include "common.cuh"
 #include "params.cuh"
@@ -30,16 +46,14 @@ namespace pka {
 
 namespace {
 
-constexpr int kPsThreads = 256;
-constexpr int kPsWarps = kPsThreads / 32;
+constexpr int kBatch = 4;  // keys of a thread read together
 
-PKA_DEVICE void mma_s8(int32_t (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+template <int D, int NT, int kThreads>
+struct PsCfg {
+    static constexpr int kWarps = kThreads / 32;
+    static constexpr int kQRow = 4 * D + 16;  // a head's codes in f16, padded by a quarter of the banks
+    static constexpr int kFixed = NT * 8 * kQRow;  // then a key and a bit per page
+};
 
 // A float's bits as an unsigned key of the same order.
 PKA_DEVICE uint32_t order_key(float x) {
@@ -47,8 +61,9 @@ PKA_DEVICE uint32_t order_key(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Exclusive sum of v over the block's threads (packed counts); total to all.
-PKA_DEVICE uint32_t block_scan(uint32_t v, uint32_t* s_warp, uint32_t* total) {
+// Exclusive sum of v over the block's threads.
+template <int kThreads>
+PKA_DEVICE uint32_t block_scan(uint32_t v, uint32_t* s_warp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t incl = v;
 #pragma unroll
@@ -58,237 +73,362 @@ PKA_DEVICE uint32_t block_scan(uint32_t v, uint32_t* s_warp, uint32_t* total) {
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    uint32_t before = 0, all = 0;
+    uint32_t before = 0;
 #pragma unroll
-    for (int w = 0; w < kPsWarps; ++w) {
-        const uint32_t x = s_warp[w];
-        before += w < warp ? x : 0u;
-        all += x;
-    }
+    for (int w = 0; w < kThreads / 32; ++w) before += w < warp ? s_warp[w] : 0u;
     __syncthreads();
-    *total = all;
     return before + incl - v;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kPsThreads) page_select_kernel(PageSelectParams p) {
-    constexpr int kSteps = 2 * D / 32;            // MMAs per 16 pages and 8 heads
-    extern __shared__ uint32_t s_key[];           // scores of the candidates, as keys (first CTA's is used)
-    __shared__ __align__(16) int8_t s_q[NT * 8][2 * D];         // per head: min(c, 0) then max(c, 0), in the records' order
-    __shared__ float s_unit[NT * 8];
-    __shared__ uint32_t s_hist[256];
-    __shared__ uint32_t s_warp[kPsWarps];
-    __shared__ uint32_t s_min, s_max, s_digit, s_above;
+template <int D, int NT, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) page_select_kernel(PageSelectParams p) {
+    using C = PsCfg<D, NT, kThreads>;
+    constexpr int kBins = kThreads;  // of a histogram: one per thread
+    constexpr int kBinBits = kThreads == 256 ? 8 : 7;
+    constexpr int kSpans = 2 * D / 64;  // 64-byte pieces of a record: four MMAs each
+    constexpr int kE = D / 32;          // elements of a head per lane
+    constexpr int kQHeads = NT * 8 / C::kWarps;  // heads whose codes a warp makes
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* s_q = smem;  // per head: min(c, 0) then max(c, 0), in the records' order
+    uint32_t* s_key = reinterpret_cast<uint32_t*>(smem + C::kFixed);  // the candidates' scores (first CTA's is used)
+    uint32_t* s_bits = s_key + (p.max_seq_len + p.block_size - 1) / p.block_size;  // the chosen candidates
+    __shared__ float s_unit[NT * 8], s_zero[NT * 8][2];
+    __shared__ uint32_t s_hist[kBins];
+    __shared__ uint32_t s_warp[C::kWarps];
+    __shared__ uint32_t s_list[kThreads];
+    __shared__ uint32_t s_min, s_max, s_digit, s_above, s_inside, s_count;
     grid_dep_launch();
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ncta = cluster_size(), cta = cluster_rank();
-    const int g = blockIdx.y;
-    const int t = (int)(blockIdx.x / ncta);
-    // ---- the token's request and position (the same for the whole cluster)
-    const int r = request_of(p.qsl, p.num_reqs, t);
-    if (r < 0) return;  // a row behind the last sequence
-    const int q1 = __ldg(p.qsl + r + 1), sl = __ldg(p.seq_lens + r);
-    const long long pos = (long long)sl - q1 + t;
-    if (t < __ldg(p.qsl + r) || pos < 0 || sl > p.max_seq_len || pos >= sl) {
-        if (tid == 0) set_error(p.err, PKA_DEVERR_SEQ_LEN);
+    if (tid == 0) s_min = 0xffffffffu, s_max = 0u, s_count = 0;
+    s_hist[tid] = 0;
+    // (waited for before the first store to the first CTA; here, where there is
+    // nothing in flight that it would wait for itself)
+    if (ncta > 1) cluster_arrive();
+    // the heads of a token side by side: their records of a page are neighbours in memory
+    const uint32_t unit_index = blockIdx.x / ncta;
+    const int t = (int)(unit_index / (uint32_t)p.Hkv), g = (int)(unit_index - (uint32_t)t * (uint32_t)p.Hkv);
+    // ---- this warp's part of the queries (needed later), and the token's request
+    // and position (the same for the whole cluster)
+    float x[kQHeads][kE];
+#pragma unroll
+    for (int j = 0; j < kQHeads; ++j) {
+        const int h = warp + j * C::kWarps;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            p.q + ((int64_t)t * p.Hq + g * p.G + (h < p.G ? h : 0)) * D + lane * kE);
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) {
+            const uint32_t v = h < p.G ? __ldg(src + i) : 0u;
+            x[j][2 * i] = bf16_lo(v);
+            x[j][2 * i + 1] = bf16_hi(v);
+        }
+    }
+    const TokenPlace place = place_of(p.qsl, p.seq_lens, p.num_reqs, t);
+    const int r = place.r;
+    if (r < 0) {  // a row behind the last sequence
+        if (ncta > 1) cluster_wait();
         return;
     }
-    const int n = (int)pos / p.block_size + 1;  // pages up to the token's own
+    const long long pos = (long long)place.len - place.q1 + t;
+    if (t < place.q0 || pos < 0 || pos >= place.len || place.len > p.max_seq_len) {
+        if (tid == 0) set_error(p.err, PKA_DEVERR_SEQ_LEN);
+        if (ncta > 1) cluster_wait();
+        return;
+    }
+    const int n = (int)((uint32_t)pos / (uint32_t)p.block_size) + 1;  // pages up to the token's own
     int32_t* out = p.sel + ((int64_t)t * p.Hkv + g) * p.num_pages;
     const int K = p.num_pages;
-    if (n <= K) {  // all of them
-        for (int i = cta * kPsThreads + tid; i < K; i += ncta * kPsThreads) out[i] = i < n ? i : -1;
+    const int nf = p.num_first, m = n - nf - p.num_last, want = K - nf - p.num_last;
+    if (n <= K || want == 0) {  // all pages, or only those that are always read
+        for (int i = cta * kThreads + tid; i < K; i += ncta * kThreads) out[i] = i >= n ? -1 : n <= K || i < nf ? i : n - K + i;
+        if (ncta > 1) cluster_wait();
         return;
     }
-    const int nf = p.num_first, m = n - nf - p.num_last, want = K - nf - p.num_last;
-    for (int i = cta * kPsThreads + tid; i < nf + p.num_last; i += ncta * kPsThreads)
-        out[i < nf ? i : K - p.num_last + (i - nf)] = i < nf ? i : n - p.num_last + (i - nf);
-    if (want == 0) return;
-    cluster_arrive();  // waited for before the first store to the first CTA
 
-    // ---- the queries' codes, one warp per head
-    if (tid < NT * 8) s_unit[tid] = 0.f;
-    __syncthreads();
-    for (int h = warp; h < NT * 8; h += kPsWarps) {
-        constexpr int kE = D / 32;
-        float x[kE];
-        float a = 0.f;
-        const bool ok = h < p.G;
+    // ---- this warp's tiles of 16 candidates [nf, nf + m): records and block ids ahead
+    const int32_t* bt = p.block_table + (int64_t)r * p.max_blocks + nf;
+    const int tiles = (m + 15) / 16;
+    const int first = (int)((uint32_t)tiles * cta / ncta), tiles_end = (int)((uint32_t)tiles * (cta + 1) / ncta);
+    {
+        const int i1 = min(m, tiles_end * 16);
+        for (int i0 = first * 16 + tid; i0 < i1; i0 += kBatch * kThreads) {
+            int id[kBatch];
 #pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            x[i] = ok ? __bfloat162float(p.q[((int64_t)t * p.Hq + g * p.G + h) * D + lane * kE + i]) : 0.f;
-            a = fmaxf(a, fabsf(x[i]));
-            if (!(fabsf(x[i]) <= 3.4e38f)) a = INFINITY;
+            for (int j = 0; j < kBatch; ++j) id[j] = i0 + j * kThreads < i1 ? __ldg(bt + i0 + j * kThreads) : 0;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (i0 + j * kThreads < i1) s_key[i0 + j * kThreads] = (uint32_t)id[j];
         }
+    }
+    __syncthreads();
+    // a tile's records as A fragments: rows lane / 4 and 8 more, piece lane % 4 of each span
+    struct Tile {
+        uint4 rec[2][kSpans];
+        float scale[2];
+    };
+    auto load = [&](Tile& x, int tile) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = tile * 16 + half * 8 + (lane >> 2);
+            int id = i < m ? (int)s_key[i] : 0;
+            const bool ok = id >= 0 && id < p.num_blocks;
+            if (!ok) {
+                set_error(p.err, PKA_DEVERR_BLOCK_ID);
+                id = 0;
+            }
+            const int64_t page = (int64_t)id * p.Hkv + g;
+            const uint4* src = reinterpret_cast<const uint4*>(p.bounds + page * 2 * D) + (lane & 3);
+#pragma unroll
+            for (int s = 0; s < kSpans; ++s) x.rec[half][s] = __ldg(src + s * 4);
+            x.scale[half] = ok ? __ldg(p.scales + page) : -INFINITY;
+        }
+        __syncwarp();  // (the ids' places are written by the scores only after all lanes have read them)
+    };
+    const int tile0 = first + warp;
+    Tile now;
+    if (tile0 < tiles_end) load(now, tile0);
+
+    // ---- the queries' codes
+#pragma unroll
+    for (int j = 0; j < kQHeads; ++j) {
+        const int h = warp + j * C::kWarps;
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < kE; ++i) a = fabsf(x[j][i]) <= 3.4e38f ? fmaxf(a, fabsf(x[j][i])) : INFINITY;
 #pragma unroll
         for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
         const bool finite = a <= 3.4e38f;  // a head with a NaN or an infinity scores 0 everywhere
         const int e = finite ? bound_exponent(a) : 0;
         const float unit = exp2i(-e);
+        int sum = 0;
+        __half* row = reinterpret_cast<__half*>(s_q + h * C::kQRow) + lane * kE;
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
-            const int c = finite ? __float2int_rn(x[i] * unit) : 0;
-            s_q[h][lane * kE + i] = (int8_t)min(c, 0);
-            s_q[h][D + lane * kE + i] = (int8_t)max(c, 0);
+            const int c = finite ? __float2int_rn(x[j][i] * unit) : 0;
+            row[i] = __int2half_rn(min(c, 0));
+            row[D + i] = __int2half_rn(max(c, 0));
+            sum += c;
         }
-        if (lane == 0) s_unit[h] = exp2i(e);
+        // an accumulator takes 8 elements of every 16: the offset of each
+        const bool second = lane * kE & 8;
+        const int s0 = __reduce_add_sync(0xffffffffu, second ? 0 : sum), s1 = __reduce_add_sync(0xffffffffu, second ? sum : 0);
+        if (lane == 0) {
+            s_unit[h] = exp2i(e);
+            s_zero[h][0] = 1152.f * (float)s0;
+            s_zero[h][1] = 1152.f * (float)s1;
+        }
     }
     __syncthreads();
-    // B fragments: head (lane / 4), 16-byte piece (lane % 4) of each 64 bytes of the record
-    uint32_t b[NT][kSteps][2];
+    float unit[NT][2], zero[NT][2][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int s = 0; s < kSteps; s += 2) {
-            const uint4 v = *reinterpret_cast<const uint4*>(&s_q[nt * 8 + (lane >> 2)][s * 32 + (lane & 3) * 16]);
-            b[nt][s][0] = v.x, b[nt][s][1] = v.y, b[nt][s + 1][0] = v.z, b[nt][s + 1][1] = v.w;
+        for (int j = 0; j < 2; ++j) {
+            const int h = nt * 8 + 2 * (lane & 3) + j;
+            unit[nt][j] = s_unit[h];
+            zero[nt][j][0] = s_zero[h][0];
+            zero[nt][j][1] = s_zero[h][1];
         }
-    float unit[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        unit[nt][0] = s_unit[nt * 8 + 2 * (lane & 3)];
-        unit[nt][1] = s_unit[nt * 8 + 2 * (lane & 3) + 1];
-    }
+    // B: head (lane / 4), the 16 codes of piece (lane % 4) of each span
+    const uint8_t* qrow = s_q + (lane >> 2) * C::kQRow + (lane & 3) * 32;
+    auto load_b = [&](uint32_t (&b)[8], int nt, int s) {
+        const uint4 u = *reinterpret_cast<const uint4*>(qrow + nt * 8 * C::kQRow + s * 128);
+        const uint4 v = *reinterpret_cast<const uint4*>(qrow + nt * 8 * C::kQRow + s * 128 + 16);
+        b[0] = u.x, b[1] = u.y, b[2] = u.z, b[3] = u.w, b[4] = v.x, b[5] = v.y, b[6] = v.z, b[7] = v.w;
+    };
+    if (ncta > 1) cluster_wait();
 
-    // ---- scores of this CTA's slice of the candidates [nf, nf + m)
-    const int32_t* bt = p.block_table + (int64_t)r * p.max_blocks + nf;
-    const int tiles = (m + 15) / 16;
-    cluster_wait();
-    for (int tile = cta * kPsWarps + warp; tile < tiles; tile += ncta * kPsWarps) {
-        uint32_t a[2][kSteps / 2][4];
-        float scale[2];
+    // ---- scores
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    auto score = [&](const Tile& x, int tile) {
+        float c[NT][2][4] = {};
+#pragma unroll
+        for (int s = 0; s < kSpans; ++s) {
+            const uint4 a = x.rec[0][s], b = x.rec[1][s];
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+            uint32_t f[4][4];  // 1152 + code, f16 pairs
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t u = aw[j] ^ 0x80808080u, v = bw[j] ^ 0x80808080u;
+                f[j][0] = __byte_perm(u, 0x64646464u, 0x4140);
+                f[j][1] = __byte_perm(v, 0x64646464u, 0x4140);
+                f[j][2] = __byte_perm(u, 0x64646464u, 0x4342);
+                f[j][3] = __byte_perm(v, 0x64646464u, 0x4342);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t q[8];
+                load_b(q, nt, s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_f16(c[nt][j >> 1], f[j][0], f[j][1], f[j][2], f[j][3], q[2 * j], q[2 * j + 1]);
+            }
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int i = tile * 16 + half * 8 + (lane >> 2);
-            int blk = i < m ? __ldg(bt + i) : 0;
-            const bool ok = blk >= 0 && blk < p.num_blocks;
-            if (!ok) {
-                set_error(p.err, PKA_DEVERR_BLOCK_ID);
-                blk = 0;
-            }
-            const int64_t page = (int64_t)blk * p.Hkv + g;
-            const uint4* rec = reinterpret_cast<const uint4*>(p.bounds + page * 2 * D) + (lane & 3);
+            float v = -INFINITY;
 #pragma unroll
-            for (int s = 0; s < kSteps / 2; ++s) {
-                const uint4 v = __ldg(rec + s * 4);
-                a[half][s][0] = v.x, a[half][s][1] = v.y, a[half][s][2] = v.z, a[half][s][3] = v.w;
-            }
-            scale[half] = ok ? __ldg(p.scales + page) : -INFINITY;
-        }
-        float best[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            int32_t c[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < kSteps / 2; ++s) {
-                mma_s8(c, a[0][s][0], a[1][s][0], a[0][s][1], a[1][s][1], b[nt][2 * s][0], b[nt][2 * s][1]);
-                mma_s8(c, a[0][s][2], a[1][s][2], a[0][s][3], a[1][s][3], b[nt][2 * s + 1][0], b[nt][2 * s + 1][1]);
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     if (nt * 8 + 2 * (lane & 3) + j < p.G)
-                        best[half] = fmaxf(best[half], (float)c[half * 2 + j] * scale[half] * unit[nt][j]);
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v = best[half];
+                        v = fmaxf(v, ((c[nt][0][half * 2 + j] - zero[nt][j][0]) + (c[nt][1][half * 2 + j] - zero[nt][j][1])) *
+                                         x.scale[half] * unit[nt][j]);
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
             // a page that bounds nothing (scale +inf) comes first, one that does not exist last
-            if (fabsf(scale[half]) == INFINITY) v = scale[half];
+            if (fabsf(x.scale[half]) == INFINITY) v = x.scale[half];
             const int i = tile * 16 + half * 8 + (lane >> 2);
-            if ((lane & 3) == 0 && i < m) store_cluster(&s_key[i], 0, order_key(v));
+            if (i < m) {
+                const uint32_t k = order_key(v);
+                lo = min(lo, k);
+                hi = max(hi, k);
+                if ((lane & 3) == 0) store_cluster(&s_key[i], 0, k);
+            }
         }
+    };
+    for (int tile = tile0; tile < tiles_end; tile += C::kWarps) {
+        score(now, tile);
+        if (tile + C::kWarps < tiles_end) load(now, tile + C::kWarps);
     }
-    cluster_barrier();
-    if (cta != 0) return;
-
-    // ---- the want-th largest key: the bits that all keys share are skipped,
-    // then eight bits at a time from the top
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    for (int i = tid; i < m; i += kPsThreads) {
-        lo = min(lo, s_key[i]);
-        hi = max(hi, s_key[i]);
-    }
-    if (tid == 0) s_min = 0xffffffffu, s_max = 0u;
-    __syncthreads();
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-        atomicMin(&s_min, lo);
-        atomicMax(&s_max, hi);
+    if (lane == 0 && lo <= hi) {
+        min_cluster(&s_min, 0, lo);
+        max_cluster(&s_max, 0, hi);
     }
-    __syncthreads();
-    lo = s_min, hi = s_max;
-    int bits = lo == hi ? 0 : 32 - __clz(lo ^ hi);  // low bits in which keys differ
-    uint32_t prefix = bits == 32 ? 0u : (hi >> bits) << bits;
-    uint32_t rank = want;  // among the keys that share the prefix
-    while (bits > 0) {
-        const int shift = max(0, bits - 8), width = bits - shift;
-        for (int i = tid; i < 256; i += kPsThreads) s_hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < m; i += kPsThreads) {
-            const uint32_t k = s_key[i];
-            if (bits == 32 || (k >> bits) == (prefix >> bits)) atomicAdd(&s_hist[(k >> shift) & ((1u << width) - 1)], 1u);
+    if (ncta == 1) __syncthreads();
+    else cluster_barrier();
+    if (cta != 0) return;
+
+    // ---- the border: keys as distances from the least, `bits` low bits of them
+    // undecided, the higher ones equal to the border's; `rank` pages are still
+    // to be taken from the `inside` ones that share them
+    const uint32_t base = s_min;
+    int bits = 32 - __clz(s_max - base);  // 0: all equal
+    uint32_t border = 0, rank = want, inside = m;
+    while (bits > 0 && inside > kThreads) {
+        const int shift = max(0, bits - kBinBits);
+        for (int i0 = tid; i0 < m; i0 += kBatch * kThreads) {
+            uint32_t k[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * kThreads < m ? s_key[i0 + j * kThreads] - base : 0u;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (i0 + j * kThreads < m && (bits == 32 || (k[j] >> bits) == (border >> bits)))
+                    atomicAdd(&s_hist[(k[j] >> shift) & ((1u << (bits - shift)) - 1)], 1u);
         }
         __syncthreads();
-        // digits from the largest down: thread d takes digit 255 - d
-        const uint32_t cnt = s_hist[255 - tid];
-        uint32_t total;
-        const uint32_t before = block_scan(cnt, s_warp, &total);
+        // bins from the largest down: thread d takes bin kBins - 1 - d
+        const int bin = kBins - 1 - tid;
+        const uint32_t cnt = s_hist[bin];
+        const uint32_t before = block_scan<kThreads>(cnt, s_warp);
+        s_hist[bin] = 0;
         if (before < rank && before + cnt >= rank) {
-            s_digit = 255 - tid;
+            s_digit = bin;
             s_above = before;
+            s_inside = cnt;
         }
         __syncthreads();
-        prefix |= s_digit << shift;
+        border |= s_digit << shift;
         rank -= s_above;
+        inside = s_inside;
         bits = shift;
         __syncthreads();
     }
-    // ---- write the chosen pages in ascending order: each thread a contiguous
-    // run of pages; keys above the threshold, and the first `rank` that equal it
-    const int per = (m + kPsThreads - 1) / kPsThreads;
-    const int i0 = min(m, tid * per), i1 = min(m, i0 + per);
-    uint32_t above = 0, equal = 0;
-    for (int i = i0; i < i1; ++i) {
-        above += s_key[i] > prefix;
-        equal += s_key[i] == prefix;
+    // ---- a bit per candidate: above the border; inside it, either a short list
+    // to rank one against all, or (all equal) the first ones
+    const bool few = inside <= kThreads;
+    const int words = (m + 31) / 32;
+    for (int w0 = warp; w0 < words; w0 += kBatch * C::kWarps) {
+        uint32_t k[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = (w0 + j * C::kWarps) * 32 + lane;
+            k[j] = i < m ? s_key[i] - base : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int w = w0 + j * C::kWarps, i = w * 32 + lane;
+            if (w >= words) break;
+            const uint32_t top = bits == 32 ? 0u : k[j] >> bits, edge = bits == 32 ? 0u : border >> bits;
+            const uint32_t above = __ballot_sync(0xffffffffu, i < m && top > edge);
+            if (lane == 0) s_bits[w] = above;
+            if (few && i < m && top == edge) s_list[atomicAdd(&s_count, 1u)] = i;
+        }
     }
-    uint32_t total;
-    const uint32_t packed = block_scan(above << 16 | equal, s_warp, &total);
-    uint32_t at_above = packed >> 16, at_equal = packed & 0xffffu;
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t k = s_key[i];
-        if (k > prefix || (k == prefix && at_equal < rank)) out[nf + at_above + min(at_equal, rank)] = nf + i;
-        at_above += k > prefix;
-        at_equal += k == prefix;
+    __syncthreads();
+    if (few) {
+        if (tid < inside) {
+            const uint32_t i = s_list[tid], k = s_key[i];
+            uint32_t better = 0;
+            for (uint32_t j = 0; j < inside; ++j) {
+                const uint32_t o = s_list[j], ko = s_key[o];
+                better += ko > k || (ko == k && o < i);
+            }
+            if (better < rank) atomicOr(&s_bits[i >> 5], 1u << (i & 31));
+        }
+    } else {
+        // more than a block of equal keys (bits == 0): by index, `rank` of them
+        const int per = (m + kThreads - 1) / kThreads;
+        const int i0 = min(m, tid * per), i1 = min(m, i0 + per);
+        uint32_t equal = 0;
+        for (int i = i0; i < i1; ++i) equal += s_key[i] - base == border;
+        uint32_t at = block_scan<kThreads>(equal, s_warp);
+        for (int i = i0; i < i1 && at < rank; ++i)
+            if (s_key[i] - base == border) {
+                atomicOr(&s_bits[i >> 5], 1u << (i & 31));
+                ++at;
+            }
     }
+    __syncthreads();
+    // ---- the chosen pages in ascending order, between those that are always
+    // read: each thread a run of words
+    for (int i = tid; i < nf + p.num_last; i += kThreads) {
+        const bool front = i < nf;
+        out[front ? i : want + i] = front ? i : n - K + want + i;
+    }
+    const int per = (words + kThreads - 1) / kThreads;
+    const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
+    uint32_t cnt = 0;
+    for (int w = w0; w < w1; ++w) cnt += __popc(s_bits[w]);
+    const uint32_t end = nf + want;
+    uint32_t at = nf + block_scan<kThreads>(cnt, s_warp);
+    for (int w = w0; w < w1; ++w)
+        for (uint32_t x = s_bits[w]; x && at < end; x &= x - 1) out[at++] = nf + w * 32 + __ffs(x) - 1;
 }
 
-template <int D, int NT>
-cudaError_t go(const PageSelectParams& p, int num_sms, cudaStream_t stream) {
-    auto kern = page_select_kernel<D, NT>;
+template <int D, int NT, int kThreads>
+cudaError_t go(const PageSelectParams& p, int cluster, cudaStream_t stream) {
+    auto kern = page_select_kernel<D, NT, kThreads>;
     const int pages = (p.max_seq_len + p.block_size - 1) / p.block_size;
-    const size_t smem = sizeof(uint32_t) * (size_t)pages;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPageSelectMaxPages * 4);
+    const int smem = PsCfg<D, NT, kThreads>::kFixed + 4 * (pages + (pages + 31) / 32);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    // as many CTAs per (token, kv head) as fill the GPU once, each with at
-    // least one tile of 16 pages per warp
-    int n = 1;
-    while (n < 8 && (int64_t)p.num_tokens * p.Hkv * n < num_sms && pages > n * kPsWarps * 16) n *= 2;
-    return launch_cluster(kern, dim3((unsigned)n * (unsigned)p.num_tokens, p.Hkv), dim3(kPsThreads), smem, n, stream, p);
+    return launch_cluster(kern, dim3((unsigned)(cluster * p.num_tokens * p.Hkv)), dim3(kThreads), smem, cluster, stream,
+                          p);
 }
 
 }  // namespace
 
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream) {
-    const bool two = p.G > 8;
-    if (head_dim == 128) return two ? go<128, 2>(p, num_sms, stream) : go<128, 1>(p, num_sms, stream);
-    if (head_dim == 64) return two ? go<64, 2>(p, num_sms, stream) : go<64, 1>(p, num_sms, stream);
+    const int pages = (p.max_seq_len + p.block_size - 1) / p.block_size;
+    const int64_t units = (int64_t)p.num_tokens * p.Hkv;
+    // (with the most pages the keys leave no room for the stages of 8 warps)
+    const bool two = p.G > 8, wide = units < num_sms && pages <= 24576;
+    int n = 1;
+    while (n < 8 && units * n < num_sms && pages > n * 128) n *= 2;
+    auto by_width = [&](auto d, auto nt) {
+        return wide ? go<decltype(d)::value, decltype(nt)::value, 256>(p, n, stream)
+                    : go<decltype(d)::value, decltype(nt)::value, 128>(p, n, stream);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    using N1 = std::integral_constant<int, 1>;
+    using N2 = std::integral_constant<int, 2>;
+    if (head_dim == 128) return two ? by_width(D128{}, N2{}) : by_width(D128{}, N1{});
+    if (head_dim == 64) return two ? by_width(D64{}, N2{}) : by_width(D64{}, N1{});
     return cudaErrorInvalidValue;
 }
 

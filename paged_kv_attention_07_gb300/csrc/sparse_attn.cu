@@ -83,11 +83,11 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
 
     const int ncta = (int)cluster_size(), cta = (int)cluster_rank();
     const int g = blockIdx.y, t = (int)(blockIdx.x / (unsigned)ncta);
-    const int r = request_of(p.qsl, p.num_reqs, t);
+    const TokenPlace at = place_of(p.qsl, p.seq_lens, p.num_reqs, t);
+    const int r = at.r;
     if (r < 0) return;  // a row behind the last sequence
-    const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1), sl = __ldg(p.seq_lens + r);
-    const long long pos = (long long)sl - q1 + t;
-    const bool bad = t < q0 || pos < 0 || pos >= sl || sl > p.max_seq_len;
+    const long long pos = (long long)at.len - at.q1 + t;
+    const bool bad = t < at.q0 || pos < 0 || pos >= at.len || at.len > p.max_seq_len;
     if (bad) {
         if (tid == 0 && cta == 0 && g == 0) set_error(p.err, PKA_DEVERR_SEQ_LEN);
         return;

@@ -397,6 +397,19 @@ def test_select_pages_long_context_over_a_cluster(ctx, bs, Hkv):
     assert err == 0
 
 
+@pytest.mark.parametrize("d,Hq", [(64, 4), (128, 8), (128, 16)])
+def test_select_pages_sums_at_the_end_of_their_range(d, Hq):
+    """Codes of 127 throughout but for single units: scores of 127 * 127 * d that differ by one are told apart."""
+    rng = np.random.default_rng(d)
+    b = batch(rng, [4000], [1], 16)
+    for sign in (1, -1):
+        bounds = np.full((b["nb"], 1, 2, d), 127.0) - (rng.random((b["nb"], 1, 2, d)) < 0.01)
+        bounds = sign * (bounds if sign > 0 else bounds[:, :, ::-1])
+        q = sign * torch.full((1, Hq, d), 127.0)
+        q[..., rng.permutation(d)[:d // 4]] = sign  # the codes are the values: units of these elements count one
+        select_check(b, q.to(BF16).cuda(), bounds, np.ones((b["nb"], 1)), 1, 2, 50)
+
+
 def test_select_pages_values_without_an_order():
     """Pages that bound nothing come first; query heads with NaN or infinity count as zero scores."""
     rng = np.random.default_rng(9)
