@@ -242,6 +242,19 @@ def test_rope_extreme_values():
                     k_cache=s["k_cache"], v_cache=s["v_cache"]))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_keeps_infinities_to_their_pair(interleaved):
+    """An infinity spoils its own pair alone; behind the rotated part only its own element."""
+    s = rope_case(3, 4, 2, 128, 64, interleaved, False, False, True, seed=7)
+    s["q"][0, 0, 70], s["q"][1, 2, 5], s["k"][2, 1, 127] = float("inf"), float("-inf"), float("inf")
+    rope_call(s)
+    bad = {n: ~torch.isfinite(s[n].float()).cpu() for n in ("q_out", "k_out")}
+    pair = [4, 5] if interleaved else [5, 37]
+    assert bad["q_out"].nonzero().tolist() == [[0, 0, 70]] + [[1, 2, i] for i in pair]
+    assert bad["k_out"].nonzero().tolist() == [[2, 1, 127]]
+    assert s["q_out"][0, 0, 70] == float("inf") and s["k_out"][2, 1, 127] == float("inf")
+
+
 def test_rope_then_cache_write_is_the_same_cache():
     """k_out and v_out through pka_cache_write give the bits that the one pass wrote."""
     s = rope_case(77, 4, 2, 128, 128, True, True, False, True, seed=6)
@@ -404,7 +417,7 @@ def test_select_pages_sums_at_the_end_of_their_range(d, Hq):
     b = batch(rng, [4000], [1], 16)
     for sign in (1, -1):
         bounds = np.full((b["nb"], 1, 2, d), 127.0) - (rng.random((b["nb"], 1, 2, d)) < 0.01)
-        bounds = sign * (bounds if sign > 0 else bounds[:, :, ::-1])
+        bounds = np.sort(sign * bounds, axis=2)  # low before high
         q = sign * torch.full((1, Hq, d), 127.0)
         q[..., rng.permutation(d)[:d // 4]] = sign  # the codes are the values: units of these elements count one
         select_check(b, q.to(BF16).cuda(), bounds, np.ones((b["nb"], 1)), 1, 2, 50)
