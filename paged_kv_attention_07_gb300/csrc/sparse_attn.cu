@@ -17,8 +17,16 @@
 // shared memory and the CTAs' over distributed shared memory, so there is one
 // launch and nothing partial goes to memory.
 //
+// Several tokens of one request (a prompt's chunk, drafted tokens) are taken in
+// groups: their lists, mostly the same pages, are united in shared memory (a
+// bit map per token, then one prefix sum), each page of the union is read and
+// widened once, and the tokens' heads lie side by side in the MMA's columns;
+// columns whose token does not list the page, or stands before the key, get
+// weight zero. A zero weight does not hide an infinite or NaN value, so a group
+// whose result is not finite throughout is done again token by token.
+//
 // Math per tile as in the split-KV decode (bf16 operands, fp32 accumulation):
-//   S^T[16 keys x 8 heads] = K Q^T;  online softmax per head;  O^T += V^T P^T
+//   S^T[16 keys x 8 columns] = K Q^T;  online softmax per column;  O^T += V^T P^T
 // P is rounded to bf16 for the product (its sum l is not): the error is that of
 // the operands' own type. Over an 8-bit cache the codes are widened to f16
 // (exact), q and P are f16, and the scales come out of the sums.
@@ -32,6 +40,7 @@ namespace {
 constexpr int kSaWarps = 4;
 constexpr int kSaThreads = kSaWarps * 32;
 constexpr int kSaTile = 16;  // keys per tile
+constexpr int kSaGroup = 8;  // tokens of a group, at most
 
 template <int D, int NT, bool kFp8>
 struct SaCfg {
@@ -40,13 +49,50 @@ struct SaCfg {
     static constexpr int kStageBytes = 2 * kTileBytes;  // K + V
     static constexpr int kStages = 3;
     static constexpr int kRing = kSaWarps * kStages * kStageBytes;
-    static constexpr int kHeads = NT * 8;
+    static constexpr int kCols = NT * 8;
+    // q's fragments: in registers up to two column blocks, beyond in shared memory
+    static constexpr bool kQShared = NT > 2;
+    static constexpr int kQ = kQShared ? NT * (D / 16) * 32 * 8 : 0;
     // the join: each warp's m, l and O (over the ring), and the CTA's own
-    static constexpr int kWarpFloats = kHeads * (D + 2);
+    static constexpr int kWarpFloats = kCols * (D + 2);
     static constexpr int kJoin = kSaWarps * kWarpFloats * 4;
     static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
-    static constexpr int kSmem = 1024 /*align*/ + kBody + kWarpFloats * 4 + kSaWarps * kStages * 8;
+    static constexpr int kSmem = 1024 /*align*/ + kBody + kWarpFloats * 4 + kQ + kSaWarps * kStages * 8;
 };
+
+// A tile's keys in a group, eight at a time: the position of the first, and the
+// tokens (bits) that list their page.
+struct SaHalf {
+    int base;
+    uint32_t who;
+};
+
+// Where group w of kGroupTokens tokens stands: groups of request r are w =
+// qsl[r] / R + r and the following (some of them empty). With whole warps.
+struct GroupPlace {
+    int r, t0, n, q1, len;  // n tokens from t0 on; 0: none
+};
+PKA_DEVICE GroupPlace group_of(const int32_t* qsl, const int32_t* seq_lens, int nreq, int w, int R) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = nreq;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int i = lo + lane * step;
+        const uint32_t at_most = __ballot_sync(0xffffffffu, i < hi && __ldg(qsl + i) / R + i <= w);
+        const int k = at_most ? 31 - __clz(at_most) : 0;
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    GroupPlace g;
+    g.r = lo;
+    const int q0 = __ldg(qsl + lo);
+    g.q1 = __ldg(qsl + lo + 1);
+    g.len = __ldg(seq_lens + lo);
+    const long long t0 = (long long)q0 + (long long)(w - (q0 / R + lo)) * R;
+    g.t0 = (int)t0;
+    g.n = t0 < q0 || t0 >= g.q1 ? 0 : min(R, g.q1 - g.t0);
+    return g;
+}
 
 PKA_DEVICE uint32_t e4m3_lo(uint32_t w) { return e4m3x2_to_f16x2(w & 0xffffu); }
 PKA_DEVICE uint32_t e4m3_hi(uint32_t w) { return e4m3x2_to_f16x2(w >> 16); }
@@ -55,20 +101,25 @@ PKA_DEVICE uint32_t e4m3_hi(uint32_t w) { return e4m3x2_to_f16x2(w >> 16); }
 // rows one after another, each in the 128-byte swizzle.
 PKA_DEVICE uint32_t seg_off(int tr, int c) { return sw128((uint32_t)((c >> 3) * kSaTile + tr), (uint32_t)(c & 7)); }
 
-template <int D, int NT, bool kFp8>
+template <int D, int NT, bool kFp8, bool kGroup>
 __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     sparse_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const SparseAttnParams p) {
     using C = SaCfg<D, NT, kFp8>;
     constexpr int kKSteps = D / 16;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int s_stop;
+    __shared__ int s_stop[kSaGroup];
+    __shared__ uint32_t s_scan[kSaWarps], s_bad;
+    __shared__ SaHalf s_half[kGroup ? kSaWarps : 1][C::kStages][2];
     grid_dep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c4 = lane & 3, r8 = lane >> 2;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* own = reinterpret_cast<float*>(smem + C::kBody);  // this CTA's O [kHeads][D], m, l
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBody + C::kWarpFloats * 4) + warp * C::kStages;
+    float* own = reinterpret_cast<float*>(smem + C::kBody);  // this CTA's O [kCols][D], m, l
+    uint4* s_q = reinterpret_cast<uint4*>(smem + C::kBody + C::kWarpFloats * 4);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBody + C::kWarpFloats * 4 + C::kQ) + warp * C::kStages;
+    // a group's united list: page | tokens << 24
+    uint32_t* s_list = reinterpret_cast<uint32_t*>(smem + C::kSmem - 1024);
     if (lane == 0) {
         for (int s = 0; s < C::kStages; ++s) mbar_init(&full[s], 1);
         fence_barrier_init();
@@ -77,45 +128,114 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
             tma_prefetch_desc(&vmap);
         }
     }
-    if (tid == 0) s_stop = p.num_pages;
+    if (tid < kSaGroup) s_stop[tid] = p.num_pages;
+    if (tid == 0) s_bad = 0;
     __syncthreads();
     grid_dep_wait();
 
+    // ---- the tokens [t0, t0 + ntok), consecutive ones of one request
     const int ncta = (int)cluster_size(), cta = (int)cluster_rank();
-    const int g = blockIdx.y, t = (int)(blockIdx.x / (unsigned)ncta);
-    const TokenPlace at = place_of(p.qsl, p.seq_lens, p.num_reqs, t);
-    const int r = at.r;
-    if (r < 0) return;  // a row behind the last sequence
-    const long long pos = (long long)at.len - at.q1 + t;
-    const bool bad = t < at.q0 || pos < 0 || pos >= at.len || at.len > p.max_seq_len;
-    if (bad) {
+    const int g = blockIdx.y, unit = (int)(blockIdx.x / (unsigned)ncta);
+    int r, t0, ntok, q1, len;
+    if constexpr (kGroup) {
+        const GroupPlace at = group_of(p.qsl, p.seq_lens, p.num_reqs, unit, p.group);
+        r = at.r, t0 = at.t0, ntok = at.n, q1 = at.q1, len = at.len;
+        if (ntok <= 0 || t0 < 0 || t0 > p.num_tokens - ntok) return;  // no such group
+    } else {
+        const TokenPlace at = place_of(p.qsl, p.seq_lens, p.num_reqs, unit);
+        r = at.r, t0 = unit, ntok = 1, q1 = at.q1, len = at.len;
+        if (r < 0) return;  // a row behind the last sequence
+        if (t0 < at.q0) len = -1;
+    }
+    const long long pos = (long long)len - q1 + t0;  // the first token's position
+    if (pos < 0 || pos + ntok > len || len > p.max_seq_len) {
         if (tid == 0 && cta == 0 && g == 0) set_error(p.err, PKA_DEVERR_SEQ_LEN);
         return;
     }
-    // ---- the list: it ends at its first negative entry; entries ascend and none is past the own page
-    const int own_page = (int)pos / p.bs;
-    const int32_t* sel = p.sel + ((int64_t)t * p.Hkv + g) * p.num_pages;
-    for (int i = tid; i < p.num_pages; i += kSaThreads) {
-        const int e = __ldg(sel + i), before = i ? __ldg(sel + i - 1) : -1;
-        if (e <= before || e > own_page) {  // e < 0 among them, before its first occurrence is kept
-            atomicMin(&s_stop, i);
-            break;
+    const int pos0 = (int)pos, pos1 = pos0 + ntok - 1;
+    const int64_t row0 = (int64_t)t0 * p.Hq + g * p.G;  // first output row of the first token
+    const int cols = ntok * p.G;
+    auto row_of = [&](int col) { return kGroup ? row0 + (int64_t)(col / p.G) * p.Hq + col % p.G : row0 + col; };
+
+    // ---- the lists: each ends at its first negative entry; entries ascend and none is past the token's page
+    const int32_t* sel = p.sel + ((int64_t)t0 * p.Hkv + g) * p.num_pages;
+    const int64_t sel_step = (int64_t)p.Hkv * p.num_pages;  // from a token's list to the next one's
+    for (int k = 0; k < ntok; ++k) {
+        const int own_page = (pos0 + k) / p.bs;
+        const int32_t* list = sel + k * sel_step;
+        for (int i = tid; i < p.num_pages; i += kSaThreads) {
+            const int e = __ldg(list + i), before = i ? __ldg(list + i - 1) : -1;
+            if (e <= before || e > own_page) {  // e < 0 among them
+                atomicMin(&s_stop[k], i);
+                break;
+            }
         }
     }
+    const int last_page = pos1 / p.bs;
+    const int words = last_page / 32 + 1;
+    uint32_t* s_map = reinterpret_cast<uint32_t*>(smem);  // (the ring is idle still) a bit map per token
+    if constexpr (kGroup)
+        for (int i = tid; i < ntok * words; i += kSaThreads) s_map[i] = 0;
     __syncthreads();
-    const int count = s_stop;
-    if (cta == 0 && tid == 0 && count < p.num_pages && __ldg(sel + count) >= 0) set_error(p.err, PKA_DEVERR_INDEX);
-    int keys = count * p.bs;
-    if (count > 0 && __ldg(sel + count - 1) == own_page) keys += (int)pos % p.bs + 1 - p.bs;
-    const int64_t row0 = (int64_t)t * p.Hq + g * p.G;  // first output row
-    if (keys == 0) {
-        if (cta == 0) {
-            for (int i = tid; i < p.G * D / 8; i += kSaThreads)
-                reinterpret_cast<uint4*>(p.out + row0 * D)[i] = make_uint4(0, 0, 0, 0);
-            if (p.lse && tid < p.G) p.lse[row0 + tid] = -INFINITY;
+    if (cta == 0 && tid < ntok && s_stop[tid] < p.num_pages && __ldg(sel + tid * sel_step + s_stop[tid]) >= 0)
+        set_error(p.err, PKA_DEVERR_INDEX);
+    int count = s_stop[0], last = -1;  // pages to read, and the last of them
+    if constexpr (kGroup) {
+        for (int k = 0; k < ntok; ++k)
+            for (int i = tid; i < s_stop[k]; i += kSaThreads) {
+                const int e = __ldg(sel + k * sel_step + i);
+                atomicOr(&s_map[k * words + (e >> 5)], 1u << (e & 31));
+            }
+        __syncthreads();
+        const int per = (words + kSaThreads - 1) / kSaThreads;
+        const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
+        uint32_t mine = 0;
+        for (int w = w0; w < w1; ++w) {
+            uint32_t any = 0;
+            for (int k = 0; k < ntok; ++k) any |= s_map[k * words + w];
+            mine += __popc(any);
         }
-        return;
+        uint32_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        uint32_t at = incl - mine;
+        count = 0;
+#pragma unroll
+        for (int w = 0; w < kSaWarps; ++w) {
+            at += w < warp ? s_scan[w] : 0u;
+            count += (int)s_scan[w];
+        }
+        for (int w = w0; w < w1; ++w) {
+            uint32_t any = 0;
+            for (int k = 0; k < ntok; ++k) any |= s_map[k * words + w];
+            for (; any; any &= any - 1) {
+                const int bit = __ffs(any) - 1;
+                uint32_t who = 0;
+                for (int k = 0; k < ntok; ++k) who |= (s_map[k * words + w] >> bit & 1u) << k;
+                s_list[at++] = (uint32_t)(w * 32 + bit) | who << 24;
+            }
+        }
+        fence_proxy_async_smem();  // the ring is written by copies from here on
+        __syncthreads();
+        if (count > 0) last = (int)(s_list[count - 1] & 0xffffffu);
+    } else {
+        if (count > 0) last = __ldg(sel + count - 1);
     }
+    const int keys = count * p.bs - (last == last_page ? p.bs - 1 - pos1 % p.bs : 0);
+    // tokens without a page: nothing to read
+    if (cta == 0)
+        for (int k = 0; k < ntok; ++k) {
+            if (s_stop[k] > 0) continue;
+            for (int i = tid; i < p.G * D / 8; i += kSaThreads)
+                reinterpret_cast<uint4*>(p.out + (row0 + (int64_t)k * p.Hq) * D)[i] = make_uint4(0, 0, 0, 0);
+            if (p.lse && tid < p.G) p.lse[row0 + (int64_t)k * p.Hq + tid] = -INFINITY;
+        }
+    if (keys == 0) return;
     const int ntiles = (keys + kSaTile - 1) / kSaTile;
     const int part = cta * kSaWarps + warp, parts = ncta * kSaWarps;
     const int i0 = (int)((int64_t)ntiles * part / parts), i1 = (int)((int64_t)ntiles * (part + 1) / parts);
@@ -125,15 +245,24 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
     const int boxr = min(p.bs, kSaTile);
     int page0 = -32, rows = 0;  // lane l holds the first cache row of listed page page0 + l
+    uint32_t entry = 0;         // and, of a group, its entry
     uint32_t ld_it = 0, cs_it = 0;
     auto issue = [&](int i) {
         const int first = i * kSaTile / p.bs;
-        if (first + kSaTile / boxr > page0 + 32) {
+        if (first < page0 || first + kSaTile / boxr > page0 + 32) {
             page0 = first;
             const int j = page0 + lane;
             int blk = 0;
+            entry = 0;
             if (j < count) {
-                blk = __ldg(p.block_table + (int64_t)r * p.max_blocks + __ldg(sel + j));
+                int e;
+                if constexpr (kGroup) {
+                    entry = s_list[j];
+                    e = (int)(entry & 0xffffffu);
+                } else {
+                    e = __ldg(sel + j);
+                }
+                blk = __ldg(p.block_table + (int64_t)r * p.max_blocks + e);
                 if (blk < 0 || blk >= p.num_blocks) {
                     set_error(p.err, PKA_DEVERR_BLOCK_ID);
                     blk = 0;
@@ -141,13 +270,25 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
             }
             rows = (blk * p.Hkv + g) * p.bs;
         }
-        const int ra = __shfl_sync(0xffffffffu, rows, first - page0) + i * kSaTile % p.bs;
+        const int off = i * kSaTile % p.bs;
+        const int ra = __shfl_sync(0xffffffffu, rows, first - page0) + off;
         const int rb = __shfl_sync(0xffffffffu, rows, (first + 1 - page0) & 31);  // bs == 8: the tile's second page
+        const int stage = ld_it % C::kStages;
+        const int nbox = boxr < kSaTile && i * kSaTile + boxr < keys ? 2 : 1;
+        if constexpr (kGroup) {
+            const uint32_t ea = __shfl_sync(0xffffffffu, entry, first - page0);
+            const uint32_t eb = boxr < kSaTile ? __shfl_sync(0xffffffffu, entry, (first + 1 - page0) & 31) : ea;
+            if (lane < 2) {
+                const uint32_t e = lane ? eb : ea;
+                SaHalf h;
+                h.base = (int)(e & 0xffffffu) * p.bs + (boxr < kSaTile ? 0 : off + 8 * lane);
+                h.who = lane && nbox == 1 && boxr < kSaTile ? 0u : e >> 24;
+                s_half[warp][stage][lane] = h;
+            }
+        }
         if (lane == 0) {
-            const int stage = ld_it % C::kStages;
             uint8_t* kdst = ring + stage * C::kStageBytes;
             uint8_t* vdst = kdst + C::kTileBytes;
-            const int nbox = boxr < kSaTile && i * kSaTile + boxr < keys ? 2 : 1;
             fence_proxy_async_smem();
             mbar_arrive_expect_tx(&full[stage], (uint32_t)(2 * nbox * boxr * C::kRowBytes));
             for (int b = 0; b < nbox; ++b) {
@@ -161,9 +302,9 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
                 } else {  // boxes of 8 rows and one segment
 #pragma unroll
                     for (int sg = 0; sg < D / 64; ++sg) {
-                        const int off = (sg * kSaTile + b * boxr) * 128;
-                        tma_load_3d(kdst + off, &kmap, &full[stage], 0, row, sg, pol);
-                        tma_load_3d(vdst + off, &vmap, &full[stage], 0, row, sg, pol);
+                        const int at = (sg * kSaTile + b * boxr) * 128;
+                        tma_load_3d(kdst + at, &kmap, &full[stage], 0, row, sg, pol);
+                        tma_load_3d(vdst + at, &vmap, &full[stage], 0, row, sg, pol);
                     }
                 }
             }
@@ -173,31 +314,66 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     };
     for (int i = i0; i < i1 && i < i0 + C::kStages; ++i) issue(i);
 
-    // ---- Q^T fragments: head n of the group, zero beyond G
-    uint32_t qf[NT][kKSteps][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int hh = nt * 8 + r8;
-        const bool ok = hh < p.G;
-        const __nv_bfloat16* qrow = p.q + (row0 + (ok ? hh : 0)) * D;
+    // ---- Q^T fragments: column n, zero behind the last
+    uint32_t qf[C::kQShared ? 1 : NT][kKSteps][2];
+    auto load_q = [&](uint32_t (&f)[kKSteps][2], int nt) {
+        const int n = nt * 8 + r8;
+        const bool ok = n < cols;
+        const __nv_bfloat16* qrow = p.q + row_of(ok ? n : 0) * D;
         if constexpr (kFp8) {  // k-step ks holds dims 32 c4 + 4 ks .. + 3, as the codes are read
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(qrow + 32 * c4) + j) : make_uint4(0, 0, 0, 0);
-                qf[nt][2 * j][0] = bf16x2_to_f16x2(v.x);
-                qf[nt][2 * j][1] = bf16x2_to_f16x2(v.y);
-                qf[nt][2 * j + 1][0] = bf16x2_to_f16x2(v.z);
-                qf[nt][2 * j + 1][1] = bf16x2_to_f16x2(v.w);
+                f[2 * j][0] = bf16x2_to_f16x2(v.x);
+                f[2 * j][1] = bf16x2_to_f16x2(v.y);
+                f[2 * j + 1][0] = bf16x2_to_f16x2(v.z);
+                f[2 * j + 1][1] = bf16x2_to_f16x2(v.w);
             }
         } else {
 #pragma unroll
             for (int ks = 0; ks < kKSteps; ++ks) {
-                qf[nt][ks][0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qrow) + ks * 8 + c4) : 0u;
-                qf[nt][ks][1] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qrow) + ks * 8 + 4 + c4) : 0u;
+                f[ks][0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qrow) + ks * 8 + c4) : 0u;
+                f[ks][1] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qrow) + ks * 8 + 4 + c4) : 0u;
             }
         }
+    };
+    if constexpr (C::kQShared) {  // one column block per warp, two k-steps per 16 bytes
+        for (int nt = warp; nt < NT; nt += kSaWarps) {
+            load_q(qf[0], nt);
+#pragma unroll
+            for (int ks = 0; ks < kKSteps; ks += 2)
+                s_q[(nt * kKSteps / 2 + ks / 2) * 32 + lane] = make_uint4(qf[0][ks][0], qf[0][ks][1], qf[0][ks + 1][0], qf[0][ks + 1][1]);
+        }
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) load_q(qf[nt], nt);
+    }
+    // q's fragments of k-steps ks and ks + 1
+    auto q_pair = [&](int nt, int ks) {
+        if constexpr (C::kQShared) return s_q[(nt * kKSteps / 2 + ks / 2) * 32 + lane];
+        else return make_uint4(qf[nt][ks][0], qf[nt][ks][1], qf[nt][ks + 1][0], qf[nt][ks + 1][1]);
+    };
+    // this lane's columns of S^T: their token's bit and position (a column behind the last: none)
+    uint32_t bit[kGroup ? NT : 1][2];
+    int limit[kGroup ? NT : 1][2];
+    if constexpr (kGroup) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int hc = 0; hc < 2; ++hc) {
+                const int n = nt * 8 + c4 * 2 + hc, k = n / p.G;
+                bit[nt][hc] = n < cols ? 1u << k : 0u;
+                limit[nt][hc] = pos0 + k;
+            }
     }
 
+    // ---- one pass over the tiles; a group with values that are not finite takes one more per token
+    for (int pass = 0;; ++pass) {
+    const uint32_t who = pass == 0 ? (1u << ntok) - 1 : 1u << (pass - 1);  // the tokens of this pass
+    const int end = pass == 0 ? pos1 : pos0 + pass - 1;                    // the last one's position
+    if (pass > 0)
+        for (int i = i0; i < i1 && i < i0 + C::kStages; ++i) issue(i);
     float o[kKSteps][NT][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -214,11 +390,22 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
         ++cs_it;
         uint8_t* kt = ring + stage * C::kStageBytes;
         uint8_t* vt = kt + C::kTileBytes;
-        const int valid = min(kSaTile, keys - i * kSaTile);
-        if (valid < kSaTile) {  // V rows past the end may hold anything: zeros instead
-            for (int ci = lane; ci < (kSaTile - valid) * (C::kRowBytes / 16); ci += 32) {
-                const int tr = valid + ci / (C::kRowBytes / 16), c = ci % (C::kRowBytes / 16);
-                *reinterpret_cast<uint4*>(vt + (kFp8 ? sw128(tr, c) : seg_off(tr, c))) = make_uint4(0, 0, 0, 0);
+        // valid keys of the tile's two halves; the rest's values may be anything: zeros instead
+        int valid0, valid1;
+        SaHalf h0, h1;
+        if constexpr (kGroup) {
+            h0 = s_half[warp][stage][0], h1 = s_half[warp][stage][1];
+            valid0 = h0.who & who ? min(8, max(0, end + 1 - h0.base)) : 0;
+            valid1 = h1.who & who ? min(8, max(0, end + 1 - h1.base)) : 0;
+        } else {
+            valid0 = min(8, keys - i * kSaTile);
+            valid1 = min(8, max(0, keys - i * kSaTile - 8));
+        }
+        if (valid0 + valid1 < kSaTile) {
+            for (int ci = lane; ci < kSaTile * (C::kRowBytes / 16); ci += 32) {
+                const int tr = ci / (C::kRowBytes / 16), c = ci % (C::kRowBytes / 16);
+                if (tr < 8 ? tr >= valid0 : tr - 8 >= valid1)
+                    *reinterpret_cast<uint4*>(vt + (kFp8 ? sw128(tr, c) : seg_off(tr, c))) = make_uint4(0, 0, 0, 0);
             }
             __syncwarp();
         }
@@ -234,30 +421,48 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
                 const uint4 lo = lds128(kb + sw128(r8, 2 * c4 + jc)), hi = lds128(kb + sw128(r8 + 8, 2 * c4 + jc));
                 const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 4; k += 2) {
                     const uint32_t a0 = e4m3_lo(wl[k]), a1 = e4m3_lo(wh[k]), a2 = e4m3_hi(wl[k]), a3 = e4m3_hi(wh[k]);
+                    const uint32_t b0 = e4m3_lo(wl[k + 1]), b1 = e4m3_lo(wh[k + 1]), b2 = e4m3_hi(wl[k + 1]), b3 = e4m3_hi(wh[k + 1]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16(sc[nt], a0, a1, a2, a3, qf[nt][4 * jc + k][0], qf[nt][4 * jc + k][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint4 q = q_pair(nt, 4 * jc + k);
+                        mma_f16(sc[nt], a0, a1, a2, a3, q.x, q.y);
+                        mma_f16(sc[nt], b0, b1, b2, b3, q.z, q.w);
+                    }
                 }
             }
         } else {
             const int mi = lane >> 3, tr = (mi & 1) * 8 + (lane & 7);
 #pragma unroll
-            for (int ks = 0; ks < kKSteps; ++ks) {
-                uint32_t a0, a1, a2, a3;
+            for (int ks = 0; ks < kKSteps; ks += 2) {
+                uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
                 ldsm_x4(kb + seg_off(tr, ks * 2 + (mi >> 1)), a0, a1, a2, a3);
+                ldsm_x4(kb + seg_off(tr, ks * 2 + 2 + (mi >> 1)), b0, b1, b2, b3);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_bf16(sc[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 q = q_pair(nt, ks);
+                    mma_bf16(sc[nt], a0, a1, a2, a3, q.x, q.y);
+                    mma_bf16(sc[nt], b0, b1, b2, b3, q.z, q.w);
+                }
             }
         }
-        // ---- online softmax in the log2 domain; keys past the end weigh nothing
-        const bool v0 = r8 < valid, v1 = r8 + 8 < valid;
+        // ---- online softmax in the log2 domain; other keys weigh nothing
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float x[4] = {v0 ? sc[nt][0] * p.scale_log2 : -INFINITY, v0 ? sc[nt][1] * p.scale_log2 : -INFINITY,
-                                v1 ? sc[nt][2] * p.scale_log2 : -INFINITY, v1 ? sc[nt][3] * p.scale_log2 : -INFINITY};
+            float x[4];
+#pragma unroll
+            for (int hc = 0; hc < 2; ++hc) {
+                bool v0 = r8 < valid0, v1 = r8 < valid1;
+                if constexpr (kGroup) {
+                    const uint32_t mine = bit[nt][hc] & who;
+                    v0 = (h0.who & mine) && h0.base + r8 <= limit[nt][hc];
+                    v1 = (h1.who & mine) && h1.base + r8 <= limit[nt][hc];
+                }
+                x[hc] = v0 ? sc[nt][hc] * p.scale_log2 : -INFINITY;
+                x[hc + 2] = v1 ? sc[nt][hc + 2] * p.scale_log2 : -INFINITY;
+            }
             float alpha[2], pr[4];
 #pragma unroll
             for (int hc = 0; hc < 2; ++hc) {
@@ -296,11 +501,12 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
             for (int pp = 0; pp < 4; ++pp) {
                 const uint32_t x01 = __byte_perm(k0w[pp], k1w[pp], 0x5140), x23 = __byte_perm(k2w[pp], k3w[pp], 0x5140);
                 const uint32_t y01 = __byte_perm(k0w[pp], k1w[pp], 0x7362), y23 = __byte_perm(k2w[pp], k3w[pp], 0x7362);
+                const uint32_t a0 = e4m3_lo(x01), a1 = e4m3_hi(x01), a2 = e4m3_lo(x23), a3 = e4m3_hi(x23);
+                const uint32_t b0 = e4m3_lo(y01), b1 = e4m3_hi(y01), b2 = e4m3_lo(y23), b3 = e4m3_hi(y23);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(o[2 * pp][nt], e4m3_lo(x01), e4m3_hi(x01), e4m3_lo(x23), e4m3_hi(x23), pb[nt][0], pb[nt][1]);
-                    mma_f16(o[2 * pp + 1][nt], e4m3_lo(y01), e4m3_hi(y01), e4m3_lo(y23), e4m3_hi(y23), pb[nt][0],
-                            pb[nt][1]);
+                    mma_f16(o[2 * pp][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                    mma_f16(o[2 * pp + 1][nt], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
                 }
             }
         } else {
@@ -322,7 +528,7 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
         ++cs_it;
     }
 
-    // ---- the warps' results, then the CTA's, join by their maxima
+    // ---- the warps' results, then the CTAs', join by their maxima
     __syncthreads();  // the ring is idle
     float* mine = reinterpret_cast<float*>(smem) + warp * C::kWarpFloats;
 #pragma unroll
@@ -335,8 +541,8 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
             lt += __shfl_xor_sync(0xffffffffu, lt, 16);
             const int hh = nt * 8 + c4 * 2 + hc;
             if (lane < 4) {
-                mine[C::kHeads * D + hh] = m[nt][hc];
-                mine[C::kHeads * (D + 1) + hh] = lt;
+                mine[C::kCols * D + hh] = m[nt][hc];
+                mine[C::kCols * (D + 1) + hh] = lt;
             }
 #pragma unroll
             for (int mt = 0; mt < kKSteps; ++mt) {
@@ -349,71 +555,106 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     __syncthreads();
     auto weight = [](float mw, float M) { return mw == -INFINITY ? 0.f : fast_exp2(mw - M); };
     const float* all = reinterpret_cast<const float*>(smem);
-    for (int it = tid; it < p.G * (D / 4); it += kSaThreads) {
+    for (int it = tid; it < cols * (D / 4); it += kSaThreads) {
         const int hh = it / (D / 4), c = it % (D / 4) * 4;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kSaWarps; ++w) M = fmaxf(M, all[w * C::kWarpFloats + C::kHeads * D + hh]);
+        for (int w = 0; w < kSaWarps; ++w) M = fmaxf(M, all[w * C::kWarpFloats + C::kCols * D + hh]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kSaWarps; ++w) {
             const float* x = all + w * C::kWarpFloats;
-            const float wt = weight(x[C::kHeads * D + hh], M);
+            const float wt = weight(x[C::kCols * D + hh], M);
             const float4 v = *reinterpret_cast<const float4*>(x + hh * D + c);
-            L += wt * x[C::kHeads * (D + 1) + hh];
+            L += wt * x[C::kCols * (D + 1) + hh];
             acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
         }
         *reinterpret_cast<float4*>(own + hh * D + c) = acc;
         if (c == 0) {
-            own[C::kHeads * D + hh] = M;
-            own[C::kHeads * (D + 1) + hh] = L;
+            own[C::kCols * D + hh] = M;
+            own[C::kCols * (D + 1) + hh] = L;
         }
     }
-    cluster_barrier();
-    for (int it = cta * kSaThreads + tid; it < p.G * (D / 4); it += ncta * kSaThreads) {
+    if (ncta == 1) __syncthreads();
+    else cluster_barrier();
+    bool bad = false;
+    for (int it = cta * kSaThreads + tid; it < cols * (D / 4); it += ncta * kSaThreads) {
         const int hh = it / (D / 4), c = it % (D / 4) * 4;
+        if (kGroup && !(who >> (hh / p.G) & 1 && s_stop[hh / p.G] > 0)) continue;
         float M = -INFINITY, L = 0.f;
-        for (int k = 0; k < ncta; ++k) M = fmaxf(M, load_cluster(own + C::kHeads * D + hh, k));
+        for (int k = 0; k < ncta; ++k) M = fmaxf(M, load_cluster(own + C::kCols * D + hh, k));
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < ncta; ++k) {
-            const float wt = weight(load_cluster(own + C::kHeads * D + hh, k), M);
+            const float wt = weight(load_cluster(own + C::kCols * D + hh, k), M);
             const float4 v = load_cluster4(own + hh * D + c, k);
-            L += wt * load_cluster(own + C::kHeads * (D + 1) + hh, k);
+            L += wt * load_cluster(own + C::kCols * (D + 1) + hh, k);
             acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
         }
         const float inv = p.v_scale / L;
-        *reinterpret_cast<uint2*>(p.out + (row0 + hh) * D + c) =
+        const int64_t row = row_of(hh);
+        if (kGroup) bad |= !(fabsf(acc.x) + fabsf(acc.y) + fabsf(acc.z) + fabsf(acc.w) <= 3.4e38f);
+        *reinterpret_cast<uint2*>(p.out + row * D + c) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (p.lse && c == 0) p.lse[row0 + hh] = (M + __log2f(L)) * 0.69314718055994531f;
+        if (p.lse && c == 0) p.lse[row] = (M + __log2f(L)) * 0.69314718055994531f;
     }
-    cluster_barrier();  // no CTA leaves while another reads its shared memory
+    if (kGroup && pass == 0 && bad)
+        for (int k = 0; k < ncta; ++k) store_cluster(&s_bad, k, 1u);
+    // no CTA goes on (or leaves) while another reads its shared memory
+    if (ncta == 1) {
+        if (!kGroup) return;
+        __syncthreads();
+    } else {
+        cluster_barrier();
+    }
+    if (!kGroup || ntok == 1 || s_bad == 0 || pass == ntok) return;
+    fence_proxy_async_smem();  // the ring is written by copies again
+    __syncthreads();
+    }
 }
 
-template <int D, int NT, bool kFp8>
+template <int D, int NT, bool kFp8, bool kGroup>
 cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnParams& p, int num_sms,
                cudaStream_t stream) {
-    using C = SaCfg<D, NT, kFp8>;
-    auto kern = sparse_attn_kernel<D, NT, kFp8>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    auto kern = sparse_attn_kernel<D, NT, kFp8, kGroup>;
+    const int smem = SaCfg<D, NT, kFp8>::kSmem + (kGroup ? 4 * p.list_cap : 0);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t units = (int64_t)p.num_tokens * p.Hkv;
+    const int64_t groups = kGroup ? (int64_t)p.num_tokens / p.group + p.num_reqs : p.num_tokens;
+    const int64_t units = groups * p.Hkv;
     const int tiles = (int)std::min<int64_t>(((int64_t)p.num_pages * p.bs + kSaTile - 1) / kSaTile, 1 << 30);
     int n = 1;
-    while (n < 8 && units * n < (int64_t)num_sms * 8 && tiles >= n * kSaWarps * 4) n *= 2;
-    return launch_cluster(kern, dim3((unsigned)n * (unsigned)p.num_tokens, p.Hkv), dim3(kSaThreads), C::kSmem, n, stream,
-                          km, vm, p);
+    while (n < 8 && units * n < (int64_t)num_sms * 4 && tiles >= n * kSaWarps * 4) n *= 2;
+    return launch_cluster(kern, dim3((unsigned)(n * groups), p.Hkv), dim3(kSaThreads), smem, n, stream, km, vm, p);
+}
+
+template <int D, bool kFp8>
+cudaError_t by_columns(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnParams& p, int num_sms,
+                       cudaStream_t stream) {
+    const int cols = p.group * p.G;
+    if (p.group == 1)
+        return cols > 8 ? go<D, 2, kFp8, false>(km, vm, p, num_sms, stream) : go<D, 1, kFp8, false>(km, vm, p, num_sms, stream);
+    return cols > 16  ? go<D, 4, kFp8, true>(km, vm, p, num_sms, stream)
+           : cols > 8 ? go<D, 2, kFp8, true>(km, vm, p, num_sms, stream)
+                      : go<D, 1, kFp8, true>(km, vm, p, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_sparse_attn(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnParams& p, int head_dim,
+cudaError_t launch_sparse_attn(const CUtensorMap& km, const CUtensorMap& vm, SparseAttnParams p, int head_dim,
                                bool fp8, int num_sms, cudaStream_t stream) {
-    const bool two = p.G > 8;
-    if (fp8)
-        return two ? go<128, 2, true>(km, vm, p, num_sms, stream) : go<128, 1, true>(km, vm, p, num_sms, stream);
-    if (head_dim == 128)
-        return two ? go<128, 2, false>(km, vm, p, num_sms, stream) : go<128, 1, false>(km, vm, p, num_sms, stream);
-    return two ? go<64, 2, false>(km, vm, p, num_sms, stream) : go<64, 1, false>(km, vm, p, num_sms, stream);
+    // Tokens of one request taken together: about as many as a request has on
+    // average, at most kSaGroup and 32 columns; where that leaves fewer groups
+    // than tokens (some groups are empty), and the bit maps and lists fit.
+    int group = 1;
+    while (group < kSaGroup && group * p.num_reqs < p.num_tokens && 2 * group * p.G <= 32) group *= 2;
+    const int64_t pages = ((int64_t)p.max_seq_len + p.bs - 1) / p.bs;
+    const int64_t cap = std::min<int64_t>((int64_t)group * p.num_pages, pages);
+    if (p.num_tokens / group + p.num_reqs >= p.num_tokens || pages > 32 * 1024 || cap > 4096) group = 1;
+    p.group = group;
+    p.list_cap = (int)cap;
+    if (fp8) return by_columns<128, true>(km, vm, p, num_sms, stream);
+    return head_dim == 128 ? by_columns<128, false>(km, vm, p, num_sms, stream)
+                           : by_columns<64, false>(km, vm, p, num_sms, stream);
 }
 
 }  // namespace pka

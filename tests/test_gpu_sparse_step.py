@@ -550,6 +550,111 @@ def test_sparse_attn_long_lists_over_clusters(bs, fp8):
     attn_near(out, lse, ref.sparse_attn(ref.f64(q), *map(ref.f64, caches), b["table"], b["qsl"], b["seq"], sel, 0.05))
 
 
+def grouped_case(Hq, Hkv, d, bs, K, new, fp8, alike, seed=0):
+    """Requests with several new tokens, whose lists share most pages (alike) or are drawn apart."""
+    rng = np.random.default_rng(seed + Hq + K + bs)
+    b = batch(rng, [0, 2 * bs - 3, 500, 40, 7, 333], new, bs, extra_rows=2)
+    q, caches, sel = attn_case(rng, b, Hq, Hkv, d, K, fp8=fp8)
+    if alike:
+        for t, r, p in ref.positions(b["qsl"], b["seq"]):
+            first = b["qsl"][r]
+            if t > first:
+                for g in range(Hkv):
+                    own = p // bs
+                    pages = sorted({e for e in sel[first, g] if e >= 0} | {own})[-K:]
+                    sel[t, g] = pages + [-1] * (K - len(pages))
+    return b, q, caches, sel
+
+
+GROUPS = [(8, 2, 128, 16, 6, [4, 4, 4, 4, 4, 4]), (6, 2, 64, 8, 9, [9, 1, 17, 3, 8, 2]), (16, 1, 128, 64, 3, [2, 3, 5, 1, 4, 2]),
+          (4, 4, 64, 16, 12, [33, 1, 0, 20, 7, 50]), (24, 2, 128, 32, 5, [3, 3, 3, 3, 3, 3]), (32, 4, 128, 8, 20, [4, 1, 6, 2, 5, 3]),
+          (8, 1, 128, 128, 2, [5, 5, 5, 5, 5, 5]), (2, 1, 64, 64, 4, [16, 16, 16, 0, 0, 16])]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,bs,K,new", GROUPS)
+@pytest.mark.parametrize("alike", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sparse_attn_of_several_tokens(Hq, Hkv, d, bs, K, new, alike, fp8):
+    if fp8 and d == 64:
+        pytest.skip("the 8-bit cache's attention has head dim 128")
+    b, q, caches, sel = grouped_case(Hq, Hkv, d, bs, K, new, fp8, alike)
+    sel[b["qsl"][1] - 1] = -1                    # the last token of a request reads nothing
+    sel[b["qsl"][3] - 2, :, 1:] = -1             # another one page only
+    units = (0.125, 0.11) if fp8 else None
+    out, lse, err = attn_run(b, q, caches, sel, d ** -0.5, units)
+    assert err == 0
+    attn_near(out, lse, ref.sparse_attn(ref.f64(q), *map(ref.f64, caches), b["table"], b["qsl"], b["seq"], sel, d ** -0.5,
+                                        [float(np.float32(u)) for u in units] if fp8 else (1.0, 1.0)))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bs", [8, 16, 64])
+def test_sparse_attn_values_of_other_tokens_stay_hidden(bs, fp8):
+    """NaN and infinities in the values and keys of pages that a token does not list, and of the tokens after
+    it, do not reach it, whoever else in its request reads them; who lists them gets them."""
+    b, q, caches, sel = grouped_case(8, 2, 128, bs, 6, [4, 4, 4, 4, 4, 4], fp8, False, seed=1)
+    spoil = 0x7F if fp8 else float("nan")
+    reads = {}
+    for r in (2, 5):  # one page of the request, listed by its second token only
+        t0 = b["qsl"][r]
+        page = 1
+        pages = sorted([page] + [e for e in sel[t0 + 1, 0] if e >= 0 and e != page][-5:])
+        sel[t0 + 1, 0] = pages + [-1] * (6 - len(pages))
+        for t in range(t0, t0 + 4):
+            for g in range(2):
+                if t != t0 + 1 or g:
+                    kept = [e for e in sel[t, g] if e >= 0 and e != page]
+                    sel[t, g] = kept + [-1] * (6 - len(kept))
+        caches[1][b["table"][r, page], 0, 3] = spoil
+        reads[t0 + 1] = True
+        if r == 5:
+            caches[0][b["table"][r, page], 0, 2] = spoil
+    # the newest token of request 3: infinite values that its earlier ones stand before
+    p = b["seq"][3] - 1
+    caches[1][b["table"][3, p // bs], :, p % bs] = spoil if fp8 else float("inf")
+    for t in range(b["qsl"][3], b["qsl"][4]):
+        own = (p - (b["qsl"][4] - 1 - t)) // bs
+        for g in range(2):
+            pages = sorted({e for e in sel[t, g] if 0 <= e < own} | {own})[-6:]
+            sel[t, g] = pages + [-1] * (6 - len(pages))
+    reads[b["qsl"][4] - 1] = True
+    units = (0.125, 0.11) if fp8 else None
+    out, lse, err = attn_run(b, q, caches, sel, 0.1, units)
+    assert err == 0
+    hit = ~torch.isfinite(out.float()).all(-1)
+    for t in range(b["qsl"][-1]):
+        heads = hit[t].cpu().numpy()
+        if t in reads and t == b["qsl"][4] - 1:
+            assert heads.all()
+        elif t in reads:
+            assert heads[:4].all() and not heads[4:].any()
+        else:
+            assert not heads.any(), t
+    want = ref.sparse_attn(ref.f64(q), *map(ref.f64, caches), b["table"], b["qsl"], b["seq"], sel, 0.1,
+                           [float(np.float32(u)) for u in units] if fp8 else (1.0, 1.0))
+    for t in reads:  # (compared above)
+        want[2][t] = 1e9
+        want[0][t] = 0
+        want[1][t] = lse[t].cpu().numpy()
+        out[t] = 0
+    out, lse = out.nan_to_num(0, 0, 0), lse.nan_to_num(0, 0, 0)
+    want = (want[0], np.nan_to_num(want[1], nan=np.nan), want[2])
+    ok = ~np.isnan(want[1])
+    assert (np.abs(ref.f64(lse) - want[1])[ok] <= 2.0 ** -14 * (1 + np.abs(want[1][ok]))).all()
+    attn_near(out, None, want)
+
+
+def test_sparse_attn_of_several_tokens_reports_bad_lists():
+    b, q, caches, sel = grouped_case(8, 2, 128, 16, 6, [4, 4, 4, 4, 4, 4], False, False, seed=2)
+    t = b["qsl"][2] + 1
+    sel[t, 1] = [3, 9, 9, 12, -1, -1]            # twice the same page: the list ends there
+    sel[t + 1, 0] = [1, 4, 5, 600, -1, -1]       # past the token's page
+    out, lse, err = attn_run(b, q, caches, sel, 0.1)
+    assert err == E["INDEX"]
+    sel[t, 1], sel[t + 1, 0] = [3, 9, -1, -1, -1, -1], [1, 4, 5, -1, -1, -1]
+    attn_near(out, lse, ref.sparse_attn(ref.f64(q), *map(ref.f64, caches), b["table"], b["qsl"], b["seq"], sel, 0.1))
+
+
 def test_sparse_attn_with_every_page_is_the_dense_decode():
     rng = np.random.default_rng(11)
     b = batch(rng, [5, 100, 1000, 333], [1, 1, 1, 1], 16)
