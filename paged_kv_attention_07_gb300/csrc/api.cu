@@ -1189,6 +1189,8 @@ pka_status sparse_attn_impl(const void* q, const void* k_cache, const void* v_ca
     p.Hkv = num_kv_heads;
     p.G = num_q_heads / num_kv_heads;
     p.bs = block_size;
+    for (p.bs_log2 = 0; 1 << p.bs_log2 < block_size; ++p.bs_log2) {
+    }
     p.num_pages = num_pages;
     p.max_seq_len = max_seq_len;
     p.scale_log2 = scale * 1.4426950408889634f * (cf.fp8 ? cf.k_scale : 1.f);

@@ -40,6 +40,7 @@ namespace {
 constexpr int kSaWarps = 4;
 constexpr int kSaThreads = kSaWarps * 32;
 constexpr int kSaTile = 16;  // keys per tile
+constexpr int kSaJoin = 8;   // CTAs' results read together
 constexpr int kSaGroup = 8;  // tokens of a group, at most
 
 template <int D, int NT, bool kFp8>
@@ -160,18 +161,29 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     // ---- the lists: each ends at its first negative entry; entries ascend and none is past the token's page
     const int32_t* sel = p.sel + ((int64_t)t0 * p.Hkv + g) * p.num_pages;
     const int64_t sel_step = (int64_t)p.Hkv * p.num_pages;  // from a token's list to the next one's
-    for (int k = 0; k < ntok; ++k) {
-        const int own_page = (pos0 + k) / p.bs;
-        const int32_t* list = sel + k * sel_step;
+    if constexpr (!kGroup) {
+        const int own_page = pos0 >> p.bs_log2;
         for (int i = tid; i < p.num_pages; i += kSaThreads) {
-            const int e = __ldg(list + i), before = i ? __ldg(list + i - 1) : -1;
+            const int e = __ldg(sel + i), before = i ? __ldg(sel + i - 1) : -1;
             if (e <= before || e > own_page) {  // e < 0 among them
-                atomicMin(&s_stop[k], i);
+                atomicMin(&s_stop[0], i);
                 break;
             }
         }
+    } else {
+        for (int i0 = tid; i0 < p.num_pages; i0 += kSaThreads) {
+            int e[kSaGroup], before[kSaGroup];
+#pragma unroll
+            for (int k = 0; k < kSaGroup; ++k) {
+                e[k] = k < ntok ? __ldg(sel + k * sel_step + i0) : 0;
+                before[k] = k < ntok && i0 ? __ldg(sel + k * sel_step + i0 - 1) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kSaGroup; ++k)
+                if (k < ntok && (e[k] <= before[k] || e[k] > (pos0 + k) >> p.bs_log2)) atomicMin(&s_stop[k], i0);
+        }
     }
-    const int last_page = pos1 / p.bs;
+    const int last_page = pos1 >> p.bs_log2;
     const int words = last_page / 32 + 1;
     uint32_t* s_map = reinterpret_cast<uint32_t*>(smem);  // (the ring is idle still) a bit map per token
     if constexpr (kGroup)
@@ -181,11 +193,14 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
         set_error(p.err, PKA_DEVERR_INDEX);
     int count = s_stop[0], last = -1;  // pages to read, and the last of them
     if constexpr (kGroup) {
-        for (int k = 0; k < ntok; ++k)
-            for (int i = tid; i < s_stop[k]; i += kSaThreads) {
-                const int e = __ldg(sel + k * sel_step + i);
-                atomicOr(&s_map[k * words + (e >> 5)], 1u << (e & 31));
-            }
+        for (int i = tid; i < p.num_pages; i += kSaThreads) {
+            int e[kSaGroup];
+#pragma unroll
+            for (int k = 0; k < kSaGroup; ++k) e[k] = k < ntok && i < s_stop[k] ? __ldg(sel + k * sel_step + i) : -1;
+#pragma unroll
+            for (int k = 0; k < kSaGroup; ++k)
+                if (e[k] >= 0) atomicOr(&s_map[k * words + (e[k] >> 5)], 1u << (e[k] & 31));
+        }
         __syncthreads();
         const int per = (words + kSaThreads - 1) / kSaThreads;
         const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
@@ -211,12 +226,17 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
             count += (int)s_scan[w];
         }
         for (int w = w0; w < w1; ++w) {
-            uint32_t any = 0;
-            for (int k = 0; k < ntok; ++k) any |= s_map[k * words + w];
+            uint32_t any = 0, map[kSaGroup];
+#pragma unroll
+            for (int k = 0; k < kSaGroup; ++k) {
+                map[k] = k < ntok ? s_map[k * words + w] : 0u;
+                any |= map[k];
+            }
             for (; any; any &= any - 1) {
                 const int bit = __ffs(any) - 1;
                 uint32_t who = 0;
-                for (int k = 0; k < ntok; ++k) who |= (s_map[k * words + w] >> bit & 1u) << k;
+#pragma unroll
+                for (int k = 0; k < kSaGroup; ++k) who |= (map[k] >> bit & 1u) << k;
                 s_list[at++] = (uint32_t)(w * 32 + bit) | who << 24;
             }
         }
@@ -226,7 +246,7 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     } else {
         if (count > 0) last = __ldg(sel + count - 1);
     }
-    const int keys = count * p.bs - (last == last_page ? p.bs - 1 - pos1 % p.bs : 0);
+    const int keys = count * p.bs - (last == last_page ? p.bs - 1 - (pos1 & (p.bs - 1)) : 0);
     // tokens without a page: nothing to read
     if (cta == 0)
         for (int k = 0; k < ntok; ++k) {
@@ -238,7 +258,10 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     if (keys == 0) return;
     const int ntiles = (keys + kSaTile - 1) / kSaTile;
     const int part = cta * kSaWarps + warp, parts = ncta * kSaWarps;
-    const int i0 = (int)((int64_t)ntiles * part / parts), i1 = (int)((int64_t)ntiles * (part + 1) / parts);
+    // (parts is a power of two up to 64, ntiles below 2^31 / kSaTile)
+    const int parts_log2 = 31 - __clz(parts);
+    const int i0 = (int)((uint32_t)ntiles >> parts_log2) * part + (((ntiles & (parts - 1)) * part) >> parts_log2);
+    const int i1 = (int)((uint32_t)ntiles >> parts_log2) * (part + 1) + (((ntiles & (parts - 1)) * (part + 1)) >> parts_log2);
 
     // ---- this warp's loads
     const uint64_t pol = policy_evict_first();
@@ -248,7 +271,7 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     uint32_t entry = 0;         // and, of a group, its entry
     uint32_t ld_it = 0, cs_it = 0;
     auto issue = [&](int i) {
-        const int first = i * kSaTile / p.bs;
+        const int first = (i * kSaTile) >> p.bs_log2;
         if (first < page0 || first + kSaTile / boxr > page0 + 32) {
             page0 = first;
             const int j = page0 + lane;
@@ -270,7 +293,7 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
             }
             rows = (blk * p.Hkv + g) * p.bs;
         }
-        const int off = i * kSaTile % p.bs;
+        const int off = (i * kSaTile) & (p.bs - 1);
         const int ra = __shfl_sync(0xffffffffu, rows, first - page0) + off;
         const int rb = __shfl_sync(0xffffffffu, rows, (first + 1 - page0) & 31);  // bs == 8: the tile's second page
         const int stage = ld_it % C::kStages;
@@ -289,7 +312,6 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
         if (lane == 0) {
             uint8_t* kdst = ring + stage * C::kStageBytes;
             uint8_t* vdst = kdst + C::kTileBytes;
-            fence_proxy_async_smem();
             mbar_arrive_expect_tx(&full[stage], (uint32_t)(2 * nbox * boxr * C::kRowBytes));
             for (int b = 0; b < nbox; ++b) {
                 const int row = b ? rb : ra;
@@ -407,6 +429,7 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
                 if (tr < 8 ? tr >= valid0 : tr - 8 >= valid1)
                     *reinterpret_cast<uint4*>(vt + (kFp8 ? sw128(tr, c) : seg_off(tr, c))) = make_uint4(0, 0, 0, 0);
             }
+            fence_proxy_async_smem();  // (a later copy writes these places again)
             __syncwarp();
         }
         const uint32_t kb = smem_u32(kt), vb = smem_u32(vt);
@@ -581,14 +604,33 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     for (int it = cta * kSaThreads + tid; it < cols * (D / 4); it += ncta * kSaThreads) {
         const int hh = it / (D / 4), c = it % (D / 4) * 4;
         if (kGroup && !(who >> (hh / p.G) & 1 && s_stop[hh / p.G] > 0)) continue;
+        // up to kSaJoin CTAs' parts in flight together
         float M = -INFINITY, L = 0.f;
-        for (int k = 0; k < ncta; ++k) M = fmaxf(M, load_cluster(own + C::kCols * D + hh, k));
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < ncta; ++k) {
-            const float wt = weight(load_cluster(own + C::kCols * D + hh, k), M);
-            const float4 v = load_cluster4(own + hh * D + c, k);
-            L += wt * load_cluster(own + C::kCols * (D + 1) + hh, k);
-            acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
+        for (int k0 = 0; k0 < ncta; k0 += kSaJoin) {
+            float mk[kSaJoin], lk[kSaJoin];
+            float4 vk[kSaJoin];
+#pragma unroll
+            for (int j = 0; j < kSaJoin; ++j) {
+                if (k0 + j >= ncta) continue;
+                mk[j] = load_cluster(own + C::kCols * D + hh, k0 + j);
+                lk[j] = load_cluster(own + C::kCols * (D + 1) + hh, k0 + j);
+                vk[j] = load_cluster4(own + hh * D + c, k0 + j);
+            }
+            float Mn = M;
+#pragma unroll
+            for (int j = 0; j < kSaJoin; ++j)
+                if (k0 + j < ncta) Mn = fmaxf(Mn, mk[j]);
+            const float keep = weight(M, Mn);
+            M = Mn;
+            L *= keep, acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+            for (int j = 0; j < kSaJoin; ++j) {
+                if (k0 + j >= ncta) continue;
+                const float wt = weight(mk[j], M);
+                L += wt * lk[j];
+                acc.x += wt * vk[j].x, acc.y += wt * vk[j].y, acc.z += wt * vk[j].z, acc.w += wt * vk[j].w;
+            }
         }
         const float inv = p.v_scale / L;
         const int64_t row = row_of(hh);
@@ -624,6 +666,7 @@ cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnPar
     const int tiles = (int)std::min<int64_t>(((int64_t)p.num_pages * p.bs + kSaTile - 1) / kSaTile, 1 << 30);
     int n = 1;
     while (n < 8 && units * n < (int64_t)num_sms * 4 && tiles >= n * kSaWarps * 4) n *= 2;
+
     return launch_cluster(kern, dim3((unsigned)(n * groups), p.Hkv), dim3(kSaThreads), smem, n, stream, km, vm, p);
 }
 
