@@ -47,8 +47,7 @@ cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream);
 cudaError_t launch_qk_rope(const QkRopeParams& p, bool fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_bounds(PageBoundsParams p, bool fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream);
-cudaError_t launch_sparse_attn(const CUtensorMap& km, const CUtensorMap& vm, SparseAttnParams p, int head_dim,
-                               bool fp8, int num_sms, cudaStream_t stream);
+cudaError_t launch_sparse_attn(SparseAttnParams p, int head_dim, bool fp8, int num_sms, cudaStream_t stream);
 
 // MLA decode units per (request, split): on the tensor-core kernel two value
 // halves per group of 128 heads, otherwise one unit per 64-head group.
@@ -117,22 +116,6 @@ bool encode_rows_u8(CUtensorMap* map, const void* base, uint64_t rows, uint32_t 
     cuuint32_t box[2] = {128, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 3-D bf16 view of dense rows [rows, D] as [D / 64 segments, rows, 64 columns],
-// read in boxes of 64 columns x box_rows rows x `segments` (128-byte swizzle):
-// one box gives whole rows, segment after segment.
-bool encode_segments(CUtensorMap* map, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows,
-                     uint32_t segments) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {64, rows, D / 64};
-    cuuint64_t strides[2] = {D * 2, 128};
-    cuuint32_t box[3] = {64, box_rows, segments};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1164,16 +1147,10 @@ pka_status sparse_attn_impl(const void* q, const void* k_cache, const void* v_ca
         return PKA_ERR_INVALID_ARG;
     const int sms = device_sm_count();
     if (sms <= 0) return PKA_ERR_CUDA;
-    const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * block_size;
-    const uint32_t br = (uint32_t)std::min(block_size, 16);
-    CUtensorMap km, vm;
-    const uint32_t segments = br == 16 ? (uint32_t)head_dim / 64 : 1;
-    const bool ok = cf.fp8 ? encode_rows_u8(&km, k_cache, rows, br) && encode_rows_u8(&vm, v_cache, rows, br)
-                           : encode_segments(&km, k_cache, rows, (uint64_t)head_dim, br, segments) &&
-                                 encode_segments(&vm, v_cache, rows, (uint64_t)head_dim, br, segments);
-    if (!ok) return PKA_ERR_CUDA;
     SparseAttnParams p;
     p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
     p.block_table = block_table;
     p.qsl = query_start_loc;
     p.seq_lens = seq_lens;
@@ -1197,7 +1174,7 @@ pka_status sparse_attn_impl(const void* q, const void* k_cache, const void* v_ca
     p.v_scale = cf.fp8 ? cf.v_scale : 1.f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(
-        timed(PKA_KERNEL_SPARSE_ATTN, st, [&] { return launch_sparse_attn(km, vm, p, head_dim, cf.fp8, sms, st); }));
+        timed(PKA_KERNEL_SPARSE_ATTN, st, [&] { return launch_sparse_attn(p, head_dim, cf.fp8, sms, st); }));
 }
 
 }  // namespace

@@ -222,6 +222,11 @@ PKA_DEVICE void cp_async_16(uint32_t smem_addr, const void* gptr) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr), "l"(gptr) : "memory");
 }
 
+PKA_DEVICE void cp_async_16_hint(uint32_t smem_addr, const void* gptr, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_addr), "l"(gptr), "l"(policy)
+                 : "memory");
+}
+
 // 16-byte copy that writes zeros instead when `valid` is false.
 PKA_DEVICE void cp_async_16_zfill(uint32_t smem_addr, const void* gptr, bool valid) {
     const uint32_t n = valid ? 16u : 0u;

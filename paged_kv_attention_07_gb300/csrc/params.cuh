@@ -186,6 +186,8 @@ struct PageSelectParams {
 
 struct SparseAttnParams {
     const __nv_bfloat16* q;  // [T, Hq, d]
+    const void* k_cache;     // [num_blocks, Hkv, bs, d] bf16 or E4M3 codes
+    const void* v_cache;
     const int32_t* block_table;
     const int32_t* qsl;
     const int32_t* seq_lens;

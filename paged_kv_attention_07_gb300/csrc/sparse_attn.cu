@@ -8,11 +8,13 @@
 // (count - 1) * bs + tail keys: tile i of 16 keys lies in page e[16 i / bs].
 //
 // HBM-bound: every listed page is read once, 16 keys of one (page, kv head) are
-// one contiguous tile that a TMA box brings into a warp's own ring of stages
-// (all 128-byte column segments of the rows with one copy). A warp owns a
-// contiguous run of tiles and never waits for another: its lanes hold the
-// cache rows of its next 32 pages (list entry -> block table -> row), a tile's
-// row is one shuffle away. The work of one (token, kv head) is split over the
+// one contiguous tile that 16-byte asynchronous copies bring into a warp's own
+// ring of stages (swizzled by the row, so that the fragments' reads meet no bank
+// twice). Tile copies by TMA boxes read a full batch as fast, but one lane's
+// TMA instructions take 390 to 750 cycles of the warp's time per tile, more than
+// the products; 32 lanes' copies some 80. A warp owns a contiguous run of tiles
+// and never waits for another: its lanes hold the cache rows of its next 32
+// pages (list entry -> block table -> row), a tile's row is one shuffle away. The work of one (token, kv head) is split over the
 // 4 warps of a CTA and the CTAs of a cluster; the warps' (m, l, O) join in
 // shared memory and the CTAs' over distributed shared memory, so there is one
 // launch and nothing partial goes to memory.
@@ -58,7 +60,7 @@ struct SaCfg {
     static constexpr int kWarpFloats = kCols * (D + 2);
     static constexpr int kJoin = kSaWarps * kWarpFloats * 4;
     static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
-    static constexpr int kSmem = 1024 /*align*/ + kBody + kWarpFloats * 4 + kQ + kSaWarps * kStages * 8;
+    static constexpr int kSmem = 1024 /*align*/ + kBody + kWarpFloats * 4 + kQ;
 };
 
 // A tile's keys in a group, eight at a time: the position of the first, and the
@@ -104,8 +106,7 @@ PKA_DEVICE uint32_t seg_off(int tr, int c) { return sw128((uint32_t)((c >> 3) * 
 
 template <int D, int NT, bool kFp8, bool kGroup>
 __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
-    sparse_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const SparseAttnParams p) {
+    sparse_attn_kernel(const SparseAttnParams p) {
     using C = SaCfg<D, NT, kFp8>;
     constexpr int kKSteps = D / 16;
     extern __shared__ uint8_t smem_raw[];
@@ -118,17 +119,8 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* own = reinterpret_cast<float*>(smem + C::kBody);  // this CTA's O [kCols][D], m, l
     uint4* s_q = reinterpret_cast<uint4*>(smem + C::kBody + C::kWarpFloats * 4);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBody + C::kWarpFloats * 4 + C::kQ) + warp * C::kStages;
     // a group's united list: page | tokens << 24
     uint32_t* s_list = reinterpret_cast<uint32_t*>(smem + C::kSmem - 1024);
-    if (lane == 0) {
-        for (int s = 0; s < C::kStages; ++s) mbar_init(&full[s], 1);
-        fence_barrier_init();
-        if (warp == 0) {
-            tma_prefetch_desc(&kmap);
-            tma_prefetch_desc(&vmap);
-        }
-    }
     if (tid < kSaGroup) s_stop[tid] = p.num_pages;
     if (tid == 0) s_bad = 0;
     __syncthreads();
@@ -240,8 +232,7 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
                 s_list[at++] = (uint32_t)(w * 32 + bit) | who << 24;
             }
         }
-        fence_proxy_async_smem();  // the ring is written by copies from here on
-        __syncthreads();
+        __syncthreads();  // (the ring is written by copies from here on)
         if (count > 0) last = (int)(s_list[count - 1] & 0xffffffu);
     } else {
         if (count > 0) last = __ldg(sel + count - 1);
@@ -263,14 +254,23 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     const int i0 = (int)((uint32_t)ntiles >> parts_log2) * part + (((ntiles & (parts - 1)) * part) >> parts_log2);
     const int i1 = (int)((uint32_t)ntiles >> parts_log2) * (part + 1) + (((ntiles & (parts - 1)) * (part + 1)) >> parts_log2);
 
-    // ---- this warp's loads
+    // ---- this warp's loads: step j of a tile copies 32 pieces of 16 bytes, kRows rows
+    constexpr int kPieces = C::kRowBytes / 16, kRows = 32 / kPieces, kSteps = kSaTile / kRows;
     const uint64_t pol = policy_evict_first();
+    const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache) + lane * 16;
+    const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache) + lane * 16;
+    uint32_t place[8 / kRows];  // of step j in a tile; 8 rows on, the same swizzle
+#pragma unroll
+    for (int j = 0; j < 8 / kRows; ++j) {
+        const int row = j * kRows + lane / kPieces, piece = lane % kPieces;
+        place[j] = kFp8 ? sw128(row, piece) : seg_off(row, piece);
+    }
     uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
     const int boxr = min(p.bs, kSaTile);
     int page0 = -32, rows = 0;  // lane l holds the first cache row of listed page page0 + l
     uint32_t entry = 0;         // and, of a group, its entry
-    uint32_t ld_it = 0, cs_it = 0;
-    auto issue = [&](int i) {
+    uint32_t it = 0;  // tiles taken
+    auto issue = [&](int i, int stage) {
         const int first = (i * kSaTile) >> p.bs_log2;
         if (first < page0 || first + kSaTile / boxr > page0 + 32) {
             page0 = first;
@@ -296,8 +296,7 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
         const int off = (i * kSaTile) & (p.bs - 1);
         const int ra = __shfl_sync(0xffffffffu, rows, first - page0) + off;
         const int rb = __shfl_sync(0xffffffffu, rows, (first + 1 - page0) & 31);  // bs == 8: the tile's second page
-        const int stage = ld_it % C::kStages;
-        const int nbox = boxr < kSaTile && i * kSaTile + boxr < keys ? 2 : 1;
+        const bool two = boxr < kSaTile && i * kSaTile + boxr < keys;
         if constexpr (kGroup) {
             const uint32_t ea = __shfl_sync(0xffffffffu, entry, first - page0);
             const uint32_t eb = boxr < kSaTile ? __shfl_sync(0xffffffffu, entry, (first + 1 - page0) & 31) : ea;
@@ -305,36 +304,32 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
                 const uint32_t e = lane ? eb : ea;
                 SaHalf h;
                 h.base = (int)(e & 0xffffffu) * p.bs + (boxr < kSaTile ? 0 : off + 8 * lane);
-                h.who = lane && nbox == 1 && boxr < kSaTile ? 0u : e >> 24;
+                h.who = lane && boxr < kSaTile && !two ? 0u : e >> 24;
                 s_half[warp][stage][lane] = h;
             }
         }
-        if (lane == 0) {
-            uint8_t* kdst = ring + stage * C::kStageBytes;
-            uint8_t* vdst = kdst + C::kTileBytes;
-            mbar_arrive_expect_tx(&full[stage], (uint32_t)(2 * nbox * boxr * C::kRowBytes));
-            for (int b = 0; b < nbox; ++b) {
-                const int row = b ? rb : ra;
-                if constexpr (kFp8) {
-                    tma_load_2d(kdst + b * boxr * 128, &kmap, &full[stage], 0, row, pol);
-                    tma_load_2d(vdst + b * boxr * 128, &vmap, &full[stage], 0, row, pol);
-                } else if (nbox == 1 && boxr == kSaTile) {
-                    tma_load_3d(kdst, &kmap, &full[stage], 0, row, 0, pol);
-                    tma_load_3d(vdst, &vmap, &full[stage], 0, row, 0, pol);
-                } else {  // boxes of 8 rows and one segment
+        const uint32_t kdst = smem_u32(ring + stage * C::kStageBytes), vdst = kdst + C::kTileBytes;
 #pragma unroll
-                    for (int sg = 0; sg < D / 64; ++sg) {
-                        const int at = (sg * kSaTile + b * boxr) * 128;
-                        tma_load_3d(kdst + at, &kmap, &full[stage], 0, row, sg, pol);
-                        tma_load_3d(vdst + at, &vmap, &full[stage], 0, row, sg, pol);
-                    }
-                }
+        for (int h = 0; h < 2; ++h) {  // eight rows each
+            if (h && boxr < kSaTile && !two) break;
+            const int64_t src = (int64_t)(h && boxr < kSaTile ? rb - 8 : ra) * C::kRowBytes;
+#pragma unroll
+            for (int j = 0; j < kSteps / 2; ++j) {
+                const int step = h * (kSteps / 2) + j;
+                cp_async_16_hint(kdst + place[j] + h * 1024, kc + src + step * 512, pol);
+                cp_async_16_hint(vdst + place[j] + h * 1024, vc + src + step * 512, pol);
             }
         }
-        ++ld_it;
-        __syncwarp();
     };
-    for (int i = i0; i < i1 && i < i0 + C::kStages; ++i) issue(i);
+    auto first_tiles = [&] {
+#pragma unroll
+        for (int s = 0; s < C::kStages; ++s) {
+            if (i0 + s < i1) issue(i0 + s, s);
+            cp_async_commit();  // (a group per tile, empty behind the last)
+        }
+        it = 0;
+    };
+    first_tiles();
 
     // ---- Q^T fragments: column n, zero behind the last
     uint32_t qf[C::kQShared ? 1 : NT][kKSteps][2];
@@ -394,8 +389,7 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     for (int pass = 0;; ++pass) {
     const uint32_t who = pass == 0 ? (1u << ntok) - 1 : 1u << (pass - 1);  // the tokens of this pass
     const int end = pass == 0 ? pos1 : pos0 + pass - 1;                    // the last one's position
-    if (pass > 0)
-        for (int i = i0; i < i1 && i < i0 + C::kStages; ++i) issue(i);
+    if (pass > 0) first_tiles();
     float o[kKSteps][NT][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -407,9 +401,10 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
     }
 
     for (int i = i0; i < i1; ++i) {
-        const int stage = cs_it % C::kStages;
-        if (!mbar_wait_warp(&full[stage], (cs_it / C::kStages) & 1, p.err)) break;
-        ++cs_it;
+        const int stage = it % C::kStages;
+        ++it;
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();
         uint8_t* kt = ring + stage * C::kStageBytes;
         uint8_t* vt = kt + C::kTileBytes;
         // valid keys of the tile's two halves; the rest's values may be anything: zeros instead
@@ -429,7 +424,6 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
                 if (tr < 8 ? tr >= valid0 : tr - 8 >= valid1)
                     *reinterpret_cast<uint4*>(vt + (kFp8 ? sw128(tr, c) : seg_off(tr, c))) = make_uint4(0, 0, 0, 0);
             }
-            fence_proxy_async_smem();  // (a later copy writes these places again)
             __syncwarp();
         }
         const uint32_t kb = smem_u32(kt), vb = smem_u32(vt);
@@ -543,14 +537,9 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
             }
         }
         __syncwarp();
-        if (i + C::kStages < i1) issue(i + C::kStages);
+        if (i + C::kStages < i1) issue(i + C::kStages, stage);
+        cp_async_commit();
     }
-    // after a wait that gave up: no copy may outlive the CTA
-    while (cs_it < ld_it) {
-        mbar_wait_warp(&full[cs_it % C::kStages], (cs_it / C::kStages) & 1, p.err);
-        ++cs_it;
-    }
-
     // ---- the warps' results, then the CTAs', join by their maxima
     __syncthreads();  // the ring is idle
     float* mine = reinterpret_cast<float*>(smem) + warp * C::kWarpFloats;
@@ -649,14 +638,11 @@ __global__ void __launch_bounds__(kSaThreads, kFp8 && NT == 1 ? 4 : 2)
         cluster_barrier();
     }
     if (!kGroup || ntok == 1 || s_bad == 0 || pass == ntok) return;
-    fence_proxy_async_smem();  // the ring is written by copies again
-    __syncthreads();
     }
 }
 
 template <int D, int NT, bool kFp8, bool kGroup>
-cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnParams& p, int num_sms,
-               cudaStream_t stream) {
+cudaError_t go(const SparseAttnParams& p, int num_sms, cudaStream_t stream) {
     auto kern = sparse_attn_kernel<D, NT, kFp8, kGroup>;
     const int smem = SaCfg<D, NT, kFp8>::kSmem + (kGroup ? 4 * p.list_cap : 0);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -667,24 +653,22 @@ cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnPar
     int n = 1;
     while (n < 8 && units * n < (int64_t)num_sms * 4 && tiles >= n * kSaWarps * 4) n *= 2;
 
-    return launch_cluster(kern, dim3((unsigned)(n * groups), p.Hkv), dim3(kSaThreads), smem, n, stream, km, vm, p);
+    return launch_cluster(kern, dim3((unsigned)(n * groups), p.Hkv), dim3(kSaThreads), smem, n, stream, p);
 }
 
 template <int D, bool kFp8>
-cudaError_t by_columns(const CUtensorMap& km, const CUtensorMap& vm, const SparseAttnParams& p, int num_sms,
-                       cudaStream_t stream) {
+cudaError_t by_columns(const SparseAttnParams& p, int num_sms, cudaStream_t stream) {
     const int cols = p.group * p.G;
     if (p.group == 1)
-        return cols > 8 ? go<D, 2, kFp8, false>(km, vm, p, num_sms, stream) : go<D, 1, kFp8, false>(km, vm, p, num_sms, stream);
-    return cols > 16  ? go<D, 4, kFp8, true>(km, vm, p, num_sms, stream)
-           : cols > 8 ? go<D, 2, kFp8, true>(km, vm, p, num_sms, stream)
-                      : go<D, 1, kFp8, true>(km, vm, p, num_sms, stream);
+        return cols > 8 ? go<D, 2, kFp8, false>(p, num_sms, stream) : go<D, 1, kFp8, false>(p, num_sms, stream);
+    return cols > 16  ? go<D, 4, kFp8, true>(p, num_sms, stream)
+           : cols > 8 ? go<D, 2, kFp8, true>(p, num_sms, stream)
+                      : go<D, 1, kFp8, true>(p, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_sparse_attn(const CUtensorMap& km, const CUtensorMap& vm, SparseAttnParams p, int head_dim,
-                               bool fp8, int num_sms, cudaStream_t stream) {
+cudaError_t launch_sparse_attn(SparseAttnParams p, int head_dim, bool fp8, int num_sms, cudaStream_t stream) {
     // Tokens of one request taken together: about as many as a request has on
     // average, at most kSaGroup and 32 columns; where that leaves fewer groups
     // than tokens (some groups are empty), and the bit maps and lists fit.
@@ -695,9 +679,9 @@ cudaError_t launch_sparse_attn(const CUtensorMap& km, const CUtensorMap& vm, Spa
     if (p.num_tokens / group + p.num_reqs >= p.num_tokens || pages > 32 * 1024 || cap > 4096) group = 1;
     p.group = group;
     p.list_cap = (int)cap;
-    if (fp8) return by_columns<128, true>(km, vm, p, num_sms, stream);
-    return head_dim == 128 ? by_columns<128, false>(km, vm, p, num_sms, stream)
-                           : by_columns<64, false>(km, vm, p, num_sms, stream);
+    if (fp8) return by_columns<128, true>(p, num_sms, stream);
+    return head_dim == 128 ? by_columns<128, false>(p, num_sms, stream)
+                           : by_columns<64, false>(p, num_sms, stream);
 }
 
 }  // namespace pka
