@@ -47,7 +47,7 @@ cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream);
 cudaError_t launch_qk_rope(const QkRopeParams& p, bool fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_bounds(PageBoundsParams p, bool fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream);
-cudaError_t launch_sparse_attn(SparseAttnParams p, int head_dim, bool fp8, int num_sms, cudaStream_t stream);
+cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, bool fp8, int num_sms, cudaStream_t stream);
 
 // MLA decode units per (request, split): on the tensor-core kernel two value
 // halves per group of 128 heads, otherwise one unit per 64-head group.

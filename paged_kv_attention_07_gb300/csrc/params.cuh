@@ -198,7 +198,6 @@ struct SparseAttnParams {
     int64_t num_blocks;
     int num_tokens, num_reqs, max_blocks, Hq, Hkv, G, bs, bs_log2, num_pages, max_seq_len;
     float scale_log2, v_scale;  // 8-bit cache: scale * k_scale, and the output's factor
-    int group, list_cap;        // tokens taken together and their united list's most pages: set by the launch
 };
 
 struct FaMaps {

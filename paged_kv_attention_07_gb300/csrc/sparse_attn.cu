@@ -20,13 +20,11 @@
 // shared memory and the CTAs' over distributed shared memory, so there is one
 // launch and nothing partial goes to memory.
 //
-// Several tokens of one request (a prompt's chunk, drafted tokens) are taken in
-// groups: their lists, mostly the same pages, are united in shared memory (a
-// bit map per token, then one prefix sum), each page of the union is read once,
-// and the tokens' heads lie side by side in the MMA's columns; columns whose
-// token does not list the page, or stands before the key, get weight zero. A
-// zero weight does not hide an infinite or NaN value, so a group whose result is
-// not finite throughout is done again token by token.
+// Each token reads its own pages, tokens of one request mostly the same ones
+// through L2. (Taking such tokens together over their united lists was measured:
+// 96 x 4 tokens 238 -> 216 us, but 24 x 4 tokens 46 -> 52 us and 8-bit caches
+// 143 -> 201 us: the lists' union and the registers of more columns cost what
+// the shared reads save.)
 //
 // Math per tile (tensor cores, fp32 accumulation):
 //   S^T[keys x 8 columns] = K Q^T;  online softmax per column;  O^T += V^T P^T
@@ -50,7 +48,6 @@ namespace {
 constexpr int kSaWarps = 4;
 constexpr int kSaThreads = kSaWarps * 32;
 constexpr int kSaJoin = 8;   // CTAs' results read together
-constexpr int kSaGroup = 8;  // tokens of a group, at most
 
 template <int D, int NT, bool kFp8>
 struct SaCfg {
@@ -69,40 +66,6 @@ struct SaCfg {
     static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
     static constexpr int kSmem = 1024 /*align*/ + kBody + kWarpFloats * 4;
 };
-
-// Eight keys of a tile in a group: the position of the first, and the tokens
-// (bits) that list their page.
-struct SaOctet {
-    int base;
-    uint32_t who;
-};
-
-// Where group w of R tokens stands: the groups of request r are w = qsl[r] / R
-// + r and the following (some of them empty). With whole warps.
-struct GroupPlace {
-    int r, t0, n, q1, len;  // n tokens from t0 on; 0: none
-};
-PKA_DEVICE GroupPlace group_of(const int32_t* qsl, const int32_t* seq_lens, int nreq, int w, int R) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = nreq;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) >> 5;
-        const int i = lo + lane * step;
-        const uint32_t at_most = __ballot_sync(0xffffffffu, i < hi && __ldg(qsl + i) / R + i <= w);
-        const int k = at_most ? 31 - __clz(at_most) : 0;
-        lo += k * step;
-        hi = min(hi, lo + step);
-    }
-    GroupPlace g;
-    g.r = lo;
-    const int q0 = __ldg(qsl + lo);
-    g.q1 = __ldg(qsl + lo + 1);
-    g.len = __ldg(seq_lens + lo);
-    const long long t0 = (long long)q0 + (long long)(w - (q0 / R + lo)) * R;
-    g.t0 = (int)t0;
-    g.n = t0 < q0 || t0 >= g.q1 ? 0 : min(R, g.q1 - g.t0);
-    return g;
-}
 
 // Row `row`, 16-byte chunk c of a tile of `tile` rows: 128-byte column segments of
 // all its rows one after another, each in the 128-byte swizzle.
@@ -132,149 +95,58 @@ PKA_DEVICE void split_e4m3(float a, float b, uint32_t& hi, uint32_t& lo) {
     lo = pair(a - back.x, b - back.y);
 }
 
-template <int D, int NT, bool kFp8, bool kGroup>
+template <int D, int NT, bool kFp8>
 __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sparse_attn_kernel(const SparseAttnParams p) {
     using C = SaCfg<D, NT, kFp8>;
     constexpr int kTile = C::kTile, kOctets = C::kOctets;
     constexpr int kMTiles = kTile / 16;  // of S^T: 16 keys each
     constexpr int kKSteps = D / 16;      // m-tiles of O^T (and k-steps of S^T over bf16)
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int s_stop[kSaGroup];
-    __shared__ uint32_t s_scan[kSaWarps], s_bad;
-    __shared__ SaOctet s_octet[kGroup ? kSaWarps : 1][C::kStages][kOctets];
+    __shared__ int s_stop;
     grid_dep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c4 = lane & 3, r8 = lane >> 2;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* own = reinterpret_cast<float*>(smem + C::kBody);  // this CTA's O [kCols][D], m, l
-    // a group's united list: page | tokens << 24
-    uint32_t* s_list = reinterpret_cast<uint32_t*>(smem + C::kSmem - 1024);
-    if (tid < kSaGroup) s_stop[tid] = p.num_pages;
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) s_stop = p.num_pages;
     __syncthreads();
     grid_dep_wait();
 
-    // ---- the tokens [t0, t0 + ntok), consecutive ones of one request
+    // ---- the token's request and position (the same for the whole cluster)
     const int ncta = (int)cluster_size(), cta = (int)cluster_rank();
-    const int g = blockIdx.y, unit = (int)(blockIdx.x / (unsigned)ncta);
-    int r, t0, ntok, q1, len;
-    if constexpr (kGroup) {
-        const GroupPlace at = group_of(p.qsl, p.seq_lens, p.num_reqs, unit, p.group);
-        r = at.r, t0 = at.t0, ntok = at.n, q1 = at.q1, len = at.len;
-        if (ntok <= 0 || t0 < 0 || t0 > p.num_tokens - ntok) return;  // no such group
-    } else {
-        const TokenPlace at = place_of(p.qsl, p.seq_lens, p.num_reqs, unit);
-        r = at.r, t0 = unit, ntok = 1, q1 = at.q1, len = at.len;
-        if (r < 0) return;  // a row behind the last sequence
-        if (t0 < at.q0) len = -1;
-    }
-    const long long pos = (long long)len - q1 + t0;  // the first token's position
-    if (pos < 0 || pos + ntok > len || len > p.max_seq_len) {
+    const int g = blockIdx.y, t0 = (int)(blockIdx.x / (unsigned)ncta);
+    const TokenPlace at = place_of(p.qsl, p.seq_lens, p.num_reqs, t0);
+    if (at.r < 0) return;  // a row behind the last sequence
+    const long long pos = (long long)at.len - at.q1 + t0;
+    if (t0 < at.q0 || pos < 0 || pos >= at.len || at.len > p.max_seq_len) {
         if (tid == 0 && cta == 0 && g == 0) set_error(p.err, PKA_DEVERR_SEQ_LEN);
         return;
     }
-    const int pos0 = (int)pos, pos1 = pos0 + ntok - 1;
-    const int64_t row0 = (int64_t)t0 * p.Hq + g * p.G;  // first output row of the first token
-    const int cols = ntok * p.G;
-    auto row_of = [&](int col) { return kGroup ? row0 + (int64_t)(col / p.G) * p.Hq + col % p.G : row0 + col; };
+    const int own_page = (int)pos >> p.bs_log2;
+    const int64_t row0 = (int64_t)t0 * p.Hq + g * p.G;  // first output row
 
-    // ---- the lists: each ends at its first negative entry; entries ascend and none is past the token's page
+    // ---- the list: it ends at its first negative entry; entries ascend and none is past the own page
     const int32_t* sel = p.sel + ((int64_t)t0 * p.Hkv + g) * p.num_pages;
-    const int64_t sel_step = (int64_t)p.Hkv * p.num_pages;  // from a token's list to the next one's
-    if constexpr (!kGroup) {
-        const int own_page = pos0 >> p.bs_log2;
-        for (int i = tid; i < p.num_pages; i += kSaThreads) {
-            const int e = __ldg(sel + i), before = i ? __ldg(sel + i - 1) : -1;
-            if (e <= before || e > own_page) {  // e < 0 among them
-                atomicMin(&s_stop[0], i);
-                break;
-            }
-        }
-    } else {
-        for (int i0 = tid; i0 < p.num_pages; i0 += kSaThreads) {
-            int e[kSaGroup], before[kSaGroup];
-#pragma unroll
-            for (int k = 0; k < kSaGroup; ++k) {
-                e[k] = k < ntok ? __ldg(sel + k * sel_step + i0) : 0;
-                before[k] = k < ntok && i0 ? __ldg(sel + k * sel_step + i0 - 1) : -1;
-            }
-#pragma unroll
-            for (int k = 0; k < kSaGroup; ++k)
-                if (k < ntok && (e[k] <= before[k] || e[k] > (pos0 + k) >> p.bs_log2)) atomicMin(&s_stop[k], i0);
+    for (int i = tid; i < p.num_pages; i += kSaThreads) {
+        const int e = __ldg(sel + i), before = i ? __ldg(sel + i - 1) : -1;
+        if (e <= before || e > own_page) {  // e < 0 among them
+            atomicMin(&s_stop, i);
+            break;
         }
     }
-    const int last_page = pos1 >> p.bs_log2;
-    const int words = last_page / 32 + 1;
-    uint32_t* s_map = reinterpret_cast<uint32_t*>(smem);  // (the ring is idle still) a bit map per token
-    if constexpr (kGroup)
-        for (int i = tid; i < ntok * words; i += kSaThreads) s_map[i] = 0;
     __syncthreads();
-    if (cta == 0 && tid < ntok && s_stop[tid] < p.num_pages && __ldg(sel + tid * sel_step + s_stop[tid]) >= 0)
-        set_error(p.err, PKA_DEVERR_INDEX);
-    int count = s_stop[0], last = -1;  // pages to read, and the last of them
-    if constexpr (kGroup) {
-        for (int i = tid; i < p.num_pages; i += kSaThreads) {
-            int e[kSaGroup];
-#pragma unroll
-            for (int k = 0; k < kSaGroup; ++k) e[k] = k < ntok && i < s_stop[k] ? __ldg(sel + k * sel_step + i) : -1;
-#pragma unroll
-            for (int k = 0; k < kSaGroup; ++k)
-                if (e[k] >= 0) atomicOr(&s_map[k * words + (e[k] >> 5)], 1u << (e[k] & 31));
-        }
-        __syncthreads();
-        const int per = (words + kSaThreads - 1) / kSaThreads;
-        const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
-        uint32_t mine = 0;
-        for (int w = w0; w < w1; ++w) {
-            uint32_t any = 0;
-            for (int k = 0; k < ntok; ++k) any |= s_map[k * words + w];
-            mine += __popc(any);
-        }
-        uint32_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 31) s_scan[warp] = incl;
-        __syncthreads();
-        uint32_t at = incl - mine;
-        count = 0;
-#pragma unroll
-        for (int w = 0; w < kSaWarps; ++w) {
-            at += w < warp ? s_scan[w] : 0u;
-            count += (int)s_scan[w];
-        }
-        for (int w = w0; w < w1; ++w) {
-            uint32_t any = 0, map[kSaGroup];
-#pragma unroll
-            for (int k = 0; k < kSaGroup; ++k) {
-                map[k] = k < ntok ? s_map[k * words + w] : 0u;
-                any |= map[k];
-            }
-            for (; any; any &= any - 1) {
-                const int bit = __ffs(any) - 1;
-                uint32_t who = 0;
-#pragma unroll
-                for (int k = 0; k < kSaGroup; ++k) who |= (map[k] >> bit & 1u) << k;
-                s_list[at++] = (uint32_t)(w * 32 + bit) | who << 24;
-            }
-        }
-        __syncthreads();  // (the ring is written by copies from here on)
-        if (count > 0) last = (int)(s_list[count - 1] & 0xffffffu);
-    } else {
-        if (count > 0) last = __ldg(sel + count - 1);
-    }
-    const int keys = count * p.bs - (last == last_page ? p.bs - 1 - (pos1 & (p.bs - 1)) : 0);
-    // tokens without a page: nothing to read
-    if (cta == 0)
-        for (int k = 0; k < ntok; ++k) {
-            if (s_stop[k] > 0) continue;
+    const int count = s_stop;
+    if (cta == 0 && tid == 0 && count < p.num_pages && __ldg(sel + count) >= 0) set_error(p.err, PKA_DEVERR_INDEX);
+    if (count == 0) {  // nothing to read
+        if (cta == 0) {
             for (int i = tid; i < p.G * D / 8; i += kSaThreads)
-                reinterpret_cast<uint4*>(p.out + (row0 + (int64_t)k * p.Hq) * D)[i] = make_uint4(0, 0, 0, 0);
-            if (p.lse && tid < p.G) p.lse[row0 + (int64_t)k * p.Hq + tid] = -INFINITY;
+                reinterpret_cast<uint4*>(p.out + row0 * D)[i] = make_uint4(0, 0, 0, 0);
+            if (p.lse && tid < p.G) p.lse[row0 + tid] = -INFINITY;
         }
-    if (keys == 0) return;
+        return;
+    }
+    const bool tail = __ldg(sel + count - 1) == own_page;
+    const int keys = count * p.bs - (tail ? p.bs - 1 - ((int)pos & (p.bs - 1)) : 0);
     const int ntiles = (keys + kTile - 1) / kTile;
     const int part = cta * kSaWarps + warp, parts = ncta * kSaWarps;
     // (parts is a power of two up to 64, ntiles below 2^31 / kTile)
@@ -292,23 +164,14 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
     for (int j = 0; j < kSteps; ++j) place[j] = seg_off<kTile>(j * kRows + lane / kPieces, lane % kPieces);
     uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
     int page0 = -32, rows = 0;  // lane l holds the first cache row of listed page page0 + l
-    uint32_t entry = 0;         // and, of a group, its entry
     auto issue = [&](int i, int stage) {
         const int first = (i * kTile) >> p.bs_log2;
-        if (first < page0 || (i * kTile + kTile - 1) >> p.bs_log2 >= page0 + 32) {
+        if ((i * kTile + kTile - 1) >> p.bs_log2 >= page0 + 32) {
             page0 = first;
             const int j = page0 + lane;
             int blk = 0;
-            entry = 0;
             if (j < count) {
-                int e;
-                if constexpr (kGroup) {
-                    entry = s_list[j];
-                    e = (int)(entry & 0xffffffu);
-                } else {
-                    e = __ldg(sel + j);
-                }
-                blk = __ldg(p.block_table + (int64_t)r * p.max_blocks + e);
+                blk = __ldg(p.block_table + (int64_t)at.r * p.max_blocks + __ldg(sel + j));
                 if (blk < 0 || blk >= p.num_blocks) {
                     set_error(p.err, PKA_DEVERR_BLOCK_ID);
                     blk = 0;
@@ -322,13 +185,6 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
             const int key = i * kTile + 8 * o, off = key & (p.bs - 1);
             const int from = ((key >> p.bs_log2) - page0) & 31;
             const int64_t src = (int64_t)(__shfl_sync(0xffffffffu, rows, from) + off) * C::kRowBytes;
-            if constexpr (kGroup) {
-                const uint32_t e = __shfl_sync(0xffffffffu, entry, from);
-                SaOctet x;
-                x.base = (int)(e & 0xffffffu) * p.bs + off;
-                x.who = key < keys ? e >> 24 : 0u;
-                if (lane == 0) s_octet[warp][stage][o] = x;
-            }
             if (key >= keys) continue;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
@@ -337,14 +193,11 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
             }
         }
     };
-    auto first_tiles = [&] {
 #pragma unroll
-        for (int s = 0; s < C::kStages; ++s) {
-            if (i0 + s < i1) issue(i0 + s, s);
-            cp_async_commit();  // (a group per tile, empty behind the last)
-        }
-    };
-    first_tiles();
+    for (int s = 0; s < C::kStages; ++s) {
+        if (i0 + s < i1) issue(i0 + s, s);
+        cp_async_commit();  // (a group per tile, empty behind the last)
+    }
 
     // ---- Q^T fragments: column n, zero behind the last. bf16: [k-step of 16 elements][2];
     // 8-bit: the first e4m3 numbers of [k-step of 32][2], then the second ones
@@ -353,8 +206,8 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int n = nt * 8 + r8;
-        const bool ok = n < cols;
-        const __nv_bfloat16* qrow = p.q + row_of(ok ? n : 0) * D;
+        const bool ok = n < p.G;
+        const __nv_bfloat16* qrow = p.q + (row0 + (ok ? n : 0)) * D;
         if constexpr (kFp8) {  // k-step s of this lane: elements 32 c4 + 8 s .. + 7, as the codes are read
             float x[32];
             float a = 0.f;
@@ -400,343 +253,299 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
             factor[nt][0] = factor[nt][1] = p.scale_log2;
         }
     }
-    // a group: this lane's columns' token bit and position (a column behind the last: none)
-    uint32_t bit[kGroup ? NT : 1][2];
-    int limit[kGroup ? NT : 1][2];
-    if constexpr (kGroup) {
+    float o[kKSteps][NT][4];
+    float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-            for (int hc = 0; hc < 2; ++hc) {
-                const int n = nt * 8 + c4 * 2 + hc, k = n / p.G;
-                bit[nt][hc] = n < cols ? 1u << k : 0u;
-                limit[nt][hc] = pos0 + k;
-            }
+        for (int mt = 0; mt < kKSteps; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
     }
-
-    // ---- one pass over the tiles; a group with values that are not finite takes one more per token
-    for (int pass = 0;; ++pass) {
-        const uint32_t who = pass == 0 ? (1u << ntok) - 1 : 1u << (pass - 1);  // the tokens of this pass
-        const int end = pass == 0 ? pos1 : pos0 + pass - 1;                    // the last one's position
-        if (pass > 0) first_tiles();
-        float o[kKSteps][NT][4];
-        float m[NT][2], l[NT][2];
+    int stage = 0;
+    for (int i = i0; i < i1; ++i) {
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();
+        uint8_t* kt = ring + stage * C::kStageBytes;
+        uint8_t* vt = kt + C::kTileBytes;
+        // valid keys of each octet; the others' values may be anything: zeros instead
+        int valid[kOctets];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.f;
+        for (int q = 0; q < kOctets; ++q) valid[q] = min(8, max(0, keys - i * kTile - 8 * q));
+        if (valid[kOctets - 1] < 8) {
 #pragma unroll
-            for (int mt = 0; mt < kKSteps; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-        }
-        int stage = 0;
-        for (int i = i0; i < i1; ++i) {
-            cp_async_wait<C::kStages - 1>();
+            for (int q = 0; q < kOctets; ++q)
+                for (int ci = valid[q] * kPieces + lane; ci < 8 * kPieces; ci += 32)
+                    *reinterpret_cast<uint4*>(vt + q * 1024 + seg_off<kTile>(ci / kPieces, ci % kPieces)) =
+                        make_uint4(0, 0, 0, 0);
             __syncwarp();
-            uint8_t* kt = ring + stage * C::kStageBytes;
-            uint8_t* vt = kt + C::kTileBytes;
-            // valid keys of each octet; the others' values may be anything: zeros instead
-            int valid[kOctets], all_valid = 0;
-            SaOctet oct[kOctets];
-#pragma unroll
-            for (int q = 0; q < kOctets; ++q) {
-                if constexpr (kGroup) {
-                    oct[q] = s_octet[warp][stage][q];
-                    valid[q] = oct[q].who & who ? min(8, max(0, end + 1 - oct[q].base)) : 0;
-                } else {
-                    valid[q] = min(8, max(0, keys - i * kTile - 8 * q));
-                }
-                all_valid += valid[q];
-            }
-            if (all_valid < kTile) {
-#pragma unroll
-                for (int q = 0; q < kOctets; ++q)
-                    for (int ci = valid[q] * kPieces + lane; ci < 8 * kPieces; ci += 32)
-                        *reinterpret_cast<uint4*>(vt + q * 1024 + seg_off<kTile>(ci / kPieces, ci % kPieces)) =
-                            make_uint4(0, 0, 0, 0);
-                __syncwarp();
-            }
-            const uint32_t kb = smem_u32(kt), vb = smem_u32(vt);
+        }
+        const uint32_t kb = smem_u32(kt), vb = smem_u32(vt);
 
-            // ---- S^T = K Q^T: rows r8 (octet 2 t) and r8 + 8 (octet 2 t + 1) of m-tile t
-            float sc[kMTiles][NT][4];
+        // ---- S^T = K Q^T: rows r8 (octet 2 t) and r8 + 8 (octet 2 t + 1) of m-tile t
+        float sc[kMTiles][NT][4];
+#pragma unroll
+        for (int t = 0; t < kMTiles; ++t)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) sc[t][nt][0] = sc[t][nt][1] = sc[t][nt][2] = sc[t][nt][3] = 0.f;
+        if constexpr (kFp8) {
 #pragma unroll
             for (int t = 0; t < kMTiles; ++t)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sc[t][nt][0] = sc[t][nt][1] = sc[t][nt][2] = sc[t][nt][3] = 0.f;
-            if constexpr (kFp8) {
-#pragma unroll
-                for (int t = 0; t < kMTiles; ++t)
-#pragma unroll
-                    for (int jc = 0; jc < 2; ++jc) {
-                        const uint4 a = lds128(kb + t * 2048 + sw128(r8, 2 * c4 + jc));
-                        const uint4 b = lds128(kb + t * 2048 + sw128(r8 + 8, 2 * c4 + jc));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int part2 = 0; part2 < 2; ++part2) {
-                                const uint32_t(&f0)[2] = qf[nt][4 * part2 + 2 * jc];
-                                const uint32_t(&f1)[2] = qf[nt][4 * part2 + 2 * jc + 1];
-                                mma_e4m3(sc[t][nt], a.x, b.x, a.y, b.y, f0[0], f0[1]);
-                                mma_e4m3(sc[t][nt], a.z, b.z, a.w, b.w, f1[0], f1[1]);
-                            }
-                    }
-            } else {
-                const int mi = lane >> 3, tr = (mi & 1) * 8 + (lane & 7);
-#pragma unroll
-                for (int ks = 0; ks < kKSteps; ++ks) {
-                    uint32_t a0, a1, a2, a3;
-                    ldsm_x4(kb + seg_off<kTile>(tr, ks * 2 + (mi >> 1)), a0, a1, a2, a3);
+                for (int jc = 0; jc < 2; ++jc) {
+                    const uint4 a = lds128(kb + t * 2048 + sw128(r8, 2 * c4 + jc));
+                    const uint4 b = lds128(kb + t * 2048 + sw128(r8 + 8, 2 * c4 + jc));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma_bf16(sc[0][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+#pragma unroll
+                        for (int part2 = 0; part2 < 2; ++part2) {
+                            const uint32_t(&f0)[2] = qf[nt][4 * part2 + 2 * jc];
+                            const uint32_t(&f1)[2] = qf[nt][4 * part2 + 2 * jc + 1];
+                            mma_e4m3(sc[t][nt], a.x, b.x, a.y, b.y, f0[0], f0[1]);
+                            mma_e4m3(sc[t][nt], a.z, b.z, a.w, b.w, f1[0], f1[1]);
+                        }
                 }
+        } else {
+            const int mi = lane >> 3, tr = (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int ks = 0; ks < kKSteps; ++ks) {
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4(kb + seg_off<kTile>(tr, ks * 2 + (mi >> 1)), a0, a1, a2, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_bf16(sc[0][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
             }
-            // ---- online softmax in the log2 domain; other keys weigh nothing
-            uint32_t pb[kFp8 ? 2 : 1][NT][2];  // P^T fragments (8-bit: of the first numbers, of the second)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float pr[kOctets][2];
-                float alpha[2];
-#pragma unroll
-                for (int hc = 0; hc < 2; ++hc) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int q = 0; q < kOctets; ++q) {
-                        bool in = r8 < valid[q];
-                        if constexpr (kGroup) in = (oct[q].who & bit[nt][hc] & who) && oct[q].base + r8 <= limit[nt][hc];
-                        pr[q][hc] = in ? sc[q / 2][nt][q % 2 * 2 + hc] * factor[nt][hc] : -INFINITY;
-                        mx = fmaxf(mx, pr[q][hc]);
-                    }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float mn = fmaxf(m[nt][hc], mx);
-                    const float sub = mn == -INFINITY ? 0.f : mn;  // scores of -inf alone so far: weights 0
-                    alpha[hc] = fast_exp2(m[nt][hc] - sub);
-                    m[nt][hc] = mn;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int q = 0; q < kOctets; ++q) {
-                        pr[q][hc] = fast_exp2(pr[q][hc] - (kFp8 ? sub - 8.f : sub));  // 8-bit: in units of 2^-8
-                        sum += pr[q][hc];
-                    }
-                    l[nt][hc] = l[nt][hc] * alpha[hc] + sum;
-                }
-                if (alpha[0] != 1.f || alpha[1] != 1.f) {
-#pragma unroll
-                    for (int mt = 0; mt < kKSteps; ++mt) {
-                        o[mt][nt][0] *= alpha[0];
-                        o[mt][nt][1] *= alpha[1];
-                        o[mt][nt][2] *= alpha[0];
-                        o[mt][nt][3] *= alpha[1];
-                    }
-                }
-                if constexpr (kFp8) {
-                    // a 16-bit element of the transposed matrix is two keys, r8 of an octet and of the next
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        uint32_t h0, l0, h1, l1;
-                        split_e4m3(pr[2 * t][0], pr[2 * t + 1][0], h0, l0);
-                        split_e4m3(pr[2 * t][1], pr[2 * t + 1][1], h1, l1);
-                        pb[0][nt][t] = movmatrix_t(h0 | h1 << 16);
-                        pb[kFp8][nt][t] = movmatrix_t(l0 | l1 << 16);
-                    }
-                } else {
-                    pb[0][nt][0] = movmatrix_t(pack_bf16(pr[0][0], pr[0][1]));  // keys 0-7
-                    pb[0][nt][1] = movmatrix_t(pack_bf16(pr[1][0], pr[1][1]));  // keys 8-15
-                }
-            }
-            // ---- O^T += V^T P^T
-            if constexpr (kFp8) {
-                // k-slots 4 c4 ..: keys 2c, 2c + 8, 2c + 1, 2c + 9, and 16 on; elements 16 r8 .. + 15 of
-                // each, 4 x 4 bytes transposed: rows of m-tile 2 pp + j are elements 16 r8 + 4 pp + 2 j, + 1
-                uint32_t w[8][4];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint4 v = lds128(vb + sw128((k / 4) * 16 + 2 * c4 + (k & 1) * 8 + (k >> 1 & 1), r8));
-                    w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
-                }
-#pragma unroll
-                for (int pp = 0; pp < 4; ++pp) {
-                    uint32_t f[2][4];
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint32_t x0 = __byte_perm(w[4 * t][pp], w[4 * t + 1][pp], 0x5140);
-                        const uint32_t x1 = __byte_perm(w[4 * t + 2][pp], w[4 * t + 3][pp], 0x5140);
-                        const uint32_t y0 = __byte_perm(w[4 * t][pp], w[4 * t + 1][pp], 0x7362);
-                        const uint32_t y1 = __byte_perm(w[4 * t + 2][pp], w[4 * t + 3][pp], 0x7362);
-                        f[t][0] = __byte_perm(x0, x1, 0x5410);
-                        f[t][1] = __byte_perm(x0, x1, 0x7632);
-                        f[t][2] = __byte_perm(y0, y1, 0x5410);
-                        f[t][3] = __byte_perm(y0, y1, 0x7632);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int part2 = 0; part2 < 2; ++part2)
-                                mma_e4m3(o[2 * pp + j][nt], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
-                                         pb[kFp8 ? part2 : 0][nt][0], pb[kFp8 ? part2 : 0][nt][1]);
-                }
-            } else {
-                const int mi = lane >> 3, tr = (mi >> 1) * 8 + (lane & 7);
-#pragma unroll
-                for (int mt = 0; mt < kKSteps; ++mt) {
-                    uint32_t a0, a1, a2, a3;
-                    ldsm_x4_t(vb + seg_off<kTile>(tr, mt * 2 + (mi & 1)), a0, a1, a2, a3);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_bf16(o[mt][nt], a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
-                }
-            }
-            __syncwarp();
-            if (i + C::kStages < i1) issue(i + C::kStages, stage);
-            cp_async_commit();
-            stage = stage + 1 == C::kStages ? 0 : stage + 1;
         }
-        cp_async_wait<0>();
-
-        // ---- the warps' results, then the CTAs', join by their maxima
-        __syncthreads();  // the ring is idle
-        float* mine = reinterpret_cast<float*>(smem) + warp * C::kWarpFloats;
+        // ---- online softmax in the log2 domain; other keys weigh nothing
+        uint32_t pb[kFp8 ? 2 : 1][NT][2];  // P^T fragments (8-bit: of the first numbers, of the second)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            float pr[kOctets][2];
+            float alpha[2];
 #pragma unroll
             for (int hc = 0; hc < 2; ++hc) {
-                float lt = l[nt][hc];
-                lt += __shfl_xor_sync(0xffffffffu, lt, 4);
-                lt += __shfl_xor_sync(0xffffffffu, lt, 8);
-                lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-                const int hh = nt * 8 + c4 * 2 + hc;
-                if (lane < 4) {
-                    mine[C::kCols * D + hh] = m[nt][hc];
-                    mine[C::kCols * (D + 1) + hh] = lt;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < kOctets; ++q) {
+                    pr[q][hc] = r8 < valid[q] ? sc[q / 2][nt][q % 2 * 2 + hc] * factor[nt][hc] : -INFINITY;
+                    mx = fmaxf(mx, pr[q][hc]);
                 }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float mn = fmaxf(m[nt][hc], mx);
+                const float sub = mn == -INFINITY ? 0.f : mn;  // scores of -inf alone so far: weights 0
+                alpha[hc] = fast_exp2(m[nt][hc] - sub);
+                m[nt][hc] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int q = 0; q < kOctets; ++q) {
+                    pr[q][hc] = fast_exp2(pr[q][hc] - (kFp8 ? sub - 8.f : sub));  // 8-bit: in units of 2^-8
+                    sum += pr[q][hc];
+                }
+                l[nt][hc] = l[nt][hc] * alpha[hc] + sum;
+            }
+            if (alpha[0] != 1.f || alpha[1] != 1.f) {
 #pragma unroll
                 for (int mt = 0; mt < kKSteps; ++mt) {
-                    // rows of O^T: elements 16 mt + r8 and + 8; over 8-bit tiles 16 r8 + 2 mt and + 1
-                    const int d0 = kFp8 ? 16 * r8 + 2 * mt : 16 * mt + r8;
-                    mine[hh * D + d0] = o[mt][nt][hc];
-                    mine[hh * D + d0 + (kFp8 ? 1 : 8)] = o[mt][nt][hc + 2];
+                    o[mt][nt][0] *= alpha[0];
+                    o[mt][nt][1] *= alpha[1];
+                    o[mt][nt][2] *= alpha[0];
+                    o[mt][nt][3] *= alpha[1];
                 }
             }
-        __syncthreads();
-        auto weight = [](float mw, float M) { return mw == -INFINITY ? 0.f : fast_exp2(mw - M); };
-        const float* all = reinterpret_cast<const float*>(smem);
-        for (int it = tid; it < cols * (D / 4); it += kSaThreads) {
-            const int hh = it / (D / 4), c = it % (D / 4) * 4;
-            float M = -INFINITY, L = 0.f;
+            if constexpr (kFp8) {
+                // a 16-bit element of the transposed matrix is two keys, r8 of an octet and of the next
 #pragma unroll
-            for (int w = 0; w < kSaWarps; ++w) M = fmaxf(M, all[w * C::kWarpFloats + C::kCols * D + hh]);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kSaWarps; ++w) {
-                const float* x = all + w * C::kWarpFloats;
-                const float wt = weight(x[C::kCols * D + hh], M);
-                const float4 v = *reinterpret_cast<const float4*>(x + hh * D + c);
-                L += wt * x[C::kCols * (D + 1) + hh];
-                acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
-            }
-            *reinterpret_cast<float4*>(own + hh * D + c) = acc;
-            if (c == 0) {
-                own[C::kCols * D + hh] = M;
-                own[C::kCols * (D + 1) + hh] = L;
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t h0, l0, h1, l1;
+                    split_e4m3(pr[2 * t][0], pr[2 * t + 1][0], h0, l0);
+                    split_e4m3(pr[2 * t][1], pr[2 * t + 1][1], h1, l1);
+                    pb[0][nt][t] = movmatrix_t(h0 | h1 << 16);
+                    pb[kFp8][nt][t] = movmatrix_t(l0 | l1 << 16);
+                }
+            } else {
+                pb[0][nt][0] = movmatrix_t(pack_bf16(pr[0][0], pr[0][1]));  // keys 0-7
+                pb[0][nt][1] = movmatrix_t(pack_bf16(pr[1][0], pr[1][1]));  // keys 8-15
             }
         }
-        if (ncta == 1) __syncthreads();
-        else cluster_barrier();
-        bool bad = false;
-        for (int it = cta * kSaThreads + tid; it < cols * (D / 4); it += ncta * kSaThreads) {
-            const int hh = it / (D / 4), c = it % (D / 4) * 4;
-            if (kGroup && !(who >> (hh / p.G) & 1 && s_stop[hh / p.G] > 0)) continue;
-            // up to kSaJoin CTAs' parts in flight together
-            float M = -INFINITY, L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k0 = 0; k0 < ncta; k0 += kSaJoin) {
-                float mk[kSaJoin], lk[kSaJoin];
-                float4 vk[kSaJoin];
+        // ---- O^T += V^T P^T
+        if constexpr (kFp8) {
+            // k-slots 4 c4 ..: keys 2c, 2c + 8, 2c + 1, 2c + 9, and 16 on; elements 16 r8 .. + 15 of
+            // each, 4 x 4 bytes transposed: rows of m-tile 2 pp + j are elements 16 r8 + 4 pp + 2 j, + 1
+            uint32_t w[8][4];
 #pragma unroll
-                for (int j = 0; j < kSaJoin; ++j) {
-                    if (k0 + j >= ncta) continue;
-                    mk[j] = load_cluster(own + C::kCols * D + hh, k0 + j);
-                    lk[j] = load_cluster(own + C::kCols * (D + 1) + hh, k0 + j);
-                    vk[j] = load_cluster4(own + hh * D + c, k0 + j);
-                }
-                float Mn = M;
-#pragma unroll
-                for (int j = 0; j < kSaJoin; ++j)
-                    if (k0 + j < ncta) Mn = fmaxf(Mn, mk[j]);
-                const float keep = weight(M, Mn);
-                M = Mn;
-                L *= keep, acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
-#pragma unroll
-                for (int j = 0; j < kSaJoin; ++j) {
-                    if (k0 + j >= ncta) continue;
-                    const float wt = weight(mk[j], M);
-                    L += wt * lk[j];
-                    acc.x += wt * vk[j].x, acc.y += wt * vk[j].y, acc.z += wt * vk[j].z, acc.w += wt * vk[j].w;
-                }
+            for (int k = 0; k < 8; ++k) {
+                const uint4 v = lds128(vb + sw128((k / 4) * 16 + 2 * c4 + (k & 1) * 8 + (k >> 1 & 1), r8));
+                w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
             }
-            const float inv = p.v_scale / L;
-            const int64_t row = row_of(hh);
-            if (kGroup) bad |= !(fabsf(acc.x) + fabsf(acc.y) + fabsf(acc.z) + fabsf(acc.w) <= 3.4e38f);
-            *reinterpret_cast<uint2*>(p.out + row * D + c) =
-                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-            // (8-bit: weights were in units of 2^-8)
-            if (p.lse && c == 0) p.lse[row] = (M + __log2f(L) - (kFp8 ? 8.f : 0.f)) * 0.69314718055994531f;
-        }
-        if (kGroup && pass == 0 && bad)
-            for (int k = 0; k < ncta; ++k) store_cluster(&s_bad, k, 1u);
-        // no CTA goes on (or leaves) while another reads its shared memory
-        if (ncta == 1) {
-            if (!kGroup) return;
-            __syncthreads();
+#pragma unroll
+            for (int pp = 0; pp < 4; ++pp) {
+                uint32_t f[2][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t x0 = __byte_perm(w[4 * t][pp], w[4 * t + 1][pp], 0x5140);
+                    const uint32_t x1 = __byte_perm(w[4 * t + 2][pp], w[4 * t + 3][pp], 0x5140);
+                    const uint32_t y0 = __byte_perm(w[4 * t][pp], w[4 * t + 1][pp], 0x7362);
+                    const uint32_t y1 = __byte_perm(w[4 * t + 2][pp], w[4 * t + 3][pp], 0x7362);
+                    f[t][0] = __byte_perm(x0, x1, 0x5410);
+                    f[t][1] = __byte_perm(x0, x1, 0x7632);
+                    f[t][2] = __byte_perm(y0, y1, 0x5410);
+                    f[t][3] = __byte_perm(y0, y1, 0x7632);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int part2 = 0; part2 < 2; ++part2)
+                            mma_e4m3(o[2 * pp + j][nt], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
+                                     pb[kFp8 ? part2 : 0][nt][0], pb[kFp8 ? part2 : 0][nt][1]);
+            }
         } else {
-            cluster_barrier();
+            const int mi = lane >> 3, tr = (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int mt = 0; mt < kKSteps; ++mt) {
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4_t(vb + seg_off<kTile>(tr, mt * 2 + (mi & 1)), a0, a1, a2, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_bf16(o[mt][nt], a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
+            }
         }
-        if (!kGroup || ntok == 1 || s_bad == 0 || pass == ntok) return;
+        __syncwarp();
+        if (i + C::kStages < i1) issue(i + C::kStages, stage);
+        cp_async_commit();
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
+    cp_async_wait<0>();
+
+    // ---- the warps' results, then the CTAs', join by their maxima
+    __syncthreads();  // the ring is idle
+    float* mine = reinterpret_cast<float*>(smem) + warp * C::kWarpFloats;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int hc = 0; hc < 2; ++hc) {
+            float lt = l[nt][hc];
+            lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+            lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+            lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+            const int hh = nt * 8 + c4 * 2 + hc;
+            if (lane < 4) {
+                mine[C::kCols * D + hh] = m[nt][hc];
+                mine[C::kCols * (D + 1) + hh] = lt;
+            }
+#pragma unroll
+            for (int mt = 0; mt < kKSteps; ++mt) {
+                // rows of O^T: elements 16 mt + r8 and + 8; over 8-bit tiles 16 r8 + 2 mt and + 1
+                const int d0 = kFp8 ? 16 * r8 + 2 * mt : 16 * mt + r8;
+                mine[hh * D + d0] = o[mt][nt][hc];
+                mine[hh * D + d0 + (kFp8 ? 1 : 8)] = o[mt][nt][hc + 2];
+            }
+        }
+    __syncthreads();
+    auto weight = [](float mw, float M) { return mw == -INFINITY ? 0.f : fast_exp2(mw - M); };
+    const float* all = reinterpret_cast<const float*>(smem);
+    for (int it = tid; it < p.G * (D / 4); it += kSaThreads) {
+        const int hh = it / (D / 4), c = it % (D / 4) * 4;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSaWarps; ++w) M = fmaxf(M, all[w * C::kWarpFloats + C::kCols * D + hh]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kSaWarps; ++w) {
+            const float* x = all + w * C::kWarpFloats;
+            const float wt = weight(x[C::kCols * D + hh], M);
+            const float4 v = *reinterpret_cast<const float4*>(x + hh * D + c);
+            L += wt * x[C::kCols * (D + 1) + hh];
+            acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
+        }
+        *reinterpret_cast<float4*>(own + hh * D + c) = acc;
+        if (c == 0) {
+            own[C::kCols * D + hh] = M;
+            own[C::kCols * (D + 1) + hh] = L;
+        }
+    }
+    if (ncta == 1) __syncthreads();
+    else cluster_barrier();
+    for (int it = cta * kSaThreads + tid; it < p.G * (D / 4); it += ncta * kSaThreads) {
+        const int hh = it / (D / 4), c = it % (D / 4) * 4;
+        // up to kSaJoin CTAs' parts in flight together
+        float M = -INFINITY, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < ncta; k0 += kSaJoin) {
+            float mk[kSaJoin], lk[kSaJoin];
+            float4 vk[kSaJoin];
+#pragma unroll
+            for (int j = 0; j < kSaJoin; ++j) {
+                if (k0 + j >= ncta) continue;
+                mk[j] = load_cluster(own + C::kCols * D + hh, k0 + j);
+                lk[j] = load_cluster(own + C::kCols * (D + 1) + hh, k0 + j);
+                vk[j] = load_cluster4(own + hh * D + c, k0 + j);
+            }
+            float Mn = M;
+#pragma unroll
+            for (int j = 0; j < kSaJoin; ++j)
+                if (k0 + j < ncta) Mn = fmaxf(Mn, mk[j]);
+            const float keep = weight(M, Mn);
+            M = Mn;
+            L *= keep, acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+            for (int j = 0; j < kSaJoin; ++j) {
+                if (k0 + j >= ncta) continue;
+                const float wt = weight(mk[j], M);
+                L += wt * lk[j];
+                acc.x += wt * vk[j].x, acc.y += wt * vk[j].y, acc.z += wt * vk[j].z, acc.w += wt * vk[j].w;
+            }
+        }
+        const float inv = p.v_scale / L;
+        const int64_t row = row0 + hh;
+        *reinterpret_cast<uint2*>(p.out + row * D + c) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        // (8-bit: weights were in units of 2^-8)
+        if (p.lse && c == 0) p.lse[row] = (M + __log2f(L) - (kFp8 ? 8.f : 0.f)) * 0.69314718055994531f;
+    }
+    if (ncta > 1) cluster_barrier();  // no CTA leaves while another reads its shared memory
 }
 
-template <int D, int NT, bool kFp8, bool kGroup>
+template <int D, int NT, bool kFp8>
 cudaError_t go(const SparseAttnParams& p, int num_sms, cudaStream_t stream) {
     using C = SaCfg<D, NT, kFp8>;
-    if (p.group * p.G > C::kCols) return cudaErrorInvalidValue;  // (the columns of a group's tokens)
-    auto kern = sparse_attn_kernel<D, NT, kFp8, kGroup>;
-    const int smem = C::kSmem + (kGroup ? 4 * p.list_cap : 0);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto kern = sparse_attn_kernel<D, NT, kFp8>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t groups = kGroup ? (int64_t)p.num_tokens / p.group + p.num_reqs : p.num_tokens;
-    const int64_t units = groups * p.Hkv;
-    const int tiles = (int)std::min<int64_t>(((int64_t)p.num_pages * p.bs + C::kTile - 1) / C::kTile, 1 << 30);
+    // CTAs per (token, kv head): more of them shorten each one's run of tiles but
+    // each costs a start of about kStart tiles; up to the resident CTAs they all
+    // run at once, beyond that in turns, with half a turn's idling at the end.
+    // Measured at 384 units: bf16, 64 tiles per warp, with 1 / 2 / 4 / 8 CTAs
+    // 133 / 120 / 132 / 147 us; 8-bit, 16 tiles per warp, 1 / 2 / 4 CTAs 36 / 40 / 49
+    // us; one request's 8 units, bf16, 1 / 2 / 4 / 8 / 16 CTAs 40 / 23 / 14 / 9.9 /
+    // 10.2 us.
+    constexpr int64_t kStart = 5;
+    const int64_t units = (int64_t)p.num_tokens * p.Hkv, slots = (int64_t)num_sms * C::kMinBlocks;
+    const int64_t tiles = ((int64_t)p.num_pages * p.bs + C::kTile * kSaWarps - 1) / (C::kTile * kSaWarps);
     int n = 1;
-    while (n < 8 && units * n < (int64_t)num_sms * 4 && tiles >= n * kSaWarps * 4) n *= 2;
-    return launch_cluster(kern, dim3((unsigned)(n * groups), p.Hkv), dim3(kSaThreads), smem, n, stream, p);
-}
-
-template <int D, bool kFp8>
-cudaError_t by_columns(const SparseAttnParams& p, int num_sms, cudaStream_t stream) {
-    const bool two = p.group * p.G > 8;
-    if (p.group == 1) return two ? go<D, 2, kFp8, false>(p, num_sms, stream) : go<D, 1, kFp8, false>(p, num_sms, stream);
-    return two ? go<D, 2, kFp8, true>(p, num_sms, stream) : go<D, 1, kFp8, true>(p, num_sms, stream);
+    int64_t best = 0;
+    for (int c = 1; c <= 8; c *= 2) {
+        const int64_t turns = units * c <= slots ? 2 * slots : 2 * units * c + slots;
+        const int64_t cost = turns * (kStart + (tiles + c - 1) / c);
+        if (c == 1 || cost < best) {
+            best = cost;
+            n = c;
+        }
+    }
+    return launch_cluster(kern, dim3((unsigned)n * (unsigned)p.num_tokens, p.Hkv), dim3(kSaThreads), C::kSmem, n, stream,
+                          p);
 }
 
 }  // namespace
 
-cudaError_t launch_sparse_attn(SparseAttnParams p, int head_dim, bool fp8, int num_sms, cudaStream_t stream) {
-    // Tokens of one request taken together: about as many as a request has on
-    // average, at most kSaGroup and 16 columns; where that leaves fewer groups
-    // than tokens (some groups are empty), and the bit maps and lists fit.
-    int group = 1;
-    while (group < kSaGroup && group * p.num_reqs < p.num_tokens && 2 * group * p.G <= 16) group *= 2;
-    const int64_t pages = ((int64_t)p.max_seq_len + p.bs - 1) / p.bs;
-    const int64_t cap = std::min<int64_t>((int64_t)group * p.num_pages, pages);
-    if (p.num_tokens / group + p.num_reqs >= p.num_tokens || pages > 32 * 1024 || cap > 4096) group = 1;
-    p.group = group;
-    p.list_cap = (int)cap;
-    if (fp8) return by_columns<128, true>(p, num_sms, stream);
-    return head_dim == 128 ? by_columns<128, false>(p, num_sms, stream) : by_columns<64, false>(p, num_sms, stream);
+cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, bool fp8, int num_sms, cudaStream_t stream) {
+    const bool two = p.G > 8;
+    if (fp8) return two ? go<128, 2, true>(p, num_sms, stream) : go<128, 1, true>(p, num_sms, stream);
+    if (head_dim == 128) return two ? go<128, 2, false>(p, num_sms, stream) : go<128, 1, false>(p, num_sms, stream);
+    return two ? go<64, 2, false>(p, num_sms, stream) : go<64, 1, false>(p, num_sms, stream);
 }
 
 }  // namespace pka
