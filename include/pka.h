@@ -630,7 +630,8 @@ PKA_API pka_status pka_select_pages(const void *q, const int8_t *bounds, const f
  *
  *   q, out         device bf16 [num_tokens, Hq, d];  lse device float32 [num_tokens, Hq], or NULL
  *   k_cache, v_cache  device [num_blocks, Hkv, block_size, d] bf16; _fp8: E4M3 codes with
- *                  k_scale and v_scale (finite, > 0), q as in pka_paged_attn_forward_fp8
+ *                  k_scale and v_scale (finite, > 0); q of any finite magnitude (elements below
+ *                  2^-22 of their head's largest are rounded)
  *   block_table, query_start_loc, seq_lens, max_seq_len  as in pka_select_pages (rows behind
  *                  the last request are left as they are)
  *   selected       device int32 [num_tokens, Hkv, num_pages]

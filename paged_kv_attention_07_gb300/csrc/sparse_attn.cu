@@ -30,14 +30,15 @@
 //   S^T[keys x 8 columns] = K Q^T;  online softmax per column;  O^T += V^T P^T
 // bf16: P is rounded to bf16 for the product (its sum l is not): the error is
 // that of the operands' own type.
-// 8-bit: the codes are the MMAs' e4m3 operands as they are, and q and P are each
-// the sum of two e4m3 numbers, x = RN(x) + RN(x - RN(x)), in units of a power of
-// two per query head (the largest |q| is 128 to 256 units) and of 2^-8 for P.
-// For q that is exact down to 2^-10 of the head's largest element (bf16 has 8
-// bits, the two numbers 4 and 4) and off by at most 2^-18 of it below; P is off
-// by 2^-9 of itself or 2^-18 of the largest weight. Widening the codes to f16
-// instead takes three times the instructions (two conversions and two
-// permutations per four codes), which bound the kernel then.
+// 8-bit: the codes are widened to f16 (exact) in registers, P is f16, and q is f16
+// in units of a power of two per query head (its largest element is 128 to 256
+// units: bf16's bits are kept down to 2^-22 of it). (The codes as e4m3 operands,
+// with q and P as two e4m3 numbers each, need no conversions but twice the
+// products: 24 x 4 tokens 36 us, 27 us this way.)
+//
+// Measured: 96 requests, 4 kv heads, 64 pages of 64 tokens each, bf16: 120 us, 6.66
+// TB/s; 8-bit: 68 us, 5.93 TB/s. One request of 8 kv heads, bf16: 9.6 us, of
+// which 5 are the chain place -> list -> block table -> tile and the join.
 #include "common.cuh"
 #include "params.cuh"
 
@@ -74,25 +75,11 @@ PKA_DEVICE uint32_t seg_off(int row, int c) {
     return sw128((uint32_t)((c >> 3) * kTile + row), (uint32_t)(c & 7));
 }
 
-// D(16x8 f32) += A(16x32 e4m3, row) * B(32x8 e4m3, col)
-PKA_DEVICE void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// x = hi + lo, two e4m3 numbers each, as code pairs (a in the low byte).
-PKA_DEVICE void split_e4m3(float a, float b, uint32_t& hi, uint32_t& lo) {
-    auto pair = [](float x, float y) {
-        uint32_t d;
-        asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(d) : "f"(x), "f"(y));
-        return d;
-    };
-    hi = pair(a, b);
-    const float2 back = __half22float2(h2(e4m3x2_to_f16x2(hi)));
-    lo = pair(a - back.x, b - back.y);
+// Four E4M3 codes to two f16 pairs (exact).
+PKA_DEVICE void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 template <int D, int NT, bool kFp8>
@@ -232,15 +219,10 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = fabsf(x[j]) <= 3.4e38f ? x[j] * unit : __int_as_float(0x7fffffff);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t h0, l0, h1, l1;
-                    split_e4m3(x[8 * s + 4 * b], x[8 * s + 4 * b + 1], h0, l0);
-                    split_e4m3(x[8 * s + 4 * b + 2], x[8 * s + 4 * b + 3], h1, l1);
-                    qf[nt][s][b] = h0 | h1 << 16;
-                    qf[nt][4 + s][b] = l0 | l1 << 16;
-                }
+            for (int ks = 0; ks < 8; ++ks) {
+                qf[nt][ks][0] = pack_f16(x[4 * ks], x[4 * ks + 1]);
+                qf[nt][ks][1] = pack_f16(x[4 * ks + 2], x[4 * ks + 3]);
+            }
             const float f = p.scale_log2 * exp2i(e);
 #pragma unroll
             for (int hc = 0; hc < 2; ++hc) factor[nt][hc] = __shfl_sync(0xffffffffu, f, (c4 * 2 + hc) * 4);
@@ -290,22 +272,25 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
             for (int nt = 0; nt < NT; ++nt) sc[t][nt][0] = sc[t][nt][1] = sc[t][nt][2] = sc[t][nt][3] = 0.f;
         if constexpr (kFp8) {
 #pragma unroll
-            for (int t = 0; t < kMTiles; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int jc = 0; jc < 2; ++jc) {
                     const uint4 a = lds128(kb + t * 2048 + sw128(r8, 2 * c4 + jc));
                     const uint4 b = lds128(kb + t * 2048 + sw128(r8 + 8, 2 * c4 + jc));
+                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t a0, a1, a2, a3;
+                        widen4(aw[k], a0, a2);
+                        widen4(bw[k], a1, a3);
 #pragma unroll
-                        for (int part2 = 0; part2 < 2; ++part2) {
-                            const uint32_t(&f0)[2] = qf[nt][4 * part2 + 2 * jc];
-                            const uint32_t(&f1)[2] = qf[nt][4 * part2 + 2 * jc + 1];
-                            mma_e4m3(sc[t][nt], a.x, b.x, a.y, b.y, f0[0], f0[1]);
-                            mma_e4m3(sc[t][nt], a.z, b.z, a.w, b.w, f1[0], f1[1]);
-                        }
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(sc[t][nt], a0, a1, a2, a3, qf[nt][4 * jc + k][0], qf[nt][4 * jc + k][1]);
+                    }
                 }
         } else {
+            // two sums side by side: half the length of the chain of products
+            float sd[NT][4] = {};
             const int mi = lane >> 3, tr = (mi & 1) * 8 + (lane & 7);
 #pragma unroll
             for (int ks = 0; ks < kKSteps; ++ks) {
@@ -313,11 +298,15 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
                 ldsm_x4(kb + seg_off<kTile>(tr, ks * 2 + (mi >> 1)), a0, a1, a2, a3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    mma_bf16(sc[0][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+                    mma_bf16(ks % 2 ? sd[nt] : sc[0][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[0][nt][e] += sd[nt][e];
         }
         // ---- online softmax in the log2 domain; other keys weigh nothing
-        uint32_t pb[kFp8 ? 2 : 1][NT][2];  // P^T fragments (8-bit: of the first numbers, of the second)
+        uint32_t pb[kOctets][NT];  // P^T fragments
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float pr[kOctets][2];
@@ -340,7 +329,7 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
                 float sum = 0.f;
 #pragma unroll
                 for (int q = 0; q < kOctets; ++q) {
-                    pr[q][hc] = fast_exp2(pr[q][hc] - (kFp8 ? sub - 8.f : sub));  // 8-bit: in units of 2^-8
+                    pr[q][hc] = fast_exp2(pr[q][hc] - sub);
                     sum += pr[q][hc];
                 }
                 l[nt][hc] = l[nt][hc] * alpha[hc] + sum;
@@ -354,53 +343,36 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
                     o[mt][nt][3] *= alpha[1];
                 }
             }
-            if constexpr (kFp8) {
-                // a 16-bit element of the transposed matrix is two keys, r8 of an octet and of the next
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    uint32_t h0, l0, h1, l1;
-                    split_e4m3(pr[2 * t][0], pr[2 * t + 1][0], h0, l0);
-                    split_e4m3(pr[2 * t][1], pr[2 * t + 1][1], h1, l1);
-                    pb[0][nt][t] = movmatrix_t(h0 | h1 << 16);
-                    pb[kFp8][nt][t] = movmatrix_t(l0 | l1 << 16);
-                }
-            } else {
-                pb[0][nt][0] = movmatrix_t(pack_bf16(pr[0][0], pr[0][1]));  // keys 0-7
-                pb[0][nt][1] = movmatrix_t(pack_bf16(pr[1][0], pr[1][1]));  // keys 8-15
-            }
+            for (int q = 0; q < kOctets; ++q)
+                pb[q][nt] = movmatrix_t(kFp8 ? pack_f16(pr[q][0], pr[q][1]) : pack_bf16(pr[q][0], pr[q][1]));
         }
         // ---- O^T += V^T P^T
         if constexpr (kFp8) {
-            // k-slots 4 c4 ..: keys 2c, 2c + 8, 2c + 1, 2c + 9, and 16 on; elements 16 r8 .. + 15 of
-            // each, 4 x 4 bytes transposed: rows of m-tile 2 pp + j are elements 16 r8 + 4 pp + 2 j, + 1
-            uint32_t w[8][4];
+            // keys 16 t + 2c, + 1, + 8, + 9; elements 16 r8 .. + 15 of each, pairs of keys per element:
+            // rows of m-tile 2 pp + j are elements 16 r8 + 4 pp + 2 j and + 1
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint4 v = lds128(vb + sw128((k / 4) * 16 + 2 * c4 + (k & 1) * 8 + (k >> 1 & 1), r8));
-                w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
-            }
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t row = t * 16 + 2 * c4;
+                const uint4 w0 = lds128(vb + sw128(row, r8)), w1 = lds128(vb + sw128(row + 1, r8));
+                const uint4 w2 = lds128(vb + sw128(row + 8, r8)), w3 = lds128(vb + sw128(row + 9, r8));
+                const uint32_t k0[4] = {w0.x, w0.y, w0.z, w0.w}, k1[4] = {w1.x, w1.y, w1.z, w1.w};
+                const uint32_t k2[4] = {w2.x, w2.y, w2.z, w2.w}, k3[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
-            for (int pp = 0; pp < 4; ++pp) {
-                uint32_t f[2][4];
+                for (int pp = 0; pp < 4; ++pp) {
+                    const uint32_t x01 = __byte_perm(k0[pp], k1[pp], 0x5140), x23 = __byte_perm(k2[pp], k3[pp], 0x5140);
+                    const uint32_t y01 = __byte_perm(k0[pp], k1[pp], 0x7362), y23 = __byte_perm(k2[pp], k3[pp], 0x7362);
+                    uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+                    widen4(x01, a0, a1);
+                    widen4(x23, a2, a3);
+                    widen4(y01, b0, b1);
+                    widen4(y23, b2, b3);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t x0 = __byte_perm(w[4 * t][pp], w[4 * t + 1][pp], 0x5140);
-                    const uint32_t x1 = __byte_perm(w[4 * t + 2][pp], w[4 * t + 3][pp], 0x5140);
-                    const uint32_t y0 = __byte_perm(w[4 * t][pp], w[4 * t + 1][pp], 0x7362);
-                    const uint32_t y1 = __byte_perm(w[4 * t + 2][pp], w[4 * t + 3][pp], 0x7362);
-                    f[t][0] = __byte_perm(x0, x1, 0x5410);
-                    f[t][1] = __byte_perm(x0, x1, 0x7632);
-                    f[t][2] = __byte_perm(y0, y1, 0x5410);
-                    f[t][3] = __byte_perm(y0, y1, 0x7632);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(o[2 * pp][nt], a0, a1, a2, a3, pb[2 * t][nt], pb[2 * t + 1][nt]);
+                        mma_f16(o[2 * pp + 1][nt], b0, b1, b2, b3, pb[2 * t][nt], pb[2 * t + 1][nt]);
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int part2 = 0; part2 < 2; ++part2)
-                            mma_e4m3(o[2 * pp + j][nt], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
-                                     pb[kFp8 ? part2 : 0][nt][0], pb[kFp8 ? part2 : 0][nt][1]);
             }
         } else {
             const int mi = lane >> 3, tr = (mi >> 1) * 8 + (lane & 7);
@@ -410,7 +382,7 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
                 ldsm_x4_t(vb + seg_off<kTile>(tr, mt * 2 + (mi & 1)), a0, a1, a2, a3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    mma_bf16(o[mt][nt], a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
+                    mma_bf16(o[mt][nt], a0, a1, a2, a3, pb[0][nt], pb[1][nt]);
             }
         }
         __syncwarp();
@@ -503,8 +475,7 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
         const int64_t row = row0 + hh;
         *reinterpret_cast<uint2*>(p.out + row * D + c) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        // (8-bit: weights were in units of 2^-8)
-        if (p.lse && c == 0) p.lse[row] = (M + __log2f(L) - (kFp8 ? 8.f : 0.f)) * 0.69314718055994531f;
+        if (p.lse && c == 0) p.lse[row] = (M + __log2f(L)) * 0.69314718055994531f;
     }
     if (ncta > 1) cluster_barrier();  // no CTA leaves while another reads its shared memory
 }
@@ -519,8 +490,8 @@ cudaError_t go(const SparseAttnParams& p, int num_sms, cudaStream_t stream) {
     // each costs a start of about kStart tiles; up to the resident CTAs they all
     // run at once, beyond that in turns, with half a turn's idling at the end.
     // Measured at 384 units: bf16, 64 tiles per warp, with 1 / 2 / 4 / 8 CTAs
-    // 133 / 120 / 132 / 147 us; 8-bit, 16 tiles per warp, 1 / 2 / 4 CTAs 36 / 40 / 49
-    // us; one request's 8 units, bf16, 1 / 2 / 4 / 8 / 16 CTAs 40 / 23 / 14 / 9.9 /
+    // 133 / 120 / 132 / 147 us; 8-bit (e4m3 products), 16 tiles per warp, 1 / 2 / 4
+    // CTAs 36 / 40 / 49 us; one request's 8 units, bf16, 1 / 2 / 4 / 8 / 16 CTAs 40 / 23 / 14 / 9.9 /
     // 10.2 us.
     constexpr int64_t kStart = 5;
     const int64_t units = (int64_t)p.num_tokens * p.Hkv, slots = (int64_t)num_sms * C::kMinBlocks;

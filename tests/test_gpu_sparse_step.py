@@ -491,8 +491,8 @@ def attn_run(b, q, caches, sel, scale, units=None, lse=True, **kw):
 
 
 def attn_near(out, lse, want):
-    """P is rounded to bf16 before the product (or to two e4m3 numbers, half that) and the result to bf16,
-    2^-8 each: of the sum of the weighted magnitudes, and of the value. Scores of up to 2^5 with a relative error of a few 2^-23
+    """P is rounded to bf16 (or f16) before the product and the result to bf16, 2^-8 each: of the sum of
+    the weighted magnitudes, and of the value. Scores of up to 2^5 with a relative error of a few 2^-23
     (products of at most 128 terms, the scale, the exponential): 2^-14 more of that sum."""
     o, l, size = want
     real = ~np.isnan(size)
@@ -535,8 +535,8 @@ def test_sparse_attn_8_bit(Hq, Hkv, bs, K):
 
 @pytest.mark.parametrize("power", [-60, -12, 0, 17, 90])
 def test_sparse_attn_8_bit_takes_queries_of_any_magnitude(power):
-    """Queries of a head far from one, elements of a head far apart: q is held as two e4m3 numbers in units of
-    a power of two of its own head, off by at most 2^-18 of the head's largest element."""
+    """Queries of a head far from one, elements of a head far apart: q is held in units of a power of two of
+    its own head, off by at most 2^-22 of the head's largest element."""
     rng = np.random.default_rng(power + 100)
     b = batch(rng, [300, 77], [1, 2], 16)
     q, caches, sel = attn_case(rng, b, 4, 2, 128, 9, fp8=True)
