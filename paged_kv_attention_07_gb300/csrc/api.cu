@@ -152,6 +152,7 @@ bool encode_tokens(CUtensorMap* map, const void* base, uint64_t T, uint64_t H, u
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
+int log2_of(int x) { return x > 1 ? 1 + log2_of(x / 2) : 0; }
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 struct Hints {
@@ -1166,8 +1167,7 @@ pka_status sparse_attn_impl(const void* q, const void* k_cache, const void* v_ca
     p.Hkv = num_kv_heads;
     p.G = num_q_heads / num_kv_heads;
     p.bs = block_size;
-    for (p.bs_log2 = 0; 1 << p.bs_log2 < block_size; ++p.bs_log2) {
-    }
+    p.bs_log2 = log2_of(block_size);
     p.num_pages = num_pages;
     p.max_seq_len = max_seq_len;
     p.scale_log2 = scale * 1.4426950408889634f * (cf.fp8 ? cf.k_scale : 1.f);
@@ -1216,6 +1216,7 @@ pka_status pka_step_tables(const int32_t* ctx_lens, const int32_t* query_lens, i
     p.max_blocks = max_blocks_per_req;
     p.block_size = block_size;
     p.num_free = num_free_pages;
+    p.bs_log2 = pow2(block_size) ? log2_of(block_size) : -1;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(timed(PKA_KERNEL_STEP_TABLES, st, [&] { return launch_step_tables(p, st); }));
 }

@@ -138,6 +138,7 @@ struct StepTablesParams {
     int32_t* err;
     int64_t num_tokens;
     int num_reqs, max_blocks, block_size, num_free;
+    int bs_log2;  // of a block_size that is a power of two, else -1
 };
 
 struct QkRopeParams {

@@ -7,9 +7,12 @@
 //   page j of request r's need is free_pages[head + sum_{i<r} need_i + j]
 //   token t of request r: p = ctx_r + (t - qsl_r), slot = table[r][p / bs] * bs + p % bs
 //
-// Two prefix sums over at most kMaxRequests requests, then one independent
-// search and write per token. The bytes are few (12 per token), so the cost is
-// latency: one launch of one cluster. Every CTA of the cluster repeats the
+// Two prefix sums over at most kMaxRequests requests, then one search and write
+// per token. The bytes are few (12 per token), so the cost is latency and, with
+// many tokens, instructions: a warp takes a contiguous run of tokens and starts
+// each search where the last one ended (300 requests with 67214 tokens 8.2 us,
+// 11.4 us with a search of its own for every token; 48 requests with one token
+// each 3.9 us). One launch of one cluster. Every CTA of the cluster repeats the
 // prefix sums in its own shared memory (a few kilobytes from L2) and writes its
 // share of the tokens and pages; the page of a token on a new page comes from
 // the free list itself, not from the table entry another CTA writes. The
@@ -29,11 +32,12 @@ constexpr int kStBatch = 4;  // tokens of a thread in flight
 constexpr int kStCluster = 8;
 constexpr int64_t kStClusterTokens = 4096;
 
-PKA_DEVICE int pages_of(int tokens, int bs) { return (int)(((uint32_t)tokens + (uint32_t)bs - 1) / (uint32_t)bs); }
+// x / bs: a shift where the page size is a power of two (log2 >= 0).
+PKA_DEVICE int page_of(uint32_t x, int bs, int log2) { return (int)(log2 >= 0 ? x >> log2 : x / (uint32_t)bs); }
+PKA_DEVICE int pages_of(int tokens, int bs, int log2) { return page_of((uint32_t)tokens + (uint32_t)bs - 1, bs, log2); }
 
-// Last r in [0, n) with first[r] <= x (first[0] == 0 <= x).
-PKA_DEVICE int last_at_most(const int32_t* first, int n, int x) {
-    int lo = 0, hi = n - 1;
+// Last r in [lo, hi] with first[r] <= x (first[lo] <= x).
+PKA_DEVICE int last_at_most(const int32_t* first, int lo, int hi, int x) {
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (first[mid] <= x) lo = mid;
@@ -52,7 +56,7 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ncta = gridDim.x, cta = blockIdx.x;
-    const int B = p.num_reqs, bs = p.block_size;
+    const int B = p.num_reqs, bs = p.block_size, log2 = p.bs_log2;
     const int head = *p.free_head;
     const long long longest = (long long)p.max_blocks * bs;
 
@@ -76,7 +80,7 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
         if (q < 0 || c < 0 || s > longest) continue;
         nw[i] = q;
         cl[i] = c;
-        nd[i] = pages_of((int)s, bs) - pages_of(c, bs);  // (s <= longest, which fits)
+        nd[i] = pages_of((int)s, bs, log2) - pages_of(c, bs, log2);  // (s <= longest, which fits)
         tok += q;
         pag += nd[i];
     }
@@ -117,6 +121,7 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
     if (total > p.num_tokens) err |= PKA_DEVERR_QUERY_START_LOC;
     if (head < 0 || taken > (long long)p.num_free - head) err |= PKA_DEVERR_CAPACITY;
     const int any = __syncthreads_or(err);
+    cluster_arrive();  // this CTA has read the list's head (here, where no stores are in flight to wait for)
     if (any) {
         // nothing is taken: empty requests and no slots, so that the calls
         // that read these tables write and read nothing
@@ -152,38 +157,49 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
         const int32_t* list = p.free_pages + head;
         // ---- the new pages' table entries
         for (int j = cta * kStThreads + tid; j < (int)taken; j += ncta * kStThreads) {
-            const int r = last_at_most(s_first, B, j);
-            const int held = pages_of(s_ctx[r], bs);
+            const int r = last_at_most(s_first, 0, B - 1, j);
+            const int held = pages_of(s_ctx[r], bs, log2);
             p.block_table[(int64_t)r * p.max_blocks + held + (j - s_first[r])] = list[j];
         }
-        // ---- the tokens, kStBatch of a thread's at a time: their table loads overlap
-        const int64_t step = (int64_t)ncta * kStThreads;
-        for (int64_t tb = (int64_t)cta * kStThreads + tid; tb < p.num_tokens; tb += step * kStBatch) {
+        // ---- the tokens: 32 neighbours at a time, kStBatch times, so that their table loads overlap
+        const int nwarps = ncta * (kStThreads / 32), me = cta * (kStThreads / 32) + warp;
+        const int rounds = (int)((p.num_tokens + 31) / 32);  // (num_tokens <= INT32_MAX)
+        const int i0 = (int)((int64_t)rounds * me / nwarps), i1 = (int)((int64_t)rounds * (me + 1) / nwarps);
+        const int last = (int)total - 1;
+        int r0 = i0 < i1 && last >= 0 ? last_at_most(s_qsl, 0, B - 1, min(i0 * 32, last)) : 0;
+        for (int ib = i0; ib < i1; ib += kStBatch) {
             int pos[kStBatch], off[kStBatch], id[kStBatch];
 #pragma unroll
             for (int i = 0; i < kStBatch; ++i) {
-                const int64_t t = tb + step * i;
                 pos[i] = id[i] = -1;
                 off[i] = 0;
-                if (t >= total) continue;
-                const int r = last_at_most(s_qsl, B, (int)t);
+                const int tb = (ib + i) * 32, t = tb + lane;
+                if (ib + i >= i1 || tb > last) continue;  // (the same for the whole warp)
+                const int end = min(tb + 31, last), x = min(t, last);
+                int r = r0;
+                if (r0 + 1 < B && s_qsl[r0 + 1] <= end) {
+                    const int far = min(r0 + 31, B - 1);  // more only with requests that have no tokens
+                    r = last_at_most(s_qsl, r0, s_qsl[far] > end ? far : B - 1, x);
+                }
+                r0 = __shfl_sync(0xffffffffu, r, 31);
+                if (t > last) continue;
                 const int c = s_ctx[r];
-                pos[i] = c + ((int)t - s_qsl[r]);
-                const int held = pages_of(c, bs), page = (int)((uint32_t)pos[i] / (uint32_t)bs);
+                pos[i] = c + (t - s_qsl[r]);
+                const int held = pages_of(c, bs, log2), page = page_of((uint32_t)pos[i], bs, log2);
                 off[i] = pos[i] - page * bs;
                 id[i] = page < held ? p.block_table[(int64_t)r * p.max_blocks + page] : list[s_first[r] + page - held];
             }
 #pragma unroll
             for (int i = 0; i < kStBatch; ++i) {
-                const int64_t t = tb + step * i;
-                if (t >= p.num_tokens) continue;
+                const int64_t t = (int64_t)(ib + i) * 32 + lane;
+                if (ib + i >= i1 || t >= p.num_tokens) continue;
                 if (p.positions) p.positions[t] = pos[i];
                 p.slots[t] = id[i] >= 0 ? (int64_t)id[i] * bs + off[i] : -1;
             }
         }
     }
     // every CTA has read the list's head before it is advanced (in place, perhaps)
-    cluster_barrier();
+    cluster_wait();
     if (cta == 0 && tid == 0) *p.free_head_out = any ? head : head + (int)taken;
 }
 

@@ -373,7 +373,8 @@ def pka_qk_rope_cache_write(q, k, v, q_weight, k_weight, eps, cos_sin, interleav
     for name, x, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
         if x.dtype is not bf16 or x.get_device() != device or x.shape != (T, heads, d):
             raise ValueError(f"{where}: {name} must be bf16 [{T}, {heads}, {d}] on the current CUDA device")
-        if (heads > 1 and x.stride(1) != d) or (d > 1 and x.stride(2) != 1):
+        _, head, element = x.stride()
+        if (head != d and heads > 1) or (element != 1 and d > 1):
             raise ValueError(f"{where}: the heads of a row of {name} must be packed")
     caches = (nb, Hkv, bs, d)
     kind = bf16 if kv_scales is None else torch.uint8
