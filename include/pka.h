@@ -493,8 +493,8 @@ PKA_API pka_status pka_gather_rows(void *dst, const void *src, const int32_t *in
  * (PKA_DEVERR_CAPACITY) set the bit and take nothing: the table is left as it
  * is, *free_head_out = head, query_start_loc and seq_lens are 0 and all
  * positions and slots -1.
- * num_reqs <= 4096 and max_blocks_per_req * block_size <= INT32_MAX, else
- * PKA_ERR_UNSUPPORTED.
+ * num_reqs <= 4096, num_tokens <= 2^30 and max_blocks_per_req * block_size <=
+ * INT32_MAX, else PKA_ERR_UNSUPPORTED.
  */
 PKA_API pka_status pka_step_tables(const int32_t *ctx_lens, const int32_t *query_lens, int num_reqs,
                                    int64_t num_tokens, int32_t *block_table, int max_blocks_per_req, int block_size,
@@ -607,8 +607,8 @@ PKA_API pka_status pka_page_bounds(const void *k_cache, int cache_dtype, const i
  *                  (columns of its block table row), then -1
  * A seq_len that does not fit its request sets PKA_DEVERR_SEQ_LEN, a block id
  * outside the cache PKA_DEVERR_BLOCK_ID.
- * head_dim 64 or 128, Hq / Hkv <= 16, max_seq_len / block_size <= 32768, num_tokens <= 2^27, else
- * PKA_ERR_UNSUPPORTED.
+ * head_dim 64 or 128, Hq / Hkv <= 16, max_seq_len / block_size <= 32768 (rounded up), num_tokens * Hkv <=
+ * 2^27, else PKA_ERR_UNSUPPORTED.
  */
 PKA_API pka_status pka_select_pages(const void *q, const int8_t *bounds, const float *bound_scales,
                                     const int32_t *block_table, int max_blocks_per_req,
@@ -636,8 +636,8 @@ PKA_API pka_status pka_select_pages(const void *q, const int8_t *bounds, const f
  *                  the last request are left as they are)
  *   selected       device int32 [num_tokens, Hkv, num_pages]
  *   scale          finite and > 0
- * head_dim 64 or 128 (_fp8: 128), Hq / Hkv <= 16, block_size a power of two in [8, 128], else
- * PKA_ERR_UNSUPPORTED.
+ * head_dim 64 or 128 (_fp8: 128), Hq / Hkv <= 16, block_size a power of two in [8, 128], num_blocks * Hkv *
+ * block_size <= INT32_MAX, num_tokens * Hkv <= 2^27, else PKA_ERR_UNSUPPORTED.
  */
 PKA_API pka_status pka_sparse_attn_forward(const void *q, const void *k_cache, const void *v_cache,
                                            const int32_t *block_table, int max_blocks_per_req,

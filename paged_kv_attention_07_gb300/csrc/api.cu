@@ -1119,7 +1119,7 @@ pka_status check_sparse_batch(int num_reqs, int num_tokens, int Hq, int Hkv, int
     if (Hq % Hkv != 0) return PKA_ERR_INVALID_ARG;
     if ((int64_t)max_blocks * block_size < max_seq_len) return PKA_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKA_ERR_UNSUPPORTED;
-    if (Hq / Hkv > 16 || Hkv > 65535 || num_tokens > (1 << 27)) return PKA_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 16 || Hkv > 65535 || (int64_t)num_tokens * Hkv > (1 << 27)) return PKA_ERR_UNSUPPORTED;
     return PKA_OK;
 }
 
@@ -1194,7 +1194,7 @@ pka_status pka_step_tables(const int32_t* ctx_lens, const int32_t* query_lens, i
     if (seq_lens == ctx_lens || seq_lens == query_lens || query_start_loc == ctx_lens || query_start_loc == query_lens)
         return PKA_ERR_INVALID_ARG;  // the lengths are read again while these are written
     if (num_reqs > kMaxRequests) return PKA_ERR_UNSUPPORTED;
-    if ((int64_t)max_blocks_per_req * block_size > INT32_MAX || num_tokens > INT32_MAX) return PKA_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_req * block_size > INT32_MAX || num_tokens > (1 << 30)) return PKA_ERR_UNSUPPORTED;
     if (!aligned(ctx_lens, 4) || !aligned(query_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
         !aligned(free_head, 4) || !aligned(free_head_out, 4) || !aligned(query_start_loc, 4) ||
         !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(slot_mapping, 8) || !aligned(error_word, 4))

@@ -403,8 +403,11 @@ template <int D, int NT, int kThreads>
 cudaError_t go(const PageSelectParams& p, int cluster, cudaStream_t stream) {
     auto kern = page_select_kernel<D, NT, kThreads>;
     const int pages = (p.max_seq_len + p.block_size - 1) / p.block_size;
-    const int smem = PsCfg<D, NT, kThreads>::kFixed + 4 * (pages + (pages + 31) / 32);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto smem_of = [](int n) { return PsCfg<D, NT, kThreads>::kFixed + 4 * (n + (n + 31) / 32); };
+    const int smem = smem_of(pages);
+    // (the most that any call takes: calls of several threads set the same)
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(kPageSelectMaxPages));
     if (e != cudaSuccess) return e;
     return launch_cluster(kern, dim3((unsigned)(cluster * p.num_tokens * p.Hkv)), dim3(kThreads), smem, cluster, stream,
                           p);
@@ -415,8 +418,9 @@ cudaError_t go(const PageSelectParams& p, int cluster, cudaStream_t stream) {
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream) {
     const int pages = (p.max_seq_len + p.block_size - 1) / p.block_size;
     const int64_t units = (int64_t)p.num_tokens * p.Hkv;
-    // (with the most pages the keys leave no room for the stages of 8 warps)
-    const bool two = p.G > 8, wide = units < num_sms && pages <= 24576;
+    // 256 threads per CTA score a few long contexts faster, 128 keep more of many
+    // CTAs resident (96 requests, 8 kv heads: 27.7 us, 32.1 us with 256)
+    const bool two = p.G > 8, wide = units < num_sms;
     int n = 1;
     while (n < 8 && units * n < num_sms && pages > n * 128) n *= 2;
     auto by_width = [&](auto d, auto nt) {

@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
 
 cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream) {
     const size_t smem = sizeof(int32_t) * 3 * (size_t)p.num_reqs;
-    if (smem > 47 * 1024) {  // past what every kernel may use
-        const cudaError_t e =
-            cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 47 * 1024) {  // past what every kernel may use; the most that any call takes
+        const cudaError_t e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)sizeof(int32_t) * 3 * kMaxRequests);
         if (e != cudaSuccess) return e;
     }
     const int n = p.num_tokens >= kStClusterTokens ? kStCluster : 1;

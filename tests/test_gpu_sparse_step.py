@@ -706,6 +706,40 @@ def test_sparse_attn_reports_bad_lists():
         assert err == E[bit]
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_caches_past_32_bits(fp8):
+    """The last pages of caches of more than 2^32 bytes: written, bounded and read where they lie."""
+    d, bs, Hkv = 128, 128, 2
+    nb = (1 << 32) // (bs * Hkv * d * (1 if fp8 else 2)) + 40
+    rng = np.random.default_rng(13)
+    T = 300
+    s = rope_case(T, 4, Hkv, d, d, False, True, fp8, True, bs=bs, nb=8, seed=13)
+    kind = torch.uint8 if fp8 else BF16
+    for name in ("k_cache", "v_cache"):
+        s[name] = torch.zeros((nb, Hkv, bs, d), dtype=kind, device="cuda")
+    table = np.array([[nb - 1, nb - 7, nb - 2]])
+    p = np.arange(T)
+    s["slots"] = dev(table[0, p // bs] * bs + p % bs, I64)
+    tail = slice(nb - 8, nb)
+    before = copies({n: x for n, x in s.items() if n not in ("k_cache", "v_cache")})
+    rope_call(s)
+    assert int(s["err"]) == 0
+    small = dict(s, slots=s["slots"] - (nb - 8) * bs, k_cache=s["k_cache"][tail], v_cache=s["v_cache"][tail])
+    rope_check(small, dict(before, k_cache=torch.zeros_like(small["k_cache"]), v_cache=torch.zeros_like(small["v_cache"])))
+    assert not any(s[n][:8].any() for n in ("k_cache", "v_cache"))
+    codes, scales = torch.zeros(nb, Hkv, 2, d, dtype=torch.int8, device="cuda"), torch.zeros(nb, Hkv, device="cuda")
+    pka.pka_page_bounds(s["k_cache"], s["slots"], codes, scales, error_word=s["err"])
+    bounds_check(small["k_cache"], small["slots"].tolist(), codes[tail] * 0, scales[tail] * 0, codes[tail], scales[tail])
+    out, lse = torch.empty(1, 4, d, dtype=BF16, device="cuda"), torch.empty(1, 4, device="cuda")
+    q, sel = s["q_out"][-1:].contiguous(), np.array([[[0, 1, 2], [0, 2, -1]]])
+    pka.pka_sparse_attn_forward(q, s["k_cache"], s["v_cache"], dev(table, I32), dev([0, 1], I32), dev([T], I32),
+                                dev(sel, I32), 0.1, T, out, lse, kv_scales=s["scales"], error_word=s["err"])
+    assert int(s["err"]) == 0
+    attn_near(out, lse, ref.sparse_attn(ref.f64(q), ref.f64(small["k_cache"]), ref.f64(small["v_cache"]),
+                                        table - (nb - 8), [0, 1], [T], sel, 0.1,
+                                        [float(np.float32(u)) for u in s["scales"]] if fp8 else (1.0, 1.0)))
+
+
 # ---------------------------------------------------------------- the step as a whole
 
 

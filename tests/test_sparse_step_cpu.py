@@ -106,7 +106,7 @@ SELECT = ("q bounds scales bt width qsl seq B T Hq Hkv d nb bs first last maxs K
     (dict(maxs=1025), 1),                          # the table is narrower than max_seq_len needs
     (dict(first=-1), 1), (dict(last=0), 1), (dict(first=7), 1), (dict(last=9, first=0), 1),
     (dict(q=P(0x10008)), 1), (dict(bounds=P(0x10008)), 1), (dict(sel=ODD), 1), (dict(err=ODD), 1),
-    (dict(d=96), 2), (dict(Hq=34), 2), (dict(Hkv=70000, Hq=70000), 2), (dict(T=(1 << 27) + 1), 2),
+    (dict(d=96), 2), (dict(Hq=34), 2), (dict(Hkv=70000, Hq=70000), 2), (dict(T=(1 << 26) + 1), 2),
     (dict(maxs=32769, width=32769, bs=1), 2),      # more pages than the selection holds
     (dict(T=0, q=None), 0),
 ])
