@@ -571,7 +571,7 @@ PKA_API pka_status pka_qk_rope_cache_write_fp8(const void *q, const void *k, con
  *                 set PKA_DEVERR_SLOT
  *   bounds        device int8 [num_blocks, Hkv, 2, d], 16-byte aligned
  *   bound_scales  device float32 [num_blocks, Hkv]
- * head_dim 64 or 128, else PKA_ERR_UNSUPPORTED.
+ * head_dim 64 or 128, num_kv_heads <= 65535, block_size <= 2^20, else PKA_ERR_UNSUPPORTED.
  */
 PKA_API pka_status pka_page_bounds(const void *k_cache, int cache_dtype, const int64_t *slot_mapping,
                                    int64_t num_tokens, int num_kv_heads, int head_dim, int64_t num_blocks,
@@ -607,8 +607,8 @@ PKA_API pka_status pka_page_bounds(const void *k_cache, int cache_dtype, const i
  *                  (columns of its block table row), then -1
  * A seq_len that does not fit its request sets PKA_DEVERR_SEQ_LEN, a block id
  * outside the cache PKA_DEVERR_BLOCK_ID.
- * head_dim 64 or 128, Hq / Hkv <= 16, max_seq_len / block_size <= 32768 (rounded up), num_tokens * Hkv <=
- * 2^27, else PKA_ERR_UNSUPPORTED.
+ * head_dim 64 or 128, Hq / Hkv <= 16, max_seq_len / block_size <= 32768 (rounded up), max_seq_len and
+ * num_pages <= 2^30, num_tokens * Hkv <= 2^27, Hkv <= 65535, else PKA_ERR_UNSUPPORTED.
  */
 PKA_API pka_status pka_select_pages(const void *q, const int8_t *bounds, const float *bound_scales,
                                     const int32_t *block_table, int max_blocks_per_req,
@@ -637,7 +637,8 @@ PKA_API pka_status pka_select_pages(const void *q, const int8_t *bounds, const f
  *   selected       device int32 [num_tokens, Hkv, num_pages]
  *   scale          finite and > 0
  * head_dim 64 or 128 (_fp8: 128), Hq / Hkv <= 16, block_size a power of two in [8, 128], num_blocks * Hkv *
- * block_size <= INT32_MAX, num_tokens * Hkv <= 2^27, else PKA_ERR_UNSUPPORTED.
+ * block_size <= INT32_MAX, max_seq_len and num_pages <= 2^30, num_tokens * Hkv <= 2^27, Hkv <= 65535, else
+ * PKA_ERR_UNSUPPORTED.
  */
 PKA_API pka_status pka_sparse_attn_forward(const void *q, const void *k_cache, const void *v_cache,
                                            const int32_t *block_table, int max_blocks_per_req,

@@ -1120,6 +1120,8 @@ pka_status check_sparse_batch(int num_reqs, int num_tokens, int Hq, int Hkv, int
     if ((int64_t)max_blocks * block_size < max_seq_len) return PKA_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKA_ERR_UNSUPPORTED;
     if (Hq / Hkv > 16 || Hkv > 65535 || (int64_t)num_tokens * Hkv > (1 << 27)) return PKA_ERR_UNSUPPORTED;
+    // (32-bit indexes of a request's keys and of a list)
+    if (max_seq_len > (1 << 30) || num_pages > (1 << 30)) return PKA_ERR_UNSUPPORTED;
     return PKA_OK;
 }
 
@@ -1255,6 +1257,7 @@ pka_status pka_page_bounds(const void* k_cache, int cache_dtype, const int64_t* 
         (cache_dtype != 1 && cache_dtype != 2))
         return PKA_ERR_INVALID_ARG;
     if ((head_dim != 64 && head_dim != 128) || num_kv_heads > 65535) return PKA_ERR_UNSUPPORTED;
+    if (block_size > (1 << 20)) return PKA_ERR_UNSUPPORTED;  // (32-bit indexes of a page's keys)
     if (num_blocks > INT64_MAX / block_size) return PKA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PKA_OK;
     if (!k_cache || !slot_mapping || !bounds || !bound_scales) return PKA_ERR_INVALID_ARG;
@@ -1288,7 +1291,7 @@ pka_status pka_select_pages(const void* q, const int8_t* bounds, const float* bo
                                              block_size, max_blocks_per_req, max_seq_len, num_pages);
     if (sc != PKA_OK) return sc;
     if (num_first < 0 || num_last < 1 || num_first > num_pages - num_last) return PKA_ERR_INVALID_ARG;
-    if (((int64_t)max_seq_len + block_size - 1) / block_size > kPageSelectMaxPages) return PKA_ERR_UNSUPPORTED;
+    if ((max_seq_len - 1) / block_size + 1 > kPageSelectMaxPages) return PKA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PKA_OK;
     if (!q || !bounds || !bound_scales || !block_table || !query_start_loc || !seq_lens || !selected)
         return PKA_ERR_INVALID_ARG;

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* s_q = smem;  // per head: min(c, 0) then max(c, 0), in the records' order
     uint32_t* s_key = reinterpret_cast<uint32_t*>(smem + C::kFixed);  // the candidates' scores (first CTA's is used)
-    uint32_t* s_bits = s_key + (p.max_seq_len + p.block_size - 1) / p.block_size;  // the chosen candidates
+    uint32_t* s_bits = s_key + ((p.max_seq_len - 1) / p.block_size + 1);  // the chosen candidates
     __shared__ float s_unit[NT * 8], s_zero[NT * 8][2];
     __shared__ uint32_t s_hist[kBins];
     __shared__ uint32_t s_warp[C::kWarps];
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
 template <int D, int NT, int kThreads>
 cudaError_t go(const PageSelectParams& p, int cluster, cudaStream_t stream) {
     auto kern = page_select_kernel<D, NT, kThreads>;
-    const int pages = (p.max_seq_len + p.block_size - 1) / p.block_size;
+    const int pages = (p.max_seq_len - 1) / p.block_size + 1;
     auto smem_of = [](int n) { return PsCfg<D, NT, kThreads>::kFixed + 4 * (n + (n + 31) / 32); };
     const int smem = smem_of(pages);
     // (the most that any call takes: calls of several threads set the same)
@@ -416,7 +416,7 @@ cudaError_t go(const PageSelectParams& p, int cluster, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream) {
-    const int pages = (p.max_seq_len + p.block_size - 1) / p.block_size;
+    const int pages = (p.max_seq_len - 1) / p.block_size + 1;
     const int64_t units = (int64_t)p.num_tokens * p.Hkv;
     // 256 threads per CTA score a few long contexts faster, 128 keep more of many
     // CTAs resident (96 requests, 8 kv heads: 27.7 us, 32.1 us with 256)

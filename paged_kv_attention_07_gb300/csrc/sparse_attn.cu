@@ -186,8 +186,7 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
         cp_async_commit();  // (a group per tile, empty behind the last)
     }
 
-    // ---- Q^T fragments: column n, zero behind the last. bf16: [k-step of 16 elements][2];
-    // 8-bit: the first e4m3 numbers of [k-step of 32][2], then the second ones
+    // ---- Q^T fragments: column n, zero behind the last; [k-step of 16 elements][2]
     uint32_t qf[NT][kKSteps][2];
     float factor[NT][2];  // 8-bit: this lane's columns of S^T, from their units to the log2 domain
 #pragma unroll

@@ -135,6 +135,22 @@ def test_sparse_attn_refuses(lib, kw, status):
     assert _call(lib.pka_sparse_attn_forward_fp8, ATTN_ORDER + " k_scale v_scale" + ATTN_TAIL, ATTN, kw) == status
 
 
+BIG = (1 << 31) - 1
+
+
+def test_indexes_of_a_request_stay_in_32_bits(lib):
+    # sums such as max_seq_len + block_size, and the last tile's key indexes, would pass them
+    for kw in (dict(maxs=BIG, width=BIG, bs=1 << 20), dict(maxs=BIG, width=1, bs=BIG), dict(K=(1 << 30) + 1),
+               dict(maxs=(1 << 30) + 1, width=65, bs=1 << 24)):
+        assert _call(lib.pka_select_pages, *SELECT, kw) == 2
+    for kw in (dict(maxs=BIG, width=BIG), dict(maxs=(1 << 30) + 1, width=1 << 30), dict(K=(1 << 30) + 1)):
+        assert _call(lib.pka_sparse_attn_forward, ATTN_ORDER + ATTN_TAIL, ATTN, kw) == 2
+        assert _call(lib.pka_sparse_attn_forward_fp8, ATTN_ORDER + " k_scale v_scale" + ATTN_TAIL, ATTN, kw) == 2
+    assert _call(lib.pka_page_bounds, *BOUNDS, dict(bs=(1 << 20) + 1)) == 2
+    # within the limits: one page longer than the request, no tokens
+    assert _call(lib.pka_select_pages, *SELECT, dict(maxs=5, width=1, bs=BIG, T=0)) == 0
+
+
 @pytest.mark.parametrize("kw,status", [(dict(d=64), 2), (dict(k_scale=0.0), 1), (dict(v_scale=NAN), 1)])
 def test_sparse_attn_fp8_refuses(lib, kw, status):
     assert _call(lib.pka_sparse_attn_forward_fp8, ATTN_ORDER + " k_scale v_scale" + ATTN_TAIL, ATTN, kw) == status
