@@ -1045,6 +1045,18 @@ namespace {
 
 bool positive_finite(float x) { return std::isfinite(x) && x > 0.f; }
 
+// s > 0 as [1, 2) times a power of two (less for the smallest s).
+QuotientBy quotient_by(float s) {
+    int e;
+    const float f = std::frexp(s, &e);
+    QuotientBy u;
+    u.pre = std::ldexp(1.f, std::min(1 - e, 127));
+    u.s = s * u.pre;
+    u.start = u.mend = (float)(1.0 / u.s);
+    if (f == 1.f - 0x1p-24f) u.mend = std::nextafter(u.start, 0.f);  // (the reciprocal lies between these)
+    return u;
+}
+
 pka_status qk_rope_impl(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
                         int rotary_dim, int max_position, int interleaved, const int32_t* positions,
@@ -1104,8 +1116,8 @@ pka_status qk_rope_impl(const void* q, const void* k, const void* v, int64_t q_s
     p.interleaved = interleaved;
     p.block_size = block_size;
     p.eps = eps;
-    p.k_scale = cf.k_scale;
-    p.v_scale = cf.v_scale;
+    p.k_unit = quotient_by(cf.k_scale);
+    p.v_unit = quotient_by(cf.v_scale);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(timed(PKA_KERNEL_QK_ROPE, st, [&] { return launch_qk_rope(p, cf.fp8, sms, st); }));
 }

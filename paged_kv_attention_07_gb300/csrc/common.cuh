@@ -299,13 +299,18 @@ PKA_DEVICE uint32_t e4m3x2_to_f16x2(uint32_t x16) {
 
 PKA_DEVICE __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 
-// Four floats -> four E4M3 codes (x / s, RN-even, saturating), lowest first.
+// Four floats -> four E4M3 codes (RN-even, saturating), lowest first.
+PKA_DEVICE uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+// The codes of x / s, the quotient rounded to float32 first.
 PKA_DEVICE uint32_t quantize4(float a, float b, float c, float d, float s) {
-    uint32_t lo, hi;
-    const float qa = __fdiv_rn(a, s), qb = __fdiv_rn(b, s), qc = __fdiv_rn(c, s), qd = __fdiv_rn(d, s);
-    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(lo) : "f"(qa), "f"(qb));
-    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(hi) : "f"(qc), "f"(qd));
-    return lo | (hi << 16);
+    return e4m3x4(__fdiv_rn(a, s), __fdiv_rn(b, s), __fdiv_rn(c, s), __fdiv_rn(d, s));
 }
 
 // Two floats -> bf16x2 (round to nearest even); `lo` lands in the low half.

@@ -141,6 +141,12 @@ struct StepTablesParams {
     int bs_log2;  // of a block_size that is a power of two, else -1
 };
 
+// What a division by s is made of: s and x times the power of two `pre`, and
+// the reciprocals of s * pre that start the quotient and mend it.
+struct QuotientBy {
+    float pre, s, start, mend;
+};
+
 struct QkRopeParams {
     const __nv_bfloat16* q;  // rows of num_heads * head_dim, `*_stride` elements apart
     const __nv_bfloat16* k;
@@ -158,7 +164,8 @@ struct QkRopeParams {
     int32_t* err;
     int64_t q_stride, k_stride, v_stride, num_tokens, num_slots;
     int Hq, Hkv, head_dim, rotary, max_position, interleaved, block_size;
-    float eps, k_scale, v_scale;
+    float eps;
+    QuotientBy k_unit, v_unit;  // 8-bit cache: of the scales
 };
 
 struct PageBoundsParams {

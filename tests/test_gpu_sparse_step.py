@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import fp8
 from paged_kv_attention_07_gb300 import pka
 from tests import sparse_ref as ref
 
@@ -196,6 +197,42 @@ def test_rope(T, Hq, Hkv, d, rotary, interleaved, norm, packed, bs, fp8):
     rope_call(s)
     assert int(s["err"]) == 0
     rope_check(s, before)
+
+
+@pytest.mark.parametrize("k_scale,v_scale", [(0.05, 0.03125), (0.75, 0.0371), (1.0, 3.3e4), (1e-3, 448.0),
+                                             (1e-40, 3e38), (2.0 ** -120, 2.0 ** 90), (1.1754944e-38, 2e-30),
+                                             (2.0 - 2.0 ** -23, 1.0 - 2.0 ** -24), (1.0 + 2.0 ** -23, 1.4e-45)])
+def test_rope_codes_are_those_of_the_cache_write(k_scale, v_scale):
+    # every bf16 pattern, NaN and infinities among them: without norms and rotation both calls store the same codes
+    x = torch.arange(65536, dtype=I32, device="cuda").to(torch.int16).view(BF16).view(128, 4, 128)
+    slots = dev(np.arange(128), I64)
+    caches = [torch.zeros(8, 4, 16, 128, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    pka.pka_qk_rope_cache_write(x, x, x, None, None, 0.0, None, False, dev(np.zeros(128), I32), slots,
+                                torch.empty_like(x), None, None, caches[0], caches[1], kv_scales=(k_scale, v_scale))
+    pka.pka_cache_write_fp8(x, x, slots, caches[2], caches[3], k_scale, v_scale)
+    assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+
+
+@pytest.mark.parametrize("scale", [0.05, 0.75, 2.0 ** -5])
+def test_rope_codes_at_the_borders(scale):
+    # rotated keys are float32: products of small integers put quotients on and next to every border of two codes
+    n = 512
+    k = torch.zeros(n, 1, 64, dtype=BF16, device="cuda")
+    k[:, 0, 0::2] = (torch.arange(32, device="cuda") * 8 + 1).to(BF16)
+    border = torch.arange(n, device="cuda", dtype=torch.float64) / 32
+    border[0] = 2.0 ** -10  # half the least code
+    table = torch.zeros(n, 64, dtype=torch.float64, device="cuda")
+    u32 = np.float32(scale).astype(np.float64)
+    table[:, :32] = border[:, None] * u32 / k[0, 0, 0::2].double()
+    step = torch.arange(n, device="cuda") % 5 - 2  # the float32 numbers around them
+    table = (table.float().view(I32) + torch.where(table != 0, step[:, None].int(), 0)).view(torch.float32)
+    caches = [torch.zeros(n // 16, 1, 16, 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pka.pka_qk_rope_cache_write(k, k, k, None, None, 0.0, table, True, dev(np.arange(n), I32), dev(np.arange(n), I64),
+                                torch.empty_like(k), None, None, *caches, kv_scales=(scale, 1.0))
+    # (a c - 0 s) and (0 c + a s) with s = 0: one rounding, of a c
+    a = (k[:, 0].float()[:, 0::2] * table[:, :32]).cpu().numpy()
+    got = caches[0].view(n, 64).cpu().numpy()
+    assert np.array_equal(got[:, 0::2], fp8.quantize_f32(a, scale)) and not got[:, 1::2].any()
 
 
 @pytest.mark.parametrize("fp8", [False, True])
