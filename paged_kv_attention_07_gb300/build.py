@@ -1,7 +1,8 @@
 """Builds libpka.so (the CUDA kernels + C ABI) in-tree for sm_103a.
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then the
-objects are linked into paged_kv_attention_07_gb300/_build/libpka.so.
+objects are linked into paged_kv_attention_07_gb300/_build/libpka.so. The
+calls with torch tensors (csrc/torch_calls.cpp) become a Python module beside it.
 Nothing is installed outside the repository.
 
     python -m paged_kv_attention_07_gb300.build [--force]
@@ -9,16 +10,19 @@ Nothing is installed outside the repository.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpka.so")
+TORCH_CALLS = os.path.join(OUT_DIR, "_pka_torch.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -49,10 +53,35 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _compile_torch_calls() -> str:
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    include = [INCLUDE, os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
+               os.path.join(cuda, "include")]
+    obj = os.path.join(OUT_DIR, "torch_calls.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[x for i in include for x in ("-I", i)], "-c",
+           os.path.join(CSRC, "torch_calls.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_torch_calls(obj: str) -> None:
+    lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = f"{TORCH_CALLS}.{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libpka.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_CALLS)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile csrc/*.cu and link libpka.so; returns the library path."""
     deps = _deps() + [os.path.abspath(__file__)]
-    if not force and not _stale(LIB, deps):
+    if not force and not _stale(LIB, deps) and not _stale(TORCH_CALLS, [*deps, LIB]):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -69,7 +98,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        torch_obj = ex.submit(_compile_torch_calls)
         objs = list(ex.map(compile_one, srcs))
     tmp = f"{LIB}.{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
@@ -77,6 +107,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_torch_calls(torch_obj.result())
     return LIB
 
 

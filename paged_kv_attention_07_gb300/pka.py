@@ -1,4 +1,5 @@
-"""ctypes binding of libpka.so (include/pka.h). Argument marshalling only.
+"""Binding of libpka.so (include/pka.h): ctypes, and for the calls of the block-sparse step a module that
+takes the tensors themselves (csrc/torch_calls.cpp). Argument marshalling only.
 
 Every function has the C entry point's name and meaning; tensors are torch
 CUDA tensors whose shapes give the sizes, streams default to torch's current
@@ -12,6 +13,7 @@ import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpka.so")
+TORCH_CALLS_PATH = os.path.join(_HERE, "_build", "_pka_torch.so")
 
 PKA_OK = 0
 STATUS_NAMES = {0: "PKA_OK", 1: "PKA_ERR_INVALID_ARG", 2: "PKA_ERR_UNSUPPORTED",
@@ -42,6 +44,7 @@ class PkaError(RuntimeError):
 
 
 _lib = None
+_torch_calls = None
 
 
 def load(path: str | None = None):
@@ -306,31 +309,21 @@ def pka_gather_rows(dst, src, index, error_word=None, stream=None):
                                   int(row_bytes), _ptr(error_word), _stream(stream)), "pka_gather_rows")
 
 
-def _packed(where, device, *specs):
-    """Every (name, tensor or None, dtype, shape) packed, of that type and shape, on that device."""
-    for name, t, dtype, shape in specs:
-        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
-                              or t.get_device() != device):
-            raise ValueError(f"{where}: {name} must be a packed {dtype} tensor of shape {shape} on the current CUDA "
-                             f"device, not {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _torch():
-    """torch, the current CUDA device, and a function from a call's `stream` to its address there (the
-    torch.cuda forms build a Stream object on each call, which costs as much as a small launch)."""
-    import torch
-    device = torch.cuda.current_device()
-
-    def address(stream):
-        if stream is None:
-            return torch._C._cuda_getCurrentRawStream(device)
-        return stream if isinstance(stream, int) else stream.cuda_stream
-
-    return torch, device, address
+def _calls():
+    """The calls with torch tensors (csrc/torch_calls.cpp): they check types, shapes, packing and device
+    (ValueError), launch on the current stream where `stream` is None, and return the status."""
+    global _torch_calls
+    if _torch_calls is None:
+        import importlib.util
+        import torch  # noqa: F401  (its libraries are the module's)
+        load()
+        if not os.path.exists(TORCH_CALLS_PATH):
+            raise RuntimeError(f"{TORCH_CALLS_PATH} not found: it must be built as libpka.so is")
+        spec = importlib.util.spec_from_file_location("_pka_torch", TORCH_CALLS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _torch_calls = module
+    return _torch_calls
 
 
 def pka_step_tables(ctx_lens, query_lens, block_table, block_size, free_pages, free_head, free_head_out,
@@ -338,21 +331,9 @@ def pka_step_tables(ctx_lens, query_lens, block_table, block_size, free_pages, f
     """ctx_lens, query_lens, seq_lens [B] int32; block_table [B, max_blocks] int32 (new pages are added);
     free_pages [n] int32, free_head / free_head_out [1] int32 (may be the same tensor); query_start_loc [B + 1]
     int32; positions [T] int32 or None, slot_mapping [T] int64 (T >= the new tokens; the rest gets -1)."""
-    torch, device, address = _torch()
-    i32 = torch.int32
-    B, width = block_table.shape
-    T, pages = slot_mapping.numel(), free_pages.numel()
-    _packed("pka_step_tables", device, ("ctx_lens", ctx_lens, i32, (B,)), ("query_lens", query_lens, i32, (B,)),
-            ("block_table", block_table, i32, (B, width)), ("free_pages", free_pages, i32, (pages,)),
-            ("free_head", free_head, i32, (1,)), ("free_head_out", free_head_out, i32, (1,)),
-            ("query_start_loc", query_start_loc, i32, (B + 1,)), ("seq_lens", seq_lens, i32, (B,)),
-            ("positions", positions, i32, (T,)), ("slot_mapping", slot_mapping, torch.int64, (T,)),
-            ("error_word", error_word, i32, (1,)))
-    st = load().pka_step_tables(ctx_lens.data_ptr(), query_lens.data_ptr(), B, T, block_table.data_ptr(), width,
-                                block_size, free_pages.data_ptr(), pages, free_head.data_ptr(),
-                                free_head_out.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(),
-                                _addr(positions), slot_mapping.data_ptr(), _addr(error_word), address(stream))
-    _check(st, "pka_step_tables")
+    _check(_calls().step_tables(ctx_lens, query_lens, block_table, block_size, free_pages, free_head, free_head_out,
+                                query_start_loc, seq_lens, positions, slot_mapping, error_word, stream),
+           "pka_step_tables")
 
 
 def pka_qk_rope_cache_write(q, k, v, q_weight, k_weight, eps, cos_sin, interleaved, positions, slot_mapping, q_out,
@@ -361,101 +342,32 @@ def pka_qk_rope_cache_write(q, k, v, q_weight, k_weight, eps, cos_sin, interleav
     k_weight [d] bf16 or None; cos_sin [max_position, rotary_dim] float32 (cosines, then sines) or None;
     positions [T] int32, slot_mapping [T] int64; q_out [T, Hq, d], k_out, v_out [T, Hkv, d] or None; caches
     [nb, Hkv, bs, d] bf16, or uint8 E4M3 codes with kv_scales=(k_scale, v_scale)."""
-    torch, device, address = _torch()
-    bf16, where = torch.bfloat16, "pka_qk_rope_cache_write"
-    T, Hq, d = q.shape
-    Hkv = k.shape[1]
-    nb, _, bs, _ = k_cache.shape
-    longest, rotary = (0, 0) if cos_sin is None else cos_sin.shape
-    q_row, k_row, v_row = Hq * d, Hkv * d, Hkv * d
-    if T > 1:  # (the row stride of a single row is free)
-        q_row, k_row, v_row = q.stride(0), k.stride(0), v.stride(0)
-    for name, x, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-        if x.dtype is not bf16 or x.get_device() != device or x.shape != (T, heads, d):
-            raise ValueError(f"{where}: {name} must be bf16 [{T}, {heads}, {d}] on the current CUDA device")
-        _, head, element = x.stride()
-        if (head != d and heads > 1) or (element != 1 and d > 1):
-            raise ValueError(f"{where}: the heads of a row of {name} must be packed")
-    caches = (nb, Hkv, bs, d)
-    kind = bf16 if kv_scales is None else torch.uint8
-    _packed(where, device, ("q_weight", q_weight, bf16, (d,)), ("k_weight", k_weight, bf16, (d,)),
-            ("cos_sin", cos_sin, torch.float32, (longest, rotary)), ("positions", positions, torch.int32, (T,)),
-            ("slot_mapping", slot_mapping, torch.int64, (T,)), ("q_out", q_out, bf16, (T, Hq, d)),
-            ("k_out", k_out, bf16, (T, Hkv, d)), ("v_out", v_out, bf16, (T, Hkv, d)),
-            ("k_cache", k_cache, kind, caches), ("v_cache", v_cache, kind, caches),
-            ("error_word", error_word, torch.int32, (1,)))
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, _addr(q_weight), _addr(k_weight), float(eps),
-            _addr(cos_sin), rotary, longest, 1 if interleaved else 0, positions.data_ptr(), slot_mapping.data_ptr(),
-            T, Hq, Hkv, d, q_out.data_ptr(), _addr(k_out), _addr(v_out), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs)
-    if kv_scales is None:
-        st = load().pka_qk_rope_cache_write(*args, _addr(error_word), address(stream))
-    else:
-        st = load().pka_qk_rope_cache_write_fp8(*args, float(kv_scales[0]), float(kv_scales[1]),
-                                                _addr(error_word), address(stream))
-    _check(st, where)
+    _check(_calls().qk_rope_cache_write(q, k, v, q_weight, k_weight, eps, cos_sin, interleaved, positions,
+                                        slot_mapping, q_out, k_out, v_out, k_cache, v_cache, kv_scales, error_word,
+                                        stream), "pka_qk_rope_cache_write")
 
 
 def pka_page_bounds(k_cache, slot_mapping, bounds, bound_scales, error_word=None, stream=None):
     """k_cache [nb, Hkv, bs, d] bf16, or uint8 E4M3 codes; slot_mapping [T] int64; bounds [nb, Hkv, 2, d] int8,
     bound_scales [nb, Hkv] float32 (the entries of pages that are not filled stay)."""
-    torch, device, address = _torch()
-    nb, Hkv, bs, d = k_cache.shape
-    T = slot_mapping.numel()
-    kind = torch.uint8 if k_cache.dtype is torch.uint8 else torch.bfloat16
-    _packed("pka_page_bounds", device, ("k_cache", k_cache, kind, (nb, Hkv, bs, d)),
-            ("slot_mapping", slot_mapping, torch.int64, (T,)), ("bounds", bounds, torch.int8, (nb, Hkv, 2, d)),
-            ("bound_scales", bound_scales, torch.float32, (nb, Hkv)), ("error_word", error_word, torch.int32, (1,)))
-    st = load().pka_page_bounds(k_cache.data_ptr(), 2 if kind is torch.uint8 else 1, slot_mapping.data_ptr(), T,
-                                Hkv, d, nb, bs, bounds.data_ptr(), bound_scales.data_ptr(), _addr(error_word), address(stream))
-    _check(st, "pka_page_bounds")
+    _check(_calls().page_bounds(k_cache, slot_mapping, bounds, bound_scales, error_word, stream), "pka_page_bounds")
 
 
 def pka_select_pages(q, bounds, bound_scales, block_table, query_start_loc, seq_lens, block_size, num_first,
                      num_last, max_seq_len, selected, error_word=None, stream=None):
     """q [T, Hq, d] bf16; bounds [nb, Hkv, 2, d] int8, bound_scales [nb, Hkv] float32; block_table [B, max_blocks]
     int32, query_start_loc [B + 1], seq_lens [B] int32; selected [T, Hkv, num_pages] int32: page indices, then -1."""
-    torch, device, address = _torch()
-    i32 = torch.int32
-    T, Hq, d = q.shape
-    nb, Hkv = bound_scales.shape
-    B, width = block_table.shape
-    pages = selected.shape[2]
-    _packed("pka_select_pages", device, ("q", q, torch.bfloat16, (T, Hq, d)),
-            ("bounds", bounds, torch.int8, (nb, Hkv, 2, d)), ("bound_scales", bound_scales, torch.float32, (nb, Hkv)),
-            ("block_table", block_table, i32, (B, width)), ("query_start_loc", query_start_loc, i32, (B + 1,)),
-            ("seq_lens", seq_lens, i32, (B,)), ("selected", selected, i32, (T, Hkv, pages)),
-            ("error_word", error_word, i32, (1,)))
-    st = load().pka_select_pages(q.data_ptr(), bounds.data_ptr(), bound_scales.data_ptr(), block_table.data_ptr(),
-                                 width, query_start_loc.data_ptr(), seq_lens.data_ptr(), B, T, Hq, Hkv, d, nb,
-                                 block_size, num_first, num_last, max_seq_len, pages, selected.data_ptr(),
-                                 _addr(error_word), address(stream))
-    _check(st, "pka_select_pages")
+    _check(_calls().select_pages(q, bounds, bound_scales, block_table, query_start_loc, seq_lens, block_size,
+                                 num_first, num_last, max_seq_len, selected, error_word, stream), "pka_select_pages")
 
 
 def pka_sparse_attn_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, selected, scale, max_seq_len,
                             out, lse, kv_scales=None, error_word=None, stream=None):
     """q, out [T, Hq, d] bf16, lse [T, Hq] float32 or None; caches [nb, Hkv, bs, d] bf16, or uint8 E4M3 codes with
     kv_scales=(k_scale, v_scale); selected [T, Hkv, num_pages] int32 as pka_select_pages writes it."""
-    torch, device, address = _torch()
-    i32, bf16, where = torch.int32, torch.bfloat16, "pka_sparse_attn_forward"
-    T, Hq, d = rows = q.shape
-    nb, Hkv, bs, _ = k_cache.shape
-    B, width = block_table.shape
-    pages = selected.shape[2]
-    kind, caches = bf16 if kv_scales is None else torch.uint8, (nb, Hkv, bs, d)
-    _packed(where, device, ("q", q, bf16, rows), ("k_cache", k_cache, kind, caches),
-            ("v_cache", v_cache, kind, caches), ("block_table", block_table, i32, (B, width)),
-            ("query_start_loc", query_start_loc, i32, (B + 1,)), ("seq_lens", seq_lens, i32, (B,)),
-            ("selected", selected, i32, (T, Hkv, pages)), ("out", out, bf16, rows),
-            ("lse", lse, torch.float32, (T, Hq)), ("error_word", error_word, i32, (1,)))
-    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), width,
-            query_start_loc.data_ptr(), seq_lens.data_ptr(), B, T, Hq, Hkv, d, nb, bs, float(scale))
-    tail = (selected.data_ptr(), pages, max_seq_len, out.data_ptr(), _addr(lse), _addr(error_word), address(stream))
-    if kv_scales is None:
-        st = load().pka_sparse_attn_forward(*args, *tail)
-    else:
-        st = load().pka_sparse_attn_forward_fp8(*args, float(kv_scales[0]), float(kv_scales[1]), *tail)
-    _check(st, where)
+    _check(_calls().sparse_attn_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, selected, scale,
+                                        max_seq_len, out, lse, kv_scales, error_word, stream),
+           "pka_sparse_attn_forward")
 
 
 def pka_selftest_wait(arrive: bool, limit_us: int, stream=None) -> int:

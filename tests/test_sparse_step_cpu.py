@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from paged_kv_attention_07_gb300 import build as B
 from paged_kv_attention_07_gb300 import pka
@@ -133,6 +134,17 @@ ATTN = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, width=64, qsl=FAKE, seq=FAKE, B=2
 def test_sparse_attn_refuses(lib, kw, status):
     assert _call(lib.pka_sparse_attn_forward, ATTN_ORDER + ATTN_TAIL, ATTN, kw) == status
     assert _call(lib.pka_sparse_attn_forward_fp8, ATTN_ORDER + " k_scale v_scale" + ATTN_TAIL, ATTN, kw) == status
+
+
+def test_calls_with_tensors_refuse_what_they_cannot_read(lib):
+    # (RuntimeError where there is no device at all)
+    t = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
+    with pytest.raises((ValueError, RuntimeError)):
+        pka.pka_page_bounds(t, t, t, t)
+    with pytest.raises((TypeError, RuntimeError)):
+        pka.pka_page_bounds(None, 3, "bounds", [])
+    with pytest.raises(TypeError):
+        pka._calls().page_bounds(t, t)
 
 
 BIG = (1 << 31) - 1
