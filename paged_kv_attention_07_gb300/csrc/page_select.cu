@@ -163,11 +163,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
     }
     __syncthreads();
     // a tile's records as A fragments: rows lane / 4 and 8 more, piece lane % 4 of each span
-    struct Tile {
-        uint4 rec[2][kSpans];
-        float scale[2];
+    struct Rows {
+        const uint4* src;
+        float scale;
     };
-    auto load = [&](Tile& x, int tile) {
+    auto locate = [&](Rows (&x)[2], int tile) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int i = tile * 16 + half * 8 + (lane >> 2);
@@ -178,16 +178,22 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
                 id = 0;
             }
             const int64_t page = (int64_t)id * p.Hkv + g;
-            const uint4* src = reinterpret_cast<const uint4*>(p.bounds + page * 2 * D) + (lane & 3);
-#pragma unroll
-            for (int s = 0; s < kSpans; ++s) x.rec[half][s] = __ldg(src + s * 4);
-            x.scale[half] = ok ? __ldg(p.scales + page) : -INFINITY;
+            x[half].src = reinterpret_cast<const uint4*>(p.bounds + page * 2 * D) + (lane & 3);
+            x[half].scale = ok ? __ldg(p.scales + page) : -INFINITY;
         }
         __syncwarp();  // (the ids' places are written by the scores only after all lanes have read them)
     };
     const int tile0 = first + warp;
-    Tile now;
-    if (tile0 < tiles_end) load(now, tile0);
+    uint4 rec[2][kSpans];
+    Rows now[2];
+    if (tile0 < tiles_end) {
+        locate(now, tile0);
+#pragma unroll
+        for (int s = 0; s < kSpans; ++s) {
+            rec[0][s] = __ldg(now[0].src + s * 4);
+            rec[1][s] = __ldg(now[1].src + s * 4);
+        }
+    }
 
     // ---- the queries' codes
 #pragma unroll
@@ -239,13 +245,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
     };
     if (ncta > 1) cluster_wait();
 
-    // ---- scores
+    // ---- scores; a span's registers take the next tile's as soon as it is multiplied
     uint32_t lo = 0xffffffffu, hi = 0u;
-    auto score = [&](const Tile& x, int tile) {
+    for (int tile = tile0; tile < tiles_end; tile += C::kWarps) {
+        const bool more = tile + C::kWarps < tiles_end;
+        Rows next[2] = {};
+        if (more) locate(next, tile + C::kWarps);
         float c[NT][2][4] = {};
 #pragma unroll
         for (int s = 0; s < kSpans; ++s) {
-            const uint4 a = x.rec[0][s], b = x.rec[1][s];
+            const uint4 a = rec[0][s], b = rec[1][s];
             const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
             uint32_t f[4][4];  // 1152 + code, f16 pairs
 #pragma unroll
@@ -264,6 +273,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
                 for (int j = 0; j < 4; ++j)
                     mma_f16(c[nt][j >> 1], f[j][0], f[j][1], f[j][2], f[j][3], q[2 * j], q[2 * j + 1]);
             }
+            if (more) {
+                rec[0][s] = __ldg(next[0].src + s * 4);
+                rec[1][s] = __ldg(next[1].src + s * 4);
+            }
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -274,11 +287,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
                 for (int j = 0; j < 2; ++j)
                     if (nt * 8 + 2 * (lane & 3) + j < p.G)
                         v = fmaxf(v, ((c[nt][0][half * 2 + j] - zero[nt][j][0]) + (c[nt][1][half * 2 + j] - zero[nt][j][1])) *
-                                         x.scale[half] * unit[nt][j]);
+                                         now[half].scale * unit[nt][j]);
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
             // a page that bounds nothing (scale +inf) comes first, one that does not exist last
-            if (fabsf(x.scale[half]) == INFINITY) v = x.scale[half];
+            if (fabsf(now[half].scale) == INFINITY) v = now[half].scale;
             const int i = tile * 16 + half * 8 + (lane >> 2);
             if (i < m) {
                 const uint32_t k = order_key(v);
@@ -286,11 +299,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
                 hi = max(hi, k);
                 if ((lane & 3) == 0) store_cluster(&s_key[i], 0, k);
             }
+            now[half].scale = next[half].scale;
         }
-    };
-    for (int tile = tile0; tile < tiles_end; tile += C::kWarps) {
-        score(now, tile);
-        if (tile + C::kWarps < tiles_end) load(now, tile + C::kWarps);
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
