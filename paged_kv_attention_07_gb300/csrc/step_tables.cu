@@ -10,14 +10,15 @@
 // Two prefix sums over at most kMaxRequests requests, then one search and write
 // per token. The bytes are few (12 per token), so the cost is latency and, with
 // many tokens, instructions: a warp takes a contiguous run of tokens and starts
-// each search where the last one ended (300 requests with 67214 tokens 8.2 us,
-// 11.4 us with a search of its own for every token; 48 requests with one token
-// each 3.9 us). One launch of one cluster. Every CTA of the cluster repeats the
-// prefix sums in its own shared memory (a few kilobytes from L2) and writes its
-// share of the tokens and pages; the page of a token on a new page comes from
-// the free list itself, not from the table entry another CTA writes. The
-// cluster barrier separates the reads of the list's head from its update, so
-// the head can be advanced in place.
+// each search where the last one ended (300 requests with 67214 tokens on 8 CTAs
+// 8.2 us, 11.4 us with a search of its own for every token; 48 requests with one
+// token each 3.7 us). Every CTA repeats the prefix sums in its own shared memory
+// (a few kilobytes from L2) and writes its share of the tokens and pages; the
+// page of a token on a new page comes from the free list itself, not from the
+// table entry another CTA writes. So no CTA waits for another, but where the
+// list's head is advanced in place: then one cluster, whose barrier separates
+// the reads of the head from its update (67214 tokens 8.2 us, 5.0 us
+// otherwise).
 #include "common.cuh"
 #include "params.cuh"
 #include "plan.cuh"
@@ -28,9 +29,8 @@ namespace {
 
 constexpr int kStThreads = 1024;
 constexpr int kStBatch = 4;  // tokens of a thread in flight
-// Tokens from which the writes are spread over a cluster of kStCluster CTAs.
-constexpr int kStCluster = 8;
-constexpr int64_t kStClusterTokens = 4096;
+constexpr int kStCluster = 8;  // CTAs at most, where the head is advanced in place
+constexpr int kStCtas = 128;   // and where it is not
 
 // x / bs: a shift where the page size is a power of two (log2 >= 0).
 PKA_DEVICE int page_of(uint32_t x, int bs, int log2) { return (int)(log2 >= 0 ? x >> log2 : x / (uint32_t)bs); }
@@ -212,8 +212,11 @@ cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream) {
                                                    (int)sizeof(int32_t) * 3 * kMaxRequests);
         if (e != cudaSuccess) return e;
     }
-    const int n = p.num_tokens >= kStClusterTokens ? kStCluster : 1;
-    return launch_cluster(step_tables_kernel, dim3(n), dim3(kStThreads), smem, n, stream, p);
+    // a token per thread, up to the CTAs there may be; in place, a cluster from some tokens on
+    const bool in_place = p.free_head == p.free_head_out;
+    const int64_t ctas = (p.num_tokens + kStThreads - 1) / kStThreads;
+    const int n = in_place ? (ctas < 4 ? 1 : kStCluster) : (int)std::max<int64_t>(1, std::min<int64_t>(ctas, kStCtas));
+    return launch_cluster(step_tables_kernel, dim3(n), dim3(kStThreads), smem, in_place ? n : 1, stream, p);
 }
 
 }  // namespace pka

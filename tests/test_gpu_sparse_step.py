@@ -89,6 +89,15 @@ def test_step_tables_takes_all_or_nothing(change, bit):
     assert not s["qsl"].any() and not s["seq"].any() and (s["slots"] == -1).all() and (s["pos"] == -1).all()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_step_tables_takes_nothing_on_many_ctas(in_place):
+    ctx, new = [700] * 30, [400] * 30
+    s, table0 = tables_case(ctx, new, 16, 12100, list(range(100)), 3, in_place=in_place)  # needs 750 pages
+    assert int(s["err"]) == E["CAPACITY"] and int(s["head_out"]) == 3
+    assert np.array_equal(s["table"].cpu().numpy(), table0)
+    assert not s["qsl"].any() and not s["seq"].any() and (s["slots"] == -1).all() and (s["pos"] == -1).all()
+
+
 # ---------------------------------------------------------------- norm, rotation, cache write
 
 
