@@ -12,12 +12,12 @@
 // many tokens, instructions: a warp takes a contiguous run of tokens and starts
 // each search where the last one ended (300 requests with 67214 tokens on 8 CTAs
 // 8.2 us, 11.4 us with a search of its own for every token; 48 requests with one
-// token each 3.7 us). Every CTA repeats the prefix sums in its own shared memory
+// token each 3.3 us). Every CTA repeats the prefix sums in its own shared memory
 // (a few kilobytes from L2) and writes its share of the tokens and pages; the
 // page of a token on a new page comes from the free list itself, not from the
 // table entry another CTA writes. So no CTA waits for another, but where the
 // list's head is advanced in place: then one cluster, whose barrier separates
-// the reads of the head from its update (67214 tokens 8.2 us, 5.0 us
+// the reads of the head from its update (67214 tokens 8.2 us, 5.1 us
 // otherwise).
 #include "common.cuh"
 #include "params.cuh"
@@ -27,7 +27,9 @@ namespace pka {
 
 namespace {
 
-constexpr int kStThreads = 1024;
+// Threads of a CTA: few for a decode step of few requests (one each), else enough
+// for kMaxRequests at a handful each (48 requests 3.3 us, 3.7 us with 1024).
+constexpr int kStFew = 256, kStMany = 1024;
 constexpr int kStBatch = 4;  // tokens of a thread in flight
 constexpr int kStCluster = 8;  // CTAs at most, where the head is advanced in place
 constexpr int kStCtas = 128;   // and where it is not
@@ -46,12 +48,16 @@ PKA_DEVICE int last_at_most(const int32_t* first, int lo, int hi, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParams p) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) step_tables_kernel(StepTablesParams p) {
+    constexpr int kWarps = kThreads / 32;
+    constexpr int kPer = kThreads == kStFew ? 1 : kMaxRequests / kThreads;  // requests of a thread, at most
+    static_assert(kWarps <= 32 && (kThreads == kStFew || kPer * kThreads == kMaxRequests), "");
     extern __shared__ int32_t s_req[];
     int32_t* s_qsl = s_req;                   // first token of each request
     int32_t* s_first = s_qsl + p.num_reqs;    // pages taken by the requests before it
     int32_t* s_ctx = s_first + p.num_reqs;    // its cached tokens
-    __shared__ long long s_tok[33], s_pag[33];
+    __shared__ long long s_tok[kWarps + 1], s_pag[kWarps + 1];
     grid_dep_launch();
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -61,11 +67,10 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
     const long long longest = (long long)p.max_blocks * bs;
 
     // ---- lengths: validate, sum, scan (each thread a contiguous run of requests)
-    const int per = (B + kStThreads - 1) / kStThreads;  // <= kMaxRequests / kStThreads
+    const int per = (B + kThreads - 1) / kThreads;  // <= kPer
     const int r0 = min(B, tid * per), r1 = min(B, r0 + per);
     int err = 0;
     long long tok = 0, pag = 0;
-    constexpr int kPer = kMaxRequests / kStThreads;
     int nw[kPer], nd[kPer], cl[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -99,7 +104,7 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
     }
     __syncthreads();
     if (warp == 0) {
-        const long long a = s_tok[lane], b = s_pag[lane];
+        const long long a = lane < kWarps ? s_tok[lane] : 0, b = lane < kWarps ? s_pag[lane] : 0;
         long long ai = a, bi = b;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -109,15 +114,17 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
                 bi += y;
             }
         }
-        s_tok[lane] = ai - a;
-        s_pag[lane] = bi - b;
+        if (lane < kWarps) {
+            s_tok[lane] = ai - a;
+            s_pag[lane] = bi - b;
+        }
         if (lane == 31) {
-            s_tok[32] = ai;
-            s_pag[32] = bi;
+            s_tok[kWarps] = ai;
+            s_pag[kWarps] = bi;
         }
     }
     __syncthreads();
-    const long long total = s_tok[32], taken = s_pag[32];
+    const long long total = s_tok[kWarps], taken = s_pag[kWarps];
     if (total > p.num_tokens) err |= PKA_DEVERR_QUERY_START_LOC;
     if (head < 0 || taken > (long long)p.num_free - head) err |= PKA_DEVERR_CAPACITY;
     const int any = __syncthreads_or(err);
@@ -126,12 +133,12 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
         // nothing is taken: empty requests and no slots, so that the calls
         // that read these tables write and read nothing
         if (err) set_error(p.err, err);
-        for (int r = cta * kStThreads + tid; r < B; r += ncta * kStThreads) {
+        for (int r = cta * kThreads + tid; r < B; r += ncta * kThreads) {
             p.qsl[r + 1] = 0;
             p.seq_lens[r] = 0;
         }
         if (cta == 0 && tid == 0) p.qsl[0] = 0;
-        for (int64_t t = (int64_t)cta * kStThreads + tid; t < p.num_tokens; t += (int64_t)ncta * kStThreads) {
+        for (int64_t t = (int64_t)cta * kThreads + tid; t < p.num_tokens; t += (int64_t)ncta * kThreads) {
             if (p.positions) p.positions[t] = -1;
             p.slots[t] = -1;
         }
@@ -156,13 +163,13 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
         __syncthreads();
         const int32_t* list = p.free_pages + head;
         // ---- the new pages' table entries
-        for (int j = cta * kStThreads + tid; j < (int)taken; j += ncta * kStThreads) {
+        for (int j = cta * kThreads + tid; j < (int)taken; j += ncta * kThreads) {
             const int r = last_at_most(s_first, 0, B - 1, j);
             const int held = pages_of(s_ctx[r], bs, log2);
             p.block_table[(int64_t)r * p.max_blocks + held + (j - s_first[r])] = list[j];
         }
         // ---- the tokens: 32 neighbours at a time, kStBatch times, so that their table loads overlap
-        const int nwarps = ncta * (kStThreads / 32), me = cta * (kStThreads / 32) + warp;
+        const int nwarps = ncta * (kThreads / 32), me = cta * (kThreads / 32) + warp;
         const int rounds = (int)((p.num_tokens + 31) / 32);  // (num_tokens <= INT32_MAX)
         const int i0 = (int)((int64_t)rounds * me / nwarps), i1 = (int)((int64_t)rounds * (me + 1) / nwarps);
         const int last = (int)total - 1;
@@ -205,18 +212,24 @@ __global__ void __launch_bounds__(kStThreads) step_tables_kernel(StepTablesParam
 
 }  // namespace
 
-cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream) {
+template <int kThreads>
+static cudaError_t go(const StepTablesParams& p, cudaStream_t stream) {
+    auto kern = step_tables_kernel<kThreads>;
     const size_t smem = sizeof(int32_t) * 3 * (size_t)p.num_reqs;
     if (smem > 47 * 1024) {  // past what every kernel may use; the most that any call takes
-        const cudaError_t e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)sizeof(int32_t) * 3 * kMaxRequests);
         if (e != cudaSuccess) return e;
     }
     // a token per thread, up to the CTAs there may be; in place, a cluster from some tokens on
     const bool in_place = p.free_head == p.free_head_out;
-    const int64_t ctas = (p.num_tokens + kStThreads - 1) / kStThreads;
+    const int64_t ctas = (p.num_tokens + kThreads - 1) / kThreads;
     const int n = in_place ? (ctas < 4 ? 1 : kStCluster) : (int)std::max<int64_t>(1, std::min<int64_t>(ctas, kStCtas));
-    return launch_cluster(step_tables_kernel, dim3(n), dim3(kStThreads), smem, in_place ? n : 1, stream, p);
+    return launch_cluster(kern, dim3(n), dim3(kThreads), smem, in_place ? n : 1, stream, p);
+}
+
+cudaError_t launch_step_tables(const StepTablesParams& p, cudaStream_t stream) {
+    return p.num_reqs <= kStFew && p.num_tokens <= 4 * kStFew ? go<kStFew>(p, stream) : go<kStMany>(p, stream);
 }
 
 }  // namespace pka

@@ -67,6 +67,13 @@ def test_step_tables(B, bs, longest, most, pad, in_place):
         assert int(s["head"]) == head
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,most,pad", [
+    (255, 1, 0), (256, 1, 0), (256, 6, 5), (257, 1, 0), (31, 50, 0), (256, 8, 0), (2, 511, 3)])
+def test_step_tables_at_the_sizes_of_a_cta(B, most, pad, in_place):
+    test_step_tables(B, 16, 100, most, pad, in_place)
+
+
 def test_step_tables_negative_page_ids_have_no_slots():
     ctx, new, bs = [5, 8], [4, 2], 4
     s, table0 = tables_case(ctx, new, bs, 6, [-3, 11, 12], 0, positions=False)
