@@ -11,12 +11,15 @@
 //
 // The pages are found from the slot mapping alone: a page is filled by the
 // token that goes to its last slot. A CTA looks at the slots of `chunk` tokens
-// with one load per warp and takes the filled pages of its kv head one after
-// another: 128 threads read a page in 16-byte pieces, all of a thread's pieces
-// in flight together, and keep minima and maxima as packed 16-bit pairs (bf16
-// as it is, codes widened to f16, exact). Bound by latency (a slot, a page, the
-// join) up to some thousand tokens, by HBM beyond: block_size x d elements
-// read per filled (page, kv head), 2 d + 4 bytes written.
+// with one load per warp and takes the filled pages of its kv head: its 128
+// threads together one after another, or, pages of up to 4 KB, each warp its
+// own (256 decodes over an 8-bit cache, pages of 2 KB: 2.9 us, 3.9 us with all
+// threads on each; 16384 tokens in pages of 4 KB: 7.1 us, 9.0 us). A page is
+// read in 16-byte pieces, all of a thread's pieces in flight together, minima
+// and maxima are packed 16-bit pairs (bf16 as it is, codes widened to f16,
+// exact). Bound by latency (a slot, a page, the join) up to some thousand
+// tokens, by HBM beyond: block_size x d elements read per filled (page, kv
+// head), 2 d + 4 bytes written (16384 tokens in pages of 16 KB: 5.2 us, 3.3 TB/s).
 #include "common.cuh"
 #include "params.cuh"
 
@@ -27,6 +30,7 @@ namespace {
 constexpr int kPbThreads = 128;
 constexpr int kPbWarps = kPbThreads / 32;
 constexpr int kPbBatch = 8;  // 16-byte pieces per thread in flight
+constexpr int64_t kPbWarpBytes = 32 * kPbBatch * 16;  // a page that one warp holds
 
 // Packed pairs: bf16, or f16 of codes. NaN wins over any value.
 template <bool kFp8>
@@ -43,25 +47,28 @@ PKA_DEVICE uint32_t max2(uint32_t a, uint32_t b) {
     else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+PKA_DEVICE uint16_t two(float x, float y) { return (uint16_t)((uint8_t)(int8_t)(int)x | (uint8_t)(int8_t)(int)y << 8); }
 template <bool kFp8>
 PKA_DEVICE float2 pair(uint32_t x) {
     return kFp8 ? __half22float2(h2(x)) : make_float2(bf16_lo(x), bf16_hi(x));
 }
 
-template <bool kFp8>
+// kWarp: a page per warp instead of a page per CTA.
+template <bool kFp8, bool kWarp>
 __global__ void __launch_bounds__(kPbThreads) page_bounds_kernel(PageBoundsParams p) {
+    constexpr int kLanes = kWarp ? 32 : kPbThreads;  // on a page
     constexpr int kVec = kFp8 ? 16 : 8;  // elements of a 16-byte piece
     constexpr int kWords = kVec / 2;     // and their packed pairs
     constexpr uint32_t kInf = kFp8 ? 0x7c007c00u : 0x7f807f80u, kMinusInf = kInf | 0x80008000u;
-    __shared__ uint32_t s_lo[kPbWarps][64], s_hi[kPbWarps][64];  // head_dim / 2 pairs per warp
+    __shared__ uint32_t s_lo[kWarp ? 1 : kPbWarps][64], s_hi[kWarp ? 1 : kPbWarps][64];  // head_dim / 2 pairs per warp
     __shared__ float s_amax[2];
     grid_dep_launch();
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = blockIdx.y;
     const int pieces = p.head_dim / kVec;  // of a key: a power of two, 4 to 16
-    const int rows = kPbThreads / pieces;  // keys read side by side
-    const int c = tid % pieces, r0 = tid / pieces;
+    const int rows = kLanes / pieces;      // keys read side by side
+    const int c = tid % kLanes % pieces, r0 = tid % kLanes / pieces;
     for (int64_t t0 = (int64_t)blockIdx.x * p.chunk; t0 < p.num_tokens; t0 += (int64_t)gridDim.x * p.chunk) {
         // the pages that this chunk fills: one token per lane, the same in every warp
         int64_t blk = -1;
@@ -74,8 +81,10 @@ __global__ void __launch_bounds__(kPbThreads) page_bounds_kernel(PageBoundsParam
                 if (slot - b * p.block_size == p.block_size - 1) blk = b;
             }
         }
-        for (uint32_t todo = __ballot_sync(0xffffffffu, blk >= 0); todo; todo &= todo - 1) {
+        uint32_t todo = __ballot_sync(0xffffffffu, blk >= 0);
+        for (int turn = 0; todo; todo &= todo - 1, ++turn) {
             const int64_t page = __shfl_sync(0xffffffffu, blk, __ffs(todo) - 1) * p.Hkv + g;
+            if (kWarp && turn % kPbWarps != warp) continue;
             const uint8_t* src = static_cast<const uint8_t*>(p.k_cache) +
                                  (page * p.block_size * p.head_dim + c * kVec) * (kFp8 ? 1 : 2);
             const int64_t row = (int64_t)p.head_dim * (kFp8 ? 1 : 2);
@@ -117,6 +126,37 @@ __global__ void __launch_bounds__(kPbThreads) page_bounds_kernel(PageBoundsParam
                     hi[i] = max2<kFp8>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
                 }
             }
+            if constexpr (kWarp) {  // the elements of piece c, in every lane that reads it
+                float a = 0.f;
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    const float2 l = pair<kFp8>(lo[i]), h = pair<kFp8>(hi[i]);
+                    a = fmaxf(a, fmaxf(fmaxf(-l.x, h.x), fmaxf(-l.y, h.y)));
+                    if (isnan(l.x) || isnan(l.y)) a = INFINITY;
+                }
+                for (int o = 1; o < pieces; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                const bool none = a == INFINITY;
+                const int e = none ? 0 : bound_exponent(a);
+                const float unit = none ? 0.f : exp2i(-e);
+                if (lane < pieces) {
+                    uint16_t codes[2][kWords];
+#pragma unroll
+                    for (int i = 0; i < kWords; ++i) {
+                        const float2 l = pair<kFp8>(lo[i]), h = pair<kFp8>(hi[i]);
+                        codes[0][i] = none ? 0 : two(floorf(l.x * unit), floorf(l.y * unit));
+                        codes[1][i] = none ? 0 : two(ceilf(h.x * unit), ceilf(h.y * unit));
+                    }
+                    uint2* dst = reinterpret_cast<uint2*>(p.bounds + page * 2 * p.head_dim + c * kVec);
+#pragma unroll
+                    for (int i = 0; i < kWords / 4; ++i) {
+                        auto four = [&](const uint16_t* x) { return make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16); };
+                        dst[i] = four(codes[0] + 4 * i);
+                        dst[i + p.head_dim / 8] = four(codes[1] + 4 * i);
+                    }
+                    if (lane == 0) p.scales[page] = none ? INFINITY : exp2i(e);
+                }
+                continue;
+            }
             __syncthreads();  // the last page's results have been read
             if (lane < pieces) {
 #pragma unroll
@@ -151,7 +191,6 @@ __global__ void __launch_bounds__(kPbThreads) page_bounds_kernel(PageBoundsParam
             const int e = none ? 0 : bound_exponent(a);
             const float unit = none ? 0.f : exp2i(-e);
             if (tid < pairs) {
-                auto two = [](float x, float y) { return (uint16_t)((uint8_t)(int8_t)(int)x | (uint8_t)(int8_t)(int)y << 8); };
                 uint16_t* code = reinterpret_cast<uint16_t*>(p.bounds + page * 2 * p.head_dim);
                 code[tid] = none ? 0 : two(floorf(l.x * unit), floorf(l.y * unit));
                 code[pairs + tid] = none ? 0 : two(ceilf(h.x * unit), ceilf(h.y * unit));
@@ -170,8 +209,10 @@ cudaError_t launch_page_bounds(PageBoundsParams p, bool fp8, int num_sms, cudaSt
     while (p.chunk > 4 && (p.num_tokens + p.chunk - 1) / p.chunk * p.Hkv < num_sms) p.chunk /= 2;
     const int64_t chunks = (p.num_tokens + p.chunk - 1) / p.chunk;
     const dim3 grid((unsigned)std::min<int64_t>(chunks, 1 << 20), (unsigned)p.Hkv);
-    return fp8 ? launch_dependent(page_bounds_kernel<true>, grid, dim3(kPbThreads), 0, stream, p)
-               : launch_dependent(page_bounds_kernel<false>, grid, dim3(kPbThreads), 0, stream, p);
+    const bool small = (int64_t)p.block_size * p.head_dim * (fp8 ? 1 : 2) <= kPbWarpBytes;
+    auto go = [&](auto kern) { return launch_dependent(kern, grid, dim3(kPbThreads), 0, stream, p); };
+    if (small) return fp8 ? go(page_bounds_kernel<true, true>) : go(page_bounds_kernel<false, true>);
+    return fp8 ? go(page_bounds_kernel<true, false>) : go(page_bounds_kernel<false, false>);
 }
 
 }  // namespace pka
