@@ -15,11 +15,13 @@
 // One warp scores 16 pages: it loads their 16 records (2 d bytes each) straight
 // into the fragments of the product. The block ids of the CTA's pages are
 // fetched together beforehand, into the places where the scores will go: the
-// chain id -> record costs the time. Other warps hide a tile's loads: a second
-// tile in registers costs more in resident CTAs than it gains (96 requests of
-// 4096 to 65536 tokens, 8 kv heads: 27.6 us, 30.0 us with two tiles; records by
-// asynchronous copies 28.4 us, by one bulk copy each 39 us, bound by the rate
-// at which an SM takes copies; int8 products 39 us).
+// chain id -> record costs the time. A tile's registers take the next tile's
+// records span by span as they are multiplied (96 requests of 4096 to 65536 tokens,
+// 8 kv heads: 25.4 us, 2.77 TB/s; 27.7 us with the loads behind the products. Slower
+// before that change: two whole tiles in registers 30.0 us, records by asynchronous
+// copies 28.4, by one bulk copy each 39, bound by the rate at which an SM takes
+// copies; int8 products 39 us. Contexts of one length, 95 requests of 23000 tokens,
+// leave no SM waiting for another's long one: 17.1 us, 4.2 TB/s).
 //
 // The product runs on the f16 tensor cores: an int8 MMA takes 65 cycles here
 // and two f16 ones of half its length 16. A code c becomes the f16 number
@@ -47,6 +49,7 @@ namespace pka {
 namespace {
 
 constexpr int kBatch = 4;  // keys of a thread read together
+constexpr int kCtaTiles = 4;  // of 16 pages: a CTA of a cluster takes part with these at least
 
 template <int D, int NT, int kThreads>
 struct PsCfg {
@@ -140,16 +143,22 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
     int32_t* out = p.sel + ((int64_t)t * p.Hkv + g) * p.num_pages;
     const int K = p.num_pages;
     const int nf = p.num_first, m = n - nf - p.num_last, want = K - nf - p.num_last;
+    const int tiles = (m + 15) / 16;
+    // CTAs that take part: the token's first `parts` of the cluster
+    const uint32_t parts = (uint32_t)max(1, min((int)ncta, tiles / kCtaTiles));
     if (n <= K || want == 0) {  // all pages, or only those that are always read
         for (int i = cta * kThreads + tid; i < K; i += ncta * kThreads) out[i] = i >= n ? -1 : n <= K || i < nf ? i : n - K + i;
         if (ncta > 1) cluster_wait();
         return;
     }
+    if (cta >= parts) {
+        cluster_wait();
+        return;
+    }
 
     // ---- this warp's tiles of 16 candidates [nf, nf + m): records and block ids ahead
     const int32_t* bt = p.block_table + (int64_t)r * p.max_blocks + nf;
-    const int tiles = (m + 15) / 16;
-    const int first = (int)((uint32_t)tiles * cta / ncta), tiles_end = (int)((uint32_t)tiles * (cta + 1) / ncta);
+    const int first = (int)((uint32_t)tiles * cta / parts), tiles_end = (int)((uint32_t)tiles * (cta + 1) / parts);
     {
         const int i1 = min(m, tiles_end * 16);
         for (int i0 = first * 16 + tid; i0 < i1; i0 += kBatch * kThreads) {
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
         min_cluster(&s_min, 0, lo);
         max_cluster(&s_max, 0, hi);
     }
-    if (ncta == 1) __syncthreads();
+    if (parts == 1) __syncthreads();
     else cluster_barrier();
     if (cta != 0) return;
 
@@ -428,11 +437,21 @@ cudaError_t go(const PageSelectParams& p, int cluster, cudaStream_t stream) {
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream) {
     const int pages = (p.max_seq_len - 1) / p.block_size + 1;
     const int64_t units = (int64_t)p.num_tokens * p.Hkv;
-    // 256 threads per CTA score a few long contexts faster, 128 keep more of many
-    // CTAs resident (96 requests, 8 kv heads: 27.7 us, 32.1 us with 256)
-    const bool two = p.G > 8, wide = units < num_sms;
+    // All CTAs run at once where they can, each with as many warps as that leaves
+    // room for: CTAs of 256 threads (two per SM), in clusters, up to two units per
+    // SM; beyond that CTAs of 128 threads (five per SM), two to a unit up to three
+    // units per SM. Measured with 8 kv heads, contexts of 4096 to 65536 tokens, in
+    // clusters of 1 / 2 / 4 / 8:
+    //     requests   256 threads                 128 threads
+    //        4        9.2 / 7.9 / 7.4 / 7.2      12.2 / 9.1 / 7.9 / 7.5 us
+    //       16       11.8 / 10.1 / 11.9 / 15.7   13.5 / 11.0 / 10.0 / 10.4
+    //       32       12.6 / 16.3 / 20.6 / 29.7   17.7 / 14.4 / 13.0 / 16.0
+    //       48       18.7 / 21.6 / 29.0 / 43.1   22.9 / 15.8 / 17.6 / 22.3
+    //       96       29.3 / 44.0 / 64.5 / 107    25.4 / 26.6 / 33.3 / 43.8
+    const bool two = p.G > 8, wide = units <= 2 * num_sms;
     int n = 1;
-    while (n < 8 && units * n < num_sms && pages > n * 128) n *= 2;
+    while (wide && n < 8 && units * n <= num_sms && pages > n * 16 * kCtaTiles) n *= 2;
+    if (!wide && units <= 3 * num_sms && pages > 16 * kCtaTiles) n = 2;
     auto by_width = [&](auto d, auto nt) {
         return wide ? go<decltype(d)::value, decltype(nt)::value, 256>(p, n, stream)
                     : go<decltype(d)::value, decltype(nt)::value, 128>(p, n, stream);
