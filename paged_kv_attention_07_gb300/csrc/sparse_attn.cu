@@ -36,8 +36,8 @@
 // with q and P as two e4m3 numbers each, need no conversions but twice the
 // products: 24 x 4 tokens 36 us, 27 us this way.)
 //
-// Measured: 96 requests, 4 kv heads, 64 pages of 64 tokens each, bf16: 120 us, 6.66
-// TB/s; 8-bit: 68 us, 5.93 TB/s. One request of 8 kv heads, bf16: 9.6 us, of
+// Measured: 96 requests, 4 kv heads, 64 pages of 64 tokens each, bf16: 119 us, 6.7
+// TB/s; 8-bit: 67 us, 5.97 TB/s. One request of 8 kv heads, bf16: 9.7 us, of
 // which 5 are the chain place -> list -> block table -> tile and the join.
 #include "common.cuh"
 #include "params.cuh"
@@ -488,10 +488,9 @@ cudaError_t go(const SparseAttnParams& p, int num_sms, cudaStream_t stream) {
     // CTAs per (token, kv head): more of them shorten each one's run of tiles but
     // each costs a start of about kStart tiles; up to the resident CTAs they all
     // run at once, beyond that in turns, with half a turn's idling at the end.
-    // Measured at 384 units: bf16, 64 tiles per warp, with 1 / 2 / 4 / 8 CTAs
-    // 133 / 120 / 132 / 147 us; 8-bit (e4m3 products), 16 tiles per warp, 1 / 2 / 4
-    // CTAs 36 / 40 / 49 us; one request's 8 units, bf16, 1 / 2 / 4 / 8 / 16 CTAs 40 / 23 / 14 / 9.9 /
-    // 10.2 us.
+    // Measured with 1 / 2 / 4 / 8 CTAs: 384 units, bf16, 64 tiles per warp
+    // 125 / 120 / 131 / 145 us; 8-bit, 16 tiles per warp 27 / 33 / 41 / 68 us; 64 units,
+    // bf16 37 / 27 / 25 / 31 us; 8 units 31 / 18 / 12 / 9.7 us (16 CTAs: no faster).
     constexpr int64_t kStart = 5;
     const int64_t units = (int64_t)p.num_tokens * p.Hkv, slots = (int64_t)num_sms * C::kMinBlocks;
     const int64_t tiles = ((int64_t)p.num_pages * p.bs + C::kTile * kSaWarps - 1) / (C::kTile * kSaWarps);
