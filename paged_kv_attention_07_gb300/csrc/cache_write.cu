@@ -40,6 +40,10 @@ struct CacheWriteParams {
     int32_t* err;
 };
 
+// The codes of x / s, the quotient rounded to float32 first.
+PKA_DEVICE uint32_t quantize4(float a, float b, float c, float d, float s) {
+    return e4m3x4(__fdiv_rn(a, s), __fdiv_rn(b, s), __fdiv_rn(c, s), __fdiv_rn(d, s));
+}
 PKA_DEVICE uint2 quantize8(uint4 x, float s) {
     uint2 r;
     r.x = quantize4(bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y), s);

@@ -297,8 +297,6 @@ PKA_DEVICE uint32_t e4m3x2_to_f16x2(uint32_t x16) {
     return d;
 }
 
-PKA_DEVICE __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
-
 // Four floats -> four E4M3 codes (RN-even, saturating), lowest first.
 PKA_DEVICE uint32_t e4m3x4(float a, float b, float c, float d) {
     uint32_t r;
@@ -307,10 +305,6 @@ PKA_DEVICE uint32_t e4m3x4(float a, float b, float c, float d) {
         : "=r"(r)
         : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
-}
-// The codes of x / s, the quotient rounded to float32 first.
-PKA_DEVICE uint32_t quantize4(float a, float b, float c, float d, float s) {
-    return e4m3x4(__fdiv_rn(a, s), __fdiv_rn(b, s), __fdiv_rn(c, s), __fdiv_rn(d, s));
 }
 
 // Two floats -> bf16x2 (round to nearest even); `lo` lands in the low half.
@@ -329,14 +323,6 @@ PKA_DEVICE void st_global_v8(void* p, uint32_t a0, uint32_t a1, uint32_t a2, uin
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a0), "r"(a1), "r"(a2),
                  "r"(a3), "r"(a4), "r"(a5), "r"(a6), "r"(a7)
                  : "memory");
-}
-
-// bf16 pair -> f16 pair (finite results saturate at the f16 maximum).
-PKA_DEVICE uint32_t bf16x2_to_f16x2(uint32_t w) {
-    uint32_t d;
-    const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
 }
 
 PKA_DEVICE uint32_t pack_f16(float lo, float hi) {

@@ -65,6 +65,14 @@ struct F8Cfg {
 PKA_DEVICE uint32_t e4m3_lo(uint32_t w) { return e4m3x2_to_f16x2(w & 0xffffu); }
 PKA_DEVICE uint32_t e4m3_hi(uint32_t w) { return e4m3x2_to_f16x2(w >> 16); }
 
+// bf16 pair -> f16 pair (finite results saturate at the f16 maximum).
+PKA_DEVICE uint32_t bf16x2_to_f16x2(uint32_t w) {
+    uint32_t d;
+    const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 }  // namespace
 
 // One decode work unit as a warp sees it. blk[0] / blk[1]: validated block

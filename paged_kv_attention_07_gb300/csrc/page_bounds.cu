@@ -47,6 +47,7 @@ PKA_DEVICE uint32_t max2(uint32_t a, uint32_t b) {
     else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+PKA_DEVICE __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 PKA_DEVICE uint16_t two(float x, float y) { return (uint16_t)((uint8_t)(int8_t)(int)x | (uint8_t)(int8_t)(int)y << 8); }
 template <bool kFp8>
 PKA_DEVICE float2 pair(uint32_t x) {

@@ -463,6 +463,16 @@ def test_select_pages_long_context_over_a_cluster(ctx, bs, Hkv):
     assert err == 0
 
 
+@pytest.mark.parametrize("B,Hkv,group", [(3, 2, 3), (20, 8, 1), (20, 8, 9), (45, 8, 1), (45, 8, 9), (60, 8, 2)])
+def test_select_pages_shares_of_a_cluster(B, Hkv, group):
+    # few units in clusters of wide CTAs, more in pairs, many alone; contexts from one page to all CTAs' worth
+    rng = np.random.default_rng(B + group)
+    ctx = np.exp(rng.uniform(0, np.log(5000), B)).astype(int)
+    ctx[:3] = 8 * 590, 8 * (64 + 3) - 1, 8 * (128 + 3)  # all CTAs; a page less than one CTA's share, two CTAs' share
+    b = batch(rng, ctx.tolist(), [1] * B, 8)
+    select_check(b, *select_case(rng, b, group * Hkv, Hkv, 64), 1, 2, 12)
+
+
 @pytest.mark.parametrize("d,Hq", [(64, 4), (128, 8), (128, 16)])
 def test_select_pages_sums_at_the_end_of_their_range(d, Hq):
     """Codes of 127 throughout but for single units: scores of 127 * 127 * d that differ by one are told apart."""
