@@ -102,6 +102,12 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
     // ---- the token's request and position (the same for the whole cluster)
     const int ncta = (int)cluster_size(), cta = (int)cluster_rank();
     const int g = blockIdx.y, t0 = (int)(blockIdx.x / (unsigned)ncta);
+    const int32_t* sel = p.sel + ((int64_t)t0 * p.Hkv + g) * p.num_pages;
+    int entry = -1, before = -1;  // this thread's first of the list, on its way meanwhile
+    if (tid < p.num_pages) {
+        entry = __ldg(sel + tid);
+        if (tid) before = __ldg(sel + tid - 1);
+    }
     const TokenPlace at = place_of(p.qsl, p.seq_lens, p.num_reqs, t0);
     if (at.r < 0) return;  // a row behind the last sequence
     const long long pos = (long long)at.len - at.q1 + t0;
@@ -113,13 +119,14 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
     const int64_t row0 = (int64_t)t0 * p.Hq + g * p.G;  // first output row
 
     // ---- the list: it ends at its first negative entry; entries ascend and none is past the own page
-    const int32_t* sel = p.sel + ((int64_t)t0 * p.Hkv + g) * p.num_pages;
-    for (int i = tid; i < p.num_pages; i += kSaThreads) {
-        const int e = __ldg(sel + i), before = i ? __ldg(sel + i - 1) : -1;
-        if (e <= before || e > own_page) {  // e < 0 among them
+    for (int i = tid; i < p.num_pages;) {
+        if (entry <= before || entry > own_page) {  // negative ones among them
             atomicMin(&s_stop, i);
             break;
         }
+        if ((i += kSaThreads) >= p.num_pages) break;
+        entry = __ldg(sel + i);
+        before = __ldg(sel + i - 1);
     }
     __syncthreads();
     const int count = s_stop;
