@@ -49,6 +49,7 @@ namespace pka {
 namespace {
 
 constexpr int kBatch = 4;  // keys of a thread read together
+constexpr uint32_t kFew = 32;  // pages in the border bin that are ranked one against all
 constexpr int kCtaTiles = 4;  // of 16 pages: a CTA of a cluster takes part with these at least
 
 template <int D, int NT, int kThreads>
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
     __shared__ float s_unit[NT * 8], s_zero[NT * 8][2];
     __shared__ uint32_t s_hist[kBins];
     __shared__ uint32_t s_warp[C::kWarps];
-    __shared__ uint32_t s_list[kThreads];
+    __shared__ uint2 s_list[kFew];  // key and page
     __shared__ uint32_t s_min, s_max, s_digit, s_above, s_inside, s_count;
     grid_dep_launch();
     grid_dep_wait();
@@ -208,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
 #pragma unroll
     for (int j = 0; j < kQHeads; ++j) {
         const int h = warp + j * C::kWarps;
+        if (h >= p.G) break;  // (the columns of other heads are not looked at)
         float a = 0.f;
 #pragma unroll
         for (int i = 0; i < kE; ++i) a = fabsf(x[j][i]) <= 3.4e38f ? fmaxf(a, fabsf(x[j][i])) : INFINITY;
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
     const uint32_t base = s_min;
     int bits = 32 - __clz(s_max - base);  // 0: all equal
     uint32_t border = 0, rank = want, inside = m;
-    while (bits > 0 && inside > kThreads) {
+    while (bits > 0 && inside > kFew) {
         const int shift = max(0, bits - kBinBits);
         for (int i0 = tid; i0 < m; i0 += kBatch * kThreads) {
             uint32_t k[kBatch];
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
     }
     // ---- a bit per candidate: above the border; inside it, either a short list
     // to rank one against all, or (all equal) the first ones
-    const bool few = inside <= kThreads;
+    const bool few = inside <= kFew;
     const int words = (m + 31) / 32;
     for (int w0 = warp; w0 < words; w0 += kBatch * C::kWarps) {
         uint32_t k[kBatch];
@@ -374,22 +376,22 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
             const uint32_t top = bits == 32 ? 0u : k[j] >> bits, edge = bits == 32 ? 0u : border >> bits;
             const uint32_t above = __ballot_sync(0xffffffffu, i < m && top > edge);
             if (lane == 0) s_bits[w] = above;
-            if (few && i < m && top == edge) s_list[atomicAdd(&s_count, 1u)] = i;
+            if (few && i < m && top == edge) s_list[atomicAdd(&s_count, 1u)] = make_uint2(k[j], i);
         }
     }
     __syncthreads();
     if (few) {
         if (tid < inside) {
-            const uint32_t i = s_list[tid], k = s_key[i];
+            const uint2 mine = s_list[tid];
             uint32_t better = 0;
             for (uint32_t j = 0; j < inside; ++j) {
-                const uint32_t o = s_list[j], ko = s_key[o];
-                better += ko > k || (ko == k && o < i);
+                const uint2 o = s_list[j];
+                better += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
             }
-            if (better < rank) atomicOr(&s_bits[i >> 5], 1u << (i & 31));
+            if (better < rank) atomicOr(&s_bits[mine.y >> 5], 1u << (mine.y & 31));
         }
     } else {
-        // more than a block of equal keys (bits == 0): by index, `rank` of them
+        // more than a few equal keys (bits == 0): by index, `rank` of them
         const int per = (m + kThreads - 1) / kThreads;
         const int i0 = min(m, tid * per), i1 = min(m, i0 + per);
         uint32_t equal = 0;
