@@ -16,7 +16,7 @@
 // owns a contiguous run of tiles and never waits for another: its lanes hold the
 // cache rows of its next 32 pages (list entry -> block table -> row), a tile's
 // rows are a shuffle away. The work of one (token, kv head) is split over the
-// 4 warps of a CTA and the CTAs of a cluster; the warps' (m, l, O) join in
+// 4 or 8 warps of a CTA and the CTAs of a cluster; the warps' (m, l, O) join in
 // shared memory and the CTAs' over distributed shared memory, so there is one
 // launch and nothing partial goes to memory.
 //
@@ -46,24 +46,23 @@ namespace pka {
 
 namespace {
 
-constexpr int kSaWarps = 4;
-constexpr int kSaThreads = kSaWarps * 32;
 constexpr int kSaJoin = 8;   // CTAs' results read together
 
-template <int D, int NT, bool kFp8>
+template <int D, int NT, bool kFp8, int kWarps>
 struct SaCfg {
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kTile = kFp8 ? 32 : 16;  // keys of a tile
     static constexpr int kOctets = kTile / 8;     // eight keys each, of one page
     static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
     static constexpr int kTileBytes = kTile * kRowBytes;
     static constexpr int kStageBytes = 2 * kTileBytes;  // K + V
     static constexpr int kStages = kFp8 ? 2 : 3;
-    static constexpr int kMinBlocks = kFp8 && NT == 1 ? 3 : 2;  // CTAs per SM
-    static constexpr int kRing = kSaWarps * kStages * kStageBytes;
+    static constexpr int kMinBlocks = kWarps == 8 ? 1 : kFp8 && NT == 1 ? 3 : 2;  // CTAs per SM
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kCols = NT * 8;
     // the join: each warp's m, l and O (over the ring), and the CTA's own
     static constexpr int kWarpFloats = kCols * (D + 2);
-    static constexpr int kJoin = kSaWarps * kWarpFloats * 4;
+    static constexpr int kJoin = kWarps * kWarpFloats * 4;
     static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
     static constexpr int kSmem = 1024 /*align*/ + kBody + kWarpFloats * 4;
 };
@@ -82,9 +81,11 @@ PKA_DEVICE void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
         : "r"(w));
 }
 
-template <int D, int NT, bool kFp8>
-__global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sparse_attn_kernel(const SparseAttnParams p) {
-    using C = SaCfg<D, NT, kFp8>;
+template <int D, int NT, bool kFp8, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, SaCfg<D, NT, kFp8, kWarps>::kMinBlocks)
+    sparse_attn_kernel(const SparseAttnParams p) {
+    using C = SaCfg<D, NT, kFp8, kWarps>;
+    constexpr int kThreads = C::kThreads;
     constexpr int kTile = C::kTile, kOctets = C::kOctets;
     constexpr int kMTiles = kTile / 16;  // of S^T: 16 keys each
     constexpr int kKSteps = D / 16;      // m-tiles of O^T (and k-steps of S^T over bf16)
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
             atomicMin(&s_stop, i);
             break;
         }
-        if ((i += kSaThreads) >= p.num_pages) break;
+        if ((i += kThreads) >= p.num_pages) break;
         entry = __ldg(sel + i);
         before = __ldg(sel + i - 1);
     }
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
     if (cta == 0 && tid == 0 && count < p.num_pages && __ldg(sel + count) >= 0) set_error(p.err, PKA_DEVERR_INDEX);
     if (count == 0) {  // nothing to read
         if (cta == 0) {
-            for (int i = tid; i < p.G * D / 8; i += kSaThreads)
+            for (int i = tid; i < p.G * D / 8; i += kThreads)
                 reinterpret_cast<uint4*>(p.out + row0 * D)[i] = make_uint4(0, 0, 0, 0);
             if (p.lse && tid < p.G) p.lse[row0 + tid] = -INFINITY;
         }
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
     const bool tail = __ldg(sel + count - 1) == own_page;
     const int keys = count * p.bs - (tail ? p.bs - 1 - ((int)pos & (p.bs - 1)) : 0);
     const int ntiles = (keys + kTile - 1) / kTile;
-    const int part = cta * kSaWarps + warp, parts = ncta * kSaWarps;
+    const int part = cta * kWarps + warp, parts = ncta * kWarps;
     // (parts is a power of two up to 64, ntiles below 2^31 / kTile)
     const int parts_log2 = 31 - __clz(parts);
     const int i0 = (ntiles >> parts_log2) * part + (((ntiles & (parts - 1)) * part) >> parts_log2);
@@ -425,14 +426,14 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
     __syncthreads();
     auto weight = [](float mw, float M) { return mw == -INFINITY ? 0.f : fast_exp2(mw - M); };
     const float* all = reinterpret_cast<const float*>(smem);
-    for (int it = tid; it < p.G * (D / 4); it += kSaThreads) {
+    for (int it = tid; it < p.G * (D / 4); it += kThreads) {
         const int hh = it / (D / 4), c = it % (D / 4) * 4;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kSaWarps; ++w) M = fmaxf(M, all[w * C::kWarpFloats + C::kCols * D + hh]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, all[w * C::kWarpFloats + C::kCols * D + hh]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kSaWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             const float* x = all + w * C::kWarpFloats;
             const float wt = weight(x[C::kCols * D + hh], M);
             const float4 v = *reinterpret_cast<const float4*>(x + hh * D + c);
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
     }
     if (ncta == 1) __syncthreads();
     else cluster_barrier();
-    for (int it = cta * kSaThreads + tid; it < p.G * (D / 4); it += ncta * kSaThreads) {
+    for (int it = cta * kThreads + tid; it < p.G * (D / 4); it += ncta * kThreads) {
         const int hh = it / (D / 4), c = it % (D / 4) * 4;
         // up to kSaJoin CTAs' parts in flight together
         float M = -INFINITY, L = 0.f;
@@ -486,42 +487,63 @@ __global__ void __launch_bounds__(kSaThreads, SaCfg<D, NT, kFp8>::kMinBlocks) sp
     if (ncta > 1) cluster_barrier();  // no CTA leaves while another reads its shared memory
 }
 
-template <int D, int NT, bool kFp8>
+template <int D, int NT, bool kFp8, int kWarps>
 cudaError_t go(const SparseAttnParams& p, int num_sms, cudaStream_t stream) {
-    using C = SaCfg<D, NT, kFp8>;
-    auto kern = sparse_attn_kernel<D, NT, kFp8>;
+    using C = SaCfg<D, NT, kFp8, kWarps>;
+    auto kern = sparse_attn_kernel<D, NT, kFp8, kWarps>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    // CTAs per (token, kv head): more of them shorten each one's run of tiles but
-    // each costs a start of about kStart tiles; up to the resident CTAs they all
-    // run at once, beyond that in turns, with half a turn's idling at the end.
-    // Measured with 1 / 2 / 4 / 8 CTAs: 384 units, bf16, 64 tiles per warp
-    // 125 / 120 / 131 / 145 us; 8-bit, 16 tiles per warp 27 / 33 / 41 / 68 us; 64 units,
-    // bf16 37 / 27 / 25 / 31 us; 8 units 31 / 18 / 12 / 9.7 us (16 CTAs: no faster).
-    constexpr int64_t kStart = 5;
-    const int64_t units = (int64_t)p.num_tokens * p.Hkv, slots = (int64_t)num_sms * C::kMinBlocks;
-    const int64_t tiles = ((int64_t)p.num_pages * p.bs + C::kTile * kSaWarps - 1) / (C::kTile * kSaWarps);
-    int n = 1;
-    int64_t best = 0;
-    for (int c = 1; c <= 8; c *= 2) {
-        const int64_t turns = units * c <= slots ? 2 * slots : 2 * units * c + slots;
-        const int64_t cost = turns * (kStart + (tiles + c - 1) / c);
-        if (c == 1 || cost < best) {
-            best = cost;
-            n = c;
+    const int64_t units = (int64_t)p.num_tokens * p.Hkv, listed = (int64_t)p.num_pages * p.bs;
+    int n = 1;  // CTAs per (token, kv head)
+    if (kWarps == 8) {
+        // One CTA per SM, all at once, a tile per warp at least. (Clusters of 8
+        // such CTAs find room on half of the SMs only: 16 units in clusters of 4 / 8
+        // 10.6 / 17.0 us.)
+        while (n < 8 && units * n * (n == 4 ? 4 : 2) <= num_sms && listed >= 2 * n * kWarps * C::kTile) n *= 2;
+    } else {
+        // More CTAs shorten each one's run of tiles but each costs a start of about
+        // kStart tiles, and beyond the resident CTAs they run in turns. Measured with
+        // 1 / 2 / 4 CTAs: bf16, 64 tiles per warp, 156 units 56 / 66 / 63 us, 308 units
+        // 117 / 107 / 107, 384 units 125 / 120 / 131; 8-bit, 32 tiles per warp, 156 units
+        // 43 / 32 / 37, 280 units 52 / 61 / 57, 612 units 109 / 102 / 111.
+        constexpr int64_t kStart = 8;
+        const int64_t slots = (int64_t)num_sms * C::kMinBlocks;
+        const int64_t tiles = (listed + C::kTile * kWarps - 1) / (C::kTile * kWarps);
+        int64_t best = 0;
+        for (int c = 1; c <= 8; c *= 2) {
+            const int64_t turns = (units * c + slots - 1) / slots;
+            const int64_t cost = turns * (kStart + (tiles + c - 1) / c);
+            if (c == 1 || cost < best) {
+                best = cost;
+                n = c;
+            }
         }
     }
-    return launch_cluster(kern, dim3((unsigned)n * (unsigned)p.num_tokens, p.Hkv), dim3(kSaThreads), C::kSmem, n, stream,
+    return launch_cluster(kern, dim3((unsigned)n * (unsigned)p.num_tokens, p.Hkv), dim3(C::kThreads), C::kSmem, n, stream,
                           p);
 }
 
 }  // namespace
 
 cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, bool fp8, int num_sms, cudaStream_t stream) {
+    // CTAs of 8 warps while there is an SM for each (token, kv head), and a tile for each
+    // warp, else of 4, several to an SM. Measured, 4096 listed keys each, best cluster of either, 4 / 8 warps:
+    // 8 units bf16 9.6 / 8.3 us, 8-bit 8.8 / 7.5; 32 units 15.9 / 15.8, 12.9 / 10.9;
+    // 64 units 25.0 / 25.2, 17.7 / 16.4; 128 units 43.8 / 43.2, 27.8 / 25.1 us.
     const bool two = p.G > 8;
-    if (fp8) return two ? go<128, 2, true>(p, num_sms, stream) : go<128, 1, true>(p, num_sms, stream);
-    if (head_dim == 128) return two ? go<128, 2, false>(p, num_sms, stream) : go<128, 1, false>(p, num_sms, stream);
-    return two ? go<64, 2, false>(p, num_sms, stream) : go<64, 1, false>(p, num_sms, stream);
+    const bool wide = (int64_t)p.num_tokens * p.Hkv <= num_sms && (int64_t)p.num_pages * p.bs >= 256;
+    auto by_warps = [&](auto d, auto nt, auto codes) {
+        constexpr int D = decltype(d)::value, NT = decltype(nt)::value;
+        constexpr bool kFp8 = decltype(codes)::value;
+        return wide ? go<D, NT, kFp8, 8>(p, num_sms, stream) : go<D, NT, kFp8, 4>(p, num_sms, stream);
+    };
+    auto by_columns = [&](auto d, auto codes) {
+        return two ? by_warps(d, std::integral_constant<int, 2>{}, codes)
+                   : by_warps(d, std::integral_constant<int, 1>{}, codes);
+    };
+    if (fp8) return by_columns(std::integral_constant<int, 128>{}, std::true_type{});
+    if (head_dim == 128) return by_columns(std::integral_constant<int, 128>{}, std::false_type{});
+    return by_columns(std::integral_constant<int, 64>{}, std::false_type{});
 }
 
 }  // namespace pka
