@@ -596,6 +596,21 @@ def test_sparse_attn_8_bit(Hq, Hkv, bs, K):
     attn_near(out, lse, want)
 
 
+@pytest.mark.parametrize("fp8,d,group,bs,K", [
+    (False, 128, 4, 16, 20), (False, 128, 12, 64, 40), (False, 64, 2, 64, 40), (False, 64, 16, 16, 20),
+    (True, 128, 4, 16, 40), (True, 128, 11, 64, 30)])
+def test_sparse_attn_of_more_tokens_than_sms(fp8, d, group, bs, K):
+    rng = np.random.default_rng(K + group)
+    ctx = np.exp(rng.uniform(0, np.log(4000), 90)).astype(int).tolist()
+    b = batch(rng, ctx, [1] * 90, bs)
+    q, caches, sel = attn_case(rng, b, 2 * group, 2, d, K, fp8=fp8)
+    units = (0.125, 0.11) if fp8 else None
+    out, lse, err = attn_run(b, q, caches, sel, d ** -0.5, units)
+    assert err == 0
+    attn_near(out, lse, ref.sparse_attn(ref.f64(q), *map(ref.f64, caches), b["table"], b["qsl"], b["seq"], sel, d ** -0.5,
+                                        [float(np.float32(u)) for u in units] if fp8 else (1.0, 1.0)))
+
+
 @pytest.mark.parametrize("power", [-60, -12, 0, 17, 90])
 def test_sparse_attn_8_bit_takes_queries_of_any_magnitude(power):
     """Queries of a head far from one, elements of a head far apart: q is held in units of a power of two of
