@@ -56,8 +56,10 @@ struct SaCfg {
     static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
     static constexpr int kTileBytes = kTile * kRowBytes;
     static constexpr int kStageBytes = 2 * kTileBytes;  // K + V
-    static constexpr int kStages = kFp8 ? 2 : 3;
-    static constexpr int kMinBlocks = kWarps == 8 ? 1 : kFp8 && NT == 1 ? 3 : 2;  // CTAs per SM
+    // Heads of 64 elements have tiles of half the bytes: more of them in flight (96
+    // requests 65 us, 68 us with 3 stages and 2 CTAs per SM; 16 requests 15.2 and 16.6).
+    static constexpr int kStages = kFp8 ? 2 : D == 64 ? 4 : 3;
+    static constexpr int kMinBlocks = kWarps == 8 ? 1 : (kFp8 || D == 64) && NT == 1 ? 3 : 2;  // CTAs per SM
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kCols = NT * 8;
     // the join: each warp's m, l and O (over the ring), and the CTA's own
