@@ -29,7 +29,9 @@
 // Math per tile (tensor cores, fp32 accumulation):
 //   S^T[keys x 8 columns] = K Q^T;  online softmax per column;  O^T += V^T P^T
 // bf16: P is rounded to bf16 for the product (its sum l is not): the error is
-// that of the operands' own type.
+// that of the operands' own type. (P as two bf16 numbers: 96 requests 119.4 us for
+// 118.4, one 8.6 for 8.4, 96 x 4 tokens 243 for 225; the error against 64 bits falls
+// from 0.0021 to that of the result's rounding, 0.0017.)
 // 8-bit: the codes are widened to f16 (exact) in registers, P is f16, and q is f16
 // in units of a power of two per query head (its largest element is 128 to 256
 // units: bf16's bits are kept down to 2^-22 of it). (The codes as e4m3 operands,
@@ -37,8 +39,8 @@
 // products: 24 x 4 tokens 36 us, 27 us this way.)
 //
 // Measured: 96 requests, 4 kv heads, 64 pages of 64 tokens each, bf16: 119 us, 6.7
-// TB/s; 8-bit: 67 us, 5.97 TB/s. One request of 8 kv heads, bf16: 9.7 us, of
-// which 5 are the chain place -> list -> block table -> tile and the join.
+// TB/s; 8-bit: 67 us, 5.97 TB/s. One request of 8 kv heads, bf16: 8.4 us: 3 until
+// the first tiles are there (launch, request, block table, tile), 3 of tiles, 2 of joins.
 #include "common.cuh"
 #include "params.cuh"
 
