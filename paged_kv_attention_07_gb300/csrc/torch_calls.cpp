@@ -92,9 +92,9 @@ public:
         if (t.scalar_type() != kBf16 || t.get_device() != device_ || n[0] != tokens || n[1] != heads || n[2] != d)
             refuse(text(name) + "must be a BFloat16 tensor of shape [" + std::to_string(tokens) + ", " +
                    std::to_string(heads) + ", " + std::to_string(d) + "] on the current CUDA device");
-        if ((by[1] != d && heads > 1) || (by[2] != 1 && d > 1))
+        if (tokens > 0 && ((by[1] != d && heads > 1) || (by[2] != 1 && d > 1)))
             refuse(text(name) + "must have the heads of a row packed");
-        stride = tokens > 1 ? by[0] : heads * d;  // (a single row's is free)
+        stride = tokens > 1 ? by[0] : heads * d;  // (a single row's is free, and what an empty tensor has)
         return t.data_ptr();
     }
 

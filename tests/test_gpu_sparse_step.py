@@ -3,6 +3,8 @@
 Tolerances, from the arithmetic: a rounding to bf16 is off by at most 2^-8 of the value
 (torch.finfo(bf16).eps / 2), to E4M3 by 2^-4 of it or half the least code; whole numbers
 (tables, codes, page lists) are equal."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -1021,3 +1023,76 @@ def test_bindings_refuse_wrong_tensors():
             rope_call(dict(s, **{n: bad}))
     with pytest.raises(pka.PkaError):
         rope_call(dict(s, kw=None))
+    for bad in (dict(scales=(0.1,)), dict(scales=3.0), dict(eps="small")):
+        with pytest.raises((ValueError, TypeError)):
+            rope_call(dict(s, k_cache=s["k_cache"].view(torch.uint8)[..., :64].contiguous(),
+                           v_cache=s["v_cache"].view(torch.uint8)[..., :64].contiguous(), **bad))
+    with pytest.raises(TypeError):
+        pka.pka_sparse_attn_forward(None, *args[1:])
+    with pytest.raises((TypeError, AttributeError)):
+        pka.pka_sparse_attn_forward(*args, stream="main")
+
+
+def test_steps_without_tokens():
+    s, table0 = tables_case([37, 0], [0, 0], 16, 0, [], 0)
+    assert int(s["err"]) == 0 and s["qsl"].tolist() == [0, 0, 0] and s["seq"].tolist() == [37, 0]
+    assert int(s["head_out"]) == 0 and np.array_equal(s["table"].cpu().numpy(), table0)
+    r = rope_case(0, 4, 2, 64, 64, False, True, False, False, nb=2)
+    before = copies(r)
+    rope_call(r)
+    assert torch.equal(r["k_cache"], before["k_cache"]) and int(r["err"]) == 0
+    rng = np.random.default_rng(33)
+    b = batch(rng, [100, 20], [0, 0], 16)
+    q, bounds, scales = select_case(rng, b, 4, 2, 64)
+    sel, err = select_run(b, q, bounds, scales, 1, 1, 5)
+    assert sel.shape == (0, 2, 5) and err == 0
+    cache = torch.zeros(b["nb"], 2, 16, 64, dtype=BF16, device="cuda")
+    assert attn_run(b, q, (cache, cache), sel, 0.1)[2] == 0
+    codes = torch.ones(b["nb"], 2, 2, 64, dtype=torch.int8, device="cuda")
+    units = torch.ones(b["nb"], 2, device="cuda")
+    pka.pka_page_bounds(cache, dev(np.zeros(0), I64), codes, units)
+    assert (codes == 1).all() and (units == 1).all()
+
+
+def test_lists_longer_than_the_pages():
+    rng = np.random.default_rng(34)
+    b = batch(rng, [300, 5], [1, 2], 16)
+    q, bounds, scales = select_case(rng, b, 8, 2, 128)
+    sel, err = select_run(b, q, bounds, scales, 3, 2, 3000)
+    assert err == 0
+    for t, n in enumerate([19, 1, 1]):
+        assert (sel[t] == np.concatenate([np.arange(n), np.full(3000 - n, -1)])).all()
+    q, caches, _ = attn_case(rng, b, 8, 2, 128, 4)
+    out, lse, err = attn_run(b, q, caches, sel, 0.1)
+    assert err == 0
+    attn_near(out, lse, ref.sparse_attn(ref.f64(q), *map(ref.f64, caches), b["table"], b["qsl"], b["seq"], sel, 0.1))
+
+
+def test_streams_and_threads():
+    rng = np.random.default_rng(35)
+    b = batch(rng, [3000, 5000, 77], [1, 2, 1], 16)
+    q, caches, sel = attn_case(rng, b, 16, 2, 128, 32)
+    want = attn_run(b, q, caches, sel, 0.1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # made there, run there by the three ways to name a stream
+        for stream in (None, side, side.cuda_stream):
+            got = attn_run(b, q, caches, sel, 0.1, stream=stream)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and got[2] == 0
+    torch.cuda.synchronize()
+    wrong = []
+
+    def serve():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                out, lse, err = attn_run(b, q, caches, sel, 0.1)
+                if err or not torch.equal(out, want[0]) or not torch.equal(lse, want[1]):
+                    wrong.append(err)
+
+    threads = [threading.Thread(target=serve) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
