@@ -49,6 +49,14 @@ PKA_DEVICE uint32_t max2(uint32_t a, uint32_t b) {
 }
 PKA_DEVICE __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 PKA_DEVICE uint16_t two(float x, float y) { return (uint16_t)((uint8_t)(int8_t)(int)x | (uint8_t)(int8_t)(int)y << 8); }
+// Codes of a pair: floor (ceil) of x times the power of two `unit`. The products are exact but where they are below
+// float32's least number, far below the page's largest: rounded away from the keys they still give -1 and 1 there.
+PKA_DEVICE uint16_t low_codes(float2 x, float unit) {
+    return two(floorf(__fmul_rd(x.x, unit)), floorf(__fmul_rd(x.y, unit)));
+}
+PKA_DEVICE uint16_t high_codes(float2 x, float unit) {
+    return two(ceilf(__fmul_ru(x.x, unit)), ceilf(__fmul_ru(x.y, unit)));
+}
 template <bool kFp8>
 PKA_DEVICE float2 pair(uint32_t x) {
     return kFp8 ? __half22float2(h2(x)) : make_float2(bf16_lo(x), bf16_hi(x));
@@ -144,8 +152,8 @@ __global__ void __launch_bounds__(kPbThreads) page_bounds_kernel(PageBoundsParam
 #pragma unroll
                     for (int i = 0; i < kWords; ++i) {
                         const float2 l = pair<kFp8>(lo[i]), h = pair<kFp8>(hi[i]);
-                        codes[0][i] = none ? 0 : two(floorf(l.x * unit), floorf(l.y * unit));
-                        codes[1][i] = none ? 0 : two(ceilf(h.x * unit), ceilf(h.y * unit));
+                        codes[0][i] = none ? 0 : low_codes(l, unit);
+                        codes[1][i] = none ? 0 : high_codes(h, unit);
                     }
                     uint2* dst = reinterpret_cast<uint2*>(p.bounds + page * 2 * p.head_dim + c * kVec);
 #pragma unroll
@@ -193,8 +201,8 @@ __global__ void __launch_bounds__(kPbThreads) page_bounds_kernel(PageBoundsParam
             const float unit = none ? 0.f : exp2i(-e);
             if (tid < pairs) {
                 uint16_t* code = reinterpret_cast<uint16_t*>(p.bounds + page * 2 * p.head_dim);
-                code[tid] = none ? 0 : two(floorf(l.x * unit), floorf(l.y * unit));
-                code[pairs + tid] = none ? 0 : two(ceilf(h.x * unit), ceilf(h.y * unit));
+                code[tid] = none ? 0 : low_codes(l, unit);
+                code[pairs + tid] = none ? 0 : high_codes(h, unit);
             }
             if (tid == 0) p.scales[page] = none ? INFINITY : exp2i(e);
         }
