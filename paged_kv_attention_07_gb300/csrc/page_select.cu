@@ -6,9 +6,10 @@
 // max |q| <= 127 * 2^x, c = q / 2^x rounded to nearest even) and a page's bounds
 //   score = max over the heads h of the group of 2^x_h * 2^e * sum_i max(c_i lo_i, c_i hi_i)
 // which no product <q, key> of the page exceeds (up to q's rounding). Every
-// term is an integer and the sum stays below 2^21: int32 tensor-core
-// accumulation is exact, the two factors are powers of two, so the scores are
-// the same bits in any order of work and ties are real ties.
+// term is an integer and the sum stays below 2^21: its accumulation is exact in
+// any order. The two factors are powers of two from 2^-60 to 2^122 each, further apart
+// than float32's exponents reach, so a score is kept as a 32-bit integer of its
+// order (score_key): exact at any magnitude, and ties are real ties.
 //
 // sum_i max(c_i lo_i, c_i hi_i) = <min(c, 0), lo> + <max(c, 0), hi>: one product
 // of length 2 d with the page's record as it lies in memory (lo then hi).
@@ -59,10 +60,15 @@ struct PsCfg {
     static constexpr int kFixed = NT * 8 * kQRow;  // then a key and a bit per page
 };
 
-// A float's bits as an unsigned key of the same order.
-PKA_DEVICE uint32_t order_key(float x) {
-    const uint32_t b = __float_as_uint(x + 0.f);  // -0 -> +0
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+// Queries' units are held as 2^(x + kUnitBias): sums below 2^21 times these are normal float32 numbers.
+constexpr int kUnitBias = -62;
+
+// An integer of the order of y * 2^e: y = sum * 2^(x + kUnitBias) is from 2^-122 to 2^81 or zero, 2^e a page's
+// scale from 2^-60 to 2^122. Their exponent fields add up to 457 at most: 9 bits, for which the last bit of y's
+// mantissa (21 bits of it count) makes room. Below INT_MAX, and -INT_MAX + 1.
+PKA_DEVICE int score_key(float y, float scale) {
+    const int size = (int)((__float_as_uint(fabsf(y)) + __float_as_uint(scale)) >> 1);
+    return y == 0.f ? 0 : y < 0.f ? -size : size;
 }
 
 // Exclusive sum of v over the block's threads.
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
         const bool second = lane * kE & 8;
         const int s0 = __reduce_add_sync(0xffffffffu, second ? 0 : sum), s1 = __reduce_add_sync(0xffffffffu, second ? sum : 0);
         if (lane == 0) {
-            s_unit[h] = exp2i(e);
+            s_unit[h] = exp2i(e + kUnitBias);
             s_zero[h][0] = 1152.f * (float)s0;
             s_zero[h][1] = 1152.f * (float)s1;
         }
@@ -291,21 +297,22 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 && NT == 1 ? 5 : 2) 
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            float v = -INFINITY;
+            float y = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     if (nt * 8 + 2 * (lane & 3) + j < p.G)
-                        v = fmaxf(v, ((c[nt][0][half * 2 + j] - zero[nt][j][0]) + (c[nt][1][half * 2 + j] - zero[nt][j][1])) *
-                                         now[half].scale * unit[nt][j]);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                        y = fmaxf(y, ((c[nt][0][half * 2 + j] - zero[nt][j][0]) + (c[nt][1][half * 2 + j] - zero[nt][j][1])) *
+                                         unit[nt][j]);
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
             // a page that bounds nothing (scale +inf) comes first, one that does not exist last
-            if (fabsf(now[half].scale) == INFINITY) v = now[half].scale;
+            int v = score_key(y, now[half].scale);
+            if (fabsf(now[half].scale) == INFINITY) v = now[half].scale > 0.f ? INT32_MAX : INT32_MIN;
             const int i = tile * 16 + half * 8 + (lane >> 2);
             if (i < m) {
-                const uint32_t k = order_key(v);
+                const uint32_t k = (uint32_t)v ^ 0x80000000u;  // in unsigned order
                 lo = min(lo, k);
                 hi = max(hi, k);
                 if ((lane & 3) == 0) store_cluster(&s_key[i], 0, k);

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from paged_kv_attention_07_gb300 import pka
-from tests.test_gpu_sparse_step import BF16, I64, bounds_check, dev, word
+from tests import sparse_ref as ref
+from tests.test_gpu_sparse_step import BF16, I64, batch, bounds_check, dev, randn, select_check, word
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,57 @@ def test_page_bounds_enclose_elements_far_below_the_largest(bs, d):
     assert int(err) == 0
     bounds_check(keys, slots, c0, s0, codes, scales)
     assert codes[0, 0, 0, 5] == -1 and codes[1, 1, 1, 5] == 1 and codes[2, 0, :, 5].tolist() == [0, 0]
+
+
+# ---------------------------------------------------------------- page selection
+
+
+def far_select_case(rng, b, Hq, Hkv, d, q_power, page_power):
+    """Queries and pages whose units are powers of two from the given ranges; bounds of both signs and of one."""
+    lo = rng.integers(-127, 100, (b["nb"], Hkv, 1, d))
+    hi = np.minimum(lo + rng.integers(0, 100, lo.shape), 127)
+    sign = rng.choice([-1, 0, 1], (b["nb"], Hkv, 1, 1))
+    bounds = np.where(sign == 0, np.concatenate([lo, hi], 2), sign * np.abs(np.concatenate([lo, hi], 2)))
+    bounds = np.sort(bounds, axis=2)  # low before high
+    scales = 2.0 ** rng.integers(*page_power, (b["nb"], Hkv))
+    q = ref.f64(randn(rng, b["T"], Hq, d)) * 2.0 ** rng.integers(*q_power, (b["T"], Hq, 1))
+    q = np.where(rng.random((b["T"], Hq, 1)) < 0.5, np.abs(q), q)  # scores below zero, with bounds of one sign
+    q = np.clip(q, -3e38, 3e38)
+    return torch.from_numpy(q).to(BF16).cuda(), bounds, scales
+
+
+@pytest.mark.parametrize("q_power,page_power", [
+    ((-3, 3), (107, 123)),     # one factor takes the sum past float32, the other brings it back
+    ((100, 126), (-60, -50)), ((-80, 126), (-60, 123)), ((110, 126), (110, 123)), ((-80, -60), (-60, -55)),
+    ((60, 64), (60, 64)),      # about the largest float32
+])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (9, 1, 64), (6, 6, 128)])
+def test_select_pages_scores_are_exact_at_any_magnitude(q_power, page_power, Hq, Hkv, d):
+    rng = np.random.default_rng(Hq + q_power[0] + 1000)
+    b = batch(rng, [900, 300, 3000], [1, 2, 1], 8)
+    q, bounds, scales = far_select_case(rng, b, Hq, Hkv, d, q_power, page_power)
+    # pages that bound nothing stand before the largest scores
+    for blk in b["table"][0, [5, 60]]:
+        scales[blk], bounds[blk] = np.inf, 0
+    for K in (4, 20):
+        select_check(b, q, bounds, scales, 1, 2, K)
+
+
+def test_select_pages_large_units_keep_their_order():
+    """127 codes of 127 in units of 2^110 against a query of ones: scores of about 2e37, of which the last page's
+    is the best."""
+    rng = np.random.default_rng(3)
+    b = batch(rng, [640], [1], 16)
+    n = 640 // 16
+    bounds = np.full((b["nb"], 1, 2, 128), 127.0)
+    for i in range(n):
+        bounds[b["table"][0, i], 0, :, 0] = i
+    q = torch.ones(1, 4, 128, dtype=BF16, device="cuda")
+    select_check(b, q, bounds, np.full((b["nb"], 1), 2.0 ** 110), 0, 1, 6)
+
+
+def test_select_pages_large_units_over_a_cluster():
+    rng = np.random.default_rng(4)
+    b = batch(rng, [20000], [1], 8)
+    q, bounds, scales = far_select_case(rng, b, 4, 1, 128, (-3, 126), (90, 123))
+    select_check(b, q, bounds, scales, 1, 2, 64)
