@@ -32,9 +32,11 @@
 // that of the operands' own type. (P as two bf16 numbers: 96 requests 119.4 us for
 // 118.4, one 8.6 for 8.4, 96 x 4 tokens 243 for 225; the error against 64 bits falls
 // from 0.0021 to that of the result's rounding, 0.0017.)
-// 8-bit: the codes are widened to f16 (exact) in registers, P is f16, and q is f16
-// in units of a power of two per query head (its largest element is 128 to 256
-// units: bf16's bits are kept down to 2^-22 of it). (The codes as e4m3 operands,
+// 8-bit: the codes are widened to f16 (exact) in registers, q is f16 in units of a
+// power of two per query head (its largest element is 128 to 256 units: bf16's
+// bits are kept down to 2^-22 of it), and P is f16, 2^-11 of each weight or 2^-40 of
+// the largest: weights are in units of 2^-15, the largest 2^15 of them, so that
+// the sum of many small ones is not lost below f16's least number. (The codes as e4m3 operands,
 // with q and P as two e4m3 numbers each, need no conversions but twice the
 // products: 24 x 4 tokens 36 us, 27 us this way.)
 //
@@ -64,6 +66,7 @@ struct SaCfg {
     static constexpr int kMinBlocks = kWarps == 8 ? 1 : (kFp8 || D == 64) && NT == 1 ? 3 : 2;  // CTAs per SM
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kCols = NT * 8;
+    static constexpr float kWeightPower = kFp8 ? 15.f : 0.f;  // weights (and l, O) in units of 2^-15: P fills f16's range
     // the join: each warp's m, l and O (over the ring), and the CTA's own
     static constexpr int kWarpFloats = kCols * (D + 2);
     static constexpr int kJoin = kWarps * kWarpFloats * 4;
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kWarps * 32, SaCfg<D, NT, kFp8, kWarps>::kMinB
                 float sum = 0.f;
 #pragma unroll
                 for (int q = 0; q < kOctets; ++q) {
-                    pr[q][hc] = fast_exp2(pr[q][hc] - sub);
+                    pr[q][hc] = fast_exp2(pr[q][hc] - sub + C::kWeightPower);
                     sum += pr[q][hc];
                 }
                 l[nt][hc] = l[nt][hc] * alpha[hc] + sum;
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(kWarps * 32, SaCfg<D, NT, kFp8, kWarps>::kMinB
         const int64_t row = row0 + hh;
         *reinterpret_cast<uint2*>(p.out + row * D + c) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (p.lse && c == 0) p.lse[row] = (M + __log2f(L)) * 0.69314718055994531f;
+        if (p.lse && c == 0) p.lse[row] = (M + __log2f(L * exp2i(-(int)C::kWeightPower))) * 0.69314718055994531f;
     }
     if (ncta > 1) cluster_barrier();  // no CTA leaves while another reads its shared memory
 }

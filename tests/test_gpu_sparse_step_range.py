@@ -5,7 +5,7 @@ import torch
 
 from paged_kv_attention_07_gb300 import pka
 from tests import sparse_ref as ref
-from tests.test_gpu_sparse_step import BF16, I64, batch, bounds_check, dev, randn, select_check, word
+from tests.test_gpu_sparse_step import BF16, I32, I64, batch, bounds_check, dev, randn, select_check, word
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,49 @@ def test_select_pages_large_units_over_a_cluster():
     b = batch(rng, [20000], [1], 8)
     q, bounds, scales = far_select_case(rng, b, 4, 1, 128, (-3, 126), (90, 123))
     select_check(b, q, bounds, scales, 1, 2, 64)
+
+
+# ---------------------------------------------------------------- attention over selected pages
+
+
+def attn(b, q, caches, sel, scale, units=None):
+    out, lse, err = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"), word()
+    pka.pka_sparse_attn_forward(q, *caches, dev(b["table"], I32), dev(b["qsl"], I32), dev(b["seq"], I32), dev(sel, I32),
+                                scale, b["longest"], out, lse, kv_scales=units, error_word=err)
+    assert int(err) == 0
+    return ref.f64(out), ref.f64(lse)
+
+
+def attn64(b, q, caches, sel, scale, units=(1.0, 1.0)):
+    return ref.sparse_attn(ref.f64(q), *map(ref.f64, caches), b["table"], b["qsl"], b["seq"], sel, scale, units)
+
+
+def lists(rng, b, Hkv, K, every=False):
+    sel = np.full((b["T"], Hkv, K), -1)
+    for t, r, p in ref.positions(b["qsl"], b["seq"]):
+        for g in range(Hkv):
+            n = p // b["bs"] + 1
+            pages = np.sort(rng.permutation(n)[:n if every else min(n, K)])
+            sel[t, g, :len(pages)] = pages
+    return sel
+
+
+@pytest.mark.parametrize("power", [20, 26, 29])
+@pytest.mark.parametrize("pages,bs", [(33, 8), (2000, 8), (40, 64)])
+def test_sparse_attn_8_bit_keeps_small_weights(power, pages, bs):
+    """Every eighth key has the largest score and a value of zero: the result is what keys with weights of 2^-power
+    of it add up to. A weight is off by 2^-11 of itself or by 2^-40 of the largest."""
+    rng = np.random.default_rng(power + pages)
+    b = batch(rng, [pages * bs - 3], [1], bs)
+    k, v = np.zeros((b["nb"], 1, bs, 128)), np.abs(rng.standard_normal((b["nb"], 1, bs, 128))) * 8
+    k[:, :, ::8, 0], v[:, :, ::8] = 1, 0
+    caches = [torch.from_numpy(x).float().to(torch.float8_e4m3fn).view(torch.uint8).cuda() for x in (k, v)]
+    q = torch.zeros(1, 2, 128, dtype=BF16, device="cuda")
+    q[0, 0, 0], q[0, 1, 0] = 1, 1.0625
+    sel = lists(rng, b, 1, pages + 1, every=True)
+    scale = float(np.float32(power * np.log(2)))
+    out, lse = attn(b, q, caches, sel, scale, (1.0, 1.0))
+    o, l, size = attn64(b, q, caches, sel, scale)
+    largest = 8 * 2.0 ** -40 * ref.f64(caches[1]).max()  # (of the seven keys beside each largest one)
+    assert (np.abs(out - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -14 + 2.0 ** -11) * size + largest).all()
+    assert (np.abs(lse - l) <= 2.0 ** -14 * (1 + np.abs(l))).all()
