@@ -23,15 +23,16 @@
 // Each token reads its own pages, tokens of one request mostly the same ones
 // through L2. (Taking such tokens together over their united lists was measured:
 // 96 x 4 tokens 238 -> 216 us, but 24 x 4 tokens 46 -> 52 us and 8-bit caches
-// 143 -> 201 us: the lists' union and the registers of more columns cost what
-// the shared reads save.)
+// 143 -> 201 us, with P as one bf16 number: the lists' union and the registers of
+// more columns cost what the shared reads save.)
 //
 // Math per tile (tensor cores, fp32 accumulation):
 //   S^T[keys x 8 columns] = K Q^T;  online softmax per column;  O^T += V^T P^T
-// bf16: P is rounded to bf16 for the product (its sum l is not): the error is
-// that of the operands' own type. (P as two bf16 numbers: 96 requests 119.4 us for
-// 118.4, one 8.6 for 8.4, 96 x 4 tokens 243 for 225; the error against 64 bits falls
-// from 0.0021 to that of the result's rounding, 0.0017.)
+// bf16: P is two bf16 numbers, the largest one below it and the rest, off by 2^-15
+// of each weight: the result's error is that of its own rounding. (Rounded to one:
+// 0.0021 against 64 bits instead of 0.0017; 96 x 4 tokens 225 us instead of 247, 96
+// requests 120.2 and 121.2, one 8.5 and 8.7.) Both are positive, so that an infinite
+// value is not taken off itself.
 // 8-bit: the codes are widened to f16 (exact) in registers, q is f16 in units of a
 // power of two per query head (its largest element is 128 to 256 units: bf16's
 // bits are kept down to 2^-22 of it), and P is f16, 2^-11 of each weight or 2^-40 of
@@ -40,8 +41,8 @@
 // with q and P as two e4m3 numbers each, need no conversions but twice the
 // products: 24 x 4 tokens 36 us, 27 us this way.)
 //
-// Measured: 96 requests, 4 kv heads, 64 pages of 64 tokens each, bf16: 119 us, 6.7
-// TB/s; 8-bit: 67 us, 5.97 TB/s. One request of 8 kv heads, bf16: 8.4 us: 3 until
+// Measured: 96 requests, 4 kv heads, 64 pages of 64 tokens each, bf16: 121 us, 6.6
+// TB/s; 8-bit: 68 us, 5.9 TB/s. One request of 8 kv heads, bf16: 8.7 us: 3 until
 // the first tiles are there (launch, request, block table, tile), 3 of tiles, 2 of joins.
 #include "common.cuh"
 #include "params.cuh"
@@ -87,6 +88,9 @@ PKA_DEVICE void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
+
+// The float of the largest bf16 number below p > 0 (in its high half; zero for zero).
+PKA_DEVICE uint32_t below(float p) { return max(__float_as_uint(p), 1u) - 1; }
 
 template <int D, int NT, bool kFp8, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32, SaCfg<D, NT, kFp8, kWarps>::kMinBlocks)
@@ -320,7 +324,8 @@ __global__ void __launch_bounds__(kWarps * 32, SaCfg<D, NT, kFp8, kWarps>::kMinB
                 for (int e = 0; e < 4; ++e) sc[0][nt][e] += sd[nt][e];
         }
         // ---- online softmax in the log2 domain; other keys weigh nothing
-        uint32_t pb[kOctets][NT];  // P^T fragments
+        uint32_t pb[kOctets][NT];             // P^T fragments
+        uint32_t pl[kFp8 ? 1 : kOctets][NT];  // bf16: what these leave of P^T
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float pr[kOctets][2];
@@ -358,8 +363,15 @@ __global__ void __launch_bounds__(kWarps * 32, SaCfg<D, NT, kFp8, kWarps>::kMinB
                 }
             }
 #pragma unroll
-            for (int q = 0; q < kOctets; ++q)
-                pb[q][nt] = movmatrix_t(kFp8 ? pack_f16(pr[q][0], pr[q][1]) : pack_bf16(pr[q][0], pr[q][1]));
+            for (int q = 0; q < kOctets; ++q) {
+                if constexpr (kFp8) {
+                    pb[q][nt] = movmatrix_t(pack_f16(pr[q][0], pr[q][1]));
+                } else {
+                    const uint32_t w = __byte_perm(below(pr[q][0]), below(pr[q][1]), 0x7632);
+                    pb[q][nt] = movmatrix_t(w);
+                    pl[q][nt] = movmatrix_t(pack_bf16(pr[q][0] - bf16_lo(w), pr[q][1] - bf16_hi(w)));
+                }
+            }
         }
         // ---- O^T += V^T P^T
         if constexpr (kFp8) {
@@ -395,8 +407,10 @@ __global__ void __launch_bounds__(kWarps * 32, SaCfg<D, NT, kFp8, kWarps>::kMinB
                 uint32_t a0, a1, a2, a3;
                 ldsm_x4_t(vb + seg_off<kTile>(tr, mt * 2 + (mi & 1)), a0, a1, a2, a3);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
                     mma_bf16(o[mt][nt], a0, a1, a2, a3, pb[0][nt], pb[1][nt]);
+                    mma_bf16(o[mt][nt], a0, a1, a2, a3, pl[0][nt], pl[1][nt]);
+                }
             }
         }
         __syncwarp();
@@ -510,9 +524,9 @@ cudaError_t go(const SparseAttnParams& p, int num_sms, cudaStream_t stream) {
     } else {
         // More CTAs shorten each one's run of tiles but each costs a start of about
         // kStart tiles, and beyond the resident CTAs they run in turns. Measured with
-        // 1 / 2 / 4 CTAs: bf16, 64 tiles per warp, 156 units 56 / 66 / 63 us, 308 units
-        // 117 / 107 / 107, 384 units 125 / 120 / 131; 8-bit, 32 tiles per warp, 156 units
-        // 43 / 32 / 37, 280 units 52 / 61 / 57, 612 units 109 / 102 / 111.
+        // 1 / 2 / 4 CTAs: bf16 (P as one number), 64 tiles per warp, 156 units 56 / 66 / 63
+        // us, 308 units 117 / 107 / 107, 384 units 125 / 120 / 131; 8-bit, 32 tiles per warp,
+        // 156 units 43 / 32 / 37, 280 units 52 / 61 / 57, 612 units 109 / 102 / 111.
         constexpr int64_t kStart = 8;
         const int64_t slots = (int64_t)num_sms * C::kMinBlocks;
         const int64_t tiles = (listed + C::kTile * kWarps - 1) / (C::kTile * kWarps);

@@ -138,3 +138,38 @@ def test_sparse_attn_8_bit_keeps_small_weights(power, pages, bs):
     largest = 8 * 2.0 ** -40 * ref.f64(caches[1]).max()  # (of the seven keys beside each largest one)
     assert (np.abs(out - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -14 + 2.0 ** -11) * size + largest).all()
     assert (np.abs(lse - l) <= 2.0 ** -14 * (1 + np.abs(l))).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,bs,K", [(8, 2, 128, 16, 6), (6, 2, 64, 8, 9), (16, 1, 128, 64, 3), (9, 1, 64, 16, 40),
+                                           (32, 4, 128, 64, 16), (2, 2, 128, 8, 80)])
+@pytest.mark.parametrize("new", [1, 4])
+def test_sparse_attn_is_off_by_its_results_rounding(Hq, Hkv, d, bs, K, new):
+    """That rounding: 2^-8 of the value. Scores of up to 2^5 with a relative error of a few 2^-23: 2^-14 of the sum of
+    the weighted magnitudes. A weight as two bf16 numbers, the first cut off, the second rounded: 2^-8 of 2^-7 of
+    it, 2^-15 of that sum."""
+    rng = np.random.default_rng(Hq + K + new)
+    b = batch(rng, [0, 2 * bs - 3, 500, 40, 7, 1200], [new] * 6, bs)
+    caches = [randn(rng, b["nb"], Hkv, bs, d) for _ in range(2)]
+    q, sel = randn(rng, b["T"], Hq, d), lists(rng, b, Hkv, K)
+    out, lse = attn(b, q, caches, sel, d ** -0.5)
+    o, l, size = attn64(b, q, caches, sel, d ** -0.5)
+    assert (np.abs(out - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -14 + 2.0 ** -15) * size).all()
+    assert (np.abs(lse - l) <= 2.0 ** -14 * (1 + np.abs(l))).all()
+
+
+@pytest.mark.parametrize("d,bs", [(128, 16), (64, 8)])
+def test_sparse_attn_infinite_values_are_infinite_results(d, bs):
+    """Also where the key's weight is a power of two, the largest one, or has all its bits."""
+    rng = np.random.default_rng(d)
+    b = batch(rng, [37 * bs - 1], [1], bs)
+    caches = [randn(rng, b["nb"], 1, bs, d) for _ in range(2)]
+    q, sel = randn(rng, 1, 4, d), lists(rng, b, 1, 40, every=True)
+    q[0, 1] = 0                                   # all weights one
+    caches[0][b["table"][0, 5], 0, 1] = q[0, 2]  # the largest weight of its head
+    caches[1][b["table"][0, 5], 0, 1, 3] = float("inf")
+    caches[1][b["table"][0, 36], 0, 0, 4] = float("-inf")
+    caches[1][b["table"][0, 8], 0, 2, 5] = float("inf")
+    caches[1][b["table"][0, 9], 0, 2, 5] = float("-inf")
+    out, lse = attn(b, q, caches, sel, d ** -0.5)
+    assert (out[..., 3] == np.inf).all() and (out[..., 4] == -np.inf).all() and np.isnan(out[..., 5]).all()
+    assert np.isfinite(np.delete(out, [3, 4, 5], -1)).all() and np.isfinite(lse).all()
