@@ -533,7 +533,8 @@ PKA_API pka_status pka_step_tables(const int32_t *ctx_lens, const int32_t *query
  *   k_cache, v_cache  device [num_blocks, Hkv, block_size, d] bf16 (_fp8: uint8 codes)
  * Two tokens with the same slot: one of them is kept, element by element.
  * head_dim a multiple of 8 up to 256, rotary_dim a multiple of 16 up to
- * head_dim, else PKA_ERR_UNSUPPORTED.
+ * head_dim, num_q_heads * head_dim and num_kv_heads * head_dim <= 2^30, else
+ * PKA_ERR_UNSUPPORTED.
  */
 PKA_API pka_status pka_qk_rope_cache_write(const void *q, const void *k, const void *v, int64_t q_stride,
                                            int64_t k_stride, int64_t v_stride, const void *q_weight,

@@ -1072,6 +1072,8 @@ pka_status qk_rope_impl(const void* q, const void* k, const void* v, int64_t q_s
     if (rotary_dim > head_dim || (rotary_dim > 0 && (!cos_sin || max_position <= 0))) return PKA_ERR_INVALID_ARG;
     if (interleaved != 0 && interleaved != 1) return PKA_ERR_INVALID_ARG;
     if (head_dim % 8 != 0 || head_dim > 256 || rotary_dim % 16 != 0) return PKA_ERR_UNSUPPORTED;
+    // (32-bit indexes of a row's elements)
+    if ((int64_t)std::max(num_q_heads, num_kv_heads) * head_dim > (1 << 30)) return PKA_ERR_UNSUPPORTED;
     if (num_blocks > INT64_MAX / block_size) return PKA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PKA_OK;
     if (!q || !k || !v || !positions || !slot_mapping || !q_out || !k_cache || !v_cache) return PKA_ERR_INVALID_ARG;
