@@ -1,8 +1,8 @@
 """Builds libpka.so (the CUDA kernels + C ABI) in-tree for sm_103a.
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then the
-objects are linked into paged_kv_attention_07_gb300/_build/libpka.so. The
-calls with torch tensors (csrc/torch_calls.cpp) become a Python module beside it.
+objects are linked into paged_kv_attention_07_gb300/_build/libpka.so. Where torch is
+installed, the calls with torch tensors (csrc/torch_calls.cpp) become a Python module beside it.
 Nothing is installed outside the repository.
 
     python -m paged_kv_attention_07_gb300.build [--force]
@@ -53,8 +53,13 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _compile_torch_calls() -> str:
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch_dir():
+    """The installed torch's directory, or None: libpka.so itself needs none."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _compile_torch_calls(torch_dir: str) -> str:
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [INCLUDE, os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
                os.path.join(cuda, "include")]
@@ -67,8 +72,8 @@ def _compile_torch_calls() -> str:
     return obj
 
 
-def _link_torch_calls(obj: str) -> None:
-    lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+def _link_torch_calls(obj: str, torch_dir: str) -> None:
+    lib = os.path.join(torch_dir, "lib")
     tmp = f"{TORCH_CALLS}.{os.getpid()}.tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libpka.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10",
            "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
@@ -78,12 +83,7 @@ def _link_torch_calls(obj: str) -> None:
     os.replace(tmp, TORCH_CALLS)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """Compile csrc/*.cu and link libpka.so; returns the library path."""
-    deps = _deps() + [os.path.abspath(__file__)]
-    if not force and not _stale(LIB, deps) and not _stale(TORCH_CALLS, [*deps, LIB]):
-        return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
+def _build_lib(verbose: bool, extra_flags) -> None:
     nvcc = _nvcc()
     flags = NVCC_FLAGS + list(extra_flags or [])
 
@@ -98,8 +98,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        torch_obj = ex.submit(_compile_torch_calls)
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
         objs = list(ex.map(compile_one, srcs))
     tmp = f"{LIB}.{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
@@ -107,7 +106,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_torch_calls(torch_obj.result())
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """Compile csrc/*.cu and link libpka.so, and the module of calls with torch tensors where torch is
+    installed; what is up to date stays. Returns the library path."""
+    deps = _deps() + [os.path.abspath(__file__)]
+    torch_dir = _torch_dir()
+    lib = force or _stale(LIB, deps)
+    calls = torch_dir is not None and (lib or _stale(TORCH_CALLS, [*deps, LIB]))
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        torch_obj = ex.submit(_compile_torch_calls, torch_dir) if calls else None
+        if lib:
+            _build_lib(verbose, extra_flags)
+        if calls:
+            _link_torch_calls(torch_obj.result(), torch_dir)
     return LIB
 
 
