@@ -12,6 +12,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -22,7 +23,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpka.so")
-TORCH_CALLS = os.path.join(OUT_DIR, "_pka_torch.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -59,6 +59,16 @@ def _torch_dir():
     return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
+def _torch_version(torch_dir: str) -> str:
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return re.search(r"^__version__\b[^=]*=\s*['\"]([^'\"]+)", f.read(), re.MULTILINE).group(1)
+
+
+def torch_calls_path(torch_version: str) -> str:
+    """The module of calls with torch tensors for that torch (its C++ interface is the version's) and this Python."""
+    return os.path.join(OUT_DIR, f"_pka_torch.{torch_version}.{sysconfig.get_config_var('SOABI')}.so")
+
+
 def _compile_torch_calls(torch_dir: str) -> str:
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [INCLUDE, os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
@@ -72,15 +82,15 @@ def _compile_torch_calls(torch_dir: str) -> str:
     return obj
 
 
-def _link_torch_calls(obj: str, torch_dir: str) -> None:
+def _link_torch_calls(obj: str, torch_dir: str, target: str) -> None:
     lib = os.path.join(torch_dir, "lib")
-    tmp = f"{TORCH_CALLS}.{os.getpid()}.tmp"
+    tmp = f"{target}.{os.getpid()}.tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libpka.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10",
            "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, TORCH_CALLS)
+    os.replace(tmp, target)
 
 
 def _build_lib(verbose: bool, extra_flags) -> None:
@@ -114,14 +124,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     deps = _deps() + [os.path.abspath(__file__)]
     torch_dir = _torch_dir()
     lib = force or _stale(LIB, deps)
-    calls = torch_dir is not None and (lib or _stale(TORCH_CALLS, [*deps, LIB]))
+    target = torch_calls_path(_torch_version(torch_dir)) if torch_dir else None
+    calls = target is not None and (lib or _stale(target, [*deps, LIB]))
     os.makedirs(OUT_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
         torch_obj = ex.submit(_compile_torch_calls, torch_dir) if calls else None
         if lib:
             _build_lib(verbose, extra_flags)
         if calls:
-            _link_torch_calls(torch_obj.result(), torch_dir)
+            _link_torch_calls(torch_obj.result(), torch_dir, target)
     return LIB
 
 

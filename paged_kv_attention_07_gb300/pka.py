@@ -13,7 +13,6 @@ import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpka.so")
-TORCH_CALLS_PATH = os.path.join(_HERE, "_build", "_pka_torch.so")
 
 PKA_OK = 0
 STATUS_NAMES = {0: "PKA_OK", 1: "PKA_ERR_INVALID_ARG", 2: "PKA_ERR_UNSUPPORTED",
@@ -315,11 +314,14 @@ def _calls():
     global _torch_calls
     if _torch_calls is None:
         import importlib.util
-        import torch  # noqa: F401  (its libraries are the module's)
+        import torch  # (its libraries are the module's)
+
+        from .build import torch_calls_path
         load()
-        if not os.path.exists(TORCH_CALLS_PATH):
-            raise RuntimeError(f"{TORCH_CALLS_PATH} not found: it must be built as libpka.so is")
-        spec = importlib.util.spec_from_file_location("_pka_torch", TORCH_CALLS_PATH)
+        path = torch_calls_path(torch.__version__)
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} not found: it is built as libpka.so is, for the torch and the Python that use it")
+        spec = importlib.util.spec_from_file_location("_pka_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         _torch_calls = module

@@ -5,6 +5,7 @@ import types
 import pytest
 
 from paged_kv_attention_07_gb300 import build as B
+from paged_kv_attention_07_gb300 import pka
 
 
 @pytest.fixture
@@ -20,7 +21,6 @@ def tools(monkeypatch, tmp_path):
 
     monkeypatch.setattr(B, "OUT_DIR", str(tmp_path))
     monkeypatch.setattr(B, "LIB", str(tmp_path / "libpka.so"))
-    monkeypatch.setattr(B, "TORCH_CALLS", str(tmp_path / "_pka_torch.so"))
     monkeypatch.setattr(B.subprocess, "run", run)
     return calls
 
@@ -41,9 +41,37 @@ def test_builds_what_is_out_of_date(tools):
     tools.clear()
     B.build()
     assert not tools
-    os.remove(B.TORCH_CALLS)  # the module alone
+    [module] = [f for f in os.listdir(B.OUT_DIR) if f.startswith("_pka_torch") and f.endswith(".so")]
+    os.remove(os.path.join(B.OUT_DIR, module))  # the module alone
     B.build()
     assert [tool for tool, _ in tools] == ["g++", "g++"]
     tools.clear()
     B.build(force=True)
     assert len(tools) == len(B.sources()) + 3
+
+
+@pytest.mark.parametrize("change", ["torch", "python"])
+def test_another_torch_or_python_gets_a_module_of_its_own(tools, monkeypatch, change):
+    torch = pytest.importorskip("torch")
+    B.build()
+    here = B.torch_calls_path(torch.__version__)
+    assert os.path.exists(here)  # where the calls look for it
+    if change == "torch":
+        monkeypatch.setattr(B, "_torch_version", lambda _: "9.9.9")
+    else:
+        soabi = B.sysconfig.get_config_var
+        monkeypatch.setattr(B.sysconfig, "get_config_var", lambda n: "cpython-399" if n == "SOABI" else soabi(n))
+    there = B.torch_calls_path("9.9.9" if change == "torch" else torch.__version__)
+    assert there != here and not os.path.exists(there)
+    tools.clear()
+    B.build()
+    assert os.path.exists(there) and [tool for tool, _ in tools] == ["g++", "g++"]  # the library is what it was
+
+
+def test_calls_do_not_load_a_module_of_another_torch(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(pka, "_torch_calls", None)
+    monkeypatch.setattr(pka, "load", lambda: None)
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    with pytest.raises(RuntimeError, match="9.9.9.*not found"):
+        pka._calls()
