@@ -1,11 +1,14 @@
-"""The block-sparse step at the far ends of the ranges its header names, against float64."""
+"""The block-sparse step at the far ends of the ranges its header names: magnitudes up to a type's own limits, weights
+far below the largest, lists of many turns, batches of many requests. Against float64; a tolerance's parts stand at
+its test."""
 import numpy as np
 import pytest
 import torch
 
 from paged_kv_attention_07_gb300 import pka
 from tests import sparse_ref as ref
-from tests.test_gpu_sparse_step import BF16, I32, I64, batch, bounds_check, dev, randn, select_check, word
+from tests.test_gpu_sparse_step import (BF16, I32, I64, attn_case, attn_near, attn_run, batch, bounds_check, dev, randn,
+                                        select_case, select_check, word)
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +176,106 @@ def test_sparse_attn_infinite_values_are_infinite_results(d, bs):
     out, lse = attn(b, q, caches, sel, d ** -0.5)
     assert (out[..., 3] == np.inf).all() and (out[..., 4] == -np.inf).all() and np.isnan(out[..., 5]).all()
     assert np.isfinite(np.delete(out, [3, 4, 5], -1)).all() and np.isfinite(lse).all()
+
+
+def page_for_each_head(rng, B, bs, keys, d, fp8):
+    """B requests that share one block table, a token each, whose heads look for a page each: keys of a page are
+    its own signs, values its own numbers, so a page that is lost, doubled or another's shows in its head's row."""
+    b = batch(rng, [keys - 1], [1], bs)
+    n = -(-keys // bs)
+    sign = torch.from_numpy(rng.choice([-1.0, 1.0], (b["nb"], d)))
+    values = torch.from_numpy(rng.standard_normal((b["nb"], d)) * (8 if fp8 else 1))
+    kind = torch.float8_e4m3fn if fp8 else BF16
+    caches = [x.float().to(kind).view(torch.uint8 if fp8 else BF16)[:, None, None].expand(-1, 1, bs, -1).contiguous()
+              for x in (sign, values)]
+    b = dict(b, table=np.repeat(b["table"], B, 0), qsl=list(range(B + 1)), seq=[keys] * B, T=B)
+    return b, caches, n, sign
+
+
+def targets_of(rng, n, count):
+    """Pages about every 32nd of each of 16 runs of the list, then any."""
+    near = [run * n // 16 + i + j for run in range(16) for i in range(0, n // 16 + 1, 32) for j in (-1, 0, 1)]
+    near = list(dict.fromkeys(x for x in near if 0 <= x < n))[:count]
+    rest = [x for x in rng.permutation(n).tolist() if x not in set(near)]
+    return np.array((near + rest * -(-count // max(len(rest), 1)))[:count])
+
+
+def each_page_case(bs, fp8):
+    rng = np.random.default_rng(bs)
+    B, G, d, keys = 40, 16, 128, 40001
+    b, caches, n, sign = page_for_each_head(rng, B, bs, keys, d, fp8)
+    look = targets_of(rng, n, B * G)
+    q = sign[torch.from_numpy(b["table"][0][look])].view(B, G, d).to(BF16)
+    return b, caches, q, np.arange(n), look.reshape(B, G)
+
+
+def attn_of_list(b, q, caches, pages, scale):
+    """Of every head over the listed pages (some twice, perhaps), all keys up to the last: out, lse, the sum of the
+    weighted magnitudes, and what the magnitudes add up to with 2^-40 of the largest weight each."""
+    bs, keys = b["bs"], b["seq"][0]
+    blk = torch.from_numpy(b["table"][0][pages])
+    there = (torch.from_numpy(pages)[:, None] * bs + torch.arange(bs) < keys).flatten()
+    k, v = (torch.from_numpy(ref.f64(c[:, 0]))[blk].flatten(0, 1)[there] for c in caches)
+    s = q.double().flatten(0, 1) @ k.T * scale
+    w = s.softmax(-1)
+    least = 2.0 ** -40 * w.amax(-1, keepdim=True) * v.abs().sum(0)
+    return tuple(x.unflatten(0, q.shape[:2]).numpy() for x in (w @ v, s.logsumexp(-1), w @ v.abs(), least))
+
+
+def each_page_near(out, lse, want, fp8):
+    """The result's rounding to bf16, 2^-8 of the value. Scores of up to 2^5 with a relative error of a few 2^-23: 2^-14
+    of the sum of the weighted magnitudes. A weight as two bf16 numbers is off by 2^-15 of itself, as one of f16 by
+    2^-11 of itself or by 2^-40 of the largest."""
+    o, l, size, least = want
+    near = np.abs(out - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -14 + (2.0 ** -11 if fp8 else 2.0 ** -15)) * size + \
+        (least if fp8 else 0)
+    return near.all(-1) & (np.abs(lse - l) <= 2.0 ** -14 * (1 + np.abs(l)))
+
+
+SCALE = 0.2
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bs", [8, 64])
+def test_sparse_attn_long_lists_page_by_page(bs, fp8):
+    b, caches, q, pages, _ = each_page_case(bs, fp8)
+    sel = np.broadcast_to(pages, (b["T"], 1, len(pages)))
+    out, lse = attn(b, q.cuda(), [c.cuda() for c in caches], sel, SCALE, (1.0, 1.0) if fp8 else None)
+    assert each_page_near(out, lse, attn_of_list(b, q, caches, pages, SCALE), fp8).all()
+    if bs == 8:  # and without every third page
+        pages = pages[pages % 3 != 1]
+        sel = np.broadcast_to(pages, (b["T"], 1, len(pages)))
+        out, lse = attn(b, q.cuda(), [c.cuda() for c in caches], sel, SCALE, (1.0, 1.0) if fp8 else None)
+        assert each_page_near(out, lse, attn_of_list(b, q, caches, pages, SCALE), fp8).all()
+
+
+# ---------------------------------------------------------------- batches of many requests
+
+
+def many_requests(B, bs):
+    """Requests of 0, 1, 2 and 5 new tokens in any order, runs of idle ones at both ends and within."""
+    rng = np.random.default_rng(B + bs)
+    new = rng.choice([0, 1, 1, 2, 5], B)
+    new[:3] = new[-2:] = 0
+    new[B // 2:B // 2 + min(B // 3, 70)] = 0
+    new[B // 4] = 5
+    ctx = rng.integers(0, 60, B)
+    return rng, batch(rng, ctx.tolist(), new.tolist(), bs, extra_rows=3)
+
+
+@pytest.mark.parametrize("B", [33, 64, 65, 1024, 1025, 3000])
+def test_select_pages_of_many_requests(B):
+    rng, b = many_requests(B, 4)
+    select_check(b, *select_case(rng, b, 2, 1, 64), 1, 1, 5)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B", [33, 64, 65, 1024, 1025, 3000])
+def test_sparse_attn_of_many_requests(B, fp8):
+    rng, b = many_requests(B, 8)
+    q, caches, sel = attn_case(rng, b, 2, 1, 128, 3, fp8=fp8)
+    units = (0.125, 0.25) if fp8 else None  # (float32 numbers)
+    out, lse, err = attn_run(b, q, caches, sel, 0.09, units)
+    assert err == 0
+    attn_near(out, lse, ref.sparse_attn(ref.f64(q), *map(ref.f64, caches), b["table"], b["qsl"], b["seq"], sel, 0.09,
+                                        units or (1.0, 1.0)))
