@@ -562,9 +562,8 @@ PKA_API pka_status pka_qk_rope_cache_write_fp8(const void *q, const void *k, con
  * least power of two with a <= 127 * 2^e and e >= -60:
  *     bounds[b][h][0][i] = floor(lo_i / 2^e),  bounds[b][h][1][i] = ceil(hi_i / 2^e)
  *     bound_scales[b][h] = 2^e
- * so bounds * bound_scales encloses the page's keys (exactly, for keys of
- * magnitude 2^-60 and more). A page with a NaN or an infinity gets bounds 0
- * and the scale +infinity. Pages that are not filled are left as they are.
+ * so bounds * bound_scales encloses the page's keys. A page with a NaN or an
+ * infinity gets bounds 0 and the scale +infinity. Pages that are not filled are left as they are.
  *
  *   k_cache       device [num_blocks, Hkv, block_size, d], cache_dtype 1 = bf16, 2 = E4M3 codes
  *                 (bounds then in units of one code, whatever the cache's k_scale)
@@ -589,15 +588,16 @@ PKA_API pka_status pka_page_bounds(const void *k_cache, int cache_dtype, const i
  *     2^x_h * bound_scales * sum_i max(c_i * lo_i, c_i * hi_i)
  * where c = round(q_h / 2^x_h), half to even, 2^x_h the least power of two with
  * max |q_h| <= 127 * 2^x_h and x_h >= -60, and lo, hi the page's bounds: an
- * upper bound of <c * 2^x_h, key> over the page's keys. The sum is an integer
- * and the factors are powers of two, so a score is exact and of equal scores
- * the lower page is taken. A head with a NaN or an infinity scores 0
+ * upper bound of <c * 2^x_h, key> over the page's keys (of the rounded query: a
+ * product with q_h itself may pass it by half a unit 2^x_h of each element). The
+ * sum is an integer and the factors are powers of two, so a score is exact at
+ * any magnitude and of equal scores the lower page is taken. A head with a NaN or an infinity scores 0
  * everywhere; a page with the scale +infinity comes first. The score of a page
  * before the last num_last ones is read from its bounds, so those pages have
  * to have been through pka_page_bounds.
  *
  *   q              device bf16 [num_tokens, Hq, d]
- *   bounds, bound_scales  as pka_page_bounds writes them
+ *   bounds, bound_scales  as pka_page_bounds writes them (powers of two from 2^-60, or +infinity)
  *   block_table    device int32 [num_reqs, max_blocks_per_req]
  *   query_start_loc, seq_lens  device int32 [num_reqs + 1], [num_reqs]; requests without new
  *                  tokens are allowed, and rows behind the last request's: those of `selected`
@@ -632,7 +632,7 @@ PKA_API pka_status pka_select_pages(const void *q, const int8_t *bounds, const f
  *   q, out         device bf16 [num_tokens, Hq, d];  lse device float32 [num_tokens, Hq], or NULL
  *   k_cache, v_cache  device [num_blocks, Hkv, block_size, d] bf16; _fp8: E4M3 codes with
  *                  k_scale and v_scale (finite, > 0); q of any finite magnitude (elements below
- *                  2^-22 of their head's largest are rounded)
+ *                  2^-22 of their head's largest are rounded). Scores are float32, over either cache.
  *   block_table, query_start_loc, seq_lens, max_seq_len  as in pka_select_pages (rows behind
  *                  the last request are left as they are)
  *   selected       device int32 [num_tokens, Hkv, num_pages]
