@@ -1,8 +1,8 @@
 """Builds libpka.so (the CUDA kernels + C ABI) in-tree for sm_103a.
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then the
-objects are linked into paged_kv_attention_07_gb300/_build/libpka.so. Where torch is
-installed, the calls with torch tensors (csrc/torch_calls.cpp) become a Python module beside it.
+objects are linked into paged_kv_attention_07_gb300/_build/libpka.so. Where torch with CUDA
+is installed, the calls with torch tensors (csrc/torch_calls.cpp) become a Python module beside it.
 Nothing is installed outside the repository.
 
     python -m paged_kv_attention_07_gb300.build [--force]
@@ -54,9 +54,10 @@ def _stale(target: str, deps) -> bool:
 
 
 def _torch_dir():
-    """The installed torch's directory, or None: libpka.so itself needs none."""
+    """The directory of the installed torch with CUDA, or None: libpka.so itself needs none."""
     spec = importlib.util.find_spec("torch")
-    return os.path.dirname(spec.origin) if spec and spec.origin else None
+    path = os.path.dirname(spec.origin) if spec and spec.origin else None
+    return path if path and os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
 
 
 def _torch_version(torch_dir: str) -> str:

@@ -25,9 +25,12 @@ def tools(monkeypatch, tmp_path):
     return calls
 
 
-def test_builds_the_library_without_torch(tools, monkeypatch):
+@pytest.mark.parametrize("installed", [False, True])
+def test_builds_the_library_without_torch(tools, monkeypatch, tmp_path, installed):
+    """None at all, or one without CUDA."""
     find_spec = B.importlib.util.find_spec
-    monkeypatch.setattr(B.importlib.util, "find_spec", lambda name: None if name == "torch" else find_spec(name))
+    other = types.SimpleNamespace(origin=str(tmp_path / "torch" / "__init__.py")) if installed else None
+    monkeypatch.setattr(B.importlib.util, "find_spec", lambda name: other if name == "torch" else find_spec(name))
     assert B.build() == B.LIB and os.path.exists(B.LIB)
     assert len(tools) == len(B.sources()) + 1 and all(tool == "nvcc" for tool, _ in tools)
     tools.clear()
