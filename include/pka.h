@@ -78,7 +78,9 @@ typedef enum {
 #define PKA_DEVERR_CAPACITY 0x80        /* the plan outgrew the workspace (inconsistent hints) */
 #define PKA_DEVERR_TIMEOUT 0x100        /* a pipeline wait gave up (bounded spin); results invalid */
 #define PKA_DEVERR_INDEX 0x200          /* pka_gather_rows: a row index outside [0, src_rows); a position past the
-                                           rotation table; a page list that does not ascend up to the token's page */
+                                           rotation table; a page list that does not ascend up to the token's page;
+                                           a parent row outside the table; group_starts that do not ascend over the batch */
+#define PKA_DEVERR_LOGITS 0x400         /* pka_beam_select: a beam with a NaN or an infinite score, or a NaN or +infinity among its logits */
 
 /*
  * pka_cache_write -- write the new tokens' K and V rows into the paged cache.
@@ -396,7 +398,12 @@ typedef enum {
     PKA_KERNEL_PAGE_BOUNDS = 11,    /* pka_page_bounds */
     PKA_KERNEL_PAGE_SELECT = 12,    /* pka_select_pages */
     PKA_KERNEL_SPARSE_ATTN = 13,    /* pka_sparse_attn_forward(_fp8) */
-    PKA_KERNEL_COUNT = 14
+    PKA_KERNEL_BEAM_SELECT = 14,    /* pka_beam_select */
+    PKA_KERNEL_FORK_PAGES = 15,     /* pka_fork_pages */
+    PKA_KERNEL_COPY_PAGES = 16,     /* pka_copy_pages */
+    PKA_KERNEL_PREFIX_ATTN = 17,    /* pka_prefix_attn_forward(_fp8), the attention */
+    PKA_KERNEL_PREFIX_JOIN = 18,    /* ... and the join of its pieces */
+    PKA_KERNEL_COUNT = 19
 } pka_kernel;
 
 /* enable != 0 turns timing on for `kernel` (and resets it); 0 turns it off. */
@@ -655,6 +662,178 @@ PKA_API pka_status pka_sparse_attn_forward_fp8(const void *q, const void *k_cach
                                                int64_t num_blocks, int block_size, float scale, float k_scale,
                                                float v_scale, const int32_t *selected, int num_pages, int max_seq_len,
                                                void *out, float *lse, int32_t *error_word, void *stream);
+
+/*
+ * Shared pages
+ * ------------
+ * Requests that have their first tokens in common (the beams or samples of one
+ * prompt, the users of one system prompt) hold the same pages for them. One step
+ * of beam search over such pages:
+ *   pka_prefix_attn_forward   attention that reads common tokens once per group
+ *   pka_beam_select           the best continuations of each group's beams
+ *   pka_fork_pages            block tables of the chosen beams: pages shared,
+ *                             counted and freed, partly filled ones to be copied
+ *   pka_copy_pages            those copies, in the caches of all layers
+ * next to the calls above (pka_step_tables takes the new tokens' pages from the
+ * same free list). They take an `error_word` as the block-sparse step's calls do,
+ * may be captured, and outputs must not overlap inputs or each other unless a
+ * call says otherwise.
+ */
+
+/*
+ * pka_beam_select -- the num_out best continuations of each group of num_beams
+ * beams. Row b = g * num_beams + i holds the logits x_b of beam i of group g;
+ * the candidate (b, v) has
+ *     score(b, v) = scores[b] + x_b[v] - log(sum_u exp(x_b[u]))
+ * A finished beam has one candidate, (b, end_token) with scores[b] itself (its
+ * logits are not read). Candidates of score -infinity do not count (a beam of
+ * score -infinity has none and is not read). The others are taken by
+ * descending score; of equal ones the lower beam's, then the larger logit's,
+ * then the lower token. Scores are compared in 64 bits, the logarithm of a row's
+ * sum (of 32-bit exponentials) being the same for equal rows of one call. The
+ * k-th best of group g:
+ *     out_scores[g][k]    its score, rounded to 32 bits
+ *     parents[g][k] = b   (a row of the logits, and of the tables of the beams)
+ *     tokens[g][k] = v
+ *     out_finished[g][k] = 1 when beam b is finished or v == end_token, else 0
+ * and where there are fewer than num_out: -infinity, -1, -1, 0.
+ * A beam whose score is NaN or +infinity, or that is not finished and has a NaN or
+ * +infinity among its logits, has no candidate and sets PKA_DEVERR_LOGITS.
+ *
+ *   logits         device [num_groups * num_beams, vocab_size], row_stride elements apart
+ *                  (>= vocab_size), io_dtype 0 = float32, 1 = bf16; any alignment of whole elements
+ *   scores         device float32 [num_groups, num_beams]
+ *   finished       device uint8 [num_groups, num_beams] (0 or not), or NULL: none is
+ *   end_token      a token, or -1: none (then finished must be NULL)
+ *   out_scores     device float32, parents, tokens device int32, out_finished device uint8 or
+ *                  NULL, all [num_groups, num_out]; scores and finished may be written in place
+ *                  when num_out == num_beams
+ * num_beams, num_out <= 64, vocab_size <= 2^26, num_groups * num_beams <= 2^24, else PKA_ERR_UNSUPPORTED.
+ */
+PKA_API pka_status pka_beam_select(const void *logits, int io_dtype, int64_t row_stride, const float *scores,
+                                   const uint8_t *finished, int num_groups, int num_beams, int vocab_size,
+                                   int end_token, int num_out, float *out_scores, int32_t *parents, int32_t *tokens,
+                                   uint8_t *out_finished, int32_t *error_word, void *stream);
+
+/*
+ * pka_fork_pages -- the next step's block table, whose row i goes on from row
+ * parents[i] of this step's: requests that fork, that change places and that
+ * end, in one call. Row r of the table holds h_r = ceil(ctx_lens[r] / bs) pages,
+ * bs = block_size. With p = parents[i] (negative: an empty row)
+ *     ctx_lens_out[i] = ctx_lens[p] (0 without a parent)
+ *     block_table_out[i][c] = block_table[p][c],  0 <= c < h_p
+ * but where ctx_lens[p] is not a multiple of bs, only the first row that goes on
+ * from p keeps its last page; each other one takes a page from the free list in
+ * its place, to be filled by pka_copy_pages:
+ *     block_table_out[i][h_p - 1] = copy_dst[i] = free_pages[head + j],  head = *free_head,
+ *     copy_src[i] = block_table[p][h_p - 1]
+ * j counting such rows i in order, F of them; copy_src[i] = copy_dst[i] = -1 for
+ * the others. Entries from h_p on stay as they are.
+ *     share_counts[b]   how many table entries hold page b, less one (0 of a free page)
+ * is brought up to date; a page that no row holds any longer is freed: with R
+ * such pages, in the order of their first places in block_table (row by row),
+ *     free_pages[head + F - R + k] = the k-th of them,   *free_head_out = head + F - R
+ * (the pages that pka_step_tables takes have count 0, as they must). A partly
+ * filled page is held by one row, as these calls leave it. Negative table
+ * entries are no pages: they are passed on, not counted (nor copied). An id past
+ * num_blocks likewise, and sets PKA_DEVERR_BLOCK_ID.
+ *
+ *   parents        device int32 [num_rows_out]
+ *   ctx_lens       device int32 [num_rows]
+ *   block_table    device int32 [num_rows, max_blocks_per_req]
+ *   share_counts   device int32 [num_blocks], updated
+ *   free_pages     device int32 [num_free_pages], of which [head, num_free_pages) are free; updated
+ *   free_head, free_head_out  device int32; may be the same address
+ *   ctx_lens_out, copy_src, copy_dst  device int32 [num_rows_out]
+ *   block_table_out  device int32 [num_rows_out, max_blocks_per_req]
+ * All or nothing: a parent >= num_rows (PKA_DEVERR_INDEX), a length that is
+ * negative (PKA_DEVERR_SEQ_LEN) or does not fit the table
+ * (PKA_DEVERR_BLOCK_TABLE), or too few free pages (PKA_DEVERR_CAPACITY) set the
+ * bit: ctx_lens_out is 0, copy_src and copy_dst are -1, counts, list and head
+ * stay as they are, and block_table_out is unspecified. A list without room for
+ * the freed pages in front (one that they were not taken from) sets
+ * PKA_DEVERR_CAPACITY too: those without room are lost.
+ * num_rows, num_rows_out <= 4096, max_blocks_per_req * block_size <= INT32_MAX, num_rows * max_blocks_per_req
+ * <= 2^30, num_blocks <= INT32_MAX, else PKA_ERR_UNSUPPORTED.
+ */
+PKA_API pka_status pka_fork_pages(const int32_t *parents, int num_rows_out, const int32_t *ctx_lens,
+                                  const int32_t *block_table, int num_rows, int max_blocks_per_req, int block_size,
+                                  int32_t *share_counts, int64_t num_blocks, int32_t *free_pages, int num_free_pages,
+                                  const int32_t *free_head, int32_t *free_head_out, int32_t *ctx_lens_out,
+                                  int32_t *block_table_out, int32_t *copy_src, int32_t *copy_dst,
+                                  int32_t *error_word, void *stream);
+
+/*
+ * pka_copy_pages -- page copy_dst[i] = page copy_src[i] in each of num_caches
+ * caches, bit for bit. A pair with a negative entry is skipped; one with an entry
+ * past num_blocks too, with PKA_DEVERR_BLOCK_ID. No page may be written by two
+ * pairs, or written by one and read by another (what it then holds is unspecified).
+ *
+ *   caches        host array of num_caches device pointers (read before the call returns), each
+ *                 to [num_blocks] pages of page_bytes, 16-byte aligned
+ *   page_bytes    a multiple of 16
+ *   copy_src, copy_dst  device int32 [num_pairs]
+ * num_caches <= PKA_MAX_COPY_CACHES, page_bytes <= 2^30, num_pairs <= 2^24, else PKA_ERR_UNSUPPORTED.
+ */
+#define PKA_MAX_COPY_CACHES 256
+PKA_API pka_status pka_copy_pages(void *const *caches, int num_caches, int64_t num_blocks, int64_t page_bytes,
+                                  const int32_t *copy_src, const int32_t *copy_dst, int num_pairs,
+                                  int32_t *error_word, void *stream);
+
+/*
+ * pka_prefix_attn_forward / _fp8 -- attention of each new token over all its
+ * request's keys (the definition of pka_paged_attn_forward, with any number of
+ * new tokens per request in any order) for groups of requests whose first tokens
+ * are the same: the keys and values of a group's common tokens are read once for
+ * all its query rows, those of the rest by each request, and the parts joined.
+ * Group j is the requests [group_starts[j], group_starts[j + 1]), and the keys
+ * and values at positions [0, prefix_lens[j]) are read through the block table
+ * row of the first of them that has new tokens; the other rows' entries for these
+ * positions are not used. A group of one, or a prefix of 0, is plain attention. Reads
+ * only the cache (the new tokens' keys and values must have been written).
+ *
+ *   q, out         device bf16 [num_tokens, Hq, d];  lse device float32 [num_tokens, Hq], or NULL
+ *   k_cache, v_cache  device [num_blocks, Hkv, block_size, d] bf16; _fp8: E4M3 codes with
+ *                  k_scale and v_scale (finite, > 0)
+ *   block_table    device int32 [num_reqs, max_blocks_per_req]
+ *   query_start_loc, seq_lens  device int32 [num_reqs + 1], [num_reqs]; requests without new
+ *                  tokens are allowed (their lengths are not looked at), and rows of q behind the
+ *                  last request's: those of out and lse are left as they are
+ *   group_starts   device int32 [num_groups + 1]: from 0 to num_reqs, not descending
+ *   prefix_lens    device int32 [num_groups]: at least 0 and at most every request's
+ *                  seq_len - query_len (the tokens before its new ones)
+ *   scale          finite and > 0
+ *   max_query_len, max_seq_len  host upper bounds of the requests' new tokens and lengths
+ *   workspace      device scratch of >= pka_prefix_workspace_size(...) bytes, 256-byte aligned,
+ *                  for this call alone while it runs (nothing in it is kept between calls)
+ * query_start_loc that does not ascend from 0 to at most num_tokens or passes
+ * max_query_len (PKA_DEVERR_QUERY_START_LOC, PKA_DEVERR_QUERY_LEN), a seq_len that
+ * does not fit (PKA_DEVERR_SEQ_LEN), a prefix that does not (PKA_DEVERR_SEQ_LEN),
+ * group_starts that do not ascend (PKA_DEVERR_INDEX) set the bit and nothing is
+ * written; a block id outside the cache sets PKA_DEVERR_BLOCK_ID.
+ * head_dim 64 or 128 (_fp8: 128), Hq / Hkv <= 16, block_size a power of two in [1, 128], num_reqs <= 4096,
+ * num_groups <= num_reqs, num_blocks * Hkv * block_size <= INT32_MAX, max_seq_len <= 2^30, num_tokens * Hq <=
+ * 2^27, else PKA_ERR_UNSUPPORTED.
+ */
+PKA_API size_t pka_prefix_workspace_size(int num_reqs, int num_groups, int num_tokens, int num_q_heads,
+                                         int num_kv_heads, int head_dim, int max_query_len);
+PKA_API pka_status pka_prefix_attn_forward(const void *q, const void *k_cache, const void *v_cache,
+                                           const int32_t *block_table, int max_blocks_per_req,
+                                           const int32_t *query_start_loc, const int32_t *seq_lens, int num_reqs,
+                                           const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,
+                                           int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                           int64_t num_blocks, int block_size, float scale, int max_query_len,
+                                           int max_seq_len, void *out, float *lse, void *workspace,
+                                           size_t workspace_bytes, int32_t *error_word, void *stream);
+PKA_API pka_status pka_prefix_attn_forward_fp8(const void *q, const void *k_cache, const void *v_cache,
+                                               const int32_t *block_table, int max_blocks_per_req,
+                                               const int32_t *query_start_loc, const int32_t *seq_lens, int num_reqs,
+                                               const int32_t *group_starts, const int32_t *prefix_lens,
+                                               int num_groups, int num_tokens, int num_q_heads, int num_kv_heads,
+                                               int head_dim, int64_t num_blocks, int block_size, float scale,
+                                               float k_scale, float v_scale, int max_query_len, int max_seq_len,
+                                               void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                               int32_t *error_word, void *stream);
 
 /*
  * pka_selftest_wait -- the library's bounded pipeline wait (the one every

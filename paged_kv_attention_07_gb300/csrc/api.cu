@@ -48,6 +48,12 @@ cudaError_t launch_qk_rope(const QkRopeParams& p, bool fp8, int num_sms, cudaStr
 cudaError_t launch_page_bounds(PageBoundsParams p, bool fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, bool fp8, int num_sms, cudaStream_t stream);
+cudaError_t launch_beam_select(const BeamSelectParams& p, bool bf16, int num_sms, cudaStream_t stream);
+cudaError_t launch_fork_pages(const ForkPagesParams& p, cudaStream_t stream);
+cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t stream);
+cudaError_t launch_prefix_attn(const PrefixMaps& maps, const PrefixParams& p, int head_dim, bool fp8, int ncta,
+                               cudaStream_t stream);
+cudaError_t launch_prefix_join(const PrefixParams& p, int head_dim, int ncta, cudaStream_t stream);
 
 // MLA decode units per (request, split): on the tensor-core kernel two value
 // halves per group of 128 heads, otherwise one unit per 64-head group.
@@ -144,6 +150,22 @@ bool encode_tokens(CUtensorMap* map, const void* base, uint64_t T, uint64_t H, u
     cuuint64_t dims[3] = {D, H, T};
     cuuint64_t strides[2] = {D * 2, H * D * 2};
     cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D bf16 view of a token-major tensor [T, H, D] read in boxes of 64 columns x
+// `heads` heads x `tokens` tokens (128-byte swizzle): the rows of a group of
+// heads of consecutive tokens.
+bool encode_head_rows(CUtensorMap* map, const void* base, uint64_t T, uint64_t H, uint64_t D, uint32_t heads,
+                      uint32_t tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {D, H, T};
+    cuuint64_t strides[2] = {D * 2, H * D * 2};
+    cuuint32_t box[3] = {64, heads, tokens};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1362,6 +1384,299 @@ pka_status pka_sparse_attn_forward_fp8(const void* q, const void* k_cache, const
                             num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, selected,
                             num_pages, max_seq_len, out, lse, error_word, stream,
                             CacheFormat{true, k_scale, v_scale});
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- shared pages
+
+namespace {
+
+struct PrefixLayout {
+    int tpt, own0, rows_pre, rows_own;
+    size_t off_cost, off_unit, off_po_pre, off_pl_pre, off_po_own, off_pl_own, total;
+};
+
+// Sizes that the call has a kernel for.
+pka_status check_prefix_sizes(int num_reqs, int num_groups, int num_tokens, int Hq, int Hkv, int head_dim,
+                              int max_query_len) {
+    if (num_reqs <= 0 || num_groups <= 0 || num_tokens < 0 || Hq <= 0 || Hkv <= 0 || head_dim <= 0 ||
+        max_query_len <= 0 || Hq % Hkv != 0 || num_groups > num_reqs)
+        return PKA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PKA_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 16 || Hkv > 65535 || num_reqs > kMaxRequests) return PKA_ERR_UNSUPPORTED;
+    if ((int64_t)num_tokens * Hq > (1 << 27)) return PKA_ERR_UNSUPPORTED;
+    return PKA_OK;
+}
+
+// A piece's slot is its unit's number plus its CTA's, so there are as many as units and CTAs together.
+PrefixLayout prefix_layout(int num_reqs, int num_groups, int num_tokens, int Hq, int Hkv, int head_dim,
+                           int max_query_len, int ncta) {
+    PrefixLayout L;
+    const int G = Hq / Hkv;
+    L.tpt = 128 / G;
+    L.own0 = (num_groups + 31) / 32 * 32;
+    const auto rows = [&](int64_t tokens) { return (int)std::min<int64_t>(128, (tokens * G + 7) / 8 * 8); };
+    L.rows_pre = rows(std::max(1, num_tokens));
+    L.rows_own = rows(std::max(1, std::min(max_query_len, num_tokens)));
+    const int64_t full = num_tokens / L.tpt;  // units of one row tile, where there are most
+    const size_t slots_pre = (size_t)((full + num_groups) * Hkv + ncta), slots_own = (size_t)((full + num_reqs) * Hkv + ncta);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = align256(off + bytes);
+        return o;
+    };
+    L.off_cost = take(sizeof(long long) * ((size_t)L.own0 + num_reqs + 1));
+    L.off_unit = take(sizeof(int) * ((size_t)L.own0 + num_reqs));
+    L.off_po_pre = take(sizeof(float) * slots_pre * 2 * L.rows_pre * head_dim);
+    L.off_pl_pre = take(sizeof(float) * slots_pre * 2 * L.rows_pre);
+    L.off_po_own = take(sizeof(float) * slots_own * 2 * L.rows_own * head_dim);
+    L.off_pl_own = take(sizeof(float) * slots_own * 2 * L.rows_own);
+    L.total = off;
+    return L;
+}
+
+pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            int max_blocks_per_req, const int32_t* query_start_loc, const int32_t* seq_lens,
+                            int num_reqs, const int32_t* group_starts, const int32_t* prefix_lens, int num_groups,
+                            int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int64_t num_blocks,
+                            int block_size, float scale, int max_query_len, int max_seq_len, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, int32_t* error_word, void* stream,
+                            const CacheFormat& cf) {
+    const pka_status sc = check_prefix_sizes(num_reqs, num_groups, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                             max_query_len);
+    if (sc == PKA_ERR_INVALID_ARG) return sc;
+    if (max_blocks_per_req <= 0 || num_blocks <= 0 || block_size <= 0 || max_seq_len <= 0) return PKA_ERR_INVALID_ARG;
+    if (!positive_finite(scale)) return PKA_ERR_INVALID_ARG;
+    if (cf.fp8 && (!positive_finite(cf.k_scale) || !positive_finite(cf.v_scale))) return PKA_ERR_INVALID_ARG;
+    if ((int64_t)max_blocks_per_req * block_size < max_seq_len) return PKA_ERR_INVALID_ARG;
+    if (sc != PKA_OK) return sc;
+    if (cf.fp8 && head_dim != 128) return PKA_ERR_UNSUPPORTED;
+    if (!pow2(block_size) || block_size > 128 || max_seq_len > (1 << 30)) return PKA_ERR_UNSUPPORTED;
+    if (num_blocks > INT32_MAX || num_blocks * block_size > INT32_MAX / num_kv_heads) return PKA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKA_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !query_start_loc || !seq_lens || !group_starts || !prefix_lens ||
+        !out || !workspace)
+        return PKA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(block_table, 4) || !aligned(query_start_loc, 4) || !aligned(seq_lens, 4) ||
+        !aligned(group_starts, 4) || !aligned(prefix_lens, 4) || !aligned(workspace, 256) || !aligned(error_word, 4))
+        return PKA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PKA_ERR_CUDA;
+    const PrefixLayout L = prefix_layout(num_reqs, num_groups, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                         max_query_len, sms);
+    if (workspace_bytes < L.total) return PKA_ERR_WORKSPACE_TOO_SMALL;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    PrefixParams p;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_table = block_table;
+    p.qsl = query_start_loc;
+    p.seq_lens = seq_lens;
+    p.starts = group_starts;
+    p.prefix = prefix_lens;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.err = error_word;
+    p.seg_cost = reinterpret_cast<long long*>(ws + L.off_cost);
+    p.seg_unit = reinterpret_cast<int*>(ws + L.off_unit);
+    p.po_pre = reinterpret_cast<float*>(ws + L.off_po_pre);
+    p.pl_pre = reinterpret_cast<float*>(ws + L.off_pl_pre);
+    p.po_own = reinterpret_cast<float*>(ws + L.off_po_own);
+    p.pl_own = reinterpret_cast<float*>(ws + L.off_pl_own);
+    p.num_blocks = num_blocks;
+    p.rows_pre = L.rows_pre;
+    p.rows_own = L.rows_own;
+    p.B = num_reqs;
+    p.groups = num_groups;
+    p.own0 = L.own0;
+    p.T = num_tokens;
+    p.max_blocks = max_blocks_per_req;
+    p.Hq = num_q_heads;
+    p.Hkv = num_kv_heads;
+    p.G = num_q_heads / num_kv_heads;
+    p.tpt = L.tpt;
+    p.upt = cf.fp8 ? L.tpt : 2 * L.tpt;
+    p.bs = block_size;
+    p.bs_log2 = log2_of(block_size);
+    p.max_query = max_query_len;
+    p.max_seq = max_seq_len;
+    p.scale_log2 = scale * 1.4426950408889634f * (cf.fp8 ? cf.k_scale : 1.f);
+    p.v_scale = cf.fp8 ? cf.v_scale : 1.f;
+    PrefixMaps maps;
+    const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * block_size;
+    const auto encode_cache = [&](CUtensorMap* map, const void* cache) {
+        return cf.fp8 ? encode_rows_u8(map, cache, rows, block_size) : encode_rows(map, cache, rows, head_dim, block_size);
+    };
+    if (!encode_head_rows(&maps.q, q, num_tokens, num_q_heads, head_dim, (uint32_t)p.G, (uint32_t)p.tpt) ||
+        !encode_cache(&maps.k, k_cache) || !encode_cache(&maps.v, v_cache))
+        return PKA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e =
+        timed(PKA_KERNEL_PREFIX_ATTN, st, [&] { return launch_prefix_attn(maps, p, head_dim, cf.fp8, sms, st); });
+    if (e == cudaSuccess)
+        e = timed(PKA_KERNEL_PREFIX_JOIN, st, [&] { return launch_prefix_join(p, head_dim, sms, st); });
+    return cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+pka_status pka_beam_select(const void* logits, int io_dtype, int64_t row_stride, const float* scores,
+                           const uint8_t* finished, int num_groups, int num_beams, int vocab_size, int end_token,
+                           int num_out, float* out_scores, int32_t* parents, int32_t* tokens, uint8_t* out_finished,
+                           int32_t* error_word, void* stream) {
+    if (num_groups < 0 || num_beams <= 0 || vocab_size <= 0 || num_out <= 0 || (io_dtype != 0 && io_dtype != 1))
+        return PKA_ERR_INVALID_ARG;
+    if (end_token < -1 || end_token >= vocab_size || (finished && end_token < 0) || row_stride < vocab_size)
+        return PKA_ERR_INVALID_ARG;
+    if (num_beams > kMaxBeams || num_out > kMaxBeams || vocab_size > kMaxVocab) return PKA_ERR_UNSUPPORTED;
+    if ((int64_t)num_groups * num_beams > (1 << 24)) return PKA_ERR_UNSUPPORTED;
+    if (row_stride > INT64_MAX / 4 / (1 << 24)) return PKA_ERR_INVALID_ARG;
+    if (num_groups == 0) return PKA_OK;
+    if (!logits || !scores || !out_scores || !parents || !tokens) return PKA_ERR_INVALID_ARG;
+    if (!aligned(logits, io_dtype ? 2 : 4) || !aligned(scores, 4) || !aligned(out_scores, 4) || !aligned(parents, 4) ||
+        !aligned(tokens, 4) || !aligned(error_word, 4))
+        return PKA_ERR_INVALID_ARG;
+    // (a group's scores are read until its own are written, not another group's)
+    if (num_out != num_beams && (out_scores == scores || (finished && out_finished == finished)))
+        return PKA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PKA_ERR_CUDA;
+    BeamSelectParams p;
+    p.logits = logits;
+    p.scores = scores;
+    p.finished = finished;
+    p.out_scores = out_scores;
+    p.parents = parents;
+    p.tokens = tokens;
+    p.out_finished = out_finished;
+    p.err = error_word;
+    p.row_stride = row_stride;
+    p.groups = num_groups;
+    p.beams = num_beams;
+    p.vocab = vocab_size;
+    p.end_token = end_token;
+    p.keep = num_out;
+    p.slices = p.slice_len = 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(
+        timed(PKA_KERNEL_BEAM_SELECT, st, [&] { return launch_beam_select(p, io_dtype == 1, sms, st); }));
+}
+
+pka_status pka_fork_pages(const int32_t* parents, int num_rows_out, const int32_t* ctx_lens,
+                          const int32_t* block_table, int num_rows, int max_blocks_per_req, int block_size,
+                          int32_t* share_counts, int64_t num_blocks, int32_t* free_pages, int num_free_pages,
+                          const int32_t* free_head, int32_t* free_head_out, int32_t* ctx_lens_out,
+                          int32_t* block_table_out, int32_t* copy_src, int32_t* copy_dst, int32_t* error_word,
+                          void* stream) {
+    if (num_rows <= 0 || num_rows_out < 0 || max_blocks_per_req <= 0 || block_size <= 0 || num_blocks <= 0 ||
+        num_free_pages < 0)
+        return PKA_ERR_INVALID_ARG;
+    if (!ctx_lens || !block_table || !share_counts || !free_head || !free_head_out ||
+        (num_free_pages > 0 && !free_pages))
+        return PKA_ERR_INVALID_ARG;
+    if (num_rows_out > 0 && (!parents || !ctx_lens_out || !block_table_out || !copy_src || !copy_dst))
+        return PKA_ERR_INVALID_ARG;
+    if (num_rows_out > 0 && (ctx_lens_out == ctx_lens || block_table_out == block_table)) return PKA_ERR_INVALID_ARG;
+    if (num_rows > kMaxRequests || num_rows_out > kMaxRequests || num_blocks > INT32_MAX) return PKA_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_req * block_size > INT32_MAX || (int64_t)num_rows * max_blocks_per_req > (1 << 30))
+        return PKA_ERR_UNSUPPORTED;
+    for (const int32_t* x : {parents, ctx_lens, block_table, static_cast<const int32_t*>(share_counts),
+                             static_cast<const int32_t*>(free_pages), free_head,
+                             static_cast<const int32_t*>(free_head_out), static_cast<const int32_t*>(ctx_lens_out),
+                             static_cast<const int32_t*>(block_table_out), static_cast<const int32_t*>(copy_src),
+                             static_cast<const int32_t*>(copy_dst), static_cast<const int32_t*>(error_word)})
+        if (!aligned(x, 4)) return PKA_ERR_INVALID_ARG;
+    ForkPagesParams p;
+    p.parents = parents;
+    p.ctx_lens = ctx_lens;
+    p.block_table = block_table;
+    p.share_counts = share_counts;
+    p.free_pages = free_pages;
+    p.free_head = free_head;
+    p.free_head_out = free_head_out;
+    p.ctx_lens_out = ctx_lens_out;
+    p.block_table_out = block_table_out;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    p.err = error_word;
+    p.num_rows = num_rows;
+    p.num_rows_out = num_rows_out;
+    p.max_blocks = max_blocks_per_req;
+    p.block_size = block_size;
+    p.num_blocks = (int)num_blocks;
+    p.num_free = num_free_pages;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed(PKA_KERNEL_FORK_PAGES, st, [&] { return launch_fork_pages(p, st); }));
+}
+
+pka_status pka_copy_pages(void* const* caches, int num_caches, int64_t num_blocks, int64_t page_bytes,
+                          const int32_t* copy_src, const int32_t* copy_dst, int num_pairs, int32_t* error_word,
+                          void* stream) {
+    if (num_caches < 0 || num_blocks <= 0 || page_bytes <= 0 || page_bytes % 16 != 0 || num_pairs < 0)
+        return PKA_ERR_INVALID_ARG;
+    if (num_caches > PKA_MAX_COPY_CACHES || page_bytes > (1 << 30) || num_pairs > (1 << 24) || num_blocks > INT32_MAX)
+        return PKA_ERR_UNSUPPORTED;
+    if (num_caches > 0 && !caches) return PKA_ERR_INVALID_ARG;
+    for (int i = 0; i < num_caches; ++i)
+        if (!caches[i] || !aligned(caches[i], 16)) return PKA_ERR_INVALID_ARG;
+    if (num_caches == 0 || num_pairs == 0) return PKA_OK;
+    if (!copy_src || !copy_dst || !aligned(copy_src, 4) || !aligned(copy_dst, 4) || !aligned(error_word, 4))
+        return PKA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PKA_ERR_CUDA;
+    CopyPagesParams p = {};
+    for (int i = 0; i < num_caches; ++i) p.caches[i] = static_cast<uint8_t*>(caches[i]);
+    p.src = copy_src;
+    p.dst = copy_dst;
+    p.err = error_word;
+    p.page_bytes = page_bytes;
+    p.num_blocks = (int)num_blocks;
+    p.num_caches = num_caches;
+    p.num_pairs = num_pairs;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed(PKA_KERNEL_COPY_PAGES, st, [&] { return launch_copy_pages(p, sms, st); }));
+}
+
+size_t pka_prefix_workspace_size(int num_reqs, int num_groups, int num_tokens, int num_q_heads, int num_kv_heads,
+                                 int head_dim, int max_query_len) {
+    if (check_prefix_sizes(num_reqs, num_groups, num_tokens, num_q_heads, num_kv_heads, head_dim, max_query_len) !=
+        PKA_OK)
+        return 0;
+    const int sms = device_sm_count();
+    if (sms <= 0) return 0;
+    return prefix_layout(num_reqs, num_groups, num_tokens, num_q_heads, num_kv_heads, head_dim, max_query_len, sms).total;
+}
+
+pka_status pka_prefix_attn_forward(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, int max_blocks_per_req, const int32_t* query_start_loc,
+                                   const int32_t* seq_lens, int num_reqs, const int32_t* group_starts,
+                                   const int32_t* prefix_lens, int num_groups, int num_tokens, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int64_t num_blocks, int block_size, float scale,
+                                   int max_query_len, int max_seq_len, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t* error_word, void* stream) {
+    return prefix_attn_impl(q, k_cache, v_cache, block_table, max_blocks_per_req, query_start_loc, seq_lens, num_reqs,
+                            group_starts, prefix_lens, num_groups, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                            num_blocks, block_size, scale, max_query_len, max_seq_len, out, lse, workspace,
+                            workspace_bytes, error_word, stream, CacheFormat{false, 1.f, 1.f});
+}
+
+pka_status pka_prefix_attn_forward_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_table, int max_blocks_per_req,
+                                       const int32_t* query_start_loc, const int32_t* seq_lens, int num_reqs,
+                                       const int32_t* group_starts, const int32_t* prefix_lens, int num_groups,
+                                       int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                       int64_t num_blocks, int block_size, float scale, float k_scale, float v_scale,
+                                       int max_query_len, int max_seq_len, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, int32_t* error_word, void* stream) {
+    return prefix_attn_impl(q, k_cache, v_cache, block_table, max_blocks_per_req, query_start_loc, seq_lens, num_reqs,
+                            group_starts, prefix_lens, num_groups, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                            num_blocks, block_size, scale, max_query_len, max_seq_len, out, lse, workspace,
+                            workspace_bytes, error_word, stream, CacheFormat{true, k_scale, v_scale});
 }
 
 }  // extern "C"

@@ -208,6 +208,82 @@ struct SparseAttnParams {
     float scale_log2, v_scale;  // 8-bit cache: scale * k_scale, and the output's factor
 };
 
+// ---- shared pages
+
+constexpr int kMaxBeams = 64, kMaxVocab = 1 << 26;
+
+struct BeamSelectParams {
+    const void* logits;  // rows of float32 or bf16, row_stride elements apart
+    const float* scores;
+    const uint8_t* finished;  // or null
+    float* out_scores;
+    int32_t* parents;
+    int32_t* tokens;
+    uint8_t* out_finished;  // or null
+    int32_t* err;
+    int64_t row_stride;
+    int groups, beams, vocab, end_token, keep;
+    int slices, slice_len;  // of a row, set by the launch
+};
+
+struct ForkPagesParams {
+    const int32_t* parents;
+    const int32_t* ctx_lens;
+    const int32_t* block_table;
+    int32_t* share_counts;
+    int32_t* free_pages;
+    const int32_t* free_head;
+    int32_t* free_head_out;
+    int32_t* ctx_lens_out;
+    int32_t* block_table_out;
+    int32_t* copy_src;
+    int32_t* copy_dst;
+    int32_t* err;
+    int num_rows, num_rows_out, max_blocks, block_size, num_blocks, num_free;
+};
+
+struct CopyPagesParams {
+    uint8_t* caches[PKA_MAX_COPY_CACHES];
+    const int32_t* src;
+    const int32_t* dst;
+    int32_t* err;
+    int64_t page_bytes;
+    int num_blocks, num_caches, num_pairs;
+    int pieces;  // of a page, set by the launch
+};
+
+struct PrefixMaps {
+    CUtensorMap q;  // [T, Hq, D]  box {64, G, 128 / G}
+    CUtensorMap k;  // [nb * Hkv * bs, D]  box {64, bs}; codes: box {128, bs}
+    CUtensorMap v;
+};
+
+struct PrefixParams {
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_table;
+    const int32_t* qsl;
+    const int32_t* seq_lens;
+    const int32_t* starts;  // [groups + 1]
+    const int32_t* prefix;  // [groups]
+    __nv_bfloat16* out;
+    float* lse;  // or null
+    int32_t* err;
+    // workspace: each segment's place on the line of costs and of units; the pieces'
+    // sums [slot][d / 4][2 * rows][4] and their log2 [slot][2 * rows], apart for common and own keys
+    long long* seg_cost;  // [own0 + B + 1], the last the total, -1: refused
+    int* seg_unit;
+    float* po_pre;
+    float* pl_pre;
+    float* po_own;
+    float* pl_own;
+    int64_t num_blocks;
+    int rows_pre, rows_own;  // rows of a lane's half of a slot
+    int B, groups, own0, T, max_blocks, Hq, Hkv, G, bs, bs_log2, max_query, max_seq;
+    int tpt, upt;  // tokens of a row tile, and of a unit (one or two)
+    float scale_log2, v_scale;
+};
+
 struct FaMaps {
     CUtensorMap q;     // [T, Hq, D]  box {64, 1, 128}
     CUtensorMap knew;  // [T, Hkv, D] box {64, 1, 128}

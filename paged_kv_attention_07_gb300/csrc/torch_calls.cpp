@@ -1,4 +1,4 @@
-// torch_calls.cpp -- the block-sparse step's entry points called with torch
+// torch_calls.cpp -- the entry points of the block-sparse step and of shared pages called with torch
 // tensors: checks of types, shapes, packing and device, then the C call on the
 // current stream. A Python module of its own next to libpka.so, which stays free
 // of torch: a launch of these calls takes some microseconds, and the checks and
@@ -55,6 +55,7 @@ public:
         }
     }
     void* stream() const { return stream_; }
+    int64_t device() const { return device_; }
 
     const Tensor& tensor(PyObject* o, const char* name, int dims) const {
         if (!THPVariable_Check(o)) {
@@ -315,6 +316,149 @@ PyObject* sparse_attn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// logits, scores, out_scores, parents, tokens, end_token, finished, out_finished, error_word, stream
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const Call c("pka_beam_select", a[9]);
+        const Tensor &x = c.tensor(a[0], "logits", 2), &s = c.tensor(a[1], "scores", 2);
+        const int64_t G = s.size(0), W = s.size(1), V = x.size(1), K = c.tensor(a[2], "out_scores", 2).size(1);
+        for (const int64_t i : {G, W, V, K})
+            if (i > INT32_MAX) refuse("pka_beam_select: a size is out of range");
+        const bool bf16 = x.scalar_type() == kBf16;
+        if ((!bf16 && x.scalar_type() != kF32) || x.get_device() != c.device() || x.size(0) != G * W ||
+            (x.numel() > 0 && V > 1 && x.stride(1) != 1))
+            refuse("pka_beam_select: logits must be BFloat16 or Float rows of packed elements, one for each of scores, on "
+                   "the current CUDA device");
+        const int64_t stride = x.size(0) > 1 ? x.stride(0) : V;
+        auto* scores = as<float>(c.packed(a[1], "scores", kF32, {G, W}));
+        auto* best = as<float>(c.packed(a[2], "out_scores", kF32, {G, K}));
+        auto* parents = as(c.packed(a[3], "parents", kI32, {G, K}));
+        auto* tokens = as(c.packed(a[4], "tokens", kI32, {G, K}));
+        const int end = (int)integer(a[5]);
+        auto* finished = as<uint8_t>(c.packed_or_none(a[6], "finished", kU8, {G, W}));
+        auto* ended = as<uint8_t>(c.packed_or_none(a[7], "out_finished", kU8, {G, K}));
+        int32_t* err = c.word(a[8]);
+        const void* logits = x.data_ptr();
+        return unlocked([&] {
+            return pka_beam_select(logits, bf16 ? 1 : 0, stride, scores, finished, (int)G, (int)W, (int)V, end, (int)K,
+                                   best, parents, tokens, ended, err, c.stream());
+        });
+    });
+}
+
+// parents, ctx_lens, block_table, block_size, share_counts, free_pages, free_head, free_head_out, ctx_lens_out,
+// block_table_out, copy_src, copy_dst, error_word, stream
+PyObject* fork_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 14, [&] {
+        const Call c("pka_fork_pages", a[13]);
+        const Tensor& table = c.tensor(a[2], "block_table", 2);
+        const int64_t B = table.size(0), width = table.size(1), N = c.tensor(a[0], "parents", 1).size(0);
+        const int64_t nb = c.tensor(a[4], "share_counts", 1).size(0), pages = c.tensor(a[5], "free_pages", 1).size(0);
+        for (const int64_t i : {B, width, N, pages})
+            if (i > INT32_MAX) refuse("pka_fork_pages: a size is out of range");
+        const int bs = (int)integer(a[3]);
+        auto* parents = as(c.packed(a[0], "parents", kI32, {N}));
+        auto* ctx = as(c.packed(a[1], "ctx_lens", kI32, {B}));
+        auto* bt = as(c.packed(a[2], "block_table", kI32, {B, width}));
+        auto* counts = as(c.packed(a[4], "share_counts", kI32, {nb}));
+        auto* free = as(c.packed(a[5], "free_pages", kI32, {pages}));
+        auto* head = as(c.packed(a[6], "free_head", kI32, {1}));
+        auto* out = as(c.packed(a[7], "free_head_out", kI32, {1}));
+        auto* ctx_out = as(c.packed(a[8], "ctx_lens_out", kI32, {N}));
+        auto* bt_out = as(c.packed(a[9], "block_table_out", kI32, {N, width}));
+        auto* src = as(c.packed(a[10], "copy_src", kI32, {N}));
+        auto* dst = as(c.packed(a[11], "copy_dst", kI32, {N}));
+        int32_t* err = c.word(a[12]);
+        return unlocked([&] {
+            return pka_fork_pages(parents, (int)N, ctx, bt, (int)B, (int)width, bs, counts, nb, free, (int)pages, head,
+                                  out, ctx_out, bt_out, src, dst, err, c.stream());
+        });
+    });
+}
+
+// caches, copy_src, copy_dst, error_word, stream
+PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&] {
+        const Call c("pka_copy_pages", a[4]);
+        PyObject* caches = PySequence_Fast(a[0], "pka_copy_pages: caches must be a sequence of tensors");
+        if (!caches) throw Raised();
+        struct Hold {
+            PyObject* o;
+            ~Hold() { Py_DECREF(o); }
+        } hold{caches};
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(caches);
+        if (count > PKA_MAX_COPY_CACHES) refuse("pka_copy_pages: too many caches for one call");
+        void* at[PKA_MAX_COPY_CACHES];
+        int64_t nb = 1, page = 16;
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            PyObject* o = PySequence_Fast_GET_ITEM(caches, i);
+            if (!THPVariable_Check(o)) {
+                PyErr_SetString(PyExc_TypeError, "pka_copy_pages: caches must be tensors");
+                throw Raised();
+            }
+            const Tensor& t = THPVariable_Unpack(o);
+            if (t.dim() < 2 || t.get_device() != c.device() || !t.is_contiguous() || t.numel() == 0)
+                refuse("pka_copy_pages: caches must be packed [num_blocks, ...] tensors on the current CUDA device");
+            const int64_t bytes = t.numel() / t.size(0) * (int64_t)t.element_size();
+            if (i > 0 && (t.size(0) != nb || bytes != page))
+                refuse("pka_copy_pages: caches must have the same number of pages, all of one size");
+            nb = t.size(0);
+            page = bytes;
+            at[i] = t.data_ptr();
+        }
+        const int64_t pairs = c.tensor(a[1], "copy_src", 1).size(0);
+        if (pairs > INT32_MAX) refuse("pka_copy_pages: a size is out of range");
+        auto* src = as(c.packed(a[1], "copy_src", kI32, {pairs}));
+        auto* dst = as(c.packed(a[2], "copy_dst", kI32, {pairs}));
+        int32_t* err = c.word(a[3]);
+        return unlocked(
+            [&] { return pka_copy_pages(at, (int)count, nb, page, src, dst, (int)pairs, err, c.stream()); });
+    });
+}
+
+// q, k_cache, v_cache, block_table, query_start_loc, seq_lens, group_starts, prefix_lens, scale, max_query_len,
+// max_seq_len, out, lse, workspace, kv_scales, error_word, stream
+PyObject* prefix_attn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 17, [&] {
+        const Call c("pka_prefix_attn_forward", a[16]);
+        const Tensor &q = c.tensor(a[0], "q", 3), &cache = c.tensor(a[1], "k_cache", 4);
+        const Tensor &table = c.tensor(a[3], "block_table", 2), &work = c.tensor(a[13], "workspace", 1);
+        const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2), nb = cache.size(0), Hkv = cache.size(1);
+        const int64_t bs = cache.size(2), B = table.size(0), width = table.size(1);
+        const int64_t groups = c.tensor(a[7], "prefix_lens", 1).size(0);
+        for (const int64_t x : {T, Hq, d, Hkv, bs, B, width, groups})
+            if (x > INT32_MAX) refuse("pka_prefix_attn_forward: a size is out of range");
+        float scales[2];
+        const bool fp8 = scales_of(a[14], scales);
+        const auto kind = fp8 ? kU8 : kBf16;
+        const float scale = number(a[8]);
+        const int most = (int)integer(a[9]), longest = (int)integer(a[10]);
+        const void* qp = c.packed(a[0], "q", kBf16, {T, Hq, d});
+        const void* kc = c.packed(a[1], "k_cache", kind, {nb, Hkv, bs, d});
+        const void* vc = c.packed(a[2], "v_cache", kind, {nb, Hkv, bs, d});
+        auto* bt = as(c.packed(a[3], "block_table", kI32, {B, width}));
+        auto* qsl = as(c.packed(a[4], "query_start_loc", kI32, {B + 1}));
+        auto* seq = as(c.packed(a[5], "seq_lens", kI32, {B}));
+        auto* starts = as(c.packed(a[6], "group_starts", kI32, {groups + 1}));
+        auto* prefix = as(c.packed(a[7], "prefix_lens", kI32, {groups}));
+        void* out = c.packed(a[11], "out", kBf16, {T, Hq, d});
+        auto* lse = as<float>(c.packed_or_none(a[12], "lse", kF32, {T, Hq}));
+        void* scratch = c.packed(a[13], "workspace", kU8, {work.size(0)});
+        const size_t size = (size_t)work.size(0);
+        int32_t* err = c.word(a[15]);
+        return unlocked([&] {
+            if (fp8)
+                return pka_prefix_attn_forward_fp8(qp, kc, vc, bt, (int)width, qsl, seq, (int)B, starts, prefix,
+                                                   (int)groups, (int)T, (int)Hq, (int)Hkv, (int)d, nb, (int)bs, scale,
+                                                   scales[0], scales[1], most, longest, out, lse, scratch, size, err,
+                                                   c.stream());
+            return pka_prefix_attn_forward(qp, kc, vc, bt, (int)width, qsl, seq, (int)B, starts, prefix, (int)groups,
+                                           (int)T, (int)Hq, (int)Hkv, (int)d, nb, (int)bs, scale, most, longest, out,
+                                           lse, scratch, size, err, c.stream());
+        });
+    });
+}
+
 template <PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
@@ -326,6 +470,10 @@ PyMethodDef methods[] = {
     method<page_bounds>("page_bounds"),
     method<select_pages>("select_pages"),
     method<sparse_attn_forward>("sparse_attn_forward"),
+    method<beam_select>("beam_select"),
+    method<fork_pages>("fork_pages"),
+    method<copy_pages>("copy_pages"),
+    method<prefix_attn_forward>("prefix_attn_forward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

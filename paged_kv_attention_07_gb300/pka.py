@@ -1,5 +1,5 @@
-"""Binding of libpka.so (include/pka.h): ctypes, and for the calls of the block-sparse step a module that
-takes the tensors themselves (csrc/torch_calls.cpp). Argument marshalling only.
+"""Binding of libpka.so (include/pka.h): ctypes, and for the calls of the block-sparse step and of shared pages a module
+that takes the tensors themselves (csrc/torch_calls.cpp). Argument marshalling only.
 
 Every function has the C entry point's name and meaning; tensors are torch
 CUDA tensors whose shapes give the sizes, streams default to torch's current
@@ -19,17 +19,20 @@ STATUS_NAMES = {0: "PKA_OK", 1: "PKA_ERR_INVALID_ARG", 2: "PKA_ERR_UNSUPPORTED",
                 3: "PKA_ERR_WORKSPACE_TOO_SMALL", 4: "PKA_ERR_CUDA", 5: "PKA_ERR_DEVICE_METADATA"}
 DEVERR = {"QUERY_START_LOC": 0x01, "SEQ_LEN": 0x02, "ORDER": 0x04, "QUERY_LEN": 0x08,
           "BLOCK_TABLE": 0x10, "BLOCK_ID": 0x20, "SLOT": 0x40, "CAPACITY": 0x80, "TIMEOUT": 0x100,
-          "INDEX": 0x200}
+          "INDEX": 0x200, "LOGITS": 0x400}
 EXPORTED = ("pka_cache_write", "pka_cache_write_fp8", "pka_workspace_size", "pka_workspace_size_fp8",
             "pka_paged_attn_forward",
             "pka_paged_attn_forward_fp8", "pka_paged_attn_step", "pka_paged_attn_step_fp8",
             "pka_merge_attn_states", "pka_get_error", "pka_paged_decode_noalloc", "pka_kernel_timer",
             "pka_kernel_timer_read", "pka_batch_order", "pka_gather_rows", "pka_selftest_wait",
             "pka_status_string", "pka_step_tables", "pka_qk_rope_cache_write", "pka_qk_rope_cache_write_fp8",
-            "pka_page_bounds", "pka_select_pages", "pka_sparse_attn_forward", "pka_sparse_attn_forward_fp8")
+            "pka_page_bounds", "pka_select_pages", "pka_sparse_attn_forward", "pka_sparse_attn_forward_fp8",
+            "pka_beam_select", "pka_fork_pages", "pka_copy_pages", "pka_prefix_workspace_size",
+            "pka_prefix_attn_forward", "pka_prefix_attn_forward_fp8")
 KERNELS = {"cache_write": 0, "planner": 1, "decode": 2, "decode_reduce": 3, "prefill_extend": 4,
            "extend_reduce": 5, "merge": 6, "gather": 7, "ctx_dequant": 8, "step_tables": 9, "qk_rope": 10,
-           "page_bounds": 11, "page_select": 12, "sparse_attn": 13}
+           "page_bounds": 11, "page_select": 12, "sparse_attn": 13, "beam_select": 14, "fork_pages": 15,
+           "copy_pages": 16, "prefix_attn": 17, "prefix_join": 18}
 
 
 class PkaError(RuntimeError):
@@ -121,6 +124,22 @@ def load(path: str | None = None):
     lib.pka_sparse_attn_forward.argtypes = sparse + tail
     lib.pka_sparse_attn_forward_fp8.restype = i32
     lib.pka_sparse_attn_forward_fp8.argtypes = sparse + [f32, f32] + tail
+    lib.pka_beam_select.restype = i32
+    lib.pka_beam_select.argtypes = [P, i32, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P, P, P]
+    lib.pka_fork_pages.restype = i32
+    lib.pka_fork_pages.argtypes = [P, i32, P, P, i32, i32, i32, P, i64, P, i32, P, P, P, P, P, P, P, P]
+    lib.pka_copy_pages.restype = i32
+    lib.pka_copy_pages.argtypes = [P, i32, i64, i64, P, P, i32, P, P]
+    lib.pka_prefix_workspace_size.restype = sz
+    lib.pka_prefix_workspace_size.argtypes = [i32] * 7
+    # q, k_cache, v_cache, block_table, max_blocks, qsl, seq_lens, B, group_starts, prefix_lens, groups, T, Hq, Hkv, d,
+    # num_blocks, bs, scale, [k_scale, v_scale,] max_query_len, max_seq_len, out, lse, ws, ws_bytes, error_word, stream
+    prefix = [P, P, P, P, i32, P, P, i32, P, P, i32, i32, i32, i32, i32, i64, i32, f32]
+    tail = [i32, i32, P, P, P, sz, P, P]
+    lib.pka_prefix_attn_forward.restype = i32
+    lib.pka_prefix_attn_forward.argtypes = prefix + tail
+    lib.pka_prefix_attn_forward_fp8.restype = i32
+    lib.pka_prefix_attn_forward_fp8.argtypes = prefix + [f32, f32] + tail
     if path is None:
         _lib = lib
     return lib
@@ -370,6 +389,47 @@ def pka_sparse_attn_forward(q, k_cache, v_cache, block_table, query_start_loc, s
     _check(_calls().sparse_attn_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, selected, scale,
                                         max_seq_len, out, lse, kv_scales, error_word, stream),
            "pka_sparse_attn_forward")
+
+
+def pka_beam_select(logits, scores, out_scores, parents, tokens, end_token=-1, finished=None, out_finished=None,
+                    error_word=None, stream=None):
+    """logits [G * W, V] float32 or bf16, rows of packed elements any distance apart; scores [G, W] float32; out_scores
+    [G, K] float32, parents (rows of the logits), tokens [G, K] int32; finished [G, W], out_finished [G, K] uint8 or None."""
+    _check(_calls().beam_select(logits, scores, out_scores, parents, tokens, end_token, finished, out_finished,
+                                error_word, stream), "pka_beam_select")
+
+
+def pka_fork_pages(parents, ctx_lens, block_table, block_size, share_counts, free_pages, free_head, free_head_out,
+                   ctx_lens_out, block_table_out, copy_src, copy_dst, error_word=None, stream=None):
+    """parents [N] int32 (rows of the table, or -1); ctx_lens [B], block_table [B, max_blocks] int32; share_counts
+    [num_blocks], free_pages [n] int32 (both updated), free_head / free_head_out [1] int32 (may be the same tensor);
+    ctx_lens_out, copy_src, copy_dst [N], block_table_out [N, max_blocks] int32."""
+    _check(_calls().fork_pages(parents, ctx_lens, block_table, block_size, share_counts, free_pages, free_head,
+                               free_head_out, ctx_lens_out, block_table_out, copy_src, copy_dst, error_word, stream),
+           "pka_fork_pages")
+
+
+def pka_copy_pages(caches, copy_src, copy_dst, error_word=None, stream=None):
+    """caches: a sequence of packed [num_blocks, ...] tensors with pages of one size (the keys' and the values' caches
+    of all layers); copy_src, copy_dst [N] int32 as pka_fork_pages writes them."""
+    _check(_calls().copy_pages(caches, copy_src, copy_dst, error_word, stream), "pka_copy_pages")
+
+
+def pka_prefix_workspace_size(num_reqs, num_groups, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                              max_query_len) -> int:
+    return int(load().pka_prefix_workspace_size(num_reqs, num_groups, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                                max_query_len))
+
+
+def pka_prefix_attn_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, group_starts, prefix_lens,
+                            scale, max_query_len, max_seq_len, out, lse, workspace, kv_scales=None, error_word=None,
+                            stream=None):
+    """q, out [T, Hq, d] bf16, lse [T, Hq] float32 or None; caches [nb, Hkv, bs, d] bf16, or uint8 E4M3 codes with
+    kv_scales=(k_scale, v_scale); block_table [B, max_blocks], query_start_loc [B + 1], seq_lens [B], group_starts
+    [groups + 1], prefix_lens [groups] int32; workspace a uint8 tensor of >= pka_prefix_workspace_size(...) bytes."""
+    _check(_calls().prefix_attn_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, group_starts,
+                                        prefix_lens, scale, max_query_len, max_seq_len, out, lse, workspace, kv_scales,
+                                        error_word, stream), "pka_prefix_attn_forward")
 
 
 def pka_selftest_wait(arrive: bool, limit_us: int, stream=None) -> int:
