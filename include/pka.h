@@ -813,7 +813,8 @@ PKA_API pka_status pka_copy_pages(void *const *caches, int num_caches, int64_t n
  * written; a block id outside the cache sets PKA_DEVERR_BLOCK_ID.
  * head_dim 64 or 128 (_fp8: 128), Hq / Hkv <= 16, block_size a power of two in [1, 128], num_reqs <= 4096,
  * num_groups <= num_reqs, num_blocks * Hkv * block_size <= INT32_MAX, max_seq_len <= 2^30, num_tokens * Hq <=
- * 2^27, else PKA_ERR_UNSUPPORTED.
+ * 2^27, (num_tokens * Hq / (128 Hkv) + num_reqs) * Hkv * max_seq_len / 128 below about 2^28, else
+ * PKA_ERR_UNSUPPORTED.
  */
 PKA_API size_t pka_prefix_workspace_size(int num_reqs, int num_groups, int num_tokens, int num_q_heads,
                                          int num_kv_heads, int head_dim, int max_query_len);

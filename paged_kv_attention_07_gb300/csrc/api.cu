@@ -1427,7 +1427,7 @@ PrefixLayout prefix_layout(int num_reqs, int num_groups, int num_tokens, int Hq,
         off = align256(off + bytes);
         return o;
     };
-    L.off_cost = take(sizeof(long long) * ((size_t)L.own0 + num_reqs + 1));
+    L.off_cost = take(sizeof(int) * ((size_t)L.own0 + num_reqs + 1));
     L.off_unit = take(sizeof(int) * ((size_t)L.own0 + num_reqs));
     L.off_po_pre = take(sizeof(float) * slots_pre * 2 * L.rows_pre * head_dim);
     L.off_pl_pre = take(sizeof(float) * slots_pre * 2 * L.rows_pre);
@@ -1455,6 +1455,10 @@ pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_ca
     if (cf.fp8 && head_dim != 128) return PKA_ERR_UNSUPPORTED;
     if (!pow2(block_size) || block_size > 128 || max_seq_len > (1 << 30)) return PKA_ERR_UNSUPPORTED;
     if (num_blocks > INT32_MAX || num_blocks * block_size > INT32_MAX / num_kv_heads) return PKA_ERR_UNSUPPORTED;
+    {   // (key tiles of all units, with their costs, are counted in 32 bits)
+        const int64_t units = ((int64_t)num_tokens / (128 / (num_q_heads / num_kv_heads)) + num_reqs) * 2 * num_kv_heads;
+        if (units * (max_seq_len / 128 + 3) > INT32_MAX / kPrefixMaxCost) return PKA_ERR_UNSUPPORTED;
+    }
     if (num_tokens == 0) return PKA_OK;
     if (!q || !k_cache || !v_cache || !block_table || !query_start_loc || !seq_lens || !group_starts || !prefix_lens ||
         !out || !workspace)
@@ -1480,7 +1484,7 @@ pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_ca
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
     p.err = error_word;
-    p.seg_cost = reinterpret_cast<long long*>(ws + L.off_cost);
+    p.seg_cost = reinterpret_cast<int*>(ws + L.off_cost);
     p.seg_unit = reinterpret_cast<int*>(ws + L.off_unit);
     p.po_pre = reinterpret_cast<float*>(ws + L.off_po_pre);
     p.pl_pre = reinterpret_cast<float*>(ws + L.off_pl_pre);

@@ -252,6 +252,10 @@ struct CopyPagesParams {
     int pieces;  // of a page, set by the launch
 };
 
+// At most: the cost of a key tile of a unit, or of the unit itself (prefix_attn.cu); the line of all costs keeps
+// to 32 bits.
+constexpr int kPrefixMaxCost = 4;
+
 struct PrefixMaps {
     CUtensorMap q;  // [T, Hq, D]  box {64, G, 128 / G}
     CUtensorMap k;  // [nb * Hkv * bs, D]  box {64, bs}; codes: box {128, bs}
@@ -271,7 +275,7 @@ struct PrefixParams {
     int32_t* err;
     // workspace: each segment's place on the line of costs and of units; the pieces'
     // sums [slot][d / 4][2 * rows][4] and their log2 [slot][2 * rows], apart for common and own keys
-    long long* seg_cost;  // [own0 + B + 1], the last the total, -1: refused
+    int* seg_cost;  // [own0 + B + 1], the last the total, -1: refused
     int* seg_unit;
     float* po_pre;
     float* pl_pre;

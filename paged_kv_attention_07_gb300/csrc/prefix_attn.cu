@@ -39,13 +39,12 @@ namespace pka {
 namespace {
 
 constexpr int kKeys = 128;  // keys of a key tile
-constexpr int kPieces = 256;  // pieces of a CTA's share that are listed at a time
+constexpr int kPieces = 256;  // pieces of a list
 constexpr int kMaxSegs = 2 * kMaxRequests;
 constexpr int kChunks = kMaxSegs / 32;  // warp-sized runs of segments
-// Cost of a key tile for one row tile and for two.
-constexpr int kCostOne = 1, kCostTwo = 1;
-
-using i64 = long long;
+// Costs on the line: a key tile for one row tile, for two, and what a unit takes besides.
+constexpr int kCostOne = 2, kCostTwo = 3, kCostUnit = 2;
+static_assert(kCostOne <= kPrefixMaxCost && kCostTwo <= kPrefixMaxCost && kCostUnit <= kPrefixMaxCost, "");
 
 struct Seg {
     int q0, n;      // its tokens
@@ -64,7 +63,7 @@ PKA_DEVICE Seg make_seg(const PrefixParams& p, int q0, int n, int c0, int c1) {
     s.c1 = c1;
     s.base = c0 & ~(p.bs - 1);
     s.nkt = n > 0 && c1 > c0 ? (c1 - s.base + kKeys - 1) / kKeys : 0;
-    s.nrt = s.nkt > 0 ? (n + p.upt - 1) / p.upt : 0;
+    s.nrt = s.nkt == 0 ? 0 : n <= p.upt ? 1 : (n + p.upt - 1) / p.upt;
     s.w = n > p.tpt ? kCostTwo : kCostOne;
     return s;
 }
@@ -75,6 +74,7 @@ PKA_DEVICE int common_keys(int r0, int r1, int prefix) { return r1 - r0 > 1 ? pr
 // The last i in [0, n) with a[i] <= x (a[0] <= x).
 PKA_DEVICE int last_at_most(const int32_t* a, int n, int x) {
     int lo = 0, hi = n - 1;
+#pragma unroll 1
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (a[mid] <= x) lo = mid;
@@ -83,13 +83,28 @@ PKA_DEVICE int last_at_most(const int32_t* a, int n, int x) {
     return lo;
 }
 
-// The CTA whose share holds position x of a line of length total.
-PKA_DEVICE int cta_of(i64 x, i64 total, int ncta) { return (int)(((x + 1) * ncta - 1) / total); }
-PKA_DEVICE i64 share_start(int cta, i64 total, int ncta) { return total * cta / ncta; }
-// Key tiles [t0, t1) of a unit that starts at `us` lie in [lo, hi).
-PKA_DEVICE int first_tile(i64 lo, i64 us, int w, int nkt) {
-    const i64 d = lo - us;
-    return d <= 0 ? 0 : (int)min((i64)nkt, (d + w - 1) / w);
+// The line in shares of `base` or base + 1.
+struct Shares {
+    int base, rem;
+    PKA_DEVICE Shares(int total, int ncta) : base(total / ncta), rem(total % ncta) {}
+    PKA_DEVICE int start(int cta) const { return cta * base + min(cta, rem); }
+    PKA_DEVICE int cta_of(int x) const {
+        const int cut = rem * (base + 1);
+        return x < cut ? x / (base + 1) : rem + (x - cut) / base;
+    }
+};
+PKA_DEVICE int unit_cost(const Seg& s) { return s.nkt > 0 ? kCostUnit + s.nkt * s.w : 0; }
+// The first key tile of a unit that starts at `us` whose place is at or past x
+// (tile t's place: us + kCostUnit + t w).
+PKA_DEVICE int first_tile(int x, int us, const Seg& s) {
+    const int d = x - us - kCostUnit;
+    return d <= 0 ? 0 : min(s.nkt, (d + s.w - 1) / s.w);
+}
+
+// Of a piece's key tiles from t0 on those behind position `end` (past the unit's
+// last token) have nothing to see: they are left out, but for one.
+PKA_DEVICE int seen_tiles(const Seg& s, int t0, int t1, int end) {
+    return max(1, min(t1 - t0, (min(s.c1, end) - (s.base + t0 * kKeys) + kKeys - 1) / kKeys));
 }
 
 struct Piece {
@@ -120,13 +135,16 @@ struct PxCfg {
     static constexpr int kOffK = kRowTiles * kTileBytes;  // two stages
     static constexpr int kOffV = kOffK + 2 * kTileBytes;  // two stages
     static constexpr int kOffCode = kOffV + 2 * kTileBytes;
-    static constexpr int kOffPiece = kOffCode + (kCodeK + kCodeV) * kCodeBytes;
+    // the lengths, while a list is made, where the tiles go later
+    static constexpr int kOffMeta = kOffK;
+    static constexpr int kMetaBytes = (int)sizeof(int32_t) * (4 * kMaxRequests + 2);
+    static constexpr int kOffTiles = kOffCode + (kCodeK + kCodeV) * kCodeBytes;
+    static constexpr int kOffPiece = kOffTiles > kOffMeta + kMetaBytes ? kOffTiles : (kOffMeta + kMetaBytes + 15) / 16 * 16;
     static constexpr int kOffSums = kOffPiece + kPieces * (int)sizeof(Piece);
-    static constexpr int kOffBar = kOffSums + (kChunks + 1) * 16;
+    static constexpr int kOffBar = kOffSums + (kChunks + 1) * 8;
     static constexpr int kSmem = kOffBar + 256 + 1024;
     static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(4 * kTileBytes >= (int)sizeof(int32_t) * (2 * kMaxRequests + 1), "the groups pass through the K and V stages");
 };
 
 // The block of lane `b` of the key tile at kb (lanes past its valid blocks get 0).
@@ -141,40 +159,60 @@ PKA_DEVICE int tile_block(const PrefixParams& p, const int32_t* bt, int kb, int 
     return blk;
 }
 
-// The line of all units: sums of costs and units before each run of 32 segments.
-struct Plan {
-    i64* cost;   // [runs + 1]
-    int* units;  // [runs + 1]
-    int runs;
-    i64 total;
+// Two E4M3 codes, each in the upper byte of a half, as a pair of bf16 (a NaN code as 480).
+PKA_DEVICE uint32_t widen2(uint32_t x) {
+    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+    uint32_t z;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0x7b807b80u));  // 2^120
+    return z;
+}
+
+// The lengths of a call in shared memory.
+struct Meta {
+    int32_t* starts;  // [groups + 1]
+    int32_t* prefix;  // [groups]
+    int32_t* qsl;     // [B + 1]
+    int32_t* lens;    // [B]
 };
 
-// Segment s from the lengths: the groups, then, from own0 on, the requests (own0
-// is the number of groups, up to whole runs of 32). The groups' starts and prefixes
-// lie in shared memory.
-PKA_DEVICE Seg seg_of(const PrefixParams& p, const int32_t* starts, const int32_t* prefix, int s, int& err) {
+// Segment s: the groups, then, from own0 on, the requests (own0 is the number of
+// groups, up to whole runs of 32).
+PKA_DEVICE Seg seg_of(const PrefixParams& p, const Meta& m, int s, int& err) {
     if (s < p.groups) {
-        const int r0 = starts[s], r1 = starts[s + 1], len = prefix[s];
+        const int r0 = m.starts[s], r1 = m.starts[s + 1], len = m.prefix[s];
         if (r0 > r1 || r0 < 0 || r1 > p.B) {
             err |= PKA_DEVERR_INDEX;
             return make_seg(p, 0, 0, 0, 0);
         }
         if (len < 0) err |= PKA_DEVERR_SEQ_LEN;
-        const int q0 = __ldg(p.qsl + r0), q1 = __ldg(p.qsl + r1);
+        const int q0 = m.qsl[r0], q1 = m.qsl[r1];
         return make_seg(p, q0, q1 - q0, 0, common_keys(r0, r1, len));
     }
-    if (s < p.own0) return make_seg(p, 0, 0, 0, 0);
+    if (s < p.own0 || s >= p.own0 + p.B) return make_seg(p, 0, 0, 0, 0);
     const int r = s - p.own0;
-    const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1), len = __ldg(p.seq_lens + r);
+    const int q0 = m.qsl[r], q1 = m.qsl[r + 1], len = m.lens[r];
     if (q0 < 0 || q1 < q0 || q1 > p.T || (r == 0 && q0 != 0)) err |= PKA_DEVERR_QUERY_START_LOC;
     const int n = q1 - q0;
     if (n <= 0) return make_seg(p, q0, 0, 0, 0);
     if (n > p.max_query) err |= PKA_DEVERR_QUERY_LEN;
     if (len < n || len > p.max_seq) err |= PKA_DEVERR_SEQ_LEN;
-    const int g = last_at_most(starts, p.groups, r);
-    const int have = prefix[g];
+    const int g = last_at_most(m.starts, p.groups, r);
+    const int have = m.prefix[g];
     if (have < 0 || have > len - n) err |= PKA_DEVERR_SEQ_LEN;
-    return make_seg(p, q0, n, common_keys(starts[g], starts[g + 1], have), len);
+    return make_seg(p, q0, n, common_keys(m.starts[g], m.starts[g + 1], have), len);
+}
+
+// Inclusive sums over the warp's lanes.
+PKA_DEVICE void warp_sums(int& a, int& b) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) {
+            a += x;
+            b += y;
+        }
+    }
 }
 
 template <int D, bool kFp8>
@@ -185,37 +223,41 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-    uint64_t* q_full = bars + 0;    // the unit's row tiles landed
-    uint64_t* q_empty = bars + 1;   // its last S product is done
-    uint64_t* k_full = bars + 2;    // [2] per K stage
-    uint64_t* k_empty = bars + 4;
-    uint64_t* v_full = bars + 6;    // [2] per V stage
-    uint64_t* v_empty = bars + 8;
-    uint64_t* s_full = bars + 10;   // [2] per lane: its S tile is in tensor memory
-    uint64_t* p_full = bars + 12;   // [2] its P is (4 warp arrivals)
-    uint64_t* pv_done = bars + 14;  // [2] the product that read its P is done
-    uint64_t* o_free = bars + 16;   // [2] its O has been read (4 warp arrivals)
-    uint64_t* p_half = bars + 18;   // [2] P of keys 0..63 is there (4 warp arrivals)
-    uint64_t* ck_full = bars + 20;  // [2] per stage of key codes: landed
-    uint64_t* ck_empty = bars + 22;  // [2] widened (4 warp arrivals)
-    uint64_t* cv_full = bars + 24;  // the same for value codes
-    uint64_t* cv_empty = bars + 26;
+    uint64_t* q_full = bars + 0;    // [2] per row tile's place: landed
+    uint64_t* q_empty = bars + 2;   // [2] its unit's last S product is done
+    uint64_t* k_full = bars + 4;    // [2] per K stage
+    uint64_t* k_empty = bars + 6;
+    uint64_t* v_full = bars + 8;    // [2] per V stage
+    uint64_t* v_empty = bars + 10;
+    uint64_t* s_full = bars + 12;   // [2] per lane: its S tile is in tensor memory
+    uint64_t* p_full = bars + 14;   // [2] its P is (4 warp arrivals)
+    uint64_t* pv_done = bars + 16;  // [2] the product that read its P is done
+    uint64_t* o_free = bars + 18;   // [2] its O has been read (4 warp arrivals)
+    uint64_t* p_half = bars + 20;   // [2] P of keys 0..63 is there (4 warp arrivals)
+    uint64_t* ck_full = bars + 22;  // [2] per stage of key codes: landed
+    uint64_t* ck_empty = bars + 24;  // [2] widened (4 warp arrivals)
+    uint64_t* cv_full = bars + 26;  // the same for value codes
+    uint64_t* cv_empty = bars + 28;
     Piece* pieces = reinterpret_cast<Piece*>(smem + C::kOffPiece);
-    i64* run_cost = reinterpret_cast<i64*>(smem + C::kOffSums);
-    int* run_units = reinterpret_cast<int*>(run_cost + kChunks + 1);
+    int* run_cost = reinterpret_cast<int*>(smem + C::kOffSums);  // before each run of 32 segments
+    int* run_units = run_cost + kChunks + 1;
+    Meta meta;
+    meta.starts = reinterpret_cast<int32_t*>(smem + C::kOffMeta);
+    meta.prefix = meta.starts + p.groups + 1;
+    meta.qsl = meta.prefix + p.groups;
+    meta.lens = meta.qsl + p.B + 1;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     // Key tiles after which lane 0's next S has been issued: with two row tiles,
     // lane 1's product lets that S go first.
     __shared__ volatile int s_next0;
-    __shared__ int s_pieces;  // of the share, all
+    __shared__ int s_pieces;  // listed
 
-    grid_dep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
             mbar_init(&k_full[i], kFp8 ? 4 : 1);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], kFp8 ? 4 : 1);
@@ -238,213 +280,151 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
         tma_prefetch_desc(&maps.v);
     }
     // rows of a row tile that no token fills (128 / G * G < 128) stay zero
-    for (int i = tid; i < C::kRowTiles * C::kTileBytes / 16; i += kPxThreads)
-        reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
+    if (p.tpt * p.G < 128)
+#pragma unroll 1
+        for (int i = tid; i < C::kRowTiles * C::kTileBytes / 16; i += kPxThreads)
+            reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
     if (warp == 1) tmem_alloc(&s_tmem, C::kTmemCols);
     grid_dep_wait();
+    grid_dep_launch();  // (the join reads the lengths before it waits: what wrote them is done)
 
     // ---------------------------------------------------------------- the line
-    const int segs = p.own0 + p.B, runs = (segs + 31) / 32;
-    int32_t* starts = reinterpret_cast<int32_t*>(smem + C::kOffK);
-    int32_t* prefix = starts + p.groups + 1;
-    for (int i = tid; i <= p.groups; i += kPxThreads) starts[i] = p.starts[i];
-    for (int i = tid; i < p.groups; i += kPxThreads) prefix[i] = p.prefix[i];
-    __syncthreads();
+    const int runs = (p.own0 + p.B + 31) / 32;
+    auto load_meta = [&] {
+#pragma unroll 1
+        for (int i = tid; i <= p.B; i += kPxThreads) {
+            meta.qsl[i] = __ldg(p.qsl + i);
+            if (i < p.B) meta.lens[i] = __ldg(p.seq_lens + i);
+            if (i <= p.groups) meta.starts[i] = __ldg(p.starts + i);
+            if (i < p.groups) meta.prefix[i] = __ldg(p.prefix + i);
+        }
+        __syncthreads();
+    };
+    load_meta();
     int err = 0;
-    if (tid == 0 && (starts[0] != 0 || starts[p.groups] != p.B)) err = PKA_DEVERR_INDEX;
-    for (int run = warp; run < runs; run += kPxThreads / 32) {
-        const int s = run * 32 + lane;
-        i64 cost = 0;
-        int units = 0;
-        if (s < segs) {
-            const Seg g = seg_of(p, starts, prefix, s, err);
-            units = g.nrt * p.Hkv;
-            cost = (i64)units * g.nkt * g.w;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            cost += __shfl_xor_sync(0xffffffffu, cost, o);
-            units += __shfl_xor_sync(0xffffffffu, units, o);
-        }
-        if (lane == 0) {
-            run_cost[run] = cost;
-            run_units[run] = units;
-        }
-    }
-    const int bad = __syncthreads_or(err);
-    if (bad) {  // the same for every CTA
-        if (blockIdx.x == 0) {
-            if (err) set_error(p.err, err);
-            if (tid == 0) p.seg_cost[segs] = -1;
-        }
-    } else if (warp == 0) {
-        i64 c0 = 0;
-        int u0 = 0;
-        for (int r0 = 0; r0 < runs; r0 += 32) {
-            const int r = r0 + lane;
-            const i64 c = r < runs ? run_cost[r] : 0;
-            const int u = r < runs ? run_units[r] : 0;
-            i64 ci = c;
-            int ui = u;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const i64 a = __shfl_up_sync(0xffffffffu, ci, o);
-                const int b = __shfl_up_sync(0xffffffffu, ui, o);
-                if (lane >= o) {
-                    ci += a;
-                    ui += b;
-                }
-            }
-            if (r < runs) {
-                run_cost[r] = c0 + ci - c;
-                run_units[r] = u0 + ui - u;
-            }
-            c0 += __shfl_sync(0xffffffffu, ci, 31);
-            u0 += __shfl_sync(0xffffffffu, ui, 31);
-        }
-        if (lane == 0) {
-            run_cost[runs] = c0;
-            run_units[runs] = u0;
-        }
-    }
+    if (tid == 0 && (meta.starts[0] != 0 || meta.starts[p.groups] != p.B)) err = PKA_DEVERR_INDEX;
+    if (tid == 0) s_pieces = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = s_tmem;
     const uint32_t sm_base = smem_u32(smem);
     const int ncta = gridDim.x, cta = blockIdx.x;
-    const i64 total = bad ? 0 : run_cost[runs];
-    const i64 lo = share_start(cta, total, ncta), hi = share_start(cta + 1, total, ncta);
+    int lo = 0, hi = 0;  // the share
 
     // state of the roles across lists
-    uint32_t kv_it = 0, q_it = 0;
+    uint32_t kv_it = 0, q_it = 0;  // key tiles and row tiles so far
     uint32_t last[2] = {0, 0};  // phase + 1 of the last copy per stage (0 = none)
     uint32_t nl[2] = {0, 0};    // S products (or P . V products) of each lane
     uint32_t n_s = 0;           // S tiles of this softmax lane
     uint32_t uo[2] = {0, 0};    // units in which each lane had key tiles
 
-    for (int listed = 0;; listed += kPieces) {
-        // ------------------------------------------------------------ a list of the share's pieces
-        if (listed > 0) {  // (the groups were overwritten by tiles)
-            for (int i = tid; i <= p.groups; i += kPxThreads) starts[i] = p.starts[i];
-            for (int i = tid; i < p.groups; i += kPxThreads) prefix[i] = p.prefix[i];
-            __syncthreads();
+    // Pass 0 sums the runs of segments; pass j > 0 lists the pieces that begin in the
+    // j-th stretch of the share (a piece costs kCostUnit + kCostOne at least but for
+    // the first, so a list holds a stretch's) and works them off. One loop body for
+    // both: what runs once per launch is bound by the fetch of its instructions.
+    constexpr int kStretch = (kPieces - 2) * (kCostUnit + kCostOne);
+    for (int pass = 0;; ++pass) {
+        if (pass > 1) load_meta();  // (tiles were there meanwhile)
+        const int from = lo + (pass - 1) * kStretch;
+#pragma unroll 1
+        for (int run = warp; run < runs; run += kPxThreads / 32) {
+            if (pass > 0 && (run_cost[run] >= min(hi, from + kStretch) || run_cost[run + 1] <= from) &&
+                (pass > 1 || run % ncta != cta))
+                continue;
+            const int s = run * 32 + lane;
+            const Seg g = seg_of(p, meta, s, err);
+            const int units = g.nrt * p.Hkv, each = unit_cost(g), cost = units * each;
+            int ci = cost, ui = units;
+            warp_sums(ci, ui);
+            if (pass == 0) {
+                if (lane == 31) {
+                    run_cost[run] = ci;
+                    run_units[run] = ui;
+                }
+                continue;
+            }
+            const int cs = run_cost[run] + ci - cost, us = run_units[run] + ui - units;
+            if (pass == 1 && run % ncta == cta && s < p.own0 + p.B) {  // for the join
+                p.seg_cost[s] = cs;
+                p.seg_unit[s] = us;
+            }
+            if (units == 0 || cs >= hi || cs + cost <= lo) continue;
+#pragma unroll 1
+            for (int u = cs >= lo ? 0 : (lo - cs) / each; u < units && cs + u * each < hi; ++u) {
+                const int at = cs + u * each, begin = max(at, lo);
+                const int t0 = first_tile(lo, at, g), t1 = first_tile(hi, at, g);
+                if (t0 >= t1 || begin < from || begin >= from + kStretch) continue;
+                Piece x;
+                x.h = g.nrt == 1 ? u : u / g.nrt;
+                const int rt = u - x.h * g.nrt;
+                x.q0 = g.q0 + rt * p.upt;
+                x.ntok = min(p.upt, g.n - rt * p.upt);
+                x.kb0 = g.base + t0 * kKeys;
+                x.c0 = g.c0;
+                x.c1 = g.c1;
+                if (s < p.groups) {
+                    int r = meta.starts[s];
+                    while (r + 1 < meta.starts[s + 1] && meta.qsl[r + 1] <= g.q0) ++r;
+                    x.table = r;
+                    x.pos0 = INT32_MAX / 2;
+                    x.nkt = t1 - t0;
+                    x.slot = (us + u + cta) | INT32_MIN;
+                } else {
+                    x.table = s - p.own0;
+                    x.pos0 = g.c1 - g.n + (x.q0 - g.q0);
+                    x.nkt = seen_tiles(g, t0, t1, x.pos0 + x.ntok);
+                    x.slot = us + u + cta - run_units[p.own0 / 32];
+                }
+                pieces[atomicAdd(&s_pieces, 1)] = x;  // (in any order: a piece's result does not depend on it)
+            }
         }
-        if (warp == 0) {
-            int found = 0;
-            if (hi > lo) {
-                int run = 0;
-                for (int r0 = 0; r0 < runs; r0 += 32) {  // the last run that starts at or before lo
-                    const uint32_t before = __ballot_sync(0xffffffffu, r0 + lane < runs && run_cost[r0 + lane] <= lo);
-                    if (before) run = r0 + 31 - __clz(before);
-                    if (before != 0xffffffffu) break;
+        if (pass == 0) {
+            if (__syncthreads_or(err)) {  // the same for every CTA
+                if (cta == 0) {
+                    if (err) set_error(p.err, err);
+                    if (tid == 0) p.seg_cost[p.own0 + p.B] = -1;
                 }
-                for (; run < runs && run_cost[run] < hi; ++run) {
-                    const int s = run * 32 + lane;
-                    int none = 0;
-                    const Seg g = s < segs ? seg_of(p, starts, prefix, s, none) : make_seg(p, 0, 0, 0, 0);
-                    const int units = g.nrt * p.Hkv;
-                    const i64 unit_cost = (i64)g.nkt * g.w, cost = units * unit_cost;
-                    i64 ci = cost;
-                    int ui = units;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const i64 a = __shfl_up_sync(0xffffffffu, ci, o);
-                        const int b = __shfl_up_sync(0xffffffffu, ui, o);
-                        if (lane >= o) {
-                            ci += a;
-                            ui += b;
-                        }
+                break;
+            }
+            if (warp == 0) {
+                int c0 = 0, u0 = 0;
+#pragma unroll 1
+                for (int r0 = 0; r0 < runs; r0 += 32) {
+                    const int r = r0 + lane;
+                    const int c = r < runs ? run_cost[r] : 0, u = r < runs ? run_units[r] : 0;
+                    int ci = c, ui = u;
+                    warp_sums(ci, ui);
+                    if (r < runs) {
+                        run_cost[r] = c0 + ci - c;
+                        run_units[r] = u0 + ui - u;
                     }
-                    const i64 cs = run_cost[run] + ci - cost;
-                    const int us0 = run_units[run] + ui - units;
-                    int first = 0, end = 0;  // units that may have tiles in the share
-                    if (units > 0 && cs < hi && cs + cost > lo) {
-                        first = cs >= lo ? 0 : (int)((lo - cs) / unit_cost);
-                        end = (int)min((i64)units, (hi - cs + unit_cost - 1) / unit_cost);
-                    }
-                    int mine = 0;
-                    for (int u = first; u < end; ++u) {
-                        const i64 at = cs + u * unit_cost;
-                        mine += first_tile(lo, at, g.w, g.nkt) < first_tile(hi, at, g.w, g.nkt);
-                    }
-                    int before = mine;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int a = __shfl_up_sync(0xffffffffu, before, o);
-                        if (lane >= o) before += a;
-                    }
-                    const int sum = __shfl_sync(0xffffffffu, before, 31);
-                    int to = found + before - mine - listed;
-                    found += sum;
-                    for (int u = first; u < end && to < kPieces; ++u) {
-                        const i64 at = cs + u * unit_cost;
-                        const int t0 = first_tile(lo, at, g.w, g.nkt), t1 = first_tile(hi, at, g.w, g.nkt);
-                        if (t0 >= t1) continue;
-                        if (to >= 0) {
-                            Piece x;
-                            const int rt = u % g.nrt;
-                            x.h = u / g.nrt;
-                            x.q0 = g.q0 + rt * p.upt;
-                            x.ntok = min(p.upt, g.n - rt * p.upt);
-                            x.kb0 = g.base + t0 * kKeys;
-                            x.c0 = g.c0;
-                            x.c1 = g.c1;
-                            x.nkt = t1 - t0;
-                            if (s < p.groups) {
-                                int r = starts[s];
-                                while (r + 1 < starts[s + 1] && __ldg(p.qsl + r + 1) <= g.q0) ++r;
-                                x.table = r;
-                                x.pos0 = INT32_MAX / 2;
-                                x.slot = (us0 + u + cta) | INT32_MIN;
-                            } else {
-                                x.table = s - p.own0;
-                                x.pos0 = g.c1 - g.n + (x.q0 - g.q0);
-                                // key tiles behind the last token's position have nothing to see; one is kept
-                                const int seen = (min(g.c1, x.pos0 + x.ntok) - x.kb0 + kKeys - 1) / kKeys;
-                                x.nkt = max(1, min(x.nkt, seen));
-                                x.slot = us0 + u + cta - run_units[p.own0 / 32];
-                            }
-                            pieces[to] = x;
-                        }
-                        ++to;
-                    }
+                    c0 += __shfl_sync(0xffffffffu, ci, 31);
+                    u0 += __shfl_sync(0xffffffffu, ui, 31);
+                }
+                if (lane == 0) {
+                    run_cost[runs] = c0;
+                    run_units[runs] = u0;
                 }
             }
-            if (lane == 0) s_pieces = found;
-        } else if (warp == 11 && listed == 0 && !bad) {
-            // the segments' places on the line, for the join
-            for (int run = cta; run < runs; run += ncta) {
-                const int s = run * 32 + lane;
-                int none = 0;
-                const Seg g = s < segs ? seg_of(p, starts, prefix, s, none) : make_seg(p, 0, 0, 0, 0);
-                const int units = g.nrt * p.Hkv;
-                const i64 cost = (i64)units * g.nkt * g.w;
-                i64 ci = cost;
-                int ui = units;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const i64 a = __shfl_up_sync(0xffffffffu, ci, o);
-                    const int b = __shfl_up_sync(0xffffffffu, ui, o);
-                    if (lane >= o) {
-                        ci += a;
-                        ui += b;
-                    }
-                }
-                if (s < segs) {
-                    p.seg_cost[s] = run_cost[run] + ci - cost;
-                    p.seg_unit[s] = run_units[run] + ui - units;
-                }
-            }
-            if (cta == 0 && lane == 0) p.seg_cost[segs] = total;
+            __syncthreads();
+            const int total = run_cost[runs];
+            if (cta == 0 && tid == 0) p.seg_cost[p.own0 + p.B] = total;
+            const Shares shares(total, ncta);
+            lo = shares.start(cta);
+            hi = shares.start(cta + 1);
+            continue;
         }
         fence_proxy_async_smem();  // (what was written where tiles go)
         __syncthreads();
-        const int count = min(kPieces, s_pieces - listed);
-        if (count <= 0) break;
+        const int count = s_pieces;
+        if (from >= hi) break;
+        // Each role first gives up or takes its registers, and none goes on before all
+        // have: a warp that took its own back early would leave the softmax lanes waiting.
 
         if (warp < 4) {
             setmaxnreg_dec<C::kRegsIssue>();
+            __syncthreads();
             if (warp == 0 || warp == 2) {
                 // -------------------------------------------------------- producers: K; V and Q
                 const int which = warp == 0 ? 0 : 1;
@@ -459,30 +439,45 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 constexpr int kStage = kFp8 ? C::kCodeBytes : C::kTileBytes;
                 constexpr int kBoxes = kFp8 ? 1 : C::kChunk;  // 128 bytes wide
                 bool ok = true;
-                for (int i = 0; i < count && ok && !warp_flag(s_abort); ++i, ++q_it) {
+                auto first_block = [&](int i) {
+                    const Piece& U = pieces[i];
+                    return tile_block(p, p.block_table + (int64_t)U.table * p.max_blocks, U.kb0, U.c1, lane);
+                };
+                int next = tma && count > 0 ? first_block(0) : 0;
+#pragma unroll 1
+                for (int i = 0; i < count && ok && !warp_flag(s_abort); ++i) {
                     const Piece U = pieces[i];
                     if (which == 1) {
-                        if (q_it > 0 && !mbar_wait_warp(q_empty, (q_it - 1) & 1, p.err)) {
+                        const int nq = !kFp8 && U.ntok > p.tpt ? 2 : 1;
+#pragma unroll 1
+                        for (int k = 0; k < nq && ok; ++k, ++q_it) {
+                            const int at = q_it % C::kRowTiles;
+                            const uint32_t n = q_it / C::kRowTiles;
+                            if (n > 0 && !mbar_wait_warp(&q_empty[at], (n - 1) & 1, p.err)) {
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&q_full[at], (uint32_t)(C::kChunk * p.tpt * p.G * 128));
+                                for (int c = 0; c < C::kChunk; ++c)
+                                    tma_load_3d(smem + C::kOffQ + at * C::kTileBytes + c * C::kChunkBytes, &maps.q,
+                                                &q_full[at], c * 64, U.h * p.G, U.q0 + k * p.tpt, pol_q);
+                            }
+                        }
+                        if (!ok) {
                             s_abort = 1;
                             break;
                         }
-                        if (lane == 0) {
-                            const int nq = !kFp8 && U.ntok > p.tpt ? 2 : 1, bytes = p.tpt * p.G * 128;
-                            mbar_arrive_expect_tx(q_full, (uint32_t)(nq * C::kChunk * bytes));
-                            for (int k = 0; k < nq; ++k)
-                                for (int c = 0; c < C::kChunk; ++c)
-                                    tma_load_3d(smem + C::kOffQ + k * C::kTileBytes + c * C::kChunkBytes, &maps.q, q_full,
-                                                c * 64, U.h * p.G, U.q0 + k * p.tpt, pol_q);
-                        }
                     }
                     const int32_t* bt = p.block_table + (int64_t)U.table * p.max_blocks;
-                    int next = tma ? tile_block(p, bt, U.kb0, U.c1, lane) : 0;
+#pragma unroll 1
                     for (int t = 0; t < U.nkt; ++t, ++kv_it) {
                         const int st = (int)(kv_it % nst);
                         const uint32_t n = kv_it / nst;
                         const int kb = U.kb0 + t * kKeys;
                         const int block = next;
                         if (tma && t + 1 < U.nkt) next = tile_block(p, bt, kb + kKeys, U.c1, lane);
+                        else if (tma && i + 1 < count) next = first_block(i + 1);
                         if (n > 0 && !mbar_wait_warp(&empties[st], (n - 1) & 1, p.err)) {
                             s_abort = 1;
                             ok = false;
@@ -503,6 +498,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         } else {  // pages of 1, 2 or 4 tokens: 16-byte copies, zeros past the end
                             const uint32_t to = smem_u32(dst);
                             const uint8_t* from = static_cast<const uint8_t*>(which ? p.v_cache : p.k_cache);
+#pragma unroll 1
                             for (int ci = lane; ci < kKeys * kBoxes * 8; ci += 32) {
                                 const int row = ci / (kBoxes * 8), c = ci % (kBoxes * 8), pos = kb + row;
                                 const bool valid = pos < U.c1;
@@ -529,32 +525,40 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 #pragma unroll
                 for (int st = 0; st < 2; ++st)
                     if (last[st]) mbar_wait_warp(&fulls[st], (last[st] - 1) & 1, p.err);
-                if (which == 1 && q_it > 0) mbar_wait_warp(q_full, (q_it - 1) & 1, p.err);
+                if (which == 1)
+#pragma unroll 1
+                    for (uint32_t back = 1; back <= C::kRowTiles && back <= q_it; ++back)
+                        mbar_wait_warp(&q_full[(q_it - back) % C::kRowTiles], ((q_it - back) / C::kRowTiles) & 1, p.err);
             } else if (lane == 0 && warp == 1) {
                 // -------------------------------------------------------- S_k = Q K^T
                 constexpr uint32_t idesc = umma_idesc_bf16(128, 128, 0, 0);
                 const uint32_t q_s = sm_base + C::kOffQ, k_s = sm_base + C::kOffK;
                 bool ok = true;
-                for (int i = 0; i < count && ok && !s_abort; ++i, ++q_it) {
+#pragma unroll 1
+                for (int i = 0; i < count && ok && !s_abort; ++i) {
                     const int nkt = pieces[i].nkt;
                     const bool two = !kFp8 && pieces[i].ntok > p.tpt;
-                    if (!mbar_wait(q_full, q_it & 1, p.err)) {
+                    const uint32_t q0 = q_it, q1 = q_it + (two ? 1 : 0);
+                    q_it = q1 + 1;
+                    if (!mbar_wait(&q_full[q0 % C::kRowTiles], (q0 / C::kRowTiles) & 1, p.err) ||
+                        (two && !mbar_wait(&q_full[q1 % C::kRowTiles], (q1 / C::kRowTiles) & 1, p.err))) {
                         ok = false;
                         break;
                     }
+#pragma unroll 1
                     for (int t = 0; t < nkt; ++t, ++kv_it) {
                         const int st = kv_it & 1;
                         if (!mbar_wait(&k_full[st], (kv_it >> 1) & 1, p.err)) { ok = false; break; }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            if (!ok || (!two && k != (t & 1))) continue;
+                            if (!ok || (!two && k != st)) continue;
                             if (nl[k] > 0 && !mbar_wait(&pv_done[k], (nl[k] - 1) & 1, p.err)) { ok = false; continue; }
                             tc_fence_after();
+                            const uint32_t qa = q_s + (k == 1 ? q1 : q0) % C::kRowTiles * C::kTileBytes;
 #pragma unroll
                             for (int ks = 0; ks < D / 16; ++ks) {
                                 const uint32_t off = (ks >> 2) * C::kChunkBytes + (ks & 3) * 32;
-                                umma_bf16(tbase + C::kColS + k * 128,
-                                          umma_desc_sw128(q_s + (two ? k * C::kTileBytes : 0) + off, 16, 1024),
+                                umma_bf16(tbase + C::kColS + k * 128, umma_desc_sw128(qa + off, 16, 1024),
                                           umma_desc_sw128(k_s + st * C::kTileBytes + off, 16, 1024), idesc, ks > 0 ? 1u : 0u);
                             }
                             umma_commit(&s_full[k]);
@@ -563,12 +567,15 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         }
                         if (!ok) break;
                         umma_commit(&k_empty[st]);
-                        if (t == nkt - 1) umma_commit(q_empty);
+                        if (t == nkt - 1) {
+                            umma_commit(&q_empty[q0 % C::kRowTiles]);
+                            if (two) umma_commit(&q_empty[q1 % C::kRowTiles]);
+                        }
                     }
                     if (ok) s_next0 = (int)kv_it;  // nothing of lane 0 follows in this unit
                 }
                 if (!ok) s_abort = 1;
-                #pragma unroll
+#pragma unroll
                 for (int k = 0; k < 2; ++k)
                     if (nl[k] > 0) mbar_wait(&s_full[k], (nl[k] - 1) & 1, p.err);
             } else if (lane == 0 && warp == 3) {
@@ -576,15 +583,17 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 constexpr uint32_t idesc = umma_idesc_bf16(128, D, 0, 1);
                 const uint32_t v_s = sm_base + C::kOffV;
                 bool ok = true;
+#pragma unroll 1
                 for (int i = 0; i < count && ok && !s_abort; ++i) {
                     const int nkt = pieces[i].nkt;
                     const bool two = !kFp8 && pieces[i].ntok > p.tpt;
+#pragma unroll 1
                     for (int t = 0; t < nkt; ++t, ++kv_it) {
                         const int st = kv_it & 1;
                         if (!mbar_wait(&v_full[st], (kv_it >> 1) & 1, p.err)) { ok = false; break; }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            if (!ok || (!two && k != (t & 1))) continue;
+                            if (!ok || (!two && k != st)) continue;
                             const bool first = two ? t == 0 : t < 2;
                             if (two && k == 1 && !wait_counter(s_next0, (int)kv_it + 1, p.err)) { ok = false; continue; }
                             for (int hh = 0; hh < 2 && ok; ++hh) {
@@ -610,11 +619,12 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         if (!ok) break;
                         umma_commit(&v_empty[st]);
                     }
-                    ++uo[0];
-                    if (two || nkt > 1) ++uo[1];
+                    const int only = two || nkt > 1 ? -1 : (int)((kv_it - 1) & 1);  // the one lane that had a key tile
+                    if (only != 1) ++uo[0];
+                    if (only != 0) ++uo[1];
                 }
                 if (!ok) s_abort = 1;
-                #pragma unroll
+#pragma unroll
                 for (int k = 0; k < 2; ++k)
                     if (nl[k] > 0) mbar_wait(&pv_done[k], (nl[k] - 1) & 1, p.err);
             }
@@ -622,14 +632,21 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             setmaxnreg_inc<C::kRegsLaunch>();
         } else if (kFp8 && warp >= 12) {
             setmaxnreg_dec<C::kRegsWiden>();
+            __syncthreads();
             // ------------------------------------------------------------ codes to bf16 tiles
-            // (E4M3 -> f16 -> f32 -> bf16, each exact.) A thread takes 16 codes of a row at a
-            // time; of its two 16-byte pieces the threads of a row's second 64 elements
+            // A code's bits, moved to those of a bf16 of the same exponent and mantissa fields,
+            // are the value times 2^-120 (subnormals too): one exact product brings it up. Of
+            // the conversions only NaN codes (0x7f) go wrong so: they are looked for and put
+            // in afterwards. (Through f16 and f32 by conversion instructions a tile took 5300
+            // cycles: they run at a quarter of the rate.) A thread takes 16 codes of a row at
+            // a time; of its two 16-byte pieces the threads of a row's second 64 elements
             // store the second one first, so that a quarter warp's stores use all banks.
             bool ok = true;
             const int wtid = tid - 384;
+#pragma unroll 1
             for (int i = 0; i < count && ok && !warp_flag(s_abort); ++i) {
                 const int nkt = pieces[i].nkt;
+#pragma unroll 1
                 for (int t = 0; t < nkt && ok; ++t, ++kv_it) {
                     const int st = (int)(kv_it & 1);
                     const uint32_t n = kv_it >> 1;
@@ -652,12 +669,17 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                             const uint32_t row = j >> 3, c = j & 7;
                             const uint4 x = lds128(from + sw128(row, c));
                             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                            uint32_t y[8];
+                            uint32_t y[8], nan = 0;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t h = e4m3x2_to_f16x2((w[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                                y[e] = pack_bf16(f.x, f.y);
+                            for (int e = 0; e < 4; ++e) {
+                                nan |= (w[e] & 0x7f7f7f7fu) + 0x01010101u;
+                                y[2 * e] = widen2(__byte_perm(w[e], 0, 0x1404));
+                                y[2 * e + 1] = widen2(__byte_perm(w[e], 0, 0x3424));
+                            }
+                            if (nan & 0x80808080u) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (((w[e >> 2] >> (8 * (e & 3))) & 0x7f) == 0x7f) y[e >> 1] |= 0x7fffu << (16 * (e & 1));
                             }
                             uint8_t* base = to + (c >> 2) * C::kChunkBytes;
                             const uint32_t p0 = 2 * (c & 3);
@@ -680,6 +702,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             setmaxnreg_inc<C::kRegsLaunch>();
         } else {
             setmaxnreg_inc<C::kRegsSoftmax>();
+            __syncthreads();
             // ------------------------------------------------------------ softmax lanes
             const int k = warp >= 8 ? 1 : 0;
             const int row = 32 * (warp & 3) + lane;  // of the row tile = tensor memory lane
@@ -689,34 +712,35 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             const uint32_t tS = tbase + lane_off + C::kColS + k * 128;
             const uint32_t tO = tbase + lane_off + C::kColO + k * D;
             const float sl2 = p.scale_log2;
+#pragma unroll 1
             for (int i = 0; i < count && !warp_flag(s_abort); ++i) {
                 const Piece U = pieces[i];
                 const bool two = !kFp8 && U.ntok > p.tpt;
                 const int tok = (two ? k * p.tpt : 0) + row_tok;  // of the unit
                 const bool write = row_tok < p.tpt && tok < U.ntok;
                 const bool common = U.slot < 0;
-                const int half = common ? p.rows_pre : p.rows_own;  // rows of a lane's half of a slot
-                const int64_t slot = U.slot & INT32_MAX;
-                float* po = (common ? p.po_pre : p.po_own) + slot * 2 * half * D + (k * half + row) * 4;
-                float* pl = (common ? p.pl_pre : p.pl_own) + slot * 2 * half + k * half + row;
                 const uint32_t kv_base = kv_it;
                 kv_it += U.nkt;
-                const int step = two ? 1 : 2, t_first = two ? 0 : k;
-                if (t_first >= U.nkt) {  // no key tile for this lane (the join reads no result of it)
-                    if (write) *pl = -INFINITY;
-                    continue;
-                }
+                const int step = two ? 1 : 2, t_first = two ? 0 : (k ^ (int)(kv_base & 1));
+                if (t_first >= U.nkt) continue;  // no key tile for this lane (and the join reads no result of it)
+                // a lane's half of a slot: its row tile's, or that of the piece's first or second key tile on
+                const int half = common ? p.rows_pre : p.rows_own;
+                const int at = (two ? k : t_first) * half + row;
+                const int64_t slot = U.slot & INT32_MAX;
+                float* po = (common ? p.po_pre : p.po_own) + slot * 2 * half * D + at * 4;
+                float* pl = (common ? p.pl_pre : p.pl_own) + slot * 2 * half + at;
+                // no row of this warp is a token's: it only keeps the lane's step
+                const bool idle = 32 * (warp & 3) >= min(p.tpt, U.ntok - (two ? k * p.tpt : 0)) * p.G;
                 const int c1 = min(U.c1, U.pos0 + tok + 1);  // the row's visible keys end here
                 const int all1 = min(U.c1, U.pos0 + 1);      // every row sees these
                 float m_used = -INFINITY, l = 0.f;
                 bool ok = true;
+#pragma unroll 1
                 for (int t = t_first; t < U.nkt; t += step) {
                     if (!mbar_wait_warp(&s_full[k], n_s & 1, p.err)) { ok = false; break; }
                     tc_fence_after();
                     const int kb = U.kb0 + t * kKeys;
                     const bool edge = kb < U.c0 || kb + kKeys > all1;
-                    const int vlo = U.c0 - kb;  // visible columns [vlo, vlo + seen)
-                    const uint32_t seen = (uint32_t)max(0, c1 - U.c0);
                     float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     bool rescale = false;
                     float alpha = 1.f;
@@ -726,11 +750,6 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     auto load_half = [&](uint32_t (&r)[64], int h) {  // scores of keys 64 h ...
                         tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(r));
                         tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
-                    };
-                    auto mask_half = [&](uint32_t (&r)[64], int h) {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if ((uint32_t)(64 * h + j - vlo) >= seen) r[j] = 0xff800000u;
                     };
                     auto max_half = [&](const uint32_t (&r)[64]) {
 #pragma unroll
@@ -772,43 +791,64 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&p_half[k]);
                     };
-                    if constexpr (!kFp8) {  // the whole row in registers
-                        uint32_t r0[64], r1[64];
-                        load_half(r0, 0);
-                        load_half(r1, 1);
-                        tmem_wait_ld();
-                        if (edge) {
-                            mask_half(r0, 0);
-                            mask_half(r1, 1);
+                    if (idle) {
+                        early = !edge;  // (value rows outside the segment's keys are zeroed by all warps)
+                        if (early) signal_half();
+                    } else if (!kFp8 && !edge) {  // the whole row in registers
+                        if constexpr (!kFp8) {
+                            uint32_t r0[64], r1[64];
+                            load_half(r0, 0);
+                            load_half(r1, 1);
+                            tmem_wait_ld();
+                            max_half(r0);
+                            max_half(r1);
+                            take_max();
+                            early = !__any_sync(0xffffffffu, rescale);
+                            store_half(r0, 0);
+                            if (early) signal_half();
+                            store_half(r1, 1);
                         }
-                        max_half(r0);
-                        max_half(r1);
+                    } else {
+                        // twice over the row, 32 scores at a time in one loop body, masked by bits: few
+                        // registers and, above all, few instructions (an unrolled masked row took 3.8 us
+                        // for the fetch of its code, once per unit)
+                        const int vlo = U.c0 - kb, vhi = max(vlo, c1 - kb);  // visible columns [vlo, vhi)
+                        auto visible = [&](int c) {
+                            const int a = min(32, max(0, vlo - 32 * c)), b = min(32, max(0, vhi - 32 * c));
+                            return (uint32_t)((1ull << b) - (1ull << a));
+                        };
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t r[32];
+                            tmem_ld32(tS + 32 * c, r);
+                            const uint32_t bits = visible(c);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2)
+                                mx[(j >> 1) & 7] = fmax3f(mx[(j >> 1) & 7], (bits >> j) & 1 ? __uint_as_float(r[j]) : -INFINITY,
+                                                          (bits >> (j + 1)) & 1 ? __uint_as_float(r[j + 1]) : -INFINITY);
+                        }
                         take_max();
                         early = !edge && !__any_sync(0xffffffffu, rescale);
-                        store_half(r0, 0);
-                        if (early) signal_half();
-                        store_half(r1, 1);
-                    } else {  // twice in halves: these lanes have fewer registers
-                        uint32_t r[64], r1[64];
-                        load_half(r, 0);
-                        tmem_wait_ld();
-                        if (edge) mask_half(r, 0);
-                        max_half(r);
-                        load_half(r1, 1);
-                        tmem_wait_ld();
-                        if (edge) mask_half(r1, 1);
-                        max_half(r1);
-                        take_max();
-                        early = !edge && !__any_sync(0xffffffffu, rescale);
-                        load_half(r, 0);
-                        tmem_wait_ld();
-                        if (edge) mask_half(r, 0);
-                        store_half(r, 0);
-                        if (early) signal_half();
-                        load_half(r1, 1);
-                        tmem_wait_ld();
-                        if (edge) mask_half(r1, 1);
-                        store_half(r1, 1);
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t r[32], pk[16];
+                            tmem_ld32(tS + 32 * c, r);
+                            const uint32_t bits = visible(c);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                float x0, x1;
+                                fma2_bcast(x0, x1, (bits >> j) & 1 ? __uint_as_float(r[j]) : -INFINITY,
+                                           (bits >> (j + 1)) & 1 ? __uint_as_float(r[j + 1]) : -INFINITY, sl2, -m_off);
+                                const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+                                const int a = (j >> 1) & 3;
+                                add2(ls[2 * a], ls[2 * a + 1], e0, e1);
+                                pk[j / 2] = pack_bf16(e0, e1);
+                            }
+                            tmem_st16(tS + 16 * c, pk);
+                            if (early && c == 1) signal_half();
+                        }
                     }
                     l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
                     // (whole warps: tcgen05.ld and .st are collective)
@@ -831,6 +871,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         const uint32_t vi = kv_base + t;
                         if (!mbar_wait_warp(&v_full[vi & 1], (vi >> 1) & 1, p.err)) { ok = false; break; }
                         uint8_t* vt = smem + C::kOffV + (vi & 1) * C::kTileBytes;
+#pragma unroll 1
                         for (int ci = wg_tid; ci < kKeys * (D / 8); ci += 128) {
                             const int vr = ci / (D / 8), c = ci % (D / 8);
                             if (vr >= zlo && vr < zhi) continue;
@@ -877,6 +918,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
         }
         __syncthreads();
         if (s_abort) break;
+        if (tid == 0) s_pieces = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -889,92 +931,113 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 // ---------------------------------------------------------------- the join
 // One CTA per token and kv head. Its pieces are those of its rows' two units (the
 // group's common keys, its request's own) in every CTA whose share has tiles of them.
-constexpr int kJoinThreads = 128;
-
 struct Source {
-    const float* o;  // the rows' first four values; those of the next four dims 4 * rows further on
-    const float* l;
-    int rows;
+    const float* o;  // the row's first four values of the group's first head; the next four dims' 4 * rows further on
+    const float* l;  // null: no piece
 };
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixParams p, int ncta) {
+template <int D, int kThreads>
+__global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParams p, int ncta) {
+    constexpr int kWarps = kThreads / 32;
     extern __shared__ __align__(16) uint8_t s_join[];
-    __shared__ float s_top[16], s_sum[16];
+    __shared__ float s_inv[16];
     Source* src = reinterpret_cast<Source*>(s_join);                    // [4 * ncta]
     float* weight = reinterpret_cast<float*>(src + 4 * (size_t)ncta);  // [4 * ncta][G]
     grid_dep_launch();
-    grid_dep_wait();
-    const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-    const i64 total = p.seg_cost[p.own0 + p.B];
-    if (total < 0) return;  // refused lengths: nothing is written
+    const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
+    // ---- the token's segments, from the lengths (in place since before the attention started)
     const TokenPlace at = place_of(p.qsl, p.seq_lens, p.B, t);
-    if (at.r < 0) return;
-    const int g = last_at_most(p.starts, p.groups, at.r);
+    int g = 0, group_n = p.groups;
+#pragma unroll 1
+    while (group_n > 1) {  // the last group that starts at or before the request, 32 places at a time
+        const int step = (group_n + 31) / 32, i = g + lane * step;
+        const uint32_t before = __ballot_sync(0xffffffffu, i < g + group_n && __ldg(p.starts + i) <= max(at.r, 0));
+        const int k = before ? 31 - __clz(before) : 0;
+        group_n = min(step, group_n - k * step);
+        g += k * step;
+    }
     const int r0 = __ldg(p.starts + g), r1 = __ldg(p.starts + g + 1);
     const int common = common_keys(r0, r1, __ldg(p.prefix + g));
-    int n = 0;  // pieces, in the order of their keys
+    const bool inside = r0 >= 0 && r1 >= r0 && r1 <= p.B;
+    const int gq0 = inside ? __ldg(p.qsl + r0) : 0, gq1 = inside ? __ldg(p.qsl + r1) : 0;
+    grid_dep_wait();
+    const int total = __ldcg(p.seg_cost + p.own0 + p.B);
+    if (total < 0 || at.r < 0) return;  // refused lengths, or a row behind the last request's: nothing is written
+    const int cost_at[2] = {__ldcg(p.seg_cost + g), __ldcg(p.seg_cost + p.own0 + at.r)};
+    const int unit_at[2] = {__ldcg(p.seg_unit + g), __ldcg(p.seg_unit + p.own0 + at.r) - __ldcg(p.seg_unit + p.own0)};
+    const Shares shares(total, ncta);
+    int n = 0, n_common = 0;  // pieces, in the order of their keys
+#pragma unroll
     for (int part = 0; part < 2; ++part) {
-        const int gq0 = __ldg(p.qsl + r0);
-        const Seg s = part == 0 ? make_seg(p, gq0, __ldg(p.qsl + r1) - gq0, 0, common)
-                                : make_seg(p, at.q0, at.q1 - at.q0, common, at.len);
+        const Seg s = part == 0 ? make_seg(p, gq0, gq1 - gq0, 0, common) : make_seg(p, at.q0, at.q1 - at.q0, common, at.len);
+        if (part == 1) n_common = n;
         if (s.nkt == 0) continue;
-        const int index = part == 0 ? g : p.own0 + at.r;
-        const int rt = (t - s.q0) / p.upt, tok = (t - s.q0) % p.upt;
+        const int rt = (t - s.q0) / p.upt, tok = (t - s.q0) - rt * p.upt;
         const bool two = min(p.upt, s.n - rt * p.upt) > p.tpt;
-        const int local = h * s.nrt + rt;
-        const i64 us = p.seg_cost[index] + (i64)local * s.nkt * s.w;
-        const int unit = p.seg_unit[index] + local - (part == 0 ? 0 : p.seg_unit[p.own0]);
+        const int local = h * s.nrt + rt, us = cost_at[part] + local * unit_cost(s), unit = unit_at[part] + local;
         const int half = part == 0 ? p.rows_pre : p.rows_own;
-        const int row = two ? tok / p.tpt * half + tok % p.tpt * p.G : tok * p.G;
-        const int first = cta_of(us, total, ncta), last = cta_of(us + (i64)(s.nkt - 1) * s.w, total, ncta);
-        const int lanes = two ? 1 : 2;
-        for (int j = tid; j < (last - first + 1) * lanes; j += kJoinThreads) {
-            const int c = first + j / lanes, k = j % lanes;
-            const int t0 = first_tile(share_start(c, total, ncta), us, s.w, s.nkt);
-            const int t1 = first_tile(share_start(c + 1, total, ncta), us, s.w, s.nkt);
-            const i64 slot = (i64)(unit + c) * 2 * half;
+        const int row = two && tok >= p.tpt ? half + (tok - p.tpt) * G : tok * G;
+        const int first = shares.cta_of(us + kCostUnit), last = shares.cta_of(us + kCostUnit + (s.nkt - 1) * s.w);
+        const int lanes = two ? 1 : 2, end = s.c1 - s.n + min(s.n, (rt + 1) * p.upt);  // (of own keys)
+#pragma unroll 1
+        for (int j = tid; j < (last - first + 1) * lanes; j += kThreads) {
+            const int c = first + (two ? j : j >> 1), k = two ? 0 : j & 1;
+            const int t0 = first_tile(shares.start(c), us, s), t1 = first_tile(shares.start(c + 1), us, s);
+            const int64_t slot = (int64_t)(unit + c) * 2 * half;
             Source x;
-            x.rows = 2 * half;
             x.o = (part == 0 ? p.po_pre : p.po_own) + slot * D + (k * half + row) * 4;
-            x.l = t1 - t0 > k ? (part == 0 ? p.pl_pre : p.pl_own) + slot + k * half + row : nullptr;  // (no tile for that lane)
+            const int tiles = t0 >= t1 ? 0 : part == 0 ? t1 - t0 : seen_tiles(s, t0, t1, end);
+            x.l = tiles > k ? (part == 0 ? p.pl_pre : p.pl_own) + slot + k * half + row : nullptr;
             src[n + j] = x;
         }
         n += (last - first + 1) * lanes;
     }
     __syncthreads();
-    const int G = p.G;
-    for (int j = tid; j < n * G; j += kJoinThreads) {
-        const float* l = src[j / G].l;
-        weight[j] = l ? __ldcg(l + j % G) : -INFINITY;
+    // ---- weights: a warp per head
+#pragma unroll 1
+    for (int hh = warp; hh < G; hh += kWarps) {
+        float top = -INFINITY, nan = 0.f;
+#pragma unroll 1
+        for (int i = lane; i < n; i += 32) {
+            const float* from = src[i].l;
+            const float l = from ? __ldcg(from + hh) : -INFINITY;
+            weight[i * G + hh] = l;
+            top = fmaxf(top, l);
+            nan += l == l ? 0.f : l;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            nan += __shfl_xor_sync(0xffffffffu, nan, o);
+        }
+        float sum = nan;
+#pragma unroll 1
+        for (int i = lane; i < n; i += 32) {
+            const float l = weight[i * G + hh];
+            const float w = l == -INFINITY ? 0.f : l == top ? 1.f : exp2f(l - top);
+            weight[i * G + hh] = w;
+            sum += w;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) {
+            s_inv[hh] = sum == 0.f ? 0.f : p.v_scale / sum;
+            if (p.lse) p.lse[(int64_t)t * p.Hq + h * G + hh] = (top + log2f(sum)) * 0.69314718055994531f;
+        }
     }
     __syncthreads();
-    // ---- weights: a thread per head
-    if (tid < G) {
-        float top = -INFINITY;
-        for (int i = 0; i < n; ++i) top = fmaxf(top, weight[i * G + tid]);
-        s_top[tid] = top;
-    }
-    __syncthreads();
-    for (int j = tid; j < n * G; j += kJoinThreads) {
-        const float l = weight[j], top = s_top[j % G];
-        weight[j] = l == -INFINITY ? 0.f : l == top ? 1.f : exp2f(l - top);  // (equal infinities are NaN anyway)
-    }
-    __syncthreads();
-    if (tid < G) {
-        float sum = 0.f;
-        for (int i = 0; i < n; ++i) sum += weight[i * G + tid];
-        s_sum[tid] = sum;
-        if (p.lse) p.lse[(int64_t)t * p.Hq + h * G + tid] = (s_top[tid] + log2f(sum)) * 0.69314718055994531f;
-    }
-    __syncthreads();
-    for (int f = tid; f < D / 4 * G; f += kJoinThreads) {
-        const int hh = f % G, d4 = f / G;
+    // ---- the weighted sums: four dims of a head per thread, the pieces dealt out where threads are left over
+    const int flats = D / 4 * G, deal = max(1, kThreads / flats);
+    float4* parts = reinterpret_cast<float4*>(weight + (size_t)4 * ncta * G);  // [deal][flats], where deal > 1
+#pragma unroll 1
+    for (int f0 = tid; f0 < flats * deal; f0 += kThreads) {
+        const int f = f0 % flats, part = f0 / flats, hh = f % G, d4 = f / G;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int at_common = d4 * 2 * p.rows_pre + hh, at_own = d4 * 2 * p.rows_own + hh;
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
+        for (int i = part; i < n; i += deal) {
             const float w = weight[i * G + hh];
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(src[i].o) + (i64)d4 * src[i].rows + hh);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(src[i].o) + (i < n_common ? at_common : at_own));
             if (w != 0.f) {  // (the place of a piece that is none may hold anything)
                 acc.x += w * o.x;
                 acc.y += w * o.y;
@@ -982,7 +1045,28 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
                 acc.w += w * o.w;
             }
         }
-        const float inv = p.v_scale / s_sum[hh];
+        if (deal > 1) parts[f0] = acc;
+        if (deal == 1) {
+            const float inv = s_inv[hh];
+            *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.Hq + h * G + hh) * D + d4 * 4) =
+                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        }
+    }
+    if (deal == 1) return;
+    __syncthreads();
+#pragma unroll 1
+    for (int f = tid; f < flats; f += kThreads) {
+        const int hh = f % G, d4 = f / G;
+        float4 acc = parts[f];
+#pragma unroll 1
+        for (int k = 1; k < deal; ++k) {
+            const float4 o = parts[k * flats + f];
+            acc.x += o.x;
+            acc.y += o.y;
+            acc.z += o.z;
+            acc.w += o.w;
+        }
+        const float inv = s_inv[hh];
         *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.Hq + h * G + hh) * D + d4 * 4) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
@@ -997,16 +1081,25 @@ cudaError_t go_attn(const PrefixMaps& maps, const PrefixParams& p, int ncta, cud
     return launch_dependent(kern, dim3(ncta), dim3(C::kThreads), C::kSmem, stream, maps, p);
 }
 
-template <int D>
+template <int D, int kThreads>
 cudaError_t go_join(const PrefixParams& p, int ncta, cudaStream_t stream) {
-    auto kern = prefix_join_kernel<D>;
-    const size_t smem = 4 * (size_t)ncta * (sizeof(Source) + sizeof(float) * p.G);
+    auto kern = prefix_join_kernel<D, kThreads>;
+    const size_t head = sizeof(Source) + sizeof(float) * p.G;
+    const int flats = D / 4 * p.G;
+    const size_t smem = 4 * (size_t)ncta * head + (kThreads / flats > 1 ? sizeof(float4) * kThreads : 0);
     if (smem > 47 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)(4 * (size_t)ncta * (sizeof(Source) + sizeof(float) * 16)));
+        const cudaError_t e = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (int)(4 * (size_t)ncta * (sizeof(Source) + sizeof(float) * 16) + sizeof(float4) * kThreads));
         if (e != cudaSuccess) return e;
     }
-    return launch_dependent(kern, dim3(p.T, p.Hkv), dim3(kJoinThreads), smem, stream, p, ncta);
+    return launch_dependent(kern, dim3(p.T, p.Hkv), dim3(kThreads), smem, stream, p, ncta);
+}
+
+template <int D>
+cudaError_t go_join_by_size(const PrefixParams& p, int ncta, cudaStream_t stream) {
+    // few tokens: their units are cut into many pieces, and SMs are idle
+    return (int64_t)p.T * p.Hkv <= 2 * ncta ? go_join<D, 512>(p, ncta, stream) : go_join<D, 128>(p, ncta, stream);
 }
 
 }  // namespace
@@ -1018,7 +1111,7 @@ cudaError_t launch_prefix_attn(const PrefixMaps& maps, const PrefixParams& p, in
 }
 
 cudaError_t launch_prefix_join(const PrefixParams& p, int head_dim, int ncta, cudaStream_t stream) {
-    return head_dim == 128 ? go_join<128>(p, ncta, stream) : go_join<64>(p, ncta, stream);
+    return head_dim == 128 ? go_join_by_size<128>(p, ncta, stream) : go_join_by_size<64>(p, ncta, stream);
 }
 
 }  // namespace pka
