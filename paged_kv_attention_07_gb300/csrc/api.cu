@@ -1474,6 +1474,7 @@ pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_ca
     if (workspace_bytes < L.total) return PKA_ERR_WORKSPACE_TOO_SMALL;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PrefixParams p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
     p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.block_table = block_table;

@@ -346,6 +346,10 @@ PKA_DEVICE uint4 lds128(uint32_t addr) {
     return v;
 }
 
+PKA_DEVICE void st_shared4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // max(a, b, c) in one instruction (three-input max, sm_100 and later).
 PKA_DEVICE float fmax3f(float a, float b, float c) {
     float d;

@@ -263,6 +263,7 @@ struct PrefixMaps {
 };
 
 struct PrefixParams {
+    const __nv_bfloat16* q;  // [T, Hq, d]
     const void* k_cache;
     const void* v_cache;
     const int32_t* block_table;

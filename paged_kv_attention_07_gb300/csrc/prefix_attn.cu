@@ -125,23 +125,26 @@ struct PxCfg {
     static constexpr int kRegsSoftmax = kFp8 ? 176 : 208, kRegsWiden = 96;
     static_assert(128 * kRegsIssue + 256 * kRegsSoftmax + (kFp8 ? 128 * kRegsWiden : 0) <= kThreads * kRegsLaunch,
                   "register split");
-    static constexpr int kRowTiles = kFp8 ? 1 : 2;   // of a unit, at most
+    static constexpr int kRowTiles = 2;              // places for row tiles
     static constexpr int kChunk = D / 64;            // 64-wide swizzle chunks per row
     static constexpr int kChunkBytes = 128 * 128;    // 128 rows x 128 B
     static constexpr int kTileBytes = kChunk * kChunkBytes;
-    static constexpr int kCodeBytes = kFp8 ? kKeys * D : 0;  // a key tile's codes
-    static constexpr int kCodeK = 2, kCodeV = 1;             // stages of codes
+    static constexpr int kCodeBytes = kKeys * D;     // a key tile in 8 bits
+    static constexpr int kStagesK = kFp8 ? 3 : 2, kStageK = kFp8 ? kCodeBytes : kTileBytes;
+    static constexpr int kStagesV = 2;               // of V in 16 bits
+    static constexpr int kStagesCode = kFp8 ? 2 : 0;  // of V's codes
     static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kRowTiles * kTileBytes;  // two stages
-    static constexpr int kOffV = kOffK + 2 * kTileBytes;  // two stages
-    static constexpr int kOffCode = kOffV + 2 * kTileBytes;
+    static constexpr int kOffK = kRowTiles * kTileBytes;
+    static constexpr int kOffV = kOffK + kStagesK * kStageK;
+    static constexpr int kOffCode = kOffV + kStagesV * kTileBytes;
     // the lengths, while a list is made, where the tiles go later
     static constexpr int kOffMeta = kOffK;
     static constexpr int kMetaBytes = (int)sizeof(int32_t) * (4 * kMaxRequests + 2);
-    static constexpr int kOffTiles = kOffCode + (kCodeK + kCodeV) * kCodeBytes;
+    static constexpr int kOffTiles = kOffCode + kStagesCode * kCodeBytes;
     static constexpr int kOffPiece = kOffTiles > kOffMeta + kMetaBytes ? kOffTiles : (kOffMeta + kMetaBytes + 15) / 16 * 16;
     static constexpr int kOffSums = kOffPiece + kPieces * (int)sizeof(Piece);
-    static constexpr int kOffBar = kOffSums + (kChunks + 1) * 8;
+    static constexpr int kOffUnit = kOffSums + (kChunks + 1) * 8;  // [4][128] of the row tiles' rows in 8 bits
+    static constexpr int kOffBar = kOffUnit + (kFp8 ? 4 * 128 * 4 : 0);
     static constexpr int kSmem = kOffBar + 256 + 1024;
     static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
     static_assert(kSmem <= 232448, "shared memory");
@@ -157,14 +160,6 @@ PKA_DEVICE int tile_block(const PrefixParams& p, const int32_t* bt, int kb, int 
         blk = 0;
     }
     return blk;
-}
-
-// Two E4M3 codes, each in the upper byte of a half, as a pair of bf16 (a NaN code as 480).
-PKA_DEVICE uint32_t widen2(uint32_t x) {
-    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-    uint32_t z;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0x7b807b80u));  // 2^120
-    return z;
 }
 
 // The lengths of a call in shared memory.
@@ -225,19 +220,18 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint64_t* q_full = bars + 0;    // [2] per row tile's place: landed
     uint64_t* q_empty = bars + 2;   // [2] its unit's last S product is done
-    uint64_t* k_full = bars + 4;    // [2] per K stage
-    uint64_t* k_empty = bars + 6;
-    uint64_t* v_full = bars + 8;    // [2] per V stage
-    uint64_t* v_empty = bars + 10;
-    uint64_t* s_full = bars + 12;   // [2] per lane: its S tile is in tensor memory
-    uint64_t* p_full = bars + 14;   // [2] its P is (4 warp arrivals)
-    uint64_t* pv_done = bars + 16;  // [2] the product that read its P is done
-    uint64_t* o_free = bars + 18;   // [2] its O has been read (4 warp arrivals)
-    uint64_t* p_half = bars + 20;   // [2] P of keys 0..63 is there (4 warp arrivals)
-    uint64_t* ck_full = bars + 22;  // [2] per stage of key codes: landed
-    uint64_t* ck_empty = bars + 24;  // [2] widened (4 warp arrivals)
-    uint64_t* cv_full = bars + 26;  // the same for value codes
-    uint64_t* cv_empty = bars + 28;
+    uint64_t* k_full = bars + 4;    // [3] per K stage
+    uint64_t* k_empty = bars + 7;
+    uint64_t* v_full = bars + 10;   // [2] per V stage
+    uint64_t* v_empty = bars + 12;
+    uint64_t* s_full = bars + 14;   // [2] per lane: its S tile is in tensor memory
+    uint64_t* p_full = bars + 16;   // [2] its P is (4 warp arrivals)
+    uint64_t* pv_done = bars + 18;  // [2] the product that read its P is done
+    uint64_t* o_free = bars + 20;   // [2] its O has been read (4 warp arrivals)
+    uint64_t* p_half = bars + 22;   // [2] P of keys 0..63 is there (4 warp arrivals)
+    uint64_t* c_full = bars + 24;   // [2] per stage of V's codes: landed
+    uint64_t* c_empty = bars + 26;  // [2] widened (4 warp arrivals)
+    float* row_unit = reinterpret_cast<float*>(smem + C::kOffUnit);
     Piece* pieces = reinterpret_cast<Piece*>(smem + C::kOffPiece);
     int* run_cost = reinterpret_cast<int*>(smem + C::kOffSums);  // before each run of 32 segments
     int* run_units = run_cost + kChunks + 1;
@@ -256,10 +250,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
+            mbar_init(&q_full[i], kFp8 ? 4 : 1);
             mbar_init(&q_empty[i], 1);
-            mbar_init(&k_full[i], kFp8 ? 4 : 1);
-            mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], kFp8 ? 4 : 1);
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
@@ -267,10 +259,12 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             mbar_init(&p_half[i], 4);
             mbar_init(&pv_done[i], 1);
             mbar_init(&o_free[i], 4);
-            mbar_init(&ck_full[i], 1);
-            mbar_init(&ck_empty[i], 4);
-            mbar_init(&cv_full[i], 1);
-            mbar_init(&cv_empty[i], 4);
+            mbar_init(&c_full[i], 1);
+            mbar_init(&c_empty[i], 4);
+        }
+        for (int i = 0; i < C::kStagesK; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
         }
         fence_barrier_init();
         s_abort = 0;
@@ -314,9 +308,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 
     // state of the roles across lists
     uint32_t kv_it = 0, q_it = 0;  // key tiles and row tiles so far
-    uint32_t last[2] = {0, 0};  // phase + 1 of the last copy per stage (0 = none)
     uint32_t nl[2] = {0, 0};    // S products (or P . V products) of each lane
-    uint32_t n_s = 0;           // S tiles of this softmax lane
+    uint32_t n_s = 0, n_p = 0;  // S tiles of this softmax lane, pieces
     uint32_t uo[2] = {0, 0};    // units in which each lane had key tiles
 
     // Pass 0 sums the runs of segments; pass j > 0 lists the pieces that begin in the
@@ -430,13 +423,12 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 const int which = warp == 0 ? 0 : 1;
                 const uint64_t pol = policy_evict_normal(), pol_q = policy_evict_last();
                 const bool tma = p.bs >= 8;
-                // over an 8-bit cache the codes' stages, else the tiles'
-                uint64_t* fulls = kFp8 ? (which ? cv_full : ck_full) : which ? v_full : k_full;
-                uint64_t* empties = kFp8 ? (which ? cv_empty : ck_empty) : which ? v_empty : k_empty;
-                const uint32_t nst = !kFp8 ? 2 : which ? C::kCodeV : C::kCodeK;
-                uint8_t* stages = smem + (kFp8 ? C::kOffCode + (which ? C::kCodeK * C::kCodeBytes : 0)
-                                               : which ? C::kOffV : C::kOffK);
-                constexpr int kStage = kFp8 ? C::kCodeBytes : C::kTileBytes;
+                // of an 8-bit cache K's codes are the product's operand, V's are widened first
+                uint64_t* fulls = !which ? k_full : kFp8 ? c_full : v_full;
+                uint64_t* empties = !which ? k_empty : kFp8 ? c_empty : v_empty;
+                const uint32_t nst = !which ? C::kStagesK : kFp8 ? C::kStagesCode : C::kStagesV;
+                uint8_t* stages = smem + (!which ? C::kOffK : kFp8 ? C::kOffCode : C::kOffV);
+                constexpr int kStage = C::kStageK;
                 constexpr int kBoxes = kFp8 ? 1 : C::kChunk;  // 128 bytes wide
                 bool ok = true;
                 auto first_block = [&](int i) {
@@ -447,8 +439,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 #pragma unroll 1
                 for (int i = 0; i < count && ok && !warp_flag(s_abort); ++i) {
                     const Piece U = pieces[i];
-                    if (which == 1) {
-                        const int nq = !kFp8 && U.ntok > p.tpt ? 2 : 1;
+                    if (!kFp8 && which == 1) {
+                        const int nq = U.ntok > p.tpt ? 2 : 1;
 #pragma unroll 1
                         for (int k = 0; k < nq && ok; ++k, ++q_it) {
                             const int at = q_it % C::kRowTiles;
@@ -517,21 +509,18 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&fulls[st]);
                         }
-                        if (st == 0) last[0] = n + 1;
-                        else last[1] = n + 1;
                     }
                 }
-                // no copy may outlive the CTA, nor meet the next list's groups
-#pragma unroll
-                for (int st = 0; st < 2; ++st)
-                    if (last[st]) mbar_wait_warp(&fulls[st], (last[st] - 1) & 1, p.err);
-                if (which == 1)
+                // no copy may outlive the CTA, nor meet the next list's lengths
 #pragma unroll 1
-                    for (uint32_t back = 1; back <= C::kRowTiles && back <= q_it; ++back)
-                        mbar_wait_warp(&q_full[(q_it - back) % C::kRowTiles], ((q_it - back) / C::kRowTiles) & 1, p.err);
+                for (uint32_t back = 1; back <= nst && back <= kv_it; ++back)
+                    mbar_wait_warp(&fulls[(kv_it - back) % nst], ((kv_it - back) / nst) & 1, p.err);
+#pragma unroll 1
+                for (uint32_t back = 1; !kFp8 && which == 1 && back <= C::kRowTiles && back <= q_it; ++back)
+                    mbar_wait_warp(&q_full[(q_it - back) % C::kRowTiles], ((q_it - back) / C::kRowTiles) & 1, p.err);
             } else if (lane == 0 && warp == 1) {
                 // -------------------------------------------------------- S_k = Q K^T
-                constexpr uint32_t idesc = umma_idesc_bf16(128, 128, 0, 0);
+                constexpr uint32_t idesc = kFp8 ? umma_idesc_f8(128, 128) : umma_idesc_bf16(128, 128, 0, 0);
                 const uint32_t q_s = sm_base + C::kOffQ, k_s = sm_base + C::kOffK;
                 bool ok = true;
 #pragma unroll 1
@@ -547,19 +536,28 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     }
 #pragma unroll 1
                     for (int t = 0; t < nkt; ++t, ++kv_it) {
-                        const int st = kv_it & 1;
-                        if (!mbar_wait(&k_full[st], (kv_it >> 1) & 1, p.err)) { ok = false; break; }
+                        const int st = (int)(kv_it % C::kStagesK), only = (int)(kv_it & 1);
+                        if (!mbar_wait(&k_full[st], (kv_it / C::kStagesK) & 1, p.err)) { ok = false; break; }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            if (!ok || (!two && k != st)) continue;
+                            if (!ok || (!two && k != only)) continue;
                             if (nl[k] > 0 && !mbar_wait(&pv_done[k], (nl[k] - 1) & 1, p.err)) { ok = false; continue; }
                             tc_fence_after();
                             const uint32_t qa = q_s + (k == 1 ? q1 : q0) % C::kRowTiles * C::kTileBytes;
+                            if constexpr (kFp8) {  // the rows' upper and lower halves (the second tile) times the codes
 #pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks) {
-                                const uint32_t off = (ks >> 2) * C::kChunkBytes + (ks & 3) * 32;
-                                umma_bf16(tbase + C::kColS + k * 128, umma_desc_sw128(qa + off, 16, 1024),
-                                          umma_desc_sw128(k_s + st * C::kTileBytes + off, 16, 1024), idesc, ks > 0 ? 1u : 0u);
+                                for (int ks = 0; ks < 2 * (D / 32); ++ks)
+                                    umma_f8(tbase + C::kColS + k * 128,
+                                            umma_desc_sw128(qa + (ks >= D / 32 ? C::kCodeBytes : 0) + ks % (D / 32) * 32, 16, 1024),
+                                            umma_desc_sw128(k_s + st * C::kStageK + ks % (D / 32) * 32, 16, 1024), idesc,
+                                            ks > 0 ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int ks = 0; ks < D / 16; ++ks) {
+                                    const uint32_t off = (ks >> 2) * C::kChunkBytes + (ks & 3) * 32;
+                                    umma_bf16(tbase + C::kColS + k * 128, umma_desc_sw128(qa + off, 16, 1024),
+                                              umma_desc_sw128(k_s + st * C::kStageK + off, 16, 1024), idesc, ks > 0 ? 1u : 0u);
+                                }
                             }
                             umma_commit(&s_full[k]);
                             ++nl[k];
@@ -580,7 +578,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     if (nl[k] > 0) mbar_wait(&s_full[k], (nl[k] - 1) & 1, p.err);
             } else if (lane == 0 && warp == 3) {
                 // -------------------------------------------------------- O_k += P_k V
-                constexpr uint32_t idesc = umma_idesc_bf16(128, D, 0, 1);
+                constexpr uint32_t idesc = kFp8 ? umma_idesc_f16(128, D, 0, 1) : umma_idesc_bf16(128, D, 0, 1);
                 const uint32_t v_s = sm_base + C::kOffV;
                 bool ok = true;
 #pragma unroll 1
@@ -633,68 +631,128 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
         } else if (kFp8 && warp >= 12) {
             setmaxnreg_dec<C::kRegsWiden>();
             __syncthreads();
-            // ------------------------------------------------------------ codes to bf16 tiles
-            // A code's bits, moved to those of a bf16 of the same exponent and mantissa fields,
-            // are the value times 2^-120 (subnormals too): one exact product brings it up. Of
-            // the conversions only NaN codes (0x7f) go wrong so: they are looked for and put
-            // in afterwards. (Through f16 and f32 by conversion instructions a tile took 5300
-            // cycles: they run at a quarter of the rate.) A thread takes 16 codes of a row at
-            // a time; of its two 16-byte pieces the threads of a row's second 64 elements
-            // store the second one first, so that a quarter warp's stores use all banks.
-            bool ok = true;
+            // ------------------------------------------------------------ rows to 8 bits, V's codes to f16
+            // S comes from the codes of K themselves: a row of q, times the power of two that
+            // brings its largest magnitude to 224 .. 448, is split into two E4M3 numbers, which
+            // hold its 8 significant bits exactly down to 2^-10 of the largest and 2^-18 of that
+            // below. V's codes are widened to f16 (exact), P is f16 in units of 2^-7, so that it
+            // keeps 11 bits down to 2^-21 and goes on to 2^-31 of the row's largest. (With V and K
+            // both widened to bf16 a tile took 5300 cycles, by integer operations 7000.) Value rows
+            // outside the segment's keys may hold anything: zeros.
             const int wtid = tid - 384;
+            bool ok = true;
+            auto split_rows = [&](int i) {  // the row tile of piece i
+                const Piece& U = pieces[i];
+                const uint32_t n = q_it / C::kRowTiles;
+                if (n > 0 && !mbar_wait_warp(&q_empty[q_it % C::kRowTiles], (n - 1) & 1, p.err)) {
+                    ok = false;
+                    return;
+                }
+                const uint32_t to = sm_base + C::kOffQ + q_it % C::kRowTiles * C::kTileBytes;
+                const int rows = U.ntok * p.G, part = lane & 7;
 #pragma unroll 1
-            for (int i = 0; i < count && ok && !warp_flag(s_abort); ++i) {
-                const int nkt = pieces[i].nkt;
-#pragma unroll 1
-                for (int t = 0; t < nkt && ok; ++t, ++kv_it) {
-                    const int st = (int)(kv_it & 1);
-                    const uint32_t n = kv_it >> 1;
+                for (int r0 = 0; r0 < rows; r0 += 32) {  // two rounds of 8 lanes per row
+                    uint4 x[2][2];
 #pragma unroll
-                    for (int which = 0; which < 2; ++which) {
-                        const uint32_t ncode = which ? C::kCodeV : C::kCodeK;
-                        const int cst = (int)(kv_it % ncode);
-                        const uint32_t cn = kv_it / ncode;
-                        uint64_t* cfull = (which ? cv_full : ck_full) + cst;
-                        uint64_t* empty = (which ? v_empty : k_empty) + st;
-                        if (!ok || !mbar_wait_warp(cfull, cn & 1, p.err) ||
-                            (n > 0 && !mbar_wait_warp(empty, (n - 1) & 1, p.err))) {
-                            ok = false;
-                            continue;
+                    for (int j = 0; j < 2; ++j) {
+                        const int row = min(r0 + 16 * j + (wtid >> 3), rows - 1), tok = row / p.G;
+                        const uint4* from = reinterpret_cast<const uint4*>(
+                            p.q + ((int64_t)(U.q0 + tok) * p.Hq + U.h * p.G + (row - tok * p.G)) * D) + 2 * part;
+                        x[j][0] = __ldg(from);
+                        x[j][1] = __ldg(from + 1);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int row = r0 + 16 * j + (wtid >> 3);
+                        const uint32_t w[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
+                        float top = 0.f, odd = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            top = fmax3f(top, fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e])));
+                            odd += (bf16_lo(w[e]) + bf16_hi(w[e])) * 0.f;  // (NaN where an element is not finite)
                         }
-                        const uint32_t from = sm_base + C::kOffCode + (which ? C::kCodeK * C::kCodeBytes : 0) + cst * C::kCodeBytes;
-                        uint8_t* to = smem + (which ? C::kOffV : C::kOffK) + st * C::kTileBytes;
-#pragma unroll 4
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) {
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            odd += __shfl_xor_sync(0xffffffffu, odd, o);
+                        }
+                        // top <= 0.875 * 2^e2: 448 at most after the product
+                        const int e2 = min(129, max((int)(__float_as_uint(top) >> 23) - 126 +
+                                                        ((__float_as_uint(top) & 0x7fffffu) > 0x600000u), -110));
+                        const float by = exp2i(9 - e2);
+                        uint32_t hi[4], low[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float v0 = bf16_lo(w[2 * e]) * by, v1 = bf16_hi(w[2 * e]) * by;
+                            const float v2 = bf16_lo(w[2 * e + 1]) * by, v3 = bf16_hi(w[2 * e + 1]) * by;
+                            hi[e] = e4m3x4(v0, v1, v2, v3);
+                            const uint32_t h01 = e4m3x2_to_f16x2(hi[e] & 0xffffu), h23 = e4m3x2_to_f16x2(hi[e] >> 16);
+                            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+                            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+                            low[e] = e4m3x4(v0 - a.x, v1 - a.y, v2 - b.x, v3 - b.y);
+                        }
+                        if (row < rows) {
+                            st_shared4(to + sw128(row, part), hi[0], hi[1], hi[2], hi[3]);
+                            st_shared4(to + C::kCodeBytes + sw128(row, part), low[0], low[1], low[2], low[3]);
+                            if (part == 0) row_unit[(q_it & 3) * 128 + row] = exp2i(e2 - 9) + odd;
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[q_it % C::kRowTiles]);
+                ++q_it;
+            };
+#pragma unroll 1
+            for (int i = -1; i < count && ok && !warp_flag(s_abort); ++i) {
+                const Piece U = pieces[max(i, 0)];
+                const int nkt = i < 0 ? 1 : U.nkt;
+#pragma unroll 1
+                for (int t = 0; t < nkt && ok; ++t) {
+                    if (i >= 0) {
+                        const int st = (int)(kv_it & 1);
+                        const uint32_t n = kv_it >> 1;
+                        if (!mbar_wait_warp(&c_full[st], n & 1, p.err) ||
+                            (n > 0 && !mbar_wait_warp(&v_empty[st], (n - 1) & 1, p.err))) {
+                            ok = false;
+                            break;
+                        }
+                        const int kb = U.kb0 + t * kKeys;
+                        const uint32_t zlo = (uint32_t)max(0, U.c0 - kb), valid = (uint32_t)(min(kKeys, U.c1 - kb) - (int)zlo);
+                        const uint32_t from = sm_base + C::kOffCode + st * C::kCodeBytes;
+                        const uint32_t to = sm_base + C::kOffV + st * C::kTileBytes;
+#pragma unroll 2
                         for (int j = wtid; j < kKeys * 8; j += 128) {
                             const uint32_t row = j >> 3, c = j & 7;
                             const uint4 x = lds128(from + sw128(row, c));
                             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                            uint32_t y[8], nan = 0;
+                            uint32_t y[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                nan |= (w[e] & 0x7f7f7f7fu) + 0x01010101u;
-                                y[2 * e] = widen2(__byte_perm(w[e], 0, 0x1404));
-                                y[2 * e + 1] = widen2(__byte_perm(w[e], 0, 0x3424));
-                            }
-                            if (nan & 0x80808080u) {
+                            for (int e = 0; e < 8; ++e) y[e] = e4m3x2_to_f16x2((w[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
+                            if (row - zlo >= valid) {
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (((w[e >> 2] >> (8 * (e & 3))) & 0x7f) == 0x7f) y[e >> 1] |= 0x7fffu << (16 * (e & 1));
+                                for (int e = 0; e < 8; ++e) y[e] = 0;
                             }
-                            uint8_t* base = to + (c >> 2) * C::kChunkBytes;
-                            const uint32_t p0 = 2 * (c & 3);
-                            const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-                            const bool second = c >= 4;
-                            *reinterpret_cast<uint4*>(base + sw128(row, p0 + second)) = second ? b : a;
-                            *reinterpret_cast<uint4*>(base + sw128(row, p0 + !second)) = second ? a : b;
+                            // (of its two 16-byte pieces the threads of a row's second 64 elements store the
+                            // second one first: a quarter warp's stores use all banks)
+                            const uint32_t base = to + (c >> 2) * C::kChunkBytes, p0 = 2 * (c & 3), odd = c >> 2;
+#pragma unroll
+                            for (int hh = 0; hh < 2; ++hh) {
+                                const uint32_t second = odd ^ hh;
+                                st_shared4(base + sw128(row, p0 + second), second ? y[4] : y[0], second ? y[5] : y[1],
+                                           second ? y[6] : y[2], second ? y[7] : y[3]);
+                            }
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive((which ? v_full : k_full) + st);
-                            mbar_arrive((which ? cv_empty : ck_empty) + cst);
+                            mbar_arrive(&v_full[st]);
+                            mbar_arrive(&c_empty[st]);
                         }
+                        ++kv_it;
                     }
+                    // the next row tile, once the products of the piece before this one are on their way
+                    if (t == 0 && i + 1 < count) split_rows(i + 1);
                 }
             }
             if (!ok) s_abort = 1;
@@ -711,7 +769,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             const int wg_tid = tid - 128 * (k + 1);
             const uint32_t tS = tbase + lane_off + C::kColS + k * 128;
             const uint32_t tO = tbase + lane_off + C::kColO + k * D;
-            const float sl2 = p.scale_log2;
+            float sl2 = p.scale_log2;
+            constexpr float kUnitP = kFp8 ? 7.f : 0.f;  // log2 of what P is multiplied by
 #pragma unroll 1
             for (int i = 0; i < count && !warp_flag(s_abort); ++i) {
                 const Piece U = pieces[i];
@@ -719,7 +778,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 const int tok = (two ? k * p.tpt : 0) + row_tok;  // of the unit
                 const bool write = row_tok < p.tpt && tok < U.ntok;
                 const bool common = U.slot < 0;
-                const uint32_t kv_base = kv_it;
+                const uint32_t kv_base = kv_it, piece = n_p++;
                 kv_it += U.nkt;
                 const int step = two ? 1 : 2, t_first = two ? 0 : (k ^ (int)(kv_base & 1));
                 if (t_first >= U.nkt) continue;  // no key tile for this lane (and the join reads no result of it)
@@ -729,8 +788,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 const int64_t slot = U.slot & INT32_MAX;
                 float* po = (common ? p.po_pre : p.po_own) + slot * 2 * half * D + at * 4;
                 float* pl = (common ? p.pl_pre : p.pl_own) + slot * 2 * half + at;
-                // no row of this warp is a token's: it only keeps the lane's step
-                const bool idle = 32 * (warp & 3) >= min(p.tpt, U.ntok - (two ? k * p.tpt : 0)) * p.G;
+                // warps with rows that are a token's; the others only keep the lane's step
+                const int busy = (min(p.tpt, U.ntok - (two ? k * p.tpt : 0)) * p.G + 31) / 32;
+                const bool idle = (warp & 3) >= busy;
                 const int c1 = min(U.c1, U.pos0 + tok + 1);  // the row's visible keys end here
                 const int all1 = min(U.c1, U.pos0 + 1);      // every row sees these
                 float m_used = -INFINITY, l = 0.f;
@@ -739,6 +799,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 for (int t = t_first; t < U.nkt; t += step) {
                     if (!mbar_wait_warp(&s_full[k], n_s & 1, p.err)) { ok = false; break; }
                     tc_fence_after();
+                    if (kFp8 && t == t_first) sl2 = p.scale_log2 * row_unit[(piece & 3) * 128 + row];
                     const int kb = U.kb0 + t * kKeys;
                     const bool edge = kb < U.c0 || kb + kKeys > all1;
                     float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -776,11 +837,11 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 #pragma unroll
                         for (int j = 0; j < 64; j += 2) {
                             float x0, x1;
-                            fma2_bcast(x0, x1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), sl2, -m_off);
+                            fma2_bcast(x0, x1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), sl2, kUnitP - m_off);
                             const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
                             const int a = (j >> 1) & 3;
                             add2(ls[2 * a], ls[2 * a + 1], e0, e1);
-                            pk[j / 2] = pack_bf16(e0, e1);
+                            pk[j / 2] = kFp8 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
                         }
                         tmem_st32(tS + 32 * h, pk);
                     };
@@ -794,8 +855,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     if (idle) {
                         early = !edge;  // (value rows outside the segment's keys are zeroed by all warps)
                         if (early) signal_half();
-                    } else if (!kFp8 && !edge) {  // the whole row in registers
-                        if constexpr (!kFp8) {
+                    } else if (!edge) {
+                        if constexpr (!kFp8) {  // the whole row in registers
                             uint32_t r0[64], r1[64];
                             load_half(r0, 0);
                             load_half(r1, 1);
@@ -807,6 +868,24 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                             store_half(r0, 0);
                             if (early) signal_half();
                             store_half(r1, 1);
+                        } else {  // twice over it in halves: these lanes have fewer registers
+#pragma unroll 1
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t r[64];
+                                load_half(r, h);
+                                tmem_wait_ld();
+                                max_half(r);
+                            }
+                            take_max();
+                            early = !__any_sync(0xffffffffu, rescale);
+#pragma unroll 1
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t r[64];
+                                load_half(r, h);
+                                tmem_wait_ld();
+                                store_half(r, h);
+                                if (h == 0 && early) signal_half();
+                            }
                         }
                     } else {
                         // twice over the row, 32 scores at a time in one loop body, masked by bits: few
@@ -820,8 +899,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t r[32];
-                            tmem_ld32(tS + 32 * c, r);
                             const uint32_t bits = visible(c);
+                            if (!__any_sync(0xffffffffu, bits)) continue;
+                            tmem_ld32(tS + 32 * c, r);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 32; j += 2)
@@ -829,25 +909,30 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                                                           (bits >> (j + 1)) & 1 ? __uint_as_float(r[j + 1]) : -INFINITY);
                         }
                         take_max();
-                        early = !edge && !__any_sync(0xffffffffu, rescale);
+                        early = false;
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t r[32], pk[16];
-                            tmem_ld32(tS + 32 * c, r);
                             const uint32_t bits = visible(c);
+                            if (!__any_sync(0xffffffffu, bits)) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) pk[j] = 0;
+                                tmem_st16(tS + 16 * c, pk);
+                                continue;
+                            }
+                            tmem_ld32(tS + 32 * c, r);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 32; j += 2) {
                                 float x0, x1;
                                 fma2_bcast(x0, x1, (bits >> j) & 1 ? __uint_as_float(r[j]) : -INFINITY,
-                                           (bits >> (j + 1)) & 1 ? __uint_as_float(r[j + 1]) : -INFINITY, sl2, -m_off);
+                                           (bits >> (j + 1)) & 1 ? __uint_as_float(r[j + 1]) : -INFINITY, sl2, kUnitP - m_off);
                                 const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
                                 const int a = (j >> 1) & 3;
                                 add2(ls[2 * a], ls[2 * a + 1], e0, e1);
-                                pk[j / 2] = pack_bf16(e0, e1);
+                                pk[j / 2] = kFp8 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
                             }
                             tmem_st16(tS + 16 * c, pk);
-                            if (early && c == 1) signal_half();
                         }
                     }
                     l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
@@ -864,17 +949,18 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         }
                     }
                     tmem_wait_st();
-                    // value rows outside the segment's keys may hold anything: zero. With two
-                    // row tiles lane 0 does it (lane 1's product of a tile follows lane 0's).
+                    // value rows outside the segment's keys may hold anything: zeros, by the warps
+                    // without rows if there are any. With two row tiles lane 0 does it (lane 1's
+                    // product of a tile follows lane 0's).
                     const int zlo = max(0, U.c0 - kb), zhi = min(kKeys, U.c1 - kb);
-                    if ((zlo > 0 || zhi < kKeys) && (k == 0 || !two)) {
+                    if (!kFp8 && (zlo > 0 || zhi < kKeys) && (k == 0 || !two) && (idle || busy == 4)) {
                         const uint32_t vi = kv_base + t;
                         if (!mbar_wait_warp(&v_full[vi & 1], (vi >> 1) & 1, p.err)) { ok = false; break; }
                         uint8_t* vt = smem + C::kOffV + (vi & 1) * C::kTileBytes;
+                        const int skip = busy == 4 ? 0 : 32 * busy;
 #pragma unroll 1
-                        for (int ci = wg_tid; ci < kKeys * (D / 8); ci += 128) {
-                            const int vr = ci / (D / 8), c = ci % (D / 8);
-                            if (vr >= zlo && vr < zhi) continue;
+                        for (int ci = wg_tid - skip; ci < (zlo + kKeys - zhi) * (D / 8); ci += 128 - skip) {
+                            const int z = ci / (D / 8), c = ci % (D / 8), vr = z < zlo ? z : zhi + z - zlo;
                             *reinterpret_cast<uint4*>(vt + (c >> 3) * C::kChunkBytes + sw128(vr, c & 7)) = make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
@@ -911,7 +997,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_free[k]);
-                if (write) *pl = m_used + log2f(l);
+                if (write) *pl = m_used + log2f(l) - kUnitP;
             }
             __syncwarp();
             setmaxnreg_dec<C::kRegsLaunch>();

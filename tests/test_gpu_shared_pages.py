@@ -2,7 +2,9 @@
 
 Tolerances, from the arithmetic. Whole numbers are equal. Attention: the result's and the weights' rounding to bf16 are
 off by at most 2^-8 of the value and of each weight; a score of d products in 32 bits by (d + 8) 2^-24 of the sum of
-their magnitudes, which moves a weight by as much of itself; exponentials and logarithms by a few 2^-22."""
+their magnitudes, which moves a weight by as much of itself; exponentials and logarithms by a few 2^-22. Over an 8-bit
+cache a query is two E4M3 numbers in units that bring its largest element to 224 at least: off by half of 2^-9, 2^-17 of
+the largest, per element; the weights there are f16 (2^-11), within the bf16 bound."""
 import math
 import threading
 
@@ -447,6 +449,9 @@ def prefix_check(s):
     n, d = qsl[-1], s["q"].shape[2]
     got = f64(s["out"])
     delta = (d + 8) * 2.0 ** -24 * reach[:n] + 2.0 ** -20
+    if s["scales"]:  # the queries' split
+        largest = np.abs(f64(s["q"])[:n]).max(-1)
+        delta += 2.0 ** -17 * largest * np.abs(k).sum(-1).max() * s["scale"] * ks
     limit = 2.0 ** -8 * np.abs(out[:n]) + (2.0 ** -8 + 3 * delta[..., None]) * mag[:n] * (1 + 2.0 ** -6) + 1e-30
     worst = np.abs(got[:n] - out[:n]) / limit
     assert np.isfinite(got[:n]).all() and (worst <= 1).all(), (worst.max(), np.unravel_index(worst.argmax(), worst.shape))
