@@ -328,15 +328,16 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             const int s = run * 32 + lane;
             const Seg g = seg_of(p, meta, s, err);
             const int units = g.nrt * p.Hkv, each = unit_cost(g), cost = units * each;
-            int ci = cost, ui = units;
-            warp_sums(ci, ui);
             if (pass == 0) {
-                if (lane == 31) {
-                    run_cost[run] = ci;
-                    run_units[run] = ui;
+                const int c = __reduce_add_sync(0xffffffffu, cost), u = __reduce_add_sync(0xffffffffu, units);
+                if (lane == 0) {
+                    run_cost[run] = c;
+                    run_units[run] = u;
                 }
                 continue;
             }
+            int ci = cost, ui = units;
+            warp_sums(ci, ui);
             const int cs = run_cost[run] + ci - cost, us = run_units[run] + ui - units;
             if (pass == 1 && run % ncta == cta && s < p.own0 + p.B) {  // for the join
                 p.seg_cost[s] = cs;
@@ -888,51 +889,44 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                             }
                         }
                     } else {
-                        // twice over the row, 32 scores at a time in one loop body, masked by bits: few
-                        // registers and, above all, few instructions (an unrolled masked row took 3.8 us
-                        // for the fetch of its code, once per unit)
+                        // twice over the row, 32 scores at a time in one loop body: few registers and, above
+                        // all, few instructions (an unrolled masked row took 3.8 us for the fetch of its
+                        // code, once per unit). Chunks that no row of the warp sees are left out, and only
+                        // those that not every row sees in full are masked.
                         const int vlo = U.c0 - kb, vhi = max(vlo, c1 - kb);  // visible columns [vlo, vhi)
-                        auto visible = [&](int c) {
-                            const int a = min(32, max(0, vlo - 32 * c)), b = min(32, max(0, vhi - 32 * c));
-                            return (uint32_t)((1ull << b) - (1ull << a));
-                        };
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t r[32];
-                            const uint32_t bits = visible(c);
-                            if (!__any_sync(0xffffffffu, bits)) continue;
-                            tmem_ld32(tS + 32 * c, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2)
-                                mx[(j >> 1) & 7] = fmax3f(mx[(j >> 1) & 7], (bits >> j) & 1 ? __uint_as_float(r[j]) : -INFINITY,
-                                                          (bits >> (j + 1)) & 1 ? __uint_as_float(r[j + 1]) : -INFINITY);
-                        }
-                        take_max();
                         early = false;
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t r[32], pk[16];
-                            const uint32_t bits = visible(c);
-                            if (!__any_sync(0xffffffffu, bits)) {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) pk[j] = 0;
-                                tmem_st16(tS + 16 * c, pk);
+                        for (int c = 0; c < 8; ++c) {
+                            const int at = 32 * (c & 3), a = min(32, max(0, vlo - at)), b = min(32, max(0, vhi - at));
+                            const uint32_t bits = (uint32_t)((1ull << b) - (1ull << a));  // (a <= b)
+                            if (c == 4) take_max();
+                            if (!__any_sync(0xffffffffu, bits != 0)) {
+                                if (c >= 4) tmem_st16_zero(tS + (at >> 1));
                                 continue;
                             }
-                            tmem_ld32(tS + 32 * c, r);
+                            uint32_t r[32];
+                            tmem_ld32(tS + at, r);
                             tmem_wait_ld();
+                            if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                float x0, x1;
-                                fma2_bcast(x0, x1, (bits >> j) & 1 ? __uint_as_float(r[j]) : -INFINITY,
-                                           (bits >> (j + 1)) & 1 ? __uint_as_float(r[j + 1]) : -INFINITY, sl2, kUnitP - m_off);
-                                const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-                                const int a = (j >> 1) & 3;
-                                add2(ls[2 * a], ls[2 * a + 1], e0, e1);
-                                pk[j / 2] = kFp8 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+                                for (int j = 0; j < 32; ++j) r[j] = (bits >> j) & 1 ? r[j] : 0xff800000u;
                             }
-                            tmem_st16(tS + 16 * c, pk);
+                            if (c < 4) {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2)
+                                    mx[(j >> 1) & 7] = fmax3f(mx[(j >> 1) & 7], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    float x0, x1;
+                                    fma2_bcast(x0, x1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), sl2, kUnitP - m_off);
+                                    const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+                                    const int q = (j >> 1) & 3;
+                                    add2(ls[2 * q], ls[2 * q + 1], e0, e1);
+                                    r[j / 2] = kFp8 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+                                }
+                                tmem_st16(tS + (at >> 1), *reinterpret_cast<const uint32_t(*)[16]>(r));
+                            }
                         }
                     }
                     l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
@@ -1046,72 +1040,92 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParam
     const int common = common_keys(r0, r1, __ldg(p.prefix + g));
     const bool inside = r0 >= 0 && r1 >= r0 && r1 <= p.B;
     const int gq0 = inside ? __ldg(p.qsl + r0) : 0, gq1 = inside ? __ldg(p.qsl + r1) : 0;
-    grid_dep_wait();
-    const int total = __ldcg(p.seg_cost + p.own0 + p.B);
-    if (total < 0 || at.r < 0) return;  // refused lengths, or a row behind the last request's: nothing is written
-    const int cost_at[2] = {__ldcg(p.seg_cost + g), __ldcg(p.seg_cost + p.own0 + at.r)};
-    const int unit_at[2] = {__ldcg(p.seg_unit + g), __ldcg(p.seg_unit + p.own0 + at.r) - __ldcg(p.seg_unit + p.own0)};
-    const Shares shares(total, ncta);
+    const Seg seg[2] = {make_seg(p, gq0, gq1 - gq0, 0, common), make_seg(p, at.q0, at.q1 - at.q0, common, at.len)};
     int n = 0, n_common = 0;  // pieces, in the order of their keys
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-        const Seg s = part == 0 ? make_seg(p, gq0, gq1 - gq0, 0, common) : make_seg(p, at.q0, at.q1 - at.q0, common, at.len);
-        if (part == 1) n_common = n;
-        if (s.nkt == 0) continue;
-        const int rt = (t - s.q0) / p.upt, tok = (t - s.q0) - rt * p.upt;
-        const bool two = min(p.upt, s.n - rt * p.upt) > p.tpt;
-        const int local = h * s.nrt + rt, us = cost_at[part] + local * unit_cost(s), unit = unit_at[part] + local;
-        const int half = part == 0 ? p.rows_pre : p.rows_own;
-        const int row = two && tok >= p.tpt ? half + (tok - p.tpt) * G : tok * G;
-        const int first = shares.cta_of(us + kCostUnit), last = shares.cta_of(us + kCostUnit + (s.nkt - 1) * s.w);
-        const int lanes = two ? 1 : 2, end = s.c1 - s.n + min(s.n, (rt + 1) * p.upt);  // (of own keys)
+    // With few CTAs, which wait for the attention's end anyway, the steps up to the weights
+    // are run through once before it, over no pieces: their instructions are then at hand.
 #pragma unroll 1
-        for (int j = tid; j < (last - first + 1) * lanes; j += kThreads) {
-            const int c = first + (two ? j : j >> 1), k = two ? 0 : j & 1;
-            const int t0 = first_tile(shares.start(c), us, s), t1 = first_tile(shares.start(c + 1), us, s);
-            const int64_t slot = (int64_t)(unit + c) * 2 * half;
-            Source x;
-            x.o = (part == 0 ? p.po_pre : p.po_own) + slot * D + (k * half + row) * 4;
-            const int tiles = t0 >= t1 ? 0 : part == 0 ? t1 - t0 : seen_tiles(s, t0, t1, end);
-            x.l = tiles > k ? (part == 0 ? p.pl_pre : p.pl_own) + slot + k * half + row : nullptr;
-            src[n + j] = x;
+    for (int pass = kThreads == 512 ? 0 : 1; pass < 2; ++pass) {
+        int total = ncta, cost_at[2] = {0, 0}, unit_at[2] = {0, 0};
+        if (pass == 1) {
+            grid_dep_wait();
+            total = __ldcg(p.seg_cost + p.own0 + p.B);
+            cost_at[0] = __ldcg(p.seg_cost + g);
+            unit_at[0] = __ldcg(p.seg_unit + g);
+            cost_at[1] = __ldcg(p.seg_cost + p.own0 + max(at.r, 0));
+            unit_at[1] = __ldcg(p.seg_unit + p.own0 + max(at.r, 0)) - __ldcg(p.seg_unit + p.own0);
+            if (total < 0 || at.r < 0) return;  // refused lengths, or a row behind the last request's: nothing is written
         }
-        n += (last - first + 1) * lanes;
+        const Shares shares(total, ncta);
+        n = 0;
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            const Seg s = part == 0 ? seg[0] : seg[1];
+            if (part == 1) n_common = n;
+            if (s.nkt == 0) continue;
+            int tok = t - s.q0, rt = 0;
+            if (s.nrt > 1) {
+                rt = tok / p.upt;
+                tok -= rt * p.upt;
+            }
+            const bool two = min(p.upt, s.n - rt * p.upt) > p.tpt;
+            const int local = h * s.nrt + rt, us = (part == 0 ? cost_at[0] : cost_at[1]) + local * unit_cost(s);
+            const int unit = (part == 0 ? unit_at[0] : unit_at[1]) + local;
+            const int half = part == 0 ? p.rows_pre : p.rows_own;
+            const int row = two && tok >= p.tpt ? half + (tok - p.tpt) * G : tok * G;
+            const int first = shares.cta_of(us + kCostUnit), last = shares.cta_of(us + kCostUnit + (s.nkt - 1) * s.w);
+            const int lanes = two ? 1 : 2, end = s.c1 - s.n + min(s.n, (rt + 1) * p.upt);  // (of own keys)
+            const float* o = part == 0 ? p.po_pre : p.po_own;
+            const float* l = part == 0 ? p.pl_pre : p.pl_own;
+#pragma unroll 1
+            for (int j = tid; j < (last - first + 1) * lanes && pass == 1; j += kThreads) {
+                const int c = first + (two ? j : j >> 1), k = two ? 0 : j & 1;
+                const int t0 = first_tile(shares.start(c), us, s), t1 = first_tile(shares.start(c + 1), us, s);
+                const int tiles = t0 >= t1 ? 0 : part == 0 ? t1 - t0 : seen_tiles(s, t0, t1, end);
+                const int64_t slot = (int64_t)(unit + c) * 2 * half;
+                Source x;
+                x.o = o + slot * D + (k * half + row) * 4;
+                x.l = tiles > k ? l + slot + k * half + row : nullptr;
+                src[n + j] = x;
+            }
+            n += (last - first + 1) * lanes;
+        }
+        if (pass == 0) n = n_common = 0;
+        __syncthreads();
+        // ---- weights: a warp per head
+#pragma unroll 1
+        for (int hh = warp; hh < G; hh += kWarps) {
+            float top = -INFINITY, nan = 0.f;
+#pragma unroll 1
+            for (int i = lane; i < n; i += 32) {
+                const float* from = src[i].l;
+                const float l = from ? __ldcg(from + hh) : -INFINITY;
+                weight[i * G + hh] = l;
+                top = fmaxf(top, l);
+                nan += l == l ? 0.f : l;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                nan += __shfl_xor_sync(0xffffffffu, nan, o);
+            }
+            float sum = nan;
+#pragma unroll 1
+            for (int i = lane; i < n; i += 32) {
+                const float l = weight[i * G + hh];
+                const float w = l == -INFINITY ? 0.f : l == top ? 1.f : exp2f(l - top);
+                weight[i * G + hh] = w;
+                sum += w;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0 && pass == 1) {
+                s_inv[hh] = sum == 0.f ? 0.f : p.v_scale / sum;
+                if (p.lse) p.lse[(int64_t)t * p.Hq + h * G + hh] = (top + log2f(sum)) * 0.69314718055994531f;
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    // ---- weights: a warp per head
-#pragma unroll 1
-    for (int hh = warp; hh < G; hh += kWarps) {
-        float top = -INFINITY, nan = 0.f;
-#pragma unroll 1
-        for (int i = lane; i < n; i += 32) {
-            const float* from = src[i].l;
-            const float l = from ? __ldcg(from + hh) : -INFINITY;
-            weight[i * G + hh] = l;
-            top = fmaxf(top, l);
-            nan += l == l ? 0.f : l;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            nan += __shfl_xor_sync(0xffffffffu, nan, o);
-        }
-        float sum = nan;
-#pragma unroll 1
-        for (int i = lane; i < n; i += 32) {
-            const float l = weight[i * G + hh];
-            const float w = l == -INFINITY ? 0.f : l == top ? 1.f : exp2f(l - top);
-            weight[i * G + hh] = w;
-            sum += w;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) {
-            s_inv[hh] = sum == 0.f ? 0.f : p.v_scale / sum;
-            if (p.lse) p.lse[(int64_t)t * p.Hq + h * G + hh] = (top + log2f(sum)) * 0.69314718055994531f;
-        }
-    }
-    __syncthreads();
     // ---- the weighted sums: four dims of a head per thread, the pieces dealt out where threads are left over
     const int flats = D / 4 * G, deal = max(1, kThreads / flats);
     float4* parts = reinterpret_cast<float4*>(weight + (size_t)4 * ncta * G);  // [deal][flats], where deal > 1
