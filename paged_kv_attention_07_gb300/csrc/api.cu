@@ -1516,6 +1516,7 @@ pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_ca
         return cf.fp8 ? encode_rows_u8(map, cache, rows, block_size) : encode_rows(map, cache, rows, head_dim, block_size);
     };
     if (!encode_head_rows(&maps.q, q, num_tokens, num_q_heads, head_dim, (uint32_t)p.G, (uint32_t)p.tpt) ||
+        !encode_head_rows(&maps.q_half, q, num_tokens, num_q_heads, head_dim, (uint32_t)p.G, (uint32_t)p.tpt / 2) ||
         !encode_cache(&maps.k, k_cache) || !encode_cache(&maps.v, v_cache))
         return PKA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -186,6 +186,8 @@ PKA_DEVICE void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
                  : "memory");
 }
 
+PKA_DEVICE void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // L2 prefetch of `bytes` (a multiple of 16) from a 16-byte aligned address.
 PKA_DEVICE void bulk_prefetch_l2(const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)

@@ -257,7 +257,8 @@ struct CopyPagesParams {
 constexpr int kPrefixMaxCost = 4;
 
 struct PrefixMaps {
-    CUtensorMap q;  // [T, Hq, D]  box {64, G, 128 / G}
+    CUtensorMap q;       // [T, Hq, D]  box {64, G, 128 / G}
+    CUtensorMap q_half;  // box {64, G, 128 / G / 2}
     CUtensorMap k;  // [nb * Hkv * bs, D]  box {64, bs}; codes: box {128, bs}
     CUtensorMap v;
 };

@@ -150,16 +150,10 @@ struct PxCfg {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// The block of lane `b` of the key tile at kb (lanes past its valid blocks get 0).
-PKA_DEVICE int tile_block(const PrefixParams& p, const int32_t* bt, int kb, int c1, int lane) {
-    const int pos = kb + (lane << p.bs_log2);
-    if (lane >= (kKeys >> p.bs_log2) || pos >= c1) return 0;
-    int blk = __ldg(bt + (pos >> p.bs_log2));
-    if (blk < 0 || blk >= p.num_blocks) {
-        set_error(p.err, PKA_DEVERR_BLOCK_ID);
-        blk = 0;
-    }
-    return blk;
+// Entries [32 chunk, 32 chunk + 32) of the table from a piece's first page on, one per lane.
+PKA_DEVICE int table_entry(const PrefixParams& p, const Piece& U, int chunk, int lane) {
+    const int pos = U.kb0 + ((32 * chunk + lane) << p.bs_log2);
+    return pos < U.c1 ? __ldg(p.block_table + (int64_t)U.table * p.max_blocks + (pos >> p.bs_log2)) : 0;
 }
 
 // The lengths of a call in shared memory.
@@ -371,6 +365,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     x.slot = us + u + cta - run_units[p.own0 / 32];
                 }
                 pieces[atomicAdd(&s_pieces, 1)] = x;  // (in any order: a piece's result does not depend on it)
+                // what its first copies hang on
+                prefetch_l2(p.block_table + (int64_t)x.table * p.max_blocks + (x.kb0 >> p.bs_log2));
+                bulk_prefetch_l2(p.q + ((int64_t)x.q0 * p.Hq + x.h * p.G) * D, (uint32_t)(p.G * D * 2));
             }
         }
         if (pass == 0) {
@@ -420,7 +417,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             setmaxnreg_dec<C::kRegsIssue>();
             __syncthreads();
             if (warp == 0 || warp == 2) {
-                // -------------------------------------------------------- producers: K; V and Q
+                // -------------------------------------------------------- producers: Q and K; V
                 const int which = warp == 0 ? 0 : 1;
                 const uint64_t pol = policy_evict_normal(), pol_q = policy_evict_last();
                 const bool tma = p.bs >= 8;
@@ -432,16 +429,17 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 constexpr int kStage = C::kStageK;
                 constexpr int kBoxes = kFp8 ? 1 : C::kChunk;  // 128 bytes wide
                 bool ok = true;
-                auto first_block = [&](int i) {
-                    const Piece& U = pieces[i];
-                    return tile_block(p, p.block_table + (int64_t)U.table * p.max_blocks, U.kb0, U.c1, lane);
-                };
-                int next = tma && count > 0 ? first_block(0) : 0;
+                // Table entries are fetched 32 at a time and a chunk (or a piece) ahead: under the
+                // kernel's own traffic such a load takes up to 3 us, and one for each tile held
+                // back the small units' tiles by as much.
+                const int per_log2 = tma ? p.bs_log2 - 2 : 0;  // log2 of a chunk's key tiles
+                int ids = 0, ids_next = tma && count > 0 ? table_entry(p, pieces[0], 0, lane) : 0;
 #pragma unroll 1
                 for (int i = 0; i < count && ok && !warp_flag(s_abort); ++i) {
                     const Piece U = pieces[i];
-                    if (!kFp8 && which == 1) {
+                    if (!kFp8 && which == 0) {  // (beside K: a unit's V waits for older products)
                         const int nq = U.ntok > p.tpt ? 2 : 1;
+                        const bool twice = U.ntok <= p.tpt / 2;
 #pragma unroll 1
                         for (int k = 0; k < nq && ok; ++k, ++q_it) {
                             const int at = q_it % C::kRowTiles;
@@ -451,10 +449,13 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                                 break;
                             }
                             if (lane == 0) {
-                                mbar_arrive_expect_tx(&q_full[at], (uint32_t)(C::kChunk * p.tpt * p.G * 128));
-                                for (int c = 0; c < C::kChunk; ++c)
-                                    tma_load_3d(smem + C::kOffQ + at * C::kTileBytes + c * C::kChunkBytes, &maps.q,
-                                                &q_full[at], c * 64, U.h * p.G, U.q0 + k * p.tpt, pol_q);
+                                const int boxes = twice ? 2 : 1, tokens = twice ? p.tpt / 2 : p.tpt;
+                                mbar_arrive_expect_tx(&q_full[at], (uint32_t)(C::kChunk * boxes * tokens * p.G * 128));
+                                for (int c = 0; c < C::kChunk * boxes; ++c)
+                                    tma_load_3d(smem + C::kOffQ + at * C::kTileBytes + c / boxes * C::kChunkBytes +
+                                                    c % boxes * (C::kChunkBytes / 2),
+                                                twice ? &maps.q_half : &maps.q, &q_full[at], c / boxes * 64, U.h * p.G,
+                                                U.q0 + k * p.tpt, pol_q);
                             }
                         }
                         if (!ok) {
@@ -468,9 +469,12 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         const int st = (int)(kv_it % nst);
                         const uint32_t n = kv_it / nst;
                         const int kb = U.kb0 + t * kKeys;
-                        const int block = next;
-                        if (tma && t + 1 < U.nkt) next = tile_block(p, bt, kb + kKeys, U.c1, lane);
-                        else if (tma && i + 1 < count) next = first_block(i + 1);
+                        if (tma && (t & ((1 << per_log2) - 1)) == 0) {
+                            const int chunk = (t >> per_log2) + 1;
+                            ids = ids_next;
+                            if (chunk << per_log2 < U.nkt) ids_next = table_entry(p, U, chunk, lane);
+                            else if (i + 1 < count) ids_next = table_entry(p, pieces[i + 1], 0, lane);
+                        }
                         if (n > 0 && !mbar_wait_warp(&empties[st], (n - 1) & 1, p.err)) {
                             s_abort = 1;
                             ok = false;
@@ -480,8 +484,13 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         if (tma) {
                             const int valid = min(kKeys >> p.bs_log2, (U.c1 - kb + p.bs - 1) >> p.bs_log2);
                             if (lane == 0) mbar_arrive_expect_tx(&fulls[st], (uint32_t)(valid * kBoxes * p.bs * 128));
-                            __syncwarp();
+                            int block = __shfl_sync(0xffffffffu, ids,
+                                                    ((t & ((1 << per_log2) - 1)) << (7 - p.bs_log2)) + lane & 31);
                             if (lane < valid) {
+                                if (block < 0 || block >= p.num_blocks) {
+                                    set_error(p.err, PKA_DEVERR_BLOCK_ID);
+                                    block = 0;
+                                }
                                 const int row = (block * p.Hkv + U.h) << p.bs_log2;
 #pragma unroll
                                 for (int c = 0; c < kBoxes; ++c)
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 for (uint32_t back = 1; back <= nst && back <= kv_it; ++back)
                     mbar_wait_warp(&fulls[(kv_it - back) % nst], ((kv_it - back) / nst) & 1, p.err);
 #pragma unroll 1
-                for (uint32_t back = 1; !kFp8 && which == 1 && back <= C::kRowTiles && back <= q_it; ++back)
+                for (uint32_t back = 1; !kFp8 && which == 0 && back <= C::kRowTiles && back <= q_it; ++back)
                     mbar_wait_warp(&q_full[(q_it - back) % C::kRowTiles], ((q_it - back) / C::kRowTiles) & 1, p.err);
             } else if (lane == 0 && warp == 1) {
                 // -------------------------------------------------------- S_k = Q K^T
@@ -642,26 +651,29 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             // outside the segment's keys may hold anything: zeros.
             const int wtid = tid - 384;
             bool ok = true;
-            auto split_rows = [&](int i) {  // the row tile of piece i
-                const Piece& U = pieces[i];
+            const int part = lane & 7;
+            // rows r0 .. r0 + 31 of a piece's row tile, 8 lanes to a row, 16 elements to a lane
+            auto load_rows = [&](const Piece& U, int r0, uint4 (&x)[2][2]) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = min(r0 + 16 * j + (wtid >> 3), U.ntok * p.G - 1), tok = row / p.G;
+                    const uint4* from = reinterpret_cast<const uint4*>(
+                        p.q + ((int64_t)(U.q0 + tok) * p.Hq + U.h * p.G + (row - tok * p.G)) * D) + 2 * part;
+                    x[j][0] = __ldg(from);
+                    x[j][1] = __ldg(from + 1);
+                }
+            };
+            auto split_rows = [&](const Piece& U, uint4 (&x)[2][2]) {  // (the first 32 are loaded)
                 const uint32_t n = q_it / C::kRowTiles;
                 if (n > 0 && !mbar_wait_warp(&q_empty[q_it % C::kRowTiles], (n - 1) & 1, p.err)) {
                     ok = false;
                     return;
                 }
                 const uint32_t to = sm_base + C::kOffQ + q_it % C::kRowTiles * C::kTileBytes;
-                const int rows = U.ntok * p.G, part = lane & 7;
+                const int rows = U.ntok * p.G;
 #pragma unroll 1
-                for (int r0 = 0; r0 < rows; r0 += 32) {  // two rounds of 8 lanes per row
-                    uint4 x[2][2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int row = min(r0 + 16 * j + (wtid >> 3), rows - 1), tok = row / p.G;
-                        const uint4* from = reinterpret_cast<const uint4*>(
-                            p.q + ((int64_t)(U.q0 + tok) * p.Hq + U.h * p.G + (row - tok * p.G)) * D) + 2 * part;
-                        x[j][0] = __ldg(from);
-                        x[j][1] = __ldg(from + 1);
-                    }
+                for (int r0 = 0; r0 < rows; r0 += 32) {
+                    if (r0 > 0) load_rows(U, r0, x);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int row = r0 + 16 * j + (wtid >> 3);
@@ -670,7 +682,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             top = fmax3f(top, fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e])));
-                            odd += (bf16_lo(w[e]) + bf16_hi(w[e])) * 0.f;  // (NaN where an element is not finite)
+                            odd += bf16_lo(w[e]) * 0.f + bf16_hi(w[e]) * 0.f;  // (NaN where an element is not finite)
                         }
 #pragma unroll
                         for (int o = 1; o < 8; o <<= 1) {
@@ -693,9 +705,14 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                             low[e] = e4m3x4(v0 - a.x, v1 - a.y, v2 - b.x, v3 - b.y);
                         }
                         if (row < rows) {
-                            st_shared4(to + sw128(row, part), hi[0], hi[1], hi[2], hi[3]);
-                            st_shared4(to + C::kCodeBytes + sw128(row, part), low[0], low[1], low[2], low[3]);
-                            if (part == 0) row_unit[(q_it & 3) * 128 + row] = exp2i(e2 - 9) + odd;
+#pragma unroll
+                            for (int copy = 0; copy < 2; ++copy) {
+                                const int at = row + 64 * copy;
+                                if (copy && U.ntok > p.tpt / 2) continue;
+                                st_shared4(to + sw128(at, part), hi[0], hi[1], hi[2], hi[3]);
+                                st_shared4(to + C::kCodeBytes + sw128(at, part), low[0], low[1], low[2], low[3]);
+                                if (part == 0) row_unit[(q_it & 3) * 128 + at] = exp2i(e2 - 9) + odd;
+                            }
                         }
                     }
                 }
@@ -710,6 +727,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 const int nkt = i < 0 ? 1 : U.nkt;
 #pragma unroll 1
                 for (int t = 0; t < nkt && ok; ++t) {
+                    uint4 x[2][2];
+                    const bool rows_next = t == 0 && i + 1 < count;
+                    if (rows_next) load_rows(pieces[i + 1], 0, x);
                     if (i >= 0) {
                         const int st = (int)(kv_it & 1);
                         const uint32_t n = kv_it >> 1;
@@ -753,7 +773,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         ++kv_it;
                     }
                     // the next row tile, once the products of the piece before this one are on their way
-                    if (t == 0 && i + 1 < count) split_rows(i + 1);
+                    if (rows_next) split_rows(pieces[i + 1], x);
                 }
             }
             if (!ok) s_abort = 1;
@@ -765,7 +785,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             // ------------------------------------------------------------ softmax lanes
             const int k = warp >= 8 ? 1 : 0;
             const int row = 32 * (warp & 3) + lane;  // of the row tile = tensor memory lane
-            const int row_tok = row / p.G;
+            const int row_tok0 = row / p.G, row_tok64 = (row & 63) / p.G;
             const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
             const int wg_tid = tid - 128 * (k + 1);
             const uint32_t tS = tbase + lane_off + C::kColS + k * 128;
@@ -776,8 +796,12 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             for (int i = 0; i < count && !warp_flag(s_abort); ++i) {
                 const Piece U = pieces[i];
                 const bool two = !kFp8 && U.ntok > p.tpt;
+                // Up to 64 rows lie in the row tile twice, and lane 1 takes the second copy: the two
+                // lanes' exponentials are then on different quarters of the SM.
+                const int shift = !two && U.ntok <= p.tpt / 2 && k == 1 ? 64 : 0;
+                const int row_tok = shift ? row_tok64 : row_tok0;
                 const int tok = (two ? k * p.tpt : 0) + row_tok;  // of the unit
-                const bool write = row_tok < p.tpt && tok < U.ntok;
+                const bool write = row >= shift && row_tok < p.tpt && tok < U.ntok;
                 const bool common = U.slot < 0;
                 const uint32_t kv_base = kv_it, piece = n_p++;
                 kv_it += U.nkt;
@@ -785,13 +809,13 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 if (t_first >= U.nkt) continue;  // no key tile for this lane (and the join reads no result of it)
                 // a lane's half of a slot: its row tile's, or that of the piece's first or second key tile on
                 const int half = common ? p.rows_pre : p.rows_own;
-                const int at = (two ? k : t_first) * half + row;
+                const int at = (two ? k : t_first) * half + row - shift;
                 const int64_t slot = U.slot & INT32_MAX;
                 float* po = (common ? p.po_pre : p.po_own) + slot * 2 * half * D + at * 4;
                 float* pl = (common ? p.pl_pre : p.pl_own) + slot * 2 * half + at;
                 // warps with rows that are a token's; the others only keep the lane's step
                 const int busy = (min(p.tpt, U.ntok - (two ? k * p.tpt : 0)) * p.G + 31) / 32;
-                const bool idle = (warp & 3) >= busy;
+                const bool idle = (uint32_t)((warp & 3) - shift / 32) >= (uint32_t)busy;
                 const int c1 = min(U.c1, U.pos0 + tok + 1);  // the row's visible keys end here
                 const int all1 = min(U.c1, U.pos0 + 1);      // every row sees these
                 float m_used = -INFINITY, l = 0.f;
@@ -951,9 +975,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         const uint32_t vi = kv_base + t;
                         if (!mbar_wait_warp(&v_full[vi & 1], (vi >> 1) & 1, p.err)) { ok = false; break; }
                         uint8_t* vt = smem + C::kOffV + (vi & 1) * C::kTileBytes;
-                        const int skip = busy == 4 ? 0 : 32 * busy;
+                        const int skip = busy == 4 ? 0 : 32 * busy;  // (threads of the lane that have rows)
 #pragma unroll 1
-                        for (int ci = wg_tid - skip; ci < (zlo + kKeys - zhi) * (D / 8); ci += 128 - skip) {
+                        for (int ci = wg_tid - ((warp & 3) >= shift / 32 ? skip : 0); ci < (zlo + kKeys - zhi) * (D / 8); ci += 128 - skip) {
                             const int z = ci / (D / 8), c = ci % (D / 8), vr = z < zlo ? z : zhi + z - zlo;
                             *reinterpret_cast<uint4*>(vt + (c >> 3) * C::kChunkBytes + sw128(vr, c & 7)) = make_uint4(0, 0, 0, 0);
                         }
