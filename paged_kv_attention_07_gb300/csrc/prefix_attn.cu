@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kKeys = 128;  // keys of a key tile
 constexpr int kPieces = 256;  // pieces of a list
+constexpr int kLongPiece = 4;  // key tiles from which a row's softmax is unrolled
 constexpr int kMaxSegs = 2 * kMaxRequests;
 constexpr int kChunks = kMaxSegs / 32;  // warp-sized runs of segments
 // Costs on the line: a key tile for one row tile, for two, and what a unit takes besides.
@@ -302,9 +303,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 
     // state of the roles across lists
     uint32_t kv_it = 0, q_it = 0;  // key tiles and row tiles so far
-    uint32_t nl[2] = {0, 0};    // S products (or P . V products) of each lane
+    uint32_t nl0 = 0, nl1 = 0;  // S products (or P . V products) of each lane
     uint32_t n_s = 0, n_p = 0;  // S tiles of this softmax lane, pieces
-    uint32_t uo[2] = {0, 0};    // units in which each lane had key tiles
+    uint32_t uo0 = 0, uo1 = 0;  // units in which each lane had key tiles
 
     // Pass 0 sums the runs of segments; pass j > 0 lists the pieces that begin in the
     // j-th stretch of the share (a piece costs kCostUnit + kCostOne at least but for
@@ -548,29 +549,30 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     for (int t = 0; t < nkt; ++t, ++kv_it) {
                         const int st = (int)(kv_it % C::kStagesK), only = (int)(kv_it & 1);
                         if (!mbar_wait(&k_full[st], (kv_it / C::kStagesK) & 1, p.err)) { ok = false; break; }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            if (!ok || (!two && k != only)) continue;
-                            if (nl[k] > 0 && !mbar_wait(&pv_done[k], (nl[k] - 1) & 1, p.err)) { ok = false; continue; }
+#pragma unroll 1
+                        for (int k = two ? 0 : only; k < (two ? 2 : only + 1); ++k) {
+                            const uint32_t done = k ? nl1 : nl0;
+                            if (done > 0 && !mbar_wait(&pv_done[k], (done - 1) & 1, p.err)) { ok = false; break; }
                             tc_fence_after();
                             const uint32_t qa = q_s + (k == 1 ? q1 : q0) % C::kRowTiles * C::kTileBytes;
+                            const uint64_t a_desc = umma_desc_sw128(qa, 16, 1024), b_desc = umma_desc_sw128(k_s + st * C::kStageK, 16, 1024);
+                            const uint32_t d = tbase + C::kColS + k * 128;
+                            // (a descriptor's address counts 16 bytes)
                             if constexpr (kFp8) {  // the rows' upper and lower halves (the second tile) times the codes
 #pragma unroll
                                 for (int ks = 0; ks < 2 * (D / 32); ++ks)
-                                    umma_f8(tbase + C::kColS + k * 128,
-                                            umma_desc_sw128(qa + (ks >= D / 32 ? C::kCodeBytes : 0) + ks % (D / 32) * 32, 16, 1024),
-                                            umma_desc_sw128(k_s + st * C::kStageK + ks % (D / 32) * 32, 16, 1024), idesc,
-                                            ks > 0 ? 1u : 0u);
+                                    umma_f8(d, a_desc + ((ks >= D / 32 ? C::kCodeBytes : 0) + ks % (D / 32) * 32) / 16,
+                                            b_desc + ks % (D / 32) * 32 / 16, idesc, ks > 0 ? 1u : 0u);
                             } else {
 #pragma unroll
                                 for (int ks = 0; ks < D / 16; ++ks) {
                                     const uint32_t off = (ks >> 2) * C::kChunkBytes + (ks & 3) * 32;
-                                    umma_bf16(tbase + C::kColS + k * 128, umma_desc_sw128(qa + off, 16, 1024),
-                                              umma_desc_sw128(k_s + st * C::kStageK + off, 16, 1024), idesc, ks > 0 ? 1u : 0u);
+                                    umma_bf16(d, a_desc + off / 16, b_desc + off / 16, idesc, ks > 0 ? 1u : 0u);
                                 }
                             }
                             umma_commit(&s_full[k]);
-                            ++nl[k];
+                            if (k) ++nl1;
+                            else ++nl0;
                             if (k == 0 && t > 0) s_next0 = (int)kv_it;
                         }
                         if (!ok) break;
@@ -583,9 +585,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     if (ok) s_next0 = (int)kv_it;  // nothing of lane 0 follows in this unit
                 }
                 if (!ok) s_abort = 1;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (nl[k] > 0) mbar_wait(&s_full[k], (nl[k] - 1) & 1, p.err);
+                if (nl0 > 0) mbar_wait(&s_full[0], (nl0 - 1) & 1, p.err);
+                if (nl1 > 0) mbar_wait(&s_full[1], (nl1 - 1) & 1, p.err);
             } else if (lane == 0 && warp == 3) {
                 // -------------------------------------------------------- O_k += P_k V
                 constexpr uint32_t idesc = kFp8 ? umma_idesc_f16(128, D, 0, 1) : umma_idesc_bf16(128, D, 0, 1);
@@ -599,42 +600,42 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     for (int t = 0; t < nkt; ++t, ++kv_it) {
                         const int st = kv_it & 1;
                         if (!mbar_wait(&v_full[st], (kv_it >> 1) & 1, p.err)) { ok = false; break; }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            if (!ok || (!two && k != st)) continue;
+#pragma unroll 1
+                        for (int k = two ? 0 : st; k < (two ? 2 : st + 1); ++k) {
                             const bool first = two ? t == 0 : t < 2;
-                            if (two && k == 1 && !wait_counter(s_next0, (int)kv_it + 1, p.err)) { ok = false; continue; }
+                            const uint32_t done = k ? nl1 : nl0, units = k ? uo1 : uo0;
+                            if (two && k == 1 && !wait_counter(s_next0, (int)kv_it + 1, p.err)) { ok = false; break; }
+                            const uint64_t b_desc = umma_desc_sw128(v_s + st * C::kTileBytes, C::kChunkBytes, 1024);
+#pragma unroll 1
                             for (int hh = 0; hh < 2 && ok; ++hh) {
-                                if (!mbar_wait(hh ? &p_full[k] : &p_half[k], nl[k] & 1, p.err)) { ok = false; break; }
+                                if (!mbar_wait((hh ? p_full : p_half) + k, done & 1, p.err)) { ok = false; break; }
                                 // a unit's first product overwrites O_k: the unit before must have been read
-                                if (hh == 0 && first && uo[k] > 0 && !mbar_wait(&o_free[k], (uo[k] - 1) & 1, p.err)) {
+                                if (hh == 0 && first && units > 0 && !mbar_wait(&o_free[k], (units - 1) & 1, p.err)) {
                                     ok = false;
                                     break;
                                 }
                                 tc_fence_after();
 #pragma unroll
-                                for (int kq = 0; kq < kKeys / 32; ++kq) {
-                                    const int kk = hh * (kKeys / 32) + kq;
-                                    umma_bf16_ts(tbase + C::kColO + k * D, tbase + C::kColS + k * 128 + kk * 8,
-                                                 umma_desc_sw128(v_s + st * C::kTileBytes + kk * 2048, C::kChunkBytes, 1024),
-                                                 idesc, (!first || kk > 0) ? 1u : 0u);
-                                }
+                                for (int kq = 0; kq < kKeys / 32; ++kq)
+                                    umma_bf16_ts(tbase + C::kColO + k * D, tbase + C::kColS + k * 128 + (hh * (kKeys / 32) + kq) * 8,
+                                                 b_desc + (hh * (kKeys / 32) + kq) * (2048 / 16), idesc,
+                                                 (!first || hh > 0 || kq > 0) ? 1u : 0u);
                             }
-                            if (!ok) continue;
+                            if (!ok) break;
                             umma_commit(&pv_done[k]);
-                            ++nl[k];
+                            if (k) ++nl1;
+                            else ++nl0;
                         }
                         if (!ok) break;
                         umma_commit(&v_empty[st]);
                     }
                     const int only = two || nkt > 1 ? -1 : (int)((kv_it - 1) & 1);  // the one lane that had a key tile
-                    if (only != 1) ++uo[0];
-                    if (only != 0) ++uo[1];
+                    if (only != 1) ++uo0;
+                    if (only != 0) ++uo1;
                 }
                 if (!ok) s_abort = 1;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (nl[k] > 0) mbar_wait(&pv_done[k], (nl[k] - 1) & 1, p.err);
+                if (nl0 > 0) mbar_wait(&pv_done[0], (nl0 - 1) & 1, p.err);
+                if (nl1 > 0) mbar_wait(&pv_done[1], (nl1 - 1) & 1, p.err);
             }
             __syncwarp();
             setmaxnreg_inc<C::kRegsLaunch>();
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         }
                         tmem_st32(tS + 32 * h, pk);
                     };
-                    bool early;
+                    bool early = false;
                     auto signal_half = [&] {  // the product over keys 0..63 may start
                         tmem_wait_st();
                         tc_fence_before();
@@ -880,7 +881,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     if (idle) {
                         early = !edge;  // (value rows outside the segment's keys are zeroed by all warps)
                         if (early) signal_half();
-                    } else if (!edge) {
+                    } else if (U.nkt >= kLongPiece && !edge) {
                         if constexpr (!kFp8) {  // the whole row in registers
                             uint32_t r0[64], r1[64];
                             load_half(r0, 0);
@@ -914,16 +915,20 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         }
                     } else {
                         // twice over the row, 32 scores at a time in one loop body: few registers and, above
-                        // all, few instructions (an unrolled masked row took 3.8 us for the fetch of its
-                        // code, once per unit). Chunks that no row of the warp sees are left out, and only
-                        // those that not every row sees in full are masked.
+                        // all, few instructions: in a share of many short units a row unrolled took 3.5 us
+                        // for the fetch of its code (0.9 us where it stays at hand, as in long pieces), this
+                        // one takes 2 us. Chunks that no row of
+                        // the warp sees are left out, and only those that not every row sees in full are
+                        // masked.
                         const int vlo = U.c0 - kb, vhi = max(vlo, c1 - kb);  // visible columns [vlo, vhi)
-                        early = false;
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
                             const int at = 32 * (c & 3), a = min(32, max(0, vlo - at)), b = min(32, max(0, vhi - at));
                             const uint32_t bits = (uint32_t)((1ull << b) - (1ull << a));  // (a <= b)
-                            if (c == 4) take_max();
+                            if (c == 4) {
+                                take_max();
+                                early = !edge && !__any_sync(0xffffffffu, rescale);
+                            }
                             if (!__any_sync(0xffffffffu, bits != 0)) {
                                 if (c >= 4) tmem_st16_zero(tS + (at >> 1));
                                 continue;
@@ -950,6 +955,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                                     r[j / 2] = kFp8 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
                                 }
                                 tmem_st16(tS + (at >> 1), *reinterpret_cast<const uint32_t(*)[16]>(r));
+                                if (c == 5 && early) signal_half();
                             }
                         }
                     }
