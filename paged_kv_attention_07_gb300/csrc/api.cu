@@ -1504,6 +1504,7 @@ pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_ca
     p.G = num_q_heads / num_kv_heads;
     p.tpt = L.tpt;
     p.upt = cf.fp8 ? L.tpt : 2 * L.tpt;
+    p.cost_unit = cf.fp8 ? kPrefixMaxCost : 2;
     p.bs = block_size;
     p.bs_log2 = log2_of(block_size);
     p.max_query = max_query_len;

@@ -252,8 +252,7 @@ struct CopyPagesParams {
     int pieces;  // of a page, set by the launch
 };
 
-// At most: the cost of a key tile of a unit, or of the unit itself (prefix_attn.cu); the line of all costs keeps
-// to 32 bits.
+// At most the cost of a unit's key tile, or of the unit itself (prefix_attn.cu): the line of all costs keeps to 32 bits.
 constexpr int kPrefixMaxCost = 4;
 
 struct PrefixMaps {
@@ -287,6 +286,7 @@ struct PrefixParams {
     int rows_pre, rows_own;  // rows of a lane's half of a slot
     int B, groups, own0, T, max_blocks, Hq, Hkv, G, bs, bs_log2, max_query, max_seq;
     int tpt, upt;  // tokens of a row tile, and of a unit (one or two)
+    int cost_unit;  // see prefix_attn.cu; at most kPrefixMaxCost
     float scale_log2, v_scale;
 };
 

@@ -43,16 +43,18 @@ constexpr int kPieces = 256;  // pieces of a list
 constexpr int kLongPiece = 4;  // key tiles from which a row's softmax is unrolled
 constexpr int kMaxSegs = 2 * kMaxRequests;
 constexpr int kChunks = kMaxSegs / 32;  // warp-sized runs of segments
-// Costs on the line: a key tile for one row tile, for two, and what a unit takes besides.
-constexpr int kCostOne = 2, kCostTwo = 3, kCostUnit = 2;
-static_assert(kCostOne <= kPrefixMaxCost && kCostTwo <= kPrefixMaxCost && kCostUnit <= kPrefixMaxCost, "");
+// Costs on the line: a key tile for one row tile, for two, and what a unit takes besides
+// (its first copies, its end, lanes that wait for one another), as measured: 24 groups of 8
+// beams with (1, 2, 2) 119 us, (1, 2, 4) 132, (2, 3, 2) 130; over an 8-bit cache, whose tiles
+// are shorter, 32 groups of 4 with (1, 2, 2) 128 us, (1, 2, 4) 115.
+constexpr int kCostOne = 1, kCostTwo = 2;
 
 struct Seg {
     int q0, n;      // its tokens
     int c0, c1;     // its keys
     int base;       // the first key tile's first key
     int nkt, nrt;   // key tiles; units per kv head
-    int w;          // cost of a key tile
+    int w, e;       // costs: of a key tile, and of a unit besides
 };
 
 // How a token's rows and a unit's key tiles come from a segment.
@@ -65,7 +67,8 @@ PKA_DEVICE Seg make_seg(const PrefixParams& p, int q0, int n, int c0, int c1) {
     s.base = c0 & ~(p.bs - 1);
     s.nkt = n > 0 && c1 > c0 ? (c1 - s.base + kKeys - 1) / kKeys : 0;
     s.nrt = s.nkt == 0 ? 0 : n <= p.upt ? 1 : (n + p.upt - 1) / p.upt;
-    s.w = n > p.tpt ? kCostTwo : kCostOne;
+    s.w = p.upt > p.tpt && n > p.tpt ? kCostTwo : kCostOne;
+    s.e = p.cost_unit;
     return s;
 }
 
@@ -94,11 +97,11 @@ struct Shares {
         return x < cut ? x / (base + 1) : rem + (x - cut) / base;
     }
 };
-PKA_DEVICE int unit_cost(const Seg& s) { return s.nkt > 0 ? kCostUnit + s.nkt * s.w : 0; }
+PKA_DEVICE int unit_cost(const Seg& s) { return s.nkt > 0 ? s.e + s.nkt * s.w : 0; }
 // The first key tile of a unit that starts at `us` whose place is at or past x
-// (tile t's place: us + kCostUnit + t w).
+// (tile t's place: us + e + t w).
 PKA_DEVICE int first_tile(int x, int us, const Seg& s) {
-    const int d = x - us - kCostUnit;
+    const int d = x - us - s.e;
     return d <= 0 ? 0 : min(s.nkt, (d + s.w - 1) / s.w);
 }
 
@@ -308,16 +311,16 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     uint32_t uo0 = 0, uo1 = 0;  // units in which each lane had key tiles
 
     // Pass 0 sums the runs of segments; pass j > 0 lists the pieces that begin in the
-    // j-th stretch of the share (a piece costs kCostUnit + kCostOne at least but for
+    // j-th stretch of the share (a piece costs cost_unit + kCostOne at least but for
     // the first, so a list holds a stretch's) and works them off. One loop body for
     // both: what runs once per launch is bound by the fetch of its instructions.
-    constexpr int kStretch = (kPieces - 2) * (kCostUnit + kCostOne);
+    const int stretch = (kPieces - 2) * (p.cost_unit + kCostOne);
     for (int pass = 0;; ++pass) {
         if (pass > 1) load_meta();  // (tiles were there meanwhile)
-        const int from = lo + (pass - 1) * kStretch;
+        const int from = lo + (pass - 1) * stretch;
 #pragma unroll 1
         for (int run = warp; run < runs; run += kPxThreads / 32) {
-            if (pass > 0 && (run_cost[run] >= min(hi, from + kStretch) || run_cost[run + 1] <= from) &&
+            if (pass > 0 && (run_cost[run] >= min(hi, from + stretch) || run_cost[run + 1] <= from) &&
                 (pass > 1 || run % ncta != cta))
                 continue;
             const int s = run * 32 + lane;
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             for (int u = cs >= lo ? 0 : (lo - cs) / each; u < units && cs + u * each < hi; ++u) {
                 const int at = cs + u * each, begin = max(at, lo);
                 const int t0 = first_tile(lo, at, g), t1 = first_tile(hi, at, g);
-                if (t0 >= t1 || begin < from || begin >= from + kStretch) continue;
+                if (t0 >= t1 || begin < from || begin >= from + stretch) continue;
                 Piece x;
                 x.h = g.nrt == 1 ? u : u / g.nrt;
                 const int rt = u - x.h * g.nrt;
@@ -1053,7 +1056,7 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParam
     __shared__ float s_inv[16];
     Source* src = reinterpret_cast<Source*>(s_join);                    // [4 * ncta]
     float* weight = reinterpret_cast<float*>(src + 4 * (size_t)ncta);  // [4 * ncta][G]
-    grid_dep_launch();
+    // (no early launch of what follows: its CTAs, waiting, could take the SMs of those still to come)
     const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
     // ---- the token's segments, from the lengths (in place since before the attention started)
     const TokenPlace at = place_of(p.qsl, p.seq_lens, p.B, t);
@@ -1103,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParam
             const int unit = (part == 0 ? unit_at[0] : unit_at[1]) + local;
             const int half = part == 0 ? p.rows_pre : p.rows_own;
             const int row = two && tok >= p.tpt ? half + (tok - p.tpt) * G : tok * G;
-            const int first = shares.cta_of(us + kCostUnit), last = shares.cta_of(us + kCostUnit + (s.nkt - 1) * s.w);
+            const int first = shares.cta_of(us + s.e), last = shares.cta_of(us + s.e + (s.nkt - 1) * s.w);
             const int lanes = two ? 1 : 2, end = s.c1 - s.n + min(s.n, (rt + 1) * p.upt);  // (of own keys)
             const float* o = part == 0 ? p.po_pre : p.po_own;
             const float* l = part == 0 ? p.pl_pre : p.pl_own;
