@@ -49,7 +49,7 @@ cudaError_t launch_page_bounds(PageBoundsParams p, bool fp8, int num_sms, cudaSt
 cudaError_t launch_page_select(const PageSelectParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, bool fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_beam_select(const BeamSelectParams& p, bool bf16, int num_sms, cudaStream_t stream);
-cudaError_t launch_fork_pages(const ForkPagesParams& p, cudaStream_t stream);
+cudaError_t launch_fork_pages(const ForkPagesParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t stream);
 cudaError_t launch_prefix_attn(const PrefixMaps& maps, const PrefixParams& p, int head_dim, bool fp8, int ncta,
                                cudaStream_t stream);
@@ -1598,6 +1598,8 @@ pka_status pka_fork_pages(const int32_t* parents, int num_rows_out, const int32_
                              static_cast<const int32_t*>(block_table_out), static_cast<const int32_t*>(copy_src),
                              static_cast<const int32_t*>(copy_dst), static_cast<const int32_t*>(error_word)})
         if (!aligned(x, 4)) return PKA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PKA_ERR_CUDA;
     ForkPagesParams p;
     p.parents = parents;
     p.ctx_lens = ctx_lens;
@@ -1618,7 +1620,7 @@ pka_status pka_fork_pages(const int32_t* parents, int num_rows_out, const int32_
     p.num_blocks = (int)num_blocks;
     p.num_free = num_free_pages;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_status(timed(PKA_KERNEL_FORK_PAGES, st, [&] { return launch_fork_pages(p, st); }));
+    return cuda_status(timed(PKA_KERNEL_FORK_PAGES, st, [&] { return launch_fork_pages(p, sms, st); }));
 }
 
 pka_status pka_copy_pages(void* const* caches, int num_caches, int64_t num_blocks, int64_t page_bytes,

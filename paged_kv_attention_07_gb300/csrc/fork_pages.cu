@@ -9,9 +9,11 @@
 // page. The order of the freed pages must not hang on that of the atomics: each
 // entry of such a row that finds its page's count below 0 enters its place into
 // the count (the least place stays), after which the page's first entry knows
-// that it is the first, and the freed pages are numbered by counts per row and a
-// prefix sum. Three barriers separate these steps, so the work is one cluster's;
-// what bounds it is their latency and the table's bytes.
+// that it is the first, and the freed pages are numbered by counts per stretch of
+// a row and a prefix sum. Three barriers separate these steps, so they are one
+// cluster's work (one CTA's for a small table); the copies of the rows need no
+// barrier and go to further clusters. What bounds it is the latency of the steps:
+// a warp takes 256 columns at a time, all loads of them in flight.
 //
 // copy_pages_kernel: bytes.
 #include <algorithm>
@@ -24,10 +26,14 @@ namespace pka {
 
 namespace {
 
-constexpr int kFpThreads = 1024, kFpWarps = kFpThreads / 32;
-constexpr int kFpCluster = 8;
+constexpr int kFpFew = 256, kFpMany = 1024;  // threads of a CTA
+constexpr int kFpCluster = 16;
+constexpr int kFpSpan = 8;                   // columns of a lane in flight
+constexpr int kFpStep = 32 * kFpSpan;
+constexpr int kFpTasks = 8192;               // stretches of ending rows that are counted apart
 
-// Exclusive prefix sum of v over the CTA's threads; *total its sum. `s`: kFpWarps + 1 words.
+// Exclusive prefix sum of v over the CTA's threads; *total its sum. `s`: 33 words.
+template <int kThreads>
 PKA_DEVICE int block_scan(int v, int* s, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -39,7 +45,7 @@ PKA_DEVICE int block_scan(int v, int* s, int* total) {
     if (lane == 31) s[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        const int w = s[lane];
+        const int w = lane < kThreads / 32 ? s[lane] : 0;
         int y = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -47,44 +53,71 @@ PKA_DEVICE int block_scan(int v, int* s, int* total) {
             if (lane >= o) y += z;
         }
         s[lane] = y - w;
-        if (lane == 31) s[kFpWarps] = y;
+        if (lane == 31) s[32] = y;
     }
     __syncthreads();
     const int before = s[warp] + x - v;
-    *total = s[kFpWarps];
+    *total = s[32];
     __syncthreads();
     return before;
 }
 
-__global__ void __launch_bounds__(kFpThreads) fork_pages_kernel(const ForkPagesParams p) {
+// The pages of columns [c0, c0 + kFpStep) of a row before `end`, those that are pages; -1 for the others.
+PKA_DEVICE void load_span(int (&page)[kFpSpan], const int32_t* row, int c0, int end, int num_blocks) {
+#pragma unroll
+    for (int j = 0; j < kFpSpan; ++j) {
+        const int c = c0 + 32 * j + (int)(threadIdx.x & 31);
+        page[j] = c < end ? __ldg(row + c) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kFpSpan; ++j)
+        if (page[j] >= num_blocks) page[j] = -1;
+}
+
+PKA_DEVICE void load_counts(int (&count)[kFpSpan], const int (&page)[kFpSpan], const int32_t* counts) {
+#pragma unroll
+    for (int j = 0; j < kFpSpan; ++j) count[j] = page[j] >= 0 ? __ldcg(counts + page[j]) : 0;
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkPagesParams p) {
+    constexpr int kWarps = kThreads / 32;
     extern __shared__ int32_t s_rows[];
-    int32_t* s_children = s_rows;              // [num_rows] rows that go on from each
+    int32_t* s_children = s_rows;                // [num_rows] rows that go on from each
     int32_t* s_first = s_children + p.num_rows;  // [num_rows] the first of them
     int32_t* s_held = s_first + p.num_rows;      // [num_rows] its pages; bit 31: the last one is partly filled
-    int32_t* s_freed = s_held + p.num_rows;      // [num_rows] pages that it is the first to free
-    int32_t* s_fresh = s_freed + p.num_rows;     // [num_rows_out] the taken page's number, or -1
-    __shared__ int s_scan[kFpWarps + 1];
-    static_assert(kFpWarps == 32, "");
-    grid_dep_launch();
-    grid_dep_wait();
+    int32_t* s_dead = s_held + p.num_rows;       // [num_rows] the rows that end
+    int32_t* s_fresh = s_dead + p.num_rows;      // [num_rows_out] the taken page's number, or -1
+    int32_t* s_freed = s_fresh + p.num_rows_out;  // [kFpTasks] pages that a stretch is the first to free
+    __shared__ int s_scan[33];
+    __shared__ int s_most;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ncta = (int)cluster_size(), cta = (int)cluster_rank();
+    const bool copies_only = blockIdx.x >= ncta;  // not of the first cluster
     const int B = p.num_rows, N = p.num_rows_out, bs = p.block_size;
-    const int head = *p.free_head;
+    if (tid == 0) s_most = 0;
+    for (int k = tid; k < kFpTasks; k += kThreads) s_freed[k] = 0;
+    grid_dep_launch();
+    grid_dep_wait();
+    const int head = copies_only ? 0 : *p.free_head;
     int err = 0;
 
     // ---- lengths and parents
-    for (int r = tid; r < B; r += kFpThreads) {
+    int most = 0;
+    for (int r = tid; r < B; r += kThreads) {
         const int c = p.ctx_lens[r];
         if (c < 0) err |= PKA_DEVERR_SEQ_LEN;
         if (c > (long long)p.max_blocks * bs) err |= PKA_DEVERR_BLOCK_TABLE;
         s_children[r] = 0;
         s_first[r] = INT32_MAX;
-        s_freed[r] = 0;
-        s_held[r] = err ? 0 : (c / bs + (c % bs != 0)) | (c % bs != 0 ? 1 << 31 : 0);
+        const int held = err ? 0 : c / bs + (c % bs != 0);
+        s_held[r] = held | (!err && c % bs != 0 ? 1 << 31 : 0);
+        most = max(most, held);
     }
     __syncthreads();
-    for (int i = tid; i < N; i += kFpThreads) {
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) atomicMax(&s_most, most);
+    for (int i = tid; i < N; i += kThreads) {
         const int r = p.parents[i];
         if (r >= B) err |= PKA_DEVERR_INDEX;
         if (r < 0 || r >= B) continue;
@@ -92,21 +125,33 @@ __global__ void __launch_bounds__(kFpThreads) fork_pages_kernel(const ForkPagesP
         atomicMin(&s_first[r], i);
     }
     __syncthreads();
-    int taken = 0;  // rows that take a page, numbered in order
-    for (int i0 = 0; i0 < N; i0 += kFpThreads) {
+    most = s_most;
+    int taken = 0, ending = 0;  // rows that take a page and rows that end, numbered in order
+    for (int i0 = 0; i0 < N; i0 += kThreads) {
         const int i = i0 + tid, r = i < N ? p.parents[i] : -1;
         const bool fresh = r >= 0 && r < B && s_held[r] < 0 && s_first[r] != i;
         int sum;
-        const int before = block_scan(fresh, s_scan, &sum);
+        const int before = block_scan<kThreads>(fresh, s_scan, &sum);
         if (i < N) s_fresh[i] = fresh ? taken + before : -1;
         taken += sum;
     }
-    if (head < 0 || taken > (long long)p.num_free - head) err |= PKA_DEVERR_CAPACITY;
+    if (!copies_only) {
+        for (int r0 = 0; r0 < B; r0 += kThreads) {
+            const int r = r0 + tid;
+            const bool ends = r < B && s_children[r] == 0 && s_held[r] != 0;
+            int sum;
+            const int before = block_scan<kThreads>(ends, s_scan, &sum);
+            if (ends) s_dead[ending + before] = r;
+            ending += sum;
+        }
+        if (head < 0 || taken > (long long)p.num_free - head) err |= PKA_DEVERR_CAPACITY;
+    }
     const int any = __syncthreads_or(err);
     if (any) {
+        if (copies_only) return;
         if (cta == 0) {
             if (err) set_error(p.err, err);
-            for (int i = tid; i < N; i += kFpThreads) {
+            for (int i = tid; i < N; i += kThreads) {
                 p.ctx_lens_out[i] = 0;
                 p.copy_src[i] = p.copy_dst[i] = -1;
             }
@@ -116,90 +161,134 @@ __global__ void __launch_bounds__(kFpThreads) fork_pages_kernel(const ForkPagesP
         return;
     }
 
-    // ---- the new rows
-    const int me = cta * kFpWarps + warp, nwarps = ncta * kFpWarps;
-    for (int i = me; i < N; i += nwarps) {
-        const int r = p.parents[i];
-        const int held = r < 0 ? 0 : s_held[r] & INT32_MAX, fresh = s_fresh[i];
-        const int32_t* from = p.block_table + (int64_t)max(r, 0) * p.max_blocks;
-        int32_t* to = p.block_table_out + (int64_t)i * p.max_blocks;
-        const int same = fresh >= 0 ? held - 1 : held;
-        for (int c = lane; c < same; c += 32) to[c] = from[c];
-        if (lane == 0) {
-            const int page = fresh >= 0 ? p.free_pages[head + fresh] : -1;
-            if (fresh >= 0) to[held - 1] = page;
-            p.ctx_lens_out[i] = r < 0 ? 0 : p.ctx_lens[r];
-            p.copy_src[i] = fresh >= 0 ? from[held - 1] : -1;
-            p.copy_dst[i] = page;
+    // ---- the new rows, by the further clusters where there are any; taken pages by the first
+    const int chunks = (most + kFpStep - 1) / kFpStep;
+    const bool alone = gridDim.x == ncta;
+    if (copies_only || alone) {
+        const int ctas = alone ? ncta : gridDim.x - ncta, c = alone ? cta : blockIdx.x - ncta;
+        for (int task = c * kWarps + warp; task < N * chunks; task += ctas * kWarps) {
+            const int i = task / chunks, r = p.parents[i], c0 = (task - i * chunks) * kFpStep;
+            const int end = r < 0 ? 0 : (s_held[r] & INT32_MAX) - (s_fresh[i] >= 0);
+            if (c0 >= end) continue;
+            const int32_t* from = p.block_table + (int64_t)r * p.max_blocks;
+            int32_t* to = p.block_table_out + (int64_t)i * p.max_blocks;
+            int page[kFpSpan];
+#pragma unroll
+            for (int j = 0; j < kFpSpan; ++j) page[j] = c0 + 32 * j + lane < end ? __ldg(from + c0 + 32 * j + lane) : 0;
+#pragma unroll
+            for (int j = 0; j < kFpSpan; ++j)
+                if (c0 + 32 * j + lane < end) to[c0 + 32 * j + lane] = page[j];
         }
+        if (copies_only) return;
+    }
+    for (int i = cta * kThreads + tid; i < N; i += ncta * kThreads) {
+        const int r = p.parents[i], fresh = s_fresh[i];
+        int src = -1, dst = -1;
+        if (fresh >= 0) {
+            const int last = (s_held[r] & INT32_MAX) - 1;
+            src = p.block_table[(int64_t)r * p.max_blocks + last];
+            dst = p.free_pages[head + fresh];
+            p.block_table_out[(int64_t)i * p.max_blocks + last] = dst;
+        }
+        p.ctx_lens_out[i] = r < 0 ? 0 : p.ctx_lens[r];
+        p.copy_src[i] = src;
+        p.copy_dst[i] = dst;
     }
     // ---- the counts
-    for (int r = me; r < B; r += nwarps) {
-        const int n = s_children[r], held = s_held[r] & INT32_MAX;
-        const bool partial = s_held[r] < 0;
-        if (n == 1) continue;
+    const int me = cta * kWarps + warp, nwarps = ncta * kWarps;
+    for (int task = me; task < B * chunks; task += nwarps) {
+        const int r = task / chunks, c0 = (task - r * chunks) * kFpStep, n = s_children[r], end = s_held[r] & INT32_MAX;
+        if (n == 1 || c0 >= end) continue;
         const int32_t* row = p.block_table + (int64_t)r * p.max_blocks;
-        for (int c = lane; c < held; c += 32) {
-            const int page = row[c];
-            const int more = partial && c == held - 1 ? min(n, 1) - 1 : n - 1;
-            if (page >= p.num_blocks) set_error(p.err, PKA_DEVERR_BLOCK_ID);
-            else if (page >= 0 && more != 0) atomicAdd(&p.share_counts[page], more);
+        const int last = s_held[r] < 0 ? end - 1 : -1;  // the column of a partly filled page
+        int page[kFpSpan];
+#pragma unroll
+        for (int j = 0; j < kFpSpan; ++j) page[j] = c0 + 32 * j + lane < end ? __ldg(row + c0 + 32 * j + lane) : -1;
+#pragma unroll
+        for (int j = 0; j < kFpSpan; ++j) {
+            const int more = c0 + 32 * j + lane == last ? min(n, 1) - 1 : n - 1;
+            if (page[j] >= p.num_blocks) set_error(p.err, PKA_DEVERR_BLOCK_ID);
+            else if (page[j] >= 0 && more != 0) atomicAdd(&p.share_counts[page[j]], more);
         }
     }
-    cluster_barrier();
-    // ---- the first place of each page that nobody holds
-    for (int r = me; r < B; r += nwarps) {
-        if (s_children[r] != 0) continue;
-        const int held = s_held[r] & INT32_MAX;
-        const int32_t* row = p.block_table + (int64_t)r * p.max_blocks;
-        for (int c = lane; c < held; c += 32) {
-            const int page = row[c];
-            if (page >= 0 && page < p.num_blocks && __ldcg(&p.share_counts[page]) < 0)
-                atomicMin(&p.share_counts[page], INT32_MIN + r * p.max_blocks + c);
-        }
+    if (ending == 0) {
+        cluster_barrier();  // (the list's head has been read)
+        if (cta == 0 && tid == 0) *p.free_head_out = head + taken;
+        return;
     }
     cluster_barrier();
-    for (int r = me; r < B; r += nwarps) {
-        if (s_children[r] != 0) continue;
-        const int held = s_held[r] & INT32_MAX;
-        const int32_t* row = p.block_table + (int64_t)r * p.max_blocks;
+    // ---- ending rows in stretches of `span` columns
+    const int parts = min(max(1, kFpTasks / ending), chunks), span = (chunks + parts - 1) / parts * kFpStep;
+    const int tasks = ending * parts;
+    // the first place of each page that nobody holds
+    for (int task = me; task < tasks; task += nwarps) {
+        const int d = task / parts, r = s_dead[d], end = s_held[r] & INT32_MAX;
+        const int from = (task - d * parts) * span;
+        bool some = false;
+        for (int c0 = from; c0 < min(end, from + span); c0 += kFpStep) {
+            int page[kFpSpan], count[kFpSpan];
+            load_span(page, p.block_table + (int64_t)r * p.max_blocks, c0, end, p.num_blocks);
+            load_counts(count, page, p.share_counts);
+#pragma unroll
+            for (int j = 0; j < kFpSpan; ++j) {
+                if (count[j] >= 0) continue;
+                atomicMin(&p.share_counts[page[j]], INT32_MIN + r * p.max_blocks + c0 + 32 * j + lane);
+                some = true;
+            }
+        }
+        // (the same warp counts the stretch below, where there is something to count)
+        if (__any_sync(0xffffffffu, some) && lane == 0) s_freed[task] = 1;
+    }
+    cluster_barrier();
+    for (int task = me; task < tasks; task += nwarps) {
+        if (s_freed[task] == 0) continue;
+        const int d = task / parts, r = s_dead[d], end = s_held[r] & INT32_MAX;
+        const int from = (task - d * parts) * span;
         int freed = 0;
-        for (int c0 = 0; c0 < held; c0 += 32) {
-            const int c = c0 + lane, page = c < held ? row[c] : -1;
-            const bool mine = page >= 0 && page < p.num_blocks &&
-                              __ldcg(&p.share_counts[page]) == INT32_MIN + r * p.max_blocks + c;
-            freed += __popc(__ballot_sync(0xffffffffu, mine));
+        for (int c0 = from; c0 < min(end, from + span); c0 += kFpStep) {
+            int page[kFpSpan], count[kFpSpan];
+            load_span(page, p.block_table + (int64_t)r * p.max_blocks, c0, end, p.num_blocks);
+            load_counts(count, page, p.share_counts);
+#pragma unroll
+            for (int j = 0; j < kFpSpan; ++j)
+                freed += count[j] == INT32_MIN + r * p.max_blocks + c0 + 32 * j + lane;
         }
-        if (lane < ncta) store_cluster(reinterpret_cast<uint32_t*>(&s_freed[r]), lane, (uint32_t)freed);
+        freed = __reduce_add_sync(0xffffffffu, freed);  // (every lane has read the flag)
+        if (lane < ncta) store_cluster(reinterpret_cast<uint32_t*>(&s_freed[task]), lane, (uint32_t)freed);
     }
     cluster_barrier();
     // ---- their places in the list
     int total = 0;
-    for (int r0 = 0; r0 < B; r0 += kFpThreads) {
-        const int r = r0 + tid;
+    for (int k0 = 0; k0 < tasks; k0 += kThreads) {
+        const int k = k0 + tid, n = k < tasks ? s_freed[k] : 0;
         int sum;
-        const int before = block_scan(r < B ? s_freed[r] : 0, s_scan, &sum);
-        if (r < B) s_first[r] = total + before;  // (the first rows are not asked for any more)
+        const int before = block_scan<kThreads>(n, s_scan, &sum);
+        if (k < tasks) s_freed[k] = n ? total + before : -1;
         total += sum;
     }
     __syncthreads();
-    const int end = head + taken, start = end - total;
-    for (int r = me; r < B; r += nwarps) {
-        if (s_freed[r] == 0) continue;
-        const int held = s_held[r] & INT32_MAX;
-        const int32_t* row = p.block_table + (int64_t)r * p.max_blocks;
-        int at = start + s_first[r];
-        for (int c0 = 0; c0 < held; c0 += 32) {
-            const int c = c0 + lane, page = c < held ? row[c] : -1;
-            const bool mine = page >= 0 && page < p.num_blocks &&
-                              __ldcg(&p.share_counts[page]) == INT32_MIN + r * p.max_blocks + c;
-            const uint32_t all = __ballot_sync(0xffffffffu, mine);
-            if (mine) {
-                const int to = at + __popc(all & ((1u << lane) - 1));
-                if (to >= 0) p.free_pages[to] = page;
-                p.share_counts[page] = 0;
+    const int start = head + taken - total;
+    for (int task = me; task < tasks; task += nwarps) {
+        int at = s_freed[task];
+        if (at < 0) continue;
+        at += start;
+        const int d = task / parts, r = s_dead[d], end = s_held[r] & INT32_MAX;
+        const int from = (task - d * parts) * span;
+        for (int c0 = from; c0 < min(end, from + span); c0 += kFpStep) {
+            int page[kFpSpan], count[kFpSpan];
+            load_span(page, p.block_table + (int64_t)r * p.max_blocks, c0, end, p.num_blocks);
+            load_counts(count, page, p.share_counts);
+#pragma unroll
+            for (int j = 0; j < kFpSpan; ++j) {
+                const bool mine = count[j] == INT32_MIN + r * p.max_blocks + c0 + 32 * j + lane;
+                const uint32_t all = __ballot_sync(0xffffffffu, mine);
+                if (mine) {
+                    const int to = at + __popc(all & ((1u << lane) - 1));
+                    if (to >= 0) p.free_pages[to] = page[j];
+                    p.share_counts[page[j]] = 0;
+                }
+                at += __popc(all);
             }
-            at += __popc(all);
         }
     }
     if (cta == 0 && tid == 0) {
@@ -245,16 +334,28 @@ __global__ void __launch_bounds__(kCpThreads) copy_pages_kernel(const __grid_con
 
 }  // namespace
 
-cudaError_t launch_fork_pages(const ForkPagesParams& p, cudaStream_t stream) {
-    const size_t smem = sizeof(int32_t) * (4 * (size_t)p.num_rows + p.num_rows_out);
+template <int kThreads>
+static cudaError_t go(const ForkPagesParams& p, int cluster, int clusters, cudaStream_t stream) {
+    auto kern = fork_pages_kernel<kThreads>;
+    const size_t smem = sizeof(int32_t) * (4 * (size_t)p.num_rows + p.num_rows_out + kFpTasks);
     if (smem > 47 * 1024) {  // past what every kernel may use; the most that any call takes
-        const cudaError_t e = cudaFuncSetAttribute(fork_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)sizeof(int32_t) * 5 * kMaxRequests);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)sizeof(int32_t) * (5 * kMaxRequests + kFpTasks));
         if (e != cudaSuccess) return e;
     }
-    const int rows = std::max(p.num_rows, p.num_rows_out);
-    const int n = rows <= kFpWarps ? 1 : kFpCluster;
-    return launch_cluster(fork_pages_kernel, dim3(n), dim3(kFpThreads), smem, n, stream, p);
+    if (cluster > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_cluster(kern, dim3(cluster * clusters), dim3(kThreads), smem, cluster, stream, p);
+}
+
+cudaError_t launch_fork_pages(const ForkPagesParams& p, int num_sms, cudaStream_t stream) {
+    // By what the table may hold: one small CTA, one cluster, or further ones for the copies.
+    const int64_t entries = (int64_t)std::max(p.num_rows, p.num_rows_out) * p.max_blocks;
+    if (entries <= 4096) return go<kFpFew>(p, 1, 1, stream);
+    const int64_t more = (int64_t)p.num_rows_out * p.max_blocks / (kFpCluster * kFpMany * kFpSpan);
+    return go<kFpMany>(p, kFpCluster, 1 + (int)std::min<int64_t>(more, num_sms / kFpCluster - 1), stream);
 }
 
 cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t stream) {
