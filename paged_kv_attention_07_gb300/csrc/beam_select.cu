@@ -9,17 +9,18 @@
 // cluster whose first CTA joins the parts' sums and lists through distributed
 // shared memory: no workspace, no second launch.
 //
-// A part goes in tiles of kTile elements held in registers. The first tile gives
-// a threshold that at least num_out of its elements reach (the num_out-th of the
-// threads' largest), elements above the threshold are collected in shared memory
-// and cut back to the best num_out now and then. A key is the logit's order in the
-// upper and the token's complement in the lower 32 bits: keys are distinct, the
-// larger one is the better, and the collected order does not matter. Where too
-// many elements reach the threshold at once (a tile of equal logits), the tile is
-// gone through one element per thread at a time.
+// A warp goes through its share of a part by itself: four 16-byte loads per lane at a
+// time with the next four on their way, the sum, and a look whether the lane's largest
+// passes the limit, a key that num_out keys of the part are known to reach. The first
+// limit is the num_out-th of the lanes' largest logits of a warp's first tile; keys past
+// the limit go to a buffer in shared memory, which is cut back to the best num_out when
+// it is full, and the limit rises to the last of them, for all the CTA's warps. A key is
+// the logit's order in the upper and the token's complement in the lower 32 bits: keys
+// are distinct, the larger one is the better, and the order of their arrival does not
+// matter, nor which warp sees a raised limit when.
 //
-// The sum runs over x - m, m the thread's largest so far, which no scale of the
-// logits overflows; threads, warps and slices are joined in a fixed order that
+// The sum runs over x - m, m the lane's largest so far, which no scale of the
+// logits overflows; lanes, warps and slices are joined in a fixed order that
 // depends on nothing but the element's index, so that equal rows have equal sums.
 // Candidates of different rows are compared by their 64-bit scores.
 #include <algorithm>
@@ -32,10 +33,8 @@ namespace pka {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPer = 32;  // elements of a thread per tile
-constexpr int kTile = kThreads * kPer;
-constexpr int kCap = 1024;    // collected keys
-constexpr int kCutAt = 128;   // keys that are cut back at a tile's end
+constexpr int kLoads = 4;     // 16-byte loads of a lane in flight
+constexpr int kBuffer = 128;  // keys that a warp collects
 constexpr int kMaxEntries = 4096;  // of all parts' lists of a group
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kMinusInf = 0x007fffffu;  // order_of(-infinity)
@@ -72,79 +71,105 @@ PKA_DEVICE float element(const void* row, int64_t i) {
     else return static_cast<const float*>(row)[i];
 }
 
-// Element e of a thread's kPer of a tile: with 16-byte loads runs of 8 (4)
-// elements, else neighbours in neighbouring threads.
+// A warp's tile: kPer elements per lane. With 16-byte loads a lane has runs of kRun
+// elements, else neighbours lie in neighbouring lanes.
 template <bool kBf16, bool kVec>
-PKA_DEVICE int place_of(int e) {
-    constexpr int kRun = !kVec ? 1 : kBf16 ? 8 : 4;
-    return (e / kRun * kThreads + (int)threadIdx.x) * kRun + e % kRun;
-}
-
-// A tile's elements of this thread; -infinity from element n of the tile on.
-template <bool kBf16, bool kVec>
-PKA_DEVICE void load_tile(float (&x)[kPer], const void* row, int64_t at, int n) {
-    if constexpr (kVec) {
-        constexpr int kRun = kBf16 ? 8 : 4;
-        uint4 raw[kPer / kRun];
+struct Tile {
+    static constexpr int kRun = kBf16 ? 8 : 4, kPer = kLoads * kRun, kSize = 32 * kPer;
+    uint32_t w[kLoads * 4];  // two bf16 or one float each
+    PKA_DEVICE static int place(int e) {
+        const int lane = threadIdx.x & 31;
+        return kVec ? (e / kRun * 32 + lane) * kRun + e % kRun : e * 32 + lane;
+    }
+    PKA_DEVICE float operator[](int e) const {
+        if constexpr (!kBf16) return __uint_as_float(w[e]);
+        else return e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    }
+    // Elements from `at` of the row on; -infinity from element n of the tile on.
+    PKA_DEVICE void load(const void* row, int at, int n) {
+        const uint32_t none = kBf16 ? 0xff80ff80u : 0xff800000u;
+        if (kVec && n >= kSize) {
 #pragma unroll
-        for (int j = 0; j < kPer / kRun; ++j) {
-            const int i = place_of<kBf16, kVec>(j * kRun);
-            if (i + kRun <= n) raw[j] = __ldcs(reinterpret_cast<const uint4*>(row) + (at + i) / kRun);
-        }
-#pragma unroll
-        for (int j = 0; j < kPer / kRun; ++j) {
-            const int i = place_of<kBf16, kVec>(j * kRun);
-            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-            if (i + kRun <= n) {
-#pragma unroll
-                for (int e = 0; e < kRun; ++e)
-                    x[j * kRun + e] = !kBf16 ? __uint_as_float(w[e % 4]) : e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kRun; ++e) x[j * kRun + e] = i + e < n ? element<kBf16>(row, at + i + e) : -INFINITY;
+            for (int j = 0; j < kLoads; ++j) {
+                const uint4 x = __ldcs(reinterpret_cast<const uint4*>(row) + (at + place(j * kRun)) / kRun);
+                w[4 * j] = x.x;
+                w[4 * j + 1] = x.y;
+                w[4 * j + 2] = x.z;
+                w[4 * j + 3] = x.w;
             }
+            return;
         }
-    } else {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int i = place_of<kBf16, kVec>(e);
-            x[e] = i < n ? element<kBf16>(row, at + i) : -INFINITY;
+        for (int e = 0; e < kPer; e += kBf16 ? 2 : 1) {
+            uint32_t x = none;
+            const int i = place(e);
+            if constexpr (!kBf16) {
+                if (i < n) x = __float_as_uint(static_cast<const float*>(row)[at + i]);
+            } else {
+                const uint16_t* r = static_cast<const uint16_t*>(row) + at;
+                const int k = place(e + 1);
+                if (i < n) x = (x & 0xffff0000u) | r[i];
+                if (k < n) x = (x & 0xffffu) | ((uint32_t)r[k] << 16);
+            }
+            w[kBf16 ? e / 2 : e] = x;
         }
     }
-}
-
-struct Shared {
-    u64 keys[kCap];
-    uint32_t tops[kThreads];
-    float m[kWarps], s[kWarps];
-    u64 limit;
-    int count;
 };
 
-// Cuts the collected keys back to the best `keep`, sorted, and raises the limit
-// to the last of them. All threads.
-PKA_DEVICE void cut(Shared& sh, int keep) {
-    const int n = sh.count;
-    u64 mine[kCap / kThreads];
-    int rank[kCap / kThreads];
+struct Shared {
+    u64 keys[kWarps][kBuffer];
+    float m[kWarps], s[kWarps];
+    u64 limit;
+    int count[kWarps];
+};
+
+// Cuts the warp's n collected keys back to the best `keep`, sorted, and raises the
+// limit to the last of them. Returns how many are left.
+PKA_DEVICE int cut(u64* keys, int n, int keep, u64* limit) {
+    const int lane = threadIdx.x & 31;
+    u64 mine[kBuffer / 32];
+    int rank[kBuffer / 32];
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < kCap / kThreads; ++j) {
-        const int i = (int)threadIdx.x + j * kThreads;
-        rank[j] = keep;
-        if (i >= n) continue;
-        mine[j] = sh.keys[i];
+    for (int j = 0; j < kBuffer / 32; ++j) {
+        mine[j] = lane + 32 * j < n ? keys[lane + 32 * j] : 0;
         rank[j] = 0;
-        for (int o = 0; o < n; ++o) rank[j] += sh.keys[o] > mine[j];
     }
-    __syncthreads();
+    for (int o = n; o < (n + 3) / 4 * 4; ++o)
+        if (lane == 0) keys[o] = 0;
+    __syncwarp();
+#pragma unroll 1
+    for (int o = 0; o < n; o += 4) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(keys + o), b = *reinterpret_cast<const ulonglong2*>(keys + o + 2);
 #pragma unroll
-    for (int j = 0; j < kCap / kThreads; ++j) {
-        if (rank[j] >= keep) continue;
-        sh.keys[rank[j]] = mine[j];
-        if (rank[j] == keep - 1) sh.limit = mine[j];
+        for (int j = 0; j < kBuffer / 32; ++j)
+            rank[j] += (a.x > mine[j]) + (a.y > mine[j]) + (b.x > mine[j]) + (b.y > mine[j]);
     }
-    if (threadIdx.x == 0) sh.count = min(n, keep);
-    __syncthreads();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kBuffer / 32; ++j) {
+        if (mine[j] == 0 || rank[j] >= keep) continue;
+        keys[rank[j]] = mine[j];
+        if (rank[j] == keep - 1) atomicMax(limit, mine[j]);
+    }
+    __syncwarp();
+    return min(n, keep);
+}
+
+// log(s) of a normal s > 0 to about 2^-33: e ln 2 + log m with m in [3/4, 3/2) and log m =
+// 2 artanh z = 2 z + z^3 (2/3 + 2/5 z^2 + ...), z = (m - 1) / (m + 1) to twice 24 bits (the
+// 64-bit logarithm takes a microsecond, much of it the fetch of its code).
+PKA_DEVICE double log_of(float s) {
+    int e = (int)(__float_as_uint(s) >> 23) - 127;
+    float m = __uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u);
+    if (m >= 1.5f) {
+        m *= 0.5f;
+        ++e;
+    }
+    const float n = m - 1.f, d = m + 1.f, d_low = (1.f - d) + m;  // (n is exact, d + d_low too)
+    const float z = __fdiv_rn(n, d), z_low = __fdiv_rn(fmaf(-z, d, n) - z * d_low, d), q = z * z;
+    const float tail = z * q * (0.666666667f + q * (0.4f + q * (0.285714286f + q * (0.222222222f + q * 0.181818182f))));
+    return (double)e * 0.69314718055994531 + 2.0 * ((double)z + (double)z_low) + (double)tail;
 }
 
 // What a CTA leaves of a part: the largest logit, the sum of exp(x - largest) and
@@ -152,118 +177,148 @@ PKA_DEVICE void cut(Shared& sh, int keep) {
 struct Part {
     float m, s;
 };
+static_assert(sizeof(Part) == sizeof(u64), "");
 
 template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectParams p) {
+__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSelectParams p) {
+    using T = Tile<kBf16, kVec>;
     extern __shared__ __align__(16) uint8_t s_dyn[];
-    __shared__ Shared sh;
+    __shared__ __align__(16) Shared sh;
     __shared__ double s_lse[kMaxBeams];
+    __shared__ float s_score[kMaxBeams];
     __shared__ int s_state[kMaxBeams];
+    __shared__ int s_found;
     grid_dep_launch();
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ncta = (int)cluster_size(), rank = (int)cluster_rank(), group = blockIdx.x / ncta;
     const int keep = p.keep, parts = p.beams * p.slices;
     const int per = (parts + ncta - 1) / ncta;
-    u64* lists = reinterpret_cast<u64*>(s_dyn);                      // [per][keep]
+    u64* lists = reinterpret_cast<u64*>(s_dyn);                      // [per][keep], each sorted, then 0
     Part* part = reinterpret_cast<Part*>(lists + (size_t)per * keep);  // [per]
+    for (int b = tid; b < p.beams; b += kThreads) {
+        const int64_t row = (int64_t)group * p.beams + b;
+        s_score[b] = p.scores[row];
+        s_state[b] = p.finished && p.finished[row] != 0;
+    }
+    if (tid == 0) s_found = 0;
+    __syncthreads();
 
     for (int i = rank, li = 0; i < parts; i += ncta, ++li) {
-        const int beam = i / p.slices, slice = i % p.slices;
-        const int64_t row = (int64_t)group * p.beams + beam;
-        const float score = p.scores[row];
-        const bool done = p.finished && p.finished[row] != 0;
+        const int beam = i / p.slices, slice = i - beam * p.slices;
         const int from = slice * p.slice_len;
-        const int n = done || !(fabsf(score) < INFINITY) ? 0 : min(p.slice_len, p.vocab - from);
-        const void* logits = kBf16 ? (const void*)(static_cast<const __nv_bfloat16*>(p.logits) + row * p.row_stride)
-                                   : (const void*)(static_cast<const float*>(p.logits) + row * p.row_stride);
-        if (tid == 0) {
-            sh.limit = kNone;
-            sh.count = 0;
-        }
+        const int n = s_state[beam] || !(fabsf(s_score[beam]) < INFINITY) ? 0 : min(p.slice_len, p.vocab - from);
+        const int64_t at = ((int64_t)group * p.beams + beam) * p.row_stride + from;
+        const void* logits = static_cast<const uint8_t*>(p.logits) + at * (kBf16 ? 2 : 4);
+        if (tid == 0) sh.limit = kNone;
+        __syncthreads();
+        u64* keys = sh.keys[warp];
         float m = -INFINITY, s = 0.f;
-        for (int t = 0; t < n; t += kTile) {
-            float x[kPer];
-            load_tile<kBf16, kVec>(x, logits, from + t, n - t);
-            float top = -INFINITY;
+        int have = 0;
+        T x, next;
+        int t = warp * T::kSize;
+        if (t < n) next.load(logits, t, n - t);
+        for (bool first = true; t < n; t += kThreads / 32 * T::kSize, first = false) {
+            x = next;
+            const int ahead = t + kThreads / 32 * T::kSize;
+            if (ahead < n) next.load(logits, ahead, n - ahead);
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) top = fmaxf(top, x[e]);
+            for (int e = 0; e < T::kPer; e += 2) tops[e / 2 % 4] = fmax3f(tops[e / 2 % 4], x[e], x[e + 1]);
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             if (top > m) {
                 s *= fast_exp2((m - top) * kLog2e);
                 m = top;
             }
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
             if (m > -INFINITY) {
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) sum[e % 4] += fast_exp2((x[e] - m) * kLog2e);
+                for (int e = 0; e < T::kPer; e += 2) {
+                    float d0, d1;
+                    fma2_bcast(d0, d1, x[e], x[e + 1], 1.f, -m);
+                    fma2_bcast(d0, d1, d0, d1, kLog2e, 0.f);
+                    add2(sum[e % 4], sum[e % 4 + 1], fast_exp2(d0), fast_exp2(d1));
+                }
+                s += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             } else {
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) sum[e % 4] += x[e] == x[e] ? 0.f : x[e];  // a NaN among -infinities
+                for (int e = 0; e < T::kPer; ++e) s += x[e] == x[e] ? 0.f : x[e];  // a NaN among -infinities
             }
-            s += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-
             // ---- candidates
             const uint32_t high = order_of(top);
-            if (t == 0) {
-                sh.tops[tid] = high;
-                __syncthreads();
-                int above = 0;
-#pragma unroll 8
-                for (int o = 0; o < kThreads; ++o) above += sh.tops[o] > high || (sh.tops[o] == high && o < tid);
-                if (above == keep - 1 && high > kMinusInf) sh.limit = ((u64)high << 32) - 1;
+            if (first && keep <= 32) {  // the keep-th of the lanes' largest
+                uint32_t left = high, kth = 0;
+                for (int k = 0; k < keep; ++k) {
+                    kth = __reduce_max_sync(0xffffffffu, left);
+                    const uint32_t who = __ballot_sync(0xffffffffu, left == kth);
+                    if (lane == __ffs(who) - 1) left = 0;
+                }
+                if (lane == 0 && kth > kMinusInf) atomicMax(&sh.limit, ((u64)kth << 32) - 1);
+                __syncwarp();
             }
-            __syncthreads();
-            const int had = sh.count;
-            const u64 limit = sh.limit;
-            __syncthreads();
-            if ((((u64)high << 32) | 0xffffffffu) > limit) {
+            u64 limit = *const_cast<volatile u64*>(&sh.limit);
+            const bool passes = (((u64)high << 32) | 0xffffffffu) > limit;
+            if (__any_sync(0xffffffffu, passes)) {
+                uint32_t hits = 0;  // of this lane's elements
+                if (passes) {
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    const u64 key = key_of(x[e], from + t + place_of<kBf16, kVec>(e));
-                    if (key <= limit) continue;
-                    const int at = atomicAdd(&sh.count, 1);
-                    if (at < kCap) sh.keys[at] = key;
+                    for (int e = 0; e < T::kPer; ++e)
+                        hits |= (uint32_t)(key_of(x[e], from + t + T::place(e)) > limit) << e;
+                }
+                while (__any_sync(0xffffffffu, hits != 0)) {
+                    if (have > kBuffer - 32) have = cut(keys, have, keep, &sh.limit);
+                    limit = *const_cast<volatile u64*>(&sh.limit);
+                    u64 key = 0;
+                    if (hits) {
+                        const int e = __ffs(hits) - 1, token = t + T::place(e);
+                        hits &= hits - 1;
+                        key = key_of(element<kBf16>(logits, token), from + token);
+                    }
+                    const uint32_t who = __ballot_sync(0xffffffffu, key > limit);
+                    if (key > limit) keys[have + __popc(who & ((1u << lane) - 1))] = key;
+                    have += __popc(who);
                 }
             }
-            __syncthreads();
-            if (sh.count > kCap) {
-                __syncthreads();
-                if (tid == 0) sh.count = had;
-                for (int e = 0; e < kPer; ++e) {
-                    __syncthreads();
-                    if (sh.count > kCap - kThreads) cut(sh, keep);
-                    const u64 now = sh.limit;
-                    const int at_row = t + place_of<kBf16, kVec>(e);
-                    const u64 key = at_row < n ? key_of(element<kBf16>(logits, from + at_row), from + at_row) : 0;
-                    __syncthreads();
-                    if (key > now) sh.keys[atomicAdd(&sh.count, 1)] = key;
-                }
-                __syncthreads();
-            }
-            if (sh.count > kCutAt) cut(sh, keep);
         }
-        __syncthreads();
-        if (n > 0) cut(sh, keep);
-        const int have = sh.count;
-        for (int k = tid; k < keep; k += kThreads) lists[(size_t)li * keep + k] = k < have ? sh.keys[k] : 0;
-        // ---- the part's sum, in a fixed order
+        // ---- the part's best keys: each warp's, then those of all warps
+        have = cut(keys, have, keep, &sh.limit);
+        if (lane == 0) sh.count[warp] = have;
+        // ... and its sum, in a fixed order
         float wm = m;
 #pragma unroll
         for (int o = 16; o; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-        if (lane == 0) sh.m[warp] = wm;
-        __syncthreads();
-        float all = sh.m[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) all = fmaxf(all, sh.m[w]);
-        float ws = m == all ? s : s * fast_exp2((m - all) * kLog2e);  // (of -infinities: 0, or NaN)
+        float ws = m == wm ? s : s * fast_exp2((m - wm) * kLog2e);  // (of -infinities: 0, or NaN)
 #pragma unroll
         for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-        if (lane == 0) sh.s[warp] = ws;
+        if (lane == 0) {
+            sh.m[warp] = wm;
+            sh.s[warp] = ws;
+        }
         __syncthreads();
+        for (int k = lane; k < have; k += 32) {
+            const u64 mine = keys[k];
+            int above = k;
+            for (int w = 1; w < kWarps && above < keep; ++w) {  // (each list is sorted: what is above is in front)
+                const u64* other = sh.keys[(warp + w) % kWarps];
+                int lo = 0, hi = sh.count[(warp + w) % kWarps];
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (other[mid] > mine) lo = mid + 1;
+                    else hi = mid;
+                }
+                above += lo;
+            }
+            if (above < keep) lists[(size_t)li * keep + above] = mine;
+        }
+        if (tid < keep) {
+            int total = 0;
+            for (int w = 0; w < kWarps; ++w) total += sh.count[w];
+            if (tid >= total) lists[(size_t)li * keep + tid] = 0;
+        }
         if (tid == 0) {
-            float total = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) total += sh.s[w];
+            float all = sh.m[0], total = 0.f;
+            for (int w = 1; w < kWarps; ++w) all = fmaxf(all, sh.m[w]);
+            for (int w = 0; w < kWarps; ++w) total += sh.m[w] == all ? sh.s[w] : sh.s[w] * fast_exp2((sh.m[w] - all) * kLog2e);
             part[li] = Part{all, total};
         }
         __syncthreads();
@@ -273,9 +328,7 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectP
     if (rank == 0) {
         // ---- log-sums of the rows
         for (int b = tid; b < p.beams; b += kThreads) {
-            const int64_t row = (int64_t)group * p.beams + b;
-            const float score = p.scores[row];
-            const bool done = p.finished && p.finished[row] != 0;
+            const float score = s_score[b];
             float m = -INFINITY, s = 0.f;
             for (int k = 0; k < p.slices; ++k) {
                 const int i = b * p.slices + k;
@@ -290,29 +343,28 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectP
             double lse = 0;
             if (!(score < INFINITY)) {
                 set_error(p.err, PKA_DEVERR_LOGITS);
-            } else if (score > -INFINITY && done) {
+            } else if (score > -INFINITY && s_state[b]) {
                 state = 2;
             } else if (score > -INFINITY) {
                 if (!(s < INFINITY) || m == INFINITY) {
                     set_error(p.err, PKA_DEVERR_LOGITS);
                 } else if (m > -INFINITY) {
                     state = 1;
-                    lse = (double)m + log((double)s);
+                    lse = (double)m + log_of(s);
                 }
             }
             s_lse[b] = lse;
             s_state[b] = state;
         }
         // the joined lists: 64-bit scores, and what decides between equal ones
-        u64* hi = reinterpret_cast<u64*>(part + per);  // [parts][keep]
+        u64* hi = lists + ((size_t)per * (keep + 1) + 1) / 2 * 2;  // [parts][keep], at 16 bytes
         u64* lo = hi + (size_t)parts * keep;
-        int32_t* picked = reinterpret_cast<int32_t*>(lo + (size_t)parts * keep);
-        if (tid == 0) sh.count = 0;
+        u64* best = lo + (size_t)parts * keep;  // [entries][2], those that may be among the best
         __syncthreads();
         const int entries = parts * keep;
+        const bool all = entries <= kThreads;
         for (int j = tid; j < entries; j += kThreads) {
-            const int i = j / keep, k = j % keep, b = i / p.slices;
-            const int64_t row = (int64_t)group * p.beams + b;
+            const int i = j / keep, k = j - i * keep, b = i / p.slices;
             const u64 key = load_cluster64(&lists[(size_t)(i / ncta) * keep + k], i % ncta);
             u64 h = 0, l = 0;
             uint32_t order = 0;
@@ -320,21 +372,26 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectP
             if (s_state[b] == 1 && key) {
                 order = (uint32_t)(key >> 32);
                 token = (int)(0xffffffffu - (uint32_t)key);
-                h = order_of((double)p.scores[row] + ((double)of_order(order) - s_lse[b]));
-            } else if (s_state[b] == 2 && i % p.slices == 0 && k == 0) {
+                h = order_of((double)s_score[b] + ((double)of_order(order) - s_lse[b]));
+            } else if (s_state[b] == 2 && i == b * p.slices && k == 0) {
                 token = p.end_token;
-                h = order_of((double)p.scores[row]);
+                h = order_of((double)s_score[b]);
             }
             if (token >= 0)
                 l = ((u64)(kMaxBeams - 1 - b) << 58) | ((u64)order << 26) | (u64)(kMaxVocab - 1 - token);
-            hi[j] = h;
-            lo[j] = l;
+            if (!all) {
+                hi[j] = h;
+                lo[j] = l;
+            } else if (token >= 0) {
+                const int to = atomicAdd(&s_found, 1);
+                best[2 * to] = h;
+                best[2 * to + 1] = l;
+            }
         }
         __syncthreads();
-        // a threshold that at least `keep` entries reach: the keep-th of the lists' first `deep`
-        const int deep = (keep + parts - 1) / parts, heads = parts * deep;
-        u64 th = 0, tl = 0;
-        if (entries > kThreads) {
+        if (!all) {
+            // a threshold that at least `keep` entries reach: the keep-th of the lists' first `deep`
+            const int deep = (keep + parts - 1) / parts, heads = parts * deep;
             for (int j = tid; j < heads; j += kThreads) {
                 const int at = j / deep * keep + j % deep;
                 const u64 h = hi[at], l = lo[at];
@@ -344,25 +401,29 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectP
                     above += hi[a] > h || (hi[a] == h && (lo[a] > l || (lo[a] == l && o < j)));
                 }
                 if (above == keep - 1) {
-                    sh.keys[0] = h;
-                    sh.keys[1] = l;
+                    sh.keys[0][0] = h;
+                    sh.keys[0][1] = l;
                 }
             }
             __syncthreads();
-            th = sh.keys[0];
-            tl = sh.keys[1];
+            const u64 th = sh.keys[0][0], tl = sh.keys[0][1];
+            for (int j = tid; j < entries; j += kThreads) {
+                if (!hi[j] || hi[j] < th || (hi[j] == th && lo[j] < tl)) continue;
+                const int to = atomicAdd(&s_found, 1);
+                best[2 * to] = hi[j];
+                best[2 * to + 1] = lo[j];
+            }
+            __syncthreads();
         }
-        for (int j = tid; j < entries; j += kThreads)
-            if (hi[j] && (hi[j] > th || (hi[j] == th && lo[j] >= tl))) picked[atomicAdd(&sh.count, 1)] = j;
-        __syncthreads();
-        const int found = sh.count;
+        const int found = s_found;
         const int64_t base = (int64_t)group * keep;
         for (int j = tid; j < found; j += kThreads) {
-            const u64 h = hi[picked[j]], l = lo[picked[j]];
+            const u64 h = best[2 * j], l = best[2 * j + 1];
             int above = 0;
+#pragma unroll 4
             for (int o = 0; o < found; ++o) {
-                const u64 a = hi[picked[o]];
-                above += a > h || (a == h && lo[picked[o]] > l);
+                const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(best + 2 * o);
+                above += a.x > h || (a.x == h && a.y > l);
             }
             if (above >= keep) continue;
             const int b = kMaxBeams - 1 - (int)(l >> 58), token = kMaxVocab - 1 - (int)(l & (kMaxVocab - 1));
@@ -385,11 +446,12 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 template <bool kBf16, bool kVec>
 cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
-    // CTAs of a group: until there is one for each tile, or two for each SM; up to the parts' lists that one CTA joins
+    // CTAs of a group: until there is one for each round of its warps' tiles, or two for each SM; up to the parts'
+    // lists that one CTA joins
     int ncta = 1, slices = 1;
     while (ncta < 8) {
         const int more = 2 * ncta, s = more / gcd(p.beams, more);
-        if ((int64_t)ncta * kTile >= (int64_t)p.beams * p.vocab || (int64_t)p.groups * ncta >= 2 * num_sms ||
+        if ((int64_t)ncta * kWarps * Tile<kBf16, kVec>::kSize >= (int64_t)p.beams * p.vocab || (int64_t)p.groups * ncta >= 2 * num_sms ||
             p.beams * s * p.keep > kMaxEntries)
             break;
         ncta = more;
@@ -398,13 +460,13 @@ cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
     p.slices = slices;
     p.slice_len = ((p.vocab + slices - 1) / slices + 7) & ~7;  // (16-byte pieces stay whole)
     const int parts = p.beams * slices, per = (parts + ncta - 1) / ncta;
-    const size_t smem = (size_t)per * (p.keep * sizeof(u64) + sizeof(Part)) +
-                        (size_t)parts * p.keep * (2 * sizeof(u64) + sizeof(int32_t));
+    const size_t smem = ((size_t)per * (p.keep + 1) + 1) / 2 * 2 * sizeof(u64) +
+                        (size_t)parts * p.keep * 4 * sizeof(u64);
     auto kern = beam_select_kernel<kBf16, kVec>;
     if (smem > 32 * 1024) {  // (the most that any call takes)
         const cudaError_t e = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (int)((size_t)kMaxEntries * (3 * sizeof(u64) + sizeof(int32_t)) + kMaxEntries * sizeof(Part)));
+            (int)((size_t)(kMaxEntries * 6 + 2) * sizeof(u64)));
         if (e != cudaSuccess) return e;
     }
     return launch_cluster(kern, dim3(p.groups * ncta), dim3(kThreads), smem, ncta, stream, p);
