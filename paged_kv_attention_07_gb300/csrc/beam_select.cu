@@ -23,6 +23,8 @@
 // logits overflows; lanes, warps and slices are joined in a fixed order that
 // depends on nothing but the element's index, so that equal rows have equal sums.
 // Candidates of different rows are compared by their 64-bit scores.
+#include <float.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -35,6 +37,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLoads = 4;     // 16-byte loads of a lane in flight
 constexpr int kBuffer = 128;  // keys that a warp collects
+constexpr int kMaxCluster = 16;
 constexpr int kMaxEntries = 4096;  // of all parts' lists of a group
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kMinusInf = 0x007fffffu;  // order_of(-infinity)
@@ -260,10 +263,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
             const bool passes = (((u64)high << 32) | 0xffffffffu) > limit;
             if (__any_sync(0xffffffffu, passes)) {
                 uint32_t hits = 0;  // of this lane's elements
-                if (passes) {
+                if (passes) {  // (those that equal the limit's logit are decided by their key below)
+                    const float reach = limit == kNone ? -FLT_MAX : of_order((uint32_t)(limit >> 32));
 #pragma unroll
-                    for (int e = 0; e < T::kPer; ++e)
-                        hits |= (uint32_t)(key_of(x[e], from + t + T::place(e)) > limit) << e;
+                    for (int e = 0; e < T::kPer; ++e) hits |= x[e] >= reach ? 1u << e : 0u;
                 }
                 while (__any_sync(0xffffffffu, hits != 0)) {
                     if (have > kBuffer - 32) have = cut(keys, have, keep, &sh.limit);
@@ -278,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
                     if (key > limit) keys[have + __popc(who & ((1u << lane) - 1))] = key;
                     have += __popc(who);
                 }
+                // (soon: every key that a low limit lets through costs more than a cut of a few keys)
+                if (have >= min(2 * keep, kBuffer - 32)) have = cut(keys, have, keep, &sh.limit);
             }
         }
         // ---- the part's best keys: each warp's, then those of all warps
@@ -442,21 +447,16 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     cluster_barrier();  // no CTA's lists go before they are read
 }
 
-int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
-
 template <bool kBf16, bool kVec>
 cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
-    // CTAs of a group: until there is one for each round of its warps' tiles, or two for each SM; up to the parts'
-    // lists that one CTA joins
-    int ncta = 1, slices = 1;
-    while (ncta < 8) {
-        const int more = 2 * ncta, s = more / gcd(p.beams, more);
-        if ((int64_t)ncta * kWarps * Tile<kBf16, kVec>::kSize >= (int64_t)p.beams * p.vocab || (int64_t)p.groups * ncta >= 2 * num_sms ||
-            p.beams * s * p.keep > kMaxEntries)
-            break;
-        ncta = more;
-        slices = s;
-    }
+    // A group's CTAs have a part each where its beams allow: as many slices of a row as give each warp a
+    // tile of its own and the SMs up to four CTAs, and no more than a cluster's 16 CTAs and the lists
+    // that one of them joins.
+    int slices = 1;
+    while (p.beams * (slices + 1) <= kMaxCluster && (int64_t)p.groups * p.beams * (slices + 1) <= 4 * num_sms &&
+           p.beams * (slices + 1) * p.keep <= kMaxEntries && p.vocab > slices * kWarps * Tile<kBf16, kVec>::kSize)
+        ++slices;
+    const int ncta = std::min(p.beams * slices, kMaxCluster);
     p.slices = slices;
     p.slice_len = ((p.vocab + slices - 1) / slices + 7) & ~7;  // (16-byte pieces stay whole)
     const int parts = p.beams * slices, per = (parts + ncta - 1) / ncta;
@@ -467,6 +467,10 @@ cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
         const cudaError_t e = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
             (int)((size_t)(kMaxEntries * 6 + 2) * sizeof(u64)));
+        if (e != cudaSuccess) return e;
+    }
+    if (ncta > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     return launch_cluster(kern, dim3(p.groups * ncta), dim3(kThreads), smem, ncta, stream, p);
