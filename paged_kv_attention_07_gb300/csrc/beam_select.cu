@@ -9,15 +9,16 @@
 // cluster whose first CTA joins the parts' sums and lists through distributed
 // shared memory: no workspace, no second launch.
 //
-// A warp goes through its share of a part by itself: four 16-byte loads per lane at a
-// time with the next four on their way, the sum, and a look whether the lane's largest
-// passes the limit, a key that num_out keys of the part are known to reach. The first
-// limit is the num_out-th of the lanes' largest logits of a warp's first tile; keys past
-// the limit go to a buffer in shared memory, which is cut back to the best num_out when
-// it is full, and the limit rises to the last of them, for all the CTA's warps. A key is
-// the logit's order in the upper and the token's complement in the lower 32 bits: keys
-// are distinct, the larger one is the better, and the order of their arrival does not
-// matter, nor which warp sees a raised limit when.
+// A part is gone through twice. First every warp streams its share, four 16-byte loads
+// per lane at a time with the next four on their way: the sum, and the lane's largest
+// logit of each of up to kEpochs stretches. num_out lanes reach the num_out-th of the
+// lanes' largest, so nothing below that limit counts, and few stretches reach it: only
+// those are loaded again, and their elements past the limit collected. (With the search in
+// the stream each tile that passed a limit cost a microsecond: 64 x 4 beams 34 us.) A
+// warp's buffer of keys is cut back to the best num_out when it is full (a part of equal
+// logits), and the limit rises to the last of them. A key is the logit's order in the upper
+// and the token's complement in the lower 32 bits: keys are distinct, the larger one is the
+// better, and the order of their arrival does not matter.
 //
 // The sum runs over x - m, m the lane's largest so far, which no scale of the
 // logits overflows; lanes, warps and slices are joined in a fixed order that
@@ -37,6 +38,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLoads = 4;     // 16-byte loads of a lane in flight
 constexpr int kBuffer = 128;  // keys that a warp collects
+constexpr int kEpochs = 16;   // stretches of a lane's share
 constexpr int kMaxCluster = 16;
 constexpr int kMaxEntries = 4096;  // of all parts' lists of a group
 constexpr float kLog2e = 1.4426950408889634f;
@@ -66,12 +68,6 @@ PKA_DEVICE u64 load_cluster64(const u64* p, uint32_t rank) {
                  : "r"(smem_u32(p)), "r"(rank)
                  : "memory");
     return v;
-}
-
-template <bool kBf16>
-PKA_DEVICE float element(const void* row, int64_t i) {
-    if constexpr (kBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(row)[i]);
-    else return static_cast<const float*>(row)[i];
 }
 
 // A warp's tile: kPer elements per lane. With 16-byte loads a lane has runs of kRun
@@ -121,6 +117,8 @@ struct Tile {
 
 struct Shared {
     u64 keys[kWarps][kBuffer];
+    float tops[kEpochs][kThreads];
+    uint32_t best[kWarps][32];
     float m[kWarps], s[kWarps];
     u64 limit;
     int count[kWarps];
@@ -216,79 +214,59 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
         if (tid == 0) sh.limit = kNone;
         __syncthreads();
         u64* keys = sh.keys[warp];
-        float m = -INFINITY, s = 0.f;
-        int have = 0;
+        // ---- the stream
+        constexpr int kRound = kWarps * T::kSize;
+        const int rounds = (n + kRound - 1) / kRound, stretch = (rounds + kEpochs - 1) / kEpochs;
+        float m = -INFINITY, s = 0.f, top = -INFINITY;
         T x, next;
         int t = warp * T::kSize;
         if (t < n) next.load(logits, t, n - t);
-        for (bool first = true; t < n; t += kThreads / 32 * T::kSize, first = false) {
-            x = next;
-            const int ahead = t + kThreads / 32 * T::kSize;
-            if (ahead < n) next.load(logits, ahead, n - ahead);
-            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int r = 0, in = 0, epoch = 0; r < rounds; ++r, t += kRound) {
+            if (t < n) {
+                x = next;
+                if (t + kRound < n) next.load(logits, t + kRound, n - t - kRound);
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < T::kPer; e += 2) tops[e / 2 % 4] = fmax3f(tops[e / 2 % 4], x[e], x[e + 1]);
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            if (top > m) {
-                s *= fast_exp2((m - top) * kLog2e);
-                m = top;
-            }
-            if (m > -INFINITY) {
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < T::kPer; e += 2) {
-                    float d0, d1;
-                    fma2_bcast(d0, d1, x[e], x[e + 1], 1.f, -m);
-                    fma2_bcast(d0, d1, d0, d1, kLog2e, 0.f);
-                    add2(sum[e % 4], sum[e % 4 + 1], fast_exp2(d0), fast_exp2(d1));
+                for (int e = 0; e < T::kPer; e += 2) tops[e / 2 % 4] = fmax3f(tops[e / 2 % 4], x[e], x[e + 1]);
+                top = fmaxf(fmax3f(top, tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                if (top > m) {
+                    s *= fast_exp2((m - top) * kLog2e);
+                    m = top;
                 }
-                s += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            } else {
+                if (m > -INFINITY) {
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < T::kPer; ++e) s += x[e] == x[e] ? 0.f : x[e];  // a NaN among -infinities
-            }
-            // ---- candidates
-            const uint32_t high = order_of(top);
-            if (first && keep <= 32) {  // the keep-th of the lanes' largest
-                uint32_t left = high, kth = 0;
-                for (int k = 0; k < keep; ++k) {
-                    kth = __reduce_max_sync(0xffffffffu, left);
-                    const uint32_t who = __ballot_sync(0xffffffffu, left == kth);
-                    if (lane == __ffs(who) - 1) left = 0;
-                }
-                if (lane == 0 && kth > kMinusInf) atomicMax(&sh.limit, ((u64)kth << 32) - 1);
-                __syncwarp();
-            }
-            u64 limit = *const_cast<volatile u64*>(&sh.limit);
-            const bool passes = (((u64)high << 32) | 0xffffffffu) > limit;
-            if (__any_sync(0xffffffffu, passes)) {
-                uint32_t hits = 0;  // of this lane's elements
-                if (passes) {  // (those that equal the limit's logit are decided by their key below)
-                    const float reach = limit == kNone ? -FLT_MAX : of_order((uint32_t)(limit >> 32));
-#pragma unroll
-                    for (int e = 0; e < T::kPer; ++e) hits |= x[e] >= reach ? 1u << e : 0u;
-                }
-                while (__any_sync(0xffffffffu, hits != 0)) {
-                    if (have > kBuffer - 32) have = cut(keys, have, keep, &sh.limit);
-                    limit = *const_cast<volatile u64*>(&sh.limit);
-                    u64 key = 0;
-                    if (hits) {
-                        const int e = __ffs(hits) - 1, token = t + T::place(e);
-                        hits &= hits - 1;
-                        key = key_of(element<kBf16>(logits, token), from + token);
+                    for (int e = 0; e < T::kPer; e += 2) {
+                        float d0, d1;
+                        fma2_bcast(d0, d1, x[e], x[e + 1], 1.f, -m);
+                        fma2_bcast(d0, d1, d0, d1, kLog2e, 0.f);
+                        add2(sum[e % 4], sum[e % 4 + 1], fast_exp2(d0), fast_exp2(d1));
                     }
-                    const uint32_t who = __ballot_sync(0xffffffffu, key > limit);
-                    if (key > limit) keys[have + __popc(who & ((1u << lane) - 1))] = key;
-                    have += __popc(who);
+                    s += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < T::kPer; ++e) s += x[e] == x[e] ? 0.f : x[e];  // a NaN among -infinities
                 }
-                // (soon: every key that a low limit lets through costs more than a cut of a few keys)
-                if (have >= min(2 * keep, kBuffer - 32)) have = cut(keys, have, keep, &sh.limit);
+            }
+            if (++in == stretch || r == rounds - 1) {
+                sh.tops[epoch++][tid] = top;
+                top = -INFINITY;
+                in = 0;
             }
         }
-        // ---- the part's best keys: each warp's, then those of all warps
-        have = cut(keys, have, keep, &sh.limit);
-        if (lane == 0) sh.count[warp] = have;
-        // ... and its sum, in a fixed order
+        // ---- the limit: the keep-th of the lanes' largest, from each warp's first `keep`
+        {
+            uint32_t left = order_of(m), mine = 0;
+            const int take = min(keep, 32);
+            for (int k = 0; k < take; ++k) {
+                const uint32_t most = __reduce_max_sync(0xffffffffu, left);
+                if (lane == k) mine = most;
+                const uint32_t who = __ballot_sync(0xffffffffu, left == most);
+                if (lane == __ffs(who) - 1) left = 0;
+            }
+            sh.best[warp][lane] = mine;
+        }
+        // ... and the part's sum, in a fixed order
         float wm = m;
 #pragma unroll
         for (int o = 16; o; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
@@ -299,6 +277,75 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
             sh.m[warp] = wm;
             sh.s[warp] = ws;
         }
+        __syncthreads();
+        if (warp == 0) {
+            uint32_t left[kWarps], most = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) left[w] = sh.best[w][lane];
+            for (int k = 0; k < keep; ++k) {
+                uint32_t mine = left[0];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) mine = max(mine, left[w]);
+                most = __reduce_max_sync(0xffffffffu, mine);
+                const uint32_t who = __ballot_sync(0xffffffffu, mine == most);
+                if (lane == __ffs(who) - 1) {
+                    bool out = false;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        if (!out && left[w] == most) {
+                            left[w] = 0;
+                            out = true;
+                        }
+                    }
+                }
+            }
+            if (lane == 0 && most > kMinusInf) sh.limit = ((u64)most << 32) - 1;
+        } else if (tid == 32) {
+            float all = sh.m[0], total = 0.f;
+            for (int w = 1; w < kWarps; ++w) all = fmaxf(all, sh.m[w]);
+            for (int w = 0; w < kWarps; ++w) total += sh.m[w] == all ? sh.s[w] : sh.s[w] * fast_exp2((sh.m[w] - all) * kLog2e);
+            part[li] = Part{all, total};
+        }
+        __syncthreads();
+        // ---- what reaches it, from the stretches that do
+        int have = 0;
+        for (int epoch = 0; epoch * stretch < rounds; ++epoch) {
+            u64 limit = *const_cast<volatile u64*>(&sh.limit);
+            // (a logit that equals the limit's is decided by its key; -infinity never counts)
+            const float reach = limit == kNone ? -FLT_MAX : of_order((uint32_t)(limit >> 32));
+            const bool again = sh.tops[epoch][tid] >= reach;
+            if (!__any_sync(0xffffffffu, again)) continue;
+            t = epoch * stretch * kRound + warp * T::kSize;
+            for (int r = 0; r < stretch && t < n; ++r, t += kRound) {
+                uint32_t hits = 0;  // of this lane's elements
+                if (again) {
+                    x.load(logits, t, n - t);
+#pragma unroll
+                    for (int e = 0; e < T::kPer; ++e) hits |= x[e] >= reach ? 1u << e : 0u;
+                }
+                while (__any_sync(0xffffffffu, hits != 0)) {
+                    if (have > kBuffer - 32) {
+                        have = cut(keys, have, keep, &sh.limit);
+                        limit = *const_cast<volatile u64*>(&sh.limit);
+                    }
+                    u64 key = 0;
+                    if (hits) {
+                        const int at = __ffs(hits) - 1;
+                        float v = x[0];
+#pragma unroll
+                        for (int e = 1; e < T::kPer; ++e) v = at == e ? x[e] : v;
+                        key = key_of(v, from + t + T::place(at));
+                        hits &= hits - 1;
+                    }
+                    const uint32_t who = __ballot_sync(0xffffffffu, key > limit);
+                    if (key > limit) keys[have + __popc(who & ((1u << lane) - 1))] = key;
+                    have += __popc(who);
+                }
+            }
+        }
+        // ---- the part's best keys: each warp's, then those of all warps
+        have = cut(keys, have, keep, &sh.limit);
+        if (lane == 0) sh.count[warp] = have;
         __syncthreads();
         for (int k = lane; k < have; k += 32) {
             const u64 mine = keys[k];
@@ -319,12 +366,6 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
             int total = 0;
             for (int w = 0; w < kWarps; ++w) total += sh.count[w];
             if (tid >= total) lists[(size_t)li * keep + tid] = 0;
-        }
-        if (tid == 0) {
-            float all = sh.m[0], total = 0.f;
-            for (int w = 1; w < kWarps; ++w) all = fmaxf(all, sh.m[w]);
-            for (int w = 0; w < kWarps; ++w) total += sh.m[w] == all ? sh.s[w] : sh.s[w] * fast_exp2((sh.m[w] - all) * kLog2e);
-            part[li] = Part{all, total};
         }
         __syncthreads();
     }
