@@ -61,13 +61,12 @@ PKA_DEVICE u64 order_of(double x) {
 }
 PKA_DEVICE double of_order(u64 o) { return __longlong_as_double((long long)((o >> 63) ? o ^ (1ull << 63) : ~o)); }
 
-PKA_DEVICE u64 load_cluster64(const u64* p, uint32_t rank) {
-    u64 v;
-    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.u64 %0, [a];\n\t}"
-                 : "=l"(v)
-                 : "r"(smem_u32(p)), "r"(rank)
+// Stores v where `p` lies in the shared memory of the cluster's first CTA (which must have started).
+PKA_DEVICE void store_first64(u64* p, u64 v) {
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u64 [a], %1;\n\t}" ::"r"(
+                     smem_u32(p)),
+                 "l"(v)
                  : "memory");
-    return v;
 }
 
 // A warp's tile: kPer elements per lane. With 16-byte loads a lane has runs of kRun
@@ -173,13 +172,6 @@ PKA_DEVICE double log_of(float s) {
     return (double)e * 0.69314718055994531 + 2.0 * ((double)z + (double)z_low) + (double)tail;
 }
 
-// What a CTA leaves of a part: the largest logit, the sum of exp(x - largest) and
-// the best keys (0 behind the last).
-struct Part {
-    float m, s;
-};
-static_assert(sizeof(Part) == sizeof(u64), "");
-
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSelectParams p) {
     using T = Tile<kBf16, kVec>;
@@ -194,9 +186,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ncta = (int)cluster_size(), rank = (int)cluster_rank(), group = blockIdx.x / ncta;
     const int keep = p.keep, parts = p.beams * p.slices;
-    const int per = (parts + ncta - 1) / ncta;
-    u64* lists = reinterpret_cast<u64*>(s_dyn);                      // [per][keep], each sorted, then 0
-    Part* part = reinterpret_cast<Part*>(lists + (size_t)per * keep);  // [per]
+    // in the first CTA's shared memory, written by all of the cluster
+    u64* lists = reinterpret_cast<u64*>(s_dyn);                          // [parts][keep], 0 behind the last key
+    u64* sums = lists + (size_t)parts * keep;                            // [parts], a Part each
+    u64* hi = sums + parts + ((parts * (keep + 1)) & 1);                 // [parts][keep], at 16 bytes
+    u64* lo = hi + (size_t)parts * keep;
+    u64* best = lo + (size_t)parts * keep;  // [parts * keep][2], those that may be among the best
+    cluster_arrive();
     for (int b = tid; b < p.beams; b += kThreads) {
         const int64_t row = (int64_t)group * p.beams + b;
         s_score[b] = p.scores[row];
@@ -205,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     if (tid == 0) s_found = 0;
     __syncthreads();
 
-    for (int i = rank, li = 0; i < parts; i += ncta, ++li) {
+    bool met = false;  // the first CTA has started
+    for (int i = rank; i < parts; i += ncta) {
         const int beam = i / p.slices, slice = i - beam * p.slices;
         const int from = slice * p.slice_len;
         const int n = s_state[beam] || !(fabsf(s_score[beam]) < INFINITY) ? 0 : min(p.slice_len, p.vocab - from);
@@ -300,11 +297,16 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
                 }
             }
             if (lane == 0 && most > kMinusInf) sh.limit = ((u64)most << 32) - 1;
-        } else if (tid == 32) {
+        }
+        if (!met) cluster_wait();
+        met = true;
+        if (tid == 32) {
             float all = sh.m[0], total = 0.f;
+#pragma unroll
             for (int w = 1; w < kWarps; ++w) all = fmaxf(all, sh.m[w]);
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) total += sh.m[w] == all ? sh.s[w] : sh.s[w] * fast_exp2((sh.m[w] - all) * kLog2e);
-            part[li] = Part{all, total};
+            store_first64(&sums[i], (u64)__float_as_uint(all) | ((u64)__float_as_uint(total) << 32));
         }
         __syncthreads();
         // ---- what reaches it, from the stretches that do
@@ -343,42 +345,38 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
                 }
             }
         }
-        // ---- the part's best keys: each warp's, then those of all warps
-        have = cut(keys, have, keep, &sh.limit);
+        // ---- the part's best keys
         if (lane == 0) sh.count[warp] = have;
         __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) total += sh.count[w];
         for (int k = lane; k < have; k += 32) {
             const u64 mine = keys[k];
-            int above = k;
-            for (int w = 1; w < kWarps && above < keep; ++w) {  // (each list is sorted: what is above is in front)
-                const u64* other = sh.keys[(warp + w) % kWarps];
-                int lo = 0, hi = sh.count[(warp + w) % kWarps];
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (other[mid] > mine) lo = mid + 1;
-                    else hi = mid;
-                }
-                above += lo;
+            int above = 0;
+#pragma unroll 1
+            for (int w = 0; w < kWarps; ++w) {
+#pragma unroll 4
+                for (int o = 0; o < sh.count[w]; ++o) above += sh.keys[w][o] > mine;
             }
-            if (above < keep) lists[(size_t)li * keep + above] = mine;
+            if (above < keep) store_first64(&lists[(size_t)i * keep + above], mine);
         }
-        if (tid < keep) {
-            int total = 0;
-            for (int w = 0; w < kWarps; ++w) total += sh.count[w];
-            if (tid >= total) lists[(size_t)li * keep + tid] = 0;
-        }
+        if (tid >= total && tid < keep) store_first64(&lists[(size_t)i * keep + tid], 0);
         __syncthreads();
     }
 
-    cluster_barrier();
-    if (rank == 0) {
+    if (!met) cluster_wait();
+    cluster_arrive();
+    if (rank != 0) return;  // (nothing of it is read)
+    cluster_wait();
+    {
         // ---- log-sums of the rows
         for (int b = tid; b < p.beams; b += kThreads) {
             const float score = s_score[b];
             float m = -INFINITY, s = 0.f;
             for (int k = 0; k < p.slices; ++k) {
-                const int i = b * p.slices + k;
-                const float pm = load_cluster(&part[i / ncta].m, i % ncta), ps = load_cluster(&part[i / ncta].s, i % ncta);
+                const u64 x = sums[b * p.slices + k];
+                const float pm = __uint_as_float((uint32_t)x), ps = __uint_as_float((uint32_t)(x >> 32));
                 if (pm > m) {
                     s *= fast_exp2((m - pm) * kLog2e);
                     m = pm;
@@ -403,15 +401,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
             s_state[b] = state;
         }
         // the joined lists: 64-bit scores, and what decides between equal ones
-        u64* hi = lists + ((size_t)per * (keep + 1) + 1) / 2 * 2;  // [parts][keep], at 16 bytes
-        u64* lo = hi + (size_t)parts * keep;
-        u64* best = lo + (size_t)parts * keep;  // [entries][2], those that may be among the best
         __syncthreads();
         const int entries = parts * keep;
         const bool all = entries <= kThreads;
         for (int j = tid; j < entries; j += kThreads) {
             const int i = j / keep, k = j - i * keep, b = i / p.slices;
-            const u64 key = load_cluster64(&lists[(size_t)(i / ncta) * keep + k], i % ncta);
+            const u64 key = lists[j];
             u64 h = 0, l = 0;
             uint32_t order = 0;
             int token = -1;
@@ -485,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
             if (p.out_finished) p.out_finished[base + k] = 0;
         }
     }
-    cluster_barrier();  // no CTA's lists go before they are read
 }
 
 template <bool kBf16, bool kVec>
@@ -500,14 +494,13 @@ cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
     const int ncta = std::min(p.beams * slices, kMaxCluster);
     p.slices = slices;
     p.slice_len = ((p.vocab + slices - 1) / slices + 7) & ~7;  // (16-byte pieces stay whole)
-    const int parts = p.beams * slices, per = (parts + ncta - 1) / ncta;
-    const size_t smem = ((size_t)per * (p.keep + 1) + 1) / 2 * 2 * sizeof(u64) +
-                        (size_t)parts * p.keep * 4 * sizeof(u64);
+    const size_t entries = (size_t)p.beams * slices * p.keep;
+    const size_t smem = (5 * entries + p.beams * slices + 1) * sizeof(u64);
     auto kern = beam_select_kernel<kBf16, kVec>;
     if (smem > 32 * 1024) {  // (the most that any call takes)
         const cudaError_t e = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (int)((size_t)(kMaxEntries * 6 + 2) * sizeof(u64)));
+            (int)((size_t)(kMaxEntries * 6 + 1) * sizeof(u64)));
         if (e != cudaSuccess) return e;
     }
     if (ncta > 8) {
