@@ -14,7 +14,7 @@
 // logit of each of up to kEpochs stretches. num_out lanes reach the num_out-th of the
 // lanes' largest, so nothing below that limit counts, and few stretches reach it: only
 // those are loaded again, and their elements past the limit collected. (With the search in
-// the stream each tile that passed a limit cost a microsecond: 64 x 4 beams 34 us.) A
+// the stream each tile that passed a limit cost a microsecond: 64 x 4 beams took 34 us, not 30.) A
 // warp's buffer of keys is cut back to the best num_out when it is full (a part of equal
 // logits), and the limit rises to the last of them. A key is the logit's order in the upper
 // and the token's complement in the lower 32 bits: keys are distinct, the larger one is the
@@ -24,6 +24,12 @@
 // logits overflows; lanes, warps and slices are joined in a fixed order that
 // depends on nothing but the element's index, so that equal rows have equal sums.
 // Candidates of different rows are compared by their 64-bit scores.
+//
+// Measured: 4 rows of 32000 bf16 logits 8.7 us; 64 groups of 4 rows of 131072 23.6 us (2.8 TB/s; at the
+// rate of a copy the 67 MB take 9.9); 17 groups of 5 rows of 50001 float32 logits 12.0 us. A
+// launch and the phases behind the stream (limit, second reading, lists, ranks: each a
+// few hundred instructions fetched for the first time) take about 7 us of each; the stream
+// of 256 rows is bound by the busiest SMs, which have two rows where the mean is 1.7.
 #include <float.h>
 
 #include <algorithm>
@@ -39,6 +45,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLoads = 4;     // 16-byte loads of a lane in flight
 constexpr int kBuffer = 128;  // keys that a warp collects
 constexpr int kEpochs = 16;   // stretches of a lane's share
+constexpr int kResident = 2;  // CTAs of an SM (of 4, with half the registers, 64 x 4 beams took 29 us, not 23)
 constexpr int kMaxCluster = 16;
 constexpr int kMaxEntries = 4096;  // of all parts' lists of a group
 constexpr float kLog2e = 1.4426950408889634f;
@@ -74,6 +81,7 @@ PKA_DEVICE void store_first64(u64* p, u64 v) {
 template <bool kBf16, bool kVec>
 struct Tile {
     static constexpr int kRun = kBf16 ? 8 : 4, kPer = kLoads * kRun, kSize = 32 * kPer;
+    static_assert(kPer <= 32, "a lane's hits are the bits of a word");
     uint32_t w[kLoads * 4];  // two bf16 or one float each
     PKA_DEVICE static int place(int e) {
         const int lane = threadIdx.x & 31;
@@ -173,7 +181,7 @@ PKA_DEVICE double log_of(float s) {
 }
 
 template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSelectParams p) {
+__global__ void __launch_bounds__(kThreads, kResident) beam_select_kernel(const BeamSelectParams p) {
     using T = Tile<kBf16, kVec>;
     extern __shared__ __align__(16) uint8_t s_dyn[];
     __shared__ __align__(16) Shared sh;
@@ -485,10 +493,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
 template <bool kBf16, bool kVec>
 cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
     // A group's CTAs have a part each where its beams allow: as many slices of a row as give each warp a
-    // tile of its own and the SMs up to four CTAs, and no more than a cluster's 16 CTAs and the lists
-    // that one of them joins.
+    // tile of its own, and no more than a cluster's 16 CTAs and the lists that one of them joins; and
+    // three CTAs for two SMs, of the four that they hold: larger clusters leave SMs of a GPC over, and
+    // with more of them some wait (17 x 5 beams in 255 CTAs 17.9 us, in 170 12.0).
     int slices = 1;
-    while (p.beams * (slices + 1) <= kMaxCluster && (int64_t)p.groups * p.beams * (slices + 1) <= 4 * num_sms &&
+    while (p.beams * (slices + 1) <= kMaxCluster && (int64_t)p.groups * p.beams * (slices + 1) * 2 <= 3 * num_sms &&
            p.beams * (slices + 1) * p.keep <= kMaxEntries && p.vocab > slices * kWarps * Tile<kBf16, kVec>::kSize)
         ++slices;
     const int ncta = std::min(p.beams * slices, kMaxCluster);
