@@ -810,7 +810,8 @@ PKA_API pka_status pka_copy_pages(void *const *caches, int num_caches, int64_t n
  * max_query_len (PKA_DEVERR_QUERY_START_LOC, PKA_DEVERR_QUERY_LEN), a seq_len that
  * does not fit (PKA_DEVERR_SEQ_LEN), a prefix that does not (PKA_DEVERR_SEQ_LEN),
  * group_starts that do not ascend (PKA_DEVERR_INDEX) set the bit and nothing is
- * written; a block id outside the cache sets PKA_DEVERR_BLOCK_ID.
+ * written; a block id outside the cache sets PKA_DEVERR_BLOCK_ID. Infinities and
+ * NaN in q, keys or values reach the tokens that see them only.
  * head_dim 64 or 128 (_fp8: 128), Hq / Hkv <= 16, block_size a power of two in [1, 128], num_reqs <= 4096,
  * num_groups <= num_reqs, num_blocks * Hkv * block_size <= INT32_MAX, max_seq_len <= 2^30, num_tokens * Hq <=
  * 2^27, (num_tokens * Hq / (128 Hkv) + num_reqs) * Hkv * max_seq_len / 128 below about 2^28, else

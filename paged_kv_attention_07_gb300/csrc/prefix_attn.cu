@@ -26,6 +26,8 @@
 // pieces. Tensor memory: S_k (128 columns, P_k written over it in bf16) and O_k.
 // P is rounded to bf16 for the product (the type of V, which the tensor cores ask
 // for); its sum is kept from the unrounded values in 32 bits.
+#include <float.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -109,6 +111,24 @@ PKA_DEVICE int first_tile(int x, int us, const Seg& s) {
 // last token) have nothing to see: they are left out, but for one.
 PKA_DEVICE int seen_tiles(const Seg& s, int t0, int t1, int end) {
     return max(1, min(t1 - t0, (min(s.c1, end) - (s.base + t0 * kKeys) + kKeys - 1) / kKeys));
+}
+
+// Replaces the halves of w whose bits are all set where kMask's are (infinities and NaN) by zeros.
+template <uint32_t kMask, int N>
+PKA_DEVICE bool take_out(uint32_t (&w)[N]) {
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if ((w[e] & kMask) == kMask) {
+            w[e] &= 0xffff0000u;
+            any = true;
+        }
+        if ((w[e] >> 16 & kMask) == kMask) {
+            w[e] &= 0xffffu;
+            any = true;
+        }
+    }
+    return any;
 }
 
 struct Piece {
@@ -208,7 +228,10 @@ PKA_DEVICE void warp_sums(int& a, int& b) {
     }
 }
 
-template <int D, bool kFp8>
+// kSeveral: requests may have more than one new token. The code that keeps a later token's
+// infinities from earlier ones costs 3 to 12 % where nothing calls for it (24 groups of 8 beams 127
+// us with it, 118 without; 8-bit 126 and 113), by its size alone.
+template <int D, bool kFp8, bool kSeveral>
 __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     prefix_attn_kernel(const __grid_constant__ PrefixMaps maps, const PrefixParams p) {
     using C = PxCfg<D, kFp8>;
@@ -244,6 +267,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     // lane 1's product lets that S go first.
     __shared__ volatile int s_next0;
     __shared__ int s_pieces;  // listed
+    __shared__ uint32_t s_odd[kPieces / 32];  // bit per piece: a value was taken out of its tiles (see below)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -296,6 +320,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     int err = 0;
     if (tid == 0 && (meta.starts[0] != 0 || meta.starts[p.groups] != p.B)) err = PKA_DEVERR_INDEX;
     if (tid == 0) s_pieces = 0;
+    if (tid < kPieces / 32) s_odd[tid] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -744,6 +769,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         }
                         const int kb = U.kb0 + t * kKeys;
                         const uint32_t zlo = (uint32_t)max(0, U.c0 - kb), valid = (uint32_t)(min(kKeys, U.c1 - kb) - (int)zlo);
+                        // (rows from `some` on are not seen by all of the piece's tokens)
+                        const uint32_t some = kSeveral && U.ntok > 1 ? (uint32_t)max(0, U.pos0 + 1 - kb) : kKeys;
                         const uint32_t from = sm_base + C::kOffCode + st * C::kCodeBytes;
                         const uint32_t to = sm_base + C::kOffV + st * C::kTileBytes;
 #pragma unroll 2
@@ -766,6 +793,22 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                                 const uint32_t second = odd ^ hh;
                                 st_shared4(base + sw128(row, p0 + second), second ? y[4] : y[0], second ? y[5] : y[1],
                                            second ? y[6] : y[2], second ? y[7] : y[3]);
+                            }
+                        }
+                        if (kSeveral && some < kKeys) {  // (a thread has the same places as above)
+#pragma unroll 1
+                            for (int j = wtid; j < kKeys * 8; j += 128) {
+                                const uint32_t row = j >> 3, c = j & 7;
+                                if (row < some) continue;
+#pragma unroll 1
+                                for (int hh = 0; hh < 2; ++hh) {
+                                    const uint32_t at = to + (c >> 2) * C::kChunkBytes + sw128(row, 2 * (c & 3) + hh);
+                                    const uint4 x = lds128(at);
+                                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                                    if (!take_out<0x7c00u>(w)) continue;
+                                    st_shared4(at, w[0], w[1], w[2], w[3]);
+                                    atomicOr(&s_odd[i >> 5], 1u << (i & 31));
+                                }
                             }
                         }
                         fence_proxy_async_smem();
@@ -828,7 +871,10 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 for (int t = t_first; t < U.nkt; t += step) {
                     if (!mbar_wait_warp(&s_full[k], n_s & 1, p.err)) { ok = false; break; }
                     tc_fence_after();
-                    if (kFp8 && t == t_first) sl2 = p.scale_log2 * row_unit[(piece & 3) * 128 + row];
+                    if (kFp8 && t == t_first) {
+                        sl2 = p.scale_log2 * row_unit[(piece & 3) * 128 + row];
+                        if (sl2 < FLT_MIN) sl2 = FLT_MIN;  // (a masked score times 0 is NaN; these scores are below 2^-99 either way)
+                    }
                     const int kb = U.kb0 + t * kKeys;
                     const bool edge = kb < U.c0 || kb + kKeys > all1;
                     float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -979,16 +1025,30 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     // value rows outside the segment's keys may hold anything: zeros, by the warps
                     // without rows if there are any. With two row tiles lane 0 does it (lane 1's
                     // product of a tile follows lane 0's).
+                    // Of the rows from `some` on, which not all tokens see, what is not finite is taken
+                    // out too (its weight of zero would not keep it from the others) and given back
+                    // at the end to those that see it.
                     const int zlo = max(0, U.c0 - kb), zhi = min(kKeys, U.c1 - kb);
-                    if (!kFp8 && (zlo > 0 || zhi < kKeys) && (k == 0 || !two) && (idle || busy == 4)) {
+                    const int some = kSeveral && U.ntok > 1 ? max(zlo, min(all1 - kb, zhi)) : zhi;
+                    if (!kFp8 && edge && (zlo > 0 || some < kKeys) && (k == 0 || !two) && (idle || busy == 4)) {
                         const uint32_t vi = kv_base + t;
                         if (!mbar_wait_warp(&v_full[vi & 1], (vi >> 1) & 1, p.err)) { ok = false; break; }
                         uint8_t* vt = smem + C::kOffV + (vi & 1) * C::kTileBytes;
                         const int skip = busy == 4 ? 0 : 32 * busy;  // (threads of the lane that have rows)
+                        const int first = wg_tid - ((warp & 3) >= shift / 32 ? skip : 0);
 #pragma unroll 1
-                        for (int ci = wg_tid - ((warp & 3) >= shift / 32 ? skip : 0); ci < (zlo + kKeys - zhi) * (D / 8); ci += 128 - skip) {
+                        for (int ci = first; ci < (zlo + kKeys - zhi) * (D / 8); ci += 128 - skip) {
                             const int z = ci / (D / 8), c = ci % (D / 8), vr = z < zlo ? z : zhi + z - zlo;
                             *reinterpret_cast<uint4*>(vt + (c >> 3) * C::kChunkBytes + sw128(vr, c & 7)) = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll 1
+                        for (int ci = first; kSeveral && ci < (zhi - some) * (D / 8); ci += 128 - skip) {
+                            const int c = ci % (D / 8);
+                            uint4* at = reinterpret_cast<uint4*>(vt + (c >> 3) * C::kChunkBytes + sw128(some + ci / (D / 8), c & 7));
+                            uint32_t w[4] = {at->x, at->y, at->z, at->w};
+                            if (!take_out<0x7f80u>(w)) continue;
+                            *at = make_uint4(w[0], w[1], w[2], w[3]);
+                            atomicOr(&s_odd[i >> 5], 1u << (i & 31));
                         }
                         fence_proxy_async_smem();
                     }
@@ -1025,6 +1085,24 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_free[k]);
                 if (write) *pl = m_used + log2f(l) - kUnitP;
+                if (kSeveral && write && (*const_cast<volatile uint32_t*>(&s_odd[i >> 5]) >> (i & 31) & 1)) {
+                    // what was taken out of this lane's key tiles and the row sees
+                    const int end = min(c1, U.kb0 + U.nkt * kKeys);
+#pragma unroll 1
+                    for (int pos = max(max(U.c0, U.kb0), all1); pos < end; ++pos) {
+                        if (!two && ((((pos - U.kb0) / kKeys) ^ t_first) & 1)) continue;
+                        int block = __ldg(p.block_table + (int64_t)U.table * p.max_blocks + (pos >> p.bs_log2));
+                        if (block < 0 || block >= p.num_blocks) block = 0;
+                        const int64_t from = ((((int64_t)block * p.Hkv + U.h) << p.bs_log2) + (pos & (p.bs - 1))) * D;
+#pragma unroll 1
+                        for (int d = 0; d < D; ++d) {
+                            float x;
+                            if constexpr (kFp8) x = (static_cast<const uint8_t*>(p.v_cache)[from + d] & 0x7fu) == 0x7fu ? NAN : 0.f;
+                            else x = __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.v_cache)[from + d] << 16);
+                            if (!(fabsf(x) < INFINITY)) po[(int64_t)(d / 4) * 8 * half + d % 4] += x;
+                        }
+                    }
+                }
             }
             __syncwarp();
             setmaxnreg_dec<C::kRegsLaunch>();
@@ -1032,6 +1110,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
         __syncthreads();
         if (s_abort) break;
         if (tid == 0) s_pieces = 0;
+        if (tid < kPieces / 32) s_odd[tid] = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -1205,10 +1284,10 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParam
     }
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kSeveral>
 cudaError_t go_attn(const PrefixMaps& maps, const PrefixParams& p, int ncta, cudaStream_t stream) {
     using C = PxCfg<D, kFp8>;
-    auto kern = prefix_attn_kernel<D, kFp8>;
+    auto kern = prefix_attn_kernel<D, kFp8, kSeveral>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, dim3(ncta), dim3(C::kThreads), C::kSmem, stream, maps, p);
@@ -1239,8 +1318,14 @@ cudaError_t go_join_by_size(const PrefixParams& p, int ncta, cudaStream_t stream
 
 cudaError_t launch_prefix_attn(const PrefixMaps& maps, const PrefixParams& p, int head_dim, bool fp8, int ncta,
                                cudaStream_t stream) {
-    if (fp8) return go_attn<128, true>(maps, p, ncta, stream);
-    return head_dim == 128 ? go_attn<128, false>(maps, p, ncta, stream) : go_attn<64, false>(maps, p, ncta, stream);
+    if (p.max_query > 1) {
+        if (fp8) return go_attn<128, true, true>(maps, p, ncta, stream);
+        return head_dim == 128 ? go_attn<128, false, true>(maps, p, ncta, stream)
+                               : go_attn<64, false, true>(maps, p, ncta, stream);
+    }
+    if (fp8) return go_attn<128, true, false>(maps, p, ncta, stream);
+    return head_dim == 128 ? go_attn<128, false, false>(maps, p, ncta, stream)
+                           : go_attn<64, false, false>(maps, p, ncta, stream);
 }
 
 cudaError_t launch_prefix_join(const PrefixParams& p, int head_dim, int ncta, cudaStream_t stream) {

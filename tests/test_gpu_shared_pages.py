@@ -612,3 +612,150 @@ def test_prefix_attention_captured_on_a_stream_and_from_threads():
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert all(torch.equal(o, want) for o in outs)
+
+
+# groups of requests with several new tokens; what is not finite lies in the last `late` of them
+LATE = [(one(40, [20, 30], 3), 1), (one(200, [64, 65, 90], 5), 2), (one(3, [260, 300], 200), 70), (one(16, [9] * 12, 2), 1),
+        ([(0, [(130, 130)]), (50, [(129, 2), (3, 3)])], 1)]
+
+
+@pytest.mark.parametrize("scales", [None, (0.02, 0.03)])
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 16), (128, 2)])
+@pytest.mark.parametrize("groups,late", LATE)
+def test_prefix_attention_values_that_are_not_finite(groups, late, d, bs, scales):
+    """Infinities and NaN among the values of later tokens reach the tokens that see them, in their dims, and no other."""
+    if scales and d != 128:
+        d, bs = 128, 1
+    rng = np.random.default_rng(late + d + bs)
+    Hq, Hkv = 8, 2
+    s = prefix_case(rng, groups, Hq, Hkv, d, bs, fp8_scales=scales)
+    (k, v), table, qsl, seq, starts, prefix = s["host"]
+    seen = np.zeros(s["q"].shape)  # the sum of what a token sees: 0, an infinity or NaN
+    for r in range(len(seq)):
+        n = qsl[r + 1] - qsl[r]
+        for j in range(max(0, n - late), n):
+            pos = seq[r] - n + j
+            page, at = int(table[r, pos // bs]), pos % bs
+            for h in range(Hkv):
+                for dim in rng.choice(d, 5, replace=False):
+                    x = float(rng.choice([np.inf, -np.inf, np.nan]))
+                    if scales:
+                        x = np.nan
+                        s["v"][page, h, at, dim] = int(rng.choice([0x7f, 0xff]))
+                    else:
+                        s["v"][page, h, at, dim] = x
+                    v[page, h, at, dim] = 0
+                    seen[qsl[r] + j:qsl[r + 1], h * (Hq // Hkv):(h + 1) * (Hq // Hkv), dim] += x
+    prefix_call(s)
+    got = f64(s["out"])
+    odd = seen != 0
+    assert odd.any() and np.array_equal(np.isnan(got), np.isnan(seen)) and np.array_equal(got[np.isinf(seen)], seen[np.isinf(seen)])
+    want = ref.prefix_attention(f64(s["q"]), k, v, table, qsl, seq, starts, prefix, s["scale"] * (scales or [1])[0],
+                                (scales or [1, 1])[1])[0]
+    s["out"] = torch.where(torch.from_numpy(odd).cuda(), torch.from_numpy(want).to(BF16).cuda(), s["out"])
+    prefix_check(s)
+
+
+def test_prefix_attention_keys_and_queries_that_are_not_finite():
+    rng = np.random.default_rng(30)
+    for scales in (None, (0.02, 0.03)):
+        s = prefix_case(rng, [(64, [(20, 1), (30, 2), (1, 1)]), (0, [(200, 3)])], 8, 2, 128, 16, fp8_scales=scales)
+        table, qsl, seq = s["host"][1:4]
+        want = ref.prefix_attention(f64(s["q"]), *s["host"][0], *s["host"][1:], s["scale"] * (scales or [1])[0], (scales or [1, 1])[1])[0]
+        bad = np.zeros(s["q"].shape[:2], bool)
+        # a key of the last new token of requests 1 and 3, head 1, and queries
+        for r in (1, 3):
+            pos = seq[r] - 1
+            s["k"][int(table[r, pos // 16]), 1, pos % 16, 3] = 0x7f if scales else math.nan
+            bad[qsl[r + 1] - 1, 4:] = True
+        for t, h, x in ((0, 2, math.inf), (3, 6, math.nan), (4, 0, -math.inf)):
+            s["q"][t, h, 9] = x
+            bad[t, h] = True
+        prefix_call(s)
+        got = f64(s["out"])
+        assert np.isnan(got[bad]).all() and np.isnan(f64(s["lse"])[bad]).all()
+        s["q"][torch.from_numpy(bad).cuda()] = 0
+        s["out"] = torch.where(torch.from_numpy(bad).cuda()[..., None], torch.from_numpy(want).to(BF16).cuda(), s["out"])
+        fixed = ref.prefix_attention(f64(s["q"]), *s["host"][0], *s["host"][1:], s["scale"] * (scales or [1])[0], (scales or [1, 1])[1])
+        s["out"] = torch.where(torch.from_numpy(bad).cuda()[..., None], torch.from_numpy(fixed[0]).to(BF16).cuda(), s["out"])
+        s["lse"] = torch.where(torch.from_numpy(bad).cuda(), torch.from_numpy(fixed[1]).float().cuda(), s["lse"])
+        prefix_check(s)
+
+
+@pytest.mark.parametrize("power", [-90, -30, 0, 30, 90])
+def test_prefix_attention_fp8_magnitudes_of_queries(power):
+    """Queries of any magnitude are split alike: with the scale that brings the scores back the results are the same."""
+    rng = np.random.default_rng(31)
+    q = torch.from_numpy(rng.standard_normal((4, 8, 128)) * np.exp2(rng.integers(-12, 1, (4, 8, 128)))).to(BF16).cuda()
+    q[1, 3] = 0
+    s = prefix_case(rng, one(100, [20, 3, 40, 1]), 8, 2, 128, 16, fp8_scales=(0.02, 0.03), q=q * 2.0 ** power, scale=0.1 * 2.0 ** -power)
+    prefix_call(s)
+    prefix_check(s)
+
+
+@pytest.mark.parametrize("bs", [4, 128])
+def test_prefix_attention_pages_past_32_bits(bs):
+    """Pages whose offsets pass 32 bits in bytes and in elements."""
+    rng = np.random.default_rng(32)
+    Hkv, d = 2, 128
+    nb = 2 ** 32 // (Hkv * bs * d) + 64
+    cache = torch.empty(nb, Hkv, bs, d, dtype=BF16, device="cuda")
+    groups, Hq = one(300, [5, 140, 40], 2), 8
+    s = prefix_case(rng, groups, Hq, Hkv, d, bs)
+    used = torch.unique(s["table"][(s["table"] >= 0) & (s["table"] < s["k"].shape[0])]).long()
+    to = torch.arange(nb - 1, -1, -1, device="cuda")[:s["k"].shape[0]].clone()
+    to[::3] = torch.arange(s["k"].shape[0], device="cuda")[::3]  # some of them in front
+    big = s["table"].clone()
+    inside = (big >= 0) & (big < s["k"].shape[0])
+    big[inside] = to[big[inside].long()].to(I32)
+    want = s["out"].clone()
+    prefix_call(s, out=want, lse=None)
+    # (keys and values in one tensor: a cache of one is enough to pass the limit)
+    cache[to[used]] = s["k"][used]
+    same = want.clone()
+    prefix_call(s, v=s["k"], out=want, lse=None)
+    prefix_call(s, k=cache, v=cache, table=big, out=same, lse=None)
+    assert torch.equal(want.view(torch.int16), same.view(torch.int16)) and int(s["err"]) == 0
+
+
+def test_prefix_attention_graphs_that_share_a_workspace():
+    rng = np.random.default_rng(33)
+    cases = [prefix_case(rng, g, 8, 2, 128, 16) for g in (one(300, [5, 1, 40]), one(64, [200, 3] * 5, 2))]
+    work = torch.empty(max(c["work"].numel() for c in cases), dtype=U8, device="cuda")
+    graphs, want = [], []
+    for c in cases:
+        prefix_call(c)
+        want.append(c["out"].clone())
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            prefix_call(c, work=work)
+    for c in cases:
+        c["out"].fill_(7.0)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(c["out"], w) for c, w in zip(cases, want))
+
+
+def test_arguments_that_are_refused():
+    x = torch.zeros(4, 64, device="cuda")
+    row = torch.zeros(1, 4, device="cuda")
+    ids = torch.zeros(1, 4, dtype=I32, device="cuda")
+    for change in (dict(logits=x.half()), dict(logits=x.cpu()), dict(logits=x.t()), dict(scores=row.double()),
+                   dict(scores=torch.zeros(1, 3, device="cuda")), dict(parents=ids.long()), dict(tokens=ids[:, :3]),
+                   dict(out_scores=torch.zeros(4, 1, device="cuda")), dict(finished=ids), dict(error_word=row)):
+        a = dict(logits=x, scores=row, out_scores=row.clone(), parents=ids, tokens=ids.clone(), end_token=1, finished=None,
+                 out_finished=None, error_word=None)
+        with pytest.raises(ValueError):
+            pka.pka_beam_select(**dict(a, **change))
+    caches = [torch.zeros(4, 2, 16, device="cuda") for _ in range(2)]
+    pka.pka_copy_pages([], ids[0], ids[0].clone())  # (nothing to copy)
+    for bad in ([caches[0], caches[1][:, :1]], [caches[0].cpu()], [caches[0].transpose(1, 2)]):
+        with pytest.raises(ValueError):
+            pka.pka_copy_pages(bad, ids[0], ids[0].clone())
+    with pytest.raises(ValueError):
+        pka.pka_copy_pages(caches, ids[0], ids[0, :2].clone())
+    with pytest.raises(ValueError):
+        pka.pka_copy_pages(caches, ids[0].long(), ids[0].long())
