@@ -19,7 +19,7 @@
 // and a second kernel joins each token's.
 //
 // Per CTA, 12 warps: K and V producers (TMA boxes of pages through the block
-// table), two MMA-issuing threads, two softmax warpgroups ("lanes" 0 and 1, one
+// table), two MMA-issuing warps, two softmax warpgroups ("lanes" 0 and 1, one
 // thread per row). With two row tiles in a unit, lane k has row tile k and every
 // key tile serves both; with one, the lanes take alternate key tiles of the same
 // rows, so that one's exponentials overlap the other's products, and leave two
@@ -42,7 +42,6 @@ namespace {
 
 constexpr int kKeys = 128;  // keys of a key tile
 constexpr int kPieces = 256;  // pieces of a list
-constexpr int kLongPiece = 4;  // key tiles from which a row's softmax is unrolled
 constexpr int kMaxSegs = 2 * kMaxRequests;
 constexpr int kChunks = kMaxSegs / 32;  // warp-sized runs of segments
 // Costs on the line: a key tile for one row tile, for two, and what a unit takes besides
@@ -154,7 +153,7 @@ struct PxCfg {
     static constexpr int kChunkBytes = 128 * 128;    // 128 rows x 128 B
     static constexpr int kTileBytes = kChunk * kChunkBytes;
     static constexpr int kCodeBytes = kKeys * D;     // a key tile in 8 bits
-    static constexpr int kStagesK = kFp8 ? 3 : 2, kStageK = kFp8 ? kCodeBytes : kTileBytes;
+    static constexpr int kStagesK = 2, kStageK = kFp8 ? kCodeBytes : kTileBytes;
     static constexpr int kStagesV = 2;               // of V in 16 bits
     static constexpr int kStagesCode = kFp8 ? 2 : 0;  // of V's codes
     static constexpr int kOffQ = 0;
@@ -443,6 +442,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
         // have: a warp that took its own back early would leave the softmax lanes waiting.
 
         if (warp < 4) {
+            // (the issuing warps stay whole and one elected lane issues: from a branch of one lane 24
+            // groups of 8 beams took 118 us, not 110)
             setmaxnreg_dec<C::kRegsIssue>();
             __syncthreads();
             if (warp == 0 || warp == 2) {
@@ -557,30 +558,30 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 #pragma unroll 1
                 for (uint32_t back = 1; !kFp8 && which == 0 && back <= C::kRowTiles && back <= q_it; ++back)
                     mbar_wait_warp(&q_full[(q_it - back) % C::kRowTiles], ((q_it - back) / C::kRowTiles) & 1, p.err);
-            } else if (lane == 0 && warp == 1) {
+            } else if (warp == 1) {
                 // -------------------------------------------------------- S_k = Q K^T
                 constexpr uint32_t idesc = kFp8 ? umma_idesc_f8(128, 128) : umma_idesc_bf16(128, 128, 0, 0);
                 const uint32_t q_s = sm_base + C::kOffQ, k_s = sm_base + C::kOffK;
                 bool ok = true;
 #pragma unroll 1
-                for (int i = 0; i < count && ok && !s_abort; ++i) {
+                for (int i = 0; i < count && ok && !warp_flag(s_abort); ++i) {
                     const int nkt = pieces[i].nkt;
                     const bool two = !kFp8 && pieces[i].ntok > p.tpt;
                     const uint32_t q0 = q_it, q1 = q_it + (two ? 1 : 0);
                     q_it = q1 + 1;
-                    if (!mbar_wait(&q_full[q0 % C::kRowTiles], (q0 / C::kRowTiles) & 1, p.err) ||
-                        (two && !mbar_wait(&q_full[q1 % C::kRowTiles], (q1 / C::kRowTiles) & 1, p.err))) {
+                    if (!mbar_wait_warp(&q_full[q0 % C::kRowTiles], (q0 / C::kRowTiles) & 1, p.err) ||
+                        (two && !mbar_wait_warp(&q_full[q1 % C::kRowTiles], (q1 / C::kRowTiles) & 1, p.err))) {
                         ok = false;
                         break;
                     }
 #pragma unroll 1
                     for (int t = 0; t < nkt; ++t, ++kv_it) {
                         const int st = (int)(kv_it % C::kStagesK), only = (int)(kv_it & 1);
-                        if (!mbar_wait(&k_full[st], (kv_it / C::kStagesK) & 1, p.err)) { ok = false; break; }
+                        if (!mbar_wait_warp(&k_full[st], (kv_it / C::kStagesK) & 1, p.err)) { ok = false; break; }
 #pragma unroll 1
                         for (int k = two ? 0 : only; k < (two ? 2 : only + 1); ++k) {
                             const uint32_t done = k ? nl1 : nl0;
-                            if (done > 0 && !mbar_wait(&pv_done[k], (done - 1) & 1, p.err)) { ok = false; break; }
+                            if (done > 0 && !mbar_wait_warp(&pv_done[k], (done - 1) & 1, p.err)) { ok = false; break; }
                             tc_fence_after();
                             const uint32_t qa = q_s + (k == 1 ? q1 : q0) % C::kRowTiles * C::kTileBytes;
                             const uint64_t a_desc = umma_desc_sw128(qa, 16, 1024), b_desc = umma_desc_sw128(k_s + st * C::kStageK, 16, 1024);
@@ -589,81 +590,81 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                             if constexpr (kFp8) {  // the rows' upper and lower halves (the second tile) times the codes
 #pragma unroll
                                 for (int ks = 0; ks < 2 * (D / 32); ++ks)
-                                    umma_f8(d, a_desc + ((ks >= D / 32 ? C::kCodeBytes : 0) + ks % (D / 32) * 32) / 16,
+                                    umma_f8_w(d, a_desc + ((ks >= D / 32 ? C::kCodeBytes : 0) + ks % (D / 32) * 32) / 16,
                                             b_desc + ks % (D / 32) * 32 / 16, idesc, ks > 0 ? 1u : 0u);
                             } else {
 #pragma unroll
                                 for (int ks = 0; ks < D / 16; ++ks) {
                                     const uint32_t off = (ks >> 2) * C::kChunkBytes + (ks & 3) * 32;
-                                    umma_bf16(d, a_desc + off / 16, b_desc + off / 16, idesc, ks > 0 ? 1u : 0u);
+                                    umma_bf16_w(d, a_desc + off / 16, b_desc + off / 16, idesc, ks > 0 ? 1u : 0u);
                                 }
                             }
-                            umma_commit(&s_full[k]);
+                            umma_commit_w(&s_full[k]);
                             if (k) ++nl1;
                             else ++nl0;
                             if (k == 0 && t > 0) s_next0 = (int)kv_it;
                         }
                         if (!ok) break;
-                        umma_commit(&k_empty[st]);
+                        umma_commit_w(&k_empty[st]);
                         if (t == nkt - 1) {
-                            umma_commit(&q_empty[q0 % C::kRowTiles]);
-                            if (two) umma_commit(&q_empty[q1 % C::kRowTiles]);
+                            umma_commit_w(&q_empty[q0 % C::kRowTiles]);
+                            if (two) umma_commit_w(&q_empty[q1 % C::kRowTiles]);
                         }
                     }
                     if (ok) s_next0 = (int)kv_it;  // nothing of lane 0 follows in this unit
                 }
                 if (!ok) s_abort = 1;
-                if (nl0 > 0) mbar_wait(&s_full[0], (nl0 - 1) & 1, p.err);
-                if (nl1 > 0) mbar_wait(&s_full[1], (nl1 - 1) & 1, p.err);
-            } else if (lane == 0 && warp == 3) {
+                if (nl0 > 0) mbar_wait_warp(&s_full[0], (nl0 - 1) & 1, p.err);
+                if (nl1 > 0) mbar_wait_warp(&s_full[1], (nl1 - 1) & 1, p.err);
+            } else if (warp == 3) {
                 // -------------------------------------------------------- O_k += P_k V
                 constexpr uint32_t idesc = kFp8 ? umma_idesc_f16(128, D, 0, 1) : umma_idesc_bf16(128, D, 0, 1);
                 const uint32_t v_s = sm_base + C::kOffV;
                 bool ok = true;
 #pragma unroll 1
-                for (int i = 0; i < count && ok && !s_abort; ++i) {
+                for (int i = 0; i < count && ok && !warp_flag(s_abort); ++i) {
                     const int nkt = pieces[i].nkt;
                     const bool two = !kFp8 && pieces[i].ntok > p.tpt;
 #pragma unroll 1
                     for (int t = 0; t < nkt; ++t, ++kv_it) {
                         const int st = kv_it & 1;
-                        if (!mbar_wait(&v_full[st], (kv_it >> 1) & 1, p.err)) { ok = false; break; }
+                        if (!mbar_wait_warp(&v_full[st], (kv_it >> 1) & 1, p.err)) { ok = false; break; }
 #pragma unroll 1
                         for (int k = two ? 0 : st; k < (two ? 2 : st + 1); ++k) {
                             const bool first = two ? t == 0 : t < 2;
                             const uint32_t done = k ? nl1 : nl0, units = k ? uo1 : uo0;
-                            if (two && k == 1 && !wait_counter(s_next0, (int)kv_it + 1, p.err)) { ok = false; break; }
+                            if (two && k == 1 && !__all_sync(0xffffffffu, wait_counter(s_next0, (int)kv_it + 1, p.err))) { ok = false; break; }
                             const uint64_t b_desc = umma_desc_sw128(v_s + st * C::kTileBytes, C::kChunkBytes, 1024);
 #pragma unroll 1
                             for (int hh = 0; hh < 2 && ok; ++hh) {
-                                if (!mbar_wait((hh ? p_full : p_half) + k, done & 1, p.err)) { ok = false; break; }
+                                if (!mbar_wait_warp((hh ? p_full : p_half) + k, done & 1, p.err)) { ok = false; break; }
                                 // a unit's first product overwrites O_k: the unit before must have been read
-                                if (hh == 0 && first && units > 0 && !mbar_wait(&o_free[k], (units - 1) & 1, p.err)) {
+                                if (hh == 0 && first && units > 0 && !mbar_wait_warp(&o_free[k], (units - 1) & 1, p.err)) {
                                     ok = false;
                                     break;
                                 }
                                 tc_fence_after();
 #pragma unroll
                                 for (int kq = 0; kq < kKeys / 32; ++kq)
-                                    umma_bf16_ts(tbase + C::kColO + k * D, tbase + C::kColS + k * 128 + (hh * (kKeys / 32) + kq) * 8,
+                                    umma_bf16_ts_w(tbase + C::kColO + k * D, tbase + C::kColS + k * 128 + (hh * (kKeys / 32) + kq) * 8,
                                                  b_desc + (hh * (kKeys / 32) + kq) * (2048 / 16), idesc,
                                                  (!first || hh > 0 || kq > 0) ? 1u : 0u);
                             }
                             if (!ok) break;
-                            umma_commit(&pv_done[k]);
+                            umma_commit_w(&pv_done[k]);
                             if (k) ++nl1;
                             else ++nl0;
                         }
                         if (!ok) break;
-                        umma_commit(&v_empty[st]);
+                        umma_commit_w(&v_empty[st]);
                     }
                     const int only = two || nkt > 1 ? -1 : (int)((kv_it - 1) & 1);  // the one lane that had a key tile
                     if (only != 1) ++uo0;
                     if (only != 0) ++uo1;
                 }
                 if (!ok) s_abort = 1;
-                if (nl0 > 0) mbar_wait(&pv_done[0], (nl0 - 1) & 1, p.err);
-                if (nl1 > 0) mbar_wait(&pv_done[1], (nl1 - 1) & 1, p.err);
+                if (nl0 > 0) mbar_wait_warp(&pv_done[0], (nl0 - 1) & 1, p.err);
+                if (nl1 > 0) mbar_wait_warp(&pv_done[1], (nl1 - 1) & 1, p.err);
             }
             __syncwarp();
             setmaxnreg_inc<C::kRegsLaunch>();
@@ -930,7 +931,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     if (idle) {
                         early = !edge;  // (value rows outside the segment's keys are zeroed by all warps)
                         if (early) signal_half();
-                    } else if (U.nkt >= kLongPiece && !edge) {
+                    } else if (!edge) {
                         if constexpr (!kFp8) {  // the whole row in registers
                             uint32_t r0[64], r1[64];
                             load_half(r0, 0);
@@ -963,12 +964,11 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                             }
                         }
                     } else {
-                        // twice over the row, 32 scores at a time in one loop body: few registers and, above
-                        // all, few instructions: in a share of many short units a row unrolled took 3.5 us
-                        // for the fetch of its code (0.9 us where it stays at hand, as in long pieces), this
-                        // one takes 2 us. Chunks that no row of
-                        // the warp sees are left out, and only those that not every row sees in full are
-                        // masked.
+                        // twice over the row, 32 scores at a time in one loop body: few registers and few
+                        // instructions, which edge tiles wait for more than for anything else (2
+                        // us; unrolled as above 3.5, while all tiles this way cost 24 groups of 8
+                        // beams 124 us, not 110). Chunks that no row of the warp sees are left out, and
+                        // only those that not every row sees in full are masked.
                         const int vlo = U.c0 - kb, vhi = max(vlo, c1 - kb);  // visible columns [vlo, vhi)
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 tc_fence_after();
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < (idle ? 0 : D / 32); ++c) {
                     uint32_t r[32];
                     tmem_ld32(tO + c * 32, r);
                     tmem_wait_ld();
