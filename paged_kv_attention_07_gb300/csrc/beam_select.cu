@@ -506,7 +506,7 @@ cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
     const size_t entries = (size_t)p.beams * slices * p.keep;
     const size_t smem = (5 * entries + p.beams * slices + 1) * sizeof(u64);
     auto kern = beam_select_kernel<kBf16, kVec>;
-    if (smem > 32 * 1024) {  // (the most that any call takes)
+    if (smem > 47 * 1024 - sizeof(Shared) - 1024) {  // past what every kernel may use; the most that any call takes
         const cudaError_t e = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
             (int)((size_t)(kMaxEntries * 6 + 1) * sizeof(u64)));

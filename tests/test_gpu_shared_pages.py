@@ -83,6 +83,13 @@ def test_beam_select(G, W, V, K, pad, offset, dtype):
     check_select(logits, scores, K, dev(rng.random((G, W)) < 0.3, U8), end)
 
 
+@pytest.mark.parametrize("W,K", [(10, 48), (13, 40), (20, 26), (20, 30), (17, 40), (20, 37), (26, 32), (41, 21)])
+def test_beam_select_lists_of_every_size(W, K):
+    """Lists about as large as the shared memory that needs no leave."""
+    rng = np.random.default_rng(W)
+    check_select(rows(rng, 3 * W, 2000, F32), torch.from_numpy(-rng.random((3, W)) * 9).float().cuda(), K)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("V", [40, 8192, 30001, 100000])
 def test_beam_select_ties(V, dtype):
