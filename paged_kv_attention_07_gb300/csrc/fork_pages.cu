@@ -13,9 +13,13 @@
 // a row and a prefix sum. Three barriers separate these steps, so they are one
 // cluster's work (one CTA's for a small table); the copies of the rows need no
 // barrier and go to further clusters. What bounds it is the latency of the steps:
-// a warp takes 256 columns at a time, all loads of them in flight.
+// a warp takes 256 columns at a time, all loads of them in flight. Measured: 4 rows of 125 pages 6.6 us
+// (one CTA), 512 rows of 32 to 1024 pages, half of which end, 25.9 us: counts 10, claims and
+// owners 8.5, each a scattered word per entry of 16 SMs. A kernel per step over all SMs took
+// 22.9 there, but 1 to 1.5 us more for every table up to 131072 entries.
 //
-// copy_pages_kernel: bytes.
+// copy_pages_kernel: bytes; a CTA's step is 16 KB of one page. Measured: 256 pages of 16 KB in 32 caches 45.8 us
+// (0.86 of the rate of one long copy), 2 of 32 KB in 16 caches 2.0 us.
 #include <algorithm>
 
 #include "common.cuh"

@@ -26,6 +26,13 @@
 // pieces. Tensor memory: S_k (128 columns, P_k written over it in bf16) and O_k.
 // P is rounded to bf16 for the product (the type of V, which the tensor cores ask
 // for); its sum is kept from the unrounded values in 32 bits.
+//
+// Measured, with the join: 24 groups of 8 (1000 to 8192 common tokens, 1 to 512 own, 8 kv heads of 128,
+// G = 4) 110 us, 3.7 TB/s of what has to be read; 64 requests behind 16384 tokens 50 us; 4 beams
+// behind 8192 24 us; 32 groups of 4 over an 8-bit cache 107 us, 2.4 TB/s. Full tiles take 1.2 us
+// each on an SM (5 TB/s); a request's own unit of a tile or two takes 2.5 us, bound by the chain of
+// its steps on one lane (first copies 2, S and softmax of an edge tile 2, P V 1, result 1.2) and the fetch
+// of their instructions.
 #include <float.h>
 
 #include <algorithm>
@@ -967,7 +974,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         // twice over the row, 32 scores at a time in one loop body: few registers and few
                         // instructions, which edge tiles wait for more than for anything else (2
                         // us; unrolled as above 3.5, while all tiles this way cost 24 groups of 8
-                        // beams 124 us, not 110). Chunks that no row of the warp sees are left out, and
+                        // beams 126 us, not 110). Chunks that no row of the warp sees are left out, and
                         // only those that not every row sees in full are masked.
                         const int vlo = U.c0 - kb, vhi = max(vlo, c1 - kb);  // visible columns [vlo, vhi)
 #pragma unroll 1
