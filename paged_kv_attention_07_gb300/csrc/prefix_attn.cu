@@ -456,7 +456,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             if (warp == 0 || warp == 2) {
                 // -------------------------------------------------------- producers: Q and K; V
                 const int which = warp == 0 ? 0 : 1;
-                const uint64_t pol = policy_evict_normal(), pol_q = policy_evict_last();
+                // (keys are read once, or by the few row tiles of a group at about the same time: not kept in L2, where
+                // the pieces wait for the join; kept, 24 groups of 8 beams took 109 us, not 103)
+                const uint64_t pol = policy_evict_first(), pol_q = policy_evict_last();
                 const bool tma = p.bs >= 8;
                 // of an 8-bit cache K's codes are the product's operand, V's are widened first
                 uint64_t* fulls = !which ? k_full : kFp8 ? c_full : v_full;
