@@ -691,6 +691,11 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             const int wtid = tid - 384;
             bool ok = true;
             const int part = lane & 7;
+            // A thread widens 16 codes of every 16th row; of their two 16-byte pieces the threads of a
+            // row's second 64 elements store the second one first: a quarter warp's stores use all banks.
+            const uint32_t own_row = wtid >> 3, far = part >> 2, own_code = sw128(own_row, part);
+            const uint32_t own_value[2] = {far * C::kChunkBytes + sw128(own_row, 2 * (part & 3) + far),
+                                           far * C::kChunkBytes + sw128(own_row, 2 * (part & 3) + (far ^ 1))};
             // rows r0 .. r0 + 31 of a piece's row tile, 8 lanes to a row, 16 elements to a lane
             auto load_rows = [&](const Piece& U, int r0, uint4 (&x)[2][2]) {
 #pragma unroll
@@ -787,27 +792,16 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     const uint32_t some = kSeveral && U.ntok > 1 ? (uint32_t)max(0, U.pos0 + 1 - kb) : kKeys;
                     const uint32_t from = sm_base + C::kOffCode + st * C::kCodeBytes;
                     const uint32_t to = sm_base + C::kOffV + st * C::kTileBytes;
-#pragma unroll 2
-                    for (int j = wtid; j < kKeys * 8; j += 128) {
-                        const uint32_t row = j >> 3, c = j & 7;
-                        const uint4 x = lds128(from + sw128(row, c));
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t y[8];
+#pragma unroll 4
+                    for (int j = 0; j < kKeys / 16; ++j) {  // 16 rows, whose places are 2 KB further on each
+                        uint4 x = lds128(from + own_code + j * 2048);
+                        if (own_row + 16 * j - zlo >= valid) x = make_uint4(0, 0, 0, 0);
+                        const uint32_t w[4] = {far ? x.z : x.x, far ? x.w : x.y, far ? x.x : x.z, far ? x.y : x.w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = e4m3x2_to_f16x2((w[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
-                        if (row - zlo >= valid) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = 0;
-                        }
-                        // (of its two 16-byte pieces the threads of a row's second 64 elements store the
-                        // second one first: a quarter warp's stores use all banks)
-                        const uint32_t base = to + (c >> 2) * C::kChunkBytes, p0 = 2 * (c & 3), odd = c >> 2;
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const uint32_t second = odd ^ hh;
-                            st_shared4(base + sw128(row, p0 + second), second ? y[4] : y[0], second ? y[5] : y[1],
-                                       second ? y[6] : y[2], second ? y[7] : y[3]);
-                        }
+                        for (int hh = 0; hh < 2; ++hh)
+                            st_shared4(to + own_value[hh] + j * 2048, e4m3x2_to_f16x2(w[2 * hh] & 0xffffu),
+                                       e4m3x2_to_f16x2(w[2 * hh] >> 16), e4m3x2_to_f16x2(w[2 * hh + 1] & 0xffffu),
+                                       e4m3x2_to_f16x2(w[2 * hh + 1] >> 16));
                     }
                     if (kSeveral && some < kKeys) {  // (a thread has the same places as above)
 #pragma unroll 1
