@@ -794,8 +794,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     const uint32_t to = sm_base + C::kOffV + st * C::kTileBytes;
 #pragma unroll 4
                     for (int j = 0; j < kKeys / 16; ++j) {  // 16 rows, whose places are 2 KB further on each
-                        uint4 x = lds128(from + own_code + j * 2048);
-                        if (own_row + 16 * j - zlo >= valid) x = make_uint4(0, 0, 0, 0);
+                        const uint4 x = lds128(from + own_code + j * 2048);
                         const uint32_t w[4] = {far ? x.z : x.x, far ? x.w : x.y, far ? x.x : x.z, far ? x.y : x.w};
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh)
@@ -803,7 +802,15 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                                        e4m3x2_to_f16x2(w[2 * hh] >> 16), e4m3x2_to_f16x2(w[2 * hh + 1] & 0xffffu),
                                        e4m3x2_to_f16x2(w[2 * hh + 1] >> 16));
                     }
-                    if (kSeveral && some < kKeys) {  // (a thread has the same places as above)
+                    if (valid < kKeys) {  // (a thread has the same places as above)
+#pragma unroll 1
+                        for (int j = 0; j < kKeys / 16; ++j) {
+                            if (own_row + 16 * j - zlo < valid) continue;
+                            st_shared4(to + own_value[0] + j * 2048, 0, 0, 0, 0);
+                            st_shared4(to + own_value[1] + j * 2048, 0, 0, 0, 0);
+                        }
+                    }
+                    if (kSeveral && some < kKeys) {
 #pragma unroll 1
                         for (int j = wtid; j < kKeys * 8; j += 128) {
                             const uint32_t row = j >> 3, c = j & 7;
