@@ -28,11 +28,11 @@
 // for); its sum is kept from the unrounded values in 32 bits.
 //
 // Measured, with the join: 24 groups of 8 (1000 to 8192 common tokens, 1 to 512 own, 8 kv heads of 128,
-// G = 4) 110 us, 3.7 TB/s of what has to be read; 64 requests behind 16384 tokens 50 us; 4 beams
-// behind 8192 24 us; 32 groups of 4 over an 8-bit cache 107 us, 2.4 TB/s. Full tiles take 1.2 us
-// each on an SM (5 TB/s); a request's own unit of a tile or two takes 2.5 us, bound by the chain of
-// its steps on one lane (first copies 2, S and softmax of an edge tile 2, P V 1, result 1.2) and the fetch
-// of their instructions.
+// G = 4) 104 us, 3.9 TB/s of what has to be read; 64 requests behind 16384 tokens 48 us; 4 beams
+// behind 8192 23 us; 32 groups of 4 over an 8-bit cache 92 us, 2.8 TB/s. Full tiles take 1.2 us
+// each on an SM (5 TB/s; of 8-bit codes 1.1), the common keys of those 24 groups alone 71 us. A
+// request's own unit of a tile or two takes 2 to 3 us: it leaves the stages half empty, and its steps
+// follow each other on one lane (first copies 2, S and softmax of an edge tile 2, P V 1, result 1).
 #include <float.h>
 
 #include <algorithm>
