@@ -53,8 +53,8 @@ constexpr int kMaxSegs = 2 * kMaxRequests;
 constexpr int kChunks = kMaxSegs / 32;  // warp-sized runs of segments
 // Costs on the line: a key tile for one row tile, for two, and what a unit takes besides
 // (its first copies, its end, lanes that wait for one another), as measured: 24 groups of 8
-// beams with (1, 2, 2) 119 us, (1, 2, 4) 132, (2, 3, 2) 130; over an 8-bit cache, whose tiles
-// are shorter, 32 groups of 4 with (1, 2, 2) 128 us, (1, 2, 4) 115.
+// beams with (1, 2, 2) 104 us, (1, 2, 1) 107, (1, 2, 3) 109; over an 8-bit cache, whose tiles
+// are shorter, 32 groups of 4 with (1, 2, 4) 91 us, (1, 2, 3) and (1, 2, 5) 95, (1, 2, 2) 101.
 constexpr int kCostOne = 1, kCostTwo = 2;
 
 struct Seg {
@@ -235,8 +235,8 @@ PKA_DEVICE void warp_sums(int& a, int& b) {
 }
 
 // kSeveral: requests may have more than one new token. The code that keeps a later token's
-// infinities from earlier ones costs 3 to 12 % where nothing calls for it (24 groups of 8 beams 127
-// us with it, 118 without; 8-bit 126 and 113), by its size alone.
+// infinities from earlier ones costs 2 to 7 % where nothing calls for it (24 groups of 8 beams 105.5
+// us with it, 103.7 without; 64 requests 49.8 and 48.0; 8-bit 97.5 and 91.4), by its size alone.
 template <int D, bool kFp8, bool kSeveral>
 __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     prefix_attn_kernel(const __grid_constant__ PrefixMaps maps, const PrefixParams p) {
@@ -450,14 +450,14 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 
         if (warp < 4) {
             // (the issuing warps stay whole and one elected lane issues: from a branch of one lane 24
-            // groups of 8 beams took 118 us, not 110)
+            // groups of 8 beams took 7 % longer)
             setmaxnreg_dec<C::kRegsIssue>();
             __syncthreads();
             if (warp == 0 || warp == 2) {
                 // -------------------------------------------------------- producers: Q and K; V
                 const int which = warp == 0 ? 0 : 1;
                 // (keys are read once, or by the few row tiles of a group at about the same time: not kept in L2, where
-                // the pieces wait for the join; kept, 24 groups of 8 beams took 109 us, not 103)
+                // the pieces wait for the join; kept, 24 groups of 8 beams take 109 us, not 104)
                 const uint64_t pol = policy_evict_first(), pol_q = policy_evict_last();
                 const bool tma = p.bs >= 8;
                 // of an 8-bit cache K's codes are the product's operand, V's are widened first
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 ++q_it;
             };
             // A piece's rows are split before the values of the piece in front of it are widened: its S
-            // products need not wait for those. (The other way round 32 groups of 4 samples took 103 us.)
+            // products need not wait for those (the other way round 32 groups of 4 samples took 2 % longer).
             uint4 x[2][2];
             if (count > 0) load_rows(pieces[0], 0, x);
 #pragma unroll 1
@@ -978,7 +978,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         // twice over the row, 32 scores at a time in one loop body: few registers and few
                         // instructions, which edge tiles wait for more than for anything else (2
                         // us; unrolled as above 3.5, while all tiles this way cost 24 groups of 8
-                        // beams 126 us, not 110). Chunks that no row of the warp sees are left out, and
+                        // beams 122 us, not 104). Chunks that no row of the warp sees are left out, and
                         // only those that not every row sees in full are masked.
                         const int vlo = U.c0 - kb, vhi = max(vlo, c1 - kb);  // visible columns [vlo, vhi)
 #pragma unroll 1
