@@ -80,7 +80,7 @@ typedef enum {
 #define PKA_DEVERR_INDEX 0x200          /* pka_gather_rows: a row index outside [0, src_rows); a position past the
                                            rotation table; a page list that does not ascend up to the token's page;
                                            a parent row outside the table; group_starts that do not ascend over the batch */
-#define PKA_DEVERR_LOGITS 0x400         /* pka_beam_select: a beam with a NaN or an infinite score, or a NaN or +infinity among its logits */
+#define PKA_DEVERR_LOGITS 0x400         /* pka_beam_select: a beam whose score is NaN or +infinity, or with one of them among its logits */
 
 /*
  * pka_cache_write -- write the new tokens' K and V rows into the paged cache.

@@ -766,3 +766,50 @@ def test_arguments_that_are_refused():
         pka.pka_copy_pages(caches, ids[0], ids[0, :2].clone())
     with pytest.raises(ValueError):
         pka.pka_copy_pages(caches, ids[0].long(), ids[0].long())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_beam_select_rows_far_apart(dtype):
+    """Rows whose offsets pass 32 bits in bytes and in elements."""
+    rng = np.random.default_rng(40)
+    W, V, stride = 40, 1000, 2 ** 27 - 8 if dtype == BF16 else 2 ** 26 + 4
+    store = torch.empty((W - 1) * stride + V, dtype=dtype, device="cuda")
+    view = store.as_strided((W, V), (stride, 1))
+    view.copy_(torch.from_numpy(rng.standard_normal((W, V)) * 3).to(dtype))
+    check_select(view, torch.from_numpy(-rng.random((1, W))).float().cuda(), 20)
+
+
+def test_beam_select_of_the_largest_vocabulary():
+    V = 2 ** 26
+    logits = torch.zeros(2, V, dtype=BF16, device="cuda")
+    logits[0, V - 1], logits[0, 12345], logits[1, V - 2], logits[1, 0] = 9, 8, 10, 8
+    s = select_case(logits, torch.tensor([[0.0, -1.5]], device="cuda"), 5)
+    # of equal scores the lower beam's; of a row's equal logits the lower tokens
+    assert s["parents"].tolist() == [[0, 1, 0, 1, 0]] and s["tokens"].tolist() == [[V - 1, V - 2, 12345, 0, 0]]
+    lse = [math.log(V - 2 + sum(math.exp(x) for x in xs)) for xs in ((9, 8), (10, 8))]
+    want = [9 - lse[0], 8.5 - lse[1], 8 - lse[0], 6.5 - lse[1], -lse[0]]
+    assert np.abs(f64(s["scores"])[0] - want).max() <= 2.0 ** -20 + 2.0 ** -24 * 20 and int(s["err"]) == 0
+
+
+def test_calls_without_an_error_word():
+    rng = np.random.default_rng(42)
+    s = prefix_case(rng, one(40, [20, 3]), 8, 2, 64, 16)
+    prefix_call(s)
+    want = s["out"].clone()
+    prefix_call(s, err=None)
+    assert torch.equal(s["out"], want)
+    bad = s["table"].clone()
+    bad[0, 0] = -1  # (set nowhere, read nowhere)
+    prefix_call(s, table=bad, err=None)
+    prefix_call(s, prefix=dev([50]), err=None)  # refused
+    x = torch.full((1, 8), math.nan, device="cuda")
+    out = torch.empty(1, 1, device="cuda")
+    ids = dev([[7]]), dev([[7]])
+    pka.pka_beam_select(x, torch.zeros(1, 1, device="cuda"), out, *ids)
+    assert out.tolist() == [[-math.inf]] and ids[0].tolist() == [[-1]]
+    cache = torch.zeros(4, 16, device="cuda")
+    pka.pka_copy_pages([cache], dev([9]), dev([0]))
+    args = dev([0]), dev([5]), dev([[0]]), 4, dev([0] * 4), dev([0, 1]), dev([1]), dev([7]), dev([7]), dev([[7]]), dev([7]), dev([7])
+    pka.pka_fork_pages(*args)  # too long for the table: refused
+    assert args[7].tolist() == [1] and args[8].tolist() == [0] and args[10].tolist() == [-1]
+    torch.cuda.synchronize()
