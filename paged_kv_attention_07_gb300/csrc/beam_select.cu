@@ -48,6 +48,8 @@ constexpr int kEpochs = 16;   // stretches of a lane's share
 constexpr int kResident = 2;  // CTAs of an SM (of 4, with half the registers, 64 x 4 beams took 29 us, not 23)
 constexpr int kMaxCluster = 16;
 constexpr int kMaxEntries = 4096;  // of all parts' lists of a group
+constexpr int kDirect = 96;        // of them that are compared with each other as they are
+static_assert(kThreads == 256, "a bin per thread");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kMinusInf = 0x007fffffu;  // order_of(-infinity)
 constexpr unsigned long long kNone = ((unsigned long long)kMinusInf << 32) | 0xffffffffu;  // below every candidate
@@ -76,24 +78,42 @@ PKA_DEVICE void store_first64(u64* p, u64 v) {
                  : "memory");
 }
 
-// A warp's tile: kPer elements per lane. With 16-byte loads a lane has runs of kRun
-// elements, else neighbours lie in neighbouring lanes.
+// A warp's tile: kPer elements per lane. With 16-byte loads a lane has runs of kRun elements,
+// else neighbouring elements, of bf16 pairs, lie in neighbouring lanes, wherever a row begins:
+// equal rows are added up alike. Pairs of a row at an odd element are put together from the halves of
+// two words, the second one the next lane's (element by element 9 rows of 166763 took
+// 24.5 us, aligned ones 15).
 template <bool kBf16, bool kVec>
 struct Tile {
     static constexpr int kRun = kBf16 ? 8 : 4, kPer = kLoads * kRun, kSize = 32 * kPer;
     static_assert(kPer <= 32, "a lane's hits are the bits of a word");
     uint32_t w[kLoads * 4];  // two bf16 or one float each
+    uint32_t last;           // of words not put together yet: the one behind the last lane's
+    bool halves = false;     // they are not
     PKA_DEVICE static int place(int e) {
         const int lane = threadIdx.x & 31;
-        return kVec ? (e / kRun * 32 + lane) * kRun + e % kRun : e * 32 + lane;
+        return kVec ? (e / kRun * 32 + lane) * kRun + e % kRun : kBf16 ? (e / 2 * 32 + lane) * 2 + e % 2 : e * 32 + lane;
     }
     PKA_DEVICE float operator[](int e) const {
         if constexpr (!kBf16) return __uint_as_float(w[e]);
         else return e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
     }
-    // Elements from `at` of the row on; -infinity from element n of the tile on.
-    PKA_DEVICE void load(const void* row, int at, int n) {
+    // Elements from `at` of the row on; -infinity from element n of the tile on. `front`: the row's
+    // element in front of them may be read.
+    PKA_DEVICE void load(const void* row, int at, int n, bool front) {
         const uint32_t none = kBf16 ? 0xff80ff80u : 0xff800000u;
+        if constexpr (kBf16 && !kVec) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(row) + 2 * (int64_t)at;
+            halves = p % 4 != 0;
+            if (halves ? front && n > kSize : n >= kSize) {
+                const uint32_t* from = reinterpret_cast<const uint32_t*>(p - p % 4) + (threadIdx.x & 31);
+#pragma unroll
+                for (int j = 0; j < kPer / 2; ++j) w[j] = __ldcs(from + 32 * j);
+                if (halves && (threadIdx.x & 31) == 31) last = __ldcs(from + 16 * kPer - 31);
+                return;
+            }
+            halves = false;
+        }
         if (kVec && n >= kSize) {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
@@ -119,6 +139,17 @@ struct Tile {
             }
             w[kBf16 ? e / 2 : e] = x;
         }
+    }
+    // Puts the pairs together (whole warps).
+    PKA_DEVICE void settle() {
+        if (kVec || !kBf16 || !halves) return;
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) {
+            const uint32_t after = __shfl_sync(0xffffffffu, lane == 0 && j + 1 < kPer / 2 ? w[j + 1 < kPer / 2 ? j + 1 : j] : w[j], (lane + 1) & 31);
+            w[j] = __funnelshift_r(w[j], lane == 31 && j + 1 == kPer / 2 ? last : after, 16);
+        }
+        halves = false;
     }
 };
 
@@ -188,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, kResident) beam_select_kernel(const 
     __shared__ double s_lse[kMaxBeams];
     __shared__ float s_score[kMaxBeams];
     __shared__ int s_state[kMaxBeams];
-    __shared__ int s_found;
+    __shared__ int s_found, s_bin, s_need;
     grid_dep_launch();
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -225,11 +256,13 @@ __global__ void __launch_bounds__(kThreads, kResident) beam_select_kernel(const 
         float m = -INFINITY, s = 0.f, top = -INFINITY;
         T x, next;
         int t = warp * T::kSize;
-        if (t < n) next.load(logits, t, n - t);
+        const bool inside = at > 0;  // (there is an element in front of the part)
+        if (t < n) next.load(logits, t, n - t, inside || t > 0);
         for (int r = 0, in = 0, epoch = 0; r < rounds; ++r, t += kRound) {
             if (t < n) {
                 x = next;
-                if (t + kRound < n) next.load(logits, t + kRound, n - t - kRound);
+                x.settle();
+                if (t + kRound < n) next.load(logits, t + kRound, n - t - kRound, true);
                 float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < T::kPer; e += 2) tops[e / 2 % 4] = fmax3f(tops[e / 2 % 4], x[e], x[e + 1]);
@@ -328,8 +361,9 @@ __global__ void __launch_bounds__(kThreads, kResident) beam_select_kernel(const 
             t = epoch * stretch * kRound + warp * T::kSize;
             for (int r = 0; r < stretch && t < n; ++r, t += kRound) {
                 uint32_t hits = 0;  // of this lane's elements
-                if (again) {
-                    x.load(logits, t, n - t);
+                if (again || !kVec) {
+                    x.load(logits, t, n - t, inside || t > 0);
+                    x.settle();
 #pragma unroll
                     for (int e = 0; e < T::kPer; ++e) hits |= x[e] >= reach ? 1u << e : 0u;
                 }
@@ -411,7 +445,6 @@ __global__ void __launch_bounds__(kThreads, kResident) beam_select_kernel(const 
         // the joined lists: 64-bit scores, and what decides between equal ones
         __syncthreads();
         const int entries = parts * keep;
-        const bool all = entries <= kThreads;
         for (int j = tid; j < entries; j += kThreads) {
             const int i = j / keep, k = j - i * keep, b = i / p.slices;
             const u64 key = lists[j];
@@ -428,42 +461,57 @@ __global__ void __launch_bounds__(kThreads, kResident) beam_select_kernel(const 
             }
             if (token >= 0)
                 l = ((u64)(kMaxBeams - 1 - b) << 58) | ((u64)order << 26) | (u64)(kMaxVocab - 1 - token);
-            if (!all) {
-                hi[j] = h;
-                lo[j] = l;
-            } else if (token >= 0) {
-                const int to = atomicAdd(&s_found, 1);
-                best[2 * to] = h;
-                best[2 * to + 1] = l;
+            hi[j] = h;
+            lo[j] = l;
+        }
+        // A bound that the best `keep` reach and few others: the keep-th of the scores' upper 32 bits, found
+        // eight bits at a time by counts of their values. (To compare all with all took 7 us of 256
+        // entries, 20 of 512.)
+        uint32_t least = 1;
+        if (entries > kDirect) {
+            uint32_t* bins = &sh.best[0][0];
+            int need = keep;
+            least = 0;
+#pragma unroll 1
+            for (int shift = 24; shift >= 0; shift -= 8) {
+                bins[tid] = 0;
+                __syncthreads();
+                if (tid == 0) s_bin = -1;
+                for (int j = tid; j < entries; j += kThreads) {
+                    const uint32_t o = (uint32_t)(hi[j] >> 32);
+                    if (o && (shift == 24 || o >> (shift + 8) == least >> (shift + 8))) atomicAdd(&bins[(o >> shift) & 255], 1);
+                }
+                __syncthreads();
+                // from the largest value on
+                const int mine = (int)bins[255 - tid];
+                int sum = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                if (lane == 31) sh.count[warp] = sum;
+                __syncthreads();
+                for (int w = 0; w < warp; ++w) sum += sh.count[w];
+                if (sum >= need && sum - mine < need) {
+                    s_bin = 255 - tid;
+                    s_need = need - (sum - mine);
+                }
+                __syncthreads();
+                if (s_bin < 0) break;  // (only of the first eight: there are no more than `keep`)
+                least |= (uint32_t)s_bin << shift;
+                need = s_need;
             }
+            least = max(least, 1u);
         }
         __syncthreads();
-        if (!all) {
-            // a threshold that at least `keep` entries reach: the keep-th of the lists' first `deep`
-            const int deep = (keep + parts - 1) / parts, heads = parts * deep;
-            for (int j = tid; j < heads; j += kThreads) {
-                const int at = j / deep * keep + j % deep;
-                const u64 h = hi[at], l = lo[at];
-                int above = 0;
-                for (int o = 0; o < heads; ++o) {
-                    const int a = o / deep * keep + o % deep;
-                    above += hi[a] > h || (hi[a] == h && (lo[a] > l || (lo[a] == l && o < j)));
-                }
-                if (above == keep - 1) {
-                    sh.keys[0][0] = h;
-                    sh.keys[0][1] = l;
-                }
-            }
-            __syncthreads();
-            const u64 th = sh.keys[0][0], tl = sh.keys[0][1];
-            for (int j = tid; j < entries; j += kThreads) {
-                if (!hi[j] || hi[j] < th || (hi[j] == th && lo[j] < tl)) continue;
-                const int to = atomicAdd(&s_found, 1);
-                best[2 * to] = hi[j];
-                best[2 * to + 1] = lo[j];
-            }
-            __syncthreads();
+        for (int j = tid; j < entries; j += kThreads) {
+            if ((uint32_t)(hi[j] >> 32) < least) continue;
+            const int to = atomicAdd(&s_found, 1);
+            best[2 * to] = hi[j];
+            best[2 * to + 1] = lo[j];
         }
+        __syncthreads();
         const int found = s_found;
         const int64_t base = (int64_t)group * keep;
         for (int j = tid; j < found; j += kThreads) {
