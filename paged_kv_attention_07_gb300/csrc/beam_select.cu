@@ -548,7 +548,11 @@ cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
     while (p.beams * (slices + 1) <= kMaxCluster && (int64_t)p.groups * p.beams * (slices + 1) * 2 <= 3 * num_sms &&
            p.beams * (slices + 1) * p.keep <= kMaxEntries && p.vocab > slices * kWarps * Tile<kBf16, kVec>::kSize)
         ++slices;
-    const int ncta = std::min(p.beams * slices, kMaxCluster);
+    // Clusters of more than 8 CTAs leave many SMs of a GPC over: where not all fit at once, half as many CTAs
+    // with twice the parts are faster (36 x 16 beams of 28464 25.5 us, not 36.4). Smaller ones are not halved:
+    // 160 x 8 beams of 18432 take 43 us, in clusters of 4 49.
+    int ncta = std::min(p.beams * slices, kMaxCluster);
+    if (ncta > 8 && (int64_t)p.groups * ncta > 2 * num_sms) ncta = (ncta + 1) / 2;
     p.slices = slices;
     p.slice_len = ((p.vocab + slices - 1) / slices + 7) & ~7;  // (16-byte pieces stay whole)
     const size_t entries = (size_t)p.beams * slices * p.keep;

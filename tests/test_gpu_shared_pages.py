@@ -83,6 +83,14 @@ def test_beam_select(G, W, V, K, pad, offset, dtype):
     check_select(logits, scores, K, dev(rng.random((G, W)) < 0.3, U8), end)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("G,W,V,K", [(30, 16, 900, 16), (25, 13, 5001, 7), (160, 8, 1029, 8), (9, 40, 3001, 40), (200, 3, 2500, 3)])
+def test_beam_select_many_groups(G, W, V, K, dtype):
+    """More clusters than run at once, parts that follow one another in a CTA, odd rows."""
+    rng = np.random.default_rng(G)
+    check_select(rows(rng, G * W, V, dtype, offset=int(dtype == BF16)), torch.from_numpy(-rng.random((G, W)) * 9).float().cuda(), K)
+
+
 @pytest.mark.parametrize("W,K", [(10, 48), (13, 40), (20, 26), (20, 30), (17, 40), (20, 37), (26, 32), (41, 21)])
 def test_beam_select_lists_of_every_size(W, K):
     """Lists about as large as the shared memory that needs no leave."""
