@@ -16,7 +16,7 @@
 // a warp takes 256 columns at a time, all loads of them in flight. Measured: 4 rows of 125 pages 6.6 us
 // (one CTA), 512 rows of 32 to 1024 pages, half of which end, 25.9 us: counts 10, claims and
 // owners 8.5, each a scattered word per entry of 16 SMs. A kernel per step over all SMs took
-// 22.9 there, but 1 to 1.5 us more for every table up to 131072 entries.
+// 22.9 there, but 1 to 1.5 us more for every table up to 131072 entries. 376 rows of 4 pages take 10.7.
 //
 // copy_pages_kernel: bytes; a CTA's step is 16 KB of one page. Measured: 256 pages of 16 KB in 32 caches 45.8 us
 // (0.86 of the rate of one long copy), 2 of 32 KB in 16 caches 2.0 us.
@@ -355,9 +355,11 @@ static cudaError_t go(const ForkPagesParams& p, int cluster, int clusters, cudaS
 }
 
 cudaError_t launch_fork_pages(const ForkPagesParams& p, int num_sms, cudaStream_t stream) {
-    // By what the table may hold: one small CTA, one cluster, or further ones for the copies.
-    const int64_t entries = (int64_t)std::max(p.num_rows, p.num_rows_out) * p.max_blocks;
-    if (entries <= 4096) return go<kFpFew>(p, 1, 1, stream);
+    // By what the table may hold: one small CTA of 8 warps, one cluster of 512, or further ones for the copies
+    // (8 rows of 3 pages 7.6 us with the first, 8.5 with the second; 32 rows 12.5 and 9.3, 376 rows 97 and 10.7).
+    const int rows = std::max(p.num_rows, p.num_rows_out);
+    const int64_t entries = (int64_t)rows * p.max_blocks;
+    if (rows <= 16 && entries <= 4096) return go<kFpFew>(p, 1, 1, stream);
     const int64_t more = (int64_t)p.num_rows_out * p.max_blocks / (kFpCluster * kFpMany * kFpSpan);
     return go<kFpMany>(p, kFpCluster, 1 + (int)std::min<int64_t>(more, num_sms / kFpCluster - 1), stream);
 }
