@@ -26,7 +26,7 @@
 // Candidates of different rows are compared by their 64-bit scores.
 //
 // Measured: 4 rows of 32000 bf16 logits 8.7 us; 64 groups of 4 rows of 131072 23.6 us (2.8 TB/s; at the
-// rate of a copy the 67 MB take 9.9); 17 groups of 5 rows of 50001 float32 logits 12.0 us. A
+// rate of a copy the 67 MB take 9.9); 17 groups of 5 rows of 50001 float32 logits 11.5 us. A
 // launch and the phases behind the stream (limit, second reading, lists, ranks: each a
 // few hundred instructions fetched for the first time) take about 7 us of each; the stream
 // of 256 rows is bound by the busiest SMs, which have two rows where the mean is 1.7.
