@@ -179,9 +179,15 @@ __global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkPagesPar
             int page[kFpSpan];
 #pragma unroll
             for (int j = 0; j < kFpSpan; ++j) page[j] = c0 + 32 * j + lane < end ? __ldg(from + c0 + 32 * j + lane) : 0;
+            // (ids of rows that go on as one are looked at here only)
+            bool bad = false;
 #pragma unroll
-            for (int j = 0; j < kFpSpan; ++j)
-                if (c0 + 32 * j + lane < end) to[c0 + 32 * j + lane] = page[j];
+            for (int j = 0; j < kFpSpan; ++j) {
+                if (c0 + 32 * j + lane >= end) continue;
+                to[c0 + 32 * j + lane] = page[j];
+                bad |= page[j] >= p.num_blocks;
+            }
+            if (bad) set_error(p.err, PKA_DEVERR_BLOCK_ID);
         }
         if (copies_only) return;
     }
