@@ -369,6 +369,15 @@ PKA_DEVICE void fma2_bcast(float& d0, float& d1, float a0, float a1, float b, fl
         : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
 
+// (d0, d1) = (a0, a1) * b + (c0, c1): one packed fp32 fma.
+PKA_DEVICE void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %6};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+
 // (s0, s1) += (a0, a1): one packed fp32 add.
 PKA_DEVICE void add2(float& s0, float& s1, float a0, float a1) {
     asm("{\n\t.reg .b64 x, y;\n\t"

@@ -23,13 +23,15 @@
 // thread per row). With two row tiles in a unit, lane k has row tile k and every
 // key tile serves both; with one, the lanes take alternate key tiles of the same
 // rows, so that one's exponentials overlap the other's products, and leave two
-// pieces. Tensor memory: S_k (128 columns, P_k written over it in bf16) and O_k.
-// P is rounded to bf16 for the product (the type of V, which the tensor cores ask
-// for); its sum is kept from the unrounded values in 32 bits.
+// pieces. Tensor memory: S_k (128 columns, P_k written over it) and O_k.
+// The tensor cores ask for P in the type of V, bf16. A weight is two bf16 numbers, off by 2^-15
+// of it, and takes two products: the result's error is that of its own rounding (0.0017 against 64 bits; with
+// one number 0.0023, 24 groups of 8 beams 104 us instead of 107, 64 requests 48 and 51, 4 beams 22.9
+// and 23.2). The weights' sum is kept from the unrounded values in 32 bits.
 //
 // Measured, with the join: 24 groups of 8 (1000 to 8192 common tokens, 1 to 512 own, 8 kv heads of 128,
-// G = 4) 104 us, 3.9 TB/s of what has to be read; 64 requests behind 16384 tokens 48 us; 4 beams
-// behind 8192 23 us; 32 groups of 4 over an 8-bit cache 92 us, 2.8 TB/s. Full tiles take 1.2 us
+// G = 4) 107 us, 3.8 TB/s of what has to be read; 64 requests behind 16384 tokens 50.5 us; 4 beams
+// behind 8192 23 us; 32 groups of 4 over an 8-bit cache 91.5 us, 2.8 TB/s. Full tiles take 1.2 us
 // each on an SM (5 TB/s; of 8-bit codes 1.1), the common keys of those 24 groups alone 71 us. A
 // request's own unit of a tile or two takes 2 to 3 us: it leaves the stages half empty, and its steps
 // follow each other on one lane (first copies 2, S and softmax of an edge tile 2, P V 1, result 1).
@@ -135,6 +137,18 @@ PKA_DEVICE bool take_out(uint32_t (&w)[N]) {
         }
     }
     return any;
+}
+
+// Two weights p >= 0 as two bf16 numbers each, p cut off and the rest cut off: off by less than 2^-14 of p, to one
+// side, which the 2^-15 of p added before halves. They also keep the rest above 0 where p is (down to
+// 2^-118), so that an infinite value is not multiplied by 0.
+PKA_DEVICE void split_weights(float p0, float p1, uint32_t& high, uint32_t& rest) {
+    const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+    high = __byte_perm(b0, b1, 0x7632);
+    float d0, d1;
+    fma2(d0, d1, p0, p1, 1.f + 1.f / 32768, __uint_as_float(b0 & 0xffff0000u | 0x80000000u),
+         __uint_as_float(b1 & 0xffff0000u | 0x80000000u));
+    rest = __byte_perm(__float_as_uint(d0), __float_as_uint(d1), 0x7632);
 }
 
 struct Piece {
@@ -654,10 +668,14 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                                 }
                                 tc_fence_after();
 #pragma unroll
-                                for (int kq = 0; kq < kKeys / 32; ++kq)
-                                    umma_bf16_ts_w(tbase + C::kColO + k * D, tbase + C::kColS + k * 128 + (hh * (kKeys / 32) + kq) * 8,
-                                                 b_desc + (hh * (kKeys / 32) + kq) * (2048 / 16), idesc,
-                                                 (!first || hh > 0 || kq > 0) ? 1u : 0u);
+                                for (int kq = 0; kq < kKeys / 32; ++kq) {
+                                    const int at = hh * (kKeys / 32) + kq;  // the 16 keys
+                                    const uint32_t a = tbase + C::kColS + k * 128 + (kFp8 ? at * 8 : at / 2 * 32 + at % 2 * 8);
+                                    umma_bf16_ts_w(tbase + C::kColO + k * D, a, b_desc + at * (2048 / 16), idesc,
+                                                   (!first || hh > 0 || kq > 0) ? 1u : 0u);
+                                    if constexpr (!kFp8)
+                                        umma_bf16_ts_w(tbase + C::kColO + k * D, a + 16, b_desc + at * (2048 / 16), idesc, 1u);
+                                }
                             }
                             if (!ok) break;
                             umma_commit_w(&pv_done[k]);
@@ -895,15 +913,6 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     float mx[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) mx[j] = -INFINITY;
-                    auto load_half = [&](uint32_t (&r)[64], int h) {  // scores of keys 64 h ...
-                        tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(r));
-                        tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
-                    };
-                    auto max_half = [&](const uint32_t (&r)[64]) {
-#pragma unroll
-                        for (int j = 0; j < 64; j += 2)
-                            mx[(j >> 1) & 7] = fmax3f(mx[(j >> 1) & 7], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-                    };
                     float m_off = 0.f;
                     auto take_max = [&] {
                         const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
@@ -918,19 +927,27 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         }
                         m_off = m_used == -INFINITY ? 0.f : m_used;
                     };
-                    // P of 64 keys, in bf16 pairs over columns 32 h of S (which have been read)
-                    auto store_half = [&](const uint32_t (&r)[64], int h) {
+                    // P of 32 keys in place of their scores: the pairs of bf16 and what these leave, in all 32
+                    // columns, or pairs of f16, in 16 of columns 0 .. 63
+                    auto store32 = [&](const uint32_t (&r)[32], int at) {
                         uint32_t pk[32];
 #pragma unroll
-                        for (int j = 0; j < 64; j += 2) {
+                        for (int j = 0; j < 32; j += 2) {
                             float x0, x1;
                             fma2_bcast(x0, x1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), sl2, kUnitP - m_off);
                             const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-                            const int a = (j >> 1) & 3;
-                            add2(ls[2 * a], ls[2 * a + 1], e0, e1);
-                            pk[j / 2] = kFp8 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+                            const int q = (j >> 1) & 3;
+                            add2(ls[2 * q], ls[2 * q + 1], e0, e1);
+                            if constexpr (kFp8) pk[j / 2] = pack_f16(e0, e1);
+                            else split_weights(e0, e1, pk[j / 2], pk[16 + j / 2]);
                         }
-                        tmem_st32(tS + 32 * h, pk);
+                        if constexpr (kFp8) tmem_st16(tS + (at >> 1), *reinterpret_cast<const uint32_t(*)[16]>(pk));
+                        else tmem_st32(tS + at, pk);
+                    };
+                    auto max32 = [&](const uint32_t (&r)[32]) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            mx[(j >> 1) & 7] = fmax3f(mx[(j >> 1) & 7], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
                     };
                     bool early = false;
                     auto signal_half = [&] {  // the product over keys 0..63 may start
@@ -943,43 +960,30 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         early = !edge;  // (value rows outside the segment's keys are zeroed by all warps)
                         if (early) signal_half();
                     } else if (!edge) {
-                        if constexpr (!kFp8) {  // the whole row in registers
-                            uint32_t r0[64], r1[64];
-                            load_half(r0, 0);
-                            load_half(r1, 1);
+                        // twice over the row, 32 scores at a time (64 at a time 24 groups of 8 beams took 110 us, the whole
+                        // row in registers 123: the code is fetched anew at each change between tiles and edge tiles)
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t r[32];
+                            tmem_ld32(tS + 32 * c, r);
                             tmem_wait_ld();
-                            max_half(r0);
-                            max_half(r1);
-                            take_max();
-                            early = !__any_sync(0xffffffffu, rescale);
-                            store_half(r0, 0);
-                            if (early) signal_half();
-                            store_half(r1, 1);
-                        } else {  // twice over it in halves: these lanes have fewer registers
+                            max32(r);
+                        }
+                        take_max();
+                        early = !__any_sync(0xffffffffu, rescale);
 #pragma unroll 1
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t r[64];
-                                load_half(r, h);
-                                tmem_wait_ld();
-                                max_half(r);
-                            }
-                            take_max();
-                            early = !__any_sync(0xffffffffu, rescale);
-#pragma unroll 1
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t r[64];
-                                load_half(r, h);
-                                tmem_wait_ld();
-                                store_half(r, h);
-                                if (h == 0 && early) signal_half();
-                            }
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t r[32];
+                            tmem_ld32(tS + 32 * c, r);
+                            tmem_wait_ld();
+                            store32(r, 32 * c);
+                            if (c == 1 && early) signal_half();
                         }
                     } else {
-                        // twice over the row, 32 scores at a time in one loop body: few registers and few
-                        // instructions, which edge tiles wait for more than for anything else (2
-                        // us; unrolled as above 3.5, while all tiles this way cost 24 groups of 8
-                        // beams 122 us, not 104). Chunks that no row of the warp sees are left out, and
-                        // only those that not every row sees in full are masked.
+                        // the same in one loop body, few instructions, which edge tiles wait for more than for
+                        // anything else (all tiles this way cost 24 groups of 8 beams 123 us, not
+                        // 107). Chunks that no row of the warp sees are left out, and only those that
+                        // not every row sees in full are masked.
                         const int vlo = U.c0 - kb, vhi = max(vlo, c1 - kb);  // visible columns [vlo, vhi)
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
@@ -990,7 +994,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                                 early = !edge && !__any_sync(0xffffffffu, rescale);
                             }
                             if (!__any_sync(0xffffffffu, bits != 0)) {
-                                if (c >= 4) tmem_st16_zero(tS + (at >> 1));
+                                if (c >= 4) tmem_st16_zero(tS + (kFp8 ? at >> 1 : at));
+                                if (!kFp8 && c >= 4) tmem_st16_zero(tS + at + 16);
                                 continue;
                             }
                             uint32_t r[32];
@@ -1001,20 +1006,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                                 for (int j = 0; j < 32; ++j) r[j] = (bits >> j) & 1 ? r[j] : 0xff800000u;
                             }
                             if (c < 4) {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2)
-                                    mx[(j >> 1) & 7] = fmax3f(mx[(j >> 1) & 7], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                                max32(r);
                             } else {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    float x0, x1;
-                                    fma2_bcast(x0, x1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), sl2, kUnitP - m_off);
-                                    const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-                                    const int q = (j >> 1) & 3;
-                                    add2(ls[2 * q], ls[2 * q + 1], e0, e1);
-                                    r[j / 2] = kFp8 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
-                                }
-                                tmem_st16(tS + (at >> 1), *reinterpret_cast<const uint32_t(*)[16]>(r));
+                                store32(r, at);
                                 if (c == 5 && early) signal_half();
                             }
                         }

@@ -1,8 +1,13 @@
-"""The calls over shared pages at the borders of what they promise: bad page ids wherever they are passed on."""
+"""The calls over shared pages at the borders of what they promise: bad page ids wherever they are passed on, the error of
+attention's results, infinite values."""
+import math
+
 import numpy as np
 import pytest
+import torch
 
-from tests.test_gpu_shared_pages import E, fork_case
+from tests import shared_ref as ref
+from tests.test_gpu_shared_pages import E, SHAPES, f64, fork_case, one, prefix_call, prefix_case
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +42,46 @@ def test_fork_pages_bad_ids_of_rows_that_go_on_as_one(B, width, bs, bad):
             table[at] = -1
             ctx[at[0]] = (at[1] + 1) * bs
             assert int(fork_case(parents, ctx, table, bs, [0] * blocks, list(range(8)), 4)["err"]) == 0
+
+
+@pytest.mark.parametrize("groups,Hq,Hkv,d,bs", SHAPES)
+def test_prefix_attention_is_off_by_its_results_rounding(groups, Hq, Hkv, d, bs):
+    """That rounding: 2^-8 of the value. A score of d products in 32 bits: (d + 8) 2^-24 of the largest sum of their
+    magnitudes, exponentials and sums 2^-20, three times for weight, sum and their quotient. A weight as two bf16 numbers,
+    both cut off: less than 2^-7 of 2^-7 of it is left, to one side; 2^-15 of it added before makes that 2^-15 to either."""
+    rng = np.random.default_rng(Hq * d + bs)
+    s = prefix_case(rng, groups, Hq, Hkv, d, bs)
+    prefix_call(s)
+    (k, v), table, qsl, seq, starts, prefix = s["host"]
+    out, lse, mag, reach = ref.prefix_attention(f64(s["q"]), k, v, table, qsl, seq, starts, prefix, s["scale"])
+    delta = (d + 8) * 2.0 ** -24 * reach + 2.0 ** -20
+    limit = 2.0 ** -8 * np.abs(out) + (2.0 ** -15 + 3 * delta[..., None]) * mag * (1 + 2.0 ** -6) + 1e-30
+    worst = np.abs(f64(s["out"]) - out) / limit
+    assert int(s["err"]) == 0 and (worst <= 1).all(), (worst.max(), np.unravel_index(worst.argmax(), worst.shape))
+
+
+@pytest.mark.parametrize("d,bs", [(128, 16), (64, 8)])
+@pytest.mark.parametrize("groups", [one(0, [300, 20]), one(384, [1, 1, 200]), one(512, [40] * 40), one(129, [1]), one(256, [7, 30], 3)])
+def test_prefix_attention_infinite_values_are_infinite_results(groups, d, bs):
+    """Also where the key's weight is a power of two, the largest one, or has all its bits."""
+    rng = np.random.default_rng(d + len(groups[0][1]))
+    s = prefix_case(rng, groups, 8, 2, d, bs)
+    (k, v), table, qsl, seq, starts, prefix = s["host"]
+    reqs = [r for r in range(len(seq)) if qsl[r + 1] > qsl[r]]
+    first = min(seq[r] - (qsl[r + 1] - qsl[r]) for r in reqs)  # keys that every token sees
+    q = s["q"]
+    q[:, 1] = 0  # all weights one
+    many = len(seq) > 1
+    for r in reqs:
+        row = [table[reqs[0]][p // bs] if many and p < prefix[0] else table[r][p // bs] for p in range(first + 1)]
+        at = lambda p: (int(row[p]), slice(None), p % bs)  # noqa: E731
+        if r == reqs[0]:
+            q[qsl[r], 2] = s["k"][int(row[first // 2]), 0, first // 2 % bs] * 4  # the largest weight of its head
+        s["v"][at(first // 2)][:, 3] = math.inf
+        s["v"][at(first)][:, 4] = -math.inf
+        s["v"][at(first // 3)][:, 5] = math.inf
+        s["v"][at(first - 1 if first else 0)][:, 5] = -math.inf
+    prefix_call(s)
+    got = f64(s["out"])
+    assert int(s["err"]) == 0 and (got[..., 3] == np.inf).all() and (got[..., 4] == -np.inf).all() and np.isnan(got[..., 5]).all()
+    assert np.isfinite(np.delete(got, [3, 4, 5], -1)).all() and torch.isfinite(s["lse"]).all()
