@@ -1393,8 +1393,8 @@ pka_status pka_sparse_attn_forward_fp8(const void* q, const void* k_cache, const
 namespace {
 
 struct PrefixLayout {
-    int tpt, own0, rows_pre, rows_own;
-    size_t off_cost, off_unit, off_po_pre, off_pl_pre, off_po_own, off_pl_own, total;
+    int tpt, own0, most_pre, most_own;
+    size_t off_cost, off_row, off_po_pre, off_pl_pre, off_po_own, off_pl_own, total;
 };
 
 // Sizes that the call has a kernel for.
@@ -1409,18 +1409,23 @@ pka_status check_prefix_sizes(int num_reqs, int num_groups, int num_tokens, int 
     return PKA_OK;
 }
 
-// A piece's slot is its unit's number plus its CTA's, so there are as many as units and CTAs together.
+// Tokens of a unit: those of one row tile, or of two where a CTA's lanes have one each.
+int prefix_unit_tokens(int tpt, bool fp8) { return fp8 ? tpt : 2 * tpt; }
+
+// Each unit has room for two results of its rows, and each CTA for those of one unit more, as a unit that ends
+// in another CTA has results of both (PrefixParams). Common keys need two requests.
 PrefixLayout prefix_layout(int num_reqs, int num_groups, int num_tokens, int Hq, int Hkv, int head_dim,
                            int max_query_len, int ncta) {
     PrefixLayout L;
     const int G = Hq / Hkv;
     L.tpt = 128 / G;
     L.own0 = (num_groups + 31) / 32 * 32;
-    const auto rows = [&](int64_t tokens) { return (int)std::min<int64_t>(128, (tokens * G + 7) / 8 * 8); };
-    L.rows_pre = rows(std::max(1, num_tokens));
-    L.rows_own = rows(std::max(1, std::min(max_query_len, num_tokens)));
-    const int64_t full = num_tokens / L.tpt;  // units of one row tile, where there are most
-    const size_t slots_pre = (size_t)((full + num_groups) * Hkv + ncta), slots_own = (size_t)((full + num_reqs) * Hkv + ncta);
+    const int unit = prefix_unit_tokens(L.tpt, false), tokens = std::max(1, num_tokens);
+    L.most_pre = num_reqs > 1 ? std::min(unit, tokens) * G : 0;
+    L.most_own = std::min(std::min(unit, tokens), max_query_len) * G;
+    const size_t all = (size_t)num_tokens * Hq;
+    const size_t rows_pre = num_reqs > 1 ? 2 * (all + (size_t)ncta * L.most_pre) : 0;
+    const size_t rows_own = 2 * (all + (size_t)ncta * L.most_own);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t o = off;
@@ -1428,11 +1433,11 @@ PrefixLayout prefix_layout(int num_reqs, int num_groups, int num_tokens, int Hq,
         return o;
     };
     L.off_cost = take(sizeof(int) * ((size_t)L.own0 + num_reqs + 1));
-    L.off_unit = take(sizeof(int) * ((size_t)L.own0 + num_reqs));
-    L.off_po_pre = take(sizeof(float) * slots_pre * 2 * L.rows_pre * head_dim);
-    L.off_pl_pre = take(sizeof(float) * slots_pre * 2 * L.rows_pre);
-    L.off_po_own = take(sizeof(float) * slots_own * 2 * L.rows_own * head_dim);
-    L.off_pl_own = take(sizeof(float) * slots_own * 2 * L.rows_own);
+    L.off_row = take(sizeof(int) * ((size_t)L.own0 + num_reqs));
+    L.off_po_pre = take(sizeof(float) * rows_pre * head_dim);
+    L.off_pl_pre = take(sizeof(float) * rows_pre);
+    L.off_po_own = take(sizeof(float) * rows_own * head_dim);
+    L.off_pl_own = take(sizeof(float) * rows_own);
     L.total = off;
     return L;
 }
@@ -1486,14 +1491,14 @@ pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_ca
     p.lse = lse;
     p.err = error_word;
     p.seg_cost = reinterpret_cast<int*>(ws + L.off_cost);
-    p.seg_unit = reinterpret_cast<int*>(ws + L.off_unit);
+    p.seg_row = reinterpret_cast<int*>(ws + L.off_row);
     p.po_pre = reinterpret_cast<float*>(ws + L.off_po_pre);
     p.pl_pre = reinterpret_cast<float*>(ws + L.off_pl_pre);
     p.po_own = reinterpret_cast<float*>(ws + L.off_po_own);
     p.pl_own = reinterpret_cast<float*>(ws + L.off_pl_own);
     p.num_blocks = num_blocks;
-    p.rows_pre = L.rows_pre;
-    p.rows_own = L.rows_own;
+    p.most_pre = L.most_pre;
+    p.most_own = L.most_own;
     p.B = num_reqs;
     p.groups = num_groups;
     p.own0 = L.own0;
@@ -1503,7 +1508,7 @@ pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_ca
     p.Hkv = num_kv_heads;
     p.G = num_q_heads / num_kv_heads;
     p.tpt = L.tpt;
-    p.upt = cf.fp8 ? L.tpt : 2 * L.tpt;
+    p.upt = prefix_unit_tokens(L.tpt, cf.fp8);
     p.cost_unit = cf.fp8 ? kPrefixMaxCost : 2;
     p.bs = block_size;
     p.bs_log2 = log2_of(block_size);

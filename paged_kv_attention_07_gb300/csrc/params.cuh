@@ -274,16 +274,18 @@ struct PrefixParams {
     __nv_bfloat16* out;
     float* lse;  // or null
     int32_t* err;
-    // workspace: each segment's place on the line of costs and of units; the pieces'
-    // sums [slot][d / 4][2 * rows][4] and their log2 [slot][2 * rows], apart for common and own keys
+    // workspace: each segment's place on the line of costs, and the rows (token x query head) of
+    // the segments before it; the pieces' sums [d / 4][2 * half][4] and their log2 [2 * half], apart for common
+    // and own keys, `half` a unit's rows (or its first row tile's). Those of a unit in front of which lie r rows,
+    // by CTA c, begin at row 2 * (r + c * most): a CTA more leaves room for one unit more.
     int* seg_cost;  // [own0 + B + 1], the last the total, -1: refused
-    int* seg_unit;
+    int* seg_row;   // [own0 + B]
     float* po_pre;
     float* pl_pre;
     float* po_own;
     float* pl_own;
     int64_t num_blocks;
-    int rows_pre, rows_own;  // rows of a lane's half of a slot
+    int most_pre, most_own;  // rows of the largest unit
     int B, groups, own0, T, max_blocks, Hq, Hkv, G, bs, bs_log2, max_query, max_seq;
     int tpt, upt;  // tokens of a row tile, and of a unit (one or two)
     int cost_unit;  // see prefix_attn.cu; at most kPrefixMaxCost

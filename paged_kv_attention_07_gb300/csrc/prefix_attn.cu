@@ -158,7 +158,7 @@ struct Piece {
     int kb0, nkt;   // first key of the first tile, key tiles
     int c0, c1;     // visible keys of the segment
     int pos0;       // position of token q0 (past everything for common keys)
-    int slot;       // where its result goes; common keys: bit 31
+    int row;        // its result's first row in the workspace; common keys: bit 31
 };
 
 template <int D, bool kFp8>
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     float* row_unit = reinterpret_cast<float*>(smem + C::kOffUnit);
     Piece* pieces = reinterpret_cast<Piece*>(smem + C::kOffPiece);
     int* run_cost = reinterpret_cast<int*>(smem + C::kOffSums);  // before each run of 32 segments
-    int* run_units = run_cost + kChunks + 1;
+    int* run_rows = run_cost + kChunks + 1;  // ... and of results
     Meta meta;
     meta.starts = reinterpret_cast<int32_t*>(smem + C::kOffMeta);
     meta.prefix = meta.starts + p.groups + 1;
@@ -370,21 +370,21 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 continue;
             const int s = run * 32 + lane;
             const Seg g = seg_of(p, meta, s, err);
-            const int units = g.nrt * p.Hkv, each = unit_cost(g), cost = units * each;
+            const int units = g.nrt * p.Hkv, each = unit_cost(g), cost = units * each, rows = units > 0 ? g.n * p.Hq : 0;
             if (pass == 0) {
-                const int c = __reduce_add_sync(0xffffffffu, cost), u = __reduce_add_sync(0xffffffffu, units);
+                const int c = __reduce_add_sync(0xffffffffu, cost), r = __reduce_add_sync(0xffffffffu, rows);
                 if (lane == 0) {
                     run_cost[run] = c;
-                    run_units[run] = u;
+                    run_rows[run] = r;
                 }
                 continue;
             }
-            int ci = cost, ui = units;
-            warp_sums(ci, ui);
-            const int cs = run_cost[run] + ci - cost, us = run_units[run] + ui - units;
+            int ci = cost, ri = rows;
+            warp_sums(ci, ri);
+            const int cs = run_cost[run] + ci - cost, rs = run_rows[run] + ri - rows;
             if (pass == 1 && run % ncta == cta && s < p.own0 + p.B) {  // for the join
                 p.seg_cost[s] = cs;
-                p.seg_unit[s] = us;
+                p.seg_row[s] = rs;
             }
             if (units == 0 || cs >= hi || cs + cost <= lo) continue;
 #pragma unroll 1
@@ -397,6 +397,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 const int rt = u - x.h * g.nrt;
                 x.q0 = g.q0 + rt * p.upt;
                 x.ntok = min(p.upt, g.n - rt * p.upt);
+                const int before = rs + (x.h * g.n + rt * p.upt) * p.G;
                 x.kb0 = g.base + t0 * kKeys;
                 x.c0 = g.c0;
                 x.c1 = g.c1;
@@ -406,12 +407,12 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                     x.table = r;
                     x.pos0 = INT32_MAX / 2;
                     x.nkt = t1 - t0;
-                    x.slot = (us + u + cta) | INT32_MIN;
+                    x.row = 2 * (before + cta * p.most_pre) | INT32_MIN;
                 } else {
                     x.table = s - p.own0;
                     x.pos0 = g.c1 - g.n + (x.q0 - g.q0);
                     x.nkt = seen_tiles(g, t0, t1, x.pos0 + x.ntok);
-                    x.slot = us + u + cta - run_units[p.own0 / 32];
+                    x.row = 2 * (before - run_rows[p.own0 / 32] + cta * p.most_own);
                 }
                 pieces[atomicAdd(&s_pieces, 1)] = x;  // (in any order: a piece's result does not depend on it)
                 // what its first copies hang on
@@ -428,23 +429,23 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 break;
             }
             if (warp == 0) {
-                int c0 = 0, u0 = 0;
+                int c0 = 0, rows0 = 0;
 #pragma unroll 1
                 for (int r0 = 0; r0 < runs; r0 += 32) {
                     const int r = r0 + lane;
-                    const int c = r < runs ? run_cost[r] : 0, u = r < runs ? run_units[r] : 0;
-                    int ci = c, ui = u;
-                    warp_sums(ci, ui);
+                    const int c = r < runs ? run_cost[r] : 0, n = r < runs ? run_rows[r] : 0;
+                    int ci = c, ni = n;
+                    warp_sums(ci, ni);
                     if (r < runs) {
                         run_cost[r] = c0 + ci - c;
-                        run_units[r] = u0 + ui - u;
+                        run_rows[r] = rows0 + ni - n;
                     }
                     c0 += __shfl_sync(0xffffffffu, ci, 31);
-                    u0 += __shfl_sync(0xffffffffu, ui, 31);
+                    rows0 += __shfl_sync(0xffffffffu, ni, 31);
                 }
                 if (lane == 0) {
                     run_cost[runs] = c0;
-                    run_units[runs] = u0;
+                    run_rows[runs] = rows0;
                 }
             }
             __syncthreads();
@@ -879,17 +880,17 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 const int row_tok = shift ? row_tok64 : row_tok0;
                 const int tok = (two ? k * p.tpt : 0) + row_tok;  // of the unit
                 const bool write = row >= shift && row_tok < p.tpt && tok < U.ntok;
-                const bool common = U.slot < 0;
+                const bool common = U.row < 0;
                 const uint32_t kv_base = kv_it, piece = n_p++;
                 kv_it += U.nkt;
                 const int step = two ? 1 : 2, t_first = two ? 0 : (k ^ (int)(kv_base & 1));
                 if (t_first >= U.nkt) continue;  // no key tile for this lane (and the join reads no result of it)
-                // a lane's half of a slot: its row tile's, or that of the piece's first or second key tile on
-                const int half = common ? p.rows_pre : p.rows_own;
+                // a lane's half of the result: its row tile's, or that of the piece's first or second key tile on
+                const int half = min(p.tpt, U.ntok) * p.G;
                 const int at = (two ? k : t_first) * half + row - shift;
-                const int64_t slot = U.slot & INT32_MAX;
-                float* po = (common ? p.po_pre : p.po_own) + slot * 2 * half * D + at * 4;
-                float* pl = (common ? p.pl_pre : p.pl_own) + slot * 2 * half + at;
+                const int64_t row0 = U.row & INT32_MAX;
+                float* po = (common ? p.po_pre : p.po_own) + row0 * D + at * 4;
+                float* pl = (common ? p.pl_pre : p.pl_own) + row0 + at;
                 // warps with rows that are a token's; the others only keep the lane's step
                 const int busy = (min(p.tpt, U.ntok - (two ? k * p.tpt : 0)) * p.G + 31) / 32;
                 const bool idle = (uint32_t)((warp & 3) - shift / 32) >= (uint32_t)busy;
@@ -1129,7 +1130,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 // One CTA per token and kv head. Its pieces are those of its rows' two units (the
 // group's common keys, its request's own) in every CTA whose share has tiles of them.
 struct Source {
-    const float* o;  // the row's first four values of the group's first head; the next four dims' 4 * rows further on
+    const float* o;  // the row's first four values of the group's first head; the next four dims' 8 * half further on
     const float* l;  // null: no piece
 };
 
@@ -1159,18 +1160,19 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParam
     const int gq0 = inside ? __ldg(p.qsl + r0) : 0, gq1 = inside ? __ldg(p.qsl + r1) : 0;
     const Seg seg[2] = {make_seg(p, gq0, gq1 - gq0, 0, common), make_seg(p, at.q0, at.q1 - at.q0, common, at.len)};
     int n = 0, n_common = 0;  // pieces, in the order of their keys
+    int half_common = 0, half_own = 0;  // rows of half a result
     // With few CTAs, which wait for the attention's end anyway, the steps up to the weights
     // are run through once before it, over no pieces: their instructions are then at hand.
 #pragma unroll 1
     for (int pass = kThreads == 512 ? 0 : 1; pass < 2; ++pass) {
-        int total = ncta, cost_at[2] = {0, 0}, unit_at[2] = {0, 0};
+        int total = ncta, cost_at[2] = {0, 0}, row_at[2] = {0, 0};
         if (pass == 1) {
             grid_dep_wait();
             total = __ldcg(p.seg_cost + p.own0 + p.B);
             cost_at[0] = __ldcg(p.seg_cost + g);
-            unit_at[0] = __ldcg(p.seg_unit + g);
+            row_at[0] = __ldcg(p.seg_row + g);
             cost_at[1] = __ldcg(p.seg_cost + p.own0 + max(at.r, 0));
-            unit_at[1] = __ldcg(p.seg_unit + p.own0 + max(at.r, 0)) - __ldcg(p.seg_unit + p.own0);
+            row_at[1] = __ldcg(p.seg_row + p.own0 + max(at.r, 0)) - __ldcg(p.seg_row + p.own0);
             if (total < 0 || at.r < 0) return;  // refused lengths, or a row behind the last request's: nothing is written
         }
         const Shares shares(total, ncta);
@@ -1185,10 +1187,12 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParam
                 rt = tok / p.upt;
                 tok -= rt * p.upt;
             }
-            const bool two = min(p.upt, s.n - rt * p.upt) > p.tpt;
-            const int local = h * s.nrt + rt, us = (part == 0 ? cost_at[0] : cost_at[1]) + local * unit_cost(s);
-            const int unit = (part == 0 ? unit_at[0] : unit_at[1]) + local;
-            const int half = part == 0 ? p.rows_pre : p.rows_own;
+            const int tokens = min(p.upt, s.n - rt * p.upt), half = min(p.tpt, tokens) * G;
+            const bool two = tokens > p.tpt;
+            const int us = (part == 0 ? cost_at[0] : cost_at[1]) + (h * s.nrt + rt) * unit_cost(s);
+            const int before = (part == 0 ? row_at[0] : row_at[1]) + (h * s.n + rt * p.upt) * G;
+            const int most = part == 0 ? p.most_pre : p.most_own;
+            (part == 0 ? half_common : half_own) = half;
             const int row = two && tok >= p.tpt ? half + (tok - p.tpt) * G : tok * G;
             const int first = shares.cta_of(us + s.e), last = shares.cta_of(us + s.e + (s.nkt - 1) * s.w);
             const int lanes = two ? 1 : 2, end = s.c1 - s.n + min(s.n, (rt + 1) * p.upt);  // (of own keys)
@@ -1199,10 +1203,10 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParam
                 const int c = first + (two ? j : j >> 1), k = two ? 0 : j & 1;
                 const int t0 = first_tile(shares.start(c), us, s), t1 = first_tile(shares.start(c + 1), us, s);
                 const int tiles = t0 >= t1 ? 0 : part == 0 ? t1 - t0 : seen_tiles(s, t0, t1, end);
-                const int64_t slot = (int64_t)(unit + c) * 2 * half;
+                const int64_t row0 = 2 * (before + c * most);
                 Source x;
-                x.o = o + slot * D + (k * half + row) * 4;
-                x.l = tiles > k ? l + slot + k * half + row : nullptr;
+                x.o = o + row0 * D + (k * half + row) * 4;
+                x.l = tiles > k ? l + row0 + k * half + row : nullptr;
                 src[n + j] = x;
             }
             n += (last - first + 1) * lanes;
@@ -1250,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const PrefixParam
     for (int f0 = tid; f0 < flats * deal; f0 += kThreads) {
         const int f = f0 % flats, part = f0 / flats, hh = f % G, d4 = f / G;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int at_common = d4 * 2 * p.rows_pre + hh, at_own = d4 * 2 * p.rows_own + hh;
+        const int at_common = d4 * 2 * half_common + hh, at_own = d4 * 2 * half_own + hh;
 #pragma unroll 4
         for (int i = part; i < n; i += deal) {
             const float w = weight[i * G + hh];

@@ -1,13 +1,14 @@
 """The calls over shared pages at the borders of what they promise: bad page ids wherever they are passed on, the error of
-attention's results, infinite values."""
+attention's results, infinite values, the size of its workspace."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
+from paged_kv_attention_07_gb300 import pka
 from tests import shared_ref as ref
-from tests.test_gpu_shared_pages import E, SHAPES, f64, fork_case, one, prefix_call, prefix_case
+from tests.test_gpu_shared_pages import E, SHAPES, f64, fork_case, one, prefix_call, prefix_case, prefix_check
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +86,27 @@ def test_prefix_attention_infinite_values_are_infinite_results(groups, d, bs):
     got = f64(s["out"])
     assert int(s["err"]) == 0 and (got[..., 3] == np.inf).all() and (got[..., 4] == -np.inf).all() and np.isnan(got[..., 5]).all()
     assert np.isfinite(np.delete(got, [3, 4, 5], -1)).all() and torch.isfinite(s["lse"]).all()
+
+
+@pytest.mark.parametrize("reqs,groups,tokens,Hq,Hkv,d,new", [
+    (1024, 1024, 1024, 32, 8, 128, 1), (4096, 4096, 4096, 32, 16, 64, 1), (256, 256, 287, 32, 8, 128, 32),
+    (192, 24, 192, 32, 8, 128, 1), (1, 1, 1, 8, 8, 128, 1), (64, 64, 8192, 64, 4, 128, 300), (40, 3, 120, 14, 2, 64, 3)])
+def test_prefix_workspace_holds_what_can_be_written(reqs, groups, tokens, Hq, Hkv, d, new):
+    """Of each token and head, for common and own keys, two partial results of d + 1 numbers, and those of one unit (up to
+    two tiles of 128 rows) more per CTA; some words per request. Not more for groups that have nothing in common."""
+    size = pka.pka_prefix_workspace_size(reqs, groups, tokens, Hq, Hkv, d, new)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    per_row = 2 * 4 * (d + 1)
+    least = 2 * tokens * Hq * per_row if reqs > 1 else tokens * Hq * per_row
+    assert least <= size <= least + 2 * sms * 256 * per_row + 16 * (reqs + groups + 64) + 8 * 256
+
+
+@pytest.mark.parametrize("scales", [None, (0.02, 0.03)])
+@pytest.mark.parametrize("groups,Hq,Hkv,bs", [(g, hq, hkv, bs) for g, hq, hkv, d, bs in SHAPES if d == 128])
+def test_prefix_attention_stays_in_its_workspace(groups, Hq, Hkv, bs, scales):
+    s = prefix_case(np.random.default_rng(Hq + bs), groups, Hq, Hkv, 128, bs, fp8_scales=scales)
+    size = s["work"].numel()
+    store = torch.full((size + (1 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    prefix_call(s, work=store[:size])
+    prefix_check(s)
+    assert (store[size:] == 0x5a).all()
