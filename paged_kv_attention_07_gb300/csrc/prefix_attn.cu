@@ -261,17 +261,17 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint64_t* q_full = bars + 0;    // [2] per row tile's place: landed
     uint64_t* q_empty = bars + 2;   // [2] its unit's last S product is done
-    uint64_t* k_full = bars + 4;    // [3] per K stage
-    uint64_t* k_empty = bars + 7;
-    uint64_t* v_full = bars + 10;   // [2] per V stage
-    uint64_t* v_empty = bars + 12;
-    uint64_t* s_full = bars + 14;   // [2] per lane: its S tile is in tensor memory
-    uint64_t* p_full = bars + 16;   // [2] its P is (4 warp arrivals)
-    uint64_t* pv_done = bars + 18;  // [2] the product that read its P is done
-    uint64_t* o_free = bars + 20;   // [2] its O has been read (4 warp arrivals)
-    uint64_t* p_half = bars + 22;   // [2] P of keys 0..63 is there (4 warp arrivals)
-    uint64_t* c_full = bars + 24;   // [2] per stage of V's codes: landed
-    uint64_t* c_empty = bars + 26;  // [2] widened (4 warp arrivals)
+    uint64_t* k_full = bars + 4;    // [2] per K stage
+    uint64_t* k_empty = bars + 6;
+    uint64_t* v_full = bars + 8;    // [2] per V stage
+    uint64_t* v_empty = bars + 10;
+    uint64_t* s_full = bars + 12;   // [2] per lane: its S tile is in tensor memory
+    uint64_t* p_full = bars + 14;   // [2] its P is (4 warp arrivals)
+    uint64_t* pv_done = bars + 16;  // [2] the product that read its P is done
+    uint64_t* o_free = bars + 18;   // [2] its O has been read (4 warp arrivals)
+    uint64_t* p_half = bars + 20;   // [2] P of keys 0..63 is there (4 warp arrivals)
+    uint64_t* c_full = bars + 22;   // [2] per stage of V's codes: landed
+    uint64_t* c_empty = bars + 24;  // [2] widened (4 warp arrivals)
     float* row_unit = reinterpret_cast<float*>(smem + C::kOffUnit);
     Piece* pieces = reinterpret_cast<Piece*>(smem + C::kOffPiece);
     int* run_cost = reinterpret_cast<int*>(smem + C::kOffSums);  // before each run of 32 segments
@@ -291,9 +291,12 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
+        static_assert(C::kRowTiles == 2 && C::kStagesK == 2 && C::kStagesV == 2, "places of the barriers");
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], kFp8 ? 4 : 1);
             mbar_init(&q_empty[i], 1);
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], kFp8 ? 4 : 1);
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
@@ -303,10 +306,6 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
             mbar_init(&o_free[i], 4);
             mbar_init(&c_full[i], 1);
             mbar_init(&c_empty[i], 4);
-        }
-        for (int i = 0; i < C::kStagesK; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
         }
         fence_barrier_init();
         s_abort = 0;
@@ -950,7 +949,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         for (int j = 0; j < 32; j += 2)
                             mx[(j >> 1) & 7] = fmax3f(mx[(j >> 1) & 7], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
                     };
-                    bool early = false;
+                    bool early = false;  // (stays so in edge tiles, whose value rows are cleared first)
                     auto signal_half = [&] {  // the product over keys 0..63 may start
                         tmem_wait_st();
                         tc_fence_before();
@@ -958,7 +957,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         if (lane == 0) mbar_arrive(&p_half[k]);
                     };
                     if (idle) {
-                        early = !edge;  // (value rows outside the segment's keys are zeroed by all warps)
+                        early = !edge;
                         if (early) signal_half();
                     } else if (!edge) {
                         // twice over the row, 32 scores at a time (64 at a time 24 groups of 8 beams took 110 us, the whole
@@ -990,10 +989,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         for (int c = 0; c < 8; ++c) {
                             const int at = 32 * (c & 3), a = min(32, max(0, vlo - at)), b = min(32, max(0, vhi - at));
                             const uint32_t bits = (uint32_t)((1ull << b) - (1ull << a));  // (a <= b)
-                            if (c == 4) {
-                                take_max();
-                                early = !edge && !__any_sync(0xffffffffu, rescale);
-                            }
+                            if (c == 4) take_max();
                             if (!__any_sync(0xffffffffu, bits != 0)) {
                                 if (c >= 4) tmem_st16_zero(tS + (kFp8 ? at >> 1 : at));
                                 if (!kFp8 && c >= 4) tmem_st16_zero(tS + at + 16);
@@ -1006,12 +1002,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
 #pragma unroll
                                 for (int j = 0; j < 32; ++j) r[j] = (bits >> j) & 1 ? r[j] : 0xff800000u;
                             }
-                            if (c < 4) {
-                                max32(r);
-                            } else {
-                                store32(r, at);
-                                if (c == 5 && early) signal_half();
-                            }
+                            if (c < 4) max32(r);
+                            else store32(r, at);
                         }
                     }
                     l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
