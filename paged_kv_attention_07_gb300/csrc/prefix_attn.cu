@@ -360,8 +360,11 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     // both: what runs once per launch is bound by the fetch of its instructions.
     const int stretch = (kPieces - 2) * (p.cost_unit + kCostOne);
     for (int pass = 0;; ++pass) {
-        if (pass > 1) load_meta();  // (tiles were there meanwhile)
         const int from = lo + (pass - 1) * stretch;
+        if (pass > 1) {
+            if (from >= hi) break;
+            load_meta();  // (tiles were there meanwhile)
+        }
 #pragma unroll 1
         for (int run = warp; run < runs; run += kPxThreads / 32) {
             if (pass > 0 && (run_cost[run] >= min(hi, from + stretch) || run_cost[run + 1] <= from) &&
