@@ -1509,7 +1509,7 @@ pka_status prefix_attn_impl(const void* q, const void* k_cache, const void* v_ca
     p.G = num_q_heads / num_kv_heads;
     p.tpt = L.tpt;
     p.upt = prefix_unit_tokens(L.tpt, cf.fp8);
-    p.cost_unit = cf.fp8 ? kPrefixMaxCost : 2;
+    p.cost_unit = cf.fp8 ? 3 : 1;
     p.bs = block_size;
     p.bs_log2 = log2_of(block_size);
     p.max_query = max_query_len;

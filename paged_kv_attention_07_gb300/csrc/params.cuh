@@ -252,7 +252,7 @@ struct CopyPagesParams {
     int pieces;  // of a page, set by the launch
 };
 
-// At most the cost of a unit's key tile, or of the unit itself (prefix_attn.cu): the line of all costs keeps to 32 bits.
+// No cost of a unit's key tile, or of the unit itself (prefix_attn.cu), is above this: the line of all costs keeps to 32 bits.
 constexpr int kPrefixMaxCost = 4;
 
 struct PrefixMaps {

@@ -55,8 +55,8 @@ constexpr int kMaxSegs = 2 * kMaxRequests;
 constexpr int kChunks = kMaxSegs / 32;  // warp-sized runs of segments
 // Costs on the line: a key tile for one row tile, for two, and what a unit takes besides
 // (its first copies, its end, lanes that wait for one another), as measured: 24 groups of 8
-// beams with (1, 2, 2) 104 us, (1, 2, 1) 107, (1, 2, 3) 109; over an 8-bit cache, whose tiles
-// are shorter, 32 groups of 4 with (1, 2, 4) 91 us, (1, 2, 3) and (1, 2, 5) 95, (1, 2, 2) 101.
+// beams with (1, 2, 1) 97 us, (1, 2, 2) 104, (1, 2, 3) 112, 64 requests 50, 50 and 51; over an 8-bit
+// cache 32 groups of 4 with (1, 2, 3) 87.6 us, (1, 2, 4) 91, (1, 2, 2) 89.4, (1, 2, 1) 103.
 constexpr int kCostOne = 1, kCostTwo = 2;
 
 struct Seg {
