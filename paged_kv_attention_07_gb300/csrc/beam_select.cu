@@ -26,7 +26,7 @@
 // Candidates of different rows are compared by their 64-bit scores.
 //
 // Measured: 4 rows of 32000 bf16 logits 8.7 us; 64 groups of 4 rows of 131072 23.6 us (2.8 TB/s; at the
-// rate of a copy the 67 MB take 9.9); 17 groups of 5 rows of 50001 float32 logits 11.5 us. A
+// rate of a copy the 67 MB take 9.9); 17 groups of 5 rows of 50001 float32 logits 11.4 us. A
 // launch and the phases behind the stream (limit, second reading, lists, ranks: each a
 // few hundred instructions fetched for the first time) take about 7 us of each; the stream
 // of 256 rows is bound by the busiest SMs, which have two rows where the mean is 1.7.
@@ -195,9 +195,9 @@ PKA_DEVICE int cut(u64* keys, int n, int keep, u64* limit) {
     return min(n, keep);
 }
 
-// log(s) of a normal s > 0 to about 2^-33: e ln 2 + log m with m in [3/4, 3/2) and log m =
-// 2 artanh z = 2 z + z^3 (2/3 + 2/5 z^2 + ...), z = (m - 1) / (m + 1) to twice 24 bits (the
-// 64-bit logarithm takes a microsecond, much of it the fetch of its code).
+// log(s) of a normal s > 0 to 2^-28 (of s up to 2^26: 2.3e-9): e ln 2 + log m with m in [3/4, 3/2) and log m =
+// 2 artanh z = 2 z + z^3 (2/3 + 2/5 z^2 + ...), z = (m - 1) / (m + 1) to twice 24 bits, the rest
+// in 32 bits, which bounds it (the 64-bit logarithm takes a microsecond, much of it the fetch of its code).
 PKA_DEVICE double log_of(float s) {
     int e = (int)(__float_as_uint(s) >> 23) - 127;
     float m = __uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u);
@@ -543,7 +543,7 @@ cudaError_t go(BeamSelectParams p, int num_sms, cudaStream_t stream) {
     // A group's CTAs have a part each where its beams allow: as many slices of a row as give each warp a
     // tile of its own, and no more than a cluster's 16 CTAs and the lists that one of them joins; and
     // three CTAs for two SMs, of the four that they hold: larger clusters leave SMs of a GPC over, and
-    // with more of them some wait (17 x 5 beams in 255 CTAs 17.9 us, in 170 12.0).
+    // with more of them some wait (17 x 5 beams in 255 CTAs 17.9 us, in 170 11.4).
     int slices = 1;
     while (p.beams * (slices + 1) <= kMaxCluster && (int64_t)p.groups * p.beams * (slices + 1) * 2 <= 3 * num_sms &&
            p.beams * (slices + 1) * p.keep <= kMaxEntries && p.vocab > slices * kWarps * Tile<kBf16, kVec>::kSize)

@@ -20,19 +20,21 @@
 //
 // Per CTA, 12 warps: K and V producers (TMA boxes of pages through the block
 // table), two MMA-issuing warps, two softmax warpgroups ("lanes" 0 and 1, one
-// thread per row). With two row tiles in a unit, lane k has row tile k and every
-// key tile serves both; with one, the lanes take alternate key tiles of the same
-// rows, so that one's exponentials overlap the other's products, and leave two
-// pieces. Tensor memory: S_k (128 columns, P_k written over it) and O_k.
+// thread per row); over codes 4 warps more, which split the rows and widen V. With
+// two row tiles in a unit, lane k has row tile k and every key tile serves both;
+// with one, the lanes take alternate key tiles of the same rows, so that one's
+// exponentials overlap the other's products, and leave two pieces. Tensor memory:
+// S_k (128 columns, P_k written over it) and O_k.
 // The tensor cores ask for P in the type of V, bf16. A weight is two bf16 numbers, off by 2^-15
 // of it, and takes two products: the result's error is that of its own rounding (0.0017 against 64 bits; with
-// one number 0.0023, 24 groups of 8 beams 104 us instead of 107, 64 requests 48 and 51, 4 beams 22.9
-// and 23.2). The weights' sum is kept from the unrounded values in 32 bits.
+// one number 0.0023, and 24 groups of 8 beams took 3 % less time, 64 requests 6, 4 beams 1). Over codes
+// P is one f16 number (below). The weights' sum is kept from the unrounded values in 32 bits.
 //
 // Measured, with the join: 24 groups of 8 (1000 to 8192 common tokens, 1 to 512 own, 8 kv heads of 128,
-// G = 4) 107 us, 3.8 TB/s of what has to be read; 64 requests behind 16384 tokens 50.5 us; 4 beams
-// behind 8192 23 us; 32 groups of 4 over an 8-bit cache 91.5 us, 2.8 TB/s. Full tiles take 1.2 us
-// each on an SM (5 TB/s; of 8-bit codes 1.1), the common keys of those 24 groups alone 71 us. A
+// G = 4) 97 us, 4.2 TB/s of what has to be read; 64 requests behind 16384 tokens 50 us; 4 beams
+// behind 8192 21.5 us; 32 groups of 4 over an 8-bit cache 87 us, 2.9 TB/s. A full tile more of
+// long groups takes 1.4 us of an SM (6.9 TB/s), of 8-bit codes 1.0 (5.0), with two row tiles 2.4 to 2.9 (0.9 PFLOP/s and
+// more, without the weights' second product); lengths, shares and the join 12 us of each call. A
 // request's own unit of a tile or two takes 2 to 3 us: it leaves the stages half empty, and its steps
 // follow each other on one lane (first copies 2, S and softmax of an edge tile 2, P V 1, result 1).
 #include <float.h>
@@ -249,8 +251,8 @@ PKA_DEVICE void warp_sums(int& a, int& b) {
 }
 
 // kSeveral: requests may have more than one new token. The code that keeps a later token's
-// infinities from earlier ones costs 2 to 7 % where nothing calls for it (24 groups of 8 beams 105.5
-// us with it, 103.7 without; 64 requests 49.8 and 48.0; 8-bit 97.5 and 91.4), by its size alone.
+// infinities from earlier ones costs 3 to 8 % where nothing calls for it (24 groups of 8 beams 105
+// us with it, 97 without; 64 requests 51.1 and 49.7; 8-bit 90.6 and 87.2), by its size alone.
 template <int D, bool kFp8, bool kSeveral>
 __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
     prefix_attn_kernel(const __grid_constant__ PrefixMaps maps, const PrefixParams p) {
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                 // -------------------------------------------------------- producers: Q and K; V
                 const int which = warp == 0 ? 0 : 1;
                 // (keys are read once, or by the few row tiles of a group at about the same time: not kept in L2, where
-                // the pieces wait for the join; kept, 24 groups of 8 beams take 109 us, not 104)
+                // the pieces wait for the join; kept, 24 groups of 8 beams take 102 us, not 97)
                 const uint64_t pol = policy_evict_first(), pol_q = policy_evict_last();
                 const bool tma = p.bs >= 8;
                 // of an 8-bit cache K's codes are the product's operand, V's are widened first
@@ -963,8 +965,8 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         early = !edge;
                         if (early) signal_half();
                     } else if (!edge) {
-                        // twice over the row, 32 scores at a time (64 at a time 24 groups of 8 beams took 110 us, the whole
-                        // row in registers 123: the code is fetched anew at each change between tiles and edge tiles)
+                        // twice over the row, 32 scores at a time (64 at a time 24 groups of 8 beams took 3 us more, with
+                        // the whole row in registers 16: the code is fetched anew at each change between full and edge tiles)
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t r[32];
@@ -984,9 +986,9 @@ __global__ void __launch_bounds__((PxCfg<D, kFp8>::kThreads), 1)
                         }
                     } else {
                         // the same in one loop body, few instructions, which edge tiles wait for more than for
-                        // anything else (all tiles this way cost 24 groups of 8 beams 123 us, not
-                        // 107). Chunks that no row of the warp sees are left out, and only those that
-                        // not every row sees in full are masked.
+                        // anything else (all tiles this way cost 24 groups of 8 beams 15 us more). Chunks that no
+                        // row of the warp sees are left out, and only those that not every row sees in full
+                        // are masked.
                         const int vlo = U.c0 - kb, vhi = max(vlo, c1 - kb);  // visible columns [vlo, vhi)
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
