@@ -141,16 +141,15 @@ PKA_DEVICE bool take_out(uint32_t (&w)[N]) {
     return any;
 }
 
-// Two weights p >= 0 as two bf16 numbers each, p cut off and the rest cut off: off by less than 2^-14 of p, to one
-// side, which the 2^-15 of p added before halves. They also keep the rest above 0 where p is (down to
-// 2^-118), so that an infinite value is not multiplied by 0.
+// Two weights p >= 0 as two bf16 numbers each, p cut off, and the rest, rounded (2^-16 of p at most). 2^-17 of p more
+// keeps the rest above 0 where p is (down to 2^-116), so that an infinite value is not multiplied by 0.
 PKA_DEVICE void split_weights(float p0, float p1, uint32_t& high, uint32_t& rest) {
     const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
     high = __byte_perm(b0, b1, 0x7632);
     float d0, d1;
-    fma2(d0, d1, p0, p1, 1.f + 1.f / 32768, __uint_as_float(b0 & 0xffff0000u | 0x80000000u),
+    fma2(d0, d1, p0, p1, 1.f + 1.f / 131072, __uint_as_float(b0 & 0xffff0000u | 0x80000000u),
          __uint_as_float(b1 & 0xffff0000u | 0x80000000u));
-    rest = __byte_perm(__float_as_uint(d0), __float_as_uint(d1), 0x7632);
+    rest = pack_bf16(d0, d1);
 }
 
 struct Piece {

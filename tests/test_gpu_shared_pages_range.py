@@ -8,7 +8,7 @@ import torch
 
 from paged_kv_attention_07_gb300 import pka
 from tests import shared_ref as ref
-from tests.test_gpu_shared_pages import E, SHAPES, f64, fork_case, one, prefix_call, prefix_case, prefix_check
+from tests.test_gpu_shared_pages import E, SHAPES, dev, f64, fork_case, one, prefix_call, prefix_case, prefix_check, word
 
 pytestmark = pytest.mark.gpu
 
@@ -49,7 +49,8 @@ def test_fork_pages_bad_ids_of_rows_that_go_on_as_one(B, width, bs, bad):
 def test_prefix_attention_is_off_by_its_results_rounding(groups, Hq, Hkv, d, bs):
     """That rounding: 2^-8 of the value. A score of d products in 32 bits: (d + 8) 2^-24 of the largest sum of their
     magnitudes, exponentials and sums 2^-20, three times for weight, sum and their quotient. A weight as two bf16 numbers,
-    both cut off: less than 2^-7 of 2^-7 of it is left, to one side; 2^-15 of it added before makes that 2^-15 to either."""
+    the first cut off, the second rounded: half a step of the eighth bit behind the first's eight, 2^-16 of it, and 2^-17 that
+    keeps the second above zero, below 2^-15 together."""
     rng = np.random.default_rng(Hq * d + bs)
     s = prefix_case(rng, groups, Hq, Hkv, d, bs)
     prefix_call(s)
@@ -110,3 +111,37 @@ def test_prefix_attention_stays_in_its_workspace(groups, Hq, Hkv, bs, scales):
     prefix_call(s, work=store[:size])
     prefix_check(s)
     assert (store[size:] == 0x5a).all()
+
+
+def test_prefix_attention_workspace_past_32_bits():
+    """Partial results whose offsets pass 32 bits: 4096 requests in pairs, 32 new tokens each, within the bound above."""
+    rng = np.random.default_rng(50)
+    B, new, common, bs, Hq, Hkv, d = 4096, 32, 16, 16, 32, 8, 128
+    T, own = B * new, new // bs
+    pages = torch.from_numpy(rng.permutation(B // 2 + B * own)).int().cuda()
+    table = torch.cat([pages[:B // 2].repeat_interleave(2)[:, None], pages[B // 2:].view(B, own)], 1).contiguous()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(50)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k, v = normal(T, Hq, d), normal(len(pages), Hkv, bs, d), normal(len(pages), Hkv, bs, d)
+    size = pka.pka_prefix_workspace_size(B, B // 2, T, Hq, Hkv, d, new)
+    assert size > 2 ** 33
+    s = dict(q=q, k=k, v=v, table=table, qsl=dev(np.arange(B + 1) * new), seq=dev([common + new] * B), starts=dev(np.arange(0, B + 1, 2)),
+             prefix=dev([common] * (B // 2)), scale=d ** -0.5, new=new, longest=common + new, out=torch.empty_like(q),
+             lse=torch.empty(T, Hq, device="cuda"), scales=None, err=word(), work=torch.empty(size, dtype=torch.uint8, device="cuda"))
+    prefix_call(s)
+    assert int(s["err"]) == 0
+    hidden = torch.ones(new, common + new, dtype=torch.bool, device="cuda").triu(common + 1)[None, :, None, None]
+    for r in range(0, B, 256):
+        at = table[r:r + 256].long()
+        K, V = (x[at].double().transpose(2, 3).reshape(256, -1, Hkv, d) for x in (k, v))
+        Q = q[r * new:(r + 256) * new].double().view(256, new, Hkv, Hq // Hkv, d)
+        score = torch.einsum("rthgd,rnhd->rthgn", Q, K).mul_(s["scale"]).masked_fill_(hidden, -math.inf)
+        reach = torch.einsum("rthgd,rnhd->rthgn", Q.abs(), K.abs()).amax(-1, keepdim=True) * s["scale"]
+        weight, lse = score.softmax(-1), score.logsumexp(-1)
+        want, mag = (torch.einsum("rthgn,rnhd->rthgd", weight, x) for x in (V, V.abs()))
+        delta = (d + 8) * 2.0 ** -24 * reach + 2.0 ** -20
+        limit = 2.0 ** -8 * want.abs() + (2.0 ** -15 + 3 * delta) * mag * (1 + 2.0 ** -6) + 1e-30
+        got = s["out"][r * new:(r + 256) * new].double().view_as(want)
+        assert ((got - want).abs() <= limit).all(), r
+        assert ((s["lse"][r * new:(r + 256) * new].view_as(lse) - lse).abs() <= 2 * delta[..., 0] + 2.0 ** -22 * lse.abs()).all()
