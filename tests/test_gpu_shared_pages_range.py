@@ -145,3 +145,52 @@ def test_prefix_attention_workspace_past_32_bits():
         got = s["out"][r * new:(r + 256) * new].double().view_as(want)
         assert ((got - want).abs() <= limit).all(), r
         assert ((s["lse"][r * new:(r + 256) * new].view_as(lse) - lse).abs() <= 2 * delta[..., 0] + 2.0 ** -22 * lse.abs()).all()
+
+
+@pytest.mark.parametrize("scales", [None, (0.02, 0.03)])
+@pytest.mark.parametrize("width,new", [(1, 1), (1, 3), (2, 1), (4, 2)])
+def test_prefix_attention_lists_that_follow_one_another(width, new, scales):
+    """More pieces in a CTA's share than it lists at a time, over either cache, of common keys too, with one new token and
+    with several: roles and their barriers go on from list to list."""
+    rng = np.random.default_rng(60 + width + new)
+    B, Hkv, d, bs, common = 4096, 16, 128, 16, 16 if width > 1 else 0
+    lens = rng.integers(new, bs + 1, B)
+    own = torch.from_numpy(rng.permutation(B + B // width)).int().cuda()
+    table = own[:B, None]
+    if common:
+        table = torch.cat([own[B:].repeat_interleave(width)[:, None], table], 1)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(width)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    q = normal(B * new, Hkv, d).bfloat16()
+    k, v = (normal(len(own), Hkv, bs, d) for _ in range(2))
+    if scales:
+        k, v = ((x / u).to(torch.float8_e4m3fn) for x, u in zip((k, v), scales))
+        K, V = (x.double() * float(np.float32(u)) for x, u in zip((k, v), scales))
+        k, v = k.view(torch.uint8), v.view(torch.uint8)
+    else:
+        k, v = k.bfloat16(), v.bfloat16()
+        K, V = k.double(), v.double()
+    size = pka.pka_prefix_workspace_size(B, B // width, B * new, Hkv, Hkv, d, new)
+    s = dict(q=q, k=k, v=v, table=table.contiguous(), qsl=dev(np.arange(B + 1) * new), seq=dev(lens + common), starts=dev(np.arange(0, B + 1, width)),
+             prefix=dev([common] * (B // width)), scale=d ** -0.5, new=new, longest=common + bs, out=torch.empty_like(q),
+             lse=torch.empty(B * new, Hkv, device="cuda"), scales=scales, err=word(),
+             work=torch.full((size,), 0xff, dtype=torch.uint8, device="cuda"))
+    prefix_call(s)
+    assert int(s["err"]) == 0
+    seen = dev(lens + common)[:, None] - new + torch.arange(1, new + 1, device="cuda")  # [B, new] keys of each token
+    for r in range(0, B, 512):
+        rows = slice(r * new, (r + 512) * new)
+        Kr, Vr = (x[table[r:r + 512].long()].transpose(2, 3).reshape(512, -1, Hkv, d) for x in (K, V))
+        Q = q[rows].double().view(512, new, Hkv, d)
+        hidden = (torch.arange(Kr.shape[1], device="cuda") >= seen[r:r + 512, :, None])[:, :, None]
+        score = torch.einsum("rthd,rnhd->rthn", Q, Kr).mul_(s["scale"]).masked_fill_(hidden, -math.inf)
+        delta = (d + 8) * 2.0 ** -24 * torch.einsum("rthd,rnhd->rthn", Q.abs(), Kr.abs()).amax(-1, keepdim=True) * s["scale"] + 2.0 ** -20
+        if scales:  # the queries' split, as beside the other tests of this cache; weights in f16
+            delta = delta + 2.0 ** -17 * Q.abs().amax(-1, keepdim=True) * Kr.abs().sum(-1).amax() * s["scale"]
+        weight = score.softmax(-1)
+        want, mag = (torch.einsum("rthn,rnhd->rthd", weight, x) for x in (Vr, Vr.abs()))
+        limit = 2.0 ** -8 * want.abs() + ((2.0 ** -11 if scales else 2.0 ** -15) + 3 * delta) * mag * (1 + 2.0 ** -6) + 1e-30
+        assert ((s["out"][rows].double().view_as(want) - want).abs() <= limit).all(), r
+        lse = score.logsumexp(-1)
+        assert ((s["lse"][rows].view_as(lse) - lse).abs() <= 2 * delta[..., 0] + 2.0 ** -22 * lse.abs()).all()
